@@ -125,6 +125,9 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 #define SPEC_STATUS_BAD_LOGITS 8u
 /* spec_tree_verify: a node's parent is not an earlier node. */
 #define SPEC_STATUS_BAD_TREE 32u
+/* spec_cache_*: a length or a number of new tokens out of range; a page id out of range. */
+#define SPEC_STATUS_BAD_LENGTH 64u
+#define SPEC_STATUS_BAD_PAGE 128u
 
 /* One verification round for B independent sequences (see the top of this
  * file for the operation, layout, ownership and errors).
@@ -290,6 +293,124 @@ spec_status spec_verify_launch_shape(int B, int gamma_max, int V, spec_dtype dty
  * unregistered host memory, another device's memory or a NULL argument, and
  * SPEC_ERR_CUDA if the runtime query fails.  Enqueues nothing. */
 spec_status spec_device_pointer(const void *ptr, const void **device_ptr);
+
+/* ---------------------------------------------------------------------------
+ * The target's key/value cache, held in 8 bits.
+ *
+ * Tokens live in blocks ("pages") of `block` tokens.  Per block and key/value
+ * head there is one scale for the keys and one for the values: token value =
+ * code * scale, the code an 8-bit float (e4m3: largest 448, or e5m2: largest
+ * 57344).  Sequence b's token j is row j % block of page
+ * block_table[b * table_stride + j / block].
+ *   k, v            codes; element (page, head, row, d) at
+ *                   page * stride[0] + head * stride[1] + row * stride[2] + d bytes;
+ *                   16-byte aligned, strides positive multiples of 16
+ *   k_scale, v_scale [num_pages, kv_heads] float32, dense
+ *   positions       [num_pages, kv_heads, block] int32, dense, or NULL: the
+ *                   position of each cached token in its text, which the bias by
+ *                   distance uses (NULL: the token's index j).  16-byte aligned.
+ *   block_table     [batch, >= max_blocks] int32
+ * A length is valid in [0, max_blocks * block].  Data problems never trap: a
+ * sequence with a length (or number of new tokens) out of range is skipped, its
+ * outputs zero (lse -inf, lengths 0), and a token on a page outside
+ * [0, num_pages) counts as not cached; SPEC_STATUS_BAD_LENGTH and
+ * SPEC_STATUS_BAD_PAGE are OR-ed into *status when status is not NULL.  Scales
+ * that a call reads are positive and finite.
+ * Ownership, stream and error rules as for spec_verify, but for two kernels
+ * where a result is joined or moved after it is found; every array is device
+ * memory.  Nothing is allocated. */
+typedef enum { SPEC_E4M3 = 0, SPEC_E5M2 = 1 } spec_code;
+
+typedef struct spec_cache {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int32_t *positions;
+    const int32_t *block_table;
+    int64_t k_stride[3], v_stride[3];
+    int64_t table_stride;
+    int32_t batch, max_blocks, num_pages, kv_heads, block, dim; /* block 16, 32, 64 or 128; dim 64 or 128 */
+    int32_t code;                                               /* spec_code */
+} spec_cache;
+
+/* Writes new tokens: token i < num_new[b] of k, v [batch, n, kv_heads, dim]
+ * (float32 or bf16, element strides of the first three dimensions in k_stride
+ * and v_stride, the last one dense) becomes cached token lengths[b] + i, in
+ * 8 bits.  For each block that is written, with s_old its scale if it already
+ * holds tokens of this sequence (index < lengths[b]) and nothing else:
+ *   s = max(s_old, 2^e), 2^e the smallest power of two with |x| <= 2^e * top
+ *       for every finite new x of the block and head (2^-100 at least);
+ *   new codes round(x / s) to nearest even; the older codes become
+ *   round(code * s_old / s) where s differs from s_old.
+ * A power of two costs a floating-point code no precision, and moving a code to
+ * a larger power of two is exact down to the subnormal codes.  Infinities and
+ * NaN are stored as NaN and do not enter s.  lengths is not changed (the caller
+ * adds num_new, or, after a verification round, the accepted part of it).
+ *   num_new    [batch] int32 in [0, n], or NULL: n for every sequence
+ *   positions  [batch, n] int32 or NULL (lengths[b] + i), written to
+ *              cache.positions where that is present */
+spec_status spec_cache_append(const spec_cache *cache, const int32_t *lengths, const void *k, const void *v,
+                              const int64_t k_stride[3], const int64_t v_stride[3], int n, spec_dtype dtype,
+                              const int32_t *num_new, const int32_t *positions, uint32_t *status, void *stream);
+
+/* How queries see the cache.  Query i < m (m = num_new[b], or n) of sequence b
+ * is the token at index a_i = lengths[b] - m + i: the newest m cached tokens
+ * ask.  It sees token j < lengths[b] when
+ *   parent == NULL: j <= a_i; else j < lengths[b] - m, or token j is node i or
+ *     an ancestor of it in the candidate tree (node k is token lengths[b] - m + k,
+ *     parent[b, k] in [0, k) for k >= 1, as in spec_tree_verify); n <= 256;
+ *   and, with window > 0, j > a_i - window;
+ *   or j < prefix[b] (a prefix that every query sees, also outside the window).
+ * Its score is x = scale * q.k, then softcap * tanh(x / softcap) where softcap
+ * > 0, then - slopes[head] * |position(a_i) - position(j)| where slopes is given.
+ * A row that sees nothing gets zeros and lse = -inf.  A parent outside [0, k)
+ * counts as no parent and sets SPEC_STATUS_BAD_TREE.  What a query does not see
+ * changes nothing in its row, NaN included; a NaN key that it sees makes its row
+ * NaN, a NaN value that dimension of its row or all of it. */
+typedef struct spec_cache_form {
+    float scale, softcap;
+    int32_t window;
+    const float *slopes;    /* [heads] or NULL */
+    const int32_t *prefix;  /* [batch] or NULL */
+    const int32_t *parent;  /* [batch, n] or NULL */
+    const int32_t *num_new; /* [batch] in [0, n] or NULL (n) */
+} spec_cache_form;
+
+/* Attention: out[b, i, h, :] = sum_j softmax_j(x) v_j, lse[b, i, h] the natural
+ * logarithm of the sum of exp(x).  Query head h reads key/value head
+ * h / (heads / kv_heads).  Rows i >= num_new[b] are zeros with lse = -inf.
+ *   q    [batch, n, heads, dim] bf16, element strides q_stride (multiples of 8),
+ *        16-byte aligned, the last dimension dense
+ *   out  [batch, n, heads, dim] bf16, 16-byte aligned; lse [batch, n, heads] float32
+ *   workspace  spec_cache_attend_workspace bytes, 16-byte aligned; its contents
+ *              do not matter and concurrent calls need one each */
+spec_status spec_cache_attend(const spec_cache *cache, const int32_t *lengths, const void *q,
+                              const int64_t q_stride[3], int n, int heads, const spec_cache_form *form, void *out,
+                              float *lse, void *workspace, int64_t workspace_bytes, uint32_t *status, void *stream);
+spec_status spec_cache_attend_workspace(const spec_cache *cache, int n, int heads, int64_t *bytes);
+
+/* Attention weight received: weights[page, kv head, row] += sum over the m
+ * queries and the head's query heads of exp(x - lse), for every cached token of
+ * every sequence (lse as spec_cache_attend gave it; rows whose lse is -inf add
+ * nothing).  weights [num_pages, kv_heads, block] float32, dense.  Each sum has
+ * a fixed order.  Pages that several sequences share must not be weighed in one
+ * call: their sums would race. */
+spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, const void *q,
+                             const int64_t q_stride[3], int n, int heads, const spec_cache_form *form,
+                             const float *lse, float *weights, uint32_t *status, void *stream);
+
+/* Eviction: of each sequence and key/value head, the `recent` newest tokens and,
+ * of the others, the keep - recent with the largest weights (the lower index on
+ * ties, NaN below every number), or all tokens when there are no more than
+ * `keep`.  They are moved, in their order, with their weights and positions, to
+ * the pages of out_table[b * out_stride + ...], ceil(keep / block) each, which
+ * must be in no sequence's block_table.  A new block's scale is the largest of
+ * its tokens' scales, the codes as for spec_cache_append.
+ *   out_lengths [batch] int32: min(lengths[b], keep)
+ *   out_index   [batch, kv_heads, keep] int32: the kept indices, then -1
+ * Limits: 1 <= keep, 0 <= recent <= keep. */
+spec_status spec_cache_evict(const spec_cache *cache, const int32_t *lengths, float *weights, int keep, int recent,
+                             const int32_t *out_table, int64_t out_stride, int32_t *out_lengths, int32_t *out_index,
+                             uint32_t *status, void *stream);
 
 /* Static description of a status code. */
 const char *spec_status_string(spec_status s);

@@ -36,6 +36,8 @@ STATUS_BAD_TEMPERATURE = 2
 STATUS_BAD_NUM_DRAFT = 4
 STATUS_BAD_LOGITS = 8
 STATUS_BAD_TREE = 32
+STATUS_BAD_LENGTH = 64  # cache_*: a length or a number of new tokens out of range
+STATUS_BAD_PAGE = 128   # cache_*: a page id out of range
 
 MAX_GAMMA = 16
 MAX_TREE_NODES = 256
@@ -425,3 +427,18 @@ def to_device(batch, device="cuda"):
         uniforms=torch.from_numpy(np.ascontiguousarray(batch.uniforms, dtype=np.float32)).to(device),
         temperature=torch.from_numpy(np.ascontiguousarray(batch.temperature, dtype=np.float32)).to(device),
     )
+
+
+# The cache's operators need torch; the rest of this module imports it inside its
+# calls, so that the host-only parts load without it.
+_CACHE_NAMES = ("KVCache", "cache_append", "cache_attend", "cache_weigh", "cache_evict")
+
+
+def __getattr__(name):
+    if name in _CACHE_NAMES:
+        from . import cache
+
+        for n in _CACHE_NAMES:
+            globals()[n] = getattr(cache, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

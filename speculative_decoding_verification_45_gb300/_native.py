@@ -12,10 +12,12 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
-# The host unit plus one unit per (dtype, proposal form) of kernels: compiled in parallel.
+# The host unit, one unit per (dtype, proposal form) of kernels, and the cache's two: compiled in parallel.
 SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "kernels_bf16.cu", "kernels_bf16_point.cu",
-                                            "kernels_f32.cu", "kernels_f32_point.cu")]
-HEADERS = [os.path.join(INCLUDE, "spec_verify.h"), os.path.join(CSRC, "spec_verify_kernels.cuh")]
+                                            "kernels_f32.cu", "kernels_f32_point.cu", "spec_cache_move.cu",
+                                            "spec_cache_attend.cu")]
+HEADERS = [os.path.join(INCLUDE, "spec_verify.h"), os.path.join(CSRC, "spec_verify_kernels.cuh"),
+           os.path.join(CSRC, "spec_cache.cuh")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libspec_verify.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -29,6 +31,22 @@ class Options(ctypes.Structure):
 
     _fields_ = [("cluster_size", ctypes.c_int), ("kernel", ctypes.c_int), ("counters", ctypes.c_void_p),
                 ("accept_hist", ctypes.c_void_p)]
+
+
+class Cache(ctypes.Structure):
+    """spec_cache of include/spec_verify.h."""
+
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("k", "v", "k_scale", "v_scale", "positions", "block_table")]
+                + [("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3), ("table_stride", ctypes.c_int64)]
+                + [(f, ctypes.c_int32) for f in ("batch", "max_blocks", "num_pages", "kv_heads", "block", "dim", "code")])
+
+
+class CacheForm(ctypes.Structure):
+    """spec_cache_form of include/spec_verify.h."""
+
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p), ("parent", ctypes.c_void_p),
+                ("num_new", ctypes.c_void_p)]
 
 
 def nvcc_path() -> str:
@@ -105,6 +123,16 @@ def load() -> ctypes.CDLL:
         lib.spec_verify_launch_shape.restype = i32
         lib.spec_device_pointer.argtypes = [vp, ctypes.POINTER(ctypes.c_void_p)]
         lib.spec_device_pointer.restype = i32
+        lib.spec_cache_append.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp]
+        lib.spec_cache_append.restype = i32
+        lib.spec_cache_attend.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, ctypes.c_int64, vp, vp]
+        lib.spec_cache_attend.restype = i32
+        lib.spec_cache_attend_workspace.argtypes = [vp, i32, i32, vp]
+        lib.spec_cache_attend_workspace.restype = i32
+        lib.spec_cache_weigh.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp]
+        lib.spec_cache_weigh.restype = i32
+        lib.spec_cache_evict.argtypes = [vp, vp, vp, i32, i32, vp, ctypes.c_int64, vp, vp, vp, vp]
+        lib.spec_cache_evict.restype = i32
         lib.spec_status_string.argtypes = [i32]
         lib.spec_status_string.restype = ctypes.c_char_p
         _lib = lib

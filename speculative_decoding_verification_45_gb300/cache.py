@@ -1,0 +1,278 @@
+"""The target's key/value cache in 8 bits: Python binding of spec_cache_*.
+
+    cache = KVCache(k, v, k_scale, v_scale)
+    cache_append(cache, block_table, lengths, new_k, new_v)      # lengths: before
+    lengths += n
+    out, lse = cache_attend(q, cache, block_table, lengths)      # the n newest tokens ask
+    cache_weigh(q, cache, block_table, lengths, lse, weights)    # weight each token received
+    lengths, index = cache_evict(cache, block_table, lengths, weights, keep, recent, out_table)
+
+Every call checks its tensors, enqueues its kernels on the current stream (or
+``stream``) and returns; include/spec_verify.h states the operations, layouts and
+error behaviour.  All tensors are CUDA tensors on the cache's device.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import NamedTuple
+
+import torch
+
+from . import _native
+
+_CODES = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+MAX_TREE_NODES = 256
+
+
+class KVCache(NamedTuple):
+    """Blocks ("pages") of cached tokens.
+
+    k, v              [num_pages, kv_heads, block, dim] float8_e4m3fn or
+                      float8_e5m2, any strides that are multiples of 16 with
+                      the last dimension dense (a [num_pages, block, kv_heads,
+                      dim] pool is passed as its transpose(1, 2))
+    k_scale, v_scale  [num_pages, kv_heads] float32: value = code * scale
+    positions         [num_pages, kv_heads, block] int32 or None: each token's
+                      position in its text for the bias by distance
+    """
+
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    positions: torch.Tensor | None = None
+
+
+def _fail(rc: int, where: str):
+    from . import SpecVerifyError
+
+    raise SpecVerifyError(rc, where)
+
+
+def _check(t, name, dtype, shape, device):
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must live on {device}, found {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _cuda(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _strides(t, name, multiple):
+    """Strides of all but the last dimension, which has to be dense (sizes of one do not matter)."""
+    shape, stride = t.shape, t.stride()
+    if shape[-1] > 1 and stride[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    got = [st if n > 1 else multiple for n, st in zip(shape[:-1], stride[:-1])]
+    for st in got:
+        if st % multiple:
+            raise ValueError(f"{name}: strides must be multiples of {multiple}, got {tuple(stride)}")
+    return got
+
+
+def _describe(cache, block_table, lengths):
+    """The spec_cache of these tensors, checked."""
+    k, v = cache.k, cache.v
+    if k.dim() != 4:
+        raise ValueError("cache.k must be a [num_pages, kv_heads, block, dim] tensor")
+    code = _CODES.get(k.dtype)
+    if code is None or v.dtype != k.dtype:
+        raise TypeError(f"cache.k and cache.v must both be float8_e4m3fn or float8_e5m2, got {k.dtype} and {v.dtype}")
+    _cuda(k, "cache.k")
+    dev, shape = k.device, k.shape
+    if v.shape != shape or v.device != dev:
+        raise ValueError(f"cache.v: expected shape {tuple(shape)} on {dev}, got {tuple(v.shape)} on {v.device}")
+    pages, heads, block, dim = shape
+    if block not in (16, 32, 64, 128) or dim not in (64, 128):
+        raise ValueError(f"cache: block must be 16, 32, 64 or 128 and dim 64 or 128, got {block} and {dim}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be a [batch, blocks] tensor")
+    batch, blocks = block_table.shape
+    c = _native.Cache()
+    c.k, c.v = k.data_ptr(), v.data_ptr()
+    c.k_scale = _check(cache.k_scale, "cache.k_scale", torch.float32, (pages, heads), dev)
+    c.v_scale = _check(cache.v_scale, "cache.v_scale", torch.float32, (pages, heads), dev)
+    if cache.positions is not None:
+        c.positions = _check(cache.positions, "cache.positions", torch.int32, (pages, heads, block), dev)
+    if block_table.dtype != torch.int32 or block_table.device != dev or (blocks > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be int32 on {dev} with dense rows")
+    c.block_table = block_table.data_ptr()
+    c.table_stride = block_table.stride(0) if batch > 1 else blocks
+    c.k_stride[:] = _strides(k, "cache.k", 16)
+    c.v_stride[:] = _strides(v, "cache.v", 16)
+    c.batch, c.max_blocks, c.num_pages, c.kv_heads, c.block, c.dim, c.code = batch, blocks, pages, heads, block, dim, code
+    return c, dev, _check(lengths, "lengths", torch.int32, (batch,), dev)
+
+
+def _optional(t, name, dtype, shape, device):
+    return None if t is None else _check(t, name, dtype, shape, device)
+
+
+def _status(t, device):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.device != device or t.numel() < 1 or not t.is_contiguous():
+        raise ValueError(f"status must be a contiguous int32 tensor on {device} with at least one element")
+    return t.data_ptr()
+
+
+def _stream(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _output(t, name, dtype, shape, device):
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _check(t, name, dtype, shape, device)
+
+
+def cache_append(cache, block_table, lengths, k, v, num_new=None, positions=None, status=None, stream=None):
+    """Write new tokens into the cache in 8 bits (spec_cache_append).
+
+    k, v: [batch, n, kv_heads, dim] bfloat16 or float32, any strides with the
+    last dimension dense (slices of a fused projection need no copy).  Token i <
+    num_new[b] becomes cached token lengths[b] + i; ``lengths`` [batch] int32
+    holds the tokens before the call and is not changed.  A block's scale is the
+    smallest power of two that its values fit, and grows (its older codes moving
+    with it) when new tokens need it.  ``num_new`` [batch] int32 or None (n
+    each); ``positions`` [batch, n] int32 or None (the index), stored where the
+    cache has positions.  ``status``: optional int32 CUDA tensor whose first
+    element receives STATUS_* bits.
+    """
+    c, dev, len_ptr = _describe(cache, block_table, lengths)
+    if k.dim() != 4 or k.shape[0] != c.batch or k.shape[2] != c.kv_heads or k.shape[3] != c.dim:
+        raise ValueError(f"k: expected shape ({c.batch}, n, {c.kv_heads}, {c.dim}), got {tuple(k.shape)}")
+    if k.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"k: expected bfloat16 or float32, got {k.dtype}")
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError(f"v: expected {tuple(k.shape)} {k.dtype}, got {tuple(v.shape)} {v.dtype}")
+    if k.device != dev or v.device != dev:
+        raise ValueError(f"k and v must live on {dev}")
+    n = k.shape[1]
+    three = ctypes.c_int64 * 3
+    rc = _native.load().spec_cache_append(
+        ctypes.byref(c), len_ptr, k.data_ptr(), v.data_ptr(), three(*_strides(k, "k", 1)), three(*_strides(v, "v", 1)),
+        n, 1 if k.dtype == torch.bfloat16 else 0, _optional(num_new, "num_new", torch.int32, (c.batch,), dev),
+        _optional(positions, "positions", torch.int32, (c.batch, n), dev), _status(status, dev), _stream(stream, dev))
+    if rc:
+        _fail(rc, "spec_cache_append")
+
+
+def _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent):
+    if q.dim() != 4 or q.shape[0] != c.batch or q.shape[3] != c.dim or q.shape[2] < 1 or q.shape[2] % c.kv_heads:
+        raise ValueError(f"q: expected shape ({c.batch}, n, a multiple of {c.kv_heads}, {c.dim}), got {tuple(q.shape)}")
+    if q.dtype != torch.bfloat16:
+        raise TypeError(f"q: expected torch.bfloat16, got {q.dtype}")
+    if q.device != dev:
+        raise ValueError(f"q must live on {dev}, found {q.device}")
+    n, heads = q.shape[1], q.shape[2]
+    if parent is not None and n > MAX_TREE_NODES:
+        raise ValueError(f"a candidate tree has at most {MAX_TREE_NODES} nodes, got {n}")
+    if window < 0 or not 0 <= softcap < math.inf:
+        raise ValueError("window and softcap must not be negative")
+    f = _native.CacheForm(
+        1 / math.sqrt(c.dim) if scale is None else scale, softcap, window,
+        _optional(slopes, "slopes", torch.float32, (heads,), dev),
+        _optional(prefix, "prefix", torch.int32, (c.batch,), dev),
+        _optional(parent, "parent", torch.int32, (c.batch, n), dev),
+        _optional(num_new, "num_new", torch.int32, (c.batch,), dev))
+    return f, n, heads, (ctypes.c_int64 * 3)(*_strides(q, "q", 8))
+
+
+def cache_attend(q, cache, block_table, lengths, num_new=None, scale=None, softcap=0.0, slopes=None, window=0,
+                 prefix=None, parent=None, out=None, lse=None, status=None, stream=None):
+    """Attention of the newest tokens over the cache (spec_cache_attend).
+
+    q: [batch, n, heads, dim] bfloat16; query i < num_new[b] (None: n) is cached
+    token lengths[b] - num_new[b] + i, so ``lengths`` counts the new tokens too.
+    Returns (out [batch, n, heads, dim] bfloat16, lse [batch, n, heads] float32).
+
+    scale    factor of q.k, 1/sqrt(dim) when None
+    softcap  scores become softcap * tanh(score / softcap) where it is > 0
+    slopes   [heads] float32: score -= slope * |distance in position|
+    window   > 0: a query sees the last ``window`` tokens up to its own
+    prefix   [batch] int32: tokens before it are seen by every query
+    parent   [batch, n] int32: the n queries are a candidate tree, as in
+             tree_verify (node 0 the root); a node sees its ancestors
+
+    Rows that see nothing, and rows i >= num_new[b], are zeros with lse -inf.
+    """
+    c, dev, len_ptr = _describe(cache, block_table, lengths)
+    f, n, heads, stride = _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent)
+    out, out_ptr = _output(out, "out", torch.bfloat16, (c.batch, n, heads, c.dim), dev)
+    lse, lse_ptr = _output(lse, "lse", torch.float32, (c.batch, n, heads), dev)
+    lib = _native.load()
+    need = ctypes.c_int64()
+    rc = lib.spec_cache_attend_workspace(ctypes.byref(c), n, heads, ctypes.byref(need))
+    if rc:
+        _fail(rc, "spec_cache_attend_workspace")
+    if stream is None:
+        work = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    else:
+        with torch.cuda.stream(stream):  # the block belongs to the stream that uses it
+            work = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    rc = lib.spec_cache_attend(ctypes.byref(c), len_ptr, q.data_ptr(), stride, n, heads, ctypes.byref(f), out_ptr,
+                               lse_ptr, work.data_ptr(), need.value, _status(status, dev), _stream(stream, dev))
+    if rc:
+        _fail(rc, "spec_cache_attend")
+    return out, lse
+
+
+def cache_weigh(q, cache, block_table, lengths, lse, weights, num_new=None, scale=None, softcap=0.0, slopes=None,
+                window=0, prefix=None, parent=None, status=None, stream=None):
+    """Add the attention weight that each cached token received (spec_cache_weigh).
+
+    ``lse`` is what cache_attend returned for the same q and form; ``weights``
+    [num_pages, kv_heads, block] float32 grows by the sum over queries and query
+    heads of exp(score - lse).  Returns ``weights``.
+    """
+    c, dev, len_ptr = _describe(cache, block_table, lengths)
+    f, n, heads, stride = _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent)
+    lse_ptr = _check(lse, "lse", torch.float32, (c.batch, n, heads), dev)
+    w_ptr = _check(weights, "weights", torch.float32, (c.num_pages, c.kv_heads, c.block), dev)
+    rc = _native.load().spec_cache_weigh(ctypes.byref(c), len_ptr, q.data_ptr(), stride, n, heads, ctypes.byref(f),
+                                         lse_ptr, w_ptr, _status(status, dev), _stream(stream, dev))
+    if rc:
+        _fail(rc, "spec_cache_weigh")
+    return weights
+
+
+def cache_evict(cache, block_table, lengths, weights, keep: int, recent: int, out_table, out_lengths=None,
+                out_index=None, status=None, stream=None):
+    """Keep the heaviest and the newest tokens (spec_cache_evict).
+
+    Of each sequence and key/value head the ``recent`` newest tokens stay and,
+    of the others, the ``keep - recent`` with the largest ``weights``.  They move
+    in order, with their weights and positions, to the pages of ``out_table``
+    [batch, >= ceil(keep / block)] int32, which no sequence may use yet; the
+    old pages are free afterwards.  Returns (lengths [batch] int32, the kept
+    indices [batch, kv_heads, keep] int32, -1 after the last).
+    """
+    c, dev, len_ptr = _describe(cache, block_table, lengths)
+    if keep < 1 or not 0 <= recent <= keep:
+        raise ValueError(f"keep must be at least 1 and recent in [0, keep], got {keep} and {recent}")
+    blocks = -(-keep // c.block)
+    if out_table.dim() != 2 or out_table.shape[0] != c.batch or out_table.shape[1] < blocks:
+        raise ValueError(f"out_table: expected shape ({c.batch}, at least {blocks}), got {tuple(out_table.shape)}")
+    if out_table.dtype != torch.int32 or out_table.device != dev or (out_table.shape[1] > 1 and out_table.stride(1) != 1):
+        raise ValueError(f"out_table must be int32 on {dev} with dense rows")
+    w_ptr = _check(weights, "weights", torch.float32, (c.num_pages, c.kv_heads, c.block), dev)
+    out_lengths, l_ptr = _output(out_lengths, "out_lengths", torch.int32, (c.batch,), dev)
+    out_index, i_ptr = _output(out_index, "out_index", torch.int32, (c.batch, c.kv_heads, keep), dev)
+    rc = _native.load().spec_cache_evict(
+        ctypes.byref(c), len_ptr, w_ptr, keep, recent, out_table.data_ptr(),
+        out_table.stride(0) if c.batch > 1 else out_table.shape[1], l_ptr, i_ptr, _status(status, dev),
+        _stream(stream, dev))
+    if rc:
+        _fail(rc, "spec_cache_evict")
+    return out_lengths, out_index

@@ -1,0 +1,496 @@
+// spec_cache_move.cu -- writing tokens into the 8-bit key/value cache and
+// moving the kept ones out of it (spec_cache_append, spec_cache_evict).
+
+#include "spec_cache.cuh"
+
+using namespace specc;
+
+namespace {
+
+// ===========================================================================
+// Append
+// ===========================================================================
+// One unit is one block of one sequence, head and side (keys or values): its
+// scale depends on nothing else.  The unit's new values are read once, kept in
+// registers as 8-value chunks while their largest magnitude is found, and
+// written as codes.  T threads serve a unit: a warp for the few tokens of a
+// round, 256 threads for a prompt's whole blocks.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendSmall = 16;  // new tokens up to which a warp's registers hold a unit (8 chunks a lane)
+
+struct AppendArgs {
+    spec_cache c;
+    const int32_t *lengths, *num_new, *positions;
+    const void *x[2];
+    int64_t stride[2][3];
+    int n, blocks;  // blocks a sequence may touch
+    uint32_t *status;
+};
+
+template <typename X> struct Chunk;
+template <> struct Chunk<__nv_bfloat16> {
+    uint4 raw;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool aligned)
+    {
+        if (aligned) {
+            raw = __ldg((const uint4 *)p);
+        } else {
+            const unsigned short *s = (const unsigned short *)p;
+            raw = make_uint4(s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)s[3] << 16, s[4] | (uint32_t)s[5] << 16,
+                             s[6] | (uint32_t)s[7] << 16);
+        }
+    }
+    __device__ __forceinline__ float2 two(int i) const
+    {
+        const uint32_t w = i == 0 ? raw.x : i == 1 ? raw.y : i == 2 ? raw.z : raw.w;
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+};
+template <> struct Chunk<float> {
+    float4 lo, hi;
+    __device__ __forceinline__ void load(const float *p, bool aligned)
+    {
+        if (aligned) {
+            lo = __ldg((const float4 *)p);
+            hi = __ldg((const float4 *)p + 1);
+        } else {
+            lo = make_float4(p[0], p[1], p[2], p[3]);
+            hi = make_float4(p[4], p[5], p[6], p[7]);
+        }
+    }
+    __device__ __forceinline__ float2 two(int i) const
+    {
+        return i == 0 ? make_float2(lo.x, lo.y) : i == 1 ? make_float2(lo.z, lo.w)
+               : i == 2 ? make_float2(hi.x, hi.y) : make_float2(hi.z, hi.w);
+    }
+};
+
+template <typename X, int T>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a)
+{
+    constexpr int kUnits = kAppendThreads / T;  // units of a CTA
+    constexpr int kChunks = 8;                  // at most: 128 tokens x 128 / 8 / 256, or 16 x 128 / 8 / 32
+    const spec_cache &c = a.c;
+    const int sub = threadIdx.x / T, t = threadIdx.x % T;
+    const long long units = (long long)c.batch * a.blocks * c.kv_heads * 2;
+    const long long u = (long long)blockIdx.x * kUnits + sub;
+    const bool here = u < units;
+    const long long u1 = here ? u : 0;
+    const int side = (int)(u1 & 1);
+    const int h = (int)((u1 >> 1) % c.kv_heads);
+    const long long u2 = (u1 >> 1) / c.kv_heads;
+    const int k = (int)(u2 % a.blocks), b = (int)(u2 / a.blocks);
+    const Seq s = sequence(c, a.lengths, a.num_new, a.n, b, false);
+    if (here && t == 0 && !s.ok && k == 0 && side == 0 && h == 0)
+        report(a.status, SPEC_STATUS_BAD_LENGTH);
+    const int P = c.block, blk = s.len / P + k;
+    const long long start = (long long)blk * P;
+    const int old = max(0, (int)((long long)s.len - start));             // tokens that the block holds
+    const int put = (int)min((long long)P, (long long)s.len + s.m - start) - old;  // tokens to write
+    bool live = here && s.ok && put > 0;
+    int page = -1;
+    if (live) {
+        page = page_of(c, b, blk);
+        if (page < 0 && t == 0)
+            report(a.status, SPEC_STATUS_BAD_PAGE);
+        live = page >= 0;
+    }
+    const int per = c.dim / 8;  // chunks of a token: 8 or 16
+    const int shift = c.dim == 64 ? 3 : 4;
+    const int todo = live ? put * per : 0;
+    const int i0 = (int)(start + old - s.len);  // index of the first token of this block among the new ones
+    const X *src = (const X *)a.x[side] + (size_t)b * a.stride[side][0] + (size_t)h * a.stride[side][2];
+    const bool aligned = (((uintptr_t)a.x[side] | (uintptr_t)(a.stride[side][0] * sizeof(X)) |
+                           (uintptr_t)(a.stride[side][1] * sizeof(X)) | (uintptr_t)(a.stride[side][2] * sizeof(X))) &
+                          15u) == 0;
+    Chunk<X> x[kChunks];
+    float amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+        const int q = t + j * T;
+        if (q < todo)
+            x[j].load(src + (size_t)(i0 + (q >> shift)) * a.stride[side][1] + (q & (per - 1)) * 8, aligned);
+    }
+    float *scale = (side ? c.v_scale : c.k_scale) + (size_t)max(page, 0) * c.kv_heads + h;
+    const float had = live && old ? *scale : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+        if (t + j * T < todo) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = x[j].two(i);
+                amax = isfinite(v.x) ? fmaxf(amax, fabsf(v.x)) : amax;
+                amax = isfinite(v.y) ? fmaxf(amax, fabsf(v.y)) : amax;
+            }
+        }
+    }
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+    if (T > 32) {
+        __shared__ float part[kAppendThreads / 32];
+        if ((threadIdx.x & 31) == 0)
+            part[threadIdx.x >> 5] = amax;
+        __syncthreads();  // also: every thread has read the old scale
+#pragma unroll
+        for (int w = 0; w < kAppendThreads / 32; ++w)
+            amax = fmaxf(amax, part[w]);
+    } else {
+        __syncwarp();
+    }
+    if (!live)
+        return;
+    const float now = fmaxf(scale_for(amax, c.code), had);
+    const int64_t *cs = side ? c.v_stride : c.k_stride;
+    uint8_t *dst = (uint8_t *)(side ? c.v : c.k) + (size_t)page * cs[0] + (size_t)h * cs[1];
+    const Divider over(now);
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+        const int q = t + j * T;
+        if (q < todo) {
+            uint32_t w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 lo = x[j].two(2 * i), hi = x[j].two(2 * i + 1);
+                w[i] = (uint32_t)encode2(over(lo.x), over(lo.y), c.code) |
+                       (uint32_t)encode2(over(hi.x), over(hi.y), c.code) << 16;
+            }
+            *(uint2 *)(dst + (size_t)(old + (q >> shift)) * cs[2] + (q & (per - 1)) * 8) = make_uint2(w[0], w[1]);
+        }
+    }
+    if (old && now != had) {  // the block's scale grew: its older codes move to the new one
+        const float f = had / now;
+        for (int q = t; q < old * per; q += T) {
+            uint2 *p = (uint2 *)(dst + (size_t)(q >> shift) * cs[2] + (q & (per - 1)) * 8);
+            uint2 w = *p;
+            uint32_t r[2] = {w.x, w.y};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 lo = decode2((uint16_t)r[i], c.code), hi = decode2((uint16_t)(r[i] >> 16), c.code);
+                r[i] = (uint32_t)encode2(lo.x * f, lo.y * f, c.code) |
+                       (uint32_t)encode2(hi.x * f, hi.y * f, c.code) << 16;
+            }
+            *p = make_uint2(r[0], r[1]);
+        }
+    }
+    if (t == 0)
+        *scale = now;
+    if (side == 0 && c.positions)
+        for (int q = t; q < put; q += T)
+            c.positions[((size_t)page * c.kv_heads + h) * P + old + q] =
+                a.positions ? a.positions[(size_t)b * a.n + i0 + q] : s.len + i0 + q;
+}
+
+// ===========================================================================
+// Evict
+// ===========================================================================
+// Two kernels: one CTA per (sequence, head) finds the kept indices, then one
+// CTA per block of kept tokens moves them.  Sources and destinations share no
+// page, so the moves need no order.
+constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kMoveThreads = 256;
+
+struct EvictArgs {
+    spec_cache c;
+    const int32_t *lengths, *out_table;
+    float *weights;
+    int64_t out_stride;
+    int32_t *out_lengths, *out_index;
+    int keep, recent;
+    uint32_t *status;
+};
+
+// Weight to an unsigned key of the same order: NaN lowest, both zeros alike.
+__device__ __forceinline__ uint32_t weight_key(float w)
+{
+    if (w != w)
+        return 0u;
+    const uint32_t u = __float_as_uint(w + 0.0f);
+    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ uint32_t key_at(const EvictArgs &a, int b, int h, int j)
+{
+    const int page = page_of(a.c, b, j / a.c.block);
+    return page < 0 ? 0u : weight_key(a.weights[((size_t)page * a.c.kv_heads + h) * a.c.block + j % a.c.block]);
+}
+
+// The (keep - recent)-th largest key is found one byte at a time from the top
+// (a histogram of the keys that share the bytes found so far); then each warp
+// counts its stretch of tokens above the key and equal to it, and a second walk
+// writes the indices in order.  The keys are kept in shared memory where they
+// fit (`staged`), else read again from L2.
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs a, int staged)
+{
+    extern __shared__ uint32_t keys[];
+    __shared__ uint32_t hist[256];
+    __shared__ int count[2][kSelectWarps];
+    __shared__ uint32_t found, left;
+    const spec_cache &c = a.c;
+    const int h = blockIdx.x % c.kv_heads, b = blockIdx.x / c.kv_heads;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const Seq s = sequence(c, a.lengths, nullptr, 0, b, true);
+    if (tid == 0 && h == 0) {
+        if (!s.ok)
+            report(a.status, SPEC_STATUS_BAD_LENGTH);
+        a.out_lengths[b] = min(s.len, a.keep);
+    }
+    int32_t *index = a.out_index + ((size_t)b * c.kv_heads + h) * a.keep;
+    for (int i = min(s.len, a.keep) + tid; i < a.keep; i += kSelectThreads)
+        index[i] = -1;
+    if (s.len <= a.keep) {
+        for (int i = tid; i < s.len; i += kSelectThreads)
+            index[i] = i;
+        return;
+    }
+    const int cand = s.len - a.recent, want = a.keep - a.recent;  // want < cand
+    for (int i = tid; i < a.recent; i += kSelectThreads)
+        index[want + i] = cand + i;
+    if (want == 0)
+        return;
+    uint32_t prefix = 0;
+    uint32_t need = (uint32_t)want;  // rank of the wanted key among those that share `prefix`
+    for (int byte = 3; byte >= 0; --byte) {
+        if (tid < 256)
+            hist[tid] = 0;
+        __syncthreads();
+        for (int j0 = 0; j0 < cand; j0 += kSelectThreads) {
+            const int j = j0 + tid;
+            bool in = j < cand;
+            uint32_t key = 0;
+            if (in) {
+                key = (staged && byte < 3) ? keys[j] : key_at(a, b, h, j);
+                if (staged && byte == 3)
+                    keys[j] = key;
+                in = byte == 3 || (key >> (8 * byte + 8)) == prefix;
+            }
+            // lanes with the same digit add once
+            const uint32_t digit = in ? (key >> (8 * byte)) & 255u : 256u;
+            const uint32_t same = __match_any_sync(0xffffffffu, digit);
+            if (in && lane == __ffs(same) - 1)
+                atomicAdd(&hist[digit], (uint32_t)__popc(same));
+        }
+        __syncthreads();
+        if (wid == 0) {  // the digit where the count from the top reaches `need`
+            uint32_t mine[8], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                mine[i] = hist[255 - (lane * 8 + i)];
+                sum += mine[i];
+            }
+            uint32_t before = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
+                before += lane >= o ? y : 0;
+            }
+            before -= sum;
+            if (before < need && need <= before + sum) {
+                int i = 0;
+                while (before + mine[i] < need)
+                    before += mine[i++];
+                found = 255 - (lane * 8 + i);
+                left = need - before;
+            }
+        }
+        __syncthreads();
+        prefix = prefix << 8 | found;
+        need = left;
+    }
+    // tokens above the key `prefix` are all kept, of those equal to it the first `need`
+    const int each = ((cand + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
+    const int lo = min(cand, wid * each), hi = min(cand, lo + each);
+    int above = 0, equal = 0;
+    for (int j0 = lo; j0 < hi; j0 += 32) {
+        const int j = j0 + lane;
+        const uint32_t key = j < hi ? (staged ? keys[j] : key_at(a, b, h, j)) : 0;
+        above += __popc(__ballot_sync(0xffffffffu, j < hi && key > prefix));
+        equal += __popc(__ballot_sync(0xffffffffu, j < hi && key == prefix));
+    }
+    if (lane == 0) {
+        count[0][wid] = above;
+        count[1][wid] = equal;
+    }
+    __syncthreads();
+    int at = 0, ties = 0;
+    for (int w = 0; w < wid; ++w) {
+        at += count[0][w];
+        ties += count[1][w];
+    }
+    int out = at + min(ties, (int)need);  // kept tokens before this warp's stretch
+    const uint32_t below = (1u << lane) - 1;
+    for (int j0 = lo; j0 < hi; j0 += 32) {
+        const int j = j0 + lane;
+        const uint32_t key = j < hi ? (staged ? keys[j] : key_at(a, b, h, j)) : 0;
+        const bool eq = j < hi && key == prefix;
+        const uint32_t tie = __ballot_sync(0xffffffffu, eq);
+        const bool take = (j < hi && key > prefix) || (eq && ties + __popc(tie & below) < (int)need);
+        const uint32_t took = __ballot_sync(0xffffffffu, take);
+        if (take)
+            index[out + __popc(took & below)] = j;
+        out += __popc(took);
+        ties += __popc(tie);
+    }
+}
+
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, int blocks)
+{
+    __shared__ int from[kMaxBlock];          // source page of each token, -1: none
+    __shared__ float had[2][kMaxBlock];      // its scales
+    __shared__ int row[kMaxBlock];
+    const spec_cache &c = a.c;
+    const int P = c.block, tid = threadIdx.x;
+    const int k = blockIdx.x % blocks;
+    const int h = (blockIdx.x / blocks) % c.kv_heads, b = blockIdx.x / blocks / c.kv_heads;
+    const int to = a.out_table[(size_t)b * a.out_stride + k];
+    const int kept = min(sequence(c, a.lengths, nullptr, 0, b, true).len, a.keep);
+    const int n = min(P, kept - k * P);
+    if (n <= 0)
+        return;
+    if ((unsigned)to >= (unsigned)c.num_pages) {
+        if (tid == 0)
+            report(a.status, SPEC_STATUS_BAD_PAGE);
+        return;
+    }
+    if (tid < n) {
+        const int j = a.out_index[((size_t)b * c.kv_heads + h) * a.keep + k * P + tid];
+        const int page = page_of(c, b, j / P);
+        if (page < 0)
+            report(a.status, SPEC_STATUS_BAD_PAGE);
+        from[tid] = page;
+        row[tid] = j % P;
+        const size_t src = (size_t)max(page, 0) * c.kv_heads + h, dst = ((size_t)to * c.kv_heads + h) * P + tid;
+        had[0][tid] = page < 0 ? 0.0f : c.k_scale[src];
+        had[1][tid] = page < 0 ? 0.0f : c.v_scale[src];
+        a.weights[dst] = page < 0 ? 0.0f : a.weights[src * P + j % P];
+        if (c.positions)
+            c.positions[dst] = page < 0 ? 0 : c.positions[src * P + j % P];
+    }
+    __syncthreads();
+    float now[2] = {0.0f, 0.0f};
+    for (int i = tid & 31; i < n; i += 32) {
+        now[0] = fmaxf(now[0], had[0][i]);
+        now[1] = fmaxf(now[1], had[1][i]);
+    }
+    // scales are positive: their bits order as they do
+    now[0] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(now[0])));
+    now[1] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(now[1])));
+    if (tid < 2) {
+        float *scale = tid ? c.v_scale : c.k_scale;
+        scale[(size_t)to * c.kv_heads + h] = now[tid];
+    }
+    const int shift = c.dim == 64 ? 2 : 3;  // 16-byte chunks of a token
+    for (int q = tid; q < 2 * (n << shift); q += kMoveThreads) {
+        const int side = q >= (n << shift);
+        const int r = q - side * (n << shift), i = r >> shift, d = (r & ((1 << shift) - 1)) * 16;
+        const int64_t *cs = side ? c.v_stride : c.k_stride;
+        uint8_t *base = (uint8_t *)(side ? c.v : c.k) + (size_t)h * cs[1] + d;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (from[i] >= 0) {
+            w = *(const uint4 *)(base + (size_t)from[i] * cs[0] + (size_t)row[i] * cs[2]);
+            if (had[side][i] != now[side]) {
+                const float f = had[side][i] / now[side];
+                uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 lo = decode2((uint16_t)x[e], c.code), hi = decode2((uint16_t)(x[e] >> 16), c.code);
+                    x[e] = (uint32_t)encode2(lo.x * f, lo.y * f, c.code) |
+                           (uint32_t)encode2(hi.x * f, hi.y * f, c.code) << 16;
+                }
+                w = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+        }
+        *(uint4 *)(base + (size_t)to * cs[0] + (size_t)i * cs[2]) = w;
+    }
+}
+
+template <typename X, int T> spec_status run_append(const AppendArgs &a, cudaStream_t stream)
+{
+    const long long units = (long long)a.c.batch * a.blocks * a.c.kv_heads * 2;
+    const long long ctas = (units + kAppendThreads / T - 1) / (kAppendThreads / T);
+    if (ctas > INT_MAX)
+        return SPEC_ERR_UNSUPPORTED;
+    append_kernel<X, T><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(a);
+    return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+spec_status spec_cache_append(const spec_cache *cache, const int32_t *lengths, const void *k, const void *v,
+                              const int64_t k_stride[3], const int64_t v_stride[3], int n, spec_dtype dtype,
+                              const int32_t *num_new, const int32_t *positions, uint32_t *status, void *stream)
+{
+    NvtxScope nvtx("spec_cache_append");
+    spec_status st = check_cache(cache);
+    if (st != SPEC_OK)
+        return st;
+    if (dtype != SPEC_F32 && dtype != SPEC_BF16)
+        return SPEC_ERR_UNSUPPORTED;
+    if (n < 0 || n > INT_MAX / 2)
+        return SPEC_ERR_INVALID_ARG;
+    if (cache->batch == 0 || n == 0)
+        return SPEC_OK;
+    const uintptr_t mask = dtype == SPEC_F32 ? 3u : 1u;
+    if (!k || !v || !k_stride || !v_stride || ((uintptr_t)k & mask) || ((uintptr_t)v & mask) ||
+        bad4(lengths, true) || bad4(num_new, false) || bad4(positions, false) || bad4(status, false))
+        return SPEC_ERR_INVALID_ARG;
+    AppendArgs a;
+    a.c = *cache;
+    a.lengths = lengths;
+    a.num_new = num_new;
+    a.positions = positions;
+    a.x[0] = k;
+    a.x[1] = v;
+    for (int i = 0; i < 3; ++i) {
+        a.stride[0][i] = k_stride[i];
+        a.stride[1][i] = v_stride[i];
+    }
+    a.n = n;
+    a.blocks = (n + cache->block - 2) / cache->block + 1;
+    a.status = status;
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (dtype == SPEC_F32)
+        return n <= kAppendSmall ? run_append<float, 32>(a, s) : run_append<float, kAppendThreads>(a, s);
+    return n <= kAppendSmall ? run_append<__nv_bfloat16, 32>(a, s) : run_append<__nv_bfloat16, kAppendThreads>(a, s);
+}
+
+spec_status spec_cache_evict(const spec_cache *cache, const int32_t *lengths, float *weights, int keep, int recent,
+                             const int32_t *out_table, int64_t out_stride, int32_t *out_lengths, int32_t *out_index,
+                             uint32_t *status, void *stream)
+{
+    NvtxScope nvtx("spec_cache_evict");
+    spec_status st = check_cache(cache);
+    if (st != SPEC_OK)
+        return st;
+    if (keep < 1 || keep > INT_MAX / 2 || recent < 0 || recent > keep)
+        return SPEC_ERR_INVALID_ARG;
+    if (cache->batch == 0)
+        return SPEC_OK;
+    const int blocks = (keep + cache->block - 1) / cache->block;
+    if (bad4(lengths, true) || bad4(weights, true) || bad4(out_table, true) || bad4(out_lengths, true) ||
+        bad4(out_index, true) || bad4(status, false) || out_stride < blocks)
+        return SPEC_ERR_INVALID_ARG;
+    const long long heads = (long long)cache->batch * cache->kv_heads;
+    if (heads * blocks > INT_MAX)
+        return SPEC_ERR_UNSUPPORTED;
+    EvictArgs a{*cache, lengths, out_table, weights, out_stride, out_lengths, out_index, keep, recent, status};
+    const cudaStream_t s = (cudaStream_t)stream;
+    // shared memory for the keys of the longest sequence; up to 48 KB needs no opt-in
+    const long long room = (long long)cache->max_blocks * cache->block;
+    const long long bytes = room * 4;
+    const int staged = bytes <= 200 * 1024;
+    if (staged && bytes > 46 * 1024 &&
+        cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess) {
+        cudaGetLastError();
+        return SPEC_ERR_CUDA;
+    }
+    select_kernel<<<(unsigned)heads, kSelectThreads, staged ? (size_t)bytes : 0, s>>>(a, staged);
+    st = launched();
+    if (st != SPEC_OK)
+        return st;
+    move_kernel<<<(unsigned)(heads * blocks), kMoveThreads, 0, s>>>(a, blocks);
+    return launched();
+}
+
+}  // extern "C"
