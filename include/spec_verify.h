@@ -128,6 +128,8 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 /* spec_cache_*: a length or a number of new tokens out of range; a page id out of range. */
 #define SPEC_STATUS_BAD_LENGTH 64u
 #define SPEC_STATUS_BAD_PAGE 128u
+/* spec_cache_*: a bounded wait inside a kernel ran out; the call's outputs are not valid. */
+#define SPEC_STATUS_INTERNAL 256u
 
 /* One verification round for B independent sequences (see the top of this
  * file for the operation, layout, ownership and errors).

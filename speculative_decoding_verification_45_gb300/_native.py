@@ -12,12 +12,13 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
-# The host unit, one unit per (dtype, proposal form) of kernels, and the cache's two: compiled in parallel.
+# The host unit, one unit per (dtype, proposal form) of kernels, and the cache's four: compiled in parallel.
 SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "kernels_bf16.cu", "kernels_bf16_point.cu",
                                             "kernels_f32.cu", "kernels_f32_point.cu", "spec_cache_move.cu",
-                                            "spec_cache_attend.cu")]
+                                            "spec_cache_attend.cu", "spec_cache_attend_d64.cu",
+                                            "spec_cache_attend_d128.cu")]
 HEADERS = [os.path.join(INCLUDE, "spec_verify.h"), os.path.join(CSRC, "spec_verify_kernels.cuh"),
-           os.path.join(CSRC, "spec_cache.cuh")]
+           os.path.join(CSRC, "spec_cache.cuh"), os.path.join(CSRC, "spec_cache_attend.cuh")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libspec_verify.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,193 +1,15 @@
-// spec_cache_attend.cu -- attention over the 8-bit key/value cache and the
-// attention weight that each cached token received (spec_cache_attend,
-// spec_cache_weigh).
+// spec_cache_attend.cu -- host side of attention over the 8-bit key/value cache
+// and of the weights that its tokens received (spec_cache_attend,
+// spec_cache_weigh): argument checks, the launch, the tensor maps.  The kernels
+// are in spec_cache_attend.cuh.
 
-#include "spec_cache.cuh"
+#include <atomic>
+
+#include "spec_cache_attend.cuh"
 
 using namespace specc;
 
 namespace {
-
-struct AttendArgs {
-    spec_cache c;
-    spec_cache_form f;
-    const int32_t *lengths;
-    const __nv_bfloat16 *q;
-    int64_t q_stride[3];
-    int n, heads;
-    __nv_bfloat16 *out;
-    float *lse;
-    const float *lse_in;
-    float *weights;
-    uint32_t *status;
-};
-
-// Does query i (at index at) see token j < s.len?
-__device__ __forceinline__ bool sees(const AttendArgs &a, const Seq &s, int b, int i, int j)
-{
-    const int at = s.len - s.m + i;
-    bool see;
-    if (!a.f.parent) {
-        see = j <= at;
-    } else {
-        const int t = j - (s.len - s.m);
-        int k = i;
-        while (k > t && t >= 0) {
-            const int p = k > 0 ? a.f.parent[(size_t)b * a.n + k] : -1;
-            k = p < k ? p : -1;
-        }
-        see = t < 0 || k == t;
-    }
-    if (a.f.window > 0)
-        see = see && j > at - a.f.window;
-    return see || (a.f.prefix && j < a.f.prefix[b]);
-}
-
-// A row's query, scaled score of one token, for a lane that holds the token.
-__device__ __forceinline__ float score(const AttendArgs &a, const float *q, int page, int h, int row, float slope,
-                                       float pos_q, int j)
-{
-    const spec_cache &c = a.c;
-    const uint8_t *k = (const uint8_t *)c.k + (size_t)page * c.k_stride[0] + (size_t)h * c.k_stride[1] +
-                       (size_t)row * c.k_stride[2];
-    float dot = 0.0f;
-    for (int d = 0; d < c.dim; d += 2) {
-        const float2 v = decode2(*(const uint16_t *)(k + d), c.code);
-        dot += v.x * q[d] + v.y * q[d + 1];
-    }
-    float x = dot * (c.k_scale[(size_t)page * c.kv_heads + h] * a.f.scale);
-    if (a.f.softcap > 0.0f)
-        x = a.f.softcap * tanhf(x / a.f.softcap);
-    if (a.f.slopes) {
-        const float p = (float)(c.positions ? c.positions[((size_t)page * c.kv_heads + h) * c.block + row] : j);
-        x -= slope * fabsf(pos_q - p);
-    }
-    return x;
-}
-
-__device__ __forceinline__ float query_position(const AttendArgs &a, int b, int h, int at)
-{
-    if (!a.c.positions)
-        return (float)at;
-    const int page = page_of(a.c, b, at / a.c.block);
-    return page < 0 ? 0.0f : (float)a.c.positions[((size_t)page * a.c.kv_heads + h) * a.c.block + at % a.c.block];
-}
-
-// One warp per query row: a lane scores one token of every 32, then all lanes
-// add the 32 tokens' values, each its own dimensions.
-__global__ void __launch_bounds__(128) attend_kernel(const AttendArgs a)
-{
-    __shared__ float sq[4][128];
-    const spec_cache &c = a.c;
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, D = c.dim;
-    const long long r = (long long)blockIdx.x * 4 + wid;
-    if (r >= (long long)c.batch * a.n * a.heads)
-        return;
-    const int H = (int)(r % a.heads), i = (int)(r / a.heads % a.n), b = (int)(r / a.heads / a.n);
-    const int h = H / (a.heads / c.kv_heads);
-    const Seq s = sequence(c, a.lengths, a.f.num_new, a.n, b, true);
-    if (!s.ok && lane == 0)
-        report(a.status, SPEC_STATUS_BAD_LENGTH);
-    if (a.f.parent && lane == 0 && i > 0 && i < s.m && (unsigned)a.f.parent[(size_t)b * a.n + i] >= (unsigned)i)
-        report(a.status, SPEC_STATUS_BAD_TREE);
-    float *q = sq[wid];
-    for (int d = lane; d < D; d += 32)
-        q[d] = __bfloat162float(a.q[b * a.q_stride[0] + i * a.q_stride[1] + H * a.q_stride[2] + d]);
-    __syncwarp();
-    const bool live = i < s.m;
-    const float slope = a.f.slopes ? a.f.slopes[H] : 0.0f;
-    const float pos_q = live && a.f.slopes ? query_position(a, b, h, s.len - s.m + i) : 0.0f;
-    float m = -INFINITY, l = 0.0f, o[4] = {0, 0, 0, 0};
-    for (int j0 = 0; live && j0 < s.len; j0 += 32) {
-        const int j = j0 + lane;
-        int page = -1;
-        float x = -INFINITY;
-        bool see = false;
-        if (j < s.len) {
-            page = page_of(c, b, j / c.block);
-            see = sees(a, s, b, i, j);
-            if (page < 0 && see)
-                report(a.status, SPEC_STATUS_BAD_PAGE);
-            see = see && page >= 0;
-            if (see)
-                x = score(a, q, page, h, j % c.block, slope, pos_q, j);
-        }
-        const bool nan = __any_sync(0xffffffffu, x != x);
-        float top = nan ? NAN : x;
-        for (int w = 16; w > 0; w >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-        if (nan)
-            top = NAN;
-        if (top == -INFINITY)
-            continue;
-        const float now = nan ? NAN : fmaxf(m, top);
-        const float keep = m == -INFINITY ? 0.0f : expf(m - now);
-        const float p = see ? expf(x - now) : 0.0f;
-        float add = p;
-        for (int w = 16; w > 0; w >>= 1)
-            add += __shfl_xor_sync(0xffffffffu, add, w);
-        l = l * keep + add;
-        m = now;
-        for (int d = 0; d < 4; ++d)
-            o[d] *= keep;
-        for (int t = 0; t < 32; ++t) {
-            const float pt = __shfl_sync(0xffffffffu, p, t);
-            const int pg = __shfl_sync(0xffffffffu, page, t);
-            if (!__shfl_sync(0xffffffffu, (int)see, t))
-                continue;
-            const uint8_t *v = (const uint8_t *)c.v + (size_t)pg * c.v_stride[0] + (size_t)h * c.v_stride[1] +
-                               (size_t)((j0 + t) % c.block) * c.v_stride[2];
-            const float w = pt * c.v_scale[(size_t)pg * c.kv_heads + h];
-            for (int d = 0; d < D / 64; ++d) {
-                const float2 x2 = decode2(*(const uint16_t *)(v + d * 64 + lane * 2), c.code);
-                o[2 * d] += w * x2.x;
-                o[2 * d + 1] += w * x2.y;
-            }
-        }
-    }
-    for (int d = 0; d < D / 64; ++d) {
-        __nv_bfloat16 *dst = a.out + r * D + d * 64 + lane * 2;
-        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-        dst[0] = __float2bfloat16(o[2 * d] * inv);
-        dst[1] = __float2bfloat16(o[2 * d + 1] * inv);
-    }
-    if (lane == 0)
-        a.lse[r] = l > 0.0f || l != l ? m + logf(l) : -INFINITY;
-}
-
-// One warp per 32 tokens of a sequence and head, a lane per token, all rows.
-__global__ void __launch_bounds__(128) weigh_kernel(const AttendArgs a, int chunks)
-{
-    __shared__ float sq[4][128];
-    const spec_cache &c = a.c;
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, D = c.dim, G = a.heads / c.kv_heads;
-    const long long u = (long long)blockIdx.x * 4 + wid;
-    if (u >= (long long)c.batch * c.kv_heads * chunks)
-        return;
-    const int j = (int)(u % chunks) * 32 + lane;
-    const int h = (int)(u / chunks % c.kv_heads), b = (int)(u / chunks / c.kv_heads);
-    const Seq s = sequence(c, a.lengths, a.f.num_new, a.n, b, true);
-    if (!s.ok && lane == 0)
-        report(a.status, SPEC_STATUS_BAD_LENGTH);
-    const int page = j < s.len ? page_of(c, b, j / c.block) : -1;
-    if (j < s.len && page < 0)
-        report(a.status, SPEC_STATUS_BAD_PAGE);
-    float *q = sq[wid], sum = 0.0f;
-    for (int i = 0; i < s.m; ++i)
-        for (int g = 0; g < G; ++g) {
-            const int H = h * G + g;
-            __syncwarp();
-            for (int d = lane; d < D; d += 32)
-                q[d] = __bfloat162float(a.q[b * a.q_stride[0] + i * a.q_stride[1] + H * a.q_stride[2] + d]);
-            __syncwarp();
-            const float lse = a.lse_in[((size_t)b * a.n + i) * a.heads + H];
-            const float pos_q = a.f.slopes ? query_position(a, b, h, s.len - s.m + i) : 0.0f;
-            if (page >= 0 && lse != -INFINITY && sees(a, s, b, i, j))
-                sum += expf(score(a, q, page, h, j % c.block, a.f.slopes ? a.f.slopes[H] : 0.0f, pos_q, j) - lse);
-        }
-    if (page >= 0)
-        a.weights[((size_t)page * c.kv_heads + h) * c.block + j % c.block] += sum;
-}
 
 spec_status check_call(const spec_cache *cache, const int32_t *lengths, const void *q, const int64_t q_stride[3],
                        int n, int heads, const spec_cache_form *form, const uint32_t *status)
@@ -212,8 +34,90 @@ spec_status check_call(const spec_cache *cache, const int32_t *lengths, const vo
     return SPEC_OK;
 }
 
+
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_sms[kMaxDevices];  // SM count, once the kernels' attributes are set
+
+spec_status device_sms(int *sms)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return SPEC_ERR_CUDA;
+    }
+    if (dev < 0 || dev >= kMaxDevices)
+        return SPEC_ERR_UNSUPPORTED;
+    int v = g_sms[dev].load(std::memory_order_acquire);
+    if (!v) {
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            cudaGetLastError();
+            return SPEC_ERR_CUDA;
+        }
+        for (const Kernels *k : {&kernels_d64(), &kernels_d128()})
+            for (int i = 0; i < 3; ++i)
+                for (int f = 0; f < 2; ++f)
+                    if (cudaFuncSetAttribute(k->attend[i][f], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             k->attend_smem[i]) != cudaSuccess ||
+                        cudaFuncSetAttribute(k->weigh[i][f], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             k->weigh_smem[i]) != cudaSuccess) {
+                        cudaGetLastError();
+                        return SPEC_ERR_CUDA;
+                    }
+        g_sms[dev].store(v, std::memory_order_release);
+    }
+    *sms = v;
+    return SPEC_OK;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder()
+{
+    static const EncodeTiled f = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return (EncodeTiled)p;
+    }();
+    return f;
+}
+
+// [dim, token, head, page] over the codes; a box is one block of one head.  A
+// token's row is one span of the swizzle, as the products read it.
+spec_status make_map(const spec_cache &c, void *base, const int64_t stride[3], CUtensorMap *map)
+{
+    const EncodeTiled encode = encoder();
+    if (!encode)
+        return SPEC_ERR_CUDA;
+    const cuuint64_t size[4] = {(cuuint64_t)c.dim, (cuuint64_t)c.block, (cuuint64_t)c.kv_heads, (cuuint64_t)c.num_pages};
+    const cuuint64_t step[3] = {(cuuint64_t)stride[2], (cuuint64_t)stride[1], (cuuint64_t)stride[0]};
+    const cuuint32_t box[4] = {(cuuint32_t)c.dim, (cuuint32_t)c.block, 1, 1}, one[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, size, step, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? SPEC_OK
+               : SPEC_ERR_INVALID_ARG;
+}
+
+// Columns of a row tile: the fewest that hold a key head's rows, 64 at most.
+struct Shape {
+    int index, nt, row_tiles;
+};
+Shape shape_for(const spec_cache &c, int n, int heads)
+{
+    const int rows = n * (heads / c.kv_heads);
+    const int i = rows <= 16 ? 0 : rows <= 32 ? 1 : 2, nt = 16 << i;
+    return {i, nt, (rows + nt - 1) / nt};
+}
+
 AttendArgs make_args(const spec_cache *cache, const int32_t *lengths, const void *q, const int64_t q_stride[3], int n,
-                     int heads, const spec_cache_form *form, uint32_t *status)
+                     int heads, const spec_cache_form *form, const Shape &shape, uint32_t *status)
 {
     AttendArgs a{};
     a.c = *cache;
@@ -224,9 +128,16 @@ AttendArgs make_args(const spec_cache *cache, const int32_t *lengths, const void
         a.q_stride[i] = q_stride[i];
     a.n = n;
     a.heads = heads;
+    a.group = heads / cache->kv_heads;
+    a.row_tiles = shape.row_tiles;
     a.status = status;
     return a;
 }
+
+bool has_form(const spec_cache_form *f) { return f->softcap > 0.0f || f->slopes; }
+
+int64_t part_bytes(const Shape &s, int dim, int sms) { return 2ll * sms * s.nt * dim * 4; }
+int64_t sum_bytes(const Shape &s, int sms) { return 2ll * sms * s.nt * 8; }
 
 }  // namespace
 
@@ -234,12 +145,22 @@ extern "C" {
 
 spec_status spec_cache_attend_workspace(const spec_cache *cache, int n, int heads, int64_t *bytes)
 {
-    const spec_status st = check_cache(cache);
+    spec_status st = check_cache(cache);
     if (st != SPEC_OK)
         return st;
     if (!bytes || n < 0 || heads < 1 || heads % cache->kv_heads)
         return SPEC_ERR_INVALID_ARG;
+    if ((long long)n * heads > INT_MAX / 2)
+        return SPEC_ERR_UNSUPPORTED;
     *bytes = 0;
+    if (cache->batch == 0 || n == 0)
+        return SPEC_OK;
+    int sms = 0;
+    st = device_sms(&sms);
+    if (st != SPEC_OK)
+        return st;
+    const Shape s = shape_for(*cache, n, heads);
+    *bytes = part_bytes(s, cache->dim, sms) + sum_bytes(s, sms) + 16ll * sms;
     return SPEC_OK;
 }
 
@@ -251,21 +172,50 @@ spec_status spec_cache_attend(const spec_cache *cache, const int32_t *lengths, c
     spec_status st = check_call(cache, lengths, q, q_stride, n, heads, form, status);
     if (st != SPEC_OK || cache->batch == 0 || n == 0)
         return st;
-    int64_t need = 0;
-    st = spec_cache_attend_workspace(cache, n, heads, &need);
+    if (!out || ((uintptr_t)out & 15u) || bad4(lse, true) || !workspace || ((uintptr_t)workspace & 15u) ||
+        workspace_bytes < 0)
+        return SPEC_ERR_INVALID_ARG;
+    int sms = 0;
+    st = device_sms(&sms);
     if (st != SPEC_OK)
         return st;
-    if (!out || ((uintptr_t)out & 15u) || bad4(lse, true) || workspace_bytes < need ||
-        (need && !workspace) || ((uintptr_t)workspace & 15u))
+    const Shape shape = shape_for(*cache, n, heads);
+    const int64_t parts = part_bytes(shape, cache->dim, sms), sums = sum_bytes(shape, sms);
+    if (workspace_bytes < parts + sums + 16ll * sms)
         return SPEC_ERR_INVALID_ARG;
-    AttendArgs a = make_args(cache, lengths, q, q_stride, n, heads, form, status);
+    AttendArgs a = make_args(cache, lengths, q, q_stride, n, heads, form, shape, status);
     a.out = (__nv_bfloat16 *)out;
     a.lse = lse;
-    const long long rows = (long long)cache->batch * n * heads;
-    if (rows / 4 >= INT_MAX)
-        return SPEC_ERR_UNSUPPORTED;
-    attend_kernel<<<(unsigned)((rows + 3) / 4), 128, 0, (cudaStream_t)stream>>>(a);
-    return launched();
+    a.part = (float *)workspace;
+    a.part_sum = (float2 *)((char *)workspace + parts);
+    a.joins = (int4 *)((char *)workspace + parts + sums);
+    CUtensorMap kmap, vmap;
+    if ((st = make_map(*cache, cache->k, cache->k_stride, &kmap)) != SPEC_OK ||
+        (st = make_map(*cache, cache->v, cache->v_stride, &vmap)) != SPEC_OK)
+        return st;
+    const Kernels &k = cache->dim == 64 ? kernels_d64() : kernels_d128();
+    void *args[] = {&a, &kmap, &vmap};
+    if (cudaLaunchKernel(k.attend[shape.index][has_form(form)], dim3(sms), dim3(kAttendThreads), args,
+                         (size_t)k.attend_smem[shape.index], (cudaStream_t)stream) != cudaSuccess) {
+        cudaGetLastError();
+        return SPEC_ERR_CUDA;
+    }
+    // the joins wait on the device for the parts; their launch overlaps the kernel before them
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms, shape.nt / kJoinRows);
+    cfg.blockDim = dim3(128);
+    cfg.stream = (cudaStream_t)stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *join_args[] = {&a};
+    if (cudaLaunchKernelExC(&cfg, k.join[shape.index], join_args) != cudaSuccess) {
+        cudaGetLastError();
+        return SPEC_ERR_CUDA;
+    }
+    return SPEC_OK;
 }
 
 spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, const void *q,
@@ -273,20 +223,30 @@ spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, co
                              const float *lse, float *weights, uint32_t *status, void *stream)
 {
     NvtxScope nvtx("spec_cache_weigh");
-    const spec_status st = check_call(cache, lengths, q, q_stride, n, heads, form, status);
+    spec_status st = check_call(cache, lengths, q, q_stride, n, heads, form, status);
     if (st != SPEC_OK || cache->batch == 0 || n == 0)
         return st;
     if (bad4(lse, true) || bad4(weights, true))
         return SPEC_ERR_INVALID_ARG;
-    AttendArgs a = make_args(cache, lengths, q, q_stride, n, heads, form, status);
+    int sms = 0;
+    st = device_sms(&sms);
+    if (st != SPEC_OK)
+        return st;
+    const Shape shape = shape_for(*cache, n, heads);
+    AttendArgs a = make_args(cache, lengths, q, q_stride, n, heads, form, shape, status);
     a.lse_in = lse;
     a.weights = weights;
-    const int chunks = (cache->max_blocks * cache->block + 31) / 32;
-    const long long warps = (long long)cache->batch * cache->kv_heads * chunks;
-    if (warps / 4 >= INT_MAX)
-        return SPEC_ERR_UNSUPPORTED;
-    weigh_kernel<<<(unsigned)((warps + 3) / 4), 128, 0, (cudaStream_t)stream>>>(a, chunks);
-    return launched();
+    CUtensorMap kmap;
+    if ((st = make_map(*cache, cache->k, cache->k_stride, &kmap)) != SPEC_OK)
+        return st;
+    const Kernels &k = cache->dim == 64 ? kernels_d64() : kernels_d128();
+    void *args[] = {&a, &kmap};
+    if (cudaLaunchKernel(k.weigh[shape.index][has_form(form)], dim3(sms), dim3(kWeighThreads), args,
+                         (size_t)k.weigh_smem[shape.index], (cudaStream_t)stream) != cudaSuccess) {
+        cudaGetLastError();
+        return SPEC_ERR_CUDA;
+    }
+    return SPEC_OK;
 }
 
 }  // extern "C"
