@@ -54,7 +54,7 @@ spec_status device_sms(int *sms)
             return SPEC_ERR_CUDA;
         }
         for (const Kernels *k : {&kernels_d64(), &kernels_d128()})
-            for (int i = 0; i < 3; ++i)
+            for (int i = 0; i < 4; ++i)
                 for (int f = 0; f < 2; ++f)
                     if (cudaFuncSetAttribute(k->attend[i][f], cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              k->attend_smem[i]) != cudaSuccess ||
@@ -112,7 +112,7 @@ struct Shape {
 Shape shape_for(const spec_cache &c, int n, int heads)
 {
     const int rows = n * (heads / c.kv_heads);
-    const int i = rows <= 16 ? 0 : rows <= 32 ? 1 : 2, nt = 16 << i;
+    const int i = rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 48 ? 2 : 3, nt = 16 * (i + 1);
     return {i, nt, (rows + nt - 1) / nt};
 }
 
@@ -195,7 +195,7 @@ spec_status spec_cache_attend(const spec_cache *cache, const int32_t *lengths, c
         return st;
     const Kernels &k = cache->dim == 64 ? kernels_d64() : kernels_d128();
     void *args[] = {&a, &kmap, &vmap};
-    if (cudaLaunchKernel(k.attend[shape.index][has_form(form)], dim3(sms), dim3(kAttendThreads), args,
+    if (cudaLaunchKernel(k.attend[shape.index][has_form(form)], dim3(sms), dim3(k.attend_threads[shape.index]), args,
                          (size_t)k.attend_smem[shape.index], (cudaStream_t)stream) != cudaSuccess) {
         cudaGetLastError();
         return SPEC_ERR_CUDA;

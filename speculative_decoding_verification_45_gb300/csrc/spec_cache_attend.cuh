@@ -11,8 +11,8 @@
 //        rounding to 4 bits needs no more than 4), down to 2^-10 of the row's
 //        largest element;
 //   p    exp(x - ..) scaled per tile and row so that the largest lies in
-//        [128, 256), as the sum of two e4m3 values: 2^-8 relative, the rounding
-//        of a bf16 weight.
+//        [224, 448], as the sum of two e4m3 values: 2^-8 relative, the rounding
+//        of a bf16 weight, on a grid of 2^-17 of the largest.
 // Each product is issued once per term into the same accumulator.
 //
 // Tokens are the M side (128 per tile), query rows the N side: a decode step
@@ -79,19 +79,21 @@ __device__ __forceinline__ bool mbar_try(uint64_t *bar, uint32_t parity)
                  : "memory");
     return ok;
 }
-// Waits for a phase, a bounded number of tries.  When they run out `dead` is set
+// Waits for a phase, about a second at most.  When that runs out `dead` is set
 // and every later wait returns at once: control flow stays the same for all
 // threads, so the CTA runs to its end (with results that the status marks bad).
-constexpr uint32_t kTries = 1u << 22;
+constexpr long long kPatience = 1ll << 31;  // clocks
 __device__ __forceinline__ void mbar_wait(uint64_t *bar, uint32_t parity, volatile int *dead)
 {
     if (mbar_try(bar, parity))
         return;
-    for (uint32_t i = 0; i < kTries; ++i) {
-        if (mbar_try(bar, parity) || *dead)
+    const long long since = clock64();
+    while (!mbar_try(bar, parity)) {
+        if (*dead)
             return;
+        if (clock64() - since > kPatience)
+            *dead = 1;
     }
-    *dead = 1;
 }
 
 // After a wait ran out: copies and products in flight end before the CTA's memory is given back.
@@ -120,6 +122,17 @@ __device__ __forceinline__ void drain_products(uint64_t *bar, volatile int *dead
 template <int N> __device__ __forceinline__ void named_barrier(int id)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
+}
+
+// Barrier of N threads that also tells whether any of them brought `p`.
+template <int N> __device__ __forceinline__ bool barrier_or(int id, bool p)
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, %2, %3, p;\nselp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)p), "r"(id), "n"(N)
+                 : "memory");
+    return r;
 }
 
 __device__ __forceinline__ void tma_load(const CUtensorMap *map, void *dst, uint64_t *bar, int d, int row, int head, int page)
@@ -186,6 +199,15 @@ template <> struct TmemLoad<32> {
         TmemLoad<16>::go(a + 16, r + 16);
     }
 };
+__device__ __forceinline__ void tmem_store16(uint32_t a, const float *r)
+{
+    const uint32_t *u = (const uint32_t *)r;
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(u[0]),
+                 "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
+                 "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(a)
+                 : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 // The registers of earlier loads are valid after this; they pass through it so that no use moves ahead.
 template <int N> __device__ __forceinline__ void tmem_wait(float *r)
 {
@@ -333,16 +355,16 @@ template <int NT> struct Columns {
 };
 
 // Rows of a row tile into shared memory as two e4m3 terms, 128- or 64-byte
-// swizzled, and the columns' constants.  Called by 256 threads (t), which have
-// met at a barrier after the last use of either; ends without one.
-template <int D, int NT>
+// swizzled, and the columns' constants.  Called by THREADS threads (t), after the
+// last use of either; ends without a barrier.
+template <int D, int NT, int THREADS>
 __device__ __forceinline__ void load_queries(const AttendArgs &a, const Unit &u, int b, int h, int rt, bool tree, uint8_t *q,
                                              Columns<NT> &col, int t)
 {
-    constexpr int kLanes = D / 8, kRows = 256 / kLanes;
+    constexpr int kLanes = D / 8, kRows = THREADS / kLanes;
     const int d = t % kLanes;
     if (tree && a.f.parent)
-        for (int k = t; k < u.m; k += 256) {
+        for (int k = t; k < u.m; k += THREADS) {
             const int up = k > 0 ? a.f.parent[(size_t)b * a.n + k] : -1;
             if (k > 0 && (unsigned)up >= (unsigned)k)
                 report(a.status, SPEC_STATUS_BAD_TREE);
@@ -351,7 +373,7 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const Unit &u,
 #pragma unroll
     for (int r0 = 0; r0 < NT; r0 += kRows) {
         const int c = r0 + t / kLanes;
-        if (kRows > NT && c >= NT)
+        if (NT % kRows && c >= NT)
             continue;  // whole warps: a warp holds 2 or 4 rows
         const int r = rt * NT + c, i = r / a.group, H = h * a.group + r % a.group;
         const bool live = i <= u.i1;
@@ -549,43 +571,70 @@ template <int NT> struct Walk {
 // ===========================================================================
 // Attention
 // ===========================================================================
-// One persistent CTA per SM, 14 warps, each with one job:
-//   warp 12      producer: block table, TMA of the blocks, their scales
-//   warp 13      issues the products and owns the tensor memory
-//   warps 4-11   softmax: two warpgroups, each NT / 2 of the columns
-//   warps 0-3    add the tiles' O^T up in registers and write the results
-// Per tile g: S^T(g) into one of two buffers; softmax turns it into P^T in
-// shared memory; O^T(g) = V^T P^T into one of two buffers, while S^T(g + 1) is
-// computed.  O^T of a tile is read out and added in 32 bits, with a power of two
-// per row and tile: the weights of a tile are scaled by that tile's own maximum
-// (not a running one), so a light tail after a heavy token keeps its bits.
+// One persistent CTA per SM, each warp with one job:
+//   producer     block table, TMA of the blocks, their scales
+//   products     issues the matrix products and owns the tensor memory
+//   softmax      NW warpgroups, tiles in turn; a thread owns one token and all columns
+//   adding       one warpgroup: adds the tiles' O^T up in registers, writes the
+//                results, and brings in the next segment's queries
+// Tile g: S^T(g) in tensor memory; warpgroup g % NW turns it into P^T in shared
+// memory; O^T(g) = V^T P^T.  A tile's softmax is a chain of short dependent
+// steps (about 3000 cycles when one pair of warpgroups shared each tile, of
+// 3900 a tile in all), so what counts is how many such chains run side by side.
 //
-// The exponents' base: exp2(x - base) in 32 bits has room for 2^127, so the base
-// of a row is set at the first tile that the row sees and moves only when a later
-// score passes it by 2^64 (or 2^32 in a tile that is looked at closely): no
-// running maximum has to be agreed upon before the exponentials.  What the 8-bit
-// weights need is the maximum's exponent only: 16-bit halves of the
-// exponentials are compared two at a time in the warp (16 shuffles for 32
-// columns) and four warps meet in shared memory.
-constexpr int kAttendThreads = 448;
+// O^T of a tile is read out and added in 32 bits, scaled by a power of two per
+// row and tile: the weights of a tile go by that tile's own maximum (not a
+// running one), so a light tail after a heavy token keeps its bits.
+//
+// The exponents' base: exp2(x - base) in 32 bits has room for 2^127, so a
+// warpgroup sets a row's base at the first tile that the row sees and moves it
+// only when a later score passes it by 2^64: no running maximum has to be agreed
+// upon before the exponentials.  What the 8-bit weights need is the maximum's
+// exponent only: 16-bit halves of the exponentials are compared two at a time
+// (16 shuffles for 32 columns) and the four warps meet in shared memory.
+template <int D, int NT> struct AttendShape {
+    static constexpr int NW = NT <= 32 ? 3 : 2;               // softmax warpgroups
+    static constexpr int kThreads = 128 * (1 + NW) + 64;
+    static constexpr int kBytes = kTile * D;                  // one side of a tile
+    static constexpr int KS = 3, VS = D == 64 || NT == 16 ? 8 : 8 - NT / 16 + (NT == 48);  // tiles of keys and values in shared memory
+    static constexpr bool kSumsInTmem = NT >= 32;             // the rows' running totals, which registers cannot hold
+    static constexpr int kColumns = (kSumsInTmem ? 2 * NW + 2 : NW + 2) * NT;
+    static constexpr int kAlloc = kColumns <= 64 ? 64 : kColumns <= 128 ? 128 : kColumns <= 256 ? 256 : 512;
+    static constexpr int kChunk = 16;                         // columns of a warp reduction
+    static constexpr int kRing = 8;                           // >= NW + 2 tiles between a writer and the adding warps
+};
+
+// What the softmax and the products need to know of a segment; the adding warps
+// write it with the segment's queries.
+struct Segment {
+    int tiles;  // 0: there is none left
+    int x0, head_tiles, low;
+    int len, first, prefix, i1, rt;
+    int seen_prefix, seen_low, seen_end;  // tiles that every query of the row tile sees whole: [0, ..) and [low, end)
+    __device__ __forceinline__ int tile(int k) const { return x0 + k < head_tiles ? x0 + k : x0 + k - head_tiles + low; }
+};
 
 template <int D, int NT> struct AttendShared {
-    static constexpr int kStages = D == 64 ? 8 : NT == 16 ? 6 : 5;
-    static constexpr int kSide = kTile * D;
-    alignas(1024) uint8_t tiles[kStages][2][kSide];
-    alignas(1024) uint8_t q[2][NT * D];
-    alignas(1024) uint8_t p[2][2][kTile * NT];
-    alignas(16) Columns<NT> col;
-    alignas(16) StageInfo info[kStages];
-    alignas(16) uint32_t top[8][NT];   // per tile: largest exponent (biased) of exp2(x - base) * v_scale
-    alignas(16) float alpha[8][NT];    // what a moved base leaves of the sums so far
-    alignas(16) float warp_total[4][NT];
-    alignas(16) float last_base[NT], inverse[NT];
-    int highest[NT];                   // ordered bits of the largest score
-    int is_set[NT];                    // the row has a base
-    int moved[8][2], unset[2];
-    alignas(8) uint64_t full[kStages], empty[kStages];
-    uint64_t s_full[2], s_free[2], p_ready[4], o_full[2], o_free[2], q_ready, sum_ready, sum_free, drained;
+    using S = AttendShape<D, NT>;
+    alignas(1024) uint8_t k[S::KS][S::kBytes];
+    alignas(1024) uint8_t v[S::VS][S::kBytes];
+    alignas(1024) uint8_t q[2][2][NT * D];
+    alignas(1024) uint8_t p[S::NW][2][kTile * NT];
+    alignas(16) Columns<NT> col[2];
+    Segment seg[2];
+    alignas(16) StageInfo info[S::VS];
+    alignas(16) float base[S::NW][NT];
+    alignas(16) uint32_t top[S::NW][4][NT];  // per tile: exponent (biased) of the largest exp2(x - base) * v_scale / 1.75, rounded up
+    alignas(16) int power[S::kRing][NT];     // per tile: O^T counts 2^power
+    alignas(16) float factor[2][NT], inverse[NT];
+    alignas(16) float warp_total[2][S::NW * 4][NT], last_base[2][S::NW][NT];
+    alignas(16) float alpha[S::NW][NT];      // what a moved base leaves of the totals
+    int highest[S::NW][NT];                  // ordered bits of the largest score
+    int is_set[S::NW][NT];                   // the row has a base
+    int moved[S::NW][2], unset[S::NW][2];    // by 32 columns
+    alignas(8) uint64_t k_full[S::KS], k_empty[S::KS], v_full[S::VS], v_empty[S::VS];
+    uint64_t s_full[S::NW], s_free[S::NW], p_ready[S::kRing], p_free[S::NW], o_full[2], o_free[2], q_ready[2];
+    uint64_t sum_ready[2], sum_free[2], drained;
     uint32_t tmem;
     int dead;
 };
@@ -596,36 +645,80 @@ __device__ __forceinline__ int ordered(float x)
     return i ^ ((i >> 31) & 0x7fffffff);
 }
 
-// Largest of each 16-bit half over the warp, W words; lane's word index comes back in `word`.
-template <int W> __device__ __forceinline__ uint32_t warp_max_halves(uint32_t *w, int lane, int &word)
+struct MaxHalves {
+    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return __vmaxu2(a, b); }
+};
+struct MaxInt {
+    __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
+};
+struct Add {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+// N values per lane, combined over the warp: each lane ends with one of them, whose index comes back in `which`
+// (N - 1 shuffles and what is left of the five halvings; lanes that differ only below 32 / N hold the same).
+template <int N, typename T, typename Op> __device__ __forceinline__ T warp_combine(T *w, int lane, int &which, Op op)
 {
-    word = 0;
+    which = 0;
     int o = 16;
 #pragma unroll
-    for (int n = W; n > 1; n >>= 1, o >>= 1) {
+    for (int n = N; n > 1; n >>= 1, o >>= 1) {
         const bool up = lane & o;
-        word = word * 2 + up;
+        which = which * 2 + up;
 #pragma unroll
         for (int i = 0; i < n / 2; ++i) {
-            const uint32_t send = up ? w[i] : w[i + n / 2], keep = up ? w[i + n / 2] : w[i];
-            w[i] = __vmaxu2(keep, __shfl_xor_sync(0xffffffffu, send, o));
+            const T send = up ? w[i] : w[i + n / 2], keep = up ? w[i + n / 2] : w[i];
+            w[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
         }
     }
 #pragma unroll
     for (; o > 0; o >>= 1)
-        w[0] = __vmaxu2(w[0], __shfl_xor_sync(0xffffffffu, w[0], o));
+        w[0] = op(w[0], __shfl_xor_sync(0xffffffffu, w[0], o));
     return w[0];
 }
 
+// 2^e for any e: 0 below the normal numbers, the largest power above them.
+__device__ __forceinline__ float power2(int e)
+{
+    return e < -126 ? 0.0f : __uint_as_float((uint32_t)(min(e, 127) + 127) << 23);
+}
+
+__device__ __forceinline__ uint64_t low_bits(long long n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
+// The columns whose queries see token j: an interval of the rows in order, or the bits of a tree.
+template <int NT>
+__device__ __forceinline__ uint64_t seen_by(const AttendArgs &a, const Segment &u, const Columns<NT> &col, int j)
+{
+    const long long t = (long long)j - u.first, r0 = (long long)u.rt * NT;
+    const uint64_t rows = low_bits(min((long long)(u.i1 + 1) * a.group - r0, (long long)NT));
+    if (j < u.prefix)
+        return rows;
+    uint64_t see = rows;
+    if (t >= 0) {
+        if (a.f.parent) {
+            see = 0;
+            for (int c = 0; c < NT; ++c)
+                see |= (uint64_t)((col.kin[c][t >> 5] >> (t & 31)) & 1) << c;
+            see &= rows;
+        } else {
+            see &= ~low_bits(t * a.group - r0);  // row r asks from query r / group, which sees up to itself
+        }
+    }
+    if (a.f.window > 0)
+        see &= low_bits((t + a.f.window) * a.group - r0);
+    return see;
+}
+
 template <int D, int NT, bool FORM>
-__global__ void __launch_bounds__(kAttendThreads, 1)
+__global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
     attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap)
 {
+    using S = AttendShape<D, NT>;
     using Shared = AttendShared<D, NT>;
-    constexpr int ST = Shared::kStages;
-    constexpr int CW = NT / 2;                        // columns of a softmax thread
-    constexpr int OC = D == 128 ? NT : NT / 2;        // columns of an adding thread
+    constexpr int NW = S::NW, KS = S::KS, VS = S::VS, kRing = S::kRing, kChunk = S::kChunk;
+    constexpr int kProducer = 4 * (1 + NW), kProducts = kProducer + 1;
+    constexpr int OC = D == 128 ? NT : NT / 2;  // columns of an adding thread
+    constexpr uint32_t kO = NW * NT, kL = kO + 2 * NT;  // S^T at 0, then O^T, then the totals
     extern __shared__ uint8_t raw[];
     Shared &sh = *(Shared *)(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -633,39 +726,44 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 
     if (tid == 0) {
         sh.dead = 0;
-        for (int i = 0; i < ST; ++i) {
-            mbar_init(&sh.full[i], 33);  // the expected bytes, and 32 lanes' copies of scales
-            mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < KS; ++i) {
+            mbar_init(&sh.k_full[i], 1);
+            mbar_init(&sh.k_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < VS; ++i) {
+            mbar_init(&sh.v_full[i], 33);  // the expected bytes, and 32 lanes' copies of scales
+            mbar_init(&sh.v_empty[i], 1);
+        }
+        for (int i = 0; i < NW; ++i) {
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_free[i], 8);
+            mbar_init(&sh.s_free[i], 4);
+            mbar_init(&sh.p_free[i], 1);
+        }
+        for (int i = 0; i < kRing; ++i)
+            mbar_init(&sh.p_ready[i], 4);
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.o_full[i], 1);
             mbar_init(&sh.o_free[i], 4);
+            mbar_init(&sh.q_ready[i], 4);
+            mbar_init(&sh.sum_ready[i], 4 * NW);
+            mbar_init(&sh.sum_free[i], 4);
         }
-        // four slots: tile g + 4's phase cannot complete before the adding warps have passed tile g's
-        for (int i = 0; i < 4; ++i)
-            mbar_init(&sh.p_ready[i], 8);
         mbar_init(&sh.drained, 1);
-        mbar_init(&sh.q_ready, 8);
-        mbar_init(&sh.sum_ready, 8);
-        mbar_init(&sh.sum_free, 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
-    for (int i = tid; i < 8 * NT; i += kAttendThreads)
+    for (int i = tid; i < NW * 4 * NT; i += S::kThreads)
         ((uint32_t *)sh.top)[i] = 0;
-    for (int i = tid; i < NT; i += kAttendThreads)
-        sh.highest[i] = INT_MIN;
-    for (int i = tid; i < ST * 8; i += kAttendThreads)
-        sh.info[i >> 3].k_scale[i & 7] = sh.info[i >> 3].v_scale[i & 7] = 1.0f;
-    if (wid == 13) {
+    for (int i = tid; i < NW * NT; i += S::kThreads)
+        ((int *)sh.highest)[i] = INT_MIN;
+    if (wid == kProducts) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
-                     "r"(4 * NT)
+                     "r"(S::kAlloc)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         tc_before();
     }
-    const Range range = find_range<kAttendThreads>(a, [&](int b) {
+    const Range range = find_range<S::kThreads>(a, [&](int b) {
         long long each = 0;
         for (int k = 0; k < a.row_tiles; ++k)
             each += max(row_unit<NT>(a, b, k).count, 1);
@@ -675,18 +773,17 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     });
     __syncthreads();
     tc_after();
-    const uint32_t tmem = sh.tmem;  // columns: S^T at 0 and NT, O^T at 2 NT and 3 NT
+    const uint32_t tmem = sh.tmem;
     const int P = a.c.block, blocks = kTile / P, log_p = 31 - __clz(P);
     Walk<NT> walk(a, range);
-    if (tid == 0)
-        a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
-    if (wid == 12) {
+    if (wid == kProducer) {
         // ---------------- producer ----------------
         if (lane < 2)
             asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &vmap : &kmap));
-        int st = 0;
-        uint32_t phase = 1, issued = 0;
+        int ks = 0, vs = 0;
+        uint32_t k_phase = 1, v_phase = 1, issued = 0;
+        const bool pos = a.f.slopes && a.c.positions;
         while (walk.next()) {
             const Unit &u = walk.u;
             if (u.count == 0)
@@ -699,387 +796,543 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             int page = page_at(walk.x0);
             for (int x = walk.x0; x < walk.x1; ++x) {
                 const int next = x + 1 < walk.x1 ? page_at(x + 1) : -2;
-                mbar_wait(&sh.empty[st], phase, dead);
                 const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
                 if (page != -2 && !ok)
                     report(a.status, SPEC_STATUS_BAD_PAGE);
-                if (!__any_sync(0xffffffffu, *dead)) {
-                    load_tile<D, true>(a, &kmap, &vmap, walk.h, page, ok, sh.info[st], sh.tiles[st][0], sh.tiles[st][1],
-                                       &sh.full[st], lane);
+                const uint32_t came = __ballot_sync(0xffffffffu, ok);
+                const size_t at = (size_t)max(page, 0) * a.c.kv_heads + walk.h;
+                mbar_wait(&sh.k_empty[ks], k_phase, dead);
+                bool go = !__any_sync(0xffffffffu, *dead);
+                if (go) {
+                    if (lane == 0)
+                        mbar_expect(&sh.k_full[ks], (uint32_t)__popc(came) * (uint32_t)(P * D));
+                    __syncwarp();
+                    if (ok)
+                        tma_load(&kmap, sh.k[ks] + lane * P * D, &sh.k_full[ks], 0, 0, walk.h, page);
+                }
+                mbar_wait(&sh.v_empty[vs], v_phase, dead);
+                go = go && !__any_sync(0xffffffffu, *dead);
+                if (go) {
+                    StageInfo &info = sh.info[vs];
+                    if (lane == 0) {
+                        info.came = came;
+                        mbar_expect(&sh.v_full[vs], (uint32_t)__popc(came) * (uint32_t)(P * D + (pos ? P * 4 : 0)));
+                    }
+                    __syncwarp();
+                    if (ok) {
+                        tma_load(&vmap, sh.v[vs] + lane * P * D, &sh.v_full[vs], 0, 0, walk.h, page);
+                        if (pos)
+                            bulk_load(a.c.positions + at * P, info.pos + lane * P, (uint32_t)P * 4, &sh.v_full[vs]);
+                        copy4(a.c.k_scale + at, info.k_scale + lane);
+                        copy4(a.c.v_scale + at, info.v_scale + lane);
+                    }
+                    copies_arrive(&sh.v_full[vs]);
                     ++issued;
                 }
                 page = next;
-                if (++st == ST) {
-                    st = 0;
-                    phase ^= 1;
+                if (++ks == KS) {
+                    ks = 0;
+                    k_phase ^= 1;
+                }
+                if (++vs == VS) {
+                    vs = 0;
+                    v_phase ^= 1;
                 }
             }
         }
-        drain<ST>(sh.full, issued, dead, a.status);
-    } else if (wid == 13) {
+        drain<KS>(sh.k_full, issued, dead, a.status);
+        drain<VS>(sh.v_full, issued, dead, a.status);
+    } else if (wid == kProducts) {
         // ---------------- products ----------------
         const uint32_t s_desc = instr_desc(NT, a.c.code, false, false), o_desc = instr_desc(NT, a.c.code, true, true);
         const uint64_t swizzle = D == 128 ? 2 : 4;
-        int st = 0, st_prev = 0;
-        uint32_t phase = 0, g = 0, seg = 0;
-        bool pending = false;  // O^T of tile g - 1 is still to be issued
-        const auto values = [&]() {
-            const uint32_t i = (g - 1) & 1, par = ((g - 1) >> 1) & 1;
-            mbar_wait(&sh.p_ready[(g - 1) & 3], ((g - 1) >> 2) & 1, dead);
-            mbar_wait(&sh.o_free[i], par ^ 1, dead);
+        int ks = 0, vs = 0, w = 0, pw = 0;  // pw: warpgroup of the next tile to be multiplied with values
+        uint32_t k_phase = 0, v_phase = 0, s_phase = 1, g = 0, done = 0, seg = 0, begun = 0;
+        const auto values = [&]() {  // O^T of tile `done`
+            const uint32_t i = done & 1;
+            mbar_wait(&sh.p_ready[done % kRing], (done / kRing) & 1, dead);
+            mbar_wait(&sh.v_full[vs], v_phase, dead);
+            mbar_wait(&sh.o_free[i], ((done >> 1) & 1) ^ 1, dead);
             tc_after();
             if (lane == 0) {
-                const uint32_t v = smem_u32(sh.tiles[st_prev][1]), p = smem_u32(sh.p[i][0]);
+                const uint32_t v = smem_u32(sh.v[vs]), p = smem_u32(sh.p[pw][0]);
 #pragma unroll
                 for (int k = 0; k < kTile / 32; ++k) {
                     const uint64_t vd = smem_desc(v + k * 32 * D, 0, 8 * D, swizzle);
 #pragma unroll
                     for (int term = 0; term < 2; ++term)
-                        tc_mma(tmem + (2 + i) * NT, vd, smem_desc(p + term * kTile * NT + k * 512, 128, kTile * 16, 0), o_desc,
+                        tc_mma(tmem + kO + i * NT, vd, smem_desc(p + term * kTile * NT + k * 512, 128, kTile * 16, 0), o_desc,
                                k + term > 0);
                 }
                 tc_commit(&sh.o_full[i]);
-                tc_commit(&sh.empty[st_prev]);
+                tc_commit(&sh.p_free[pw]);
+                tc_commit(&sh.v_empty[vs]);
             }
             __syncwarp();
-            pending = false;
+            ++done;
+            pw = pw + 1 == NW ? 0 : pw + 1;
+            if (++vs == VS) {
+                vs = 0;
+                v_phase ^= 1;
+            }
         };
-        while (walk.next()) {
-            if (walk.u.count == 0)
-                continue;
-            if (pending)
+        while (!*dead) {
+            // the next queries come once the segment before the last is complete: its products must not wait for them
+            while (done < begun)
                 values();
-            mbar_wait(&sh.q_ready, seg++ & 1, dead);
-            for (int x = walk.x0; x < walk.x1; ++x) {
-                const uint32_t i = g & 1, par = (g >> 1) & 1;
-                mbar_wait(&sh.full[st], phase, dead);
-                mbar_wait(&sh.s_free[i], par ^ 1, dead);
+            begun = g;
+            mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, dead);
+            const int tiles = sh.seg[seg & 1].tiles;
+            if (tiles == 0)
+                break;
+            const uint32_t q = smem_u32(sh.q[seg & 1][0]);
+            ++seg;
+            for (int x = 0; x < tiles; ++x) {
+                mbar_wait(&sh.k_full[ks], k_phase, dead);
+                mbar_wait(&sh.s_free[w], s_phase, dead);
                 tc_after();
                 if (lane == 0) {
-                    const uint32_t k = smem_u32(sh.tiles[st][0]), q = smem_u32(sh.q[0]);
+                    const uint32_t k = smem_u32(sh.k[ks]);
 #pragma unroll
                     for (int d = 0; d < D / 32; ++d) {
                         const uint64_t kd = smem_desc(k + d * 32, 16, 8 * D, swizzle);
 #pragma unroll
                         for (int term = 0; term < 2; ++term)
-                            tc_mma(tmem + i * NT, kd, smem_desc(q + term * NT * D + d * 32, 16, 8 * D, swizzle), s_desc,
+                            tc_mma(tmem + w * NT, kd, smem_desc(q + term * NT * D + d * 32, 16, 8 * D, swizzle), s_desc,
                                    d + term > 0);
                     }
-                    tc_commit(&sh.s_full[i]);
+                    tc_commit(&sh.s_full[w]);
+                    tc_commit(&sh.k_empty[ks]);
                 }
                 __syncwarp();
-                if (pending)
-                    values();
-                ++g;
-                pending = true;
-                st_prev = st;
-                if (++st == ST) {
-                    st = 0;
-                    phase ^= 1;
+                if (++w == NW) {
+                    w = 0;
+                    s_phase ^= 1;
                 }
+                if (++ks == KS) {
+                    ks = 0;
+                    k_phase ^= 1;
+                }
+                if (++g > NW)
+                    values();
             }
         }
-        if (pending)
+        while (done < g)
             values();
         drain_products(&sh.drained, dead);
     } else if (wid >= 4) {
         // ---------------- softmax ----------------
-        const int w = (wid - 4) >> 2, t = (tid - 128) & 127, all = tid - 128, c0 = w * CW;
-        const uint32_t lanes = (uint32_t)(wid & 3) << 21;
-        int st = 0;
-        uint32_t phase = 0, g = 0, seg = 0;
-        float l[CW], e[CW];
-        while (walk.next()) {
-            const Unit u = walk.u;
-            if (u.count == 0)
-                continue;
-            named_barrier<256>(3);  // the last segment's columns are done with
-            const bool tree = a.f.parent && (long long)(u.tile(walk.x1 - 1) + 1) * kTile > u.first;
-            load_queries<D, NT>(a, u, walk.b, walk.h, walk.rt, tree, sh.q[0], sh.col, all);
-            if (t < CW) {
-                sh.col.base[c0 + t] = 0.0f;
-                sh.is_set[c0 + t] = 0;
-            }
-            if (t == 0)
-                sh.unset[w] = 1;
-            proxy_fence();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sh.q_ready);
-            named_barrier<256>(3);
-            if (tree) {
-                mark_kin<NT>(u, sh.col, all);
-                named_barrier<256>(3);
+        const int w = (wid >> 2) - 1, t = tid & 127, bar = 1 + w;
+        const uint32_t lanes = (uint32_t)(wid & 3) << 21, s_at = tmem + lanes + w * NT;
+        constexpr int LR = S::kSumsInTmem ? 1 : NT;
+        const uint32_t l_at = tmem + lanes + kL + w * NT;
+        int vs = 0, turn = 0;  // turn: whose tile it is
+        uint32_t v_phase = 0, g = 0, mine = 0, seg = 0;
+        float l[LR], e[NT];
+        while (true) {
+            mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, dead);
+            const Segment &u = sh.seg[seg & 1];
+            const Columns<NT> &col = sh.col[seg & 1];
+            const int tiles = u.tiles;
+            if (barrier_or<128>(bar, tiles == 0 || *dead))
+                break;
+            bool fresh = true;
+            if (t < NT) {
+                sh.base[w][t] = 0.0f;
+                sh.is_set[w][t] = 0;
             }
 #pragma unroll
-            for (int c = 0; c < CW; ++c)
+            for (int c = 0; c < LR; ++c)
                 l[c] = 0.0f;
-            for (int x = walk.x0; x < walk.x1; ++x) {
-                const uint32_t i = g & 1, par = (g >> 1) & 1, slot = g & 7;
-                mbar_wait(&sh.full[st], phase, dead);
-                const StageInfo &info = sh.info[st];
-                const int j0 = u.tile(x) * kTile, j = j0 + t;
-                const uint32_t came = info.came;
-                const bool edge = came != (1u << blocks) - 1 || !interior(a, u, j0);
-                const bool cached = !edge || (j < u.len && ((came >> (t >> log_p)) & 1));
-                float ks = cached ? info.k_scale[t >> log_p] : 0.0f, vs = cached ? info.v_scale[t >> log_p] : 1.0f;
-                const float pos = FORM && a.f.slopes ? (a.c.positions ? (float)info.pos[t] : (float)j) : 0.0f;
-                float small = info.v_scale[0];
-                for (int k = 1; k < blocks; ++k)
-                    small = fminf(small, info.v_scale[k]);
-                bool closely = sh.unset[w] != 0 && (edge || x == walk.x0);
-                closely = closely || small < 0x1p-40f;
-                if (edge) {
-                    // what V holds where nothing is cached, and NaN where some row sees it and some do not: neither
-                    // may reach the product.  Both warpgroups look, then the first one cleans.
-                    uint32_t *row = (uint32_t *)(sh.tiles[st][1] + t * D);
-                    const uint32_t add = a.c.code == SPEC_E4M3 ? 0x01010101u : 0x04040404u;
-                    uint32_t bad = 0;
-                    for (int k = 0; k < D / 4; ++k)
-                        bad |= ((row[(k + t) & (D / 4 - 1)] & 0x7f7f7f7fu) + add) & 0x80808080u;
-                    named_barrier<256>(3);
-                    if (w == 0 && (bad || !cached))
-                        for (int k = 0; k < D / 4; ++k) {
-                            const uint32_t v = row[k], nan = ((v & 0x7f7f7f7fu) + add) & 0x80808080u;
-                            row[k] = cached ? v & ~((nan >> 7) * 0xffu) : 0u;
-                        }
-                    if (cached && bad)
-                        vs = __int_as_float(0x7fffffff);
-                }
-                const uint32_t s_at = tmem + lanes + i * NT + c0;
-                mbar_wait(&sh.s_full[i], par, dead);
-                tc_after();
-
-                // one column's score, less base
-                const auto score_of = [&](int c, float s, float f, float base) {
-                    return score<FORM>(a, s, ks * f, base, FORM && a.f.slopes ? sh.col.slope[c0 + c] : 0.0f,
-                                       FORM && a.f.slopes ? sh.col.pos[c0 + c] - pos : 0.0f);
-                };
-                const auto rebase = [&]() {
-                    TmemLoad<CW>::go(s_at, e);
-                    tmem_wait<CW>(e);
-#pragma unroll
-                    for (int c = 0; c < CW; ++c) {
-                        float y = score_of(c, e[c], sh.col.factor[c0 + c], 0.0f);
-                        if (edge && !(cached && sees<NT>(a, u, sh.col, c0 + c, j)))
-                            y = -INFINITY;
-                        const int top = __reduce_max_sync(0xffffffffu, y == y ? ordered(y) : INT_MIN);
-                        if (lane == 0)
-                            atomicMax(&sh.highest[c0 + c], top);
-                    }
-                    named_barrier<128>(1 + w);
-                    if (t < 32) {
-                        float alpha = 1.0f;
-                        bool set = true;
-                        if (t < CW) {
-                            const int top = sh.highest[c0 + t];
-                            const float high = __int_as_float(top ^ ((top >> 31) & 0x7fffffff)), old = sh.col.base[c0 + t];
-                            sh.highest[c0 + t] = INT_MIN;
-                            set = sh.is_set[c0 + t];
-                            if (top != INT_MIN && high > -INFINITY) {
-                                if (!set || high - old > 32.0f) {
-                                    const float now = ceilf(high);
-                                    alpha = set ? exp2f(old - now) : 1.0f;
-                                    sh.col.base[c0 + t] = now;
-                                }
-                                sh.is_set[c0 + t] = 1;
-                                set = true;
-                            }
-                            set = set || sh.col.query[c0 + t] < 0;
-                            sh.alpha[g & 7][c0 + t] = alpha;
-                        }
-                        const bool any = __any_sync(0xffffffffu, alpha != 1.0f), open = __any_sync(0xffffffffu, !set);
-                        if (t == 0) {
-                            sh.moved[g & 7][w] = any;
-                            sh.unset[w] = open;
-                        }
-                    }
-                    named_barrier<128>(1 + w);
-                    if (sh.moved[g & 7][w]) {
-#pragma unroll
-                        for (int c = 0; c < CW; ++c)
-                            l[c] *= sh.alpha[g & 7][c0 + c];
-                    }
-                };
-                // exponentials into e, and the tile's largest exponents into top[slot]
-                const auto exponentials = [&]() {
-                    TmemLoad<CW>::go(s_at, e);
-                    tmem_wait<CW>(e);
-                    uint32_t half[CW / 2];
-#pragma unroll
-                    for (int c4 = 0; c4 < CW / 4; ++c4) {
-                        const float4 f4 = ((const float4 *)(sh.col.factor + c0))[c4], b4 = ((const float4 *)(sh.col.base + c0))[c4];
-                        const float f[4] = {f4.x, f4.y, f4.z, f4.w}, bs[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int c = c4 * 4 + k;
-                            e[c] = exp2_fast(score_of(c, e[c], f[k], bs[k]));
-                        }
-                    }
+            for (int x = 0; x < tiles; ++x) {
+                if (turn == w) {
+                    const int tile = u.tile(x), j = tile * kTile + t;
+                    mbar_wait(&sh.v_full[vs], v_phase, dead);
+                    const StageInfo &info = sh.info[vs];
+                    const uint32_t came = info.came;
+                    float k_scale = info.k_scale[t >> log_p], v_scale = info.v_scale[t >> log_p];
+                    const float pos = FORM && a.f.slopes ? (a.c.positions ? (float)info.pos[t] : (float)j) : 0.0f;
+                    const bool edge = came != (1u << blocks) - 1 ||
+                                      !(tile < u.seen_prefix || (tile >= u.seen_low && tile < u.seen_end));
+                    bool closely = fresh;
+                    uint64_t see = ~0ull;
                     if (edge) {
-#pragma unroll
-                        for (int c = 0; c < CW; ++c)
-                            if (!(cached && sees<NT>(a, u, sh.col, c0 + c, j)))
-                                e[c] = 0.0f;
-                    }
-#pragma unroll
-                    for (int c = 0; c < CW; c += 2) {
-                        float y0 = e[c] * vs, y1 = e[c + 1] * vs;
-                        if (edge) {
-                            y0 = e[c] == 0.0f ? 0.0f : y0;
-                            y1 = e[c + 1] == 0.0f ? 0.0f : y1;
+                        if (!fresh)
+                            closely = sh.unset[w][0] || (NT > 32 && sh.unset[w][1]);
+                        const bool cached = j < u.len && ((came >> (t >> log_p)) & 1);
+                        see = cached ? seen_by<NT>(a, u, col, j) : 0;
+                        const bool all =
+                            see == low_bits(min((long long)(u.i1 + 1) * a.group - (long long)u.rt * NT, (long long)NT));
+                        uint4 *row = (uint4 *)(sh.v[vs] + t * D);
+                        if (!cached) {  // nothing was loaded here
+                            k_scale = 0.0f;
+                            v_scale = 1.0f;
+                            for (int k = 0; k < D / 16; ++k)
+                                row[(k + t) & (D / 16 - 1)] = make_uint4(0, 0, 0, 0);
+                        } else if (!all) {
+                            // a NaN that some row does not see must not reach the product: 0 stands in its place, and
+                            // the weights of the rows that do see it become NaN
+                            const uint32_t add = a.c.code == SPEC_E4M3 ? 0x01010101u : 0x04040404u;
+                            uint32_t bad = 0;
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint4 v = row[(k + t) & (D / 16 - 1)];
+                                bad |= ((v.x & 0x7f7f7f7fu) + add) | ((v.y & 0x7f7f7f7fu) + add) |
+                                       ((v.z & 0x7f7f7f7fu) + add) | ((v.w & 0x7f7f7f7fu) + add);
+                            }
+                            if (bad & 0x80808080u) {
+                                for (int k = 0; k < D / 4; ++k) {
+                                    const uint32_t v = ((uint32_t *)row)[k], nan = ((v & 0x7f7f7f7fu) + add) & 0x80808080u;
+                                    ((uint32_t *)row)[k] = v & ~((nan >> 7) * 0xffu);
+                                }
+                                v_scale = __int_as_float(0x7fffffff);
+                            }
                         }
-                        half[c / 2] = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632);
                     }
-                    int word;
-                    const uint32_t top = warp_max_halves<CW / 2>(half, lane, word);
-                    constexpr int kSame = 32 / (CW / 2);  // lanes with the same word
-                    if ((lane & (kSame - 1)) < 2) {
-                        const int up = lane & 1;  // kSame >= 2: one lane for each half
-                        atomicMax(&sh.top[slot][c0 + 2 * word + up], ((up ? top >> 16 : top) & 0x7fffu) >> 7);
+                    const uint32_t slot = mine & 3;
+                    if (t < NT)
+                        sh.top[w][(slot + 1) & 3][t] = 0;
+                    mbar_wait(&sh.s_full[w], mine & 1, dead);
+                    tc_after();
+
+                    const auto load_scores = [&]() {
+#pragma unroll
+                        for (int c = 0; c < NT; c += 16)
+                            TmemLoad<16>::go(s_at + c, e + c);
+                        tmem_wait<NT>(e);
+                    };
+                    // scores less base, for columns c .. c + 3
+                    const auto scores = [&](int c, bool based) {
+                        const float4 f4 = *(const float4 *)(col.factor + c);
+                        float4 b4 = make_float4(0, 0, 0, 0), sl = b4, ps = b4;
+                        if (based)
+                            b4 = *(const float4 *)(sh.base[w] + c);
+                        if (FORM && a.f.slopes) {
+                            sl = *(const float4 *)(col.slope + c);
+                            ps = *(const float4 *)(col.pos + c);
+                        }
+                        e[c] = score<FORM>(a, e[c], k_scale * f4.x, b4.x, sl.x, ps.x - pos);
+                        e[c + 1] = score<FORM>(a, e[c + 1], k_scale * f4.y, b4.y, sl.y, ps.y - pos);
+                        e[c + 2] = score<FORM>(a, e[c + 2], k_scale * f4.z, b4.z, sl.z, ps.z - pos);
+                        e[c + 3] = score<FORM>(a, e[c + 3], k_scale * f4.w, b4.w, sl.w, ps.w - pos);
+                    };
+                    while (true) {
+                        if (closely) {
+                            // bases from the rows' largest scores
+                            load_scores();
+#pragma unroll
+                            for (int c = 0; c < NT; c += 4)
+                                scores(c, false);
+#pragma unroll
+                            for (int c0 = 0; c0 < NT; c0 += kChunk) {
+                                int key[kChunk], which;
+#pragma unroll
+                                for (int c = 0; c < kChunk; ++c) {
+                                    const float y = e[c0 + c];
+                                    key[c] = ((see >> (c0 + c)) & 1) && y == y ? ordered(y) : INT_MIN;
+                                }
+                                const int most = warp_combine<kChunk>(key, lane, which, MaxInt());
+                                if ((lane & (32 / kChunk - 1)) == 0)
+                                    atomicMax(&sh.highest[w][c0 + which], most);
+                            }
+                            named_barrier<128>(bar);
+                            if (t < (NT + 31) / 32 * 32) {
+                                float alpha = 1.0f;
+                                bool set = true;
+                                if (t < NT) {
+                                    const int top = sh.highest[w][t];
+                                    const float high = __int_as_float(top ^ ((top >> 31) & 0x7fffffff)), old = sh.base[w][t];
+                                    sh.highest[w][t] = INT_MIN;
+                                    set = sh.is_set[w][t];
+                                    if (top != INT_MIN && high > -INFINITY) {
+                                        if (!set || high - old > 32.0f) {
+                                            const float now = fminf(fmaxf(ceilf(high), -0x1p30f), 0x1p30f);
+                                            alpha = set ? exp2f(old - now) : 1.0f;
+                                            sh.base[w][t] = now;
+                                        }
+                                        sh.is_set[w][t] = 1;
+                                        set = true;
+                                    }
+                                    set = set || col.query[t] < 0;
+                                    sh.alpha[w][t] = alpha;
+                                }
+                                const bool any = __any_sync(0xffffffffu, alpha != 1.0f), open = __any_sync(0xffffffffu, !set);
+                                if (lane == 0) {
+                                    sh.moved[w][t >> 5] = any;
+                                    sh.unset[w][t >> 5] = open;
+                                }
+                            }
+                            named_barrier<128>(bar);
+                            if (!fresh && (sh.moved[w][0] || (NT > 32 && sh.moved[w][1]))) {
+                                if (S::kSumsInTmem) {
+#pragma unroll 1
+                                    for (int c0 = 0; c0 < NT; c0 += 16) {
+                                        float y[16];
+                                        TmemLoad<16>::go(l_at + c0, y);
+                                        tmem_wait<16>(y);
+#pragma unroll
+                                        for (int c = 0; c < 16; ++c)
+                                            y[c] *= sh.alpha[w][c0 + c];
+                                        tmem_store16(l_at + c0, y);
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int c = 0; c < LR; ++c)
+                                        l[c] *= sh.alpha[w][c];
+                                }
+                            }
+                        }
+                        load_scores();
+#pragma unroll
+                        for (int c = 0; c < NT; c += 4) {
+                            scores(c, true);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                e[c + k] = exp2_fast(e[c + k]);
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int c = 0; c < NT; ++c)
+                                e[c] = (see >> c) & 1 ? e[c] : 0.0f;
+                        }
+                        // the tile's largest exponents; a score that passed its base by 2^64, or a block of values so small
+                        // that this would not show, sends the warpgroup round again
+                        bool again = v_scale < 0x1p-40f;
+#pragma unroll
+                        for (int c0 = 0; c0 < NT; c0 += kChunk) {
+                            uint32_t half[kChunk / 2];
+#pragma unroll
+                            for (int c = 0; c < kChunk; c += 2) {
+                                float y0 = e[c0 + c] * v_scale, y1 = e[c0 + c + 1] * v_scale;
+                                if (edge) {
+                                    y0 = e[c0 + c] == 0.0f ? 0.0f : y0;
+                                    y1 = e[c0 + c + 1] == 0.0f ? 0.0f : y1;
+                                }
+                                half[c / 2] = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632);
+                            }
+                            int which;
+                            const uint32_t most = warp_combine<kChunk / 2>(half, lane, which, MaxHalves());
+                            constexpr int kSame = 64 / kChunk;  // lanes with the same two columns: 2 or 4
+                            const uint32_t ex = (((lane & 1 ? most >> 16 : most) & 0x7fffu) + 0x1fu) >> 7;
+                            if ((lane & (kSame - 1)) < 2)
+                                atomicMax(&sh.top[w][slot][c0 + 2 * which + (lane & 1)], ex);
+                            again = again || ex >= 127 + 64;
+                        }
+                        const bool once_more = barrier_or<128>(bar, again && !closely);
+                        if (!once_more)
+                            break;
+                        if (t < NT)
+                            sh.top[w][slot][t] = 0;
+                        closely = true;
                     }
-                };
-                if (t < CW)
-                    sh.top[(slot + 1) & 7][c0 + t] = 0;
-                if (t == 0)
-                    sh.moved[g & 7][w] = 0;
-                const uint4 *top4 = (const uint4 *)(sh.top[slot] + c0);
-                while (true) {
-                    if (closely)
-                        rebase();
-                    exponentials();
-                    named_barrier<128>(1 + w);
-                    if (closely)
-                        break;
-                    uint32_t most = 0;
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sh.s_free[w]);
+                    const uint32_t *tops = sh.top[w][slot];
+                    if (t < NT)
+                        sh.power[g % kRing][t] = (int)max(tops[t], 9u) - 135 + (int)sh.base[w][t];
+                    if (S::kSumsInTmem) {
 #pragma unroll
-                    for (int c4 = 0; c4 < CW / 4; ++c4) {
-                        const uint4 y = top4[c4];
-                        most = max(max(most, max(y.x, y.y)), max(y.z, y.w));
-                    }
-                    if (most < 127 + 64)
-                        break;
-                    // a score passed its base by 2^64 (the same verdict in the whole warpgroup): once more, closely
-                    named_barrier<128>(1 + w);
-                    if (t < CW)
-                        sh.top[slot][c0 + t] = 0;
-                    closely = true;
-                }
-                tc_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sh.s_free[i]);
-                mbar_wait(&sh.o_full[i], par ^ 1, dead);  // the products of tile g - 2 have read this buffer
-                uint32_t hi[CW / 4], lo[CW / 4];
+                        for (int c0 = 0; c0 < NT; c0 += 16) {
+                            float y[16];
+                            if (!fresh) {
+                                TmemLoad<16>::go(l_at + c0, y);
+                                tmem_wait<16>(y);
+                            }
 #pragma unroll
-                for (int c4 = 0; c4 < CW / 4; ++c4) {
-                    const uint4 y = top4[c4];
-                    const uint32_t ex[4] = {y.x, y.y, y.z, y.w};
-                    float p[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int c = c4 * 4 + k;
-                        // 2^(7 - exponent): the tile's largest weight of the row lands in [128, 256)
-                        const float scale = __uint_as_float((261u - max(ex[k], 8u)) << 23) * vs;
-                        l[c] += e[c];
-                        p[k] = e[c] * scale;
-                        if (edge && e[c] == 0.0f)
-                            p[k] = 0.0f;
-                    }
-                    uint32_t first[2], rest[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t h2, back;
-                        uint16_t b1, b2;
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h2) : "f"(p[2 * k + 1]), "f"(p[2 * k]));
-                        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b1) : "r"(h2));
-                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(b1));
-                        asm("sub.f16x2 %0, %1, %2;" : "=r"(back) : "r"(h2), "r"(back));
-                        asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b2) : "r"(back));
-                        first[k] = b1;
-                        rest[k] = b2;
-                    }
-                    hi[c4] = first[0] | first[1] << 16;
-                    lo[c4] = rest[0] | rest[1] << 16;
-                }
-#pragma unroll
-                for (int term = 0; term < 2; ++term) {
-                    const uint32_t *b = term ? lo : hi;
-                    uint8_t *dst = sh.p[i][term] + (c0 >> 4) * (kTile * 16) + t * 16 + (c0 & 15);
-                    if (CW >= 16) {
-#pragma unroll
-                        for (int k = 0; k < CW / 16; ++k)
-                            *(uint4 *)(dst + k * kTile * 16) = make_uint4(b[4 * k], b[4 * k + 1], b[4 * k + 2], b[4 * k + 3]);
+                            for (int c = 0; c < 16; ++c)
+                                y[c] = (fresh ? 0.0f : y[c]) + e[c0 + c];
+                            tmem_store16(l_at + c0, y);
+                        }
                     } else {
-                        *(uint2 *)dst = make_uint2(b[0], b[1]);
+#pragma unroll
+                        for (int c = 0; c < LR; ++c)
+                            l[c] += e[c];
                     }
+                    mbar_wait(&sh.p_free[w], (mine & 1) ^ 1, dead);
+#pragma unroll
+                    for (int c0 = 0; c0 < NT; c0 += 16) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int c4 = 0; c4 < 4; ++c4) {
+                            const uint4 y = *(const uint4 *)(tops + c0 + c4 * 4);
+                            const uint32_t ex[4] = {y.x, y.y, y.z, y.w};
+                            float p[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int c = c0 + c4 * 4 + k;
+                                // 2^(135 - exponent): the tile's largest weight of the row lands in [224, 448]
+                                const float scale = __uint_as_float((262u - max(ex[k], 9u)) << 23) * v_scale;
+                                p[k] = e[c] * scale;
+                                if (edge && e[c] == 0.0f)
+                                    p[k] = 0.0f;
+                            }
+                            uint32_t first[2], rest[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                uint32_t h2, back;
+                                uint16_t b1, b2;
+                                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h2) : "f"(p[2 * k + 1]), "f"(p[2 * k]));
+                                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b1) : "r"(h2));
+                                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(b1));
+                                asm("sub.f16x2 %0, %1, %2;" : "=r"(back) : "r"(h2), "r"(back));
+                                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b2) : "r"(back));
+                                first[k] = b1;
+                                rest[k] = b2;
+                            }
+                            hi[c4] = first[0] | first[1] << 16;
+                            lo[c4] = rest[0] | rest[1] << 16;
+                        }
+                        uint8_t *dst = sh.p[w][0] + (c0 >> 4) * (kTile * 16) + t * 16;
+                        *(uint4 *)dst = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *(uint4 *)(dst + kTile * NT) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
+                    proxy_fence();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sh.p_ready[g % kRing]);
+                    ++mine;
+                    fresh = false;
                 }
-                proxy_fence();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sh.p_ready[g & 3]);
                 ++g;
-                if (++st == ST) {
-                    st = 0;
-                    phase ^= 1;
+                turn = turn + 1 == NW ? 0 : turn + 1;
+                if (++vs == VS) {
+                    vs = 0;
+                    v_phase ^= 1;
                 }
             }
-            // the rows' totals: lanes, then four warps in shared memory
-            mbar_wait(&sh.sum_free, (seg & 1) ^ 1, dead);
+            // the rows' totals, warp by warp
+            mbar_wait(&sh.sum_free[seg & 1], ((seg >> 1) & 1) ^ 1, dead);
+            if (t < NT)
+                sh.last_base[seg & 1][w][t] = sh.base[w][t];
 #pragma unroll
-            for (int c = 0; c < CW; ++c) {
-                float y = l[c];
+            for (int c0 = 0; c0 < NT; c0 += 16) {
+                float y[16];
+                int which;
+                if (S::kSumsInTmem) {
+                    if (!fresh) {
+                        TmemLoad<16>::go(l_at + c0, y);
+                        tmem_wait<16>(y);
+                    }
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    y += __shfl_xor_sync(0xffffffffu, y, o);
-                if (lane == 0)
-                    sh.warp_total[wid & 3][c0 + c] = y;
+                    for (int c = 0; c < 16; ++c)
+                        y[c] = fresh ? 0.0f : y[c];
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        y[c] = l[(c0 + c) % LR];
+                }
+                const float sum = warp_combine<16>(y, lane, which, Add());
+                if ((lane & 1) == 0)
+                    sh.warp_total[seg & 1][w * 4 + (wid & 3)][c0 + which] = sum;
             }
-            if (t < CW)
-                sh.last_base[c0 + t] = sh.col.base[c0 + t];
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&sh.sum_ready);
+                mbar_arrive(&sh.sum_ready[seg & 1]);
             ++seg;
+            named_barrier<128>(bar);  // base has been read: the next segment may reset it
         }
     } else {
         // ---------------- adding up ----------------
         const int o0 = D == 128 ? 0 : (wid >> 1) * OC, d = D == 128 ? tid : tid & 63;
         const uint32_t lanes = (uint32_t)wid << 21;
-        constexpr int kPart = OC < 16 ? OC : 16;
-        uint32_t g = 0, seg = 0;
+        constexpr int kPart = OC % 16 == 0 ? 16 : 8;
+        uint32_t g = 0, seg = 0, prepared = 0;
+        bool told = false;
         float o[OC];
+        Walk<NT> ahead = walk;
+        // the queries of the next segment that has any work
+        const auto prepare = [&]() {
+            while (ahead.next()) {
+                const Unit &u = ahead.u;
+                if (u.count == 0)
+                    continue;
+                const bool tree = a.f.parent && (long long)(u.tile(ahead.x1 - 1) + 1) * kTile > u.first;
+                Columns<NT> &col = sh.col[prepared & 1];
+                load_queries<D, NT, 128>(a, u, ahead.b, ahead.h, ahead.rt, tree, sh.q[prepared & 1][0], col, tid);
+                if (tree) {
+                    named_barrier<128>(4 + NW);
+                    mark_kin<NT>(u, col, tid);
+                }
+                if (tid == 0) {
+                    Segment &g = sh.seg[prepared & 1];
+                    g.tiles = ahead.x1 - ahead.x0;
+                    g.x0 = ahead.x0;
+                    g.head_tiles = u.head_tiles;
+                    g.low = u.low;
+                    g.len = u.len;
+                    g.first = u.first;
+                    g.prefix = u.prefix;
+                    g.i1 = u.i1;
+                    g.rt = ahead.rt;
+                    g.seen_prefix = u.prefix / kTile;
+                    g.seen_end = (a.f.parent ? u.first : u.first + u.i0 + 1) / kTile;
+                    g.seen_low = a.f.window > 0 ? (int)((max((long long)u.first + u.i1 - a.f.window + 1, 0ll) + kTile - 1) / kTile)
+                                                : 0;
+                }
+                proxy_fence();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.q_ready[prepared & 1]);
+                ++prepared;
+                return;
+            }
+            if (!told) {  // that was the last one
+                if (tid == 0)
+                    sh.seg[prepared & 1].tiles = 0;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.q_ready[prepared & 1]);
+                told = true;
+            }
+        };
+        prepare();
         while (walk.next()) {
+            const bool none = walk.u.count == 0;
+            if (!none)
+                prepare();
 #pragma unroll
             for (int c = 0; c < OC; ++c)
                 o[c] = 0.0f;
-            const bool none = walk.u.count == 0;
+            int ref = INT_MIN;  // of column tid: its sums count 2^ref
             for (int x = walk.x0; x < walk.x1 && !none; ++x) {
-                const uint32_t i = g & 1, par = (g >> 1) & 1;
-                mbar_wait(&sh.p_ready[g & 3], (g >> 2) & 1, dead);  // top, alpha and moved of the tile
-#pragma unroll
-                for (int w = 0; w < 2; ++w)
-                    if (sh.moved[g & 7][w]) {
-#pragma unroll
-                        for (int c = 0; c < OC; ++c)
-                            if ((o0 + c) / CW == w)
-                                o[c] *= sh.alpha[g & 7][o0 + c];
+                const uint32_t i = g & 1;
+                mbar_wait(&sh.p_ready[g % kRing], (g / kRing) & 1, dead);  // the tile's powers
+                bool moved = false;
+                float alpha = 1.0f;
+                if (tid < NT) {
+                    const int power = sh.power[g % kRing][tid];
+                    if (ref == INT_MIN) {
+                        ref = power;
+                    } else if (power > ref + 60) {
+                        alpha = power2(max(ref - power, -200));
+                        ref = power;
+                        moved = true;
                     }
-                mbar_wait(&sh.o_full[i], par, dead);
+                    sh.factor[i][tid] = power2(max(power - ref, -200));
+                }
+                if (barrier_or<128>(4 + NW, moved)) {
+                    if (tid < NT)
+                        sh.inverse[tid] = alpha;
+                    named_barrier<128>(4 + NW);
+#pragma unroll
+                    for (int c = 0; c < OC; ++c)
+                        o[c] *= sh.inverse[o0 + c];
+                }
+                mbar_wait(&sh.o_full[i], (g >> 1) & 1, dead);
                 tc_after();
 #pragma unroll
                 for (int c1 = 0; c1 < OC; c1 += kPart) {
                     float y[kPart];
-                    TmemLoad<kPart>::go(tmem + lanes + (2 + i) * NT + o0 + c1, y);
+                    TmemLoad<kPart>::go(tmem + lanes + kO + i * NT + o0 + c1, y);
                     tmem_wait<kPart>(y);
 #pragma unroll
-                    for (int c4 = 0; c4 < kPart / 4; ++c4) {
-                        const uint4 ex = ((const uint4 *)(sh.top[g & 7] + o0 + c1))[c4];
-                        const uint32_t x4[4] = {ex.x, ex.y, ex.z, ex.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            o[c1 + c4 * 4 + k] =
-                                fmaf(y[c4 * 4 + k], __uint_as_float((max(x4[k], 8u) - 7u) << 23), o[c1 + c4 * 4 + k]);
+                    for (int c = 0; c < kPart; c += 4) {
+                        const float4 f = *(const float4 *)(sh.factor[i] + o0 + c1 + c);
+                        o[c1 + c] = fmaf(y[c], f.x, o[c1 + c]);
+                        o[c1 + c + 1] = fmaf(y[c + 1], f.y, o[c1 + c + 1]);
+                        o[c1 + c + 2] = fmaf(y[c + 2], f.z, o[c1 + c + 2]);
+                        o[c1 + c + 3] = fmaf(y[c + 3], f.w, o[c1 + c + 3]);
                     }
                 }
                 tc_before();
@@ -1093,43 +1346,55 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
             const long long slot = 2ll * blockIdx.x + (walk.x0 == 0);
             const int rows = a.n * a.group;
             if (!none)
-                mbar_wait(&sh.sum_ready, seg & 1, dead);
-            named_barrier<128>(4);
+                mbar_wait(&sh.sum_ready[seg & 1], (seg >> 1) & 1, dead);
+            named_barrier<128>(4 + NW);
             if (tid < NT) {
                 const int r = walk.rt * NT + tid, i = r / a.group;
-                float total = 0.0f, base = 0.0f;
-                if (!none) {
-                    total = (sh.warp_total[0][tid] + sh.warp_total[1][tid]) + (sh.warp_total[2][tid] + sh.warp_total[3][tid]);
-                    base = sh.last_base[tid];
+                float total = 0.0f, base = 0.0f, part[NW];
+                if (!none && i <= walk.u.i1) {
+                    bool any = false;
+                    const float(*y)[NT] = sh.warp_total[seg & 1], (*last)[NT] = sh.last_base[seg & 1];
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) {
+                        part[w] = (y[4 * w][tid] + y[4 * w + 1][tid]) + (y[4 * w + 2][tid] + y[4 * w + 3][tid]);
+                        if (!(part[w] == 0.0f)) {
+                            base = any ? fmaxf(base, last[w][tid]) : last[w][tid];
+                            any = true;
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < NW; ++w)
+                        total += part[w] == 0.0f ? 0.0f : part[w] * exp2f(last[w][tid] - base);
                 }
-                const bool live = !none && i <= walk.u.i1 && !(total == 0.0f);
+                const bool live = !(total == 0.0f);
+                // sums count 2^ref, totals 2^base
+                const float level = ref == INT_MIN ? 0.0f : power2(max(min(ref - (int)base, 127), -200));
+                sh.inverse[tid] = whole ? (live ? level / total : 0.0f) : level;
                 if (whole) {
-                    sh.inverse[tid] = live ? 1.0f / total : 0.0f;
                     if (r < rows)
                         a.lse[((size_t)walk.b * a.n + i) * a.heads + walk.h * a.group + r % a.group] =
                             live ? (base + log2f(total)) * 0.6931471805599453f : -INFINITY;
                 } else {
-                    a.part_sum[slot * NT + tid] = make_float2(i <= walk.u.i1 ? total : 0.0f, base);
+                    a.part_sum[slot * NT + tid] = make_float2(total, base);
                 }
             }
             if (!whole && walk.x1 == max(walk.count, 1) && tid == 0)
                 a.joins[blockIdx.x] = make_int4((int)((walk.at - walk.x0) / range.each), walk.b, walk.h, walk.rt);
-            named_barrier<128>(4);
+            named_barrier<128>(4 + NW);
             if (!none) {
                 if (lane == 0)
-                    mbar_arrive(&sh.sum_free);
+                    mbar_arrive(&sh.sum_free[seg & 1]);
                 ++seg;
             }
 #pragma unroll
             for (int c = 0; c < OC; ++c) {
                 const int r = walk.rt * NT + o0 + c;
-                if (!whole) {
-                    a.part[(slot * NT + o0 + c) * D + d] = o[c];
-                } else if (r < rows) {
-                    const float inv = sh.inverse[o0 + c];
+                const float inv = sh.inverse[o0 + c], y = inv == 0.0f ? 0.0f : o[c] * inv;
+                if (!whole)
+                    a.part[(slot * NT + o0 + c) * D + d] = y;
+                else if (r < rows)
                     a.out[(((size_t)walk.b * a.n + r / a.group) * a.heads + walk.h * a.group + r % a.group) * D + d] =
-                        __float2bfloat16(inv == 0.0f ? 0.0f : o[c] * inv);
-                }
+                        __float2bfloat16(y);
             }
         }
     }
@@ -1137,8 +1402,8 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
     tc_before();
     __syncthreads();
     tc_after();
-    if (wid == 13)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(4 * NT));
+    if (wid == kProducts)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kAlloc));
 }
 
 // ===========================================================================
@@ -1151,7 +1416,7 @@ __global__ void __launch_bounds__(kAttendThreads, 1)
 constexpr int kWeighThreads = 320;
 
 template <int D, int NT> struct WeighShared {
-    static constexpr int kStages = 10;
+    static constexpr int kStages = 10, kAlloc = NT == 48 ? 128 : 2 * NT;
     alignas(1024) uint8_t tiles[kStages][kTile * D];
     alignas(1024) uint8_t q[2][NT * D];
     alignas(16) Columns<NT> col;
@@ -1193,7 +1458,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     }
     if (wid == 9) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
-                     "r"(2 * NT)
+                     "r"(Shared::kAlloc)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         tc_before();
@@ -1282,7 +1547,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                 const int w = wid >> 2, t = tid & 127;
                 named_barrier<256>(3);
                 const bool tree = a.f.parent && (long long)(all.tile(x1 - 1) + 1) * kTile > u.first;
-                load_queries<D, NT>(a, u, b, h, rt, tree, sh.q[0], sh.col, tid);
+                load_queries<D, NT, 256>(a, u, b, h, rt, tree, sh.q[0], sh.col, tid);
                 if (tid < NT) {
                     const int r = rt * NT + tid, i = r / a.group;
                     const float lse =
@@ -1316,7 +1581,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                         mbar_wait(&sh.s_full[g & 1], (g >> 1) & 1, dead);
                         tc_after();
                         float sum = 0.0f;
-                        constexpr int kPart = NT < 32 ? NT : 32;
+                        constexpr int kPart = NT % 32 == 0 ? 32 : 16;
 #pragma unroll 1
                         for (int c1 = 0; c1 < NT; c1 += kPart) {
                             float s[kPart];
@@ -1365,7 +1630,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     __syncthreads();
     tc_after();
     if (wid == 9)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * NT));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Shared::kAlloc));
 }
 
 // Joins the parts of units that several CTAs worked on: CTA (c, y) joins rows
@@ -1408,10 +1673,10 @@ template <int D, int NT> __global__ void __launch_bounds__(128) join_kernel(cons
     }
 }
 
-// The kernels of one head size, by columns per row tile (16, 32 or 64).
+// The kernels of one head size, by columns per row tile (16, 32, 48 or 64).
 struct Kernels {
-    const void *attend[3][2], *join[3], *weigh[3][2];  // [..][a cap or a bias]
-    int attend_smem[3], weigh_smem[3];
+    const void *attend[4][2], *join[4], *weigh[4][2];  // [..][a cap or a bias]
+    int attend_smem[4], attend_threads[4], weigh_smem[4];
 };
 const Kernels &kernels_d64();
 const Kernels &kernels_d128();
@@ -1424,6 +1689,7 @@ template <int D, int NT> void fill(Kernels &k, int i)
     k.weigh[i][0] = (const void *)weigh_kernel<D, NT, false>;
     k.weigh[i][1] = (const void *)weigh_kernel<D, NT, true>;
     k.attend_smem[i] = (int)sizeof(AttendShared<D, NT>) + 1024;  // room to align
+    k.attend_threads[i] = AttendShape<D, NT>::kThreads;
     k.weigh_smem[i] = (int)sizeof(WeighShared<D, NT>) + 1024;
     static_assert(sizeof(AttendShared<D, NT>) + 2048 <= 227 * 1024 && sizeof(WeighShared<D, NT>) + 2048 <= 227 * 1024,
                   "shared memory of a CTA");
@@ -1433,7 +1699,8 @@ template <int D> Kernels all_kernels()
     Kernels k{};
     fill<D, 16>(k, 0);
     fill<D, 32>(k, 1);
-    fill<D, 64>(k, 2);
+    fill<D, 48>(k, 2);
+    fill<D, 64>(k, 3);
     return k;
 }
 

@@ -90,6 +90,20 @@ def check_both(sv, case, **kw):
     return ref, out, lse
 
 
+def test_many_short_sequences(sv):
+    """Several short units to a CTA, of one tile and of a few, empty ones among them."""
+    lengths = [(b * 37) % 290 for b in range(330)]
+    new = [min(2, (b + 1) % 3, x) for b, x in enumerate(lengths)]
+    check_both(sv, Case(lengths, 2, heads=6, kv_heads=3, num_new=new, seed=20))
+
+
+def test_many_row_tiles(sv):
+    """More queries than one row tile holds, in sequences that are hardly longer."""
+    lengths = [70 + 9 * b for b in range(24)]
+    new = [min(64, 5 + 7 * b) for b in range(24)]
+    check_both(sv, Case(lengths, 64, heads=16, kv_heads=4, dim=128, block=32, num_new=new, seed=21))
+
+
 TREE = [[0, 0, 0, 1, 1, 2, 3], [0, 0, 1, 2, 3, 4, 5]]
 
 
