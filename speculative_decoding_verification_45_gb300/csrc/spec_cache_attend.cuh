@@ -206,8 +206,8 @@ __device__ __forceinline__ void tmem_store16(uint32_t a, const float *r)
                  "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]), "r"(u[10]),
                  "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(a)
                  : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // The registers of earlier loads are valid after this; they pass through it so that no use moves ahead.
 template <int N> __device__ __forceinline__ void tmem_wait(float *r)
 {
@@ -248,7 +248,7 @@ struct Unit {
     __device__ __forceinline__ int tile(int x) const { return x < head_tiles ? x : x - head_tiles + low; }
 };
 
-__device__ __forceinline__ Unit unit_for(const AttendArgs &a, int b, int i0, int i1)
+__device__ __noinline__ inline Unit unit_for(const AttendArgs &a, int b, int i0, int i1)
 {
     Unit u;
     const Seq s = sequence(a.c, a.lengths, a.f.num_new, a.n, b, true);
@@ -303,6 +303,7 @@ template <int THREADS, typename Cost> __device__ __forceinline__ Range find_rang
     long long total = 0;
     if (tid == 0)
         range.begin = range.end = 0;
+#pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         long long seen = 0, each = 0, begin = 0;
         if (pass == 1) {
@@ -440,7 +441,7 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const Unit &u,
 }
 
 // The ancestors of each column's query, after a barrier behind load_queries.
-template <int NT> __device__ __forceinline__ void mark_kin(const Unit &u, Columns<NT> &col, int t)
+template <int NT> __device__ __forceinline__ void mark_kin(Columns<NT> &col, int t)
 {
     if (t < NT) {
         for (int w = 0; w < kMaxNodes / 32; ++w)
@@ -471,8 +472,14 @@ __device__ __forceinline__ float score(const AttendArgs &a, float s, float f, fl
     if (!FORM)
         return fmaf(s, f, -base);
     float x = s * f;
-    if (a.f.softcap > 0.0f)  // cap tanh(y) = cap (1 - 2 / (1 + exp(2 y))); the quotient is 0 from 2^126 on
-        x = (1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x * (2.0f * kLog2e)))) * (a.f.softcap * kLog2e);
+    if (a.f.softcap > 0.0f) {
+        // tanh(y) = 1 - 2 / (1 + exp(2 y)) (the quotient is 0 from 2^126 on), which cancels near 0: there the first
+        // terms of its series, whose remainder is below 2^-24 of it up to 1/4
+        const float z = x * x;
+        const float series = x * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 62.0f / 2835, -17.0f / 315), 2.0f / 15), -1.0f / 3), 1.0f);
+        const float whole = 1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x * (2.0f * kLog2e)));
+        x = (fabsf(x) < 0.25f ? series : whole) * (a.f.softcap * kLog2e);
+    }
     if (a.f.slopes)
         x = fmaf(-slope, fabsf(distance), x);
     return x - base;
@@ -517,14 +524,15 @@ __device__ __forceinline__ void load_tile(const AttendArgs &a, const CUtensorMap
 
 // The segments of a CTA's stretch: units, or parts of them, in order.
 template <int NT> struct Walk {
-    const AttendArgs &a;
     long long at, end;
-    int b, h, rt, x0, x1, count;  // tiles [x0, x1) of the unit's max(count, 1)
+    int b, h, rt, x0, x1;  // tiles [x0, x1) of the unit's max(count, 1)
     Unit u;
-    bool started = false;
-    __device__ __forceinline__ Walk(const AttendArgs &args, const Range &r) : a(args), at(r.begin), end(r.end), b(r.b)
+    __device__ __noinline__ void start(const AttendArgs &a, const Range &r)
     {
-        h = rt = x0 = x1 = count = 0;
+        at = r.begin;
+        end = r.end;
+        b = r.b;
+        h = rt = x0 = x1 = 0;
         if (at >= end)
             return;
         // the unit that holds the first tile
@@ -541,31 +549,24 @@ template <int NT> struct Walk {
             ++rt;
         }
         x0 = (int)skip;
+        x1 = (int)min((long long)max(u.count, 1), x0 + (end - at));
     }
-    __device__ __forceinline__ bool next()
+    __device__ __noinline__ void next(const AttendArgs &a)
     {
-        if (started) {
-            at += x1 - x0;
-            if (at >= end)
-                return false;
-            x0 = 0;
-            if (++rt == a.row_tiles) {
-                rt = 0;
-                if (++h == a.c.kv_heads) {
-                    h = 0;
-                    ++b;
-                }
+        at += x1 - x0;
+        if (at >= end)
+            return;
+        x0 = 0;
+        if (++rt == a.row_tiles) {
+            rt = 0;
+            if (++h == a.c.kv_heads) {
+                h = 0;
+                ++b;
             }
-            u = row_unit<NT>(a, b, rt);
-        } else if (at >= end) {
-            return false;
         }
-        started = true;
-        count = u.count;
-        x1 = (int)min((long long)max(count, 1), x0 + (end - at));
-        return true;
+        u = row_unit<NT>(a, b, rt);
+        x1 = (int)min((long long)max(u.count, 1), end - at);
     }
-    __device__ __forceinline__ bool whole() const { return x0 == 0 && x1 == max(count, 1); }
 };
 
 // ===========================================================================
@@ -592,25 +593,30 @@ template <int NT> struct Walk {
 // upon before the exponentials.  What the 8-bit weights need is the maximum's
 // exponent only: 16-bit halves of the exponentials are compared two at a time
 // (16 shuffles for 32 columns) and the four warps meet in shared memory.
+//
+// Four softmax warpgroups want few registers and a short program: columns are
+// taken 16 at a time by the same instructions (with all columns unrolled, warps
+// waited for instructions more than for anything else), exponentials and running
+// totals live in tensor memory between the passes.
 template <int D, int NT> struct AttendShape {
-    static constexpr int NW = NT <= 32 ? 3 : 2;               // softmax warpgroups
+    static constexpr int NW = NT <= 32 ? 4 : NT == 48 ? 3 : 2;  // softmax warpgroups
     static constexpr int kThreads = 128 * (1 + NW) + 64;
-    static constexpr int kBytes = kTile * D;                  // one side of a tile
-    static constexpr int KS = 3, VS = D == 64 || NT == 16 ? 8 : 8 - NT / 16 + (NT == 48);  // tiles of keys and values in shared memory
-    static constexpr bool kSumsInTmem = NT >= 32;             // the rows' running totals, which registers cannot hold
-    static constexpr int kColumns = (kSumsInTmem ? 2 * NW + 2 : NW + 2) * NT;
-    static constexpr int kAlloc = kColumns <= 64 ? 64 : kColumns <= 128 ? 128 : kColumns <= 256 ? 256 : 512;
-    static constexpr int kChunk = 16;                         // columns of a warp reduction
-    static constexpr int kRing = 8;                           // >= NW + 2 tiles between a writer and the adding warps
+    static constexpr int kBytes = kTile * D;                    // one side of a tile
+    static constexpr int KS = 3, VS = D == 64 || NT == 16 ? 8 : NT >= 48 ? 5 : 6;  // tiles of keys and values in shared memory
+    static constexpr bool kKeep = (3 * NW + 2) * NT <= 512;     // room for the exponentials between the passes
+    static constexpr int kColumns = ((kKeep ? 3 : 2) * NW + 2) * NT;  // S^T, totals (and these) of each warpgroup, two O^T
+    static constexpr int kAlloc = kColumns <= 256 ? 256 : 512;
+    static constexpr int kRing = 8;                             // >= NW + 2 tiles between a writer and the adding warps
 };
 
-// What the softmax and the products need to know of a segment; the adding warps
-// write it with the segment's queries.
+// What the other warps need to know of a segment.
 struct Segment {
     int tiles;  // 0: there is none left
     int x0, head_tiles, low;
-    int len, first, prefix, i1, rt;
+    int len, first, prefix, i1, b, h, rt;
     int seen_prefix, seen_low, seen_end;  // tiles that every query of the row tile sees whole: [0, ..) and [low, end)
+    int whole, last;                      // the whole unit; its last part
+    long long at;                         // first tile's place in the order of all
     __device__ __forceinline__ int tile(int k) const { return x0 + k < head_tiles ? x0 + k : x0 + k - head_tiles + low; }
 };
 
@@ -624,20 +630,22 @@ template <int D, int NT> struct AttendShared {
     Segment seg[2];
     alignas(16) StageInfo info[S::VS];
     alignas(16) float base[S::NW][NT];
-    alignas(16) uint32_t top[S::NW][4][NT];  // per tile: exponent (biased) of the largest exp2(x - base) * v_scale / 1.75, rounded up
-    alignas(16) int power[S::kRing][NT];     // per tile: O^T counts 2^power
+    alignas(16) uint32_t scale[S::NW][4][NT];  // per tile: 2^k, as bits, that brings the largest weight to [224, 448]
+    alignas(16) int power[S::kRing][NT];       // per tile: O^T counts 2^power
     alignas(16) float factor[2][NT], inverse[NT];
     alignas(16) float warp_total[2][S::NW * 4][NT], last_base[2][S::NW][NT];
-    alignas(16) float alpha[S::NW][NT];      // what a moved base leaves of the totals
-    int highest[S::NW][NT];                  // ordered bits of the largest score
-    int is_set[S::NW][NT];                   // the row has a base
-    int moved[S::NW][2], unset[S::NW][2];    // by 32 columns
+    alignas(16) float alpha[S::NW][NT];        // what a moved base leaves of the totals
+    int highest[S::NW][NT];                    // ordered bits of the largest score
+    int is_set[S::NW][NT];                     // the row has a base
+    int moved[S::NW][2], unset[S::NW][2];      // by 32 columns
     alignas(8) uint64_t k_full[S::KS], k_empty[S::KS], v_full[S::VS], v_empty[S::VS];
-    uint64_t s_full[S::NW], s_free[S::NW], p_ready[S::kRing], p_free[S::NW], o_full[2], o_free[2], q_ready[2];
+    uint64_t s_full[S::NW], s_free[S::NW], p_ready[S::kRing], p_free[S::NW], o_full[2], o_free[2], seg_ready[2], q_ready[2];
     uint64_t sum_ready[2], sum_free[2], drained;
     uint32_t tmem;
     int dead;
 };
+
+constexpr uint32_t kNoScale = 253u << 23;  // where a tile leaves nothing to a row
 
 __device__ __forceinline__ int ordered(float x)
 {
@@ -646,7 +654,11 @@ __device__ __forceinline__ int ordered(float x)
 }
 
 struct MaxHalves {
-    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return __vmaxu2(a, b); }
+    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const {
+        uint32_t r;
+        asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
 };
 struct MaxInt {
     __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
@@ -715,7 +727,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 {
     using S = AttendShape<D, NT>;
     using Shared = AttendShared<D, NT>;
-    constexpr int NW = S::NW, KS = S::KS, VS = S::VS, kRing = S::kRing, kChunk = S::kChunk;
+    constexpr int NW = S::NW, KS = S::KS, VS = S::VS, kRing = S::kRing;
     constexpr int kProducer = 4 * (1 + NW), kProducts = kProducer + 1;
     constexpr int OC = D == 128 ? NT : NT / 2;  // columns of an adding thread
     constexpr uint32_t kO = NW * NT, kL = kO + 2 * NT;  // S^T at 0, then O^T, then the totals
@@ -744,6 +756,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.o_full[i], 1);
             mbar_init(&sh.o_free[i], 4);
+            mbar_init(&sh.seg_ready[i], 1);
             mbar_init(&sh.q_ready[i], 4);
             mbar_init(&sh.sum_ready[i], 4 * NW);
             mbar_init(&sh.sum_free[i], 4);
@@ -753,7 +766,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
     for (int i = tid; i < NW * 4 * NT; i += S::kThreads)
-        ((uint32_t *)sh.top)[i] = 0;
+        ((uint32_t *)sh.scale)[i] = kNoScale;
     for (int i = tid; i < NW * NT; i += S::kThreads)
         ((int *)sh.highest)[i] = INT_MIN;
     if (wid == kProducts) {
@@ -775,7 +788,6 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
     tc_after();
     const uint32_t tmem = sh.tmem;
     const int P = a.c.block, blocks = kTile / P, log_p = 31 - __clz(P);
-    Walk<NT> walk(a, range);
 
     if (wid == kProducer) {
         // ---------------- producer ----------------
@@ -784,23 +796,25 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         int ks = 0, vs = 0;
         uint32_t k_phase = 1, v_phase = 1, issued = 0;
         const bool pos = a.f.slopes && a.c.positions;
-        while (walk.next()) {
-            const Unit &u = walk.u;
-            if (u.count == 0)
-                continue;
+        for (uint32_t seg = 0; !__any_sync(0xffffffffu, *dead); ++seg) {
+            mbar_wait(&sh.seg_ready[seg & 1], (seg >> 1) & 1, dead);
+            const Segment &u = sh.seg[seg & 1];
+            const int tiles = u.tiles, h = u.h;
+            if (tiles == 0)
+                break;
+            const int32_t *table = a.c.block_table + (size_t)u.b * a.c.table_stride;
             const auto page_at = [&](int x) {
                 const int blk = u.tile(x) * blocks + lane;
-                return lane < blocks && (long long)blk * P < u.len ? a.c.block_table[(size_t)walk.b * a.c.table_stride + blk]
-                                                                   : -2;
+                return lane < blocks && (long long)blk * P < u.len ? table[blk] : -2;
             };
-            int page = page_at(walk.x0);
-            for (int x = walk.x0; x < walk.x1; ++x) {
-                const int next = x + 1 < walk.x1 ? page_at(x + 1) : -2;
+            int page = page_at(0);
+            for (int x = 0; x < tiles; ++x) {
+                const int next = x + 1 < tiles ? page_at(x + 1) : -2;
                 const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
                 if (page != -2 && !ok)
                     report(a.status, SPEC_STATUS_BAD_PAGE);
                 const uint32_t came = __ballot_sync(0xffffffffu, ok);
-                const size_t at = (size_t)max(page, 0) * a.c.kv_heads + walk.h;
+                const size_t at = (size_t)max(page, 0) * a.c.kv_heads + h;
                 mbar_wait(&sh.k_empty[ks], k_phase, dead);
                 bool go = !__any_sync(0xffffffffu, *dead);
                 if (go) {
@@ -808,7 +822,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                         mbar_expect(&sh.k_full[ks], (uint32_t)__popc(came) * (uint32_t)(P * D));
                     __syncwarp();
                     if (ok)
-                        tma_load(&kmap, sh.k[ks] + lane * P * D, &sh.k_full[ks], 0, 0, walk.h, page);
+                        tma_load(&kmap, sh.k[ks] + lane * P * D, &sh.k_full[ks], 0, 0, h, page);
                 }
                 mbar_wait(&sh.v_empty[vs], v_phase, dead);
                 go = go && !__any_sync(0xffffffffu, *dead);
@@ -820,7 +834,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     }
                     __syncwarp();
                     if (ok) {
-                        tma_load(&vmap, sh.v[vs] + lane * P * D, &sh.v_full[vs], 0, 0, walk.h, page);
+                        tma_load(&vmap, sh.v[vs] + lane * P * D, &sh.v_full[vs], 0, 0, h, page);
                         if (pos)
                             bulk_load(a.c.positions + at * P, info.pos + lane * P, (uint32_t)P * 4, &sh.v_full[vs]);
                         copy4(a.c.k_scale + at, info.k_scale + lane);
@@ -845,9 +859,14 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
     } else if (wid == kProducts) {
         // ---------------- products ----------------
         const uint32_t s_desc = instr_desc(NT, a.c.code, false, false), o_desc = instr_desc(NT, a.c.code, true, true);
-        const uint64_t swizzle = D == 128 ? 2 : 4;
+        constexpr uint64_t swizzle = D == 128 ? 2 : 4;
+        // descriptors of the first buffers; others lie a whole number of 16 bytes further
+        const uint64_t k_desc = smem_desc(smem_u32(sh.k[0]), 16, 8 * D, swizzle),
+                       q_desc = smem_desc(smem_u32(sh.q[0][0]), 16, 8 * D, swizzle),
+                       v_desc = smem_desc(smem_u32(sh.v[0]), 0, 8 * D, swizzle),
+                       p_desc = smem_desc(smem_u32(sh.p[0][0]), 128, kTile * 16, 0);
         int ks = 0, vs = 0, w = 0, pw = 0;  // pw: warpgroup of the next tile to be multiplied with values
-        uint32_t k_phase = 0, v_phase = 0, s_phase = 1, g = 0, done = 0, seg = 0, begun = 0;
+        uint32_t k_phase = 0, v_phase = 0, s_phase = 1, g = 0, done = 0, begun = 0;
         const auto values = [&]() {  // O^T of tile `done`
             const uint32_t i = done & 1;
             mbar_wait(&sh.p_ready[done % kRing], (done / kRing) & 1, dead);
@@ -855,14 +874,12 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             mbar_wait(&sh.o_free[i], ((done >> 1) & 1) ^ 1, dead);
             tc_after();
             if (lane == 0) {
-                const uint32_t v = smem_u32(sh.v[vs]), p = smem_u32(sh.p[pw][0]);
+                const uint64_t vd = v_desc + (uint32_t)vs * (S::kBytes >> 4), pd = p_desc + (uint32_t)pw * (2 * kTile * NT >> 4);
+                const uint32_t d = tmem + kO + i * NT;
 #pragma unroll
                 for (int k = 0; k < kTile / 32; ++k) {
-                    const uint64_t vd = smem_desc(v + k * 32 * D, 0, 8 * D, swizzle);
-#pragma unroll
-                    for (int term = 0; term < 2; ++term)
-                        tc_mma(tmem + kO + i * NT, vd, smem_desc(p + term * kTile * NT + k * 512, 128, kTile * 16, 0), o_desc,
-                               k + term > 0);
+                    tc_mma(d, vd + (k * 32 * D >> 4), pd + (k * 512 >> 4), o_desc, k > 0);
+                    tc_mma(d, vd + (k * 32 * D >> 4), pd + ((kTile * NT + k * 512) >> 4), o_desc, true);
                 }
                 tc_commit(&sh.o_full[i]);
                 tc_commit(&sh.p_free[pw]);
@@ -876,30 +893,39 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 v_phase ^= 1;
             }
         };
-        while (!*dead) {
-            // the next queries come once the segment before the last is complete: its products must not wait for them
-            while (done < begun)
-                values();
-            begun = g;
-            mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, dead);
-            const int tiles = sh.seg[seg & 1].tiles;
-            if (tiles == 0)
-                break;
-            const uint32_t q = smem_u32(sh.q[seg & 1][0]);
-            ++seg;
-            for (int x = 0; x < tiles; ++x) {
+        int tiles = 0, x = 0;
+        uint32_t seg = 0;
+        uint64_t qd = q_desc;
+        bool more = true;
+        // one turn: the scores of the next tile, if there is one, and the values of the tile NW before it
+#pragma unroll 1
+        while (more || done < g) {
+            bool issue = more;
+            if (more && x == tiles) {
+                // the next queries come once the segment before the last is complete: its products must not wait for them
+                if (done < begun) {
+                    issue = false;
+                } else {
+                    begun = g;
+                    mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, dead);
+                    tiles = *dead ? 0 : sh.seg[seg & 1].tiles;
+                    tiles = __shfl_sync(0xffffffffu, tiles, 0);
+                    qd = q_desc + (seg & 1) * (2 * NT * D >> 4);
+                    ++seg;
+                    x = 0;
+                    more = issue = tiles > 0;
+                }
+            }
+            if (issue) {
                 mbar_wait(&sh.k_full[ks], k_phase, dead);
                 mbar_wait(&sh.s_free[w], s_phase, dead);
                 tc_after();
                 if (lane == 0) {
-                    const uint32_t k = smem_u32(sh.k[ks]);
+                    const uint64_t kd = k_desc + (uint32_t)ks * (S::kBytes >> 4);
 #pragma unroll
                     for (int d = 0; d < D / 32; ++d) {
-                        const uint64_t kd = smem_desc(k + d * 32, 16, 8 * D, swizzle);
-#pragma unroll
-                        for (int term = 0; term < 2; ++term)
-                            tc_mma(tmem + w * NT, kd, smem_desc(q + term * NT * D + d * 32, 16, 8 * D, swizzle), s_desc,
-                                   d + term > 0);
+                        tc_mma(tmem + w * NT, kd + (d * 32 >> 4), qd + (d * 32 >> 4), s_desc, d > 0);
+                        tc_mma(tmem + w * NT, kd + (d * 32 >> 4), qd + ((NT * D + d * 32) >> 4), s_desc, true);
                     }
                     tc_commit(&sh.s_full[w]);
                     tc_commit(&sh.k_empty[ks]);
@@ -913,42 +939,45 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     ks = 0;
                     k_phase ^= 1;
                 }
-                if (++g > NW)
-                    values();
+                ++g;
+                ++x;
             }
+            if (!issue || g - done > NW)
+                if (done < g)
+                    values();
         }
-        while (done < g)
-            values();
         drain_products(&sh.drained, dead);
     } else if (wid >= 4) {
         // ---------------- softmax ----------------
         const int w = (wid >> 2) - 1, t = tid & 127, bar = 1 + w;
-        const uint32_t lanes = (uint32_t)(wid & 3) << 21, s_at = tmem + lanes + w * NT;
-        constexpr int LR = S::kSumsInTmem ? 1 : NT;
-        const uint32_t l_at = tmem + lanes + kL + w * NT;
+        const uint32_t lanes = (uint32_t)(wid & 3) << 21, s_at = tmem + lanes + w * NT, l_at = s_at + kL, e_at = l_at + NW * NT;
         int vs = 0, turn = 0;  // turn: whose tile it is
-        uint32_t v_phase = 0, g = 0, mine = 0, seg = 0;
-        float l[LR], e[NT];
-        while (true) {
+        uint32_t v_phase = 0, g = 0, mine = 0;
+#pragma unroll 1
+        for (uint32_t seg = 0;; ++seg) {
             mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, dead);
             const Segment &u = sh.seg[seg & 1];
             const Columns<NT> &col = sh.col[seg & 1];
             const int tiles = u.tiles;
             if (barrier_or<128>(bar, tiles == 0 || *dead))
                 break;
-            bool fresh = true;
+            bool fresh = true;  // no tile of this segment yet
+            {
+                const float zero[16] = {};
+                for (int c0 = 0; c0 < NT; c0 += 16)
+                    tmem_store16(l_at + c0, zero);
+                tmem_store_wait();
+            }
             if (t < NT) {
                 sh.base[w][t] = 0.0f;
                 sh.is_set[w][t] = 0;
             }
-#pragma unroll
-            for (int c = 0; c < LR; ++c)
-                l[c] = 0.0f;
+#pragma unroll 1
             for (int x = 0; x < tiles; ++x) {
                 if (turn == w) {
-                    const int tile = u.tile(x), j = tile * kTile + t;
                     mbar_wait(&sh.v_full[vs], v_phase, dead);
                     const StageInfo &info = sh.info[vs];
+                    const int tile = u.tile(x), j = tile * kTile + t;
                     const uint32_t came = info.came;
                     float k_scale = info.k_scale[t >> log_p], v_scale = info.v_scale[t >> log_p];
                     const float pos = FORM && a.f.slopes ? (a.c.positions ? (float)info.pos[t] : (float)j) : 0.0f;
@@ -956,6 +985,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                                       !(tile < u.seen_prefix || (tile >= u.seen_low && tile < u.seen_end));
                     bool closely = fresh;
                     uint64_t see = ~0ull;
+                    float v_most = v_scale;
                     if (edge) {
                         if (!fresh)
                             closely = sh.unset[w][0] || (NT > 32 && sh.unset[w][1]);
@@ -967,6 +997,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                         if (!cached) {  // nothing was loaded here
                             k_scale = 0.0f;
                             v_scale = 1.0f;
+                            v_most = 0.0f;
+#pragma unroll 1
                             for (int k = 0; k < D / 16; ++k)
                                 row[(k + t) & (D / 16 - 1)] = make_uint4(0, 0, 0, 0);
                         } else if (!all) {
@@ -974,12 +1006,14 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             // the weights of the rows that do see it become NaN
                             const uint32_t add = a.c.code == SPEC_E4M3 ? 0x01010101u : 0x04040404u;
                             uint32_t bad = 0;
+#pragma unroll 1
                             for (int k = 0; k < D / 16; ++k) {
                                 const uint4 v = row[(k + t) & (D / 16 - 1)];
                                 bad |= ((v.x & 0x7f7f7f7fu) + add) | ((v.y & 0x7f7f7f7fu) + add) |
                                        ((v.z & 0x7f7f7f7fu) + add) | ((v.w & 0x7f7f7f7fu) + add);
                             }
                             if (bad & 0x80808080u) {
+#pragma unroll 1
                                 for (int k = 0; k < D / 4; ++k) {
                                     const uint32_t v = ((uint32_t *)row)[k], nan = ((v & 0x7f7f7f7fu) + add) & 0x80808080u;
                                     ((uint32_t *)row)[k] = v & ~((nan >> 7) * 0xffu);
@@ -987,51 +1021,66 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                                 v_scale = __int_as_float(0x7fffffff);
                             }
                         }
+                        __syncwarp();
                     }
-                    const uint32_t slot = mine & 3;
-                    if (t < NT)
-                        sh.top[w][(slot + 1) & 3][t] = 0;
+                    // the largest scale among the warp's blocks (positive: the bits order as they do)
+                    v_most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v_most)));
+                    uint32_t *scales = sh.scale[w][mine & 3];
                     mbar_wait(&sh.s_full[w], mine & 1, dead);
                     tc_after();
 
-                    const auto load_scores = [&]() {
+                    // scores of columns c0 .. c0 + 15, less base
+                    const auto scores = [&](int c0, float *e, bool based) {
+                        const float4 *factor = (const float4 *)(col.factor + c0), *base = (const float4 *)(sh.base[w] + c0),
+                                     *slope = (const float4 *)(col.slope + c0), *from = (const float4 *)(col.pos + c0);
 #pragma unroll
-                        for (int c = 0; c < NT; c += 16)
-                            TmemLoad<16>::go(s_at + c, e + c);
-                        tmem_wait<NT>(e);
-                    };
-                    // scores less base, for columns c .. c + 3
-                    const auto scores = [&](int c, bool based) {
-                        const float4 f4 = *(const float4 *)(col.factor + c);
-                        float4 b4 = make_float4(0, 0, 0, 0), sl = b4, ps = b4;
-                        if (based)
-                            b4 = *(const float4 *)(sh.base[w] + c);
-                        if (FORM && a.f.slopes) {
-                            sl = *(const float4 *)(col.slope + c);
-                            ps = *(const float4 *)(col.pos + c);
+                        for (int c = 0; c < 4; ++c) {
+                            const float4 f = factor[c];
+                            float4 b4 = make_float4(0, 0, 0, 0), sl = b4, ps = b4;
+                            if (based)
+                                b4 = base[c];
+                            if (FORM && a.f.slopes) {
+                                sl = slope[c];
+                                ps = from[c];
+                            }
+                            e[4 * c] = score<FORM>(a, e[4 * c], k_scale * f.x, b4.x, sl.x, ps.x - pos);
+                            e[4 * c + 1] = score<FORM>(a, e[4 * c + 1], k_scale * f.y, b4.y, sl.y, ps.y - pos);
+                            e[4 * c + 2] = score<FORM>(a, e[4 * c + 2], k_scale * f.z, b4.z, sl.z, ps.z - pos);
+                            e[4 * c + 3] = score<FORM>(a, e[4 * c + 3], k_scale * f.w, b4.w, sl.w, ps.w - pos);
                         }
-                        e[c] = score<FORM>(a, e[c], k_scale * f4.x, b4.x, sl.x, ps.x - pos);
-                        e[c + 1] = score<FORM>(a, e[c + 1], k_scale * f4.y, b4.y, sl.y, ps.y - pos);
-                        e[c + 2] = score<FORM>(a, e[c + 2], k_scale * f4.z, b4.z, sl.z, ps.z - pos);
-                        e[c + 3] = score<FORM>(a, e[c + 3], k_scale * f4.w, b4.w, sl.w, ps.w - pos);
+                    };
+                    if (t < NT)
+                        sh.scale[w][(mine + 1) & 3][t] = kNoScale;
+                    const auto exponentials = [&](int c0, float *e) {
+                        TmemLoad<16>::go(s_at + c0, e);
+                        tmem_wait<16>(e);
+                        scores(c0, e, true);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            e[c] = exp2_fast(e[c]);
+                        if (edge) {
+                            const uint32_t bits = (uint32_t)(see >> c0);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                e[c] = (bits >> c) & 1 ? e[c] : 0.0f;
+                        }
                     };
                     while (true) {
                         if (closely) {
                             // bases from the rows' largest scores
-                            load_scores();
+#pragma unroll 1
+                            for (int c0 = 0; c0 < NT; c0 += 16) {
+                                float e[16];
+                                TmemLoad<16>::go(s_at + c0, e);
+                                tmem_wait<16>(e);
+                                scores(c0, e, false);
+                                int key[16], which;
+                                const uint32_t bits = (uint32_t)(see >> c0);
 #pragma unroll
-                            for (int c = 0; c < NT; c += 4)
-                                scores(c, false);
-#pragma unroll
-                            for (int c0 = 0; c0 < NT; c0 += kChunk) {
-                                int key[kChunk], which;
-#pragma unroll
-                                for (int c = 0; c < kChunk; ++c) {
-                                    const float y = e[c0 + c];
-                                    key[c] = ((see >> (c0 + c)) & 1) && y == y ? ordered(y) : INT_MIN;
-                                }
-                                const int most = warp_combine<kChunk>(key, lane, which, MaxInt());
-                                if ((lane & (32 / kChunk - 1)) == 0)
+                                for (int c = 0; c < 16; ++c)
+                                    key[c] = ((bits >> c) & 1) && e[c] == e[c] ? ordered(e[c]) : INT_MIN;
+                                const int most = warp_combine<16>(key, lane, which, MaxInt());
+                                if ((lane & 1) == 0)
                                     atomicMax(&sh.highest[w][c0 + which], most);
                             }
                             named_barrier<128>(bar);
@@ -1062,110 +1111,83 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                                 }
                             }
                             named_barrier<128>(bar);
-                            if (!fresh && (sh.moved[w][0] || (NT > 32 && sh.moved[w][1]))) {
-                                if (S::kSumsInTmem) {
+                            if (sh.moved[w][0] || (NT > 32 && sh.moved[w][1])) {
 #pragma unroll 1
-                                    for (int c0 = 0; c0 < NT; c0 += 16) {
-                                        float y[16];
-                                        TmemLoad<16>::go(l_at + c0, y);
-                                        tmem_wait<16>(y);
+                                for (int c0 = 0; c0 < NT; c0 += 16) {
+                                    float y[16];
+                                    TmemLoad<16>::go(l_at + c0, y);
+                                    tmem_wait<16>(y);
 #pragma unroll
-                                        for (int c = 0; c < 16; ++c)
-                                            y[c] *= sh.alpha[w][c0 + c];
-                                        tmem_store16(l_at + c0, y);
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int c = 0; c < LR; ++c)
-                                        l[c] *= sh.alpha[w][c];
+                                    for (int c = 0; c < 16; ++c)
+                                        y[c] *= sh.alpha[w][c0 + c];
+                                    tmem_store16(l_at + c0, y);
                                 }
+                                tmem_store_wait();
                             }
                         }
-                        load_scores();
+                        // exponentials, and what the tile's largest weight of each row has to be scaled by
+                        bool again = false;
+#pragma unroll 1
+                        for (int c0 = 0; c0 < NT; c0 += 16) {
+                            float e[16];
+                            exponentials(c0, e);
+                            if (S::kKeep)
+                                tmem_store16(e_at + c0, e);
+                            uint32_t half[8];
 #pragma unroll
-                        for (int c = 0; c < NT; c += 4) {
-                            scores(c, true);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                e[c + k] = exp2_fast(e[c + k]);
-                        }
-                        if (edge) {
-#pragma unroll
-                            for (int c = 0; c < NT; ++c)
-                                e[c] = (see >> c) & 1 ? e[c] : 0.0f;
-                        }
-                        // the tile's largest exponents; a score that passed its base by 2^64, or a block of values so small
-                        // that this would not show, sends the warpgroup round again
-                        bool again = v_scale < 0x1p-40f;
-#pragma unroll
-                        for (int c0 = 0; c0 < NT; c0 += kChunk) {
-                            uint32_t half[kChunk / 2];
-#pragma unroll
-                            for (int c = 0; c < kChunk; c += 2) {
-                                float y0 = e[c0 + c] * v_scale, y1 = e[c0 + c + 1] * v_scale;
-                                if (edge) {
-                                    y0 = e[c0 + c] == 0.0f ? 0.0f : y0;
-                                    y1 = e[c0 + c + 1] == 0.0f ? 0.0f : y1;
-                                }
-                                half[c / 2] = __byte_perm(__float_as_uint(y0), __float_as_uint(y1), 0x7632);
-                            }
+                            for (int c = 0; c < 8; ++c)
+                                half[c] = __byte_perm(__float_as_uint(e[2 * c]), __float_as_uint(e[2 * c + 1]), 0x7632);
                             int which;
-                            const uint32_t most = warp_combine<kChunk / 2>(half, lane, which, MaxHalves());
-                            constexpr int kSame = 64 / kChunk;  // lanes with the same two columns: 2 or 4
-                            const uint32_t ex = (((lane & 1 ? most >> 16 : most) & 0x7fffu) + 0x1fu) >> 7;
-                            if ((lane & (kSame - 1)) < 2)
-                                atomicMax(&sh.top[w][slot][c0 + 2 * which + (lane & 1)], ex);
-                            again = again || ex >= 127 + 64;
+                            const uint32_t two = warp_combine<8>(half, lane, which, MaxHalves());
+                            const uint32_t most = lane & 1 ? two & 0xffff0000u : two << 16;  // a float, cut to 16 bits
+                            again = again || most >= 191u << 23;
+                            // 2^k with 224 <= 2^k * largest weight <= 448 (448 = 1.75 * 2^8)
+                            const uint32_t top = (__float_as_uint(__uint_as_float(most) * v_most) + (0x1fu << 16)) >> 23;
+                            if ((lane & 3) < 2)
+                                atomicMin(&scales[c0 + 2 * which + (lane & 1)], (262u - max(top, 9u)) << 23);
                         }
-                        const bool once_more = barrier_or<128>(bar, again && !closely);
-                        if (!once_more)
+                        // a score that passed its base by 2^64 sends the warpgroup round again
+                        if (!barrier_or<128>(bar, again && !closely))
                             break;
                         if (t < NT)
-                            sh.top[w][slot][t] = 0;
+                            scales[t] = kNoScale;
                         closely = true;
                     }
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&sh.s_free[w]);
-                    const uint32_t *tops = sh.top[w][slot];
-                    if (t < NT)
-                        sh.power[g % kRing][t] = (int)max(tops[t], 9u) - 135 + (int)sh.base[w][t];
-                    if (S::kSumsInTmem) {
-#pragma unroll
-                        for (int c0 = 0; c0 < NT; c0 += 16) {
-                            float y[16];
-                            if (!fresh) {
-                                TmemLoad<16>::go(l_at + c0, y);
-                                tmem_wait<16>(y);
-                            }
-#pragma unroll
-                            for (int c = 0; c < 16; ++c)
-                                y[c] = (fresh ? 0.0f : y[c]) + e[c0 + c];
-                            tmem_store16(l_at + c0, y);
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < LR; ++c)
-                            l[c] += e[c];
+                    if (S::kKeep) {
+                        tmem_store_wait();
+                        tc_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&sh.s_free[w]);
                     }
+                    if (t < NT)
+                        sh.power[g % kRing][t] = 127 - (int)(scales[t] >> 23) + (int)sh.base[w][t];
                     mbar_wait(&sh.p_free[w], (mine & 1) ^ 1, dead);
-#pragma unroll
+#pragma unroll 1
                     for (int c0 = 0; c0 < NT; c0 += 16) {
+                        float e[16], l[16];
+                        TmemLoad<16>::go(l_at + c0, l);
+                        if (S::kKeep) {
+                            TmemLoad<16>::go(e_at + c0, e);
+                            tmem_wait<16>(e);
+                        } else {
+                            exponentials(c0, e);
+                        }
+                        tmem_wait<16>(l);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            l[c] += e[c];
+                        tmem_store16(l_at + c0, l);
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int c4 = 0; c4 < 4; ++c4) {
-                            const uint4 y = *(const uint4 *)(tops + c0 + c4 * 4);
-                            const uint32_t ex[4] = {y.x, y.y, y.z, y.w};
-                            float p[4];
+                            const float4 y = *(const float4 *)(scales + c0 + c4 * 4);
+                            float p[4] = {e[4 * c4] * (y.x * v_scale), e[4 * c4 + 1] * (y.y * v_scale),
+                                          e[4 * c4 + 2] * (y.z * v_scale), e[4 * c4 + 3] * (y.w * v_scale)};
+                            if (edge) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int c = c0 + c4 * 4 + k;
-                                // 2^(135 - exponent): the tile's largest weight of the row lands in [224, 448]
-                                const float scale = __uint_as_float((262u - max(ex[k], 9u)) << 23) * v_scale;
-                                p[k] = e[c] * scale;
-                                if (edge && e[c] == 0.0f)
-                                    p[k] = 0.0f;
+                                for (int k = 0; k < 4; ++k)
+                                    p[k] = e[4 * c4 + k] == 0.0f ? 0.0f : p[k];
                             }
                             uint32_t first[2], rest[2];
 #pragma unroll
@@ -1187,10 +1209,15 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                         *(uint4 *)dst = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *(uint4 *)(dst + kTile * NT) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
+                    tmem_store_wait();
                     proxy_fence();
+                    tc_before();
                     __syncwarp();
-                    if (lane == 0)
+                    if (lane == 0) {
+                        if (!S::kKeep)
+                            mbar_arrive(&sh.s_free[w]);
                         mbar_arrive(&sh.p_ready[g % kRing]);
+                    }
                     ++mine;
                     fresh = false;
                 }
@@ -1205,23 +1232,12 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             mbar_wait(&sh.sum_free[seg & 1], ((seg >> 1) & 1) ^ 1, dead);
             if (t < NT)
                 sh.last_base[seg & 1][w][t] = sh.base[w][t];
-#pragma unroll
+#pragma unroll 1
             for (int c0 = 0; c0 < NT; c0 += 16) {
                 float y[16];
                 int which;
-                if (S::kSumsInTmem) {
-                    if (!fresh) {
-                        TmemLoad<16>::go(l_at + c0, y);
-                        tmem_wait<16>(y);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        y[c] = fresh ? 0.0f : y[c];
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c)
-                        y[c] = l[(c0 + c) % LR];
-                }
+                TmemLoad<16>::go(l_at + c0, y);
+                tmem_wait<16>(y);
                 const float sum = warp_combine<16>(y, lane, which, Add());
                 if ((lane & 1) == 0)
                     sh.warp_total[seg & 1][w * 4 + (wid & 3)][c0 + which] = sum;
@@ -1229,73 +1245,95 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.sum_ready[seg & 1]);
-            ++seg;
             named_barrier<128>(bar);  // base has been read: the next segment may reset it
         }
     } else {
         // ---------------- adding up ----------------
-        const int o0 = D == 128 ? 0 : (wid >> 1) * OC, d = D == 128 ? tid : tid & 63;
+        const int o0 = D == 128 ? 0 : (wid >> 1) * OC, d = D == 128 ? tid : tid & 63, bar = 1 + NW;
         const uint32_t lanes = (uint32_t)wid << 21;
         constexpr int kPart = OC % 16 == 0 ? 16 : 8;
-        uint32_t g = 0, seg = 0, prepared = 0;
-        bool told = false;
-        float o[OC];
-        Walk<NT> ahead = walk;
-        // the queries of the next segment that has any work
-        const auto prepare = [&]() {
-            while (ahead.next()) {
-                const Unit &u = ahead.u;
-                if (u.count == 0)
-                    continue;
-                const bool tree = a.f.parent && (long long)(u.tile(ahead.x1 - 1) + 1) * kTile > u.first;
-                Columns<NT> &col = sh.col[prepared & 1];
-                load_queries<D, NT, 128>(a, u, ahead.b, ahead.h, ahead.rt, tree, sh.q[prepared & 1][0], col, tid);
-                if (tree) {
-                    named_barrier<128>(4 + NW);
-                    mark_kin<NT>(u, col, tid);
-                }
-                if (tid == 0) {
-                    Segment &g = sh.seg[prepared & 1];
-                    g.tiles = ahead.x1 - ahead.x0;
-                    g.x0 = ahead.x0;
-                    g.head_tiles = u.head_tiles;
-                    g.low = u.low;
-                    g.len = u.len;
-                    g.first = u.first;
-                    g.prefix = u.prefix;
-                    g.i1 = u.i1;
-                    g.rt = ahead.rt;
-                    g.seen_prefix = u.prefix / kTile;
-                    g.seen_end = (a.f.parent ? u.first : u.first + u.i0 + 1) / kTile;
-                    g.seen_low = a.f.window > 0 ? (int)((max((long long)u.first + u.i1 - a.f.window + 1, 0ll) + kTile - 1) / kTile)
-                                                : 0;
-                }
-                proxy_fence();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sh.q_ready[prepared & 1]);
-                ++prepared;
-                return;
-            }
-            if (!told) {  // that was the last one
-                if (tid == 0)
-                    sh.seg[prepared & 1].tiles = 0;
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sh.q_ready[prepared & 1]);
-                told = true;
-            }
+        const int rows = a.n * a.group;
+        const auto row_of = [&](int b, int h, int r) {
+            return ((size_t)b * a.n + r / a.group) * a.heads + h * a.group + r % a.group;
         };
-        prepare();
-        while (walk.next()) {
-            const bool none = walk.u.count == 0;
-            if (!none)
+        uint32_t prepared = 0;
+        Walk<NT> walk;
+        walk.start(a, range);
+        // describes the next segment that has tiles and brings in its queries; writes the rows that see nothing
+        const auto prepare = [&]() {
+            while (walk.at < walk.end && walk.u.count == 0) {
+                for (int c = 0; c < NT; ++c) {
+                    const int r = walk.rt * NT + c;
+                    if (r >= rows)
+                        break;
+                    const size_t row = row_of(walk.b, walk.h, r);
+                    if (tid < D)
+                        a.out[row * D + tid] = __float2bfloat16(0.0f);
+                    if (tid == 0)
+                        a.lse[row] = -INFINITY;
+                }
+                walk.next(a);
+            }
+            const uint32_t i = prepared & 1;
+            const Unit &u = walk.u;
+            const bool some = walk.at < walk.end;
+            if (tid == 0) {
+                Segment &g = sh.seg[i];
+                g.tiles = some ? walk.x1 - walk.x0 : 0;
+                g.x0 = walk.x0;
+                g.head_tiles = u.head_tiles;
+                g.low = u.low;
+                g.len = u.len;
+                g.first = u.first;
+                g.prefix = u.prefix;
+                g.i1 = u.i1;
+                g.b = walk.b;
+                g.h = walk.h;
+                g.rt = walk.rt;
+                g.seen_prefix = u.prefix / kTile;
+                g.seen_end = (a.f.parent ? u.first : u.first + u.i0 + 1) / kTile;
+                g.seen_low = a.f.window > 0
+                                 ? (int)((max((long long)u.first + u.i1 - a.f.window + 1, 0ll) + kTile - 1) / kTile)
+                                 : 0;
+                g.whole = walk.x0 == 0 && walk.x1 == u.count;
+                g.last = walk.x1 == u.count;
+                g.at = walk.at;
+                mbar_arrive(&sh.seg_ready[i]);
+            }
+            if (some) {
+                const bool tree = a.f.parent && (long long)(u.tile(walk.x1 - 1) + 1) * kTile > u.first;
+                load_queries<D, NT, 128>(a, u, walk.b, walk.h, walk.rt, tree, sh.q[i][0], sh.col[i], tid);
+                if (tree) {
+                    named_barrier<128>(bar);
+                    mark_kin<NT>(sh.col[i], tid);
+                }
+                walk.next(a);
+            }
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.q_ready[i]);
+            ++prepared;
+        };
+        uint32_t g = 0;
+        float o[OC];
+#pragma unroll 1
+        for (uint32_t seg = 0;; ++seg) {
+            if (seg == 0) {
                 prepare();
+                named_barrier<128>(bar);  // the segment's description
+            }
+            const Segment &u = sh.seg[seg & 1];
+            const int tiles = u.tiles;
+            if (tiles == 0)
+                break;
+            prepare();
 #pragma unroll
             for (int c = 0; c < OC; ++c)
                 o[c] = 0.0f;
             int ref = INT_MIN;  // of column tid: its sums count 2^ref
-            for (int x = walk.x0; x < walk.x1 && !none; ++x) {
+#pragma unroll 1
+            for (int x = 0; x < tiles; ++x) {
                 const uint32_t i = g & 1;
                 mbar_wait(&sh.p_ready[g % kRing], (g / kRing) & 1, dead);  // the tile's powers
                 bool moved = false;
@@ -1311,10 +1349,10 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     }
                     sh.factor[i][tid] = power2(max(power - ref, -200));
                 }
-                if (barrier_or<128>(4 + NW, moved)) {
+                if (barrier_or<128>(bar, moved)) {
                     if (tid < NT)
                         sh.inverse[tid] = alpha;
-                    named_barrier<128>(4 + NW);
+                    named_barrier<128>(bar);
 #pragma unroll
                     for (int c = 0; c < OC; ++c)
                         o[c] *= sh.inverse[o0 + c];
@@ -1342,16 +1380,15 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 ++g;
             }
             // whole units are finished here; parts go to the workspace for join_kernel
-            const bool whole = walk.whole();
-            const long long slot = 2ll * blockIdx.x + (walk.x0 == 0);
-            const int rows = a.n * a.group;
-            if (!none)
-                mbar_wait(&sh.sum_ready[seg & 1], (seg >> 1) & 1, dead);
-            named_barrier<128>(4 + NW);
+            const bool whole = u.whole;
+            const int b = u.b, h = u.h, rt = u.rt;
+            const long long slot = 2ll * blockIdx.x + (u.x0 == 0);
+            mbar_wait(&sh.sum_ready[seg & 1], (seg >> 1) & 1, dead);
+            named_barrier<128>(bar);
             if (tid < NT) {
-                const int r = walk.rt * NT + tid, i = r / a.group;
+                const int r = rt * NT + tid;
                 float total = 0.0f, base = 0.0f, part[NW];
-                if (!none && i <= walk.u.i1) {
+                if (r / a.group <= u.i1) {
                     bool any = false;
                     const float(*y)[NT] = sh.warp_total[seg & 1], (*last)[NT] = sh.last_base[seg & 1];
 #pragma unroll
@@ -1372,29 +1409,24 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 sh.inverse[tid] = whole ? (live ? level / total : 0.0f) : level;
                 if (whole) {
                     if (r < rows)
-                        a.lse[((size_t)walk.b * a.n + i) * a.heads + walk.h * a.group + r % a.group] =
-                            live ? (base + log2f(total)) * 0.6931471805599453f : -INFINITY;
+                        a.lse[row_of(b, h, r)] = live ? (base + log2f(total)) * 0.6931471805599453f : -INFINITY;
                 } else {
                     a.part_sum[slot * NT + tid] = make_float2(total, base);
                 }
             }
-            if (!whole && walk.x1 == max(walk.count, 1) && tid == 0)
-                a.joins[blockIdx.x] = make_int4((int)((walk.at - walk.x0) / range.each), walk.b, walk.h, walk.rt);
-            named_barrier<128>(4 + NW);
-            if (!none) {
-                if (lane == 0)
-                    mbar_arrive(&sh.sum_free[seg & 1]);
-                ++seg;
-            }
+            if (!whole && u.last && tid == 0)
+                a.joins[blockIdx.x] = make_int4((int)((u.at - u.x0) / range.each), b, h, rt);
+            named_barrier<128>(bar);
+            if (lane == 0)
+                mbar_arrive(&sh.sum_free[seg & 1]);
 #pragma unroll
             for (int c = 0; c < OC; ++c) {
-                const int r = walk.rt * NT + o0 + c;
+                const int r = rt * NT + o0 + c;
                 const float inv = sh.inverse[o0 + c], y = inv == 0.0f ? 0.0f : o[c] * inv;
                 if (!whole)
                     a.part[(slot * NT + o0 + c) * D + d] = y;
                 else if (r < rows)
-                    a.out[(((size_t)walk.b * a.n + r / a.group) * a.heads + walk.h * a.group + r % a.group) * D + d] =
-                        __float2bfloat16(y);
+                    a.out[row_of(b, h, r) * D + d] = __float2bfloat16(y);
             }
         }
     }
@@ -1405,6 +1437,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
     if (wid == kProducts)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kAlloc));
 }
+
 
 // ===========================================================================
 // Weights
@@ -1560,7 +1593,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                     mbar_arrive(&sh.q_ready);
                 named_barrier<256>(3);
                 if (tree) {
-                    mark_kin<NT>(u, sh.col, tid);
+                    mark_kin<NT>(sh.col, tid);
                     named_barrier<256>(3);
                 }
                 for (int x = x0; x < x1; ++x) {
