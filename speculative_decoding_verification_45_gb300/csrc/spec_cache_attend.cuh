@@ -119,6 +119,13 @@ __device__ __forceinline__ void drain_products(uint64_t *bar, volatile int *dead
         ;
 }
 
+__device__ __forceinline__ bool elected()  // one lane of a warp whose lanes are all here
+{
+    uint32_t r;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r;
+}
+
 template <int N> __device__ __forceinline__ void named_barrier(int id)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
@@ -451,38 +458,62 @@ template <int NT> __device__ __forceinline__ void mark_kin(Columns<NT> &col, int
     }
 }
 
-// Does column c's query see token j (cached)?
-template <int NT>
-__device__ __forceinline__ bool sees(const AttendArgs &a, const Unit &u, const Columns<NT> &col, int c, int j)
+// Scores in units of log2, less base, of 16 columns from c0 on; e: the accumulator
+// values of a token with this scale and position.  FORM: there may be a cap or a bias.
+template <bool FORM, int NT>
+__device__ __forceinline__ void scores(const AttendArgs &a, const Columns<NT> &col, const float *base, int c0, float k_scale,
+                                       float pos, float *e)
 {
-    const int i = col.query[c], t = j - u.first;
-    bool see = t <= i;
-    if (a.f.parent && t >= 0 && t < u.m)
-        see = (col.kin[c][t >> 5] >> (t & 31)) & 1;
-    if (a.f.window > 0)
-        see = see && (long long)t > (long long)i - a.f.window;
-    return (see || j < u.prefix) && i >= 0;
-}
-
-// The score of accumulator value s in units of log2, less `base`.  f: the token's
-// and the column's factor.  FORM: there may be a cap or a bias (slope, distance).
-template <bool FORM>
-__device__ __forceinline__ float score(const AttendArgs &a, float s, float f, float base, float slope, float distance)
-{
-    if (!FORM)
-        return fmaf(s, f, -base);
-    float x = s * f;
-    if (a.f.softcap > 0.0f) {
-        // tanh(y) = 1 - 2 / (1 + exp(2 y)) (the quotient is 0 from 2^126 on), which cancels near 0: there the first
-        // terms of its series, whose remainder is below 2^-24 of it up to 1/4
-        const float z = x * x;
-        const float series = x * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 62.0f / 2835, -17.0f / 315), 2.0f / 15), -1.0f / 3), 1.0f);
-        const float whole = 1.0f - __fdividef(2.0f, 1.0f + exp2_fast(x * (2.0f * kLog2e)));
-        x = (fabsf(x) < 0.25f ? series : whole) * (a.f.softcap * kLog2e);
+    const float4 *factor4 = (const float4 *)(col.factor + c0), *base4 = (const float4 *)(base + c0);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float4 f = factor4[c], b = base4[c];
+        if (FORM) {
+            e[4 * c] *= k_scale * f.x;
+            e[4 * c + 1] *= k_scale * f.y;
+            e[4 * c + 2] *= k_scale * f.z;
+            e[4 * c + 3] *= k_scale * f.w;
+        } else {
+            e[4 * c] = fmaf(e[4 * c], k_scale * f.x, -b.x);
+            e[4 * c + 1] = fmaf(e[4 * c + 1], k_scale * f.y, -b.y);
+            e[4 * c + 2] = fmaf(e[4 * c + 2], k_scale * f.z, -b.z);
+            e[4 * c + 3] = fmaf(e[4 * c + 3], k_scale * f.w, -b.w);
+        }
     }
-    if (a.f.slopes)
-        x = fmaf(-slope, fabsf(distance), x);
-    return x - base;
+    if (!FORM)
+        return;
+    if (a.f.softcap > 0.0f) {
+        const float cap = a.f.softcap * kLog2e;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+            // tanh(y) = 1 - 2 / (1 + exp(2 y)) (the quotient is 0 from 2^126 on), which cancels near 0: there the first
+            // terms of its series, whose remainder is below 2^-24 of it up to 1/4
+            const float y = e[c], z = y * y;
+            const float series = y * fmaf(z, fmaf(z, fmaf(z, fmaf(z, 62.0f / 2835, -17.0f / 315), 2.0f / 15), -1.0f / 3), 1.0f);
+            const float whole = 1.0f - __fdividef(2.0f, 1.0f + exp2_fast(y * (2.0f * kLog2e)));
+            e[c] = (fabsf(y) < 0.25f ? series : whole) * cap;
+        }
+    }
+    if (a.f.slopes) {
+        const float4 *slope4 = (const float4 *)(col.slope + c0), *from4 = (const float4 *)(col.pos + c0);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float4 sl = slope4[c], from = from4[c], b = base4[c];
+            e[4 * c] = fmaf(-sl.x, fabsf(from.x - pos), e[4 * c]) - b.x;
+            e[4 * c + 1] = fmaf(-sl.y, fabsf(from.y - pos), e[4 * c + 1]) - b.y;
+            e[4 * c + 2] = fmaf(-sl.z, fabsf(from.z - pos), e[4 * c + 2]) - b.z;
+            e[4 * c + 3] = fmaf(-sl.w, fabsf(from.w - pos), e[4 * c + 3]) - b.w;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float4 b = base4[c];
+            e[4 * c] -= b.x;
+            e[4 * c + 1] -= b.y;
+            e[4 * c + 2] -= b.z;
+            e[4 * c + 3] -= b.w;
+        }
+    }
 }
 
 struct StageInfo {
@@ -617,7 +648,13 @@ struct Segment {
     int seen_prefix, seen_low, seen_end;  // tiles that every query of the row tile sees whole: [0, ..) and [low, end)
     int whole, last;                      // the whole unit; its last part
     long long at;                         // first tile's place in the order of all
-    __device__ __forceinline__ int tile(int k) const { return x0 + k < head_tiles ? x0 + k : x0 + k - head_tiles + low; }
+    // k-th tile to be worked on: from the newest tokens back, since scores with a bias by distance fall that way and
+    // bases set first then stay
+    __device__ __forceinline__ int tile(int k) const
+    {
+        const int x = x0 + tiles - 1 - k;
+        return x < head_tiles ? x : x - head_tiles + low;
+    }
 };
 
 template <int D, int NT> struct AttendShared {
@@ -632,7 +669,7 @@ template <int D, int NT> struct AttendShared {
     alignas(16) float base[S::NW][NT];
     alignas(16) uint32_t scale[S::NW][4][NT];  // per tile: 2^k, as bits, that brings the largest weight to [224, 448]
     alignas(16) int power[S::kRing][NT];       // per tile: O^T counts 2^power
-    alignas(16) float factor[2][NT], inverse[NT];
+    alignas(16) float factor[2][NT], inverse[NT], none[NT];  // none: bases of 0
     alignas(16) float warp_total[2][S::NW * 4][NT], last_base[2][S::NW][NT];
     alignas(16) float alpha[S::NW][NT];        // what a moved base leaves of the totals
     int highest[S::NW][NT];                    // ordered bits of the largest score
@@ -733,7 +770,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
     constexpr uint32_t kO = NW * NT, kL = kO + 2 * NT;  // S^T at 0, then O^T, then the totals
     extern __shared__ uint8_t raw[];
     Shared &sh = *(Shared *)(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
     volatile int *dead = &sh.dead;
 
     if (tid == 0) {
@@ -769,6 +806,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         ((uint32_t *)sh.scale)[i] = kNoScale;
     for (int i = tid; i < NW * NT; i += S::kThreads)
         ((int *)sh.highest)[i] = INT_MIN;
+    for (int i = tid; i < NT; i += S::kThreads)
+        sh.none[i] = 0.0f;
     if (wid == kProducts) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
                      "r"(S::kAlloc)
@@ -873,7 +912,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             mbar_wait(&sh.v_full[vs], v_phase, dead);
             mbar_wait(&sh.o_free[i], ((done >> 1) & 1) ^ 1, dead);
             tc_after();
-            if (lane == 0) {
+            if (elected()) {
                 const uint64_t vd = v_desc + (uint32_t)vs * (S::kBytes >> 4), pd = p_desc + (uint32_t)pw * (2 * kTile * NT >> 4);
                 const uint32_t d = tmem + kO + i * NT;
 #pragma unroll
@@ -920,7 +959,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 mbar_wait(&sh.k_full[ks], k_phase, dead);
                 mbar_wait(&sh.s_free[w], s_phase, dead);
                 tc_after();
-                if (lane == 0) {
+                if (elected()) {
                     const uint64_t kd = k_desc + (uint32_t)ks * (S::kBytes >> 4);
 #pragma unroll
                     for (int d = 0; d < D / 32; ++d) {
@@ -983,12 +1022,10 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     const float pos = FORM && a.f.slopes ? (a.c.positions ? (float)info.pos[t] : (float)j) : 0.0f;
                     const bool edge = came != (1u << blocks) - 1 ||
                                       !(tile < u.seen_prefix || (tile >= u.seen_low && tile < u.seen_end));
-                    bool closely = fresh;
+                    bool closely = fresh || sh.unset[w][0] || (NT > 32 && sh.unset[w][1]);
                     uint64_t see = ~0ull;
                     float v_most = v_scale;
                     if (edge) {
-                        if (!fresh)
-                            closely = sh.unset[w][0] || (NT > 32 && sh.unset[w][1]);
                         const bool cached = j < u.len && ((came >> (t >> log_p)) & 1);
                         see = cached ? seen_by<NT>(a, u, col, j) : 0;
                         const bool all =
@@ -1029,32 +1066,12 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     mbar_wait(&sh.s_full[w], mine & 1, dead);
                     tc_after();
 
-                    // scores of columns c0 .. c0 + 15, less base
-                    const auto scores = [&](int c0, float *e, bool based) {
-                        const float4 *factor = (const float4 *)(col.factor + c0), *base = (const float4 *)(sh.base[w] + c0),
-                                     *slope = (const float4 *)(col.slope + c0), *from = (const float4 *)(col.pos + c0);
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const float4 f = factor[c];
-                            float4 b4 = make_float4(0, 0, 0, 0), sl = b4, ps = b4;
-                            if (based)
-                                b4 = base[c];
-                            if (FORM && a.f.slopes) {
-                                sl = slope[c];
-                                ps = from[c];
-                            }
-                            e[4 * c] = score<FORM>(a, e[4 * c], k_scale * f.x, b4.x, sl.x, ps.x - pos);
-                            e[4 * c + 1] = score<FORM>(a, e[4 * c + 1], k_scale * f.y, b4.y, sl.y, ps.y - pos);
-                            e[4 * c + 2] = score<FORM>(a, e[4 * c + 2], k_scale * f.z, b4.z, sl.z, ps.z - pos);
-                            e[4 * c + 3] = score<FORM>(a, e[4 * c + 3], k_scale * f.w, b4.w, sl.w, ps.w - pos);
-                        }
-                    };
                     if (t < NT)
                         sh.scale[w][(mine + 1) & 3][t] = kNoScale;
                     const auto exponentials = [&](int c0, float *e) {
                         TmemLoad<16>::go(s_at + c0, e);
                         tmem_wait<16>(e);
-                        scores(c0, e, true);
+                        scores<FORM>(a, col, sh.base[w], c0, k_scale, pos, e);
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
                             e[c] = exp2_fast(e[c]);
@@ -1073,7 +1090,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                                 float e[16];
                                 TmemLoad<16>::go(s_at + c0, e);
                                 tmem_wait<16>(e);
-                                scores(c0, e, false);
+                                scores<FORM>(a, col, sh.none, c0, k_scale, pos, e);
                                 int key[16], which;
                                 const uint32_t bits = (uint32_t)(see >> c0);
 #pragma unroll
@@ -1473,7 +1490,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     constexpr int ST = Shared::kStages;
     extern __shared__ uint8_t raw[];
     Shared &sh = *(Shared *)(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
     volatile int *dead = &sh.dead;
     if (tid == 0) {
         sh.dead = 0;
@@ -1555,7 +1572,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                     mbar_wait(&sh.full[st], phase, dead);
                     mbar_wait(&sh.s_free[g & 1], ((g >> 1) & 1) ^ 1, dead);
                     tc_after();
-                    if (lane == 0) {
+                    if (elected()) {
                         const uint32_t k = smem_u32(sh.tiles[st]), q = smem_u32(sh.q[0]);
 #pragma unroll
                         for (int d = 0; d < D / 32; ++d) {
@@ -1578,6 +1595,11 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
             } else {
                 // ---------------- sums ----------------
                 const int w = wid >> 2, t = tid & 127;
+                Segment rows_of;
+                rows_of.first = u.first;
+                rows_of.prefix = u.prefix;
+                rows_of.i1 = u.i1;
+                rows_of.rt = rt;
                 named_barrier<256>(3);
                 const bool tree = a.f.parent && (long long)(all.tile(x1 - 1) + 1) * kTile > u.first;
                 load_queries<D, NT, 256>(a, u, b, h, rt, tree, sh.q[0], sh.col, tid);
@@ -1609,31 +1631,22 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                         const bool cached = !edge || (j < u.len && ((came >> (t >> log_p)) & 1));
                         const float ks = cached ? info.k_scale[t >> log_p] : 0.0f;
                         const float pos = FORM && a.f.slopes ? (a.c.positions ? (float)info.pos[t] : (float)j) : 0.0f;
+                        const uint64_t see = edge && cached ? seen_by<NT>(a, rows_of, sh.col, j) : 0;
                         float *weight = a.weights + ((size_t)(cached ? page : 0) * a.c.kv_heads + h) * P + (t & (P - 1));
                         const float before = cached ? *weight : 0.0f;
                         mbar_wait(&sh.s_full[g & 1], (g >> 1) & 1, dead);
                         tc_after();
                         float sum = 0.0f;
-                        constexpr int kPart = NT % 32 == 0 ? 32 : 16;
 #pragma unroll 1
-                        for (int c1 = 0; c1 < NT; c1 += kPart) {
-                            float s[kPart];
-                            TmemLoad<kPart>::go(tmem + ((uint32_t)(wid & 3) << 21) + (g & 1) * NT + c1, s);
-                            tmem_wait<kPart>(s);
+                        for (int c0 = 0; c0 < NT; c0 += 16) {
+                            float e[16];
+                            TmemLoad<16>::go(tmem + ((uint32_t)(wid & 3) << 21) + (g & 1) * NT + c0, e);
+                            tmem_wait<16>(e);
+                            scores<FORM>(a, sh.col, sh.col.base, c0, ks, pos, e);
+                            const uint32_t bits = (uint32_t)(see >> c0);
 #pragma unroll
-                            for (int c4 = 0; c4 < kPart / 4; ++c4) {
-                                const float4 f4 = ((const float4 *)(sh.col.factor + c1))[c4],
-                                             b4 = ((const float4 *)(sh.col.base + c1))[c4];
-                                const float f[4] = {f4.x, f4.y, f4.z, f4.w}, bs[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const int c = c1 + c4 * 4 + k;
-                                    const float e = exp2_fast(score<FORM>(a, s[c4 * 4 + k], ks * f[k], bs[k],
-                                                                          FORM && a.f.slopes ? sh.col.slope[c] : 0.0f,
-                                                                          FORM && a.f.slopes ? sh.col.pos[c] - pos : 0.0f));
-                                    sum += !edge || (cached && sees<NT>(a, u, sh.col, c, j)) ? e : 0.0f;
-                                }
-                            }
+                            for (int c = 0; c < 16; ++c)
+                                sum += !edge || ((bits >> c) & 1) ? exp2_fast(e[c]) : 0.0f;
                         }
                         tc_before();
                         __syncwarp();
