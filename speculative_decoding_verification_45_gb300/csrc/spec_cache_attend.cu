@@ -21,7 +21,7 @@ spec_status check_call(const spec_cache *cache, const int32_t *lengths, const vo
         !(form->softcap >= 0.0f) || !(form->scale - form->scale == 0.0f) || !(form->softcap - form->softcap == 0.0f) ||
         (form->parent && n > SPEC_MAX_TREE_NODES))
         return SPEC_ERR_INVALID_ARG;
-    if ((long long)n * heads > INT_MAX / 2)
+    if ((long long)n * heads > INT_MAX / 2 || heads / cache->kv_heads > 4096)
         return SPEC_ERR_UNSUPPORTED;
     if (cache->batch == 0 || n == 0)
         return SPEC_OK;
@@ -129,6 +129,7 @@ AttendArgs make_args(const spec_cache *cache, const int32_t *lengths, const void
     a.n = n;
     a.heads = heads;
     a.group = heads / cache->kv_heads;
+    a.per_group = a.group == 1 ? 0 : (uint32_t)(((1ull << 32) + a.group - 1) / a.group);
     a.row_tiles = shape.row_tiles;
     a.status = status;
     return a;

@@ -38,6 +38,7 @@ struct AttendArgs {
     const __nv_bfloat16 *q;
     int64_t q_stride[3];
     int n, heads, group;   // group: query heads per key/value head
+    uint32_t per_group;    // ceil(2^32 / group), 0 for a group of 1
     int row_tiles;         // ceil(n * group / NT)
     __nv_bfloat16 *out;
     float *lse;
@@ -281,6 +282,19 @@ template <int NT> __device__ __forceinline__ Unit row_unit(const AttendArgs &a, 
     return unit_for(a, b, rt * NT / a.group, (rt * NT + NT - 1) / a.group);
 }
 
+// Row c of row tile rt: its query and, among its key head's, its query head.  Quotients of less than
+// group + 64 come exact from the high half of a product.
+struct RowAt {
+    int i0, g0;
+    __device__ __forceinline__ RowAt(const AttendArgs &a, int first) : i0(first / a.group), g0(first % a.group) {}
+    __device__ __forceinline__ void of(const AttendArgs &a, int c, int &i, int &g) const
+    {
+        const uint32_t k = (uint32_t)(g0 + c), whole = a.per_group ? __umulhi(k, a.per_group) : k;
+        i = i0 + (int)whole;
+        g = (int)(k - whole * (uint32_t)a.group);
+    }
+};
+
 // Every token of the tile at j0 is seen by every query of the unit.
 __device__ __forceinline__ bool interior(const AttendArgs &a, const Unit &u, int j0)
 {
@@ -378,17 +392,26 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const Unit &u,
                 report(a.status, SPEC_STATUS_BAD_TREE);
             col.up[k] = (unsigned)up < (unsigned)k ? up : -1;
         }
-#pragma unroll
+    const RowAt at(a, rt * NT);
+    const auto fetch = [&](int c) {
+        int i, g;
+        at.of(a, c, i, g);
+        return c < NT && i <= u.i1 ? __ldg((const uint4 *)(a.q + (size_t)b * a.q_stride[0] + (size_t)i * a.q_stride[1] +
+                                                           (size_t)(h * a.group + g) * a.q_stride[2] + d * 8))
+                                   : make_uint4(0, 0, 0, 0);
+    };
+    uint4 next = fetch(t / kLanes);
+#pragma unroll 1
     for (int r0 = 0; r0 < NT; r0 += kRows) {
         const int c = r0 + t / kLanes;
         if (NT % kRows && c >= NT)
-            continue;  // whole warps: a warp holds 2 or 4 rows
-        const int r = rt * NT + c, i = r / a.group, H = h * a.group + r % a.group;
+            break;  // whole warps: a warp holds 2 or 4 rows
+        int i, g;
+        at.of(a, c, i, g);
+        const int H = h * a.group + g;
         const bool live = i <= u.i1;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (live)
-            w = __ldg((const uint4 *)(a.q + (size_t)b * a.q_stride[0] + (size_t)i * a.q_stride[1] +
-                                      (size_t)H * a.q_stride[2] + d * 8));
+        const uint4 w = next;
+        next = fetch(c + kRows);
         float x[8];
         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
         float amax = 0.0f;
@@ -425,9 +448,9 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const Unit &u,
             hi[e] = code[0] | code[1] << 16;
             lo[e] = rest[0] | rest[1] << 16;
         }
-        const int at = c * D + ((d * 8) ^ (D == 128 ? (c & 7) << 4 : ((c >> 1) & 3) << 4));
-        *(uint2 *)(q + at) = make_uint2(hi[0], hi[1]);
-        *(uint2 *)(q + NT * D + at) = make_uint2(lo[0], lo[1]);
+        const int to = c * D + ((d * 8) ^ (D == 128 ? (c & 7) << 4 : ((c >> 1) & 3) << 4));
+        *(uint2 *)(q + to) = make_uint2(hi[0], hi[1]);
+        *(uint2 *)(q + NT * D + to) = make_uint2(lo[0], lo[1]);
         if (d == 0) {
             const float row = __uint_as_float((uint32_t)ex << 23) * a.f.scale;
             col.factor[c] = a.f.softcap > 0.0f ? row / a.f.softcap : row * kLog2e;
@@ -448,13 +471,13 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const Unit &u,
 }
 
 // The ancestors of each column's query, after a barrier behind load_queries.
-template <int NT> __device__ __forceinline__ void mark_kin(Columns<NT> &col, int t)
+template <int NT, int THREADS> __device__ __forceinline__ void mark_kin(Columns<NT> &col, int t)
 {
-    if (t < NT) {
+    for (int c = t; c < NT; c += THREADS) {
         for (int w = 0; w < kMaxNodes / 32; ++w)
-            col.kin[t][w] = 0;
-        for (int k = col.query[t]; k >= 0; k = col.up[k])
-            col.kin[t][k >> 5] |= 1u << (k & 31);
+            col.kin[c][w] = 0;
+        for (int k = col.query[c]; k >= 0; k = col.up[k])
+            col.kin[c][k >> 5] |= 1u << (k & 31);
     }
 }
 
@@ -604,11 +627,11 @@ template <int NT> struct Walk {
 // Attention
 // ===========================================================================
 // One persistent CTA per SM, each warp with one job:
+//   queries      walks the CTA's segments, one ahead: describes them, splits their queries
 //   producer     block table, TMA of the blocks, their scales
-//   products     issues the matrix products and owns the tensor memory
+//   scores, values   issue one of the two matrix products each
 //   softmax      NW warpgroups, tiles in turn; a thread owns one token and all columns
-//   adding       one warpgroup: adds the tiles' O^T up in registers, writes the
-//                results, and brings in the next segment's queries
+//   adding       one warpgroup: adds the tiles' O^T up in registers, writes the results
 // Tile g: S^T(g) in tensor memory; warpgroup g % NW turns it into P^T in shared
 // memory; O^T(g) = V^T P^T.  A tile's softmax is a chain of short dependent
 // steps (about 3000 cycles when one pair of warpgroups shared each tile, of
@@ -631,11 +654,12 @@ template <int NT> struct Walk {
 // totals live in tensor memory between the passes.
 template <int D, int NT> struct AttendShape {
     static constexpr int NW = NT <= 32 ? 4 : NT == 48 ? 3 : 2;  // softmax warpgroups
-    static constexpr int kThreads = 128 * (1 + NW) + 64;
+    static constexpr int kThreads = 128 * (2 + NW);
+    static constexpr int NO = NT == 48 ? 1 : 2;                 // O^T at a time (one: room to keep the exponentials)
     static constexpr int kBytes = kTile * D;                    // one side of a tile
     static constexpr int KS = 3, VS = D == 64 || NT == 16 ? 8 : NT >= 48 ? 5 : 6;  // tiles of keys and values in shared memory
-    static constexpr bool kKeep = (3 * NW + 2) * NT <= 512;     // room for the exponentials between the passes
-    static constexpr int kColumns = ((kKeep ? 3 : 2) * NW + 2) * NT;  // S^T, totals (and these) of each warpgroup, two O^T
+    static constexpr bool kKeep = (3 * NW + NO) * NT <= 512;     // room for the exponentials between the passes
+    static constexpr int kColumns = ((kKeep ? 3 : 2) * NW + NO) * NT;  // S^T, totals (and these) of each warpgroup, O^T
     static constexpr int kAlloc = kColumns <= 256 ? 256 : 512;
     static constexpr int kRing = 8;                             // >= NW + 2 tiles between a writer and the adding warps
 };
@@ -648,6 +672,7 @@ struct Segment {
     int seen_prefix, seen_low, seen_end;  // tiles that every query of the row tile sees whole: [0, ..) and [low, end)
     int whole, last;                      // the whole unit; its last part
     long long at;                         // first tile's place in the order of all
+    long long rows[64];                   // of the outputs, by column; -1: none
     // k-th tile to be worked on: from the newest tokens back, since scores with a bias by distance fall that way and
     // bases set first then stay
     __device__ __forceinline__ int tile(int k) const
@@ -677,7 +702,7 @@ template <int D, int NT> struct AttendShared {
     int moved[S::NW][2], unset[S::NW][2];      // by 32 columns
     alignas(8) uint64_t k_full[S::KS], k_empty[S::KS], v_full[S::VS], v_empty[S::VS];
     uint64_t s_full[S::NW], s_free[S::NW], p_ready[S::kRing], p_free[S::NW], o_full[2], o_free[2], seg_ready[2], q_ready[2];
-    uint64_t sum_ready[2], sum_free[2], drained;
+    uint64_t sum_ready[2], sum_free[2], drained[2];
     uint32_t tmem;
     int dead;
 };
@@ -765,9 +790,9 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
     using S = AttendShape<D, NT>;
     using Shared = AttendShared<D, NT>;
     constexpr int NW = S::NW, KS = S::KS, VS = S::VS, kRing = S::kRing;
-    constexpr int kProducer = 4 * (1 + NW), kProducts = kProducer + 1;
+    constexpr int kQueries = 4 * (1 + NW), kProducer = kQueries + 1, kScores = kQueries + 2, kValues = kQueries + 3, NO = S::NO;
     constexpr int OC = D == 128 ? NT : NT / 2;  // columns of an adding thread
-    constexpr uint32_t kO = NW * NT, kL = kO + 2 * NT;  // S^T at 0, then O^T, then the totals
+    constexpr uint32_t kO = NW * NT, kL = kO + NO * NT;  // S^T at 0, then O^T, then the totals
     extern __shared__ uint8_t raw[];
     Shared &sh = *(Shared *)(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
     const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -794,11 +819,12 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             mbar_init(&sh.o_full[i], 1);
             mbar_init(&sh.o_free[i], 4);
             mbar_init(&sh.seg_ready[i], 1);
-            mbar_init(&sh.q_ready[i], 4);
+            mbar_init(&sh.q_ready[i], 1);
             mbar_init(&sh.sum_ready[i], 4 * NW);
             mbar_init(&sh.sum_free[i], 4);
         }
-        mbar_init(&sh.drained, 1);
+        mbar_init(&sh.drained[0], 1);
+        mbar_init(&sh.drained[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
@@ -808,7 +834,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         ((int *)sh.highest)[i] = INT_MIN;
     for (int i = tid; i < NT; i += S::kThreads)
         sh.none[i] = 0.0f;
-    if (wid == kProducts) {
+    if (wid == kValues) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
                      "r"(S::kAlloc)
                      : "memory");
@@ -828,7 +854,82 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
     const uint32_t tmem = sh.tmem;
     const int P = a.c.block, blocks = kTile / P, log_p = 31 - __clz(P);
 
-    if (wid == kProducer) {
+    if (wid == kQueries) {
+        // ---------------- queries ----------------
+        Walk<NT> walk;
+        walk.start(a, range);
+#pragma unroll 1
+        for (uint32_t seg = 0;; ++seg) {
+            const uint32_t i = seg & 1;
+            mbar_wait(&sh.sum_free[i], ((seg >> 1) & 1) ^ 1, dead);  // the segment before the last is complete
+            const int rows = a.n * a.group;
+            const auto row_of = [&](const RowAt &at, int c) {
+                int q, g;
+                at.of(a, c, q, g);
+                return walk.rt * NT + c < rows ? ((long long)walk.b * a.n + q) * a.heads + walk.h * a.group + g : -1ll;
+            };
+            while (walk.at < walk.end && walk.u.count == 0) {  // rows that see nothing
+                const RowAt at(a, walk.rt * NT);
+                for (int c = 0; c < NT; ++c) {
+                    const long long row = row_of(at, c);
+                    if (row < 0)
+                        break;
+                    for (int d = lane; d < D / 8; d += 32)
+                        ((uint4 *)(a.out + row * D))[d] = make_uint4(0, 0, 0, 0);
+                    if (lane == 0)
+                        a.lse[row] = -INFINITY;
+                }
+                walk.next(a);
+            }
+            const Unit &u = walk.u;
+            const bool some = walk.at < walk.end && !__any_sync(0xffffffffu, *dead);
+            Segment &g = sh.seg[i];
+            if (some) {
+                const RowAt at(a, walk.rt * NT);
+                for (int c = lane; c < NT; c += 32)
+                    g.rows[c] = row_of(at, c);
+            }
+            if (lane == 0) {
+                g.tiles = some ? walk.x1 - walk.x0 : 0;
+                g.x0 = walk.x0;
+                g.head_tiles = u.head_tiles;
+                g.low = u.low;
+                g.len = u.len;
+                g.first = u.first;
+                g.prefix = u.prefix;
+                g.i1 = u.i1;
+                g.b = walk.b;
+                g.h = walk.h;
+                g.rt = walk.rt;
+                g.seen_prefix = u.prefix / kTile;
+                g.seen_end = (a.f.parent ? u.first : u.first + u.i0 + 1) / kTile;
+                g.seen_low = a.f.window > 0
+                                 ? (int)((max((long long)u.first + u.i1 - a.f.window + 1, 0ll) + kTile - 1) / kTile)
+                                 : 0;
+                g.whole = walk.x0 == 0 && walk.x1 == u.count;
+                g.last = walk.x1 == u.count;
+                g.at = walk.at;
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.seg_ready[i]);
+            if (some) {
+                const bool tree = a.f.parent && (long long)(u.tile(walk.x1 - 1) + 1) * kTile > u.first;
+                load_queries<D, NT, 32>(a, u, walk.b, walk.h, walk.rt, tree, sh.q[i][0], sh.col[i], lane);
+                if (tree) {
+                    __syncwarp();
+                    mark_kin<NT, 32>(sh.col[i], lane);
+                }
+            }
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.q_ready[i]);
+            if (!some)
+                break;
+            walk.next(a);
+        }
+    } else if (wid == kProducer) {
         // ---------------- producer ----------------
         if (lane < 2)
             asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &vmap : &kmap));
@@ -895,67 +996,24 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         }
         drain<KS>(sh.k_full, issued, dead, a.status);
         drain<VS>(sh.v_full, issued, dead, a.status);
-    } else if (wid == kProducts) {
-        // ---------------- products ----------------
-        const uint32_t s_desc = instr_desc(NT, a.c.code, false, false), o_desc = instr_desc(NT, a.c.code, true, true);
+    } else if (wid == kScores) {
+        // ---------------- S^T = K Q^T ----------------
+        const uint32_t desc = instr_desc(NT, a.c.code, false, false);
         constexpr uint64_t swizzle = D == 128 ? 2 : 4;
         // descriptors of the first buffers; others lie a whole number of 16 bytes further
         const uint64_t k_desc = smem_desc(smem_u32(sh.k[0]), 16, 8 * D, swizzle),
-                       q_desc = smem_desc(smem_u32(sh.q[0][0]), 16, 8 * D, swizzle),
-                       v_desc = smem_desc(smem_u32(sh.v[0]), 0, 8 * D, swizzle),
-                       p_desc = smem_desc(smem_u32(sh.p[0][0]), 128, kTile * 16, 0);
-        int ks = 0, vs = 0, w = 0, pw = 0;  // pw: warpgroup of the next tile to be multiplied with values
-        uint32_t k_phase = 0, v_phase = 0, s_phase = 1, g = 0, done = 0, begun = 0;
-        const auto values = [&]() {  // O^T of tile `done`
-            const uint32_t i = done & 1;
-            mbar_wait(&sh.p_ready[done % kRing], (done / kRing) & 1, dead);
-            mbar_wait(&sh.v_full[vs], v_phase, dead);
-            mbar_wait(&sh.o_free[i], ((done >> 1) & 1) ^ 1, dead);
-            tc_after();
-            if (elected()) {
-                const uint64_t vd = v_desc + (uint32_t)vs * (S::kBytes >> 4), pd = p_desc + (uint32_t)pw * (2 * kTile * NT >> 4);
-                const uint32_t d = tmem + kO + i * NT;
-#pragma unroll
-                for (int k = 0; k < kTile / 32; ++k) {
-                    tc_mma(d, vd + (k * 32 * D >> 4), pd + (k * 512 >> 4), o_desc, k > 0);
-                    tc_mma(d, vd + (k * 32 * D >> 4), pd + ((kTile * NT + k * 512) >> 4), o_desc, true);
-                }
-                tc_commit(&sh.o_full[i]);
-                tc_commit(&sh.p_free[pw]);
-                tc_commit(&sh.v_empty[vs]);
-            }
-            __syncwarp();
-            ++done;
-            pw = pw + 1 == NW ? 0 : pw + 1;
-            if (++vs == VS) {
-                vs = 0;
-                v_phase ^= 1;
-            }
-        };
-        int tiles = 0, x = 0;
-        uint32_t seg = 0;
-        uint64_t qd = q_desc;
-        bool more = true;
-        // one turn: the scores of the next tile, if there is one, and the values of the tile NW before it
+                       q_desc = smem_desc(smem_u32(sh.q[0][0]), 16, 8 * D, swizzle);
+        int ks = 0, w = 0;
+        uint32_t k_phase = 0, s_phase = 1;
 #pragma unroll 1
-        while (more || done < g) {
-            bool issue = more;
-            if (more && x == tiles) {
-                // the next queries come once the segment before the last is complete: its products must not wait for them
-                if (done < begun) {
-                    issue = false;
-                } else {
-                    begun = g;
-                    mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, dead);
-                    tiles = *dead ? 0 : sh.seg[seg & 1].tiles;
-                    tiles = __shfl_sync(0xffffffffu, tiles, 0);
-                    qd = q_desc + (seg & 1) * (2 * NT * D >> 4);
-                    ++seg;
-                    x = 0;
-                    more = issue = tiles > 0;
-                }
-            }
-            if (issue) {
+        for (uint32_t seg = 0; !__any_sync(0xffffffffu, *dead); ++seg) {
+            mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, dead);
+            const int tiles = __shfl_sync(0xffffffffu, sh.seg[seg & 1].tiles, 0);
+            if (tiles == 0)
+                break;
+            const uint64_t qd = q_desc + (seg & 1) * (2 * NT * D >> 4);
+#pragma unroll 1
+            for (int x = 0; x < tiles; ++x) {
                 mbar_wait(&sh.k_full[ks], k_phase, dead);
                 mbar_wait(&sh.s_free[w], s_phase, dead);
                 tc_after();
@@ -963,29 +1021,61 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     const uint64_t kd = k_desc + (uint32_t)ks * (S::kBytes >> 4);
 #pragma unroll
                     for (int d = 0; d < D / 32; ++d) {
-                        tc_mma(tmem + w * NT, kd + (d * 32 >> 4), qd + (d * 32 >> 4), s_desc, d > 0);
-                        tc_mma(tmem + w * NT, kd + (d * 32 >> 4), qd + ((NT * D + d * 32) >> 4), s_desc, true);
+                        tc_mma(tmem + w * NT, kd + (d * 32 >> 4), qd + (d * 32 >> 4), desc, d > 0);
+                        tc_mma(tmem + w * NT, kd + (d * 32 >> 4), qd + ((NT * D + d * 32) >> 4), desc, true);
                     }
                     tc_commit(&sh.s_full[w]);
                     tc_commit(&sh.k_empty[ks]);
                 }
                 __syncwarp();
-                if (++w == NW) {
-                    w = 0;
-                    s_phase ^= 1;
-                }
-                if (++ks == KS) {
-                    ks = 0;
-                    k_phase ^= 1;
-                }
-                ++g;
-                ++x;
+                w = w + 1 == NW ? 0 : w + 1;
+                s_phase ^= w == 0;
+                ks = ks + 1 == KS ? 0 : ks + 1;
+                k_phase ^= ks == 0;
             }
-            if (!issue || g - done > NW)
-                if (done < g)
-                    values();
         }
-        drain_products(&sh.drained, dead);
+        drain_products(&sh.drained[0], dead);
+    } else if (wid == kValues) {
+        // ---------------- O^T = V^T P^T ----------------
+        const uint32_t desc = instr_desc(NT, a.c.code, true, true);
+        const uint64_t v_desc = smem_desc(smem_u32(sh.v[0]), 0, 8 * D, D == 128 ? 2 : 4),
+                       p_desc = smem_desc(smem_u32(sh.p[0][0]), 128, kTile * 16, 0);
+        int vs = 0, w = 0;
+        uint32_t v_phase = 0, g = 0;
+#pragma unroll 1
+        for (uint32_t seg = 0; !__any_sync(0xffffffffu, *dead); ++seg) {
+            mbar_wait(&sh.seg_ready[seg & 1], (seg >> 1) & 1, dead);
+            const int tiles = __shfl_sync(0xffffffffu, sh.seg[seg & 1].tiles, 0);
+            if (tiles == 0)
+                break;
+#pragma unroll 1
+            for (int x = 0; x < tiles; ++x) {
+                const uint32_t i = g % NO;
+                mbar_wait(&sh.p_ready[g % kRing], (g / kRing) & 1, dead);
+                mbar_wait(&sh.v_full[vs], v_phase, dead);
+                mbar_wait(&sh.o_free[i], ((g / NO) & 1) ^ 1, dead);
+                tc_after();
+                if (elected()) {
+                    const uint64_t vd = v_desc + (uint32_t)vs * (S::kBytes >> 4),
+                                   pd = p_desc + (uint32_t)w * (2 * kTile * NT >> 4);
+                    const uint32_t d = tmem + kO + i * NT;
+#pragma unroll
+                    for (int k = 0; k < kTile / 32; ++k) {
+                        tc_mma(d, vd + (k * 32 * D >> 4), pd + (k * 512 >> 4), desc, k > 0);
+                        tc_mma(d, vd + (k * 32 * D >> 4), pd + ((kTile * NT + k * 512) >> 4), desc, true);
+                    }
+                    tc_commit(&sh.o_full[i]);
+                    tc_commit(&sh.p_free[w]);
+                    tc_commit(&sh.v_empty[vs]);
+                }
+                __syncwarp();
+                ++g;
+                w = w + 1 == NW ? 0 : w + 1;
+                vs = vs + 1 == VS ? 0 : vs + 1;
+                v_phase ^= vs == 0;
+            }
+        }
+        drain_products(&sh.drained[1], dead);
     } else if (wid >= 4) {
         // ---------------- softmax ----------------
         const int w = (wid >> 2) - 1, t = tid & 127, bar = 1 + w;
@@ -1022,7 +1112,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     const float pos = FORM && a.f.slopes ? (a.c.positions ? (float)info.pos[t] : (float)j) : 0.0f;
                     const bool edge = came != (1u << blocks) - 1 ||
                                       !(tile < u.seen_prefix || (tile >= u.seen_low && tile < u.seen_end));
-                    bool closely = fresh || sh.unset[w][0] || (NT > 32 && sh.unset[w][1]);
+                    const bool check = fresh || sh.unset[w][0] || (NT > 32 && sh.unset[w][1]);
+                    bool closely = false;
                     uint64_t see = ~0ull;
                     float v_most = v_scale;
                     if (edge) {
@@ -1160,11 +1251,31 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             again = again || most >= 191u << 23;
                             // 2^k with 224 <= 2^k * largest weight <= 448 (448 = 1.75 * 2^8)
                             const uint32_t top = (__float_as_uint(__uint_as_float(most) * v_most) + (0x1fu << 16)) >> 23;
-                            if ((lane & 3) < 2)
-                                atomicMin(&scales[c0 + 2 * which + (lane & 1)], (262u - max(top, 9u)) << 23);
+                            if ((lane & 3) < 2) {
+                                const int c = c0 + 2 * which + (lane & 1);
+                                atomicMin(&scales[c], (262u - max(top, 9u)) << 23);
+                                if (check && !closely)
+                                    atomicMax(&sh.highest[w][c], (int)most);
+                            }
                         }
                         // a score that passed its base by 2^64 sends the warpgroup round again
-                        if (!barrier_or<128>(bar, again && !closely))
+                        bool redo = barrier_or<128>(bar, again && !closely);
+                        if (check && !closely) {
+                            // rows without a base keep 0 if their largest exponential is not far below 1
+                            bool low = false;
+                            if (t < NT) {
+                                low = !sh.is_set[w][t] && col.query[t] >= 0;
+                                if (low && sh.highest[w][t] >= 67 << 23) {
+                                    sh.is_set[w][t] = 1;
+                                    low = false;
+                                }
+                                sh.highest[w][t] = INT_MIN;
+                            }
+                            if (t == 0)
+                                sh.unset[w][0] = sh.unset[w][1] = 0;
+                            redo = barrier_or<128>(bar, low) || redo;
+                        }
+                        if (!redo)
                             break;
                         if (t < NT)
                             scales[t] = kNoScale;
@@ -1269,89 +1380,22 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         const int o0 = D == 128 ? 0 : (wid >> 1) * OC, d = D == 128 ? tid : tid & 63, bar = 1 + NW;
         const uint32_t lanes = (uint32_t)wid << 21;
         constexpr int kPart = OC % 16 == 0 ? 16 : 8;
-        const int rows = a.n * a.group;
-        const auto row_of = [&](int b, int h, int r) {
-            return ((size_t)b * a.n + r / a.group) * a.heads + h * a.group + r % a.group;
-        };
-        uint32_t prepared = 0;
-        Walk<NT> walk;
-        walk.start(a, range);
-        // describes the next segment that has tiles and brings in its queries; writes the rows that see nothing
-        const auto prepare = [&]() {
-            while (walk.at < walk.end && walk.u.count == 0) {
-                for (int c = 0; c < NT; ++c) {
-                    const int r = walk.rt * NT + c;
-                    if (r >= rows)
-                        break;
-                    const size_t row = row_of(walk.b, walk.h, r);
-                    if (tid < D)
-                        a.out[row * D + tid] = __float2bfloat16(0.0f);
-                    if (tid == 0)
-                        a.lse[row] = -INFINITY;
-                }
-                walk.next(a);
-            }
-            const uint32_t i = prepared & 1;
-            const Unit &u = walk.u;
-            const bool some = walk.at < walk.end;
-            if (tid == 0) {
-                Segment &g = sh.seg[i];
-                g.tiles = some ? walk.x1 - walk.x0 : 0;
-                g.x0 = walk.x0;
-                g.head_tiles = u.head_tiles;
-                g.low = u.low;
-                g.len = u.len;
-                g.first = u.first;
-                g.prefix = u.prefix;
-                g.i1 = u.i1;
-                g.b = walk.b;
-                g.h = walk.h;
-                g.rt = walk.rt;
-                g.seen_prefix = u.prefix / kTile;
-                g.seen_end = (a.f.parent ? u.first : u.first + u.i0 + 1) / kTile;
-                g.seen_low = a.f.window > 0
-                                 ? (int)((max((long long)u.first + u.i1 - a.f.window + 1, 0ll) + kTile - 1) / kTile)
-                                 : 0;
-                g.whole = walk.x0 == 0 && walk.x1 == u.count;
-                g.last = walk.x1 == u.count;
-                g.at = walk.at;
-                mbar_arrive(&sh.seg_ready[i]);
-            }
-            if (some) {
-                const bool tree = a.f.parent && (long long)(u.tile(walk.x1 - 1) + 1) * kTile > u.first;
-                load_queries<D, NT, 128>(a, u, walk.b, walk.h, walk.rt, tree, sh.q[i][0], sh.col[i], tid);
-                if (tree) {
-                    named_barrier<128>(bar);
-                    mark_kin<NT>(sh.col[i], tid);
-                }
-                walk.next(a);
-            }
-            proxy_fence();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sh.q_ready[i]);
-            ++prepared;
-        };
         uint32_t g = 0;
         float o[OC];
 #pragma unroll 1
         for (uint32_t seg = 0;; ++seg) {
-            if (seg == 0) {
-                prepare();
-                named_barrier<128>(bar);  // the segment's description
-            }
+            mbar_wait(&sh.seg_ready[seg & 1], (seg >> 1) & 1, dead);
             const Segment &u = sh.seg[seg & 1];
             const int tiles = u.tiles;
-            if (tiles == 0)
+            if (barrier_or<128>(bar, tiles == 0 || *dead))
                 break;
-            prepare();
 #pragma unroll
             for (int c = 0; c < OC; ++c)
                 o[c] = 0.0f;
             int ref = INT_MIN;  // of column tid: its sums count 2^ref
 #pragma unroll 1
             for (int x = 0; x < tiles; ++x) {
-                const uint32_t i = g & 1;
+                const uint32_t i = g & 1, io = g % NO;
                 mbar_wait(&sh.p_ready[g % kRing], (g / kRing) & 1, dead);  // the tile's powers
                 bool moved = false;
                 float alpha = 1.0f;
@@ -1374,12 +1418,12 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     for (int c = 0; c < OC; ++c)
                         o[c] *= sh.inverse[o0 + c];
                 }
-                mbar_wait(&sh.o_full[i], (g >> 1) & 1, dead);
+                mbar_wait(&sh.o_full[io], (g / NO) & 1, dead);
                 tc_after();
 #pragma unroll
                 for (int c1 = 0; c1 < OC; c1 += kPart) {
                     float y[kPart];
-                    TmemLoad<kPart>::go(tmem + lanes + kO + i * NT + o0 + c1, y);
+                    TmemLoad<kPart>::go(tmem + lanes + kO + io * NT + o0 + c1, y);
                     tmem_wait<kPart>(y);
 #pragma unroll
                     for (int c = 0; c < kPart; c += 4) {
@@ -1393,19 +1437,17 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 tc_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&sh.o_free[i]);
+                    mbar_arrive(&sh.o_free[io]);
                 ++g;
             }
             // whole units are finished here; parts go to the workspace for join_kernel
             const bool whole = u.whole;
-            const int b = u.b, h = u.h, rt = u.rt;
             const long long slot = 2ll * blockIdx.x + (u.x0 == 0);
             mbar_wait(&sh.sum_ready[seg & 1], (seg >> 1) & 1, dead);
             named_barrier<128>(bar);
             if (tid < NT) {
-                const int r = rt * NT + tid;
                 float total = 0.0f, base = 0.0f, part[NW];
-                if (r / a.group <= u.i1) {
+                if (sh.col[seg & 1].query[tid] >= 0) {
                     bool any = false;
                     const float(*y)[NT] = sh.warp_total[seg & 1], (*last)[NT] = sh.last_base[seg & 1];
 #pragma unroll
@@ -1421,37 +1463,39 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                         total += part[w] == 0.0f ? 0.0f : part[w] * exp2f(last[w][tid] - base);
                 }
                 const bool live = !(total == 0.0f);
+                const long long row = u.rows[tid];
                 // sums count 2^ref, totals 2^base
                 const float level = ref == INT_MIN ? 0.0f : power2(max(min(ref - (int)base, 127), -200));
                 sh.inverse[tid] = whole ? (live ? level / total : 0.0f) : level;
                 if (whole) {
-                    if (r < rows)
-                        a.lse[row_of(b, h, r)] = live ? (base + log2f(total)) * 0.6931471805599453f : -INFINITY;
+                    if (row >= 0)
+                        a.lse[row] = live ? (base + log2f(total)) * 0.6931471805599453f : -INFINITY;
                 } else {
                     a.part_sum[slot * NT + tid] = make_float2(total, base);
                 }
             }
             if (!whole && u.last && tid == 0)
-                a.joins[blockIdx.x] = make_int4((int)((u.at - u.x0) / range.each), b, h, rt);
+                a.joins[blockIdx.x] = make_int4((int)((u.at - u.x0) / range.each), u.b, u.h, u.rt);
             named_barrier<128>(bar);
-            if (lane == 0)
-                mbar_arrive(&sh.sum_free[seg & 1]);
 #pragma unroll
             for (int c = 0; c < OC; ++c) {
-                const int r = rt * NT + o0 + c;
                 const float inv = sh.inverse[o0 + c], y = inv == 0.0f ? 0.0f : o[c] * inv;
+                const long long row = u.rows[o0 + c];
                 if (!whole)
                     a.part[(slot * NT + o0 + c) * D + d] = y;
-                else if (r < rows)
-                    a.out[row_of(b, h, r) * D + d] = __float2bfloat16(y);
+                else if (row >= 0)
+                    a.out[row * D + d] = __float2bfloat16(y);
             }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sh.sum_free[seg & 1]);
         }
     }
     asm volatile("griddepcontrol.launch_dependents;");
     tc_before();
     __syncthreads();
     tc_after();
-    if (wid == kProducts)
+    if (wid == kValues)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kAlloc));
 }
 
@@ -1615,7 +1659,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                     mbar_arrive(&sh.q_ready);
                 named_barrier<256>(3);
                 if (tree) {
-                    mark_kin<NT>(sh.col, tid);
+                    mark_kin<NT, 256>(sh.col, tid);
                     named_barrier<256>(3);
                 }
                 for (int x = x0; x < x1; ++x) {
