@@ -376,6 +376,27 @@ template <int NT> struct Columns {
     int up[kMaxNodes];
 };
 
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)  // of unsigned 16-bit halves
+{
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Two values as pairs of e4m3: what 4 bits hold of them, and of the rest.
+__device__ __forceinline__ void split8(float x0, float x1, uint32_t &first, uint32_t &rest)
+{
+    uint32_t h, back;
+    uint16_t b1, b2;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b1) : "r"(h));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(b1));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(back) : "r"(h), "r"(back));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b2) : "r"(back));
+    first = b1;
+    rest = b2;
+}
+
 // Rows of a row tile into shared memory as two e4m3 terms, 128- or 64-byte
 // swizzled, and the columns' constants.  Called by THREADS threads (t), after the
 // last use of either; ends without a barrier.
@@ -408,64 +429,58 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const Unit &u,
             break;  // whole warps: a warp holds 2 or 4 rows
         int i, g;
         at.of(a, c, i, g);
-        const int H = h * a.group + g;
-        const bool live = i <= u.i1;
         const uint4 w = next;
         next = fetch(c + kRows);
-        float x[8];
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-        float amax = 0.0f;
+        uint32_t x[4] = {w.x, w.y, w.z, w.w};  // pairs of bf16
+        uint32_t most = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[2 * e] = __uint_as_float(ww[e] << 16);
-            x[2 * e + 1] = __uint_as_float(ww[e] & 0xffff0000u);
+        for (int e = 0; e < 4; ++e)
+            most = max_halves(most, x[e] & 0x7fff7fffu);
+        if ((most & 0xffffu) >= 0x7f80u || (most >> 16) >= 0x7f80u) {  // infinities and NaN: NaN, and not the largest
+            most = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 16)
+                    if (((x[e] >> k) & 0x7fffu) >= 0x7f80u)
+                        x[e] |= 0x7fffu << k;
+                    else
+                        most = max(most, (x[e] >> k) & 0x7fffu);
+            }
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            amax = isfinite(x[e]) ? fmaxf(amax, fabsf(x[e])) : amax;
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            most = max_halves(most, __shfl_xor_sync(0xffffffffu, most, o));
+        most = max(most & 0xffffu, most >> 16);
         // the row's power of two: its largest element becomes [128, 256)
-        const int ex = amax > 0.0f ? max((int)(__float_as_uint(amax) >> 23), 16) - 7 : 127;  // biased
+        const int ex = most ? max((int)(most >> 7), 16) - 7 : 127;  // biased
         const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
-        uint32_t hi[2], lo[2];
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float y[4], z[4];
-            uint32_t code[2], rest[2];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                y[k] = x[4 * e + k] * inv;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                code[k] = encode2(y[2 * k], y[2 * k + 1], SPEC_E4M3);
-                const float2 back = decode2((uint16_t)code[k], SPEC_E4M3);
-                z[2 * k] = y[2 * k] - back.x;
-                z[2 * k + 1] = y[2 * k + 1] - back.y;
-                rest[k] = encode2(z[2 * k], z[2 * k + 1], SPEC_E4M3);
-            }
-            hi[e] = code[0] | code[1] << 16;
-            lo[e] = rest[0] | rest[1] << 16;
-        }
+        for (int e = 0; e < 4; ++e)
+            split8(__uint_as_float(x[e] << 16) * inv, __uint_as_float(x[e] & 0xffff0000u) * inv, hi[e], lo[e]);
         const int to = c * D + ((d * 8) ^ (D == 128 ? (c & 7) << 4 : ((c >> 1) & 3) << 4));
-        *(uint2 *)(q + to) = make_uint2(hi[0], hi[1]);
-        *(uint2 *)(q + NT * D + to) = make_uint2(lo[0], lo[1]);
+        *(uint2 *)(q + to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+        *(uint2 *)(q + NT * D + to) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
         if (d == 0) {
             const float row = __uint_as_float((uint32_t)ex << 23) * a.f.scale;
             col.factor[c] = a.f.softcap > 0.0f ? row / a.f.softcap : row * kLog2e;
-            col.query[c] = live ? i : -1;
-            if (a.f.slopes) {
-                const int at_j = u.first + i;
-                float p = (float)at_j;
-                if (live && a.c.positions) {
-                    const int page = page_of(a.c, b, at_j / a.c.block);
-                    p = page < 0 ? 0.0f
-                                 : (float)a.c.positions[((size_t)page * a.c.kv_heads + h) * a.c.block + at_j % a.c.block];
-                }
-                col.pos[c] = p;
-                col.slope[c] = live ? a.f.slopes[H] * kLog2e : 0.0f;
+            col.query[c] = i <= u.i1 ? i : -1;
+        }
+    }
+    if (a.f.slopes) {
+        for (int c = t; c < NT; c += THREADS) {
+            int i, g;
+            at.of(a, c, i, g);
+            const bool live = i <= u.i1;
+            const int j = u.first + i;
+            float p = (float)j;
+            if (live && a.c.positions) {
+                const int page = page_of(a.c, b, j / a.c.block);
+                p = page < 0 ? 0.0f : (float)a.c.positions[((size_t)page * a.c.kv_heads + h) * a.c.block + j % a.c.block];
             }
+            col.pos[c] = p;
+            col.slope[c] = live ? a.f.slopes[h * a.group + g] * kLog2e : 0.0f;
         }
     }
 }
@@ -716,11 +731,7 @@ __device__ __forceinline__ int ordered(float x)
 }
 
 struct MaxHalves {
-    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const {
-        uint32_t r;
-        asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return max_halves(a, b); }
 };
 struct MaxInt {
     __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
@@ -1318,18 +1329,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                                     p[k] = e[4 * c4 + k] == 0.0f ? 0.0f : p[k];
                             }
                             uint32_t first[2], rest[2];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                uint32_t h2, back;
-                                uint16_t b1, b2;
-                                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h2) : "f"(p[2 * k + 1]), "f"(p[2 * k]));
-                                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b1) : "r"(h2));
-                                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(b1));
-                                asm("sub.f16x2 %0, %1, %2;" : "=r"(back) : "r"(h2), "r"(back));
-                                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b2) : "r"(back));
-                                first[k] = b1;
-                                rest[k] = b2;
-                            }
+                            split8(p[0], p[1], first[0], rest[0]);
+                            split8(p[2], p[3], first[1], rest[1]);
                             hi[c4] = first[0] | first[1] << 16;
                             lo[c4] = rest[0] | rest[1] << 16;
                         }
