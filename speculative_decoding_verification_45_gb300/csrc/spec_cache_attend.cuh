@@ -372,6 +372,7 @@ template <int NT> struct Columns {
     float slope[NT];   // times log2(e)
     float pos[NT];
     int query[NT];     // its query, -1: none
+    alignas(8) long long from[NT];  // where the query's row lies, in elements
     uint32_t kin[NT][kMaxNodes / 32];
     int up[kMaxNodes];
 };
@@ -414,65 +415,13 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const Unit &u,
             col.up[k] = (unsigned)up < (unsigned)k ? up : -1;
         }
     const RowAt at(a, rt * NT);
-    const auto fetch = [&](int c) {
+    for (int c = t; c < NT; c += THREADS) {
         int i, g;
         at.of(a, c, i, g);
-        return c < NT && i <= u.i1 ? __ldg((const uint4 *)(a.q + (size_t)b * a.q_stride[0] + (size_t)i * a.q_stride[1] +
-                                                           (size_t)(h * a.group + g) * a.q_stride[2] + d * 8))
-                                   : make_uint4(0, 0, 0, 0);
-    };
-    uint4 next = fetch(t / kLanes);
-#pragma unroll 1
-    for (int r0 = 0; r0 < NT; r0 += kRows) {
-        const int c = r0 + t / kLanes;
-        if (NT % kRows && c >= NT)
-            break;  // whole warps: a warp holds 2 or 4 rows
-        int i, g;
-        at.of(a, c, i, g);
-        const uint4 w = next;
-        next = fetch(c + kRows);
-        uint32_t x[4] = {w.x, w.y, w.z, w.w};  // pairs of bf16
-        uint32_t most = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            most = max_halves(most, x[e] & 0x7fff7fffu);
-        if ((most & 0xffffu) >= 0x7f80u || (most >> 16) >= 0x7f80u) {  // infinities and NaN: NaN, and not the largest
-            most = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                for (int k = 0; k < 32; k += 16)
-                    if (((x[e] >> k) & 0x7fffu) >= 0x7f80u)
-                        x[e] |= 0x7fffu << k;
-                    else
-                        most = max(most, (x[e] >> k) & 0x7fffu);
-            }
-        }
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1)
-            most = max_halves(most, __shfl_xor_sync(0xffffffffu, most, o));
-        most = max(most & 0xffffu, most >> 16);
-        // the row's power of two: its largest element becomes [128, 256)
-        const int ex = most ? max((int)(most >> 7), 16) - 7 : 127;  // biased
-        const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            split8(__uint_as_float(x[e] << 16) * inv, __uint_as_float(x[e] & 0xffff0000u) * inv, hi[e], lo[e]);
-        const int to = c * D + ((d * 8) ^ (D == 128 ? (c & 7) << 4 : ((c >> 1) & 3) << 4));
-        *(uint2 *)(q + to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-        *(uint2 *)(q + NT * D + to) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-        if (d == 0) {
-            const float row = __uint_as_float((uint32_t)ex << 23) * a.f.scale;
-            col.factor[c] = a.f.softcap > 0.0f ? row / a.f.softcap : row * kLog2e;
-            col.query[c] = i <= u.i1 ? i : -1;
-        }
-    }
-    if (a.f.slopes) {
-        for (int c = t; c < NT; c += THREADS) {
-            int i, g;
-            at.of(a, c, i, g);
-            const bool live = i <= u.i1;
+        const bool live = i <= u.i1;
+        col.query[c] = live ? i : -1;
+        col.from[c] = (long long)b * a.q_stride[0] + (long long)i * a.q_stride[1] + (long long)(h * a.group + g) * a.q_stride[2];
+        if (a.f.slopes) {
             const int j = u.first + i;
             float p = (float)j;
             if (live && a.c.positions) {
@@ -482,6 +431,89 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const Unit &u,
             col.pos[c] = p;
             col.slope[c] = live ? a.f.slopes[h * a.group + g] * kLog2e : 0.0f;
         }
+    }
+    if (THREADS == 32)
+        __syncwarp();
+    else
+        named_barrier<THREADS>(3);
+    const auto fetch = [&](int c) {
+        return c < NT && col.query[c] >= 0 ? __ldg((const uint4 *)(a.q + col.from[c] + d * 8)) : make_uint4(0, 0, 0, 0);
+    };
+    // two rows a turn, the next two turns' loads on their way, one short loop: unrolled, this waited for instructions
+    int c = t / kLanes;
+    uint4 next[4] = {fetch(c), fetch(c + kRows), fetch(c + 2 * kRows), fetch(c + 3 * kRows)};
+#pragma unroll 1
+    for (; c - t / kLanes < NT; c += 2 * kRows) {
+        uint32_t x[2][4] = {{next[0].x, next[0].y, next[0].z, next[0].w}, {next[1].x, next[1].y, next[1].z, next[1].w}};
+        next[0] = next[2];
+        next[1] = next[3];
+        next[2] = fetch(c + 4 * kRows);
+        next[3] = fetch(c + 5 * kRows);
+        uint32_t most[2];  // of pairs of bf16
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            most[k] = max_halves(max_halves(x[k][0] & 0x7fff7fffu, x[k][1] & 0x7fff7fffu),
+                                 max_halves(x[k][2] & 0x7fff7fffu, x[k][3] & 0x7fff7fffu));
+        const uint32_t any = max_halves(most[0], most[1]);
+        if ((any & 0xffffu) >= 0x7f80u || (any >> 16) >= 0x7f80u) {  // infinities and NaN: NaN, and not the largest
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+                most[k] = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int at = 16 * (e & 1);
+                    if (((x[k][e >> 1] >> at) & 0x7fffu) >= 0x7f80u)
+                        x[k][e >> 1] |= 0x7fffu << at;
+                    else
+                        most[k] = max(most[k], (x[k][e >> 1] >> at) & 0x7fffu);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                most[k] = max_halves(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int row = c + k * kRows;
+            const uint32_t top = max(most[k] & 0xffffu, most[k] >> 16);
+            // the row's power of two: its largest element becomes [128, 256)
+            const int ex = top ? max((int)(top >> 7), 16) - 7 : 127;  // biased
+            const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                split8(__uint_as_float(x[k][e] << 16) * inv, __uint_as_float(x[k][e] & 0xffff0000u) * inv, hi[e], lo[e]);
+            const int to = row * D + ((d * 8) ^ (D == 128 ? (row & 7) << 4 : ((row >> 1) & 3) << 4));
+            if (row < NT) {
+                *(uint2 *)(q + to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+                *(uint2 *)(q + NT * D + to) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                if (d == 0) {
+                    const float f = __uint_as_float((uint32_t)ex << 23) * a.f.scale;
+                    col.factor[row] = a.f.softcap > 0.0f ? f / a.f.softcap : f * kLog2e;
+                }
+            }
+        }
+    }
+}
+
+// The rows of a row tile on their way into L2; a warp calls it.
+template <int D, int NT>
+__device__ __forceinline__ void prefetch_queries(const AttendArgs &a, const Unit &u, int b, int h, int rt, int lane)
+{
+    const RowAt at(a, rt * NT);
+    for (int c = lane; c < NT; c += 32) {
+        int i, g;
+        at.of(a, c, i, g);
+        if (i > u.i1)
+            continue;
+        const __nv_bfloat16 *row =
+            a.q + (size_t)b * a.q_stride[0] + (size_t)i * a.q_stride[1] + (size_t)(h * a.group + g) * a.q_stride[2];
+#pragma unroll
+        for (int d = 0; d < D; d += 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row + d));
     }
 }
 
@@ -709,6 +741,7 @@ template <int D, int NT> struct AttendShared {
     alignas(16) float base[S::NW][NT];
     alignas(16) uint32_t scale[S::NW][4][NT];  // per tile: 2^k, as bits, that brings the largest weight to [224, 448]
     alignas(16) int power[S::kRing][NT];       // per tile: O^T counts 2^power
+    alignas(16) long long out_row[NT];
     alignas(16) float factor[2][NT], inverse[NT], none[NT];  // none: bases of 0
     alignas(16) float warp_total[2][S::NW * 4][NT], last_base[2][S::NW][NT];
     alignas(16) float alpha[S::NW][NT];        // what a moved base leaves of the totals
@@ -939,6 +972,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             if (!some)
                 break;
             walk.next(a);
+            if (walk.at < walk.end)
+                prefetch_queries<D, NT>(a, walk.u, walk.b, walk.h, walk.rt, lane);
         }
     } else if (wid == kProducer) {
         // ---------------- producer ----------------
@@ -1465,6 +1500,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 }
                 const bool live = !(total == 0.0f);
                 const long long row = u.rows[tid];
+                sh.out_row[tid] = row;
                 // sums count 2^ref, totals 2^base
                 const float level = ref == INT_MIN ? 0.0f : power2(max(min(ref - (int)base, 127), -200));
                 sh.inverse[tid] = whole ? (live ? level / total : 0.0f) : level;
@@ -1478,18 +1514,24 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             if (!whole && u.last && tid == 0)
                 a.joins[blockIdx.x] = make_int4((int)((u.at - u.x0) / range.each), u.b, u.h, u.rt);
             named_barrier<128>(bar);
-#pragma unroll
-            for (int c = 0; c < OC; ++c) {
-                const float inv = sh.inverse[o0 + c], y = inv == 0.0f ? 0.0f : o[c] * inv;
-                const long long row = u.rows[o0 + c];
-                if (!whole)
-                    a.part[(slot * NT + o0 + c) * D + d] = y;
-                else if (row >= 0)
-                    a.out[row * D + d] = __float2bfloat16(y);
-            }
-            __syncwarp();
-            if (lane == 0)
+            if (lane == 0)  // the segment's place is free
                 mbar_arrive(&sh.sum_free[seg & 1]);
+            if (whole) {
+#pragma unroll
+                for (int c = 0; c < OC; ++c) {
+                    const float inv = sh.inverse[o0 + c];
+                    const long long row = sh.out_row[o0 + c];
+                    if (row >= 0)
+                        a.out[row * D + d] = __float2bfloat16(inv == 0.0f ? 0.0f : o[c] * inv);
+                }
+            } else {
+                float *part = a.part + (slot * NT + o0) * D + d;
+#pragma unroll
+                for (int c = 0; c < OC; ++c) {
+                    const float inv = sh.inverse[o0 + c];
+                    part[c * D] = inv == 0.0f ? 0.0f : o[c] * inv;
+                }
+            }
         }
     }
     asm volatile("griddepcontrol.launch_dependents;");
