@@ -318,9 +318,9 @@ spec_status spec_device_pointer(const void *ptr, const void **device_ptr);
  * [0, num_pages) counts as not cached; SPEC_STATUS_BAD_LENGTH and
  * SPEC_STATUS_BAD_PAGE are OR-ed into *status when status is not NULL.  Scales
  * that a call reads are positive and finite.
- * Ownership, stream and error rules as for spec_verify, but for two kernels
- * where a result is joined or moved after it is found; every array is device
- * memory.  Nothing is allocated. */
+ * Ownership, stream and error rules as for spec_verify, but that a call may
+ * enqueue up to three kernels; every array is device memory.  Nothing is
+ * allocated. */
 typedef enum { SPEC_E4M3 = 0, SPEC_E5M2 = 1 } spec_code;
 
 typedef struct spec_cache {
@@ -394,11 +394,12 @@ spec_status spec_cache_attend_workspace(const spec_cache *cache, int n, int head
  * queries and the head's query heads of exp(x - lse), for every cached token of
  * every sequence (lse as spec_cache_attend gave it; rows whose lse is -inf add
  * nothing).  weights [num_pages, kv_heads, block] float32, dense.  Each sum has
- * a fixed order.  Pages that several sequences share must not be weighed in one
+ * a fixed order.  workspace: as for spec_cache_attend.  Pages that several sequences share must not be weighed in one
  * call: their sums would race. */
 spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, const void *q,
                              const int64_t q_stride[3], int n, int heads, const spec_cache_form *form,
-                             const float *lse, float *weights, uint32_t *status, void *stream);
+                             const float *lse, float *weights, void *workspace, int64_t workspace_bytes,
+                             uint32_t *status, void *stream);
 
 /* Eviction: of each sequence and key/value head, the `recent` newest tokens and,
  * of the others, the keep - recent with the largest weights (the lower index on

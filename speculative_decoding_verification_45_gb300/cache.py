@@ -189,6 +189,18 @@ def _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent):
     return f, n, heads, (ctypes.c_int64 * 3)(*_strides(q, "q", 8))
 
 
+def _workspace(lib, c, n, heads, dev, stream):
+    """A workspace for one call, and its size; the block belongs to the stream that uses it."""
+    need = ctypes.c_int64()
+    rc = lib.spec_cache_attend_workspace(ctypes.byref(c), n, heads, ctypes.byref(need))
+    if rc:
+        _fail(rc, "spec_cache_attend_workspace")
+    if stream is None:
+        return torch.empty(need.value, dtype=torch.uint8, device=dev), need.value
+    with torch.cuda.stream(stream):
+        return torch.empty(need.value, dtype=torch.uint8, device=dev), need.value
+
+
 def cache_attend(q, cache, block_table, lengths, num_new=None, scale=None, softcap=0.0, slopes=None, window=0,
                  prefix=None, parent=None, out=None, lse=None, status=None, stream=None):
     """Attention of the newest tokens over the cache (spec_cache_attend).
@@ -212,17 +224,9 @@ def cache_attend(q, cache, block_table, lengths, num_new=None, scale=None, softc
     out, out_ptr = _output(out, "out", torch.bfloat16, (c.batch, n, heads, c.dim), dev)
     lse, lse_ptr = _output(lse, "lse", torch.float32, (c.batch, n, heads), dev)
     lib = _native.load()
-    need = ctypes.c_int64()
-    rc = lib.spec_cache_attend_workspace(ctypes.byref(c), n, heads, ctypes.byref(need))
-    if rc:
-        _fail(rc, "spec_cache_attend_workspace")
-    if stream is None:
-        work = torch.empty(need.value, dtype=torch.uint8, device=dev)
-    else:
-        with torch.cuda.stream(stream):  # the block belongs to the stream that uses it
-            work = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    work, size = _workspace(lib, c, n, heads, dev, stream)
     rc = lib.spec_cache_attend(ctypes.byref(c), len_ptr, q.data_ptr(), stride, n, heads, ctypes.byref(f), out_ptr,
-                               lse_ptr, work.data_ptr(), need.value, _status(status, dev), _stream(stream, dev))
+                               lse_ptr, work.data_ptr(), size, _status(status, dev), _stream(stream, dev))
     if rc:
         _fail(rc, "spec_cache_attend")
     return out, lse
@@ -240,8 +244,10 @@ def cache_weigh(q, cache, block_table, lengths, lse, weights, num_new=None, scal
     f, n, heads, stride = _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent)
     lse_ptr = _check(lse, "lse", torch.float32, (c.batch, n, heads), dev)
     w_ptr = _check(weights, "weights", torch.float32, (c.num_pages, c.kv_heads, c.block), dev)
-    rc = _native.load().spec_cache_weigh(ctypes.byref(c), len_ptr, q.data_ptr(), stride, n, heads, ctypes.byref(f),
-                                         lse_ptr, w_ptr, _status(status, dev), _stream(stream, dev))
+    lib = _native.load()
+    work, size = _workspace(lib, c, n, heads, dev, stream)
+    rc = lib.spec_cache_weigh(ctypes.byref(c), len_ptr, q.data_ptr(), stride, n, heads, ctypes.byref(f), lse_ptr, w_ptr,
+                              work.data_ptr(), size, _status(status, dev), _stream(stream, dev))
     if rc:
         _fail(rc, "spec_cache_weigh")
     return weights

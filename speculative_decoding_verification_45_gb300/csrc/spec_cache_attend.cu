@@ -137,6 +137,46 @@ AttendArgs make_args(const spec_cache *cache, const int32_t *lengths, const void
 
 bool has_form(const spec_cache_form *f) { return f->softcap > 0.0f || f->slopes; }
 
+// The split queries and their factors; rows of row tiles filled up.
+int64_t split_bytes(const spec_cache &c, const Shape &s) { return (int64_t)c.batch * c.kv_heads * s.row_tiles * s.nt * (2 * c.dim + 4); }
+
+// Points the arguments into the workspace and launches split_kernel.
+spec_status split_queries(AttendArgs &a, const Shape &s, void *workspace, const Kernels &k, cudaStream_t stream)
+{
+    const int64_t rows = (int64_t)a.c.batch * a.c.kv_heads * s.row_tiles * s.nt, each = 256 / (a.c.dim / 8);
+    if ((rows + each - 1) / each > INT_MAX)
+        return SPEC_ERR_UNSUPPORTED;
+    a.split = (uint8_t *)workspace;
+    a.factor = (float *)(a.split + rows * 2 * a.c.dim);
+    int nt = s.nt;
+    void *args[] = {&a, &nt};
+    if (cudaLaunchKernel(k.split, dim3((unsigned)((rows + each - 1) / each)), dim3(256), args, 0, stream) != cudaSuccess) {
+        cudaGetLastError();
+        return SPEC_ERR_CUDA;
+    }
+    return SPEC_OK;
+}
+
+// Launches a kernel that may begin before the one ahead of it in the stream has ended (it waits on the device).
+spec_status launch_behind(const void *kernel, dim3 grid, int threads, size_t smem, void **args, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelExC(&cfg, kernel, args) != cudaSuccess) {
+        cudaGetLastError();
+        return SPEC_ERR_CUDA;
+    }
+    return SPEC_OK;
+}
+
 int64_t part_bytes(const Shape &s, int dim, int sms) { return 2ll * sms * s.nt * dim * 4; }
 int64_t sum_bytes(const Shape &s, int sms) { return 2ll * sms * s.nt * 8; }
 
@@ -161,7 +201,7 @@ spec_status spec_cache_attend_workspace(const spec_cache *cache, int n, int head
     if (st != SPEC_OK)
         return st;
     const Shape s = shape_for(*cache, n, heads);
-    *bytes = part_bytes(s, cache->dim, sms) + sum_bytes(s, sms) + 16ll * sms;
+    *bytes = split_bytes(*cache, s) + part_bytes(s, cache->dim, sms) + sum_bytes(s, sms) + 16ll * sms;
     return SPEC_OK;
 }
 
@@ -182,52 +222,40 @@ spec_status spec_cache_attend(const spec_cache *cache, const int32_t *lengths, c
         return st;
     const Shape shape = shape_for(*cache, n, heads);
     const int64_t parts = part_bytes(shape, cache->dim, sms), sums = sum_bytes(shape, sms);
-    if (workspace_bytes < parts + sums + 16ll * sms)
+    const int64_t split = split_bytes(*cache, shape);
+    if (workspace_bytes < split + parts + sums + 16ll * sms)
         return SPEC_ERR_INVALID_ARG;
     AttendArgs a = make_args(cache, lengths, q, q_stride, n, heads, form, shape, status);
     a.out = (__nv_bfloat16 *)out;
     a.lse = lse;
-    a.part = (float *)workspace;
-    a.part_sum = (float2 *)((char *)workspace + parts);
-    a.joins = (int4 *)((char *)workspace + parts + sums);
+    a.part = (float *)((char *)workspace + split);  // a multiple of 64 bytes in
+    a.part_sum = (float2 *)((char *)a.part + parts);
+    a.joins = (int4 *)((char *)a.part_sum + sums);
     CUtensorMap kmap, vmap;
     if ((st = make_map(*cache, cache->k, cache->k_stride, &kmap)) != SPEC_OK ||
         (st = make_map(*cache, cache->v, cache->v_stride, &vmap)) != SPEC_OK)
         return st;
     const Kernels &k = cache->dim == 64 ? kernels_d64() : kernels_d128();
-    void *args[] = {&a, &kmap, &vmap};
-    if (cudaLaunchKernel(k.attend[shape.index][has_form(form)], dim3(sms), dim3(k.attend_threads[shape.index]), args,
-                         (size_t)k.attend_smem[shape.index], (cudaStream_t)stream) != cudaSuccess) {
-        cudaGetLastError();
-        return SPEC_ERR_CUDA;
-    }
-    // the joins wait on the device for the parts; their launch overlaps the kernel before them
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sms, shape.nt / kJoinRows);
-    cfg.blockDim = dim3(128);
-    cfg.stream = (cudaStream_t)stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    void *join_args[] = {&a};
-    if (cudaLaunchKernelExC(&cfg, k.join[shape.index], join_args) != cudaSuccess) {
-        cudaGetLastError();
-        return SPEC_ERR_CUDA;
-    }
-    return SPEC_OK;
+    if ((st = split_queries(a, shape, workspace, k, (cudaStream_t)stream)) != SPEC_OK)
+        return st;
+    void *args[] = {&a, &kmap, &vmap}, *join_args[] = {&a};
+    st = launch_behind(k.attend[shape.index][has_form(form)], dim3(sms), k.attend_threads[shape.index],
+                       (size_t)k.attend_smem[shape.index], args, (cudaStream_t)stream);
+    return st != SPEC_OK ? st
+                         : launch_behind(k.join[shape.index], dim3(sms, shape.nt / kJoinRows), 128, 0, join_args,
+                                         (cudaStream_t)stream);
 }
 
 spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, const void *q,
                              const int64_t q_stride[3], int n, int heads, const spec_cache_form *form,
-                             const float *lse, float *weights, uint32_t *status, void *stream)
+                             const float *lse, float *weights, void *workspace, int64_t workspace_bytes,
+                             uint32_t *status, void *stream)
 {
     NvtxScope nvtx("spec_cache_weigh");
     spec_status st = check_call(cache, lengths, q, q_stride, n, heads, form, status);
     if (st != SPEC_OK || cache->batch == 0 || n == 0)
         return st;
-    if (bad4(lse, true) || bad4(weights, true))
+    if (bad4(lse, true) || bad4(weights, true) || !workspace || ((uintptr_t)workspace & 15u))
         return SPEC_ERR_INVALID_ARG;
     int sms = 0;
     st = device_sms(&sms);
@@ -237,17 +265,17 @@ spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, co
     AttendArgs a = make_args(cache, lengths, q, q_stride, n, heads, form, shape, status);
     a.lse_in = lse;
     a.weights = weights;
+    if (workspace_bytes < split_bytes(*cache, shape))
+        return SPEC_ERR_INVALID_ARG;
     CUtensorMap kmap;
     if ((st = make_map(*cache, cache->k, cache->k_stride, &kmap)) != SPEC_OK)
         return st;
     const Kernels &k = cache->dim == 64 ? kernels_d64() : kernels_d128();
+    if ((st = split_queries(a, shape, workspace, k, (cudaStream_t)stream)) != SPEC_OK)
+        return st;
     void *args[] = {&a, &kmap};
-    if (cudaLaunchKernel(k.weigh[shape.index][has_form(form)], dim3(sms), dim3(kWeighThreads), args,
-                         (size_t)k.weigh_smem[shape.index], (cudaStream_t)stream) != cudaSuccess) {
-        cudaGetLastError();
-        return SPEC_ERR_CUDA;
-    }
-    return SPEC_OK;
+    return launch_behind(k.weigh[shape.index][has_form(form)], dim3(sms), kWeighThreads, (size_t)k.weigh_smem[shape.index],
+                         args, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -44,6 +44,8 @@ struct AttendArgs {
     float *lse;
     const float *lse_in;
     float *weights;
+    uint8_t *split;        // [batch][kv heads][row tiles][2][NT * D]: the queries as split_kernel leaves them
+    float *factor;         // [batch][kv heads][row tiles][NT]
     float *part;           // [2 * CTAs][NT][D] partial sums, then [2 * CTAs][NT] (total, base)
     float2 *part_sum;
     int4 *joins;           // [CTAs]: (first CTA or -1, sequence, head, row tile)
@@ -372,7 +374,6 @@ template <int NT> struct Columns {
     float slope[NT];   // times log2(e)
     float pos[NT];
     int query[NT];     // its query, -1: none
-    alignas(8) long long from[NT];  // where the query's row lies, in elements
     uint32_t kin[NT][kMaxNodes / 32];
     int up[kMaxNodes];
 };
@@ -398,29 +399,81 @@ __device__ __forceinline__ void split8(float x0, float x1, uint32_t &first, uint
     rest = b2;
 }
 
-// Rows of a row tile into shared memory as two e4m3 terms, 128- or 64-byte
-// swizzled, and the columns' constants.  Called by THREADS threads (t), after the
-// last use of either; ends without a barrier.
-template <int D, int NT, int THREADS>
-__device__ __forceinline__ void load_queries(const AttendArgs &a, const Unit &u, int b, int h, int rt, bool tree, uint8_t *q,
-                                             Columns<NT> &col, int t)
+// Queries as two e4m3 terms, row tile by row tile, laid out as the products read
+// them from shared memory (128- or 64-byte swizzled), and the factor of each
+// row's accumulators.  A kernel of its own, D / 8 lanes a row: one warp of the
+// attention kernel took 18,000 cycles for the 32 rows of a segment, as long as
+// their attention over 2,000 tokens.
+template <int D> __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ AttendArgs a, int nt)
 {
-    constexpr int kLanes = D / 8, kRows = THREADS / kLanes;
-    const int d = t % kLanes;
-    if (tree && a.f.parent)
-        for (int k = t; k < u.m; k += THREADS) {
-            const int up = k > 0 ? a.f.parent[(size_t)b * a.n + k] : -1;
-            if (k > 0 && (unsigned)up >= (unsigned)k)
-                report(a.status, SPEC_STATUS_BAD_TREE);
-            col.up[k] = (unsigned)up < (unsigned)k ? up : -1;
-        }
+    constexpr int kLanes = D / 8;
+    const int d = threadIdx.x % kLanes;
+    const long long padded = (long long)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;  // row, row tiles filled up
+    const long long tile = padded / nt;
+    const int c = (int)(padded % nt), rt = (int)(tile % a.row_tiles);
+    const long long unit = tile / a.row_tiles;
+    const int h = (int)(unit % a.c.kv_heads), b = (int)min(unit / a.c.kv_heads, (long long)a.c.batch - 1);
+    const bool here = unit < (long long)a.c.batch * a.c.kv_heads;
+    const int r = rt * nt + c, i = r / a.group, g = r % a.group;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (here && i < a.n && i < (a.f.num_new ? a.f.num_new[b] : a.n))
+        w = __ldg((const uint4 *)(a.q + (size_t)b * a.q_stride[0] + (size_t)i * a.q_stride[1] +
+                                  (size_t)(h * a.group + g) * a.q_stride[2] + d * 8));
+    uint32_t x[4] = {w.x, w.y, w.z, w.w}, most = 0;  // pairs of bf16
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int at = 16 * (e & 1);
+        const uint32_t y = (x[e >> 1] >> at) & 0x7fffu;
+        if (y >= 0x7f80u)  // infinities and NaN: NaN, and not the largest
+            x[e >> 1] |= 0x7fffu << at;
+        else
+            most = max(most, y);
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    asm volatile("griddepcontrol.launch_dependents;");
+    // the row's power of two: its largest element becomes [128, 256)
+    const int ex = most ? max((int)(most >> 7), 16) - 7 : 127;  // biased
+    const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        split8(__uint_as_float(x[e] << 16) * inv, __uint_as_float(x[e] & 0xffff0000u) * inv, hi[e], lo[e]);
+    if (!here)
+        return;
+    uint8_t *to = a.split + tile * (2ll * nt * D) + c * D + ((d * 8) ^ (D == 128 ? (c & 7) << 4 : ((c >> 1) & 3) << 4));
+    *(uint2 *)to = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    *(uint2 *)(to + (size_t)nt * D) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+    if (d == 0) {
+        const float f = __uint_as_float((uint32_t)ex << 23) * a.f.scale;
+        a.factor[tile * nt + c] = a.f.softcap > 0.0f ? f / a.f.softcap : f * kLog2e;
+    }
+}
+
+// Bytes of a row tile's split queries and factors.
+template <int D, int NT> constexpr uint32_t kQueryBytes = 2 * NT * D + 4 * NT;
+
+// A row tile's split queries and factors into shared memory; one thread, which has announced the bytes.
+template <int D, int NT>
+__device__ __forceinline__ void load_queries(const AttendArgs &a, int b, int h, int rt, uint8_t *q, Columns<NT> &col, uint64_t *bar)
+{
+    const long long tile = ((long long)b * a.c.kv_heads + h) * a.row_tiles + rt;
+    bulk_load(a.split + tile * (2 * NT * D), q, 2 * NT * D, bar);
+    bulk_load(a.factor + tile * NT, col.factor, 4 * NT, bar);
+}
+
+// The columns' other constants, by THREADS threads; ends without a barrier.
+template <int NT, int THREADS>
+__device__ __forceinline__ void describe_columns(const AttendArgs &a, const Unit &u, int b, int h, int rt, bool tree,
+                                                 Columns<NT> &col, int t)
+{
     const RowAt at(a, rt * NT);
     for (int c = t; c < NT; c += THREADS) {
         int i, g;
         at.of(a, c, i, g);
         const bool live = i <= u.i1;
         col.query[c] = live ? i : -1;
-        col.from[c] = (long long)b * a.q_stride[0] + (long long)i * a.q_stride[1] + (long long)(h * a.group + g) * a.q_stride[2];
         if (a.f.slopes) {
             const int j = u.first + i;
             float p = (float)j;
@@ -432,89 +485,13 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, const Unit &u,
             col.slope[c] = live ? a.f.slopes[h * a.group + g] * kLog2e : 0.0f;
         }
     }
-    if (THREADS == 32)
-        __syncwarp();
-    else
-        named_barrier<THREADS>(3);
-    const auto fetch = [&](int c) {
-        return c < NT && col.query[c] >= 0 ? __ldg((const uint4 *)(a.q + col.from[c] + d * 8)) : make_uint4(0, 0, 0, 0);
-    };
-    // two rows a turn, the next two turns' loads on their way, one short loop: unrolled, this waited for instructions
-    int c = t / kLanes;
-    uint4 next[4] = {fetch(c), fetch(c + kRows), fetch(c + 2 * kRows), fetch(c + 3 * kRows)};
-#pragma unroll 1
-    for (; c - t / kLanes < NT; c += 2 * kRows) {
-        uint32_t x[2][4] = {{next[0].x, next[0].y, next[0].z, next[0].w}, {next[1].x, next[1].y, next[1].z, next[1].w}};
-        next[0] = next[2];
-        next[1] = next[3];
-        next[2] = fetch(c + 4 * kRows);
-        next[3] = fetch(c + 5 * kRows);
-        uint32_t most[2];  // of pairs of bf16
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            most[k] = max_halves(max_halves(x[k][0] & 0x7fff7fffu, x[k][1] & 0x7fff7fffu),
-                                 max_halves(x[k][2] & 0x7fff7fffu, x[k][3] & 0x7fff7fffu));
-        const uint32_t any = max_halves(most[0], most[1]);
-        if ((any & 0xffffu) >= 0x7f80u || (any >> 16) >= 0x7f80u) {  // infinities and NaN: NaN, and not the largest
-#pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
-                most[k] = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int at = 16 * (e & 1);
-                    if (((x[k][e >> 1] >> at) & 0x7fffu) >= 0x7f80u)
-                        x[k][e >> 1] |= 0x7fffu << at;
-                    else
-                        most[k] = max(most[k], (x[k][e >> 1] >> at) & 0x7fffu);
-                }
-            }
+    if (tree && a.f.parent)
+        for (int k = t; k < u.m; k += THREADS) {
+            const int up = k > 0 ? a.f.parent[(size_t)b * a.n + k] : -1;
+            if (k > 0 && (unsigned)up >= (unsigned)k)
+                report(a.status, SPEC_STATUS_BAD_TREE);
+            col.up[k] = (unsigned)up < (unsigned)k ? up : -1;
         }
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                most[k] = max_halves(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int row = c + k * kRows;
-            const uint32_t top = max(most[k] & 0xffffu, most[k] >> 16);
-            // the row's power of two: its largest element becomes [128, 256)
-            const int ex = top ? max((int)(top >> 7), 16) - 7 : 127;  // biased
-            const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                split8(__uint_as_float(x[k][e] << 16) * inv, __uint_as_float(x[k][e] & 0xffff0000u) * inv, hi[e], lo[e]);
-            const int to = row * D + ((d * 8) ^ (D == 128 ? (row & 7) << 4 : ((row >> 1) & 3) << 4));
-            if (row < NT) {
-                *(uint2 *)(q + to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-                *(uint2 *)(q + NT * D + to) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-                if (d == 0) {
-                    const float f = __uint_as_float((uint32_t)ex << 23) * a.f.scale;
-                    col.factor[row] = a.f.softcap > 0.0f ? f / a.f.softcap : f * kLog2e;
-                }
-            }
-        }
-    }
-}
-
-// The rows of a row tile on their way into L2; a warp calls it.
-template <int D, int NT>
-__device__ __forceinline__ void prefetch_queries(const AttendArgs &a, const Unit &u, int b, int h, int rt, int lane)
-{
-    const RowAt at(a, rt * NT);
-    for (int c = lane; c < NT; c += 32) {
-        int i, g;
-        at.of(a, c, i, g);
-        if (i > u.i1)
-            continue;
-        const __nv_bfloat16 *row =
-            a.q + (size_t)b * a.q_stride[0] + (size_t)i * a.q_stride[1] + (size_t)(h * a.group + g) * a.q_stride[2];
-#pragma unroll
-        for (int d = 0; d < D; d += 64)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(row + d));
-    }
 }
 
 // The ancestors of each column's query, after a barrier behind load_queries.
@@ -902,6 +879,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         // ---------------- queries ----------------
         Walk<NT> walk;
         walk.start(a, range);
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // for split_kernel
 #pragma unroll 1
         for (uint32_t seg = 0;; ++seg) {
             const uint32_t i = seg & 1;
@@ -959,21 +937,25 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 mbar_arrive(&sh.seg_ready[i]);
             if (some) {
                 const bool tree = a.f.parent && (long long)(u.tile(walk.x1 - 1) + 1) * kTile > u.first;
-                load_queries<D, NT, 32>(a, u, walk.b, walk.h, walk.rt, tree, sh.q[i][0], sh.col[i], lane);
+                describe_columns<NT, 32>(a, u, walk.b, walk.h, walk.rt, tree, sh.col[i], lane);
                 if (tree) {
                     __syncwarp();
                     mark_kin<NT, 32>(sh.col[i], lane);
                 }
             }
-            proxy_fence();
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sh.q_ready[i]);
-            if (!some)
+            if (lane == 0) {
+                mbar_expect(&sh.q_ready[i], some ? kQueryBytes<D, NT> : 0);
+                if (some)
+                    load_queries<D, NT>(a, walk.b, walk.h, walk.rt, sh.q[i][0], sh.col[i], &sh.q_ready[i]);
+            }
+            if (!some) {
+                if (*dead && seg > 0)  // the last queries in flight land
+                    for (uint32_t k = 0; k < 4096 && !mbar_try(&sh.q_ready[i ^ 1], ((seg - 1) >> 1) & 1); ++k)
+                        ;
                 break;
+            }
             walk.next(a);
-            if (walk.at < walk.end)
-                prefetch_queries<D, NT>(a, walk.u, walk.b, walk.h, walk.rt, lane);
         }
     } else if (wid == kProducer) {
         // ---------------- producer ----------------
@@ -1589,7 +1571,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.s_free[i], 4);
         }
-        mbar_init(&sh.q_ready, 8);
+        mbar_init(&sh.q_ready, 1);
         mbar_init(&sh.drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -1608,6 +1590,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     __syncthreads();
     tc_after();
     const uint32_t tmem = sh.tmem;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for split_kernel
     const int P = a.c.block, blocks = kTile / P, log_p = 31 - __clz(P);
     int b = range.b;
     long long at = range.begin, skip = range.skip;
@@ -1625,8 +1608,9 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         const int x1 = (int)min((long long)all.count, x0 + (range.end - at));
         for (int rt = 0; rt < a.row_tiles; ++rt) {
             const Unit u = row_unit<NT>(a, b, rt);
-            if (u.count == 0)
-                continue;
+            const int low = all.tile(x0), high = all.tile(x1 - 1);
+            if (u.count == 0 || !(low < u.head_tiles || (high >= u.low && low < u.low + u.count - u.head_tiles)))
+                continue;  // no tile of the stretch
             if (wid == 8) {
                 // ---------------- producer ----------------
                 for (int x = x0; x < x1; ++x) {
@@ -1689,22 +1673,23 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                 rows_of.rt = rt;
                 named_barrier<256>(3);
                 const bool tree = a.f.parent && (long long)(all.tile(x1 - 1) + 1) * kTile > u.first;
-                load_queries<D, NT, 256>(a, u, b, h, rt, tree, sh.q[0], sh.col, tid);
+                describe_columns<NT, 256>(a, u, b, h, rt, tree, sh.col, tid);
                 if (tid < NT) {
                     const int r = rt * NT + tid, i = r / a.group;
                     const float lse =
                         i <= u.i1 ? a.lse_in[((size_t)b * a.n + i) * a.heads + h * a.group + r % a.group] : -INFINITY;
                     sh.col.base[tid] = lse == -INFINITY ? INFINITY : lse * kLog2e;
                 }
-                proxy_fence();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sh.q_ready);
+                if (tid == 0) {
+                    mbar_expect(&sh.q_ready, kQueryBytes<D, NT>);
+                    load_queries<D, NT>(a, b, h, rt, sh.q[0], sh.col, &sh.q_ready);
+                }
                 named_barrier<256>(3);
                 if (tree) {
                     mark_kin<NT, 256>(sh.col, tid);
                     named_barrier<256>(3);
                 }
+                mbar_wait(&sh.q_ready, seg++ & 1, dead);
                 for (int x = x0; x < x1; ++x) {
                     const int tile = all.tile(x);
                     if (!covers(u, tile))
@@ -1808,7 +1793,7 @@ template <int D, int NT> __global__ void __launch_bounds__(128) join_kernel(cons
 
 // The kernels of one head size, by columns per row tile (16, 32, 48 or 64).
 struct Kernels {
-    const void *attend[4][2], *join[4], *weigh[4][2];  // [..][a cap or a bias]
+    const void *split, *attend[4][2], *join[4], *weigh[4][2];  // [..][a cap or a bias]
     int attend_smem[4], attend_threads[4], weigh_smem[4];
 };
 const Kernels &kernels_d64();
@@ -1830,6 +1815,7 @@ template <int D, int NT> void fill(Kernels &k, int i)
 template <int D> Kernels all_kernels()
 {
     Kernels k{};
+    k.split = (const void *)split_kernel<D>;
     fill<D, 16>(k, 0);
     fill<D, 32>(k, 1);
     fill<D, 48>(k, 2);

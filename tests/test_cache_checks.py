@@ -62,10 +62,10 @@ def attend(lib, c, **o):
 
 
 def weigh(lib, c, **o):
-    a = dict(lengths=FAKE, q=FAKE, n=4, heads=4, form=form(), lse=FAKE, weights=FAKE)
+    a = dict(lengths=FAKE, q=FAKE, n=4, heads=4, form=form(), lse=FAKE, weights=FAKE, work=FAKE, size=1 << 40)
     a.update(o)
     return lib.spec_cache_weigh(ctypes.byref(c), a["lengths"], a["q"], three, a["n"], a["heads"], a["form"], a["lse"],
-                                a["weights"], None, None)
+                                a["weights"], a["work"], a["size"], None, None)
 
 
 def evict(lib, c, **o):
@@ -117,6 +117,7 @@ def test_attend_only(lib, over, code):
 
 def test_weigh_only(lib):
     assert weigh(lib, make(), lse=0) == 1 and weigh(lib, make(), weights=FAKE + 2) == 1
+    assert weigh(lib, make(), work=0) == 1 and weigh(lib, make(), work=FAKE + 8) == 1
 
 
 @pytest.mark.parametrize("over,code", [
