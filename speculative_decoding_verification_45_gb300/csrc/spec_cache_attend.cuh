@@ -27,6 +27,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "spec_cache.cuh"
 
 namespace specc {
@@ -1751,44 +1753,53 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Shared::kAlloc));
 }
 
-// Joins the parts of units that several CTAs worked on: CTA (c, y) joins rows
-// [y * kJoinRows, ...) of the unit that ended in CTA c of attend_kernel.
+// Joins the parts of units that several CTAs worked on: a warp joins one row of
+// the unit that ended in CTA blockIdx.x of attend_kernel, its lanes D / 32
+// dimensions each (or, for the parts' totals, a part each).
 constexpr int kJoinRows = 4;
 
-template <int D, int NT> __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttendArgs a)
+template <int D, int NT> __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const __grid_constant__ AttendArgs a)
 {
+    using Vec = typename std::conditional<D == 128, float4, float2>::type;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int c = blockIdx.x;
-    const int4 join = a.joins[c];
+    const int last = blockIdx.x, lane = threadIdx.x & 31;
+    const int4 join = a.joins[last];
     if (join.x < 0)
         return;
-    constexpr int kAtOnce = 128 / D;  // rows
-    const int d = threadIdx.x % D, rows = a.n * a.group;
-    for (int k = threadIdx.x / D; k < kJoinRows; k += kAtOnce) {
-        const int col = blockIdx.y * kJoinRows + k, r = join.w * NT + col;
-        if (r >= rows)
-            return;
-        float top = -INFINITY;
-        for (int p = join.x; p <= c; ++p) {
-            const float2 s = a.part_sum[(2ll * p + (p == join.x)) * NT + col];
-            if (!(s.x == 0.0f))
-                top = fmaxf(top, s.y);
-        }
-        float total = 0.0f, o = 0.0f;
-#pragma unroll 4
-        for (int p = join.x; p <= c; ++p) {
-            const long long at = (2ll * p + (p == join.x)) * NT + col;
-            const float2 s = a.part_sum[at];
-            const float w = s.x == 0.0f ? 0.0f : exp2f(s.y - top), y = a.part[at * D + d];
-            total += s.x * w;
-            o += s.x == 0.0f ? 0.0f : y * w;
-        }
-        const size_t row = ((size_t)join.y * a.n + r / a.group) * a.heads + join.z * a.group + r % a.group;
-        const bool live = !(total == 0.0f);
-        a.out[row * D + d] = __float2bfloat16(live ? o / total : 0.0f);
-        if (d == 0)
-            a.lse[row] = live ? (top + log2f(total)) * 0.6931471805599453f : -INFINITY;
+    const int col = blockIdx.y * kJoinRows + (threadIdx.x >> 5), r = join.w * NT + col;
+    if (r >= a.n * a.group)
+        return;
+    const auto slot = [&](int p) { return (2ll * p + (p == join.x)) * NT + col; };
+    float top = -INFINITY;
+    for (int p = join.x + lane; p <= last; p += 32) {
+        const float2 s = a.part_sum[slot(p)];
+        if (!(s.x == 0.0f))
+            top = fmaxf(top, s.y);
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float total = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int p = join.x; p <= last; ++p) {
+        const float2 s = a.part_sum[slot(p)];
+        const Vec y = *(const Vec *)(a.part + slot(p) * D + lane * (D / 32));
+        const bool some = !(s.x == 0.0f);
+        const float w = some ? exp2f(s.y - top) : 0.0f;
+        total += s.x * w;
+        const float *v = (const float *)&y;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+            o[k] += some ? v[k] * w : 0.0f;
+    }
+    const size_t row = ((size_t)join.y * a.n + r / a.group) * a.heads + join.z * a.group + r % a.group;
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    __nv_bfloat162 *out = (__nv_bfloat162 *)(a.out + row * D + lane * (D / 32));
+#pragma unroll
+    for (int k = 0; k < D / 32; k += 2)
+        out[k / 2] = total == 0.0f ? __floats2bfloat162_rn(0.0f, 0.0f) : __floats2bfloat162_rn(o[k] * inv, o[k + 1] * inv);
+    if (lane == 0)
+        a.lse[row] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
 }
 
 // The kernels of one head size, by columns per row tile (16, 32, 48 or 64).

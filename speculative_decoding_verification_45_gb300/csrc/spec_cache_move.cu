@@ -1,6 +1,8 @@
 // spec_cache_move.cu -- writing tokens into the 8-bit key/value cache and
 // moving the kept ones out of it (spec_cache_append, spec_cache_evict).
 
+#include <algorithm>
+
 #include "spec_cache.cuh"
 
 using namespace specc;
@@ -12,9 +14,9 @@ namespace {
 // ===========================================================================
 // One unit is one block of one sequence, head and side (keys or values): its
 // scale depends on nothing else.  The unit's new values are read once, kept in
-// registers as 8-value chunks while their largest magnitude is found, and
-// written as codes.  T threads serve a unit: a warp for the few tokens of a
-// round, 256 threads for a prompt's whole blocks.
+// registers as 8-value chunks (kChunks a thread) while their largest magnitude is
+// found, and written as codes.  T threads serve a unit: a warp for the few tokens
+// of a round, 256 threads for a prompt's whole blocks.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendSmall = 16;  // new tokens up to which a warp's registers hold a unit (8 chunks a lane)
 
@@ -65,11 +67,10 @@ template <> struct Chunk<float> {
     }
 };
 
-template <typename X, int T>
+template <typename X, int T, int kChunks>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a)
 {
     constexpr int kUnits = kAppendThreads / T;  // units of a CTA
-    constexpr int kChunks = 8;                  // at most: 128 tokens x 128 / 8 / 256, or 16 x 128 / 8 / 32
     const spec_cache &c = a.c;
     const int sub = threadIdx.x / T, t = threadIdx.x % T;
     const long long units = (long long)c.batch * a.blocks * c.kv_heads * 2;
@@ -185,8 +186,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
 // Two kernels: one CTA per (sequence, head) finds the kept indices, then one
 // CTA per block of kept tokens moves them.  Sources and destinations share no
 // page, so the moves need no order.
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kDigits = 2048;  // 11 bits at a time: 3 rounds
 constexpr int kMoveThreads = 256;
 
 struct EvictArgs {
@@ -208,25 +210,26 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ uint32_t key_at(const EvictArgs &a, int b, int h, int j)
+__device__ __forceinline__ uint32_t key_at(const EvictArgs &a, int b, int h, int j, int log_p)
 {
-    const int page = page_of(a.c, b, j / a.c.block);
-    return page < 0 ? 0u : weight_key(a.weights[((size_t)page * a.c.kv_heads + h) * a.c.block + j % a.c.block]);
+    const int page = page_of(a.c, b, j >> log_p);
+    return page < 0 ? 0u : weight_key(a.weights[(((size_t)page * a.c.kv_heads + h) << log_p) + (j & ((1 << log_p) - 1))]);
 }
 
-// The (keep - recent)-th largest key is found one byte at a time from the top
-// (a histogram of the keys that share the bytes found so far); then each warp
-// counts its stretch of tokens above the key and equal to it, and a second walk
-// writes the indices in order.  The keys are kept in shared memory where they
-// fit (`staged`), else read again from L2.
+// The (keep - recent)-th largest key is found 11 bits at a time from the top (a
+// histogram of the keys that share the bits found so far); then each warp counts
+// its stretch of tokens above the key and equal to it, and a second walk writes
+// the indices in order.  The keys are kept in shared memory where they fit
+// (`staged`), else read again from L2.  Keys equal to zero's, the one value that
+// repeats in earnest (tokens that no query looked at), are counted by ballot.
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs a, int staged)
 {
     extern __shared__ uint32_t keys[];
-    __shared__ uint32_t hist[256];
+    __shared__ uint32_t hist[kDigits], warp_sum[kSelectWarps];
     __shared__ int count[2][kSelectWarps];
     __shared__ uint32_t found, left;
     const spec_cache &c = a.c;
-    const int h = blockIdx.x % c.kv_heads, b = blockIdx.x / c.kv_heads;
+    const int h = blockIdx.x % c.kv_heads, b = blockIdx.x / c.kv_heads, log_p = 31 - __clz(c.block);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const Seq s = sequence(c, a.lengths, nullptr, 0, b, true);
     if (tid == 0 && h == 0) {
@@ -247,80 +250,78 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
         index[want + i] = cand + i;
     if (want == 0)
         return;
-    uint32_t prefix = 0;
-    uint32_t need = (uint32_t)want;  // rank of the wanted key among those that share `prefix`
-    for (int byte = 3; byte >= 0; --byte) {
-        if (tid < 256)
-            hist[tid] = 0;
+    if (staged) {
+#pragma unroll 4
+        for (int j = tid; j < cand; j += kSelectThreads)
+            keys[j] = key_at(a, b, h, j, log_p);
+    }
+    const uint32_t zero = 0x80000000u;
+    uint32_t prefix = 0, need = (uint32_t)want;  // rank of the wanted key among those that share `prefix`
+    int shift = 21;
+    for (int round = 0; round < 3; ++round) {
+        const int bits = round < 2 ? 11 : 10;
+        for (int i = tid; i < kDigits; i += kSelectThreads)
+            hist[i] = 0;
         __syncthreads();
         for (int j0 = 0; j0 < cand; j0 += kSelectThreads) {
             const int j = j0 + tid;
             bool in = j < cand;
-            uint32_t key = 0;
-            if (in) {
-                key = (staged && byte < 3) ? keys[j] : key_at(a, b, h, j);
-                if (staged && byte == 3)
-                    keys[j] = key;
-                in = byte == 3 || (key >> (8 * byte + 8)) == prefix;
-            }
-            // lanes with the same digit add once
-            const uint32_t digit = in ? (key >> (8 * byte)) & 255u : 256u;
-            const uint32_t same = __match_any_sync(0xffffffffu, digit);
-            if (in && lane == __ffs(same) - 1)
-                atomicAdd(&hist[digit], (uint32_t)__popc(same));
+            const uint32_t key = in ? (staged ? keys[j] : key_at(a, b, h, j, log_p)) : 0;
+            in = in && (round == 0 || (key >> (shift + bits)) == prefix);
+            const uint32_t digit = (key >> shift) & ((1u << bits) - 1);
+            const uint32_t none = __ballot_sync(0xffffffffu, in && key == zero);
+            if (in && key != zero)
+                atomicAdd(&hist[digit], 1u);
+            else if (in && lane == __ffs(none) - 1)
+                atomicAdd(&hist[digit], (uint32_t)__popc(none));
         }
         __syncthreads();
-        if (wid == 0) {  // the digit where the count from the top reaches `need`
-            uint32_t mine[8], sum = 0;
+        // the digit where the count from the top reaches `need`: two bins a thread, top first
+        const uint32_t upper = hist[kDigits - 1 - 2 * tid], lower = hist[kDigits - 2 - 2 * tid];
+        uint32_t up = upper + lower;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                mine[i] = hist[255 - (lane * 8 + i)];
-                sum += mine[i];
-            }
-            uint32_t before = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
-                before += lane >= o ? y : 0;
-            }
-            before -= sum;
-            if (before < need && need <= before + sum) {
-                int i = 0;
-                while (before + mine[i] < need)
-                    before += mine[i++];
-                found = 255 - (lane * 8 + i);
-                left = need - before;
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, up, o);
+            up += lane >= o ? y : 0;
+        }
+        if (lane == 31)
+            warp_sum[wid] = up;
+        __syncthreads();
+        uint32_t ahead = lane < wid ? warp_sum[lane] : 0;
+        ahead = __reduce_add_sync(0xffffffffu, ahead) + up - upper - lower;
+        if (ahead < need && need <= ahead + upper + lower) {
+            const bool second = need > ahead + upper;
+            found = kDigits - 1 - 2 * tid - second;
+            left = need - ahead - (second ? upper : 0);
         }
         __syncthreads();
-        prefix = prefix << 8 | found;
+        prefix = prefix << bits | found;
         need = left;
+        shift -= round == 0 ? 11 : 10;
     }
     // tokens above the key `prefix` are all kept, of those equal to it the first `need`
     const int each = ((cand + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
     const int lo = min(cand, wid * each), hi = min(cand, lo + each);
     int above = 0, equal = 0;
-    for (int j0 = lo; j0 < hi; j0 += 32) {
-        const int j = j0 + lane;
-        const uint32_t key = j < hi ? (staged ? keys[j] : key_at(a, b, h, j)) : 0;
-        above += __popc(__ballot_sync(0xffffffffu, j < hi && key > prefix));
-        equal += __popc(__ballot_sync(0xffffffffu, j < hi && key == prefix));
+    for (int j = lo + lane; j < hi; j += 32) {
+        const uint32_t key = staged ? keys[j] : key_at(a, b, h, j, log_p);
+        above += key > prefix;
+        equal += key == prefix;
     }
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
     if (lane == 0) {
         count[0][wid] = above;
         count[1][wid] = equal;
     }
     __syncthreads();
-    int at = 0, ties = 0;
-    for (int w = 0; w < wid; ++w) {
-        at += count[0][w];
-        ties += count[1][w];
-    }
+    const int at = __reduce_add_sync(0xffffffffu, lane < wid ? count[0][lane] : 0);
+    int ties = __reduce_add_sync(0xffffffffu, lane < wid ? count[1][lane] : 0);
     int out = at + min(ties, (int)need);  // kept tokens before this warp's stretch
     const uint32_t below = (1u << lane) - 1;
     for (int j0 = lo; j0 < hi; j0 += 32) {
         const int j = j0 + lane;
-        const uint32_t key = j < hi ? (staged ? keys[j] : key_at(a, b, h, j)) : 0;
+        const uint32_t key = j < hi ? (staged ? keys[j] : key_at(a, b, h, j, log_p)) : 0;
         const bool eq = j < hi && key == prefix;
         const uint32_t tie = __ballot_sync(0xffffffffu, eq);
         const bool take = (j < hi && key > prefix) || (eq && ties + __popc(tie & below) < (int)need);
@@ -379,38 +380,66 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
         scale[(size_t)to * c.kv_heads + h] = now[tid];
     }
     const int shift = c.dim == 64 ? 2 : 3;  // 16-byte chunks of a token
-    for (int q = tid; q < 2 * (n << shift); q += kMoveThreads) {
-        const int side = q >= (n << shift);
-        const int r = q - side * (n << shift), i = r >> shift, d = (r & ((1 << shift) - 1)) * 16;
-        const int64_t *cs = side ? c.v_stride : c.k_stride;
-        uint8_t *base = (uint8_t *)(side ? c.v : c.k) + (size_t)h * cs[1] + d;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (from[i] >= 0) {
-            w = *(const uint4 *)(base + (size_t)from[i] * cs[0] + (size_t)row[i] * cs[2]);
-            if (had[side][i] != now[side]) {
+    const int todo = 2 * (n << shift);
+    constexpr int kAtOnce = 4;  // loads in flight
+    for (int q0 = tid; q0 < todo; q0 += kAtOnce * kMoveThreads) {
+        uint4 w[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int q = q0 + k * kMoveThreads, side = q >= (n << shift), r = q - side * (n << shift), i = r >> shift;
+            w[k] = make_uint4(0, 0, 0, 0);
+            if (q < todo && from[i] >= 0) {
+                const int64_t *cs = side ? c.v_stride : c.k_stride;
+                w[k] = *(const uint4 *)((const uint8_t *)(side ? c.v : c.k) + (size_t)from[i] * cs[0] + (size_t)h * cs[1] +
+                                        (size_t)row[i] * cs[2] + (r & ((1 << shift) - 1)) * 16);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int q = q0 + k * kMoveThreads, side = q >= (n << shift), r = q - side * (n << shift), i = r >> shift;
+            if (q >= todo)
+                break;
+            if (from[i] >= 0 && had[side][i] != now[side]) {
                 const float f = had[side][i] / now[side];
-                uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 lo = decode2((uint16_t)x[e], c.code), hi = decode2((uint16_t)(x[e] >> 16), c.code);
                     x[e] = (uint32_t)encode2(lo.x * f, lo.y * f, c.code) |
                            (uint32_t)encode2(hi.x * f, hi.y * f, c.code) << 16;
                 }
-                w = make_uint4(x[0], x[1], x[2], x[3]);
+                w[k] = make_uint4(x[0], x[1], x[2], x[3]);
             }
+            const int64_t *cs = side ? c.v_stride : c.k_stride;
+            *(uint4 *)((uint8_t *)(side ? c.v : c.k) + (size_t)to * cs[0] + (size_t)h * cs[1] + (size_t)i * cs[2] +
+                       (r & ((1 << shift) - 1)) * 16) = w[k];
         }
-        *(uint4 *)(base + (size_t)to * cs[0] + (size_t)i * cs[2]) = w;
     }
 }
 
-template <typename X, int T> spec_status run_append(const AppendArgs &a, cudaStream_t stream)
+template <typename X, int T, int kChunks> spec_status run_append(const AppendArgs &a, cudaStream_t stream)
 {
     const long long units = (long long)a.c.batch * a.blocks * a.c.kv_heads * 2;
     const long long ctas = (units + kAppendThreads / T - 1) / (kAppendThreads / T);
     if (ctas > INT_MAX)
         return SPEC_ERR_UNSUPPORTED;
-    append_kernel<X, T><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(a);
+    append_kernel<X, T, kChunks><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(a);
     return launched();
+}
+
+// Chunks a thread: as many as the unit's tokens (a block, or the new ones) need.  Fewer registers let more units
+// be in flight.
+template <typename X> spec_status choose_append(const AppendArgs &a, cudaStream_t s)
+{
+    const int chunks = a.c.dim / 8;
+    if (a.n <= kAppendSmall) {
+        const int each = (std::min(a.n, a.c.block) * chunks + 31) / 32;
+        return each <= 2 ? run_append<X, 32, 2>(a, s) : each <= 4 ? run_append<X, 32, 4>(a, s) : run_append<X, 32, 8>(a, s);
+    }
+    const int each = (a.c.block * chunks + kAppendThreads - 1) / kAppendThreads;
+    return each <= 2   ? run_append<X, kAppendThreads, 2>(a, s)
+           : each <= 4 ? run_append<X, kAppendThreads, 4>(a, s)
+                       : run_append<X, kAppendThreads, 8>(a, s);
 }
 
 }  // namespace
@@ -450,9 +479,7 @@ spec_status spec_cache_append(const spec_cache *cache, const int32_t *lengths, c
     a.blocks = (n + cache->block - 2) / cache->block + 1;
     a.status = status;
     const cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == SPEC_F32)
-        return n <= kAppendSmall ? run_append<float, 32>(a, s) : run_append<float, kAppendThreads>(a, s);
-    return n <= kAppendSmall ? run_append<__nv_bfloat16, 32>(a, s) : run_append<__nv_bfloat16, kAppendThreads>(a, s);
+    return dtype == SPEC_F32 ? choose_append<float>(a, s) : choose_append<__nv_bfloat16>(a, s);
 }
 
 spec_status spec_cache_evict(const spec_cache *cache, const int32_t *lengths, float *weights, int keep, int recent,
@@ -480,7 +507,7 @@ spec_status spec_cache_evict(const spec_cache *cache, const int32_t *lengths, fl
     const long long room = (long long)cache->max_blocks * cache->block;
     const long long bytes = room * 4;
     const int staged = bytes <= 200 * 1024;
-    if (staged && bytes > 46 * 1024 &&
+    if (staged && bytes > 36 * 1024 &&
         cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess) {
         cudaGetLastError();
         return SPEC_ERR_CUDA;
