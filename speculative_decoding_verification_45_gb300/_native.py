@@ -99,6 +99,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 def load() -> ctypes.CDLL:
     """Load the built library; raises if it has not been built (no fallback exists)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -14,6 +14,7 @@ error behaviour.  All tensors are CUDA tensors on the cache's device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import NamedTuple
 
@@ -62,32 +63,29 @@ def _check(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
-def _cuda(t, name):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-
-
 def _strides(t, name, multiple):
     """Strides of all but the last dimension, which has to be dense (sizes of one do not matter)."""
-    shape, stride = t.shape, t.stride()
-    if shape[-1] > 1 and stride[-1] != 1:
+    *st, last = t.stride()
+    if last == 1 and all(st) and not any(x % multiple for x in st):
+        return st
+    if last != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be dense")
-    got = [st if n > 1 else multiple for n, st in zip(shape[:-1], stride[:-1])]
-    for st in got:
-        if st % multiple:
-            raise ValueError(f"{name}: strides must be multiples of {multiple}, got {tuple(stride)}")
-    return got
+    st = [x if n > 1 else multiple for n, x in zip(t.shape[:-1], st)]
+    if any(x % multiple for x in st):
+        raise ValueError(f"{name}: strides must be multiples of {multiple}, got {tuple(t.stride())}")
+    return st
 
 
 def _describe(cache, block_table, lengths):
-    """The spec_cache of these tensors, checked."""
-    k, v = cache.k, cache.v
+    """The spec_cache of these tensors, checked; their device; the lengths' address."""
+    k, v, k_scale, v_scale, positions = cache
     if k.dim() != 4:
         raise ValueError("cache.k must be a [num_pages, kv_heads, block, dim] tensor")
     code = _CODES.get(k.dtype)
     if code is None or v.dtype != k.dtype:
         raise TypeError(f"cache.k and cache.v must both be float8_e4m3fn or float8_e5m2, got {k.dtype} and {v.dtype}")
-    _cuda(k, "cache.k")
+    if not k.is_cuda:
+        raise ValueError("cache.k must be a CUDA tensor")
     dev, shape = k.device, k.shape
     if v.shape != shape or v.device != dev:
         raise ValueError(f"cache.v: expected shape {tuple(shape)} on {dev}, got {tuple(v.shape)} on {v.device}")
@@ -97,19 +95,15 @@ def _describe(cache, block_table, lengths):
     if block_table.dim() != 2:
         raise ValueError("block_table must be a [batch, blocks] tensor")
     batch, blocks = block_table.shape
-    c = _native.Cache()
-    c.k, c.v = k.data_ptr(), v.data_ptr()
-    c.k_scale = _check(cache.k_scale, "cache.k_scale", torch.float32, (pages, heads), dev)
-    c.v_scale = _check(cache.v_scale, "cache.v_scale", torch.float32, (pages, heads), dev)
-    if cache.positions is not None:
-        c.positions = _check(cache.positions, "cache.positions", torch.int32, (pages, heads, block), dev)
-    if block_table.dtype != torch.int32 or block_table.device != dev or (blocks > 1 and block_table.stride(1) != 1):
+    step, dense = block_table.stride()
+    if block_table.dtype != torch.int32 or block_table.device != dev or (blocks > 1 and dense != 1):
         raise ValueError(f"block_table must be int32 on {dev} with dense rows")
-    c.block_table = block_table.data_ptr()
-    c.table_stride = block_table.stride(0) if batch > 1 else blocks
-    c.k_stride[:] = _strides(k, "cache.k", 16)
-    c.v_stride[:] = _strides(v, "cache.v", 16)
-    c.batch, c.max_blocks, c.num_pages, c.kv_heads, c.block, c.dim, c.code = batch, blocks, pages, heads, block, dim, code
+    c = _native.Cache(
+        k.data_ptr(), v.data_ptr(), _check(k_scale, "cache.k_scale", torch.float32, (pages, heads), dev),
+        _check(v_scale, "cache.v_scale", torch.float32, (pages, heads), dev),
+        _optional(positions, "cache.positions", torch.int32, (pages, heads, block), dev), block_table.data_ptr(),
+        tuple(_strides(k, "cache.k", 16)), tuple(_strides(v, "cache.v", 16)), step if batch > 1 else blocks, batch,
+        blocks, pages, heads, block, dim, code)
     return c, dev, _check(lengths, "lengths", torch.int32, (batch,), dev)
 
 
@@ -126,14 +120,23 @@ def _status(t, device):
 
 
 def _stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
-def _output(t, name, dtype, shape, device):
-    if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-        return t, t.data_ptr()
-    return t, _check(t, name, dtype, shape, device)
+def _new(shape, dtype, device, stream):
+    """A new tensor whose block belongs to the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _output(t, name, dtype, shape, device, stream):
+    """An output that the caller gave, or a new one; and its address."""
+    if t is not None:
+        return t, _check(t, name, dtype, shape, device)
+    t = _new(shape, dtype, device, stream)
+    return t, t.data_ptr()
 
 
 def cache_append(cache, block_table, lengths, k, v, num_new=None, positions=None, status=None, stream=None):
@@ -189,16 +192,23 @@ def _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent):
     return f, n, heads, (ctypes.c_int64 * 3)(*_strides(q, "q", 8))
 
 
-def _workspace(lib, c, n, heads, dev, stream):
-    """A workspace for one call, and its size; the block belongs to the stream that uses it."""
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(batch, kv_heads, block, dim, n, heads, device):
+    """Bytes that spec_cache_attend_workspace asks for; they follow from these sizes and the device."""
+    fake = 16  # an address for the check of the description; nothing is read
+    c = _native.Cache(fake, fake, fake, fake, None, fake, (16,) * 3, (16,) * 3, 1, batch, 1, 1, kv_heads, block, dim, 0)
     need = ctypes.c_int64()
-    rc = lib.spec_cache_attend_workspace(ctypes.byref(c), n, heads, ctypes.byref(need))
+    with torch.cuda.device(device):
+        rc = _native.load().spec_cache_attend_workspace(ctypes.byref(c), n, heads, ctypes.byref(need))
     if rc:
         _fail(rc, "spec_cache_attend_workspace")
-    if stream is None:
-        return torch.empty(need.value, dtype=torch.uint8, device=dev), need.value
-    with torch.cuda.stream(stream):
-        return torch.empty(need.value, dtype=torch.uint8, device=dev), need.value
+    return need.value
+
+
+def _workspace(c, n, heads, dev, stream):
+    """A workspace for one call, and its size."""
+    size = _workspace_bytes(c.batch, c.kv_heads, c.block, c.dim, n, heads, dev.index)
+    return _new(size, torch.uint8, dev, stream), size
 
 
 def cache_attend(q, cache, block_table, lengths, num_new=None, scale=None, softcap=0.0, slopes=None, window=0,
@@ -221,11 +231,10 @@ def cache_attend(q, cache, block_table, lengths, num_new=None, scale=None, softc
     """
     c, dev, len_ptr = _describe(cache, block_table, lengths)
     f, n, heads, stride = _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent)
-    out, out_ptr = _output(out, "out", torch.bfloat16, (c.batch, n, heads, c.dim), dev)
-    lse, lse_ptr = _output(lse, "lse", torch.float32, (c.batch, n, heads), dev)
-    lib = _native.load()
-    work, size = _workspace(lib, c, n, heads, dev, stream)
-    rc = lib.spec_cache_attend(ctypes.byref(c), len_ptr, q.data_ptr(), stride, n, heads, ctypes.byref(f), out_ptr,
+    out, out_ptr = _output(out, "out", torch.bfloat16, (c.batch, n, heads, c.dim), dev, stream)
+    lse, lse_ptr = _output(lse, "lse", torch.float32, (c.batch, n, heads), dev, stream)
+    work, size = _workspace(c, n, heads, dev, stream)
+    rc = _native.load().spec_cache_attend(ctypes.byref(c), len_ptr, q.data_ptr(), stride, n, heads, ctypes.byref(f), out_ptr,
                                lse_ptr, work.data_ptr(), size, _status(status, dev), _stream(stream, dev))
     if rc:
         _fail(rc, "spec_cache_attend")
@@ -244,9 +253,8 @@ def cache_weigh(q, cache, block_table, lengths, lse, weights, num_new=None, scal
     f, n, heads, stride = _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent)
     lse_ptr = _check(lse, "lse", torch.float32, (c.batch, n, heads), dev)
     w_ptr = _check(weights, "weights", torch.float32, (c.num_pages, c.kv_heads, c.block), dev)
-    lib = _native.load()
-    work, size = _workspace(lib, c, n, heads, dev, stream)
-    rc = lib.spec_cache_weigh(ctypes.byref(c), len_ptr, q.data_ptr(), stride, n, heads, ctypes.byref(f), lse_ptr, w_ptr,
+    work, size = _workspace(c, n, heads, dev, stream)
+    rc = _native.load().spec_cache_weigh(ctypes.byref(c), len_ptr, q.data_ptr(), stride, n, heads, ctypes.byref(f), lse_ptr, w_ptr,
                               work.data_ptr(), size, _status(status, dev), _stream(stream, dev))
     if rc:
         _fail(rc, "spec_cache_weigh")
@@ -273,8 +281,8 @@ def cache_evict(cache, block_table, lengths, weights, keep: int, recent: int, ou
     if out_table.dtype != torch.int32 or out_table.device != dev or (out_table.shape[1] > 1 and out_table.stride(1) != 1):
         raise ValueError(f"out_table must be int32 on {dev} with dense rows")
     w_ptr = _check(weights, "weights", torch.float32, (c.num_pages, c.kv_heads, c.block), dev)
-    out_lengths, l_ptr = _output(out_lengths, "out_lengths", torch.int32, (c.batch,), dev)
-    out_index, i_ptr = _output(out_index, "out_index", torch.int32, (c.batch, c.kv_heads, keep), dev)
+    out_lengths, l_ptr = _output(out_lengths, "out_lengths", torch.int32, (c.batch,), dev, stream)
+    out_index, i_ptr = _output(out_index, "out_index", torch.int32, (c.batch, c.kv_heads, keep), dev, stream)
     rc = _native.load().spec_cache_evict(
         ctypes.byref(c), len_ptr, w_ptr, keep, recent, out_table.data_ptr(),
         out_table.stride(0) if c.batch > 1 else out_table.shape[1], l_ptr, i_ptr, _status(status, dev),

@@ -241,9 +241,10 @@ spec_status spec_cache_attend(const spec_cache *cache, const int32_t *lengths, c
     void *args[] = {&a, &kmap, &vmap}, *join_args[] = {&a};
     st = launch_behind(k.attend[shape.index][has_form(form)], dim3(sms), k.attend_threads[shape.index],
                        (size_t)k.attend_smem[shape.index], args, (cudaStream_t)stream);
-    return st != SPEC_OK ? st
-                         : launch_behind(k.join[shape.index], dim3(sms, shape.nt / kJoinRows), 128, 0, join_args,
-                                         (cudaStream_t)stream);
+    if (st != SPEC_OK || (long long)cache->max_blocks * cache->block <= kTile)
+        return st;  // units of one tile are never in parts
+    return launch_behind(k.join[shape.index], dim3(sms, shape.nt / kJoinRows), 32 * kJoinRows, 0, join_args,
+                         (cudaStream_t)stream);
 }
 
 spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, const void *q,
