@@ -973,13 +973,25 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             if (tiles == 0)
                 break;
             const int32_t *table = a.c.block_table + (size_t)u.b * a.c.table_stride;
-            const auto page_at = [&](int x) {
-                const int blk = u.tile(x) * blocks + lane;
-                return lane < blocks && (long long)blk * P < u.len ? table[blk] : -2;
+            // the table's entries 32 at a time, the next 32 on their way: a tile's entries asked for one tile ahead came
+            // later than the tile was due
+            const int batch = 32 / blocks;  // tiles
+            const auto pages_from = [&](int x) {
+                const int k = x + lane / blocks;
+                if (k >= tiles)
+                    return -2;
+                const int blk = u.tile(k) * blocks + (lane & (blocks - 1));
+                return (long long)blk * P < u.len ? table[blk] : -2;
             };
-            int page = page_at(0);
+            int pages = 0, more = pages_from(0);
             for (int x = 0; x < tiles; ++x) {
-                const int next = x + 1 < tiles ? page_at(x + 1) : -2;
+                const int at_x = x & (batch - 1);
+                if (at_x == 0) {
+                    pages = more;
+                    more = pages_from(x + batch);
+                }
+                const int got = __shfl_sync(0xffffffffu, pages, (at_x * blocks + lane) & 31);
+                const int page = lane < blocks ? got : -2;
                 const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
                 if (page != -2 && !ok)
                     report(a.status, SPEC_STATUS_BAD_PAGE);
@@ -1013,7 +1025,6 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     copies_arrive(&sh.v_full[vs]);
                     ++issued;
                 }
-                page = next;
                 if (++ks == KS) {
                     ks = 0;
                     k_phase ^= 1;
