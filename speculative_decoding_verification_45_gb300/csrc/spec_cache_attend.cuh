@@ -779,29 +779,45 @@ __device__ __forceinline__ float power2(int e)
     return e < -126 ? 0.0f : __uint_as_float((uint32_t)(min(e, 127) + 127) << 23);
 }
 
-__device__ __forceinline__ uint64_t low_bits(long long n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
-
-// The columns whose queries see token j: an interval of the rows in order, or the bits of a tree.
-template <int NT>
-__device__ __forceinline__ uint64_t seen_by(const AttendArgs &a, const Segment &u, const Columns<NT> &col, int j)
+// A set of columns, one bit each.
+template <int NT> using Mask = typename std::conditional<NT <= 32, uint32_t, uint64_t>::type;
+template <int NT> __device__ __forceinline__ Mask<NT> low_bits(int n)
 {
-    const long long t = (long long)j - u.first, r0 = (long long)u.rt * NT;
-    const uint64_t rows = low_bits(min((long long)(u.i1 + 1) * a.group - r0, (long long)NT));
-    if (j < u.prefix)
+    return n <= 0 ? 0 : n >= NT ? ~Mask<NT>(0) >> (8 * (int)sizeof(Mask<NT>) - NT) : (Mask<NT>(1) << n) - 1;
+}
+
+// Which columns ask, and where they lie among the rows of their key head.
+struct Askers {
+    int first, prefix;  // of the sequence
+    int i1, r0, group;  // last query, row of column 0, rows a query
+};
+template <int NT> __device__ __forceinline__ Mask<NT> all_columns(const Askers &k) { return low_bits<NT>((k.i1 + 1) * k.group - k.r0); }
+
+// The columns whose queries see token j: an interval of the rows in order (row r asks from query r / group, which
+// sees up to itself), or the bits of a tree.
+template <int NT>
+__device__ __forceinline__ Mask<NT> seen_by(const AttendArgs &a, const Askers &k, const Columns<NT> &col, int j)
+{
+    const Mask<NT> rows = all_columns<NT>(k);
+    if (j < k.prefix)
         return rows;
-    uint64_t see = rows;
+    const int t = j - k.first;  // its own query, if it has one
+    if (t > k.i1)
+        return 0;
+    Mask<NT> see = rows;
     if (t >= 0) {
         if (a.f.parent) {
             see = 0;
+#pragma unroll 1
             for (int c = 0; c < NT; ++c)
-                see |= (uint64_t)((col.kin[c][t >> 5] >> (t & 31)) & 1) << c;
+                see |= Mask<NT>((col.kin[c][t >> 5] >> (t & 31)) & 1) << c;
             see &= rows;
         } else {
-            see &= ~low_bits(t * a.group - r0);  // row r asks from query r / group, which sees up to itself
+            see &= ~low_bits<NT>(t * k.group - k.r0);
         }
     }
-    if (a.f.window > 0)
-        see &= low_bits((t + a.f.window) * a.group - r0);
+    if (a.f.window > 0 && (long long)t + a.f.window <= k.i1)
+        see &= low_bits<NT>((t + a.f.window) * k.group - k.r0);
     return see;
 }
 
@@ -1155,13 +1171,13 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                                       !(tile < u.seen_prefix || (tile >= u.seen_low && tile < u.seen_end));
                     const bool check = fresh || sh.unset[w][0] || (NT > 32 && sh.unset[w][1]);
                     bool closely = false;
-                    uint64_t see = ~0ull;
+                    Mask<NT> see = ~Mask<NT>(0);
                     float v_most = v_scale;
                     if (edge) {
                         const bool cached = j < u.len && ((came >> (t >> log_p)) & 1);
-                        see = cached ? seen_by<NT>(a, u, col, j) : 0;
-                        const bool all =
-                            see == low_bits(min((long long)(u.i1 + 1) * a.group - (long long)u.rt * NT, (long long)NT));
+                        const Askers askers{u.first, u.prefix, u.i1, u.rt * NT, a.group};
+                        see = cached ? seen_by<NT>(a, askers, col, j) : 0;
+                        const bool all = see == all_columns<NT>(askers);
                         uint4 *row = (uint4 *)(sh.v[vs] + t * D);
                         if (!cached) {  // nothing was loaded here
                             k_scale = 0.0f;
@@ -1175,7 +1191,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             // the weights of the rows that do see it become NaN
                             const uint32_t add = a.c.code == SPEC_E4M3 ? 0x01010101u : 0x04040404u;
                             uint32_t bad = 0;
-#pragma unroll 1
+#pragma unroll 4
                             for (int k = 0; k < D / 16; ++k) {
                                 const uint4 v = row[(k + t) & (D / 16 - 1)];
                                 bad |= ((v.x & 0x7f7f7f7fu) + add) | ((v.y & 0x7f7f7f7fu) + add) |
@@ -1404,7 +1420,6 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sh.sum_ready[seg & 1]);
-            named_barrier<128>(bar);  // base has been read: the next segment may reset it
         }
     } else {
         // ---------------- adding up ----------------
@@ -1679,11 +1694,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
             } else {
                 // ---------------- sums ----------------
                 const int w = wid >> 2, t = tid & 127;
-                Segment rows_of;
-                rows_of.first = u.first;
-                rows_of.prefix = u.prefix;
-                rows_of.i1 = u.i1;
-                rows_of.rt = rt;
+                const Askers askers{u.first, u.prefix, u.i1, rt * NT, a.group};
                 named_barrier<256>(3);
                 const bool tree = a.f.parent && (long long)(all.tile(x1 - 1) + 1) * kTile > u.first;
                 describe_columns<NT, 256>(a, u, b, h, rt, tree, sh.col, tid);
@@ -1716,7 +1727,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                         const bool cached = !edge || (j < u.len && ((came >> (t >> log_p)) & 1));
                         const float ks = cached ? info.k_scale[t >> log_p] : 0.0f;
                         const float pos = FORM && a.f.slopes ? (a.c.positions ? (float)info.pos[t] : (float)j) : 0.0f;
-                        const uint64_t see = edge && cached ? seen_by<NT>(a, rows_of, sh.col, j) : 0;
+                        const Mask<NT> see = edge && cached ? seen_by<NT>(a, askers, sh.col, j) : 0;
                         float *weight = a.weights + ((size_t)(cached ? page : 0) * a.c.kv_heads + h) * P + (t & (P - 1));
                         const float before = cached ? *weight : 0.0f;
                         mbar_wait(&sh.s_full[g & 1], (g >> 1) & 1, dead);
