@@ -143,12 +143,12 @@ int64_t split_bytes(const spec_cache &c, const Shape &s) { return (int64_t)c.bat
 // Points the arguments into the workspace and launches split_kernel.
 spec_status split_queries(AttendArgs &a, const Shape &s, void *workspace, const Kernels &k, cudaStream_t stream)
 {
-    const int64_t rows = (int64_t)a.c.batch * a.c.kv_heads * s.row_tiles * s.nt, each = 256 / (a.c.dim / 8);
-    if ((rows + each - 1) / each > INT_MAX)
+    const int64_t rows = (int64_t)a.c.batch * a.c.kv_heads * s.row_tiles * s.nt, each = 256 / (a.c.dim / 8) * kSplitRows;
+    if (rows > INT_MAX / 2)
         return SPEC_ERR_UNSUPPORTED;
     a.split = (uint8_t *)workspace;
     a.factor = (float *)(a.split + rows * 2 * a.c.dim);
-    int nt = s.nt;
+    uint32_t nt = (uint32_t)s.nt;
     void *args[] = {&a, &nt};
     if (cudaLaunchKernel(k.split, dim3((unsigned)((rows + each - 1) / each)), dim3(256), args, 0, stream) != cudaSuccess) {
         cudaGetLastError();

@@ -311,8 +311,7 @@ __device__ __forceinline__ bool interior(const AttendArgs &a, const Unit &u, int
            (a.f.window <= 0 || (long long)j0 > (long long)u.first + u.i1 - a.f.window);
 }
 
-// The tiles of all units in order, cut into equal stretches, one per CTA.  A
-// unit without a tile counts as one, so that its rows are written.
+// The tiles of all units in order, cut into equal stretches, one per CTA.
 struct Range {
     long long begin, end, each;
     int b;
@@ -403,53 +402,81 @@ __device__ __forceinline__ void split8(float x0, float x1, uint32_t &first, uint
 
 // Queries as two e4m3 terms, row tile by row tile, laid out as the products read
 // them from shared memory (128- or 64-byte swizzled), and the factor of each
-// row's accumulators.  A kernel of its own, D / 8 lanes a row: one warp of the
+// row's accumulators; rows of `out` without a query are written here too.  A kernel of its own, D / 8 lanes a row: one warp of the
 // attention kernel took 18,000 cycles for the 32 rows of a segment, as long as
 // their attention over 2,000 tokens.
-template <int D> __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ AttendArgs a, int nt)
+constexpr int kSplitRows = 4;  // rows a thread helps with, their loads in flight together
+
+template <int D> __global__ void __launch_bounds__(256) split_kernel(const __grid_constant__ AttendArgs a, uint32_t nt)
 {
-    constexpr int kLanes = D / 8;
-    const int d = threadIdx.x % kLanes;
-    const long long padded = (long long)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;  // row, row tiles filled up
-    const long long tile = padded / nt;
-    const int c = (int)(padded % nt), rt = (int)(tile % a.row_tiles);
-    const long long unit = tile / a.row_tiles;
-    const int h = (int)(unit % a.c.kv_heads), b = (int)min(unit / a.c.kv_heads, (long long)a.c.batch - 1);
-    const bool here = unit < (long long)a.c.batch * a.c.kv_heads;
-    const int r = rt * nt + c, i = r / a.group, g = r % a.group;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (here && i < a.n && i < (a.f.num_new ? a.f.num_new[b] : a.n))
-        w = __ldg((const uint4 *)(a.q + (size_t)b * a.q_stride[0] + (size_t)i * a.q_stride[1] +
-                                  (size_t)(h * a.group + g) * a.q_stride[2] + d * 8));
-    uint32_t x[4] = {w.x, w.y, w.z, w.w}, most = 0;  // pairs of bf16
+    constexpr uint32_t kLanes = D / 8, kStep = 256 / kLanes;
+    const uint32_t d = threadIdx.x % kLanes;
+    const uint32_t units = (uint32_t)(a.c.batch * a.c.kv_heads);
+    uint32_t tile[kSplitRows], c[kSplitRows];
+    int b[kSplitRows], i[kSplitRows], H[kSplitRows], m[kSplitRows];
+    uint4 w[kSplitRows];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int at = 16 * (e & 1);
-        const uint32_t y = (x[e >> 1] >> at) & 0x7fffu;
-        if (y >= 0x7f80u)  // infinities and NaN: NaN, and not the largest
-            x[e >> 1] |= 0x7fffu << at;
-        else
-            most = max(most, y);
+    for (int k = 0; k < kSplitRows; ++k) {
+        // the row, with row tiles filled up
+        const uint32_t padded = (blockIdx.x * kSplitRows + k) * kStep + threadIdx.x / kLanes;
+        tile[k] = padded / nt;
+        c[k] = padded - tile[k] * nt;
+        const uint32_t unit = tile[k] / (uint32_t)a.row_tiles, rt = tile[k] - unit * (uint32_t)a.row_tiles;
+        const uint32_t r = rt * nt + c[k], q = r / (uint32_t)a.group;
+        b[k] = (int)(unit / (uint32_t)a.c.kv_heads);
+        i[k] = (int)q;
+        H[k] = (int)((unit - b[k] * a.c.kv_heads) * a.group + (r - q * a.group));
+        m[k] = -1;
+        w[k] = make_uint4(0, 0, 0, 0);
+        if (unit < units) {
+            m[k] = sequence(a.c, a.lengths, a.f.num_new, a.n, b[k], true).m;
+            if (i[k] < a.n)
+                w[k] = __ldg((const uint4 *)(a.q + (size_t)b[k] * a.q_stride[0] + (size_t)i[k] * a.q_stride[1] +
+                                             (size_t)H[k] * a.q_stride[2] + d * 8));
+        }
     }
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1)
-        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     asm volatile("griddepcontrol.launch_dependents;");
-    // the row's power of two: its largest element becomes [128, 256)
-    const int ex = most ? max((int)(most >> 7), 16) - 7 : 127;  // biased
-    const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
-    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        split8(__uint_as_float(x[e] << 16) * inv, __uint_as_float(x[e] & 0xffff0000u) * inv, hi[e], lo[e]);
-    if (!here)
-        return;
-    uint8_t *to = a.split + tile * (2ll * nt * D) + c * D + ((d * 8) ^ (D == 128 ? (c & 7) << 4 : ((c >> 1) & 3) << 4));
-    *(uint2 *)to = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-    *(uint2 *)(to + (size_t)nt * D) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-    if (d == 0) {
-        const float f = __uint_as_float((uint32_t)ex << 23) * a.f.scale;
-        a.factor[tile * nt + c] = a.f.softcap > 0.0f ? f / a.f.softcap : f * kLog2e;
+    for (int k = 0; k < kSplitRows; ++k) {
+        if (i[k] >= m[k]) {
+            w[k] = make_uint4(0, 0, 0, 0);
+            if (m[k] >= 0 && i[k] < a.n && a.out) {  // a row without a query
+                const size_t row = ((size_t)b[k] * a.n + i[k]) * a.heads + H[k];
+                *(uint4 *)(a.out + row * D + d * 8) = w[k];
+                if (d == 0)
+                    a.lse[row] = -INFINITY;
+            }
+        }
+        uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w}, most = 0;  // pairs of bf16
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int at = 16 * (e & 1);
+            const uint32_t y = (x[e >> 1] >> at) & 0x7fffu;
+            if (y >= 0x7f80u)  // infinities and NaN: NaN, and not the largest
+                x[e >> 1] |= 0x7fffu << at;
+            else
+                most = max(most, y);
+        }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1)
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        // the row's power of two: its largest element becomes [128, 256)
+        const int ex = most ? max((int)(most >> 7), 16) - 7 : 127;  // biased
+        const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            split8(__uint_as_float(x[e] << 16) * inv, __uint_as_float(x[e] & 0xffff0000u) * inv, hi[e], lo[e]);
+        if (m[k] < 0)
+            continue;
+        uint8_t *to = a.split + (size_t)tile[k] * (2 * nt * D) + c[k] * D +
+                      ((d * 8) ^ (D == 128 ? (c[k] & 7) << 4 : ((c[k] >> 1) & 3) << 4));
+        *(uint2 *)to = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+        *(uint2 *)(to + nt * D) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        if (d == 0) {
+            const float f = __uint_as_float((uint32_t)ex << 23) * a.f.scale;
+            a.factor[(size_t)tile[k] * nt + c[k]] = a.f.softcap > 0.0f ? f / a.f.softcap : f * kLog2e;
+        }
     }
 }
 
@@ -466,7 +493,7 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, int b, int h, 
 }
 
 // The columns' other constants, by THREADS threads; ends without a barrier.
-template <int NT, int THREADS>
+template <int NT, int THREADS, typename Unit>
 __device__ __forceinline__ void describe_columns(const AttendArgs &a, const Unit &u, int b, int h, int rt, bool tree,
                                                  Columns<NT> &col, int t)
 {
@@ -602,10 +629,11 @@ __device__ __forceinline__ void load_tile(const AttendArgs &a, const CUtensorMap
     copies_arrive(full);
 }
 
-// The segments of a CTA's stretch: units, or parts of them, in order.
+// The segments of a CTA's stretch: units, or parts of them, in order; units
+// without a tile are passed over.  A whole warp walks.
 template <int NT> struct Walk {
     long long at, end;
-    int b, h, rt, x0, x1;  // tiles [x0, x1) of the unit's max(count, 1)
+    int b, h, rt, x0, x1;  // tiles [x0, x1) of the unit
     Unit u;
     __device__ __noinline__ void start(const AttendArgs &a, const Range &r)
     {
@@ -618,34 +646,43 @@ template <int NT> struct Walk {
         // the unit that holds the first tile
         long long skip = r.skip, each = 0;
         for (int k = 0; k < a.row_tiles; ++k)
-            each += max(row_unit<NT>(a, b, k).count, 1);
+            each += row_unit<NT>(a, b, k).count;
         h = (int)(skip / each);
         skip -= (long long)h * each;
         while (true) {
             u = row_unit<NT>(a, b, rt);
-            if (skip < max(u.count, 1))
+            if (skip < u.count)
                 break;
-            skip -= max(u.count, 1);
+            skip -= u.count;
             ++rt;
         }
         x0 = (int)skip;
-        x1 = (int)min((long long)max(u.count, 1), x0 + (end - at));
+        x1 = (int)min((long long)u.count, x0 + (end - at));
     }
     __device__ __noinline__ void next(const AttendArgs &a)
     {
         at += x1 - x0;
         if (at >= end)
             return;
-        x0 = 0;
-        if (++rt == a.row_tiles) {
+        if (++rt == a.row_tiles || rt * NT / a.group >= u.m) {
             rt = 0;
             if (++h == a.c.kv_heads) {
                 h = 0;
-                ++b;
+                // the next sequence with a query: there is one, since tiles are left
+                uint32_t some;
+                int b0 = b + 1 - 32;
+                do {
+                    b0 += 32;
+                    const int k = b0 + (int)(threadIdx.x & 31);
+                    some = __ballot_sync(0xffffffffu,
+                                         k < a.c.batch && sequence(a.c, a.lengths, a.f.num_new, a.n, k, true).m > 0);
+                } while (!some && b0 + 32 < a.c.batch);
+                b = b0 + max(__ffs(some) - 1, 0);
             }
         }
         u = row_unit<NT>(a, b, rt);
-        x1 = (int)min((long long)max(u.count, 1), end - at);
+        x0 = 0;
+        x1 = (int)min((long long)u.count, end - at);
     }
 };
 
@@ -694,7 +731,7 @@ template <int D, int NT> struct AttendShape {
 struct Segment {
     int tiles;  // 0: there is none left
     int x0, head_tiles, low;
-    int len, first, prefix, i1, b, h, rt;
+    int len, m, first, prefix, i1, b, h, rt;
     int seen_prefix, seen_low, seen_end;  // tiles that every query of the row tile sees whole: [0, ..) and [low, end)
     int whole, last;                      // the whole unit; its last part
     long long at;                         // first tile's place in the order of all
@@ -715,7 +752,7 @@ template <int D, int NT> struct AttendShared {
     alignas(1024) uint8_t q[2][2][NT * D];
     alignas(1024) uint8_t p[S::NW][2][kTile * NT];
     alignas(16) Columns<NT> col[2];
-    Segment seg[2];
+    Segment seg[4];
     alignas(16) StageInfo info[S::VS];
     alignas(16) float base[S::NW][NT];
     alignas(16) uint32_t scale[S::NW][4][NT];  // per tile: 2^k, as bits, that brings the largest weight to [224, 448]
@@ -728,7 +765,7 @@ template <int D, int NT> struct AttendShared {
     int is_set[S::NW][NT];                     // the row has a base
     int moved[S::NW][2], unset[S::NW][2];      // by 32 columns
     alignas(8) uint64_t k_full[S::KS], k_empty[S::KS], v_full[S::VS], v_empty[S::VS];
-    uint64_t s_full[S::NW], s_free[S::NW], p_ready[S::kRing], p_free[S::NW], o_full[2], o_free[2], seg_ready[2], q_ready[2];
+    uint64_t s_full[S::NW], s_free[S::NW], p_ready[S::kRing], p_free[S::NW], o_full[2], o_free[2], seg_ready[4], q_ready[2];
     uint64_t sum_ready[2], sum_free[2], drained[2];
     uint32_t tmem;
     int dead;
@@ -854,10 +891,11 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         }
         for (int i = 0; i < kRing; ++i)
             mbar_init(&sh.p_ready[i], 4);
+        for (int i = 0; i < 4; ++i)
+            mbar_init(&sh.seg_ready[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.o_full[i], 1);
             mbar_init(&sh.o_free[i], 4);
-            mbar_init(&sh.seg_ready[i], 1);
             mbar_init(&sh.q_ready[i], 1);
             mbar_init(&sh.sum_ready[i], 4 * NW);
             mbar_init(&sh.sum_free[i], 4);
@@ -883,7 +921,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
     const Range range = find_range<S::kThreads>(a, [&](int b) {
         long long each = 0;
         for (int k = 0; k < a.row_tiles; ++k)
-            each += max(row_unit<NT>(a, b, k).count, 1);
+            each += row_unit<NT>(a, b, k).count;
         if (blockIdx.x == 0 && !sequence(a.c, a.lengths, a.f.num_new, a.n, b, true).ok)
             report(a.status, SPEC_STATUS_BAD_LENGTH);
         return each * a.c.kv_heads;
@@ -898,64 +936,61 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         Walk<NT> walk;
         walk.start(a, range);
         asm volatile("griddepcontrol.wait;" ::: "memory");  // for split_kernel
+        uint32_t described = 0;
+        bool end = false;
 #pragma unroll 1
         for (uint32_t seg = 0;; ++seg) {
             const uint32_t i = seg & 1;
             mbar_wait(&sh.sum_free[i], ((seg >> 1) & 1) ^ 1, dead);  // the segment before the last is complete
-            const int rows = a.n * a.group;
-            const auto row_of = [&](const RowAt &at, int c) {
-                int q, g;
-                at.of(a, c, q, g);
-                return walk.rt * NT + c < rows ? ((long long)walk.b * a.n + q) * a.heads + walk.h * a.group + g : -1ll;
-            };
-            while (walk.at < walk.end && walk.u.count == 0) {  // rows that see nothing
-                const RowAt at(a, walk.rt * NT);
-                for (int c = 0; c < NT; ++c) {
-                    const long long row = row_of(at, c);
-                    if (row < 0)
-                        break;
-                    for (int d = lane; d < D / 8; d += 32)
-                        ((uint4 *)(a.out + row * D))[d] = make_uint4(0, 0, 0, 0);
-                    if (lane == 0)
-                        a.lse[row] = -INFINITY;
+            // descriptions run two segments ahead, so that the producer need not stop between segments
+            while (!end && described <= (seg ? seg + 2 : 0)) {
+                const auto row_of = [&](const RowAt &at, int c) {
+                    int q, g;
+                    at.of(a, c, q, g);
+                    return q <= walk.u.i1 ? ((long long)walk.b * a.n + q) * a.heads + walk.h * a.group + g : -1ll;
+                };
+                const Unit &u = walk.u;
+                end = walk.at >= walk.end || __any_sync(0xffffffffu, *dead);
+                Segment &g = sh.seg[described & 3];
+                if (!end) {
+                    const RowAt at(a, walk.rt * NT);
+                    for (int c = lane; c < NT; c += 32)
+                        g.rows[c] = row_of(at, c);
                 }
-                walk.next(a);
+                if (lane == 0) {
+                    g.tiles = end ? 0 : walk.x1 - walk.x0;
+                    g.x0 = walk.x0;
+                    g.head_tiles = u.head_tiles;
+                    g.low = u.low;
+                    g.len = u.len;
+                    g.m = u.m;
+                    g.first = u.first;
+                    g.prefix = u.prefix;
+                    g.i1 = u.i1;
+                    g.b = walk.b;
+                    g.h = walk.h;
+                    g.rt = walk.rt;
+                    g.seen_prefix = u.prefix / kTile;
+                    g.seen_end = (a.f.parent ? u.first : u.first + u.i0 + 1) / kTile;
+                    g.seen_low = a.f.window > 0
+                                     ? (int)((max((long long)u.first + u.i1 - a.f.window + 1, 0ll) + kTile - 1) / kTile)
+                                     : 0;
+                    g.whole = walk.x0 == 0 && walk.x1 == u.count;
+                    g.last = walk.x1 == u.count;
+                    g.at = walk.at;
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sh.seg_ready[described & 3]);
+                ++described;
+                if (!end)
+                    walk.next(a);
             }
-            const Unit &u = walk.u;
-            const bool some = walk.at < walk.end && !__any_sync(0xffffffffu, *dead);
-            Segment &g = sh.seg[i];
+            const Segment &g = sh.seg[seg & 3];
+            const bool some = g.tiles > 0 && !__any_sync(0xffffffffu, *dead);
             if (some) {
-                const RowAt at(a, walk.rt * NT);
-                for (int c = lane; c < NT; c += 32)
-                    g.rows[c] = row_of(at, c);
-            }
-            if (lane == 0) {
-                g.tiles = some ? walk.x1 - walk.x0 : 0;
-                g.x0 = walk.x0;
-                g.head_tiles = u.head_tiles;
-                g.low = u.low;
-                g.len = u.len;
-                g.first = u.first;
-                g.prefix = u.prefix;
-                g.i1 = u.i1;
-                g.b = walk.b;
-                g.h = walk.h;
-                g.rt = walk.rt;
-                g.seen_prefix = u.prefix / kTile;
-                g.seen_end = (a.f.parent ? u.first : u.first + u.i0 + 1) / kTile;
-                g.seen_low = a.f.window > 0
-                                 ? (int)((max((long long)u.first + u.i1 - a.f.window + 1, 0ll) + kTile - 1) / kTile)
-                                 : 0;
-                g.whole = walk.x0 == 0 && walk.x1 == u.count;
-                g.last = walk.x1 == u.count;
-                g.at = walk.at;
-            }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sh.seg_ready[i]);
-            if (some) {
-                const bool tree = a.f.parent && (long long)(u.tile(walk.x1 - 1) + 1) * kTile > u.first;
-                describe_columns<NT, 32>(a, u, walk.b, walk.h, walk.rt, tree, sh.col[i], lane);
+                const bool tree = a.f.parent && (long long)(g.tile(0) + 1) * kTile > g.first;
+                describe_columns<NT, 32>(a, g, g.b, g.h, g.rt, tree, sh.col[i], lane);
                 if (tree) {
                     __syncwarp();
                     mark_kin<NT, 32>(sh.col[i], lane);
@@ -965,7 +1000,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             if (lane == 0) {
                 mbar_expect(&sh.q_ready[i], some ? kQueryBytes<D, NT> : 0);
                 if (some)
-                    load_queries<D, NT>(a, walk.b, walk.h, walk.rt, sh.q[i][0], sh.col[i], &sh.q_ready[i]);
+                    load_queries<D, NT>(a, g.b, g.h, g.rt, sh.q[i][0], sh.col[i], &sh.q_ready[i]);
             }
             if (!some) {
                 if (*dead && seg > 0)  // the last queries in flight land
@@ -973,7 +1008,6 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                         ;
                 break;
             }
-            walk.next(a);
         }
     } else if (wid == kProducer) {
         // ---------------- producer ----------------
@@ -983,8 +1017,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         uint32_t k_phase = 1, v_phase = 1, issued = 0;
         const bool pos = a.f.slopes && a.c.positions;
         for (uint32_t seg = 0; !__any_sync(0xffffffffu, *dead); ++seg) {
-            mbar_wait(&sh.seg_ready[seg & 1], (seg >> 1) & 1, dead);
-            const Segment &u = sh.seg[seg & 1];
+            mbar_wait(&sh.seg_ready[seg & 3], (seg >> 2) & 1, dead);
+            const Segment &u = sh.seg[seg & 3];
             const int tiles = u.tiles, h = u.h;
             if (tiles == 0)
                 break;
@@ -1065,7 +1099,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 #pragma unroll 1
         for (uint32_t seg = 0; !__any_sync(0xffffffffu, *dead); ++seg) {
             mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, dead);
-            const int tiles = __shfl_sync(0xffffffffu, sh.seg[seg & 1].tiles, 0);
+            const int tiles = __shfl_sync(0xffffffffu, sh.seg[seg & 3].tiles, 0);
             if (tiles == 0)
                 break;
             const uint64_t qd = q_desc + (seg & 1) * (2 * NT * D >> 4);
@@ -1101,8 +1135,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         uint32_t v_phase = 0, g = 0;
 #pragma unroll 1
         for (uint32_t seg = 0; !__any_sync(0xffffffffu, *dead); ++seg) {
-            mbar_wait(&sh.seg_ready[seg & 1], (seg >> 1) & 1, dead);
-            const int tiles = __shfl_sync(0xffffffffu, sh.seg[seg & 1].tiles, 0);
+            mbar_wait(&sh.seg_ready[seg & 3], (seg >> 2) & 1, dead);
+            const int tiles = __shfl_sync(0xffffffffu, sh.seg[seg & 3].tiles, 0);
             if (tiles == 0)
                 break;
 #pragma unroll 1
@@ -1142,7 +1176,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 #pragma unroll 1
         for (uint32_t seg = 0;; ++seg) {
             mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, dead);
-            const Segment &u = sh.seg[seg & 1];
+            const Segment &u = sh.seg[seg & 3];
             const Columns<NT> &col = sh.col[seg & 1];
             const int tiles = u.tiles;
             if (barrier_or<128>(bar, tiles == 0 || *dead))
@@ -1430,8 +1464,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         float o[OC];
 #pragma unroll 1
         for (uint32_t seg = 0;; ++seg) {
-            mbar_wait(&sh.seg_ready[seg & 1], (seg >> 1) & 1, dead);
-            const Segment &u = sh.seg[seg & 1];
+            mbar_wait(&sh.seg_ready[seg & 3], (seg >> 2) & 1, dead);
+            const Segment &u = sh.seg[seg & 3];
             const int tiles = u.tiles;
             if (barrier_or<128>(bar, tiles == 0 || *dead))
                 break;
