@@ -54,7 +54,7 @@ spec_status device_sms(int *sms)
             return SPEC_ERR_CUDA;
         }
         for (const Kernels *k : {&kernels_d64(), &kernels_d128()})
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 3; ++i)
                 for (int f = 0; f < 2; ++f)
                     if (cudaFuncSetAttribute(k->attend[i][f], cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              k->attend_smem[i]) != cudaSuccess ||
@@ -105,14 +105,16 @@ spec_status make_map(const spec_cache &c, void *base, const int64_t stride[3], C
                : SPEC_ERR_INVALID_ARG;
 }
 
-// Columns of a row tile: the fewest that hold a key head's rows, 64 at most.
+// Columns of a row tile: the fewest that hold a key head's rows, 48 at most.  (64 columns, with two softmax
+// warpgroups, took 5 to 12% longer than 48 with three for trees of 64 nodes and chunks of 1000 tokens; 32 with four
+// took 17% longer for the chunks, and 5% less for the trees.)
 struct Shape {
     int index, nt, row_tiles;
 };
 Shape shape_for(const spec_cache &c, int n, int heads)
 {
     const int rows = n * (heads / c.kv_heads);
-    const int i = rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 48 ? 2 : 3, nt = 16 * (i + 1);
+    const int i = rows <= 16 ? 0 : rows <= 32 ? 1 : 2, nt = 16 * (i + 1);
     return {i, nt, (rows + nt - 1) / nt};
 }
 

@@ -236,6 +236,33 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// Two 32-bit operations by one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmul.rn.f32x2 z, x, y;\nmov.b64 {%0, %1}, z;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 r;
+    asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 z, x, y;\nmov.b64 {%0, %1}, z;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{\n.reg .b64 x, y, z, w;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\nfma.rn.f32x2 w, x, y, "
+        "z;\nmov.b64 {%0, %1}, w;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
 // Shared-memory matrix descriptor.  swizzle: 0 none, 2 128-byte, 4 64-byte.
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint64_t swizzle)
 {
@@ -371,8 +398,8 @@ template <int THREADS, typename Cost> __device__ __forceinline__ Range find_rang
 // ---------------------------------------------------------------------------
 template <int NT> struct Columns {
     float factor[NT];  // of the accumulator, times the token's scale: the score, in units of log2 (of softcap with one)
-    float base[NT];    // attend: the exponent's reference; weigh: the row's lse, in units of log2
-    float slope[NT];   // times log2(e)
+    float less[NT];    // weigh: the row's -lse, in units of log2
+    float slope[NT];   // times -log2(e)
     float pos[NT];
     int query[NT];     // its query, -1: none
     uint32_t kin[NT][kMaxNodes / 32];
@@ -511,7 +538,7 @@ __device__ __forceinline__ void describe_columns(const AttendArgs &a, const Unit
                 p = page < 0 ? 0.0f : (float)a.c.positions[((size_t)page * a.c.kv_heads + h) * a.c.block + j % a.c.block];
             }
             col.pos[c] = p;
-            col.slope[c] = live ? a.f.slopes[h * a.group + g] * kLog2e : 0.0f;
+            col.slope[c] = live ? -a.f.slopes[h * a.group + g] * kLog2e : 0.0f;
         }
     }
     if (tree && a.f.parent)
@@ -534,26 +561,26 @@ template <int NT, int THREADS> __device__ __forceinline__ void mark_kin(Columns<
     }
 }
 
-// Scores in units of log2, less base, of 16 columns from c0 on; e: the accumulator
-// values of a token with this scale and position.  FORM: there may be a cap or a bias.
+// Scores in units of log2, less base (given negated), of 16 columns from c0 on; e:
+// the accumulator values of a token with this scale and position.  FORM: there
+// may be a cap or a bias.
 template <bool FORM, int NT>
-__device__ __forceinline__ void scores(const AttendArgs &a, const Columns<NT> &col, const float *base, int c0, float k_scale,
+__device__ __forceinline__ void scores(const AttendArgs &a, const Columns<NT> &col, const float *less, int c0, float k_scale,
                                        float pos, float *e)
 {
-    const float4 *factor4 = (const float4 *)(col.factor + c0), *base4 = (const float4 *)(base + c0);
+    const float4 *factor4 = (const float4 *)(col.factor + c0), *less4 = (const float4 *)(less + c0);
+    float2 *e2 = (float2 *)e;
+    const float2 k2 = make_float2(k_scale, k_scale);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        const float4 f = factor4[c], b = base4[c];
+        const float4 f = factor4[c], b = less4[c];
+        const float2 f0 = mul2(k2, make_float2(f.x, f.y)), f1 = mul2(k2, make_float2(f.z, f.w));
         if (FORM) {
-            e[4 * c] *= k_scale * f.x;
-            e[4 * c + 1] *= k_scale * f.y;
-            e[4 * c + 2] *= k_scale * f.z;
-            e[4 * c + 3] *= k_scale * f.w;
+            e2[2 * c] = mul2(e2[2 * c], f0);
+            e2[2 * c + 1] = mul2(e2[2 * c + 1], f1);
         } else {
-            e[4 * c] = fmaf(e[4 * c], k_scale * f.x, -b.x);
-            e[4 * c + 1] = fmaf(e[4 * c + 1], k_scale * f.y, -b.y);
-            e[4 * c + 2] = fmaf(e[4 * c + 2], k_scale * f.z, -b.z);
-            e[4 * c + 3] = fmaf(e[4 * c + 3], k_scale * f.w, -b.w);
+            e2[2 * c] = fma2(e2[2 * c], f0, make_float2(b.x, b.y));
+            e2[2 * c + 1] = fma2(e2[2 * c + 1], f1, make_float2(b.z, b.w));
         }
     }
     if (!FORM)
@@ -571,24 +598,23 @@ __device__ __forceinline__ void scores(const AttendArgs &a, const Columns<NT> &c
         }
     }
     if (a.f.slopes) {
-        const float4 *slope4 = (const float4 *)(col.slope + c0), *from4 = (const float4 *)(col.pos + c0);
+        const float4 *slope4 = (const float4 *)(col.slope + c0), *from4 = (const float4 *)(col.pos + c0);  // slopes negated
+        const float2 p2 = make_float2(-pos, -pos);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float4 sl = slope4[c], from = from4[c], b = base4[c];
-            e[4 * c] = fmaf(-sl.x, fabsf(from.x - pos), e[4 * c]) - b.x;
-            e[4 * c + 1] = fmaf(-sl.y, fabsf(from.y - pos), e[4 * c + 1]) - b.y;
-            e[4 * c + 2] = fmaf(-sl.z, fabsf(from.z - pos), e[4 * c + 2]) - b.z;
-            e[4 * c + 3] = fmaf(-sl.w, fabsf(from.w - pos), e[4 * c + 3]) - b.w;
+            const float4 sl = slope4[c], from = from4[c];
+            float2 d0 = add2(make_float2(from.x, from.y), p2), d1 = add2(make_float2(from.z, from.w), p2);
+            d0 = make_float2(fabsf(d0.x), fabsf(d0.y));
+            d1 = make_float2(fabsf(d1.x), fabsf(d1.y));
+            e2[2 * c] = fma2(make_float2(sl.x, sl.y), d0, e2[2 * c]);
+            e2[2 * c + 1] = fma2(make_float2(sl.z, sl.w), d1, e2[2 * c + 1]);
         }
-    } else {
+    }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const float4 b = base4[c];
-            e[4 * c] -= b.x;
-            e[4 * c + 1] -= b.y;
-            e[4 * c + 2] -= b.z;
-            e[4 * c + 3] -= b.w;
-        }
+    for (int c = 0; c < 4; ++c) {
+        const float4 b = less4[c];
+        e2[2 * c] = add2(e2[2 * c], make_float2(b.x, b.y));
+        e2[2 * c + 1] = add2(e2[2 * c + 1], make_float2(b.z, b.w));
     }
 }
 
@@ -716,7 +742,7 @@ template <int NT> struct Walk {
 // waited for instructions more than for anything else), exponentials and running
 // totals live in tensor memory between the passes.
 template <int D, int NT> struct AttendShape {
-    static constexpr int NW = NT <= 32 ? 4 : NT == 48 ? 3 : 2;  // softmax warpgroups
+    static constexpr int NW = NT <= 32 ? 4 : 3;  // softmax warpgroups
     static constexpr int kThreads = 128 * (2 + NW);
     static constexpr int NO = NT == 48 ? 1 : 2;                 // O^T at a time (one: room to keep the exponentials)
     static constexpr int kBytes = kTile * D;                    // one side of a tile
@@ -735,7 +761,7 @@ struct Segment {
     int seen_prefix, seen_low, seen_end;  // tiles that every query of the row tile sees whole: [0, ..) and [low, end)
     int whole, last;                      // the whole unit; its last part
     long long at;                         // first tile's place in the order of all
-    long long rows[64];                   // of the outputs, by column; -1: none
+    long long rows[48];                   // of the outputs, by column; -1: none
     // k-th tile to be worked on: from the newest tokens back, since scores with a bias by distance fall that way and
     // bases set first then stay
     __device__ __forceinline__ int tile(int k) const
@@ -754,7 +780,7 @@ template <int D, int NT> struct AttendShared {
     alignas(16) Columns<NT> col[2];
     Segment seg[4];
     alignas(16) StageInfo info[S::VS];
-    alignas(16) float base[S::NW][NT];
+    alignas(16) float less[S::NW][NT];   // the exponents' bases, negated
     alignas(16) uint32_t scale[S::NW][4][NT];  // per tile: 2^k, as bits, that brings the largest weight to [224, 448]
     alignas(16) int power[S::kRing][NT];       // per tile: O^T counts 2^power
     alignas(16) long long out_row[NT];
@@ -1189,7 +1215,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 tmem_store_wait();
             }
             if (t < NT) {
-                sh.base[w][t] = 0.0f;
+                sh.less[w][t] = 0.0f;
                 sh.is_set[w][t] = 0;
             }
 #pragma unroll 1
@@ -1253,7 +1279,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     const auto exponentials = [&](int c0, float *e) {
                         TmemLoad<16>::go(s_at + c0, e);
                         tmem_wait<16>(e);
-                        scores<FORM>(a, col, sh.base[w], c0, k_scale, pos, e);
+                        scores<FORM>(a, col, sh.less[w], c0, k_scale, pos, e);
 #pragma unroll
                         for (int c = 0; c < 16; ++c)
                             e[c] = exp2_fast(e[c]);
@@ -1269,7 +1295,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             // bases from the rows' largest scores
 #pragma unroll 1
                             for (int c0 = 0; c0 < NT; c0 += 16) {
-                                float e[16];
+                                alignas(8) float e[16];
                                 TmemLoad<16>::go(s_at + c0, e);
                                 tmem_wait<16>(e);
                                 scores<FORM>(a, col, sh.none, c0, k_scale, pos, e);
@@ -1288,14 +1314,14 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                                 bool set = true;
                                 if (t < NT) {
                                     const int top = sh.highest[w][t];
-                                    const float high = __int_as_float(top ^ ((top >> 31) & 0x7fffffff)), old = sh.base[w][t];
+                                    const float high = __int_as_float(top ^ ((top >> 31) & 0x7fffffff)), old = -sh.less[w][t];
                                     sh.highest[w][t] = INT_MIN;
                                     set = sh.is_set[w][t];
                                     if (top != INT_MIN && high > -INFINITY) {
                                         if (!set || high - old > 32.0f) {
                                             const float now = fminf(fmaxf(ceilf(high), -0x1p30f), 0x1p30f);
                                             alpha = set ? exp2f(old - now) : 1.0f;
-                                            sh.base[w][t] = now;
+                                            sh.less[w][t] = -now;
                                         }
                                         sh.is_set[w][t] = 1;
                                         set = true;
@@ -1328,7 +1354,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                         bool again = false;
 #pragma unroll 1
                         for (int c0 = 0; c0 < NT; c0 += 16) {
-                            float e[16];
+                            alignas(8) float e[16];
                             exponentials(c0, e);
                             if (S::kKeep)
                                 tmem_store16(e_at + c0, e);
@@ -1380,11 +1406,11 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             mbar_arrive(&sh.s_free[w]);
                     }
                     if (t < NT)
-                        sh.power[g % kRing][t] = 127 - (int)(scales[t] >> 23) + (int)sh.base[w][t];
+                        sh.power[g % kRing][t] = 127 - (int)(scales[t] >> 23) - (int)sh.less[w][t];
                     mbar_wait(&sh.p_free[w], (mine & 1) ^ 1, dead);
 #pragma unroll 1
                     for (int c0 = 0; c0 < NT; c0 += 16) {
-                        float e[16], l[16];
+                        alignas(8) float e[16], l[16];
                         TmemLoad<16>::go(l_at + c0, l);
                         if (S::kKeep) {
                             TmemLoad<16>::go(e_at + c0, e);
@@ -1393,16 +1419,18 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             exponentials(c0, e);
                         }
                         tmem_wait<16>(l);
+                        const float2 v2 = make_float2(v_scale, v_scale);
 #pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            l[c] += e[c];
+                        for (int c = 0; c < 8; ++c)
+                            ((float2 *)l)[c] = add2(((float2 *)l)[c], ((float2 *)e)[c]);
                         tmem_store16(l_at + c0, l);
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int c4 = 0; c4 < 4; ++c4) {
                             const float4 y = *(const float4 *)(scales + c0 + c4 * 4);
-                            float p[4] = {e[4 * c4] * (y.x * v_scale), e[4 * c4 + 1] * (y.y * v_scale),
-                                          e[4 * c4 + 2] * (y.z * v_scale), e[4 * c4 + 3] * (y.w * v_scale)};
+                            const float2 p0 = mul2(((float2 *)e)[2 * c4], mul2(make_float2(y.x, y.y), v2)),
+                                         p1 = mul2(((float2 *)e)[2 * c4 + 1], mul2(make_float2(y.z, y.w), v2));
+                            float p[4] = {p0.x, p0.y, p1.x, p1.y};
                             if (edge) {
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
@@ -1440,7 +1468,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             // the rows' totals, warp by warp
             mbar_wait(&sh.sum_free[seg & 1], ((seg >> 1) & 1) ^ 1, dead);
             if (t < NT)
-                sh.last_base[seg & 1][w][t] = sh.base[w][t];
+                sh.last_base[seg & 1][w][t] = -sh.less[w][t];
 #pragma unroll 1
             for (int c0 = 0; c0 < NT; c0 += 16) {
                 float y[16];
@@ -1461,7 +1489,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         const uint32_t lanes = (uint32_t)wid << 21;
         constexpr int kPart = OC % 16 == 0 ? 16 : 8;
         uint32_t g = 0;
-        float o[OC];
+        alignas(8) float o[OC];
 #pragma unroll 1
         for (uint32_t seg = 0;; ++seg) {
             mbar_wait(&sh.seg_ready[seg & 3], (seg >> 2) & 1, dead);
@@ -1508,10 +1536,9 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 #pragma unroll
                     for (int c = 0; c < kPart; c += 4) {
                         const float4 f = *(const float4 *)(sh.factor[i] + o0 + c1 + c);
-                        o[c1 + c] = fmaf(y[c], f.x, o[c1 + c]);
-                        o[c1 + c + 1] = fmaf(y[c + 1], f.y, o[c1 + c + 1]);
-                        o[c1 + c + 2] = fmaf(y[c + 2], f.z, o[c1 + c + 2]);
-                        o[c1 + c + 3] = fmaf(y[c + 3], f.w, o[c1 + c + 3]);
+                        float2 *o2 = (float2 *)(o + c1 + c);
+                        o2[0] = fma2(make_float2(y[c], y[c + 1]), make_float2(f.x, f.y), o2[0]);
+                        o2[1] = fma2(make_float2(y[c + 2], y[c + 3]), make_float2(f.z, f.w), o2[1]);
                     }
                 }
                 tc_before();
@@ -1736,7 +1763,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                     const int r = rt * NT + tid, i = r / a.group;
                     const float lse =
                         i <= u.i1 ? a.lse_in[((size_t)b * a.n + i) * a.heads + h * a.group + r % a.group] : -INFINITY;
-                    sh.col.base[tid] = lse == -INFINITY ? INFINITY : lse * kLog2e;
+                    sh.col.less[tid] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
                 }
                 if (tid == 0) {
                     mbar_expect(&sh.q_ready, kQueryBytes<D, NT>);
@@ -1769,10 +1796,10 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                         float sum = 0.0f;
 #pragma unroll 1
                         for (int c0 = 0; c0 < NT; c0 += 16) {
-                            float e[16];
+                            alignas(8) float e[16];
                             TmemLoad<16>::go(tmem + ((uint32_t)(wid & 3) << 21) + (g & 1) * NT + c0, e);
                             tmem_wait<16>(e);
-                            scores<FORM>(a, sh.col, sh.col.base, c0, ks, pos, e);
+                            scores<FORM>(a, sh.col, sh.col.less, c0, ks, pos, e);
                             const uint32_t bits = (uint32_t)(see >> c0);
 #pragma unroll
                             for (int c = 0; c < 16; ++c)
@@ -1858,10 +1885,10 @@ template <int D, int NT> __global__ void __launch_bounds__(32 * kJoinRows) join_
         a.lse[row] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
 }
 
-// The kernels of one head size, by columns per row tile (16, 32, 48 or 64).
+// The kernels of one head size, by columns per row tile (16, 32 or 48).
 struct Kernels {
-    const void *split, *attend[4][2], *join[4], *weigh[4][2];  // [..][a cap or a bias]
-    int attend_smem[4], attend_threads[4], weigh_smem[4];
+    const void *split, *attend[3][2], *join[3], *weigh[3][2];  // [..][a cap or a bias]
+    int attend_smem[3], attend_threads[3], weigh_smem[3];
 };
 const Kernels &kernels_d64();
 const Kernels &kernels_d128();
@@ -1886,7 +1913,6 @@ template <int D> Kernels all_kernels()
     fill<D, 16>(k, 0);
     fill<D, 32>(k, 1);
     fill<D, 48>(k, 2);
-    fill<D, 64>(k, 3);
     return k;
 }
 
