@@ -88,17 +88,18 @@ __device__ __forceinline__ bool mbar_try(uint64_t *bar, uint32_t parity)
 // and every later wait returns at once: control flow stays the same for all
 // threads, so the CTA runs to its end (with results that the status marks bad).
 constexpr long long kPatience = 1ll << 31;  // clocks
-__device__ __forceinline__ void mbar_wait(uint64_t *bar, uint32_t parity, volatile int *dead)
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *dead)  // whether it came
 {
     if (mbar_try(bar, parity))
-        return;
+        return true;
     const long long since = clock64();
     while (!mbar_try(bar, parity)) {
         if (*dead)
-            return;
+            return false;
         if (clock64() - since > kPatience)
             *dead = 1;
     }
+    return true;
 }
 
 // After a wait ran out: copies and products in flight end before the CTA's memory is given back.
@@ -626,33 +627,31 @@ struct StageInfo {
     uint32_t pad[3];
 };
 
-// Brings one tile's blocks into shared memory; a warp calls it.  info: which blocks came.
-template <int D, bool VALUES>
-__device__ __forceinline__ void load_tile(const AttendArgs &a, const CUtensorMap *kmap, const CUtensorMap *vmap, int h, int page,
-                                          bool here, StageInfo &st, uint8_t *k, uint8_t *v, uint64_t *full, int lane)
+// Brings one tile's blocks of keys into shared memory, and what belongs to them; a
+// warp calls it, a lane per block.
+template <int D>
+__device__ __forceinline__ void load_keys(const AttendArgs &a, const CUtensorMap *kmap, int h, int page, bool here, int blocks,
+                                          StageInfo &st, uint8_t *k, uint64_t *full, int lane)
 {
     const int P = a.c.block;
-    const uint32_t came = __ballot_sync(0xffffffffu, here && page >= 0);
+    const uint32_t came = __ballot_sync(0xffffffffu, here);
     const bool pos = a.f.slopes && a.c.positions;
     if (lane == 0) {
         st.came = came;  // bit k: block k of the tile came
-        mbar_expect(full, (uint32_t)__popc(came) * (uint32_t)(P * D * (VALUES ? 2 : 1) + (pos ? P * 4 : 0)));
+        mbar_expect(full, (uint32_t)__popc(came) * (uint32_t)(P * D + (pos ? P * 4 : 0)));
     }
     __syncwarp();
-    if (lane < 8)
+    if (lane < blocks) {
         st.page[lane] = page;
-    if (here && page >= 0) {
-        const size_t at = (size_t)page * a.c.kv_heads + h;
-        tma_load(kmap, k + lane * P * D, full, 0, 0, h, page);
-        if (VALUES)
-            tma_load(vmap, v + lane * P * D, full, 0, 0, h, page);
-        if (pos)
-            bulk_load(a.c.positions + at * P, st.pos + lane * P, (uint32_t)P * 4, full);
-        copy4(a.c.k_scale + at, st.k_scale + lane);
-        if (VALUES)
-            copy4(a.c.v_scale + at, st.v_scale + lane);
+        if (here) {
+            const size_t at = (size_t)page * a.c.kv_heads + h;
+            tma_load(kmap, k + lane * P * D, full, 0, 0, h, page);
+            if (pos)
+                bulk_load(a.c.positions + at * P, st.pos + lane * P, (uint32_t)P * 4, full);
+            copy4(a.c.k_scale + at, st.k_scale + lane);
+        }
+        copies_arrive(full);
     }
-    copies_arrive(full);
 }
 
 // The segments of a CTA's stretch: units, or parts of them, in order; units
@@ -907,7 +906,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             mbar_init(&sh.k_empty[i], 1);
         }
         for (int i = 0; i < VS; ++i) {
-            mbar_init(&sh.v_full[i], 33);  // the expected bytes, and 32 lanes' copies of scales
+            mbar_init(&sh.v_full[i], 1 + kTile / a.c.block);  // the expected bytes, and each block's scales
             mbar_init(&sh.v_empty[i], 1);
         }
         for (int i = 0; i < NW; ++i) {
@@ -1073,8 +1072,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     report(a.status, SPEC_STATUS_BAD_PAGE);
                 const uint32_t came = __ballot_sync(0xffffffffu, ok);
                 const size_t at = (size_t)max(page, 0) * a.c.kv_heads + h;
-                mbar_wait(&sh.k_empty[ks], k_phase, dead);
-                bool go = !__any_sync(0xffffffffu, *dead);
+                bool go = __all_sync(0xffffffffu, mbar_wait(&sh.k_empty[ks], k_phase, dead));
                 if (go) {
                     if (lane == 0)
                         mbar_expect(&sh.k_full[ks], (uint32_t)__popc(came) * (uint32_t)(P * D));
@@ -1082,8 +1080,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     if (ok)
                         tma_load(&kmap, sh.k[ks] + lane * P * D, &sh.k_full[ks], 0, 0, h, page);
                 }
-                mbar_wait(&sh.v_empty[vs], v_phase, dead);
-                go = go && !__any_sync(0xffffffffu, *dead);
+                go = __all_sync(0xffffffffu, mbar_wait(&sh.v_empty[vs], v_phase, dead)) && go;
                 if (go) {
                     StageInfo &info = sh.info[vs];
                     if (lane == 0) {
@@ -1098,7 +1095,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                         copy4(a.c.k_scale + at, info.k_scale + lane);
                         copy4(a.c.v_scale + at, info.v_scale + lane);
                     }
-                    copies_arrive(&sh.v_full[vs]);
+                    if (lane < blocks)
+                        copies_arrive(&sh.v_full[vs]);
                     ++issued;
                 }
                 if (++ks == KS) {
@@ -1619,18 +1617,19 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 // ===========================================================================
 // The same S^T tiles, read once more against the known lse: weight of a token
 // += sum over the rows of exp2(x - lse).  A thread owns a token of its tile and
-// adds its columns up, so a sum needs no other thread and no atomic.  Two
-// warpgroups take alternate tiles.  Keys only: half of what attention reads.
-constexpr int kWeighThreads = 320;
+// adds its columns up, so a sum needs no other thread and no atomic.  Three
+// warpgroups take tiles in turn.  Keys only: half of what attention reads.
+constexpr int kWeighGroups = 3;  // 55 us for 32 sequences of 8192 tokens; two took 60, four 56
+constexpr int kWeighThreads = 128 * kWeighGroups + 64;
 
 template <int D, int NT> struct WeighShared {
-    static constexpr int kStages = 10, kAlloc = NT == 48 ? 128 : 2 * NT;
+    static constexpr int kStages = 10, kAlloc = NT * kWeighGroups <= 64 ? 64 : NT * kWeighGroups <= 128 ? 128 : 256;
     alignas(1024) uint8_t tiles[kStages][kTile * D];
     alignas(1024) uint8_t q[2][NT * D];
     alignas(16) Columns<NT> col;
     alignas(16) StageInfo info[kStages];
     alignas(8) uint64_t full[kStages], empty[kStages];
-    uint64_t s_full[2], s_free[2], q_ready, drained;
+    uint64_t s_full[kWeighGroups], s_free[kWeighGroups], q_ready, drained;
     uint32_t tmem;
     int dead;
 };
@@ -1645,7 +1644,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     weigh_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap kmap)
 {
     using Shared = WeighShared<D, NT>;
-    constexpr int ST = Shared::kStages;
+    constexpr int ST = Shared::kStages, NW = kWeighGroups, kProducer = 4 * NW, kProducts = kProducer + 1;
     extern __shared__ uint8_t raw[];
     Shared &sh = *(Shared *)(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
     const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -1653,10 +1652,10 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     if (tid == 0) {
         sh.dead = 0;
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&sh.full[i], 33);
+            mbar_init(&sh.full[i], 1 + kTile / a.c.block);  // the expected bytes, and each block's scales
             mbar_init(&sh.empty[i], 5);  // the products, and the four warps that read the scales
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kWeighGroups; ++i) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.s_free[i], 4);
         }
@@ -1664,7 +1663,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         mbar_init(&sh.drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (wid == 9) {
+    if (wid == kProducts) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
                      "r"(Shared::kAlloc)
                      : "memory");
@@ -1700,21 +1699,33 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
             const int low = all.tile(x0), high = all.tile(x1 - 1);
             if (u.count == 0 || !(low < u.head_tiles || (high >= u.low && low < u.low + u.count - u.head_tiles)))
                 continue;  // no tile of the stretch
-            if (wid == 8) {
+            if (wid == kProducer) {
                 // ---------------- producer ----------------
+                const int32_t *table = a.c.block_table + (size_t)b * a.c.table_stride;
+                const int batch = 32 / blocks;  // tiles whose table entries come together, a batch ahead
+                const auto pages_from = [&](int x) {
+                    const int k = x + lane / blocks;
+                    if (k >= x1)
+                        return -2;
+                    const int blk = all.tile(k) * blocks + (lane & (blocks - 1));
+                    return (long long)blk * P < u.len ? table[blk] : -2;
+                };
+                int pages = 0, more = pages_from(x0);
                 for (int x = x0; x < x1; ++x) {
-                    const int tile = all.tile(x), blk = tile * blocks + lane;
-                    if (!covers(u, tile))
+                    const int at_x = (x - x0) & (batch - 1);
+                    if (at_x == 0) {
+                        pages = more;
+                        more = pages_from(x + batch);
+                    }
+                    const int got = __shfl_sync(0xffffffffu, pages, (at_x * blocks + lane) & 31);
+                    if (!covers(u, all.tile(x)))
                         continue;
-                    const bool some = lane < blocks && (long long)blk * P < u.len;
-                    const int page = some ? a.c.block_table[(size_t)b * a.c.table_stride + blk] : -1;
+                    const int page = lane < blocks ? got : -2;
                     const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
-                    if (some && !ok)
+                    if (page != -2 && !ok)
                         report(a.status, SPEC_STATUS_BAD_PAGE);
-                    mbar_wait(&sh.empty[st], phase ^ 1, dead);
-                    if (!__any_sync(0xffffffffu, *dead)) {
-                        load_tile<D, false>(a, &kmap, nullptr, h, page, ok, sh.info[st], sh.tiles[st], nullptr, &sh.full[st],
-                                            lane);
+                    if (__all_sync(0xffffffffu, mbar_wait(&sh.empty[st], phase ^ 1, dead))) {
+                        load_keys<D>(a, &kmap, h, page, ok, blocks, sh.info[st], sh.tiles[st], &sh.full[st], lane);
                         ++issued;
                     }
                     if (++st == ST) {
@@ -1722,7 +1733,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                         phase ^= 1;
                     }
                 }
-            } else if (wid == 9) {
+            } else if (wid == kProducts) {
                 // ---------------- products ----------------
                 const uint32_t desc = instr_desc(NT, a.c.code, false, false);
                 mbar_wait(&sh.q_ready, seg++ & 1, dead);
@@ -1730,19 +1741,17 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                     if (!covers(u, all.tile(x)))
                         continue;
                     mbar_wait(&sh.full[st], phase, dead);
-                    mbar_wait(&sh.s_free[g & 1], ((g >> 1) & 1) ^ 1, dead);
+                    mbar_wait(&sh.s_free[g % NW], ((g / NW) & 1) ^ 1, dead);
                     tc_after();
                     if (elected()) {
-                        const uint32_t k = smem_u32(sh.tiles[st]), q = smem_u32(sh.q[0]);
+                        const uint64_t kd = smem_desc(smem_u32(sh.tiles[st]), 16, 8 * D, D == 128 ? 2 : 4),
+                                       qd = smem_desc(smem_u32(sh.q[0]), 16, 8 * D, D == 128 ? 2 : 4);
 #pragma unroll
                         for (int d = 0; d < D / 32; ++d) {
-                            const uint64_t kd = smem_desc(k + d * 32, 16, 8 * D, D == 128 ? 2 : 4);
-#pragma unroll
-                            for (int term = 0; term < 2; ++term)
-                                tc_mma(tmem + (g & 1) * NT, kd,
-                                       smem_desc(q + term * NT * D + d * 32, 16, 8 * D, D == 128 ? 2 : 4), desc, d + term > 0);
+                            tc_mma(tmem + (g % NW) * NT, kd + (d * 32 >> 4), qd + (d * 32 >> 4), desc, d > 0);
+                            tc_mma(tmem + (g % NW) * NT, kd + (d * 32 >> 4), qd + ((NT * D + d * 32) >> 4), desc, true);
                         }
-                        tc_commit(&sh.s_full[g & 1]);
+                        tc_commit(&sh.s_full[g % NW]);
                         tc_commit(&sh.empty[st]);
                     }
                     __syncwarp();
@@ -1756,9 +1765,9 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                 // ---------------- sums ----------------
                 const int w = wid >> 2, t = tid & 127;
                 const Askers askers{u.first, u.prefix, u.i1, rt * NT, a.group};
-                named_barrier<256>(3);
+                named_barrier<128 * NW>(3);
                 const bool tree = a.f.parent && (long long)(all.tile(x1 - 1) + 1) * kTile > u.first;
-                describe_columns<NT, 256>(a, u, b, h, rt, tree, sh.col, tid);
+                describe_columns<NT, 128 * NW>(a, u, b, h, rt, tree, sh.col, tid);
                 if (tid < NT) {
                     const int r = rt * NT + tid, i = r / a.group;
                     const float lse =
@@ -1769,17 +1778,17 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                     mbar_expect(&sh.q_ready, kQueryBytes<D, NT>);
                     load_queries<D, NT>(a, b, h, rt, sh.q[0], sh.col, &sh.q_ready);
                 }
-                named_barrier<256>(3);
+                named_barrier<128 * NW>(3);
                 if (tree) {
-                    mark_kin<NT, 256>(sh.col, tid);
-                    named_barrier<256>(3);
+                    mark_kin<NT, 128 * NW>(sh.col, tid);
+                    named_barrier<128 * NW>(3);
                 }
                 mbar_wait(&sh.q_ready, seg++ & 1, dead);
                 for (int x = x0; x < x1; ++x) {
                     const int tile = all.tile(x);
                     if (!covers(u, tile))
                         continue;
-                    if ((int)(g & 1) == w) {
+                    if ((int)(g % NW) == w) {
                         mbar_wait(&sh.full[st], phase, dead);
                         const StageInfo &info = sh.info[st];
                         const int j0 = tile * kTile, j = j0 + t, page = info.page[t >> log_p];
@@ -1791,24 +1800,36 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                         const Mask<NT> see = edge && cached ? seen_by<NT>(a, askers, sh.col, j) : 0;
                         float *weight = a.weights + ((size_t)(cached ? page : 0) * a.c.kv_heads + h) * P + (t & (P - 1));
                         const float before = cached ? *weight : 0.0f;
-                        mbar_wait(&sh.s_full[g & 1], (g >> 1) & 1, dead);
+                        mbar_wait(&sh.s_full[w], (g / NW) & 1, dead);
                         tc_after();
                         float sum = 0.0f;
 #pragma unroll 1
                         for (int c0 = 0; c0 < NT; c0 += 16) {
                             alignas(8) float e[16];
-                            TmemLoad<16>::go(tmem + ((uint32_t)(wid & 3) << 21) + (g & 1) * NT + c0, e);
+                            TmemLoad<16>::go(tmem + ((uint32_t)(wid & 3) << 21) + w * NT + c0, e);
                             tmem_wait<16>(e);
                             scores<FORM>(a, sh.col, sh.col.less, c0, ks, pos, e);
-                            const uint32_t bits = (uint32_t)(see >> c0);
 #pragma unroll
                             for (int c = 0; c < 16; ++c)
-                                sum += !edge || ((bits >> c) & 1) ? exp2_fast(e[c]) : 0.0f;
+                                e[c] = exp2_fast(e[c]);
+                            if (edge) {
+                                const uint32_t bits = (uint32_t)(see >> c0);
+#pragma unroll
+                                for (int c = 0; c < 16; ++c)
+                                    e[c] = (bits >> c) & 1 ? e[c] : 0.0f;
+                            }
+                            float2 *e2 = (float2 *)e;
+#pragma unroll
+                            for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+                                for (int c = 0; c < n; ++c)
+                                    e2[c] = add2(e2[c], e2[c + n]);
+                            sum += e[0] + e[1];
                         }
                         tc_before();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive(&sh.s_free[g & 1]);
+                            mbar_arrive(&sh.s_free[w]);
                             mbar_arrive(&sh.empty[st]);
                         }
                         if (cached)
@@ -1825,14 +1846,14 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         at += x1 - x0;
         skip += x1 - x0;
     }
-    if (wid == 8)
+    if (wid == kProducer)
         drain<ST>(sh.full, issued, dead, a.status);
-    if (wid == 9)
+    if (wid == kProducts)
         drain_products(&sh.drained, dead);
     tc_before();
     __syncthreads();
     tc_after();
-    if (wid == 9)
+    if (wid == kProducts)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Shared::kAlloc));
 }
 
