@@ -24,6 +24,7 @@ from . import _native
 
 _CODES = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 MAX_TREE_NODES = 256
+_Three = ctypes.c_int64 * 3
 
 
 class KVCache(NamedTuple):
@@ -65,12 +66,13 @@ def _check(t, name, dtype, shape, device):
 
 def _strides(t, name, multiple):
     """Strides of all but the last dimension, which has to be dense (sizes of one do not matter)."""
-    *st, last = t.stride()
-    if last == 1 and all(st) and not any(x % multiple for x in st):
+    a, b, c, last = t.stride()
+    st = (a, b, c)
+    if last == 1 and a and b and c and not (a | b | c) % multiple:
         return st
     if last != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be dense")
-    st = [x if n > 1 else multiple for n, x in zip(t.shape[:-1], st)]
+    st = tuple(x if n > 1 else multiple for n, x in zip(t.shape[:-1], st))
     if any(x % multiple for x in st):
         raise ValueError(f"{name}: strides must be multiples of {multiple}, got {tuple(t.stride())}")
     return st
@@ -102,7 +104,7 @@ def _describe(cache, block_table, lengths):
         k.data_ptr(), v.data_ptr(), _check(k_scale, "cache.k_scale", torch.float32, (pages, heads), dev),
         _check(v_scale, "cache.v_scale", torch.float32, (pages, heads), dev),
         _optional(positions, "cache.positions", torch.int32, (pages, heads, block), dev), block_table.data_ptr(),
-        tuple(_strides(k, "cache.k", 16)), tuple(_strides(v, "cache.v", 16)), step if batch > 1 else blocks, batch,
+        _strides(k, "cache.k", 16), _strides(v, "cache.v", 16), step if batch > 1 else blocks, batch,
         blocks, pages, heads, block, dim, code)
     return c, dev, _check(lengths, "lengths", torch.int32, (batch,), dev)
 
@@ -162,9 +164,8 @@ def cache_append(cache, block_table, lengths, k, v, num_new=None, positions=None
     if k.device != dev or v.device != dev:
         raise ValueError(f"k and v must live on {dev}")
     n = k.shape[1]
-    three = ctypes.c_int64 * 3
     rc = _native.load().spec_cache_append(
-        ctypes.byref(c), len_ptr, k.data_ptr(), v.data_ptr(), three(*_strides(k, "k", 1)), three(*_strides(v, "v", 1)),
+        ctypes.byref(c), len_ptr, k.data_ptr(), v.data_ptr(), _Three(*_strides(k, "k", 1)), _Three(*_strides(v, "v", 1)),
         n, 1 if k.dtype == torch.bfloat16 else 0, _optional(num_new, "num_new", torch.int32, (c.batch,), dev),
         _optional(positions, "positions", torch.int32, (c.batch, n), dev), _status(status, dev), _stream(stream, dev))
     if rc:
@@ -185,11 +186,11 @@ def _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent):
         raise ValueError("window and softcap must not be negative")
     f = _native.CacheForm(
         1 / math.sqrt(c.dim) if scale is None else scale, softcap, window,
-        _optional(slopes, "slopes", torch.float32, (heads,), dev),
-        _optional(prefix, "prefix", torch.int32, (c.batch,), dev),
-        _optional(parent, "parent", torch.int32, (c.batch, n), dev),
-        _optional(num_new, "num_new", torch.int32, (c.batch,), dev))
-    return f, n, heads, (ctypes.c_int64 * 3)(*_strides(q, "q", 8))
+        None if slopes is None else _check(slopes, "slopes", torch.float32, (heads,), dev),
+        None if prefix is None else _check(prefix, "prefix", torch.int32, (c.batch,), dev),
+        None if parent is None else _check(parent, "parent", torch.int32, (c.batch, n), dev),
+        None if num_new is None else _check(num_new, "num_new", torch.int32, (c.batch,), dev))
+    return f, n, heads, _Three(*_strides(q, "q", 8))
 
 
 @functools.lru_cache(maxsize=256)

@@ -352,19 +352,46 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
             report(a.status, SPEC_STATUS_BAD_PAGE);
         return;
     }
+    const int log_p = 31 - __clz(P);
     if (tid < n) {
         const int j = a.out_index[((size_t)b * c.kv_heads + h) * a.keep + k * P + tid];
-        const int page = page_of(c, b, j / P);
+        const int page = page_of(c, b, j >> log_p);
         if (page < 0)
             report(a.status, SPEC_STATUS_BAD_PAGE);
         from[tid] = page;
-        row[tid] = j % P;
-        const size_t src = (size_t)max(page, 0) * c.kv_heads + h, dst = ((size_t)to * c.kv_heads + h) * P + tid;
-        had[0][tid] = page < 0 ? 0.0f : c.k_scale[src];
-        had[1][tid] = page < 0 ? 0.0f : c.v_scale[src];
-        a.weights[dst] = page < 0 ? 0.0f : a.weights[src * P + j % P];
+        row[tid] = j & (P - 1);
+    }
+    __syncthreads();
+    // the codes are asked for before the scales that they may have to be changed by
+    const int shift = c.dim == 64 ? 2 : 3;  // 16-byte chunks of a token
+    const int one = n << shift, todo = 2 * one;
+    constexpr int kAtOnce = 4;  // loads in flight
+    uint4 w[kAtOnce];
+    const auto load = [&](int q0) {
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int q = q0 + k * kMoveThreads, side = q >= one, r = q - side * one, i = r >> shift;
+            w[k] = make_uint4(0, 0, 0, 0);
+            if (q < todo && from[i] >= 0) {
+                const int64_t *cs = side ? c.v_stride : c.k_stride;
+                w[k] = *(const uint4 *)((const uint8_t *)(side ? c.v : c.k) + (size_t)from[i] * cs[0] + (size_t)h * cs[1] +
+                                        (size_t)row[i] * cs[2] + (r & ((1 << shift) - 1)) * 16);
+            }
+        }
+    };
+    load(tid);
+    if (tid < n) {
+        const int page = from[tid];
+        const size_t src = (size_t)max(page, 0) * c.kv_heads + h, dst = ((((size_t)to * c.kv_heads + h)) << log_p) + tid;
+        const size_t at = (src << log_p) + row[tid];
+        const float ks = page < 0 ? 0.0f : c.k_scale[src], vs = page < 0 ? 0.0f : c.v_scale[src];
+        const float weight = page < 0 ? 0.0f : a.weights[at];
+        const int position = page < 0 || !c.positions ? 0 : c.positions[at];
+        had[0][tid] = ks;
+        had[1][tid] = vs;
+        a.weights[dst] = weight;
         if (c.positions)
-            c.positions[dst] = page < 0 ? 0 : c.positions[src * P + j % P];
+            c.positions[dst] = position;
     }
     __syncthreads();
     float now[2] = {0.0f, 0.0f};
@@ -379,24 +406,12 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
         float *scale = tid ? c.v_scale : c.k_scale;
         scale[(size_t)to * c.kv_heads + h] = now[tid];
     }
-    const int shift = c.dim == 64 ? 2 : 3;  // 16-byte chunks of a token
-    const int todo = 2 * (n << shift);
-    constexpr int kAtOnce = 4;  // loads in flight
     for (int q0 = tid; q0 < todo; q0 += kAtOnce * kMoveThreads) {
-        uint4 w[kAtOnce];
+        if (q0 != tid)
+            load(q0);
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
-            const int q = q0 + k * kMoveThreads, side = q >= (n << shift), r = q - side * (n << shift), i = r >> shift;
-            w[k] = make_uint4(0, 0, 0, 0);
-            if (q < todo && from[i] >= 0) {
-                const int64_t *cs = side ? c.v_stride : c.k_stride;
-                w[k] = *(const uint4 *)((const uint8_t *)(side ? c.v : c.k) + (size_t)from[i] * cs[0] + (size_t)h * cs[1] +
-                                        (size_t)row[i] * cs[2] + (r & ((1 << shift) - 1)) * 16);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            const int q = q0 + k * kMoveThreads, side = q >= (n << shift), r = q - side * (n << shift), i = r >> shift;
+            const int q = q0 + k * kMoveThreads, side = q >= one, r = q - side * one, i = r >> shift;
             if (q >= todo)
                 break;
             if (from[i] >= 0 && had[side][i] != now[side]) {

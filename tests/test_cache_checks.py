@@ -165,12 +165,12 @@ def test_the_cache_has_four_dimensions():
 
 
 def test_strides():
-    assert cache._strides(torch.zeros(2, 3, 64), "x", 16) == [192, 64]
-    assert cache._strides(torch.zeros(1, 3, 1, 24)[:, :1], "x", 16) == [16, 16, 16]
+    assert cache._strides(torch.zeros(2, 5, 3, 64), "x", 16) == (960, 192, 64)
+    assert cache._strides(torch.zeros(1, 3, 1, 24)[:, :1], "x", 16) == (16, 16, 16)
     with pytest.raises(ValueError, match="multiples of 16"):
-        cache._strides(torch.zeros(2, 3, 24), "x", 16)
+        cache._strides(torch.zeros(2, 2, 3, 24), "x", 16)
     with pytest.raises(ValueError, match="dense"):
-        cache._strides(torch.zeros(2, 16, 32).transpose(1, 2), "x", 16)
+        cache._strides(torch.zeros(2, 2, 16, 32).transpose(2, 3), "x", 16)
 
 
 @pytest.mark.parametrize("t,exc,msg", [
