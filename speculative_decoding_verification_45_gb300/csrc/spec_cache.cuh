@@ -47,15 +47,42 @@ __device__ __forceinline__ float2 decode2(uint16_t two, int code)
     return __half22float2(__half2(h));
 }
 
-// Two values to codes, nearest even; a value that is not finite becomes NaN.
-__device__ __forceinline__ uint16_t encode2(float a, float b, int code)
+// Two finite values to codes, nearest even.
+__device__ __forceinline__ uint16_t encode2_finite(float a, float b, int code)
 {
-    if (!isfinite(a))
-        a = __int_as_float(0x7fffffff);
-    if (!isfinite(b))
-        b = __int_as_float(0x7fffffff);
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, code == SPEC_E4M3 ? __NV_E4M3 : __NV_E5M2);
 }
+
+// Two values to codes; a value that is not finite becomes NaN.
+__device__ __forceinline__ uint16_t encode2(float a, float b, int code)
+{
+    return encode2_finite(isfinite(a) ? a : __int_as_float(0x7fffffff), isfinite(b) ? b : __int_as_float(0x7fffffff), code);
+}
+
+// Codes times f <= 1, to codes.  A power of two is multiplied in 16-bit floats: a
+// product that they do not hold exactly is below half the smallest code.
+struct Mover {
+    float f;
+    __half2 f2;
+    bool halves;
+    __device__ explicit Mover(float factor)
+        : f(factor), f2(__float2half2_rn(factor)), halves(is_pow2(factor))
+    {
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t x, int code) const  // four of them
+    {
+        // an infinity (e5m2) takes the other way, where it becomes NaN
+        if (halves && !(code == SPEC_E5M2 && __vcmpeq4(x & 0x7f7f7f7fu, 0x7c7c7c7cu))) {
+            const __nv_fp8_interpretation_t kind = code == SPEC_E4M3 ? __NV_E4M3 : __NV_E5M2;
+            const __half2 lo = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2((uint16_t)x, kind)), f2),
+                          hi = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2((uint16_t)(x >> 16), kind)), f2);
+            return (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__half2_raw(lo), __NV_SATFINITE, kind) |
+                   (uint32_t)__nv_cvt_halfraw2_to_fp8x2(__half2_raw(hi), __NV_SATFINITE, kind) << 16;
+        }
+        const float2 lo = decode2((uint16_t)x, code), hi = decode2((uint16_t)(x >> 16), code);
+        return (uint32_t)encode2(lo.x * f, lo.y * f, code) | (uint32_t)encode2(hi.x * f, hi.y * f, code) << 16;
+    }
+};
 
 // One sequence's lengths, checked: `len` cached tokens (0 where they are invalid).
 struct Seq {

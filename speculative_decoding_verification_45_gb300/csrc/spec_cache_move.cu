@@ -47,6 +47,13 @@ template <> struct Chunk<__nv_bfloat16> {
         const uint32_t w = i == 0 ? raw.x : i == 1 ? raw.y : i == 2 ? raw.z : raw.w;
         return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
+    __device__ __forceinline__ float largest() const  // magnitude; not finite if a value is not
+    {
+        uint32_t m = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu),
+                              __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
+        m = max(m & 0xffffu, m >> 16);
+        return __uint_as_float(m << 16);
+    }
 };
 template <> struct Chunk<float> {
     float4 lo, hi;
@@ -64,6 +71,14 @@ template <> struct Chunk<float> {
     {
         return i == 0 ? make_float2(lo.x, lo.y) : i == 1 ? make_float2(lo.z, lo.w)
                : i == 2 ? make_float2(hi.x, hi.y) : make_float2(hi.z, hi.w);
+    }
+    __device__ __forceinline__ float largest() const
+    {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // the bits of magnitudes order as they do, and NaN above them
+            m = max(m, max(__float_as_uint(two(i).x) & 0x7fffffffu, __float_as_uint(two(i).y) & 0x7fffffffu));
+        return __uint_as_float(m);
     }
 };
 
@@ -106,6 +121,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
                           15u) == 0;
     Chunk<X> x[kChunks];
     float amax = 0.0f;
+    bool odd = false;  // a value is not finite
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
         const int q = t + j * T;
@@ -117,11 +133,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
         if (t + j * T < todo) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 v = x[j].two(i);
-                amax = isfinite(v.x) ? fmaxf(amax, fabsf(v.x)) : amax;
-                amax = isfinite(v.y) ? fmaxf(amax, fabsf(v.y)) : amax;
+            const float most = x[j].largest();
+            if (isfinite(most)) {
+                amax = fmaxf(amax, most);
+            } else {
+                odd = true;
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = x[j].two(i);
+                    amax = isfinite(v.x) ? fmaxf(amax, fabsf(v.x)) : amax;
+                    amax = isfinite(v.y) ? fmaxf(amax, fabsf(v.y)) : amax;
+                }
             }
         }
     }
@@ -151,25 +172,20 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float2 lo = x[j].two(2 * i), hi = x[j].two(2 * i + 1);
-                w[i] = (uint32_t)encode2(over(lo.x), over(lo.y), c.code) |
-                       (uint32_t)encode2(over(hi.x), over(hi.y), c.code) << 16;
+                w[i] = odd ? (uint32_t)encode2(over(lo.x), over(lo.y), c.code) |
+                                 (uint32_t)encode2(over(hi.x), over(hi.y), c.code) << 16
+                           : (uint32_t)encode2_finite(over(lo.x), over(lo.y), c.code) |
+                                 (uint32_t)encode2_finite(over(hi.x), over(hi.y), c.code) << 16;
             }
             *(uint2 *)(dst + (size_t)(old + (q >> shift)) * cs[2] + (q & (per - 1)) * 8) = make_uint2(w[0], w[1]);
         }
     }
     if (old && now != had) {  // the block's scale grew: its older codes move to the new one
-        const float f = had / now;
+        const Mover move(had / now);
         for (int q = t; q < old * per; q += T) {
             uint2 *p = (uint2 *)(dst + (size_t)(q >> shift) * cs[2] + (q & (per - 1)) * 8);
-            uint2 w = *p;
-            uint32_t r[2] = {w.x, w.y};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 lo = decode2((uint16_t)r[i], c.code), hi = decode2((uint16_t)(r[i] >> 16), c.code);
-                r[i] = (uint32_t)encode2(lo.x * f, lo.y * f, c.code) |
-                       (uint32_t)encode2(hi.x * f, hi.y * f, c.code) << 16;
-            }
-            *p = make_uint2(r[0], r[1]);
+            const uint2 w = *p;
+            *p = make_uint2(move(w.x, c.code), move(w.y, c.code));
         }
     }
     if (t == 0)
@@ -415,15 +431,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
             if (q >= todo)
                 break;
             if (from[i] >= 0 && had[side][i] != now[side]) {
-                const float f = had[side][i] / now[side];
-                uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 lo = decode2((uint16_t)x[e], c.code), hi = decode2((uint16_t)(x[e] >> 16), c.code);
-                    x[e] = (uint32_t)encode2(lo.x * f, lo.y * f, c.code) |
-                           (uint32_t)encode2(hi.x * f, hi.y * f, c.code) << 16;
-                }
-                w[k] = make_uint4(x[0], x[1], x[2], x[3]);
+                const Mover move(had[side][i] / now[side]);
+                w[k] = make_uint4(move(w[k].x, c.code), move(w[k].y, c.code), move(w[k].z, c.code), move(w[k].w, c.code));
             }
             const int64_t *cs = side ? c.v_stride : c.k_stride;
             *(uint4 *)((uint8_t *)(side ? c.v : c.k) + (size_t)to * cs[0] + (size_t)h * cs[1] + (size_t)i * cs[2] +
