@@ -122,11 +122,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     Chunk<X> x[kChunks];
     float amax = 0.0f;
     bool odd = false;  // a value is not finite
+    // a thread's chunks are the same part of every (T / per)-th token
+    const int token = t >> shift, d = (t & (per - 1)) * 8, step = T >> shift;
+    {
+        const X *p = src + (int64_t)(i0 + token) * a.stride[side][1] + d;
+        const int64_t next = (int64_t)step * a.stride[side][1];
 #pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-        const int q = t + j * T;
-        if (q < todo)
-            x[j].load(src + (size_t)(i0 + (q >> shift)) * a.stride[side][1] + (q & (per - 1)) * 8, aligned);
+        for (int j = 0; j < kChunks; ++j, p += next)
+            if (t + j * T < todo)
+                x[j].load(p, aligned);
     }
     float *scale = (side ? c.v_scale : c.k_scale) + (size_t)max(page, 0) * c.kv_heads + h;
     const float had = live && old ? *scale : 0.0f;
@@ -163,23 +167,25 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     const float now = fmaxf(scale_for(amax, c.code), had);
     const int64_t *cs = side ? c.v_stride : c.k_stride;
     uint8_t *dst = (uint8_t *)(side ? c.v : c.k) + (size_t)page * cs[0] + (size_t)h * cs[1];
-    const Divider over(now);
+    const auto write = [&](auto encode) {
+        uint8_t *p = dst + (int64_t)(old + token) * cs[2] + d;
+        const int64_t next = (int64_t)step * cs[2];
 #pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-        const int q = t + j * T;
-        if (q < todo) {
-            uint32_t w[2];
+        for (int j = 0; j < kChunks; ++j, p += next) {
+            if (t + j * T < todo) {
+                uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float2 lo = x[j].two(2 * i), hi = x[j].two(2 * i + 1);
-                w[i] = odd ? (uint32_t)encode2(over(lo.x), over(lo.y), c.code) |
-                                 (uint32_t)encode2(over(hi.x), over(hi.y), c.code) << 16
-                           : (uint32_t)encode2_finite(over(lo.x), over(lo.y), c.code) |
-                                 (uint32_t)encode2_finite(over(hi.x), over(hi.y), c.code) << 16;
+                for (int i = 0; i < 4; ++i)
+                    w[i] = encode(x[j].two(i));
+                *(uint2 *)p = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
             }
-            *(uint2 *)(dst + (size_t)(old + (q >> shift)) * cs[2] + (q & (per - 1)) * 8) = make_uint2(w[0], w[1]);
         }
-    }
+    };
+    const Divider over(now);
+    if (over.exact && !odd)
+        write([&](float2 v) -> uint32_t { return encode2_finite(v.x * over.inv, v.y * over.inv, c.code); });
+    else
+        write([&](float2 v) -> uint32_t { return encode2(over(v.x), over(v.y), c.code); });
     if (old && now != had) {  // the block's scale grew: its older codes move to the new one
         const Mover move(had / now);
         for (int q = t; q < old * per; q += T) {
@@ -351,9 +357,9 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, int blocks)
 {
-    __shared__ int from[kMaxBlock];          // source page of each token, -1: none
-    __shared__ float had[2][kMaxBlock];      // its scales
-    __shared__ int row[kMaxBlock];
+    __shared__ int from[kMaxBlock], row[kMaxBlock];  // source page of each token, -1: none
+    __shared__ float had[2][kMaxBlock];              // its scales
+    __shared__ long long off[2][kMaxBlock];          // where its codes lie, -1: nowhere
     const spec_cache &c = a.c;
     const int P = c.block, tid = threadIdx.x;
     const int k = blockIdx.x % blocks;
@@ -376,26 +382,27 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
             report(a.status, SPEC_STATUS_BAD_PAGE);
         from[tid] = page;
         row[tid] = j & (P - 1);
+        off[0][tid] = page < 0 ? -1 : (long long)page * c.k_stride[0] + (long long)h * c.k_stride[1] + row[tid] * c.k_stride[2];
+        off[1][tid] = page < 0 ? -1 : (long long)page * c.v_stride[0] + (long long)h * c.v_stride[1] + row[tid] * c.v_stride[2];
     }
     __syncthreads();
-    // the codes are asked for before the scales that they may have to be changed by
-    const int shift = c.dim == 64 ? 2 : 3;  // 16-byte chunks of a token
-    const int one = n << shift, todo = 2 * one;
+    // the codes are asked for before the scales that they may have to be changed by; half of the threads move keys, half
+    // values, each the same 16 bytes of every few tokens
+    const int shift = c.dim == 64 ? 2 : 3, side = tid >= kMoveThreads / 2, t = tid & (kMoveThreads / 2 - 1);
+    const int d = (t & ((1 << shift) - 1)) * 16, step = (kMoveThreads / 2) >> shift;
+    uint8_t *codes = (uint8_t *)(side ? c.v : c.k) + d;
+    const int64_t *cs = side ? c.v_stride : c.k_stride;
     constexpr int kAtOnce = 4;  // loads in flight
     uint4 w[kAtOnce];
-    const auto load = [&](int q0) {
+    const auto load = [&](int i0) {
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
-            const int q = q0 + k * kMoveThreads, side = q >= one, r = q - side * one, i = r >> shift;
-            w[k] = make_uint4(0, 0, 0, 0);
-            if (q < todo && from[i] >= 0) {
-                const int64_t *cs = side ? c.v_stride : c.k_stride;
-                w[k] = *(const uint4 *)((const uint8_t *)(side ? c.v : c.k) + (size_t)from[i] * cs[0] + (size_t)h * cs[1] +
-                                        (size_t)row[i] * cs[2] + (r & ((1 << shift) - 1)) * 16);
-            }
+            const int i = i0 + k * step;
+            const long long at = i < n ? off[side][i] : -1;
+            w[k] = at >= 0 ? *(const uint4 *)(codes + at) : make_uint4(0, 0, 0, 0);
         }
     };
-    load(tid);
+    load(t >> shift);
     if (tid < n) {
         const int page = from[tid];
         const size_t src = (size_t)max(page, 0) * c.kv_heads + h, dst = ((((size_t)to * c.kv_heads + h)) << log_p) + tid;
@@ -422,21 +429,27 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
         float *scale = tid ? c.v_scale : c.k_scale;
         scale[(size_t)to * c.kv_heads + h] = now[tid];
     }
-    for (int q0 = tid; q0 < todo; q0 += kAtOnce * kMoveThreads) {
-        if (q0 != tid)
-            load(q0);
+    __shared__ float factor[2][kMaxBlock];  // 1: the codes stay
+    if (tid < n) {
+        factor[0][tid] = from[tid] < 0 ? 1.0f : had[0][tid] / now[0];
+        factor[1][tid] = from[tid] < 0 ? 1.0f : had[1][tid] / now[1];
+    }
+    __syncthreads();
+    uint8_t *out = codes + (size_t)to * cs[0] + (size_t)h * cs[1];
+    for (int i0 = t >> shift; i0 < n; i0 += kAtOnce * step) {
+        if (i0 != t >> shift)
+            load(i0);
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
-            const int q = q0 + k * kMoveThreads, side = q >= one, r = q - side * one, i = r >> shift;
-            if (q >= todo)
+            const int i = i0 + k * step;
+            if (i >= n)
                 break;
-            if (from[i] >= 0 && had[side][i] != now[side]) {
-                const Mover move(had[side][i] / now[side]);
+            const float f = factor[side][i];
+            if (f != 1.0f) {
+                const Mover move(f);
                 w[k] = make_uint4(move(w[k].x, c.code), move(w[k].y, c.code), move(w[k].z, c.code), move(w[k].w, c.code));
             }
-            const int64_t *cs = side ? c.v_stride : c.k_stride;
-            *(uint4 *)((uint8_t *)(side ? c.v : c.k) + (size_t)to * cs[0] + (size_t)h * cs[1] + (size_t)i * cs[2] +
-                       (r & ((1 << shift) - 1)) * 16) = w[k];
+            *(uint4 *)(out + (int64_t)i * cs[2]) = w[k];
         }
     }
 }
