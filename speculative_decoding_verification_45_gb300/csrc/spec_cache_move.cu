@@ -82,7 +82,7 @@ template <> struct Chunk<float> {
     }
 };
 
-template <typename X, int T, int kChunks>
+template <typename X, int T, int kChunks, int CODE>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a)
 {
     constexpr int kUnits = kAppendThreads / T;  // units of a CTA
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     }
     if (!live)
         return;
-    const float now = fmaxf(scale_for(amax, c.code), had);
+    const float now = fmaxf(scale_for(amax, CODE), had);
     const int64_t *cs = side ? c.v_stride : c.k_stride;
     uint8_t *dst = (uint8_t *)(side ? c.v : c.k) + (size_t)page * cs[0] + (size_t)h * cs[1];
     const auto write = [&](auto encode) {
@@ -183,15 +183,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     };
     const Divider over(now);
     if (over.exact && !odd)
-        write([&](float2 v) -> uint32_t { return encode2_finite(v.x * over.inv, v.y * over.inv, c.code); });
+        write([&](float2 v) -> uint32_t { return encode2_finite(v.x * over.inv, v.y * over.inv, CODE); });
     else
-        write([&](float2 v) -> uint32_t { return encode2(over(v.x), over(v.y), c.code); });
+        write([&](float2 v) -> uint32_t { return encode2(over(v.x), over(v.y), CODE); });
     if (old && now != had) {  // the block's scale grew: its older codes move to the new one
         const Mover move(had / now);
         for (int q = t; q < old * per; q += T) {
             uint2 *p = (uint2 *)(dst + (size_t)(q >> shift) * cs[2] + (q & (per - 1)) * 8);
             const uint2 w = *p;
-            *p = make_uint2(move(w.x, c.code), move(w.y, c.code));
+            *p = make_uint2(move(w.x, CODE), move(w.y, CODE));
         }
     }
     if (t == 0)
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
     }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, int blocks)
+template <int CODE> __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, int blocks)
 {
     __shared__ int from[kMaxBlock], row[kMaxBlock];  // source page of each token, -1: none
     __shared__ float had[2][kMaxBlock];              // its scales
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, i
             const float f = factor[side][i];
             if (f != 1.0f) {
                 const Mover move(f);
-                w[k] = make_uint4(move(w[k].x, c.code), move(w[k].y, c.code), move(w[k].z, c.code), move(w[k].w, c.code));
+                w[k] = make_uint4(move(w[k].x, CODE), move(w[k].y, CODE), move(w[k].z, CODE), move(w[k].w, CODE));
             }
             *(uint4 *)(out + (int64_t)i * cs[2]) = w[k];
         }
@@ -460,7 +460,10 @@ template <typename X, int T, int kChunks> spec_status run_append(const AppendArg
     const long long ctas = (units + kAppendThreads / T - 1) / (kAppendThreads / T);
     if (ctas > INT_MAX)
         return SPEC_ERR_UNSUPPORTED;
-    append_kernel<X, T, kChunks><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(a);
+    if (a.c.code == SPEC_E4M3)
+        append_kernel<X, T, kChunks, SPEC_E4M3><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(a);
+    else
+        append_kernel<X, T, kChunks, SPEC_E5M2><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(a);
     return launched();
 }
 
@@ -553,7 +556,10 @@ spec_status spec_cache_evict(const spec_cache *cache, const int32_t *lengths, fl
     st = launched();
     if (st != SPEC_OK)
         return st;
-    move_kernel<<<(unsigned)(heads * blocks), kMoveThreads, 0, s>>>(a, blocks);
+    if (cache->code == SPEC_E4M3)
+        move_kernel<SPEC_E4M3><<<(unsigned)(heads * blocks), kMoveThreads, 0, s>>>(a, blocks);
+    else
+        move_kernel<SPEC_E5M2><<<(unsigned)(heads * blocks), kMoveThreads, 0, s>>>(a, blocks);
     return launched();
 }
 
