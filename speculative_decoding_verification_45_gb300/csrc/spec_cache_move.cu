@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
     }
 }
 
-template <int CODE> __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a, int blocks)
+template <int CODE> __global__ void __launch_bounds__(kMoveThreads, 6) move_kernel(const EvictArgs a, int blocks)
 {
     __shared__ int from[kMaxBlock], row[kMaxBlock];  // source page of each token, -1: none
     __shared__ float had[2][kMaxBlock];              // its scales
