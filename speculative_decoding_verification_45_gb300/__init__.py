@@ -38,6 +38,7 @@ STATUS_BAD_LOGITS = 8
 STATUS_BAD_TREE = 32
 STATUS_BAD_LENGTH = 64  # cache_*: a length or a number of new tokens out of range
 STATUS_BAD_PAGE = 128   # cache_*: a page id out of range
+STATUS_INTERNAL = 256   # cache_*: a bounded wait inside a kernel ran out; the outputs are not valid
 
 MAX_GAMMA = 16
 MAX_TREE_NODES = 256

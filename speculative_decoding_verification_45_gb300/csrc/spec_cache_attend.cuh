@@ -17,7 +17,7 @@
 //
 // Tokens are the M side (128 per tile), query rows the N side: a decode step
 // has few rows (new tokens x query heads per key head), which would fill a
-// fraction of an M = 128 tile, while N may be 16, 32 or 64.  So
+// fraction of an M = 128 tile, while N may be 16, 32 or 48.  So
 //   S^T [128 tokens, NT rows] = K [128, D] Q^T        (K is K-major as stored)
 //   O^T [D, NT rows]          = V^T [D, 128] P^T      (V is M-major as stored)
 // and a thread of the softmax owns one token and NT / 2 rows, with every lane
@@ -672,14 +672,17 @@ template <int NT> struct Walk {
         long long skip = r.skip, each = 0;
         for (int k = 0; k < a.row_tiles; ++k)
             each += row_unit<NT>(a, b, k).count;
-        h = (int)(skip / each);
+        h = (int)(skip / max(each, 1ll));
         skip -= (long long)h * each;
-        while (true) {
+        for (; rt < a.row_tiles; ++rt) {
             u = row_unit<NT>(a, b, rt);
             if (skip < u.count)
                 break;
             skip -= u.count;
-            ++rt;
+        }
+        if (rt == a.row_tiles || h >= a.c.kv_heads) {  // lengths that changed while they were read
+            at = end;
+            return;
         }
         x0 = (int)skip;
         x1 = (int)min((long long)u.count, x0 + (end - at));
@@ -702,7 +705,11 @@ template <int NT> struct Walk {
                     some = __ballot_sync(0xffffffffu,
                                          k < a.c.batch && sequence(a.c, a.lengths, a.f.num_new, a.n, k, true).m > 0);
                 } while (!some && b0 + 32 < a.c.batch);
-                b = b0 + max(__ffs(some) - 1, 0);
+                if (!some) {
+                    at = end;
+                    return;
+                }
+                b = b0 + __ffs(some) - 1;
             }
         }
         u = row_unit<NT>(a, b, rt);
@@ -722,24 +729,29 @@ template <int NT> struct Walk {
 //   adding       one warpgroup: adds the tiles' O^T up in registers, writes the results
 // Tile g: S^T(g) in tensor memory; warpgroup g % NW turns it into P^T in shared
 // memory; O^T(g) = V^T P^T.  A tile's softmax is a chain of short dependent
-// steps (about 3000 cycles when one pair of warpgroups shared each tile, of
-// 3900 a tile in all), so what counts is how many such chains run side by side.
+// steps, so several run side by side, each on a tile of its own.
 //
 // O^T of a tile is read out and added in 32 bits, scaled by a power of two per
 // row and tile: the weights of a tile go by that tile's own maximum (not a
 // running one), so a light tail after a heavy token keeps its bits.
 //
 // The exponents' base: exp2(x - base) in 32 bits has room for 2^127, so a
-// warpgroup sets a row's base at the first tile that the row sees and moves it
-// only when a later score passes it by 2^64: no running maximum has to be agreed
-// upon before the exponentials.  What the 8-bit weights need is the maximum's
-// exponent only: 16-bit halves of the exponentials are compared two at a time
-// (16 shuffles for 32 columns) and the four warps meet in shared memory.
+// warpgroup keeps a row's base (0, unless the row's first scores lie far below)
+// until a score passes it by 2^64: no running maximum has to be agreed upon
+// before the exponentials.  What the 8-bit weights need is the maximum's exponent
+// only: 16-bit halves of the exponentials are compared two at a time (9 shuffles
+// for 16 columns) and the four warps meet in shared memory.
 //
-// Four softmax warpgroups want few registers and a short program: columns are
-// taken 16 at a time by the same instructions (with all columns unrolled, warps
-// waited for instructions more than for anything else), exponentials and running
-// totals live in tensor memory between the passes.
+// What bounds it: up to 48 rows a key head, memory (2 D bytes a token; 64
+// sequences of 4,000 to 8,000 tokens, 20 rows: 152 us, 5.4 TB/s; one token per
+// sequence, 4 rows: 143 us, 5.7 TB/s, of 6.8 that a copy reaches), and between
+// units the filling and draining of this chain, about 5,000 cycles each (256
+// sequences of 1,000 to 2,000 tokens: 193 us for 828 MB).  With a cap or a bias,
+// or more rows, the softmax's instructions: about 900 issue slots of an SM
+// quarter for a tile of 32 columns, issued at 0.5 to 0.6 a cycle.  The program
+// has to stay short: columns are taken 16 at a time by the same instructions
+// (all unrolled, warps waited for instructions more than for anything else),
+// exponentials and running totals live in tensor memory between the passes.
 template <int D, int NT> struct AttendShape {
     static constexpr int NW = NT == 16 ? 4 : 3;  // softmax warpgroups (four at 32 columns, with fewer registers each: 1 to 5% slower)
     static constexpr int kThreads = 128 * (2 + NW);
@@ -1689,7 +1701,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         const Unit all = unit_for(a, b, 0, a.n - 1);
         if (skip >= (long long)all.count * a.c.kv_heads) {
             skip = 0;
-            ++b;
+            if (++b == a.c.batch)
+                break;
             continue;
         }
         const int h = (int)(skip / all.count), x0 = (int)(skip % all.count);

@@ -97,6 +97,71 @@ def test_many_short_sequences(sv):
     check_both(sv, Case(lengths, 2, heads=6, kv_heads=3, num_new=new, seed=20))
 
 
+def test_more_sequences_than_threads(sv):
+    lengths = [1 + (b * 13) % 60 for b in range(1300)]
+    new = [(b % 5) > 0 for b in range(1300)]  # every fifth asks nothing
+    check_both(sv, Case(lengths, 1, heads=1, kv_heads=1, num_new=new, seed=22))
+
+
+def test_nobody_asks(sv):
+    case = Case([50, 300], 2, num_new=[0, 0])
+    _, _, (out, lse) = case.run(sv)
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_odd_queries_stay_in_their_rows(sv):
+    """NaN, infinities and zeros in some rows; the others are as without them."""
+    case = Case([200, 333], 3, heads=8, kv_heads=2, dim=128, seed=23)
+    ref = case.reference()
+    case.q[0, 1, 3, 7] = math.nan
+    case.q[1, 2, 0, :] = math.inf
+    case.q[1, 0, 5, 100] = -math.inf
+    _, _, (out, lse) = case.run(sv)
+    odd = torch.zeros(2, 3, 8, dtype=torch.bool)
+    odd[0, 1, 3] = odd[1, 2, 0] = odd[1, 0, 5] = True
+    assert torch.isnan(out.cpu()[odd]).all() and torch.isnan(lse.cpu()[odd]).all()
+    out, lse = out.cpu(), lse.cpu()
+    for key in ("out", "lse", "mean", "dx"):
+        ref[key][odd] = 0
+    out[odd], lse[odd] = 0, 0
+    check_attend(ref, out, lse)
+
+
+def test_pages_past_four_gigabytes(sv):
+    """The same tokens on the first pages of a small pool and the last ones of a large one give the same bits."""
+    pages, heads, block, dim = 36000, 8, 128, 128  # 4.7 GB each side
+    small = cr.Pool(12, heads, block, dim, positions=True, seed=24)
+    table, out_table = torch.arange(8).reshape(2, 4).int(), torch.tensor([[8, 9], [10, 11]]).int()
+    g = torch.Generator().manual_seed(24)
+    q = torch.randn(2, 3, 16, dim, generator=g).to(torch.bfloat16).cuda()
+    new = torch.randn(2, 3, heads, dim, generator=g).to(torch.bfloat16).cuda()
+    weights = torch.rand(12, heads, block, generator=g)
+    lens = torch.tensor([300, 411]).int().cuda()
+    slopes = torch.rand(16, generator=g).cuda()
+    got = []
+    for base in (0, pages - 12):
+        n = 12 if base == 0 else pages
+        a = small.to(sv)
+        if base:
+            big = []
+            for t in a:
+                x = torch.zeros((n, *t.shape[1:]), dtype=torch.uint8 if t.element_size() == 1 else t.dtype, device="cuda")
+                x[base:] = t.view(torch.uint8) if t.element_size() == 1 else t
+                big.append(x.view(t.dtype))
+            a = sv.KVCache(*big)
+        w = torch.zeros(n, heads, block, device="cuda")
+        w[base:] = weights.cuda()
+        t, o = (table + base).cuda(), (out_table + base).cuda()
+        sv.cache_append(a, t, lens, new, new)
+        out, lse = sv.cache_attend(q, a, t, lens + 3, slopes=slopes)
+        sv.cache_weigh(q, a, t, lens + 3, lse, w, slopes=slopes)
+        kept, index = sv.cache_evict(a, t, lens + 3, w, 200, 20, o)
+        got.append([out, lse, kept, index, w[base:], a.k.view(torch.uint8)[base:], a.v.view(torch.uint8)[base:],
+                    a.k_scale[base:], a.v_scale[base:], a.positions[base:]])
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
 def test_many_row_tiles(sv):
     """More queries than one row tile holds, in sequences that are hardly longer."""
     lengths = [70 + 9 * b for b in range(24)]
