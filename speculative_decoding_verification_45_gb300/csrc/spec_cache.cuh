@@ -59,6 +59,13 @@ __device__ __forceinline__ uint16_t encode2(float a, float b, int code)
     return encode2_finite(isfinite(a) ? a : __int_as_float(0x7fffffff), isfinite(b) ? b : __int_as_float(0x7fffffff), code);
 }
 
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)  // of unsigned 16-bit halves
+{
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Codes times f <= 1, to codes.  A power of two is multiplied in 16-bit floats: a
 // product that they do not hold exactly is below half the smallest code.
 struct Mover {

@@ -407,13 +407,6 @@ template <int NT> struct Columns {
     int up[kMaxNodes];
 };
 
-__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)  // of unsigned 16-bit halves
-{
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 // Two values as pairs of e4m3: what 4 bits hold of them, and of the rest.
 __device__ __forceinline__ void split8(float x0, float x1, uint32_t &first, uint32_t &rest)
 {

@@ -26,6 +26,7 @@ struct AppendArgs {
     const void *x[2];
     int64_t stride[2][3];
     int n, blocks;  // blocks a sequence may touch
+    uint32_t units;
     uint32_t *status;
 };
 
@@ -49,8 +50,8 @@ template <> struct Chunk<__nv_bfloat16> {
     }
     __device__ __forceinline__ float largest() const  // magnitude; not finite if a value is not
     {
-        uint32_t m = __vmaxu2(__vmaxu2(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu),
-                              __vmaxu2(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
+        uint32_t m = max_halves(max_halves(raw.x & 0x7fff7fffu, raw.y & 0x7fff7fffu),
+                                max_halves(raw.z & 0x7fff7fffu, raw.w & 0x7fff7fffu));
         m = max(m & 0xffffu, m >> 16);
         return __uint_as_float(m << 16);
     }
@@ -88,14 +89,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     constexpr int kUnits = kAppendThreads / T;  // units of a CTA
     const spec_cache &c = a.c;
     const int sub = threadIdx.x / T, t = threadIdx.x % T;
-    const long long units = (long long)c.batch * a.blocks * c.kv_heads * 2;
-    const long long u = (long long)blockIdx.x * kUnits + sub;
-    const bool here = u < units;
-    const long long u1 = here ? u : 0;
-    const int side = (int)(u1 & 1);
-    const int h = (int)((u1 >> 1) % c.kv_heads);
-    const long long u2 = (u1 >> 1) / c.kv_heads;
-    const int k = (int)(u2 % a.blocks), b = (int)(u2 / a.blocks);
+    // 32-bit quotients: in 64 bits they were half of the kernel's instructions
+    const uint32_t u = blockIdx.x * kUnits + sub;
+    const bool here = u < a.units;
+    const uint32_t u1 = here ? u : 0, u2 = (u1 >> 1) / (uint32_t)c.kv_heads, u3 = u2 / (uint32_t)a.blocks;
+    const int side = (int)(u1 & 1), h = (int)((u1 >> 1) - u2 * c.kv_heads), k = (int)(u2 - u3 * a.blocks), b = (int)u3;
     const Seq s = sequence(c, a.lengths, a.num_new, a.n, b, false);
     if (here && t == 0 && !s.ok && k == 0 && side == 0 && h == 0)
         report(a.status, SPEC_STATUS_BAD_LENGTH);
@@ -454,12 +452,13 @@ template <int CODE> __global__ void __launch_bounds__(kMoveThreads, 6) move_kern
     }
 }
 
-template <typename X, int T, int kChunks> spec_status run_append(const AppendArgs &a, cudaStream_t stream)
+template <typename X, int T, int kChunks> spec_status run_append(AppendArgs a, cudaStream_t stream)
 {
     const long long units = (long long)a.c.batch * a.blocks * a.c.kv_heads * 2;
     const long long ctas = (units + kAppendThreads / T - 1) / (kAppendThreads / T);
-    if (ctas > INT_MAX)
+    if (units > INT_MAX)
         return SPEC_ERR_UNSUPPORTED;
+    a.units = (uint32_t)units;
     if (a.c.code == SPEC_E4M3)
         append_kernel<X, T, kChunks, SPEC_E4M3><<<(unsigned)ctas, kAppendThreads, 0, stream>>>(a);
     else
