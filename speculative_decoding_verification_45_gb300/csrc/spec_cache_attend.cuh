@@ -1805,7 +1805,6 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                         const float pos = FORM && a.f.slopes ? (a.c.positions ? (float)info.pos[t] : (float)j) : 0.0f;
                         const Mask<NT> see = edge && cached ? seen_by<NT>(a, askers, sh.col, j) : 0;
                         float *weight = a.weights + ((size_t)(cached ? page : 0) * a.c.kv_heads + h) * P + (t & (P - 1));
-                        const float before = cached ? *weight : 0.0f;
                         mbar_wait(&sh.s_full[w], (g / NW) & 1, dead);
                         tc_after();
                         float sum = 0.0f;
@@ -1838,8 +1837,10 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                             mbar_arrive(&sh.s_free[w]);
                             mbar_arrive(&sh.empty[st]);
                         }
+                        // one addition a token and row tile, those of several row tiles a barrier apart: no order is left open,
+                        // and nothing waits for the weight's old value
                         if (cached)
-                            *weight = before + sum;
+                            atomicAdd(weight, sum);
                     }
                     ++g;
                     if (++st == ST) {
