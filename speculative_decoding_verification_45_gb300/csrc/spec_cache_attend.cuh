@@ -716,7 +716,8 @@ template <int NT> struct Walk {
 // ===========================================================================
 // One persistent CTA per SM, each warp with one job:
 //   queries      walks the CTA's segments, one ahead: describes them, splits their queries
-//   producer     block table, TMA of the blocks, their scales
+//   producer     block table, TMA of the blocks, their scales (at 16 columns one
+//                for keys and one for values: about 600 cycles a tile and side)
 //   scores, values   issue one of the two matrix products each
 //   softmax      NW warpgroups, tiles in turn; a thread owns one token and all columns
 //   adding       one warpgroup: adds the tiles' O^T up in registers, writes the results
@@ -746,8 +747,9 @@ template <int NT> struct Walk {
 // (all unrolled, warps waited for instructions more than for anything else),
 // exponentials and running totals live in tensor memory between the passes.
 template <int D, int NT> struct AttendShape {
-    static constexpr int NW = NT == 16 ? 4 : 3;  // softmax warpgroups (four at 32 columns, with fewer registers each: 1 to 5% slower)
-    static constexpr int kThreads = 128 * (2 + NW);
+    static constexpr int NW = 3;                                // softmax warpgroups (four at 32 columns, with fewer registers each: 1 to 5% slower)
+    static constexpr int NP = NT == 16 ? 2 : 1;                 // producers: one for each side, or one for both
+    static constexpr int kThreads = 128 * (1 + NW) + 32 * (3 + NP);
     static constexpr int NO = NT == 48 ? 1 : 2;                 // O^T at a time (one: room to keep the exponentials)
     static constexpr int kBytes = kTile * D;                    // one side of a tile
     static constexpr int KS = 3, VS = D == 64 || NT == 16 ? 8 : NT >= 48 ? 5 : 6;  // tiles of keys and values in shared memory
@@ -896,7 +898,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
     using S = AttendShape<D, NT>;
     using Shared = AttendShared<D, NT>;
     constexpr int NW = S::NW, KS = S::KS, VS = S::VS, kRing = S::kRing;
-    constexpr int kQueries = 4 * (1 + NW), kProducer = kQueries + 1, kScores = kQueries + 2, kValues = kQueries + 3, NO = S::NO;
+    constexpr int kQueries = 4 * (1 + NW), kScores = kQueries + 1, kValues = kQueries + 2, kProducer = kQueries + 3, NO = S::NO;
     constexpr int OC = D == 128 ? NT : NT / 2;  // columns of an adding thread
     constexpr uint32_t kO = NW * NT, kL = kO + NO * NT;  // S^T at 0, then O^T, then the totals
     extern __shared__ uint8_t raw[];
@@ -1039,8 +1041,9 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 break;
             }
         }
-    } else if (wid == kProducer) {
+    } else if (wid >= kProducer) {
         // ---------------- producer ----------------
+        const bool keys = S::NP == 1 || wid == kProducer, values = S::NP == 1 || wid != kProducer;
         if (lane < 2)
             asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &vmap : &kmap));
         int ks = 0, vs = 0;
@@ -1073,20 +1076,23 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 const int got = __shfl_sync(0xffffffffu, pages, (at_x * blocks + lane) & 31);
                 const int page = lane < blocks ? got : -2;
                 const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
-                if (page != -2 && !ok)
+                if (values && page != -2 && !ok)
                     report(a.status, SPEC_STATUS_BAD_PAGE);
                 const uint32_t came = __ballot_sync(0xffffffffu, ok);
                 const size_t at = (size_t)max(page, 0) * a.c.kv_heads + h;
-                bool go = __all_sync(0xffffffffu, mbar_wait(&sh.k_empty[ks], k_phase, dead));
-                if (go) {
+                bool go = true;
+                if (keys)
+                    go = __all_sync(0xffffffffu, mbar_wait(&sh.k_empty[ks], k_phase, dead));
+                if (keys && go) {
                     if (lane == 0)
                         mbar_expect(&sh.k_full[ks], (uint32_t)__popc(came) * (uint32_t)(P * D));
                     __syncwarp();
                     if (ok)
                         tma_load(&kmap, sh.k[ks] + lane * P * D, &sh.k_full[ks], 0, 0, h, page);
                 }
-                go = __all_sync(0xffffffffu, mbar_wait(&sh.v_empty[vs], v_phase, dead)) && go;
-                if (go) {
+                if (values)
+                    go = __all_sync(0xffffffffu, mbar_wait(&sh.v_empty[vs], v_phase, dead)) && go;
+                if (values && go) {
                     StageInfo &info = sh.info[vs];
                     if (lane == 0) {
                         info.came = came;
@@ -1102,8 +1108,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     }
                     if (lane < blocks)
                         copies_arrive(&sh.v_full[vs]);
-                    ++issued;
                 }
+                issued += go;
                 if (++ks == KS) {
                     ks = 0;
                     k_phase ^= 1;
@@ -1114,8 +1120,10 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 }
             }
         }
-        drain<KS>(sh.k_full, issued, dead, a.status);
-        drain<VS>(sh.v_full, issued, dead, a.status);
+        if (keys)
+            drain<KS>(sh.k_full, issued, dead, a.status);
+        if (values)
+            drain<VS>(sh.v_full, issued, dead, a.status);
     } else if (wid == kScores) {
         // ---------------- S^T = K Q^T ----------------
         const uint32_t desc = instr_desc(NT, a.c.code, false, false);
@@ -1625,10 +1633,10 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 // adds its columns up, so a sum needs no other thread and no atomic.  Three
 // warpgroups take tiles in turn.  Keys only: half of what attention reads.
 constexpr int kWeighGroups = 3;  // 55 us for 32 sequences of 8192 tokens; two took 60, four 56
-constexpr int kWeighThreads = 128 * kWeighGroups + 64;
+constexpr int kWeighThreads = 128 * kWeighGroups + 96;
 
 template <int D, int NT> struct WeighShared {
-    static constexpr int kStages = 10, kAlloc = NT * kWeighGroups <= 64 ? 64 : NT * kWeighGroups <= 128 ? 128 : 256;
+    static constexpr int kStages = 10, kAlloc = 2 * NT * kWeighGroups <= 128 ? 128 : 2 * NT * kWeighGroups <= 256 ? 256 : 512;
     alignas(1024) uint8_t tiles[kStages][kTile * D];
     alignas(1024) uint8_t q[2][NT * D];
     alignas(16) Columns<NT> col;
@@ -1649,7 +1657,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     weigh_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap kmap)
 {
     using Shared = WeighShared<D, NT>;
-    constexpr int ST = Shared::kStages, NW = kWeighGroups, kProducer = 4 * NW, kProducts = kProducer + 1;
+    constexpr int ST = Shared::kStages, NW = kWeighGroups, kProducts = 4 * NW, kProducer = kProducts + 1;
     extern __shared__ uint8_t raw[];
     Shared &sh = *(Shared *)(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
     const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -1705,7 +1713,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
             const int low = all.tile(x0), high = all.tile(x1 - 1);
             if (u.count == 0 || !(low < u.head_tiles || (high >= u.low && low < u.low + u.count - u.head_tiles)))
                 continue;  // no tile of the stretch
-            if (wid == kProducer) {
+            if (wid >= kProducer) {
                 // ---------------- producer ----------------
                 const int32_t *table = a.c.block_table + (size_t)b * a.c.table_stride;
                 const int batch = 32 / blocks;  // tiles whose table entries come together, a batch ahead
@@ -1730,9 +1738,10 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                     const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
                     if (page != -2 && !ok)
                         report(a.status, SPEC_STATUS_BAD_PAGE);
-                    if (__all_sync(0xffffffffu, mbar_wait(&sh.empty[st], phase ^ 1, dead))) {
+                    if ((int)(g++ & 1) == wid - kProducer &&  // two producers, tiles in turn
+                        __all_sync(0xffffffffu, mbar_wait(&sh.empty[st], phase ^ 1, dead))) {
                         load_keys<D>(a, &kmap, h, page, ok, blocks, sh.info[st], sh.tiles[st], &sh.full[st], lane);
-                        ++issued;
+                        issued = g;
                     }
                     if (++st == ST) {
                         st = 0;
@@ -1741,7 +1750,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                 }
             } else if (wid == kProducts) {
                 // ---------------- products ----------------
-                const uint32_t desc = instr_desc(NT, a.c.code, false, false);
+                const uint32_t desc = instr_desc(2 * NT, a.c.code, false, false);  // both terms' columns side by side
                 mbar_wait(&sh.q_ready, seg++ & 1, dead);
                 for (int x = x0; x < x1; ++x) {
                     if (!covers(u, all.tile(x)))
@@ -1753,10 +1762,8 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                         const uint64_t kd = smem_desc(smem_u32(sh.tiles[st]), 16, 8 * D, D == 128 ? 2 : 4),
                                        qd = smem_desc(smem_u32(sh.q[0]), 16, 8 * D, D == 128 ? 2 : 4);
 #pragma unroll
-                        for (int d = 0; d < D / 32; ++d) {
-                            tc_mma(tmem + (g % NW) * NT, kd + (d * 32 >> 4), qd + (d * 32 >> 4), desc, d > 0);
-                            tc_mma(tmem + (g % NW) * NT, kd + (d * 32 >> 4), qd + ((NT * D + d * 32) >> 4), desc, true);
-                        }
+                        for (int d = 0; d < D / 32; ++d)
+                            tc_mma(tmem + (g % NW) * 2 * NT, kd + (d * 32 >> 4), qd + (d * 32 >> 4), desc, d > 0);
                         tc_commit(&sh.s_full[g % NW]);
                         tc_commit(&sh.empty[st]);
                     }
@@ -1811,8 +1818,15 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
 #pragma unroll 1
                         for (int c0 = 0; c0 < NT; c0 += 16) {
                             alignas(8) float e[16];
-                            TmemLoad<16>::go(tmem + ((uint32_t)(wid & 3) << 21) + w * NT + c0, e);
+                            alignas(8) float rest[16];
+                            const uint32_t at = tmem + ((uint32_t)(wid & 3) << 21) + w * 2 * NT + c0;
+                            TmemLoad<16>::go(at, e);
+                            TmemLoad<16>::go(at + NT, rest);
                             tmem_wait<16>(e);
+                            tmem_wait<16>(rest);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                ((float2 *)e)[c] = add2(((float2 *)e)[c], ((float2 *)rest)[c]);
                             scores<FORM>(a, sh.col, sh.col.less, c0, ks, pos, e);
 #pragma unroll
                             for (int c = 0; c < 16; ++c)
@@ -1853,8 +1867,12 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         at += x1 - x0;
         skip += x1 - x0;
     }
-    if (wid == kProducer)
-        drain<ST>(sh.full, issued, dead, a.status);
+    if (wid >= kProducer && *dead) {  // the copies of this producer's last tiles land
+        for (int t = (int)issued - 1; t >= 0 && t + ST >= (int)issued; t -= 2)
+            for (uint32_t k = 0; k < 4096 && !mbar_try(&sh.full[t % ST], (t / ST) & 1); ++k)
+                ;
+        report(a.status, SPEC_STATUS_INTERNAL);
+    }
     if (wid == kProducts)
         drain_products(&sh.drained, dead);
     tc_before();
