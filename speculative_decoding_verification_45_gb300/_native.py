@@ -12,13 +12,14 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
+CACHE = os.path.join(CSRC, "cache")
 # The host unit, one unit per (dtype, proposal form) of kernels, and the cache's four: compiled in parallel.
-SOURCES = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "kernels_bf16.cu", "kernels_bf16_point.cu",
-                                            "kernels_f32.cu", "kernels_f32_point.cu", "spec_cache_move.cu",
-                                            "spec_cache_attend.cu", "spec_cache_attend_d64.cu",
-                                            "spec_cache_attend_d128.cu")]
+SOURCES = ([os.path.join(CSRC, f) for f in ("spec_verify.cu", "kernels_bf16.cu", "kernels_bf16_point.cu",
+                                             "kernels_f32.cu", "kernels_f32_point.cu")]
+           + [os.path.join(CACHE, f) for f in ("spec_cache_move.cu", "spec_cache_attend.cu",
+                                               "spec_cache_attend_d64.cu", "spec_cache_attend_d128.cu")])
 HEADERS = [os.path.join(INCLUDE, "spec_verify.h"), os.path.join(CSRC, "spec_verify_kernels.cuh"),
-           os.path.join(CSRC, "spec_cache.cuh"), os.path.join(CSRC, "spec_cache_attend.cuh")]
+           os.path.join(CACHE, "spec_cache.cuh"), os.path.join(CACHE, "spec_cache_attend.cuh")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libspec_verify.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -72,7 +73,7 @@ def _run(cmd):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/*.cu for sm_103a (one nvcc per unit, in parallel) and link
+    """Compile csrc/*.cu and csrc/cache/*.cu for sm_103a (one nvcc per unit, in parallel) and link
     _build/libspec_verify.so."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     if not force and not _stale():
