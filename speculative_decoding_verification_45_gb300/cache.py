@@ -24,6 +24,7 @@ from . import _native
 
 _CODES = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 MAX_TREE_NODES = 256
+_BLOCKS, _DIMS = (16, 32, 64, 128), (64, 128)
 _Three = ctypes.c_int64 * 3
 
 
@@ -53,15 +54,16 @@ def _fail(rc: int, where: str):
 
 
 def _check(t, name, dtype, shape, device):
+    """The address of a tensor that is what it has to be."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must live on {device}, found {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _strides(t, name, multiple):
@@ -92,7 +94,7 @@ def _describe(cache, block_table, lengths):
     if v.shape != shape or v.device != dev:
         raise ValueError(f"cache.v: expected shape {tuple(shape)} on {dev}, got {tuple(v.shape)} on {v.device}")
     pages, heads, block, dim = shape
-    if block not in (16, 32, 64, 128) or dim not in (64, 128):
+    if block not in _BLOCKS or dim not in _DIMS:
         raise ValueError(f"cache: block must be 16, 32, 64 or 128 and dim 64 or 128, got {block} and {dim}")
     if block_table.dim() != 2:
         raise ValueError("block_table must be a [batch, blocks] tensor")
@@ -103,14 +105,11 @@ def _describe(cache, block_table, lengths):
     c = _native.Cache(
         k.data_ptr(), v.data_ptr(), _check(k_scale, "cache.k_scale", torch.float32, (pages, heads), dev),
         _check(v_scale, "cache.v_scale", torch.float32, (pages, heads), dev),
-        _optional(positions, "cache.positions", torch.int32, (pages, heads, block), dev), block_table.data_ptr(),
+        None if positions is None else _check(positions, "cache.positions", torch.int32, (pages, heads, block), dev),
+        block_table.data_ptr(),
         _strides(k, "cache.k", 16), _strides(v, "cache.v", 16), step if batch > 1 else blocks, batch,
         blocks, pages, heads, block, dim, code)
     return c, dev, _check(lengths, "lengths", torch.int32, (batch,), dev)
-
-
-def _optional(t, name, dtype, shape, device):
-    return None if t is None else _check(t, name, dtype, shape, device)
 
 
 def _status(t, device):
@@ -164,10 +163,11 @@ def cache_append(cache, block_table, lengths, k, v, num_new=None, positions=None
     if k.device != dev or v.device != dev:
         raise ValueError(f"k and v must live on {dev}")
     n = k.shape[1]
+    new = None if num_new is None else _check(num_new, "num_new", torch.int32, (c.batch,), dev)
+    pos = None if positions is None else _check(positions, "positions", torch.int32, (c.batch, n), dev)
     rc = _native.load().spec_cache_append(
         ctypes.byref(c), len_ptr, k.data_ptr(), v.data_ptr(), _Three(*_strides(k, "k", 1)), _Three(*_strides(v, "v", 1)),
-        n, 1 if k.dtype == torch.bfloat16 else 0, _optional(num_new, "num_new", torch.int32, (c.batch,), dev),
-        _optional(positions, "positions", torch.int32, (c.batch, n), dev), _status(status, dev), _stream(stream, dev))
+        n, 1 if k.dtype == torch.bfloat16 else 0, new, pos, _status(status, dev), _stream(stream, dev))
     if rc:
         _fail(rc, "spec_cache_append")
 
