@@ -715,7 +715,7 @@ template <int NT> struct Walk {
 // Attention
 // ===========================================================================
 // One persistent CTA per SM, each warp with one job:
-//   queries      walks the CTA's segments, one ahead: describes them, splits their queries
+//   queries      walks the CTA's segments: describes them two ahead, brings in their split queries
 //   producer     block table, TMA of the blocks, their scales (at 16 columns one
 //                for keys and one for values: about 600 cycles a tile and side)
 //   scores, values   issue one of the two matrix products each
@@ -886,7 +886,7 @@ __device__ __forceinline__ Mask<NT> seen_by(const AttendArgs &a, const Askers &k
         }
     }
     if (a.f.window > 0 && (long long)t + a.f.window <= k.i1)
-        see &= low_bits<NT>((t + a.f.window) * k.group - k.r0);
+        see &= low_bits<NT>(max(t + a.f.window, 0) * k.group - k.r0);  // far below, the product would pass 32 bits
     return see;
 }
 

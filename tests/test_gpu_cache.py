@@ -279,6 +279,28 @@ def test_a_heavy_first_token_and_a_long_light_tail(sv):
     check_both(sv, case)
 
 
+def far_out(case, times):
+    """The case's table with its first page `times` over, and the lengths to match."""
+    table = torch.cat([case.table[:, :1].expand(-1, times), case.table[:, 1:]], 1).contiguous()
+    return table.cuda(), (case.lengths + (times - 1) * case.pool.block).int().cuda()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_window_far_from_its_prefix(sv, dim):
+    """Between the prefix and the window lie 200 million tokens that nobody sees."""
+    case = Case([300], 2, heads=20, kv_heads=1, dim=dim, block=128, window=4, prefix=[5], seed=31)
+    ref, _, lse = check_both(sv, case)
+    cache = case.pool.to(sv)
+    table, lengths = far_out(case, 1562500)
+    f = {k: dev(v) for k, v in case.form.items()}
+    out, lse = sv.cache_attend(case.q.cuda(), cache, table, lengths, **f)
+    check_attend(ref, out, lse)
+    w = torch.zeros(len(case.pool.codes[0]), 1, 128)
+    got = sv.cache_weigh(case.q.cuda(), cache, table, lengths, lse, w.cuda(), **f)
+    want, bound = cr.weigh(case.pool, case.table, case.lengths, ref, lse.cpu(), w)
+    assert ((got.cpu().double() - want).abs() <= bound).all()
+
+
 def test_blocks_of_very_different_value_scales(sv):
     case = Case([256], 1, dim=64, seed=13)
     for blk in range(case.table.shape[1]):
