@@ -398,14 +398,16 @@ template <int THREADS, typename Cost> __device__ __forceinline__ Range find_rang
 // What both kernels keep in shared memory for the columns (query rows) of a row tile
 // ---------------------------------------------------------------------------
 template <int NT> struct Columns {
-    float factor[NT];  // of the accumulator, times the token's scale: the score, in units of log2 (of softcap with one)
+    alignas(16) float factor[NT];  // of the accumulator, times the token's scale: the score, in units of log2 (of softcap with one)
     float less[NT];    // weigh: the row's -lse, in units of log2
     float slope[NT];   // times -log2(e)
-    float pos[NT];
+    float pos[NT];     // position, from origin on
+    int origin;        // position of the first column's query: differences keep their bits however far out they lie
     int query[NT];     // its query, -1: none
     uint32_t kin[NT][kMaxNodes / 32];
     int up[kMaxNodes];
 };
+static_assert(sizeof(Columns<16>) % 16 == 0 && sizeof(Columns<48>) % 16 == 0, "copies arrive at 16 bytes");
 
 // Two values as pairs of e4m3: what 4 bits hold of them, and of the rest.
 __device__ __forceinline__ void split8(float x0, float x1, uint32_t &first, uint32_t &rest)
@@ -513,25 +515,37 @@ __device__ __forceinline__ void load_queries(const AttendArgs &a, int b, int h, 
     bulk_load(a.factor + tile * NT, col.factor, 4 * NT, bar);
 }
 
+// The position that token j has in its text, for the bias.
+__device__ __forceinline__ int position_of(const AttendArgs &a, int b, int h, int j)
+{
+    if (!a.c.positions)
+        return j;
+    const int page = page_of(a.c, b, j / a.c.block);
+    return page < 0 ? 0 : a.c.positions[((size_t)page * a.c.kv_heads + h) * a.c.block + j % a.c.block];
+}
+
+// p - origin, rounded once.
+__device__ __forceinline__ float from_origin(int p, int origin)
+{
+    return (float)((long long)p - origin);
+}
+
 // The columns' other constants, by THREADS threads; ends without a barrier.
 template <int NT, int THREADS, typename Unit>
 __device__ __forceinline__ void describe_columns(const AttendArgs &a, const Unit &u, int b, int h, int rt, bool tree,
                                                  Columns<NT> &col, int t)
 {
     const RowAt at(a, rt * NT);
+    const int origin = a.f.slopes && at.i0 <= u.i1 ? position_of(a, b, h, u.first + at.i0) : 0;
+    if (t == 0)
+        col.origin = origin;
     for (int c = t; c < NT; c += THREADS) {
         int i, g;
         at.of(a, c, i, g);
         const bool live = i <= u.i1;
         col.query[c] = live ? i : -1;
         if (a.f.slopes) {
-            const int j = u.first + i;
-            float p = (float)j;
-            if (live && a.c.positions) {
-                const int page = page_of(a.c, b, j / a.c.block);
-                p = page < 0 ? 0.0f : (float)a.c.positions[((size_t)page * a.c.kv_heads + h) * a.c.block + j % a.c.block];
-            }
-            col.pos[c] = p;
+            col.pos[c] = live ? from_origin(position_of(a, b, h, u.first + i), origin) : 0.0f;
             col.slope[c] = live ? -a.f.slopes[h * a.group + g] * kLog2e : 0.0f;
         }
     }
@@ -1237,7 +1251,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     const int tile = u.tile(x), j = tile * kTile + t;
                     const uint32_t came = info.came;
                     float k_scale = info.k_scale[t >> log_p], v_scale = info.v_scale[t >> log_p];
-                    const float pos = FORM && a.f.slopes ? (a.c.positions ? (float)info.pos[t] : (float)j) : 0.0f;
+                    const float pos = FORM && a.f.slopes ? from_origin(a.c.positions ? info.pos[t] : j, col.origin) : 0.0f;
                     const bool edge = came != (1u << blocks) - 1 ||
                                       !(tile < u.seen_prefix || (tile >= u.seen_low && tile < u.seen_end));
                     const bool check = fresh || sh.unset[w][0] || (NT > 32 && sh.unset[w][1]);
@@ -1809,7 +1823,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                         const bool edge = came != (1u << blocks) - 1 || !interior(a, u, j0);
                         const bool cached = !edge || (j < u.len && ((came >> (t >> log_p)) & 1));
                         const float ks = cached ? info.k_scale[t >> log_p] : 0.0f;
-                        const float pos = FORM && a.f.slopes ? (a.c.positions ? (float)info.pos[t] : (float)j) : 0.0f;
+                        const float pos = FORM && a.f.slopes ? from_origin(a.c.positions ? info.pos[t] : j, sh.col.origin) : 0.0f;
                         const Mask<NT> see = edge && cached ? seen_by<NT>(a, askers, sh.col, j) : 0;
                         float *weight = a.weights + ((size_t)(cached ? page : 0) * a.c.kv_heads + h) * P + (t & (P - 1));
                         mbar_wait(&sh.s_full[w], (g / NW) & 1, dead);

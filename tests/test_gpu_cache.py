@@ -301,6 +301,25 @@ def test_a_window_far_from_its_prefix(sv, dim):
     assert ((got.cpu().double() - want).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("offset", [100_000_001, 2 ** 31 - 2000, -2 ** 31])
+def test_far_positions(sv, offset):
+    """A bias goes by the distance, however far out both positions are."""
+    case = Case([333, 70], 3, heads=6, kv_heads=2, positions=True, slopes=True, seed=32)
+    case.pool.positions -= case.pool.positions.min()
+    assert case.pool.positions.max() < 2000
+    case.pool.positions += offset
+    check_both(sv, case)
+
+
+def test_a_bias_at_the_end_of_a_long_cache(sv):
+    case = Case([500], 3, heads=4, kv_heads=2, block=128, window=200, slopes=True, seed=33)
+    ref = case.reference()
+    table, lengths = far_out(case, 1000000)
+    f = {k: dev(v) for k, v in case.form.items()}
+    out, lse = sv.cache_attend(case.q.cuda(), case.pool.to(sv), table, lengths, **f)
+    check_attend(ref, out, lse)
+
+
 def test_blocks_of_very_different_value_scales(sv):
     case = Case([256], 1, dim=64, seed=13)
     for blk in range(case.table.shape[1]):
