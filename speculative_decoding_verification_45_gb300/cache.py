@@ -184,6 +184,8 @@ def _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent):
         raise ValueError(f"a candidate tree has at most {MAX_TREE_NODES} nodes, got {n}")
     if window < 0 or not 0 <= softcap < math.inf:
         raise ValueError("window and softcap must not be negative")
+    if window >= 1 << 31:
+        raise ValueError(f"window must be below 2^31 (0: none), got {window}")
     f = _native.CacheForm(
         1 / math.sqrt(c.dim) if scale is None else scale, softcap, window,
         None if slopes is None else _check(slopes, "slopes", torch.float32, (heads,), dev),

@@ -189,6 +189,7 @@ def test_small_arrays(t, exc, msg):
     (dict(q=torch.zeros(1, 3, 3, 64)), ValueError, "multiple of 2"),
     (dict(q=torch.zeros(1, 3, 4, 64)), TypeError, "bfloat16"),
     (dict(q=torch.zeros(1, 300, 4, 64, dtype=torch.bfloat16), parent=torch.zeros(1, 300)), ValueError, "at most 256"),
+    (dict(window=2 ** 31), ValueError, "below 2"), (dict(window=2 ** 32 + 5), ValueError, "below 2"),
     (dict(window=-1), ValueError, "negative"), (dict(softcap=-2.0), ValueError, "negative"),
     (dict(slopes=torch.zeros(2)), ValueError, "slopes"), (dict(prefix=torch.zeros(1)), TypeError, "prefix"),
     (dict(num_new=torch.zeros(2, dtype=torch.int32)), ValueError, "num_new"),
