@@ -312,7 +312,7 @@ spec_status spec_device_pointer(const void *ptr, const void **device_ptr);
  *                   position of each cached token in its text, which the bias by
  *                   distance uses (NULL: the token's index j).  16-byte aligned.
  *   block_table     [batch, >= max_blocks] int32
- * A length is valid in [0, max_blocks * block].  Data problems never trap: a
+ * A length is valid in [0, max_blocks * block], which is SPEC_MAX_CACHED at most.  Data problems never trap: a
  * sequence with a length (or number of new tokens) out of range is skipped, its
  * outputs zero (lse -inf, lengths 0), and a token on a page outside
  * [0, num_pages) counts as not cached; SPEC_STATUS_BAD_LENGTH and
@@ -321,6 +321,8 @@ spec_status spec_device_pointer(const void *ptr, const void **device_ptr);
  * Ownership, stream and error rules as for spec_verify, but that a call may
  * enqueue up to three kernels; every array is device memory.  Nothing is
  * allocated. */
+#define SPEC_MAX_CACHED (1 << 30) /* tokens of a sequence: loops over them count in 32 bits */
+
 typedef enum { SPEC_E4M3 = 0, SPEC_E5M2 = 1 } spec_code;
 
 typedef struct spec_cache {

@@ -138,7 +138,7 @@ inline spec_status check_cache(const spec_cache *c)
     if ((c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) ||
         (c->dim != 64 && c->dim != 128) || (c->code != SPEC_E4M3 && c->code != SPEC_E5M2))
         return SPEC_ERR_UNSUPPORTED;
-    if ((int64_t)c->max_blocks * c->block > INT_MAX)
+    if ((int64_t)c->max_blocks * c->block > SPEC_MAX_CACHED)
         return SPEC_ERR_INVALID_ARG;
     for (int i = 0; i < 3; ++i)
         if (c->k_stride[i] < 16 || c->v_stride[i] < 16 || (c->k_stride[i] & 15) || (c->v_stride[i] & 15) ||

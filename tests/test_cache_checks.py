@@ -37,6 +37,7 @@ BAD_CACHE = [
     (dict(batch=-1), 1), (dict(max_blocks=0), 1), (dict(num_pages=0), 1), (dict(kv_heads=0), 1), (dict(block=24), 2),
     (dict(dim=96), 2), (dict(code=2), 2), (dict(k_stride=[2048, 1024, 72]), 1), (dict(v_stride=[0, 1024, 64]), 1),
     (dict(k_stride=[1 << 41, 1024, 64]), 1), (dict(max_blocks=1 << 28, table_stride=1 << 28), 1),
+    (dict(max_blocks=(1 << 26) + 1, table_stride=1 << 28), 1),
 ]
 # Never dereferenced: every case below fails validation, or has an empty batch or no new token.
 three = (ctypes.c_int64 * 3)(256, 128, 64)
