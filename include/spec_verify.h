@@ -410,7 +410,7 @@ spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, co
  * the pages of out_table[b * out_stride + ...], ceil(keep / block) each, which
  * must be in no sequence's block_table.  A new block's scale is the largest of
  * its tokens' scales, the codes as for spec_cache_append.
- *   out_lengths [batch] int32: min(lengths[b], keep)
+ *   out_lengths [batch] int32: min(lengths[b], keep); may be lengths itself
  *   out_index   [batch, kv_heads, keep] int32: the kept indices, then -1
  * Limits: 1 <= keep, 0 <= recent <= keep. */
 spec_status spec_cache_evict(const spec_cache *cache, const int32_t *lengths, float *weights, int keep, int recent,

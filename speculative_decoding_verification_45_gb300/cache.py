@@ -273,7 +273,8 @@ def cache_evict(cache, block_table, lengths, weights, keep: int, recent: int, ou
     in order, with their weights and positions, to the pages of ``out_table``
     [batch, >= ceil(keep / block)] int32, which no sequence may use yet; the
     old pages are free afterwards.  Returns (lengths [batch] int32, the kept
-    indices [batch, kv_heads, keep] int32, -1 after the last).
+    indices [batch, kv_heads, keep] int32, -1 after the last); ``out_lengths``
+    may be ``lengths`` itself.
     """
     c, dev, len_ptr = _describe(cache, block_table, lengths)
     if keep < 1 or not 0 <= recent <= keep:

@@ -252,11 +252,8 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
     const int h = blockIdx.x % c.kv_heads, b = blockIdx.x / c.kv_heads, log_p = 31 - __clz(c.block);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const Seq s = sequence(c, a.lengths, nullptr, 0, b, true);
-    if (tid == 0 && h == 0) {
-        if (!s.ok)
-            report(a.status, SPEC_STATUS_BAD_LENGTH);
-        a.out_lengths[b] = min(s.len, a.keep);
-    }
+    if (tid == 0 && h == 0 && !s.ok)
+        report(a.status, SPEC_STATUS_BAD_LENGTH);
     int32_t *index = a.out_index + ((size_t)b * c.kv_heads + h) * a.keep;
     for (int i = min(s.len, a.keep) + tid; i < a.keep; i += kSelectThreads)
         index[i] = -1;
@@ -365,6 +362,8 @@ template <int CODE> __global__ void __launch_bounds__(kMoveThreads, 6) move_kern
     const int to = a.out_table[(size_t)b * a.out_stride + k];
     const int kept = min(sequence(c, a.lengths, nullptr, 0, b, true).len, a.keep);
     const int n = min(P, kept - k * P);
+    if (tid == 0 && h == 0 && k == 0)
+        a.out_lengths[b] = kept;  // may be a.lengths: who reads it afterwards comes to the same
     if (n <= 0)
         return;
     if ((unsigned)to >= (unsigned)c.num_pages) {

@@ -463,6 +463,25 @@ def test_evict(sv, kw, weights):
     assert torch.equal(dw.cpu().nan_to_num(nan=1e9), w.nan_to_num(nan=1e9))
 
 
+def test_evict_in_place_of_the_lengths(sv):
+    """More (sequence, head) pairs than run at once: the later ones must not see the new lengths."""
+    B, KH, blocks, keep = 90, 16, 40, 32
+    pages = B * (blocks + 2)
+    x = torch.zeros(pages, KH, 16, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    cache = sv.KVCache(x, x.clone(), torch.ones(pages, KH, device="cuda"), torch.ones(pages, KH, device="cuda"))
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(2)).reshape(B, blocks + 2).int().cuda()
+    lengths = torch.randint(0, 641, (B,), generator=torch.Generator().manual_seed(3)).int().cuda()
+    w = torch.rand(pages, KH, 16, generator=torch.Generator().manual_seed(4)).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kept, index = sv.cache_evict(cache, table[:, :blocks], lengths, w.clone(), keep, 8, table[:, blocks:])
+    for _ in range(5):
+        own = lengths.clone()
+        got, again = sv.cache_evict(cache, table[:, :blocks], own, w.clone(), keep, 8, table[:, blocks:], out_lengths=own,
+                                    status=status)
+        assert got is own and torch.equal(own, kept) and torch.equal(again, index)
+    assert status.item() == 0 and torch.equal(kept, lengths.clamp(max=keep))
+
+
 def test_evict_from_more_tokens_than_shared_memory_holds(sv):
     """70,000 tokens in the table: the keys are read from memory at each step."""
     pages = 70000 // 128 + 1
