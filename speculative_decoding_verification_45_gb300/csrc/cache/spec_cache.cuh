@@ -66,14 +66,15 @@ __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)  // of un
     return r;
 }
 
-// Codes times f <= 1, to codes.  A power of two is multiplied in 16-bit floats: a
-// product that they do not hold exactly is below half the smallest code.
+// Codes times f <= 1, to codes.  A power of two that 16-bit floats hold (2^-24 is
+// their smallest) is multiplied in them: a product that they do not hold exactly
+// is below half the smallest code.
 struct Mover {
     float f;
     __half2 f2;
     bool halves;
     __device__ explicit Mover(float factor)
-        : f(factor), f2(__float2half2_rn(factor)), halves(is_pow2(factor))
+        : f(factor), f2(__float2half2_rn(factor)), halves(is_pow2(factor) && factor >= 0x1p-24f)
     {
     }
     __device__ __forceinline__ uint32_t operator()(uint32_t x, int code) const  // four of them

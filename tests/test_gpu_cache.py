@@ -415,6 +415,28 @@ def test_append_values_at_the_ends_of_the_range(sv, code):
             equal_cache(pool, cache)
 
 
+@pytest.mark.parametrize("code", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("shift", [1, 23, 24, 25, 28, 31, 40, 130])
+def test_scales_far_apart_in_a_block(sv, code, shift):
+    """Codes move by 2^-shift, when a block's scale grows and when an eviction brings blocks together."""
+    pool, table = cr.Pool(6, 2, 16, 64, code, seed=shift), torch.tensor([[2, 0]], dtype=torch.int32)
+    top = 448.0 if code == "e4m3" else 57344.0
+    for page in (2, 0):
+        pool.codes[:, page, :, :, 0] = top
+        pool.scale[:, page] = 2.0 ** -60
+    pool.scale[:, 0] = 2.0 ** (-60 + shift)
+    cache, w = pool.to(sv), torch.rand(6, 2, 16, generator=torch.Generator().manual_seed(shift))
+    out = torch.tensor([[4, 5]], dtype=torch.int32)
+    dw = w.cuda()
+    sv.cache_evict(cache, table.cuda(), torch.tensor([30]).int().cuda(), dw, 20, 6, out.cuda())
+    cr.evict(pool, table, [30], w, 20, 6, out)
+    equal_cache(pool, cache)
+    k = torch.full((1, 3, 2, 64), top * 2.0 ** (-60 + shift))
+    sv.cache_append(cache, table[:, :1].contiguous().cuda(), torch.tensor([9]).int().cuda(), k.cuda(), k.cuda())
+    cr.append(pool, table, [9], k, k)
+    equal_cache(pool, cache)
+
+
 def test_append_refuses_bad_data(sv):
     pool = cr.Pool(8, 2, 16, 64, seed=4)
     table = torch.tensor([[0, 1], [2, 3], [-1, 99], [4, 5]], dtype=torch.int32)
