@@ -230,10 +230,24 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ uint32_t key_at(const EvictArgs &a, int b, int h, int j, int log_p)
+// Keys of the tokens j, j + step, ... below end, 0 where there is none.  All their pages are asked for at once, then all
+// their weights: taken one by one, the two latencies were a third of the kernel's time.
+constexpr int kAhead = 8;
+__device__ __forceinline__ void load_keys(const EvictArgs &a, int b, int h, int log_p, int j, int step, int end,
+                                          uint32_t (&key)[kAhead])
 {
-    const int page = page_of(a.c, b, j >> log_p);
-    return page < 0 ? 0u : weight_key(a.weights[(((size_t)page * a.c.kv_heads + h) << log_p) + (j & ((1 << log_p) - 1))]);
+    int page[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        page[i] = j + i * step < end ? page_of(a.c, b, (j + i * step) >> log_p) : -1;
+    float w[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        w[i] = page[i] < 0 ? __int_as_float(0x7fffffff)
+                           : a.weights[(((size_t)page[i] * a.c.kv_heads + h) << log_p) + ((j + i * step) & ((1 << log_p) - 1))];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        key[i] = weight_key(w[i]);
 }
 
 // The (keep - recent)-th largest key is found 11 bits at a time from the top (a
@@ -267,11 +281,13 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
         index[want + i] = cand + i;
     if (want == 0)
         return;
-    if (staged) {
-#pragma unroll 4
-        for (int j = tid; j < cand; j += kSelectThreads)
-            keys[j] = key_at(a, b, h, j, log_p);
-    }
+    const auto get = [&](int j, int step, int end, uint32_t (&key)[kAhead]) {
+        if (!staged)
+            return load_keys(a, b, h, log_p, j, step, end, key);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            key[i] = j + i * step < end ? keys[j + i * step] : 0;
+    };
     const uint32_t zero = 0x80000000u;
     uint32_t prefix = 0, need = (uint32_t)want;  // rank of the wanted key among those that share `prefix`
     int shift = 21;
@@ -280,17 +296,29 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
         for (int i = tid; i < kDigits; i += kSelectThreads)
             hist[i] = 0;
         __syncthreads();
-        for (int j0 = 0; j0 < cand; j0 += kSelectThreads) {
-            const int j = j0 + tid;
-            bool in = j < cand;
-            const uint32_t key = in ? (staged ? keys[j] : key_at(a, b, h, j, log_p)) : 0;
-            in = in && (round == 0 || (key >> (shift + bits)) == prefix);
-            const uint32_t digit = (key >> shift) & ((1u << bits) - 1);
-            const uint32_t none = __ballot_sync(0xffffffffu, in && key == zero);
-            if (in && key != zero)
-                atomicAdd(&hist[digit], 1u);
-            else if (in && lane == __ffs(none) - 1)
-                atomicAdd(&hist[digit], (uint32_t)__popc(none));
+        const bool zeros = round == 0 || prefix == zero >> (shift + bits);  // zeros may be among those that share it
+        for (int j0 = tid; j0 - tid < cand; j0 += kAhead * kSelectThreads) {
+            uint32_t key[kAhead];
+            if (round == 0)
+                load_keys(a, b, h, log_p, j0, kSelectThreads, cand, key);
+            else
+                get(j0, kSelectThreads, cand, key);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int j = j0 + i * kSelectThreads;
+                if (round == 0 && staged && j < cand)
+                    keys[j] = key[i];
+                const bool in = j < cand && (round == 0 || (key[i] >> (shift + bits)) == prefix);
+                uint32_t *bin = &hist[(key[i] >> shift) & ((1u << bits) - 1)];
+                const bool none = zeros && in && key[i] == zero;
+                if (in && !none)
+                    atomicAdd(bin, 1u);
+                if (zeros) {
+                    const uint32_t all = __ballot_sync(0xffffffffu, none);
+                    if (none && lane == __ffs(all) - 1)
+                        atomicAdd(bin, (uint32_t)__popc(all));
+                }
+            }
         }
         __syncthreads();
         // the digit where the count from the top reaches `need`: two bins a thread, top first
@@ -320,10 +348,14 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
     const int each = ((cand + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
     const int lo = min(cand, wid * each), hi = min(cand, lo + each);
     int above = 0, equal = 0;
-    for (int j = lo + lane; j < hi; j += 32) {
-        const uint32_t key = staged ? keys[j] : key_at(a, b, h, j, log_p);
-        above += key > prefix;
-        equal += key == prefix;
+    for (int j = lo + lane; j < hi; j += kAhead * 32) {
+        uint32_t key[kAhead];
+        get(j, 32, hi, key);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            above += j + i * 32 < hi && key[i] > prefix;
+            equal += j + i * 32 < hi && key[i] == prefix;
+        }
     }
     above = __reduce_add_sync(0xffffffffu, above);
     equal = __reduce_add_sync(0xffffffffu, equal);
@@ -336,17 +368,21 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
     int ties = __reduce_add_sync(0xffffffffu, lane < wid ? count[1][lane] : 0);
     int out = at + min(ties, (int)need);  // kept tokens before this warp's stretch
     const uint32_t below = (1u << lane) - 1;
-    for (int j0 = lo; j0 < hi; j0 += 32) {
-        const int j = j0 + lane;
-        const uint32_t key = j < hi ? (staged ? keys[j] : key_at(a, b, h, j, log_p)) : 0;
-        const bool eq = j < hi && key == prefix;
-        const uint32_t tie = __ballot_sync(0xffffffffu, eq);
-        const bool take = (j < hi && key > prefix) || (eq && ties + __popc(tie & below) < (int)need);
-        const uint32_t took = __ballot_sync(0xffffffffu, take);
-        if (take)
-            index[out + __popc(took & below)] = j;
-        out += __popc(took);
-        ties += __popc(tie);
+    for (int j0 = lo; j0 < hi; j0 += kAhead * 32) {
+        uint32_t key[kAhead];
+        get(j0 + lane, 32, hi, key);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int j = j0 + i * 32 + lane;
+            const bool eq = j < hi && key[i] == prefix;
+            const uint32_t tie = __ballot_sync(0xffffffffu, eq);
+            const bool take = (j < hi && key[i] > prefix) || (eq && ties + __popc(tie & below) < (int)need);
+            const uint32_t took = __ballot_sync(0xffffffffu, take);
+            if (take)
+                index[out + __popc(took & below)] = j;
+            out += __popc(took);
+            ties += __popc(tie);
+        }
     }
 }
 
