@@ -1,11 +1,14 @@
 // spec_cache_move.cu -- writing tokens into the 8-bit key/value cache and
 // moving the kept ones out of it (spec_cache_append, spec_cache_evict).
 
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "spec_cache.cuh"
 
 using namespace specc;
+namespace cg = cooperative_groups;
 
 namespace {
 
@@ -203,8 +206,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
 // ===========================================================================
 // Evict
 // ===========================================================================
-// Two kernels: one CTA per (sequence, head) finds the kept indices, then one
-// CTA per block of kept tokens moves them.  Sources and destinations share no
+// Two kernels: one CTA or cluster per (sequence, head) finds the kept indices,
+// then one CTA per block of kept tokens moves them.  Sources and destinations share no
 // page, so the moves need no order.
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
@@ -256,34 +259,58 @@ __device__ __forceinline__ void load_keys(const EvictArgs &a, int b, int h, int 
 // the indices in order.  The keys are kept in shared memory where they fit
 // (`staged`), else read again from L2.  Keys equal to zero's, the one value that
 // repeats in earnest (tokens that no query looked at), are counted by ballot.
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs a, int staged)
+// A cluster's CTAs take a stretch of the tokens each; every one of them adds the
+// same histograms up and comes to the same digits.
+template <int CS> __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs a, int staged)
 {
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int rank = CS > 1 ? (int)cluster.block_rank() : 0;
+    const auto meet = [&] {
+        if (CS > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
     extern __shared__ uint32_t keys[];
-    __shared__ uint32_t hist[kDigits], warp_sum[kSelectWarps];
+    __shared__ alignas(8) uint32_t hist[kDigits];
+    __shared__ uint32_t warp_sum[kSelectWarps];
     __shared__ int count[2][kSelectWarps];
     __shared__ uint32_t found, left;
+    __shared__ int len0, sum[2];
     const spec_cache &c = a.c;
-    const int h = blockIdx.x % c.kv_heads, b = blockIdx.x / c.kv_heads, log_p = 31 - __clz(c.block);
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int unit = blockIdx.x / CS, h = unit % c.kv_heads, b = unit / c.kv_heads, log_p = 31 - __clz(c.block);
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, all_tid = rank * kSelectThreads + tid;
     const Seq s = sequence(c, a.lengths, nullptr, 0, b, true);
-    if (tid == 0 && h == 0 && !s.ok)
+    if (all_tid == 0 && h == 0 && !s.ok)
         report(a.status, SPEC_STATUS_BAD_LENGTH);
+    int len = s.len;
+    if (CS > 1) {  // one length for the cluster, whatever becomes of the array
+        if (tid == 0)
+            len0 = len;
+        cluster.sync();
+        len = *cluster.map_shared_rank(&len0, 0);
+    }
     int32_t *index = a.out_index + ((size_t)b * c.kv_heads + h) * a.keep;
-    for (int i = min(s.len, a.keep) + tid; i < a.keep; i += kSelectThreads)
+    for (int i = min(len, a.keep) + all_tid; i < a.keep; i += CS * kSelectThreads)
         index[i] = -1;
-    if (s.len <= a.keep) {
-        for (int i = tid; i < s.len; i += kSelectThreads)
+    const int all = len - a.recent, want = a.keep - a.recent;  // candidates; want < all where it matters
+    if (len <= a.keep) {
+        for (int i = all_tid; i < len; i += CS * kSelectThreads)
             index[i] = i;
+    } else {
+        for (int i = all_tid; i < a.recent; i += CS * kSelectThreads)
+            index[want + i] = all + i;
+    }
+    if (len <= a.keep || want == 0) {
+        if (CS > 1)
+            cluster.sync();  // len0 is read
         return;
     }
-    const int cand = s.len - a.recent, want = a.keep - a.recent;  // want < cand
-    for (int i = tid; i < a.recent; i += kSelectThreads)
-        index[want + i] = cand + i;
-    if (want == 0)
-        return;
+    // this CTA's candidates: [begin, begin + cand)
+    const int share = (all + CS - 1) / CS, begin = min(all, rank * share), cand = min(all, begin + share) - begin;
     const auto get = [&](int j, int step, int end, uint32_t (&key)[kAhead]) {
         if (!staged)
-            return load_keys(a, b, h, log_p, j, step, end, key);
+            return load_keys(a, b, h, log_p, begin + j, step, begin + end, key);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
             key[i] = j + i * step < end ? keys[j + i * step] : 0;
@@ -300,7 +327,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
         for (int j0 = tid; j0 - tid < cand; j0 += kAhead * kSelectThreads) {
             uint32_t key[kAhead];
             if (round == 0)
-                load_keys(a, b, h, log_p, j0, kSelectThreads, cand, key);
+                load_keys(a, b, h, log_p, begin + j0, kSelectThreads, begin + cand, key);
             else
                 get(j0, kSelectThreads, cand, key);
 #pragma unroll
@@ -320,9 +347,16 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
                 }
             }
         }
-        __syncthreads();
+        meet();
         // the digit where the count from the top reaches `need`: two bins a thread, top first
-        const uint32_t upper = hist[kDigits - 1 - 2 * tid], lower = hist[kDigits - 2 - 2 * tid];
+        uint32_t upper = 0, lower = 0;
+#pragma unroll
+        for (int r = 0; r < CS; ++r) {
+            uint32_t *at = &hist[kDigits - 2 - 2 * tid];
+            const uint2 two = *(const uint2 *)(CS > 1 ? cluster.map_shared_rank(at, r) : at);
+            upper += two.y;
+            lower += two.x;
+        }
         uint32_t up = upper + lower;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -339,7 +373,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
             found = kDigits - 1 - 2 * tid - second;
             left = need - ahead - (second ? upper : 0);
         }
-        __syncthreads();
+        meet();
         prefix = prefix << bits | found;
         need = left;
         shift -= round == 0 ? 11 : 10;
@@ -364,8 +398,21 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
         count[1][wid] = equal;
     }
     __syncthreads();
-    const int at = __reduce_add_sync(0xffffffffu, lane < wid ? count[0][lane] : 0);
+    int at = __reduce_add_sync(0xffffffffu, lane < wid ? count[0][lane] : 0);
     int ties = __reduce_add_sync(0xffffffffu, lane < wid ? count[1][lane] : 0);
+    if (CS > 1) {  // and the CTAs before this one
+        if (wid == kSelectWarps - 1 && lane == 0) {
+            sum[0] = at + above;
+            sum[1] = ties + equal;
+        }
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) {
+            const int *before = cluster.map_shared_rank(sum, r);
+            at += before[0];
+            ties += before[1];
+        }
+        cluster.sync();  // nobody leaves while its sums are read
+    }
     int out = at + min(ties, (int)need);  // kept tokens before this warp's stretch
     const uint32_t below = (1u << lane) - 1;
     for (int j0 = lo; j0 < hi; j0 += kAhead * 32) {
@@ -379,7 +426,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const EvictArgs 
             const bool take = (j < hi && key[i] > prefix) || (eq && ties + __popc(tie & below) < (int)need);
             const uint32_t took = __ballot_sync(0xffffffffu, take);
             if (take)
-                index[out + __popc(took & below)] = j;
+                index[out + __popc(took & below)] = begin + j;
             out += __popc(took);
             ties += __popc(tie);
         }
@@ -577,19 +624,38 @@ spec_status spec_cache_evict(const spec_cache *cache, const int32_t *lengths, fl
         return SPEC_ERR_UNSUPPORTED;
     EvictArgs a{*cache, lengths, out_table, weights, out_stride, out_lengths, out_index, keep, recent, status};
     const cudaStream_t s = (cudaStream_t)stream;
-    // shared memory for the keys of the longest sequence; up to 48 KB needs no opt-in
     const long long room = (long long)cache->max_blocks * cache->block;
-    const long long bytes = room * 4;
+    // few long sequences: clusters, as many CTAs as the SMs hold, of 8,192 tokens or more each (2 sequences of 100,000
+    // tokens and 8 heads: 68 us against 171; 7 of 16,384: 45 against 47; pairs of 4,096 tokens each: 44 against 40)
+    int log_cluster = 0;
+    while (log_cluster < 3 && heads << (log_cluster + 1) <= 128 && room >= 8192ll << (log_cluster + 1))
+        ++log_cluster;
+    static constexpr void (*kSelect[])(EvictArgs, int) = {select_kernel<1>, select_kernel<2>, select_kernel<4>, select_kernel<8>};
+    const auto select = kSelect[log_cluster];
+    const int cluster = 1 << log_cluster;
+    // shared memory for the keys of the longest sequence; up to 48 KB needs no opt-in
+    const long long bytes = (room + cluster - 1) / cluster * 4;
     const int staged = bytes <= 200 * 1024;
     if (staged && bytes > 36 * 1024 &&
-        cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess) {
+        cudaFuncSetAttribute((const void *)select, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) != cudaSuccess) {
         cudaGetLastError();
         return SPEC_ERR_CUDA;
     }
-    select_kernel<<<(unsigned)heads, kSelectThreads, staged ? (size_t)bytes : 0, s>>>(a, staged);
-    st = launched();
-    if (st != SPEC_OK)
-        return st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(heads * cluster));
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.dynamicSmemBytes = staged ? (size_t)bytes : 0;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1;
+    if (cudaLaunchKernelEx(&cfg, select, a, staged) != cudaSuccess) {
+        cudaGetLastError();
+        return SPEC_ERR_CUDA;
+    }
     if (cache->code == SPEC_E4M3)
         move_kernel<SPEC_E4M3><<<(unsigned)(heads * blocks), kMoveThreads, 0, s>>>(a, blocks);
     else

@@ -485,6 +485,42 @@ def test_evict(sv, kw, weights):
     assert torch.equal(dw.cpu().nan_to_num(nan=1e9), w.nan_to_num(nan=1e9))
 
 
+@pytest.mark.parametrize("kw", [
+    dict(lengths=[9000, 8192, 300, 0], heads=2), dict(lengths=[40001], heads=1), dict(lengths=[32768, 32761], heads=3),
+    dict(lengths=[17000, 4, 16383], heads=11, keep=3000, recent=0), dict(lengths=[33000], heads=2, keep=64, recent=64),
+    dict(lengths=[33000, 2999, 3000, 3001], heads=1, keep=3000, recent=2999),
+], ids=str)
+@pytest.mark.parametrize("weights", ["spread", "ties", "none"])
+def test_evict_from_long_sequences(sv, kw, weights):
+    """Lengths at which several CTAs share a sequence's selection, uneven shares and empty ones among them."""
+    lengths, heads, keep, recent = kw["lengths"], kw["heads"], kw.get("keep", 700), kw.get("recent", 33)
+    block, B = 64, len(kw["lengths"])
+    blocks, out_blocks = -(-max(lengths) // block), -(-keep // block)
+    pages = B * (blocks + out_blocks)
+    x = torch.zeros(pages, heads, block, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    one = torch.ones(pages, heads, device="cuda")
+    table = table_for(B, blocks + out_blocks, pages, 41)
+    g = torch.Generator().manual_seed(keep + heads)
+    w = torch.randn(pages, heads, block, generator=g).exp()
+    if weights == "ties":
+        w = torch.randint(0, 3, w.shape, generator=g).float()
+    if weights == "none":
+        w.zero_()
+    kept, index = sv.cache_evict(sv.KVCache(x, x.clone(), one, one.clone()), table[:, :blocks].cuda(),
+                                 torch.tensor(lengths).int().cuda(), w.cuda(), keep, recent, table[:, blocks:].cuda())
+    assert kept.tolist() == [min(n, keep) for n in lengths]
+    for b, n in enumerate(lengths):
+        for h in range(heads):
+            got = index[b, h].cpu()
+            if n <= keep:
+                want = torch.arange(n)
+            else:
+                j = torch.arange(n - recent)
+                heavy = w[table[b, j // block].long(), h, j % block].sort(descending=True, stable=True).indices[:keep - recent]
+                want = torch.cat([heavy.sort().values, torch.arange(n - recent, n)])
+            assert torch.equal(got[:len(want)].long(), want) and (got[len(want):] == -1).all()
+
+
 def test_evict_in_place_of_the_lengths(sv):
     """More (sequence, head) pairs than run at once: the later ones must not see the new lengths."""
     B, KH, blocks, keep = 90, 16, 40, 32
