@@ -265,6 +265,7 @@ template <int CS> __global__ void __launch_bounds__(kSelectThreads) select_kerne
 {
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = CS > 1 ? (int)cluster.block_rank() : 0;
+    asm volatile("griddepcontrol.launch_dependents;");  // the moving CTAs may take their places, and wait there
     const auto meet = [&] {
         if (CS > 1)
             cluster.sync();
@@ -440,6 +441,7 @@ template <int CODE> __global__ void __launch_bounds__(kMoveThreads, 6) move_kern
     __shared__ long long off[2][kMaxBlock];          // where its codes lie, -1: nowhere
     const spec_cache &c = a.c;
     const int P = c.block, tid = threadIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for select_kernel
     const int k = blockIdx.x % blocks;
     const int h = (blockIdx.x / blocks) % c.kv_heads, b = blockIdx.x / blocks / c.kv_heads;
     const int to = a.out_table[(size_t)b * a.out_stride + k];
@@ -656,11 +658,18 @@ spec_status spec_cache_evict(const spec_cache *cache, const int32_t *lengths, fl
         cudaGetLastError();
         return SPEC_ERR_CUDA;
     }
-    if (cache->code == SPEC_E4M3)
-        move_kernel<SPEC_E4M3><<<(unsigned)(heads * blocks), kMoveThreads, 0, s>>>(a, blocks);
-    else
-        move_kernel<SPEC_E5M2><<<(unsigned)(heads * blocks), kMoveThreads, 0, s>>>(a, blocks);
-    return launched();
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)(heads * blocks));
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.dynamicSmemBytes = 0;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, cache->code == SPEC_E4M3 ? move_kernel<SPEC_E4M3> : move_kernel<SPEC_E5M2>, a, blocks) !=
+        cudaSuccess) {
+        cudaGetLastError();
+        return SPEC_ERR_CUDA;
+    }
+    return SPEC_OK;
 }
 
 }  // extern "C"
