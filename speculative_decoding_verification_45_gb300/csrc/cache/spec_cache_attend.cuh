@@ -48,7 +48,7 @@ struct AttendArgs {
     float *weights;
     uint8_t *split;        // [batch][kv heads][row tiles][2][NT * D]: the queries as split_kernel leaves them
     float *factor;         // [batch][kv heads][row tiles][NT]
-    float *part;           // [2 * CTAs][NT][D] partial sums, then [2 * CTAs][NT] (total, base)
+    float *part;           // [2 * CTAs][NT][D] outputs of parts, then [2 * CTAs][NT] (total, base)
     float2 *part_sum;
     int4 *joins;           // [CTAs]: (first CTA or -1, sequence, head, row tile)
     uint32_t *status;
@@ -817,7 +817,8 @@ template <int D, int NT> struct AttendShared {
     int dead;
 };
 
-constexpr uint32_t kNoScale = 253u << 23;  // where a tile leaves nothing to a row
+constexpr uint32_t kNoScale = 253u << 23;  // 2^126, where a tile leaves nothing to a row; others have 2^125 at most
+constexpr uint32_t kUnseen = 0x80000000u;  // -0: the exponential of a token that the row does not see
 
 __device__ __forceinline__ int ordered(float x)
 {
@@ -825,8 +826,13 @@ __device__ __forceinline__ int ordered(float x)
     return i ^ ((i >> 31) & 0x7fffffff);
 }
 
-struct MaxHalves {
-    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return max_halves(a, b); }
+struct MaxHalves {  // signed: kUnseen is the least
+    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const
+    {
+        uint32_t r;
+        asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
 };
 struct MaxInt {
     __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
@@ -861,6 +867,9 @@ __device__ __forceinline__ float power2(int e)
 {
     return e < -126 ? 0.0f : __uint_as_float((uint32_t)(min(e, 127) + 127) << 23);
 }
+
+// 2^(a - b) for a <= b + 60, the two up to 2^30 and some from 0.
+__device__ __forceinline__ float power_gap(int a, int b) { return a < b - 200 ? 0.0f : power2(a - b); }
 
 // A set of columns, one bit each.
 template <int NT> using Mask = typename std::conditional<NT <= 32, uint32_t, uint64_t>::type;
@@ -1263,11 +1272,11 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                         const Askers askers{u.first, u.prefix, u.i1, u.rt * NT, a.group};
                         see = cached ? seen_by<NT>(a, askers, col, j) : 0;
                         const bool all = see == all_columns<NT>(askers);
+                        v_most = see ? v_scale : 0.0f;
                         uint4 *row = (uint4 *)(sh.v[vs] + t * D);
                         if (!cached) {  // nothing was loaded here
                             k_scale = 0.0f;
                             v_scale = 1.0f;
-                            v_most = 0.0f;
 #pragma unroll 1
                             for (int k = 0; k < D / 16; ++k)
                                 row[(k + t) & (D / 16 - 1)] = make_uint4(0, 0, 0, 0);
@@ -1312,7 +1321,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             const uint32_t bits = (uint32_t)(see >> c0);
 #pragma unroll
                             for (int c = 0; c < 16; ++c)
-                                e[c] = (bits >> c) & 1 ? e[c] : 0.0f;
+                                e[c] = (bits >> c) & 1 ? e[c] : __uint_as_float(kUnseen);
                         }
                     };
                     while (true) {
@@ -1343,7 +1352,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                                     sh.highest[w][t] = INT_MIN;
                                     set = sh.is_set[w][t];
                                     if (top != INT_MIN && high > -INFINITY) {
-                                        if (!set || high - old > 32.0f) {
+                                        if (!set || high > old) {
                                             const float now = fminf(fmaxf(ceilf(high), -0x1p30f), 0x1p30f);
                                             alpha = set ? exp2f(old - now) : 1.0f;
                                             sh.less[w][t] = -now;
@@ -1388,22 +1397,24 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             for (int c = 0; c < 8; ++c)
                                 half[c] = __byte_perm(__float_as_uint(e[2 * c]), __float_as_uint(e[2 * c + 1]), 0x7632);
                             int which;
-                            const uint32_t two = warp_combine<8>(half, lane, which, MaxHalves());
+                            const uint32_t two = warp_combine<8>(half, lane, which, MaxHalves()) & 0x7fff7fffu;
                             const uint32_t most = lane & 1 ? two & 0xffff0000u : two << 16;  // a float, cut to 16 bits
-                            again = again || most >= 191u << 23;
                             // 2^k with 224 <= 2^k * largest weight <= 448 (448 = 1.75 * 2^8)
-                            const uint32_t top = (__float_as_uint(__uint_as_float(most) * v_most) + (0x1fu << 16)) >> 23;
+                            const uint32_t largest = __float_as_uint(__uint_as_float(most) * v_most), top = (largest + (0x1fu << 16)) >> 23;
+                            again = again || most >= 191u << 23 || largest >= 246u << 23;
                             if ((lane & 3) < 2) {
                                 const int c = c0 + 2 * which + (lane & 1);
-                                atomicMin(&scales[c], (262u - max(top, 9u)) << 23);
+                                atomicMin(&scales[c], (262u - max(top, 9u + min(top, 1u))) << 23);
                                 if (check && !closely)
-                                    atomicMax(&sh.highest[w][c], (int)most);
+                                    atomicMax(&sh.highest[w][c], (int)min(most, largest));
                             }
                         }
-                        // a score that passed its base by 2^64 sends the warpgroup round again
+                        // a score that passed its base by 2^64, or by what brings it to 2^119 with its scale, sends the
+                        // warpgroup round again
                         bool redo = barrier_or<128>(bar, again && !closely);
                         if (check && !closely) {
-                            // rows without a base keep 0 if their largest exponential is not far below 1
+                            // rows without a base keep 0 if their largest exponential, alone and times the scale, is not
+                            // far below 1
                             bool low = false;
                             if (t < NT) {
                                 low = !sh.is_set[w][t] && col.query[t] >= 0;
@@ -1453,13 +1464,14 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 #pragma unroll
                         for (int c4 = 0; c4 < 4; ++c4) {
                             const float4 y = *(const float4 *)(scales + c0 + c4 * 4);
-                            const float2 p0 = mul2(((float2 *)e)[2 * c4], mul2(make_float2(y.x, y.y), v2)),
-                                         p1 = mul2(((float2 *)e)[2 * c4 + 1], mul2(make_float2(y.z, y.w), v2));
+                            // e * v first: y * v may pass the floats where e is 0
+                            const float2 p0 = mul2(mul2(((float2 *)e)[2 * c4], v2), make_float2(y.x, y.y)),
+                                         p1 = mul2(mul2(((float2 *)e)[2 * c4 + 1], v2), make_float2(y.z, y.w));
                             float p[4] = {p0.x, p0.y, p1.x, p1.y};
-                            if (edge) {
+                            if (edge) {  // a scale that is NaN does not reach the rows that do not see it
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    p[k] = e[4 * c4 + k] == 0.0f ? 0.0f : p[k];
+                                    p[k] = __float_as_uint(e[4 * c4 + k]) == kUnseen ? 0.0f : p[k];
                             }
                             uint32_t first[2], rest[2];
                             split8(p[0], p[1], first[0], rest[0]);
@@ -1537,11 +1549,11 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     if (ref == INT_MIN) {
                         ref = power;
                     } else if (power > ref + 60) {
-                        alpha = power2(max(ref - power, -200));
+                        alpha = power_gap(ref, power);
                         ref = power;
                         moved = true;
                     }
-                    sh.factor[i][tid] = power2(max(power - ref, -200));
+                    sh.factor[i][tid] = power_gap(power, ref);
                 }
                 if (barrier_or<128>(bar, moved)) {
                     if (tid < NT)
@@ -1577,6 +1589,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             const long long slot = 2ll * blockIdx.x + (u.x0 == 0);
             mbar_wait(&sh.sum_ready[seg & 1], (seg >> 1) & 1, dead);
             named_barrier<128>(bar);
+            bool far = false;
             if (tid < NT) {
                 float total = 0.0f, base = 0.0f, part[NW];
                 if (sh.col[seg & 1].query[tid] >= 0) {
@@ -1598,8 +1611,13 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 const long long row = u.rows[tid];
                 sh.out_row[tid] = row;
                 // sums count 2^ref, totals 2^base
-                const float level = ref == INT_MIN ? 0.0f : power2(max(min(ref - (int)base, 127), -200));
-                sh.inverse[tid] = whole ? (live ? level / total : 0.0f) : level;
+                int up = 0;
+                const float significand = isfinite(total) ? frexpf(total, &up) : total;
+                const int level = (int)max(min((long long)ref - (long long)base - up, 250ll), -250ll);
+                far = live && abs(level) > 100;  // a power that no float may hold goes in two
+                const int first = far ? level / 2 : 0;
+                sh.factor[0][tid] = power2(first);
+                sh.inverse[tid] = live && ref != INT_MIN ? power2(level - first) / significand : 0.0f;
                 if (whole) {
                     if (row >= 0)
                         a.lse[row] = live ? (base + log2f(total)) * 0.6931471805599453f : -INFINITY;
@@ -1609,7 +1627,11 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             }
             if (!whole && u.last && tid == 0)
                 a.joins[blockIdx.x] = make_int4((int)((u.at - u.x0) / range.each), u.b, u.h, u.rt);
-            named_barrier<128>(bar);
+            if (barrier_or<128>(bar, far)) {
+#pragma unroll
+                for (int c = 0; c < OC; ++c)
+                    o[c] *= sh.factor[0][o0 + c];
+            }
             if (lane == 0)  // the segment's place is free
                 mbar_arrive(&sh.sum_free[seg & 1]);
             if (whole) {
@@ -1922,25 +1944,32 @@ template <int D, int NT> __global__ void __launch_bounds__(32 * kJoinRows) join_
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // each part's output counts by its share of the total
     float total = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = join.x + lane; p <= last; p += 32) {
+        const float2 s = a.part_sum[slot(p)];
+        total += s.x == 0.0f ? 0.0f : s.x * exp2f(s.y - top);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll 4
     for (int p = join.x; p <= last; ++p) {
         const float2 s = a.part_sum[slot(p)];
         const Vec y = *(const Vec *)(a.part + slot(p) * D + lane * (D / 32));
         const bool some = !(s.x == 0.0f);
-        const float w = some ? exp2f(s.y - top) : 0.0f;
-        total += s.x * w;
+        const float w = s.x * exp2f(s.y - top) * inv;
         const float *v = (const float *)&y;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k)
             o[k] += some ? v[k] * w : 0.0f;
     }
     const size_t row = ((size_t)join.y * a.n + r / a.group) * a.heads + join.z * a.group + r % a.group;
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     __nv_bfloat162 *out = (__nv_bfloat162 *)(a.out + row * D + lane * (D / 32));
 #pragma unroll
     for (int k = 0; k < D / 32; k += 2)
-        out[k / 2] = total == 0.0f ? __floats2bfloat162_rn(0.0f, 0.0f) : __floats2bfloat162_rn(o[k] * inv, o[k + 1] * inv);
+        out[k / 2] = __floats2bfloat162_rn(o[k], o[k + 1]);
     if (lane == 0)
         a.lse[row] = total == 0.0f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
 }

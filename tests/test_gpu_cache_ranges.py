@@ -1,0 +1,108 @@
+"""Attention over the 8-bit cache where scales and scores lie far from 1.
+
+Bounds: those of test_gpu_cache, whose absolute part goes by the value scale
+here, and the grid of the weights written out: a token's weight times its value
+scale is held to half of 2^-9 of a number of which the largest of its 128 tokens
+has 224 or more, 2^-17 of that largest one."""
+import math
+
+import pytest
+import torch
+
+from tests import cache_reference as cr
+from tests.test_gpu_cache import Case, sv  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def grid(case, ref):
+    """How far the weights' grid may move each output."""
+    off = torch.zeros_like(ref["out"])
+    group = ref["lse"].shape[2] // case.pool.heads
+    for (b, i, h), (see, x, _) in ref["xs"].items():
+        j = see.nonzero()[:, 0]
+        page, row = case.table[b][j // case.pool.block].long(), j % case.pool.block
+        scale = case.pool.scale[1, page, h // group]
+        weight = torch.exp(x - ref["lse"][b, i, h]) * scale
+        most = torch.zeros(int(j.max()) // 128 + 1, dtype=torch.float64).scatter_reduce(0, j // 128, weight, "amax")
+        off[b, i, h] = 2.0 ** -17 * most[j // 128] @ case.pool.codes[1, page, h // group, row].abs()
+    return off
+
+
+def check(case, sv, unit, copies=90):  # noqa: F811
+    """Alone, where an SM takes a tile or two, and `copies` times over, where it takes whole sequences."""
+    ref = case.reference()
+    none = torch.isneginf(ref["lse"])
+    bound = (2.0 ** -8 * ref["out"].abs() + (1.5 * 2.0 ** -8 + 2 * ref["dx"][..., None]) * ref["mean"] + grid(case, ref)
+             + 2.0 ** -30 * unit)
+    cache = case.pool.to(sv)
+    for n in (1, copies):
+        def again(x):
+            return x.cuda().repeat(n, *[1] * (x.dim() - 1))
+        form = {k: again(v) if k in ("num_new", "prefix", "parent") else v.cuda() if k == "slopes" else v
+                for k, v in case.form.items()}
+        out, lse = sv.cache_attend(again(case.q), cache, again(case.table), again(case.lengths), **form)
+        out, lse = out.cpu().double().unflatten(0, (n, -1)), lse.cpu().double().unflatten(0, (n, -1))
+        assert torch.isfinite(out).all()
+        assert (none == torch.isneginf(lse)).all() and (out[:, none] == 0).all()
+        assert ((lse - ref["lse"]).abs()[:, ~none] <= ref["dx"][~none]).all()
+        far = ((out - ref["out"]).abs() - bound)[:, ~none]
+        assert (far <= 0).all(), (n, float(far.max() / unit))
+
+
+COLUMNS = [dict(new=2, heads=8, kv_heads=1), dict(new=4, heads=16, kv_heads=2), dict(new=7, heads=16, kv_heads=2)]
+SCALES = [-100, -40, 2, 20, 100]
+
+
+def at_scale(case, exponent):
+    case.pool.scale[1] = 2.0 ** exponent
+    return 2.0 ** exponent * case.pool.codes[1].abs().mean().item()
+
+
+@pytest.mark.parametrize("exponent", SCALES)
+@pytest.mark.parametrize("columns", COLUMNS, ids=[16, 32, 48])
+@pytest.mark.parametrize("dim,code", [(64, "e4m3"), (128, "e5m2"), (128, "e4m3")])
+def test_value_scales_with_a_bias_that_leaves_tiles_nothing(sv, exponent, columns, dim, code):  # noqa: F811
+    case = Case([650, 700, 90], dim=dim, block=32, code=code, seed=51, **columns)
+    case.form["slopes"] = torch.linspace(0.3, 3.0, columns["heads"])
+    check(case, sv, at_scale(case, exponent))
+
+
+def opposed(case, nats, first=0):
+    """Keys of the tokens from `first` blocks before the last on score about -nats."""
+    case.q = case.q.abs()
+    keys, scale, dim = case.pool.codes[0], case.pool.scale[0], case.q.shape[3]
+    for b in range(len(case.lengths)):
+        pages = case.table[b][: case.table.shape[1] - first].long()
+        keys[pages] = -keys[pages].abs()
+        size = keys[pages].abs().mean(dim=(2, 3)) * 0.8 * dim * case.form["scale"]
+        scale[pages] = torch.exp2(torch.round(torch.log2(nats / size)))
+
+
+@pytest.mark.parametrize("exponent", SCALES)
+@pytest.mark.parametrize("columns", COLUMNS, ids=[16, 32, 48])
+def test_value_scales_with_scores_that_leave_tiles_nothing(sv, exponent, columns):  # noqa: F811
+    case = Case([640, 640], dim=64, block=16, seed=52, **columns)
+    opposed(case, 300.0, first=6)
+    check(case, sv, at_scale(case, exponent))
+
+
+@pytest.mark.parametrize("exponent", SCALES)
+@pytest.mark.parametrize("columns", COLUMNS, ids=[16, 32, 48])
+@pytest.mark.parametrize("length", [300, 2100])
+def test_value_scales_with_high_and_low_scores(sv, exponent, columns, length):  # noqa: F811
+    case = Case([length], dim=128, block=64, seed=53, **columns)
+    case.form["scale"] *= 12
+    check(case, sv, at_scale(case, exponent))
+    case = Case([length], dim=128, block=64, seed=54, **columns)
+    opposed(case, 33.0)
+    check(case, sv, at_scale(case, exponent))
+
+
+def test_scales_of_blocks_that_nobody_sees(sv):  # noqa: F811
+    """A scale next to a window, past a prefix or of later queries' tokens decides nothing."""
+    case = Case([260], 9, heads=16, kv_heads=2, dim=64, block=16, window=20, prefix=[16], seed=55)
+    unit = at_scale(case, -100)
+    for blk in (1, 2, 3, 7, 9, 13):  # tokens 16 to 223: outside the prefix and every window
+        case.pool.scale[1, case.table[0, blk]] = 2.0 ** 110
+    check(case, sv, unit)
