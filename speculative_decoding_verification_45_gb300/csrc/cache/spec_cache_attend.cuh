@@ -802,7 +802,7 @@ template <int D, int NT> struct AttendShared {
     alignas(16) StageInfo info[S::VS];
     alignas(16) float less[S::NW][NT];   // the exponents' bases, negated
     alignas(16) uint32_t scale[S::NW][4][NT];  // per tile: 2^k, as bits, that brings the largest weight to [224, 448]
-    alignas(16) int power[S::kRing][NT];       // per tile: O^T counts 2^power
+    alignas(16) int power[S::kRing][NT];       // per tile: O^T counts 2^power, or kNothing
     alignas(16) long long out_row[NT];
     alignas(16) float factor[2][NT], inverse[NT], none[NT];  // none: bases of 0
     alignas(16) float warp_total[2][S::NW * 4][NT], last_base[2][S::NW][NT];
@@ -818,6 +818,7 @@ template <int D, int NT> struct AttendShared {
 };
 
 constexpr uint32_t kNoScale = 253u << 23;  // 2^126, where a tile leaves nothing to a row; others have 2^125 at most
+constexpr int kNothing = INT_MIN;           // the power of such a tile's sums, and of none yet: it says nothing of the row's level
 constexpr uint32_t kUnseen = 0x80000000u;  // -0: the exponential of a token that the row does not see
 
 __device__ __forceinline__ int ordered(float x)
@@ -1442,7 +1443,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             mbar_arrive(&sh.s_free[w]);
                     }
                     if (t < NT)
-                        sh.power[g % kRing][t] = 127 - (int)(scales[t] >> 23) - (int)sh.less[w][t];
+                        sh.power[g % kRing][t] =
+                            scales[t] == kNoScale ? kNothing : 127 - (int)(scales[t] >> 23) - (int)sh.less[w][t];
                     mbar_wait(&sh.p_free[w], (mine & 1) ^ 1, dead);
 #pragma unroll 1
                     for (int c0 = 0; c0 < NT; c0 += 16) {
@@ -1537,7 +1539,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 #pragma unroll
             for (int c = 0; c < OC; ++c)
                 o[c] = 0.0f;
-            int ref = INT_MIN;  // of column tid: its sums count 2^ref
+            int ref = kNothing;  // of column tid: its sums count 2^ref
 #pragma unroll 1
             for (int x = 0; x < tiles; ++x) {
                 const uint32_t i = g & 1, io = g % NO;
@@ -1546,14 +1548,14 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 float alpha = 1.0f;
                 if (tid < NT) {
                     const int power = sh.power[g % kRing][tid];
-                    if (ref == INT_MIN) {
+                    if (ref == kNothing) {
                         ref = power;
                     } else if (power > ref + 60) {
                         alpha = power_gap(ref, power);
                         ref = power;
                         moved = true;
                     }
-                    sh.factor[i][tid] = power_gap(power, ref);
+                    sh.factor[i][tid] = power == kNothing ? 0.0f : power_gap(power, ref);
                 }
                 if (barrier_or<128>(bar, moved)) {
                     if (tid < NT)
@@ -1617,7 +1619,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 far = live && abs(level) > 100;  // a power that no float may hold goes in two
                 const int first = far ? level / 2 : 0;
                 sh.factor[0][tid] = power2(first);
-                sh.inverse[tid] = live && ref != INT_MIN ? power2(level - first) / significand : 0.0f;
+                sh.inverse[tid] = live && ref != kNothing ? power2(level - first) / significand : 0.0f;
                 if (whole) {
                     if (row >= 0)
                         a.lse[row] = live ? (base + log2f(total)) * 0.6931471805599453f : -INFINITY;

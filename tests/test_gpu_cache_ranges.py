@@ -106,3 +106,14 @@ def test_scales_of_blocks_that_nobody_sees(sv):  # noqa: F811
     for blk in (1, 2, 3, 7, 9, 13):  # tokens 16 to 223: outside the prefix and every window
         case.pool.scale[1, case.table[0, blk]] = 2.0 ** 110
     check(case, sv, unit)
+
+
+@pytest.mark.parametrize("form", [dict(), dict(window=3), dict(window=130), dict(window=40, prefix=[3, 0, 130, 2])], ids=str)
+@pytest.mark.parametrize("nats", [200.0, 600.0, 2000.0])
+@pytest.mark.parametrize("columns", [dict(new=5, heads=4, kv_heads=2), dict(new=5, heads=12, kv_heads=2),
+                                     dict(new=9, heads=8, kv_heads=2)], ids=[16, 32, 48])
+def test_low_scores_where_a_row_does_not_see_every_tile(sv, columns, nats, form):  # noqa: F811
+    """Queries on both sides of a tile's border, and tiles that only some of them see."""
+    case = Case([129, 131, 260, 390], dim=64, block=16, seed=56, **columns, **form)
+    opposed(case, nats)
+    check(case, sv, 1.0)
