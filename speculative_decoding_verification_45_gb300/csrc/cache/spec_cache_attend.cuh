@@ -1088,7 +1088,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 if (k >= tiles)
                     return -2;
                 const int blk = u.tile(k) * blocks + (lane & (blocks - 1));
-                return (long long)blk * P < u.len ? table[blk] : -2;
+                return (long long)blk * P < u.len ? max(table[blk], -1) : -2;  // -2: no block here
             };
             int pages = 0, more = pages_from(0);
             for (int x = 0; x < tiles; ++x) {
@@ -1760,7 +1760,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                     if (k >= x1)
                         return -2;
                     const int blk = all.tile(k) * blocks + (lane & (blocks - 1));
-                    return (long long)blk * P < u.len ? table[blk] : -2;
+                    return (long long)blk * P < u.len ? max(table[blk], -1) : -2;  // -2: no block here
                 };
                 int pages = 0, more = pages_from(x0);
                 for (int x = x0; x < x1; ++x) {

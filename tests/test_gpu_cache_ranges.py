@@ -117,3 +117,19 @@ def test_low_scores_where_a_row_does_not_see_every_tile(sv, columns, nats, form)
     case = Case([129, 131, 260, 390], dim=64, block=16, seed=56, **columns, **form)
     opposed(case, nats)
     check(case, sv, 1.0)
+
+
+@pytest.mark.parametrize("page", [-2, -1, -2 ** 31, 2 ** 31 - 1])
+@pytest.mark.parametrize("block", [16, 128])
+def test_every_page_out_of_range_is_reported(sv, page, block):  # noqa: F811
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    case = Case([400, 90], 3, block=block, seed=57)
+    case.table[0, 1] = page
+    ref = case.reference()
+    cache, f, (out, lse) = case.run(sv, status=status)
+    assert status.item() == sv.STATUS_BAD_PAGE
+    assert ((lse.cpu() - ref["lse"]).abs() <= ref["dx"]).all()
+    status.zero_()
+    w = torch.zeros(len(case.pool.codes[0]), 2, block, device="cuda")
+    sv.cache_weigh(case.q.cuda(), cache, case.table.cuda(), case.lengths.cuda(), lse, w, status=status, **f)
+    assert status.item() == sv.STATUS_BAD_PAGE
