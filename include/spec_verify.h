@@ -409,7 +409,9 @@ spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, co
  * `keep`.  They are moved, in their order, with their weights and positions, to
  * the pages of out_table[b * out_stride + ...], ceil(keep / block) each, which
  * must be in no sequence's block_table.  A new block's scale is the largest of
- * its tokens' scales, the codes as for spec_cache_append.
+ * its tokens' scales, the codes as for spec_cache_append.  A kept token on a page
+ * out of range becomes one of zeros with weight and position 0 (a block of
+ * nothing else gets the scale 2^-100).
  *   out_lengths [batch] int32: min(lengths[b], keep); may be lengths itself
  *   out_index   [batch, kv_heads, keep] int32: the kept indices, then -1
  * Limits: 1 <= keep, 0 <= recent <= keep. */

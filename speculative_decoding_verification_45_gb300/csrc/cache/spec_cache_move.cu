@@ -507,6 +507,9 @@ template <int CODE> __global__ void __launch_bounds__(kMoveThreads, 6) move_kern
     // scales are positive: their bits order as they do
     now[0] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(now[0])));
     now[1] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(now[1])));
+    // none of the block's tokens is cached: their codes are zeros, at the scale that append gives zeros
+    now[0] = now[0] > 0.0f ? now[0] : 0x1p-100f;
+    now[1] = now[1] > 0.0f ? now[1] : 0x1p-100f;
     if (tid < 2) {
         float *scale = tid ? c.v_scale : c.k_scale;
         scale[(size_t)to * c.kv_heads + h] = now[tid];

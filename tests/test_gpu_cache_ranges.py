@@ -133,3 +133,23 @@ def test_every_page_out_of_range_is_reported(sv, page, block):  # noqa: F811
     w = torch.zeros(len(case.pool.codes[0]), 2, block, device="cuda")
     sv.cache_weigh(case.q.cuda(), cache, case.table.cuda(), case.lengths.cuda(), lse, w, status=status, **f)
     assert status.item() == sv.STATUS_BAD_PAGE
+
+
+def test_an_evicted_block_of_bad_pages_has_a_scale(sv):  # noqa: F811
+    """Its tokens are zeros, its scale the smallest one: what reads it later finds numbers."""
+    pool = cr.Pool(8, 2, 16, 64, positions=True, seed=58)
+    table, out = torch.tensor([[-1, 0, 3]], dtype=torch.int32), torch.tensor([[6, 7]], dtype=torch.int32)
+    cache, status = pool.to(sv), torch.zeros(1, dtype=torch.int32, device="cuda")
+    w = torch.ones(8, 2, 16, device="cuda")
+    lengths, index = sv.cache_evict(cache, table.cuda(), torch.tensor([30]).int().cuda(), w, 32, 4, out.cuda(), status=status)
+    assert status.item() == sv.STATUS_BAD_PAGE and lengths.tolist() == [30] and index[0, 0, :30].tolist() == list(range(30))
+    for codes, scale, side in ((cache.k, cache.k_scale, 0), (cache.v, cache.v_scale, 1)):
+        assert (scale[6] == 2.0 ** -100).all() and (codes[6].float() == 0).all()
+        assert torch.equal(scale[7].cpu().double(), pool.scale[side, 0])
+    assert (w[6] == 0).all() and (cache.positions[6] == 0).all()
+    # a second eviction of them, and attention over them, give numbers
+    q = torch.randn(1, 1, 4, 64).to(torch.bfloat16).cuda()
+    value, lse = sv.cache_attend(q, cache, out.cuda(), lengths)
+    assert torch.isfinite(value).all() and torch.isfinite(lse).all()
+    sv.cache_evict(cache, out.cuda(), lengths, w, 32, 4, torch.tensor([[1, 2]], dtype=torch.int32, device="cuda"))
+    assert not torch.isnan(cache.k.float()).any() and (cache.k_scale > 0).all()
