@@ -396,7 +396,11 @@ spec_status spec_cache_attend_workspace(const spec_cache *cache, int n, int head
  * queries and the head's query heads of exp(x - lse), for every cached token of
  * every sequence (lse as spec_cache_attend gave it; rows whose lse is -inf add
  * nothing).  weights [num_pages, kv_heads, block] float32, dense.  Each sum has
- * a fixed order.  workspace: as for spec_cache_attend.  Pages that several sequences share must not be weighed in one
+ * a fixed order.  Nothing else adds to weights or clears them (spec_cache_append
+ * leaves them as they are): a slot must hold 0 when a token is written to it.  In
+ * a speculative round, call this after the accept test with the accepted tokens
+ * only (their number as num_new, lengths to match, the same q and lse); then the
+ * slots of rejected tokens stay at 0 and what those looked at does not count.  workspace: as for spec_cache_attend.  Pages that several sequences share must not be weighed in one
  * call: their sums would race. */
 spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, const void *q,
                              const int64_t q_stride[3], int n, int heads, const spec_cache_form *form,

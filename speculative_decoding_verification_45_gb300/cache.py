@@ -250,7 +250,11 @@ def cache_weigh(q, cache, block_table, lengths, lse, weights, num_new=None, scal
 
     ``lse`` is what cache_attend returned for the same q and form; ``weights``
     [num_pages, kv_heads, block] float32 grows by the sum over queries and query
-    heads of exp(score - lse).  Returns ``weights``.
+    heads of exp(score - lse).  Returns ``weights``.  In a speculative round this
+    comes after the accept test, with the accepted tokens only (``num_new`` their
+    number, ``lengths`` to match, the same q and lse): weight given to a rejected
+    token would pass to the next one in its slot, since nothing clears weights but
+    the caller.
     """
     c, dev, len_ptr = _describe(cache, block_table, lengths)
     f, n, heads, stride = _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent)

@@ -8,7 +8,9 @@ transpose) decodes a batch of sequences: per round, prompt-lookup drafts
 cache_attend), the accept test (verify), the weight that each cached token
 received (cache_weigh), and, when a sequence has grown past ``limit``, eviction
 to ``keep`` tokens (cache_evict).  Rejected drafts leave the cache by length
-alone: the next append writes over them.
+alone: the next append writes over them.  Weights are added after the accept
+test, from the accepted tokens' queries only: what a rejected draft looked at
+must not count, and its own slot must hold no weight when another token takes it.
 """
 from __future__ import annotations
 
@@ -54,18 +56,25 @@ class Decoder:
         self.evictions = 0
 
     def forward(self, tokens, num_new, positions):
-        """Logits [batch, n, vocab] of the newest tokens; their keys and values enter the cache."""
+        """Logits [batch, n, vocab] of the newest tokens; their keys and values enter the cache.  What `weigh` needs of
+        them is kept until the next forward."""
         batch, n = tokens.shape
         x = self.embed[tokens.long()]
         q = (x @ self.wq).view(batch, n, self.heads, self.dim)
         kv = (x @ self.wkv).view(batch, n, 2, self.kv_heads, self.dim)
-        form = dict(num_new=num_new, slopes=self.slopes)
         sv.cache_append(self.cache, self.table, self.lengths, kv[:, :, 0], kv[:, :, 1], num_new=num_new,
                         positions=positions, status=self.status)
         lengths = self.lengths + num_new
-        out, lse = sv.cache_attend(q, self.cache, self.table, lengths, status=self.status, **form)
-        sv.cache_weigh(q, self.cache, self.table, lengths, lse, self.weights, status=self.status, **form)
+        out, lse = sv.cache_attend(q, self.cache, self.table, lengths, num_new=num_new, slopes=self.slopes,
+                                   status=self.status)
+        self.asked = q, lse
         return (x + out.view(batch, n, -1)) @ self.embed.t()
+
+    def weigh(self, num_new):
+        """Weights from the first num_new queries of the last forward; `lengths` counts their tokens already."""
+        q, lse = self.asked
+        sv.cache_weigh(q, self.cache, self.table, self.lengths, lse, self.weights, num_new=num_new, slopes=self.slopes,
+                       status=self.status)
 
     def step(self, temperature=0.7):
         """One round; returns (emitted tokens [batch, gamma + 1], accepted drafts [batch])."""
@@ -85,6 +94,7 @@ class Decoder:
         self.text.scatter_(1, at.clamp(max=self.text.shape[1] - 1).long(), torch.where(keep, emitted, 0).to(torch.int32))
         self.text_len += accepted + 1
         self.lengths += accepted + 1  # the accepted part of what was appended
+        self.weigh(accepted + 1)
         if int(self.lengths.max()) + gamma + 1 > self.limit:
             self.lengths, _ = sv.cache_evict(self.cache, self.table, self.lengths, self.weights, self.keep, self.recent,
                                              self.other, status=self.status)
