@@ -304,6 +304,10 @@ spec_status spec_device_pointer(const void *ptr, const void **device_ptr);
  * code * scale, the code an 8-bit float (e4m3: largest 448, or e5m2: largest
  * 57344).  Sequence b's token j is row j % block of page
  * block_table[b * table_stride + j / block].
+ * Rejected drafts of a chain leave the cache by length alone: the next append
+ * writes over them.  The accepted path of a candidate tree lies scattered among
+ * its nodes: append its keys and values once more at the length before the tree
+ * (node 0, then spec_tree_verify's out_path), and count those.
  *   k, v            codes; element (page, head, row, d) at
  *                   page * stride[0] + head * stride[1] + row * stride[2] + d bytes;
  *                   16-byte aligned, strides positive multiples of 16

@@ -228,7 +228,9 @@ def cache_attend(q, cache, block_table, lengths, num_new=None, scale=None, softc
     window   > 0: a query sees the last ``window`` tokens up to its own
     prefix   [batch] int32: tokens before it are seen by every query
     parent   [batch, n] int32: the n queries are a candidate tree, as in
-             tree_verify (node 0 the root); a node sees its ancestors
+             tree_verify (node 0 the root); a node sees its ancestors.
+             Before the next round the accepted path's rows are appended
+             once more, at the length before the tree (out_path says which)
 
     Rows that see nothing, and rows i >= num_new[b], are zeros with lse -inf.
     """
