@@ -20,8 +20,8 @@
 // fraction of an M = 128 tile, while N may be 16, 32 or 48.  So
 //   S^T [128 tokens, NT rows] = K [128, D] Q^T        (K is K-major as stored)
 //   O^T [D, NT rows]          = V^T [D, 128] P^T      (V is M-major as stored)
-// and a thread of the softmax owns one token and NT / 2 rows, with every lane
-// busy whatever the number of rows.
+// and a thread of the softmax owns one token and all NT rows, 16 at a time, with
+// every lane busy whatever the number of rows.
 #ifndef SPEC_CACHE_ATTEND_CUH
 #define SPEC_CACHE_ATTEND_CUH
 
@@ -203,13 +203,6 @@ template <> struct TmemLoad<16> {
                      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
                        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
                      : "r"(a));
-    }
-};
-template <> struct TmemLoad<32> {
-    static __device__ __forceinline__ void go(uint32_t a, float *r)
-    {
-        TmemLoad<16>::go(a, r);
-        TmemLoad<16>::go(a + 16, r + 16);
     }
 };
 __device__ __forceinline__ void tmem_store16(uint32_t a, const float *r)
@@ -558,7 +551,7 @@ __device__ __forceinline__ void describe_columns(const AttendArgs &a, const Unit
         }
 }
 
-// The ancestors of each column's query, after a barrier behind load_queries.
+// The ancestors of each column's query, after a barrier behind describe_columns.
 template <int NT, int THREADS> __device__ __forceinline__ void mark_kin(Columns<NT> &col, int t)
 {
     for (int c = t; c < NT; c += THREADS) {
@@ -767,9 +760,9 @@ template <int D, int NT> struct AttendShape {
     static constexpr int NO = NT == 48 ? 1 : 2;                 // O^T at a time (one: room to keep the exponentials)
     static constexpr int kBytes = kTile * D;                    // one side of a tile
     static constexpr int KS = 3, VS = D == 64 || NT == 16 ? 8 : NT >= 48 ? 5 : 6;  // tiles of keys and values in shared memory
-    static constexpr bool kKeep = (3 * NW + NO) * NT <= 512;     // room for the exponentials between the passes
-    static constexpr int kColumns = ((kKeep ? 3 : 2) * NW + NO) * NT;  // S^T, totals (and these) of each warpgroup, O^T
+    static constexpr int kColumns = (3 * NW + NO) * NT;         // S^T, totals and exponentials of each warpgroup, O^T
     static constexpr int kAlloc = kColumns <= 256 ? 256 : 512;
+    static_assert(kColumns <= 512, "tensor memory");
     static constexpr int kRing = 8;                             // >= NW + 2 tiles between a writer and the adding warps
 };
 
@@ -1391,8 +1384,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                         for (int c0 = 0; c0 < NT; c0 += 16) {
                             alignas(8) float e[16];
                             exponentials(c0, e);
-                            if (S::kKeep)
-                                tmem_store16(e_at + c0, e);
+                            tmem_store16(e_at + c0, e);
                             uint32_t half[8];
 #pragma unroll
                             for (int c = 0; c < 8; ++c)
@@ -1435,13 +1427,11 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             scales[t] = kNoScale;
                         closely = true;
                     }
-                    if (S::kKeep) {
-                        tmem_store_wait();
-                        tc_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&sh.s_free[w]);
-                    }
+                    tmem_store_wait();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&sh.s_free[w]);
                     if (t < NT)
                         sh.power[g % kRing][t] =
                             scales[t] == kNoScale ? kNothing : 127 - (int)(scales[t] >> 23) - (int)sh.less[w][t];
@@ -1450,12 +1440,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     for (int c0 = 0; c0 < NT; c0 += 16) {
                         alignas(8) float e[16], l[16];
                         TmemLoad<16>::go(l_at + c0, l);
-                        if (S::kKeep) {
-                            TmemLoad<16>::go(e_at + c0, e);
-                            tmem_wait<16>(e);
-                        } else {
-                            exponentials(c0, e);
-                        }
+                        TmemLoad<16>::go(e_at + c0, e);
+                        tmem_wait<16>(e);
                         tmem_wait<16>(l);
                         const float2 v2 = make_float2(v_scale, v_scale);
 #pragma unroll
@@ -1489,11 +1475,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     proxy_fence();
                     tc_before();
                     __syncwarp();
-                    if (lane == 0) {
-                        if (!S::kKeep)
-                            mbar_arrive(&sh.s_free[w]);
+                    if (lane == 0)
                         mbar_arrive(&sh.p_ready[g % kRing]);
-                    }
                     ++mine;
                     fresh = false;
                 }
