@@ -396,6 +396,13 @@ spec_status spec_cache_attend(const spec_cache *cache, const int32_t *lengths, c
                               float *lse, void *workspace, int64_t workspace_bytes, uint32_t *status, void *stream);
 spec_status spec_cache_attend_workspace(const spec_cache *cache, int n, int heads, int64_t *bytes);
 
+/* How many clocks of an SM a wait inside spec_cache_attend's and spec_cache_weigh's
+ * kernels may take (2^31 - 1, about a second, if this is never called).  A kernel
+ * whose wait ran out ends all the same and sets SPEC_STATUS_INTERNAL: give those
+ * calls a status to learn of it.  The limit holds for the calls that this process
+ * makes from now on; a captured call keeps the one it was captured with. */
+spec_status spec_cache_set_wait_limit(int clocks);
+
 /* Attention weight received: weights[page, kv head, row] += sum over the m
  * queries and the head's query heads of exp(x - lse), for every cached token of
  * every sequence (lse as spec_cache_attend gave it; rows whose lse is -inf add

@@ -133,6 +133,8 @@ def load() -> ctypes.CDLL:
         lib.spec_cache_attend.restype = i32
         lib.spec_cache_attend_workspace.argtypes = [vp, i32, i32, vp]
         lib.spec_cache_attend_workspace.restype = i32
+        lib.spec_cache_set_wait_limit.argtypes = [i32]
+        lib.spec_cache_set_wait_limit.restype = i32
         lib.spec_cache_weigh.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, ctypes.c_int64, vp, vp]
         lib.spec_cache_weigh.restype = i32
         lib.spec_cache_evict.argtypes = [vp, vp, vp, i32, i32, vp, ctypes.c_int64, vp, vp, vp, vp]

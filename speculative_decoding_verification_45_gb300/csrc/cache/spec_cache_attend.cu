@@ -37,6 +37,7 @@ spec_status check_call(const spec_cache *cache, const int32_t *lengths, const vo
 
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_sms[kMaxDevices];  // SM count, once the kernels' attributes are set
+std::atomic<int> g_wait_limit{INT_MAX};  // clocks
 
 spec_status device_sms(int *sms)
 {
@@ -134,6 +135,7 @@ AttendArgs make_args(const spec_cache *cache, const int32_t *lengths, const void
     a.per_group = a.group == 1 ? 0 : (uint32_t)(((1ull << 32) + a.group - 1) / a.group);
     a.row_tiles = shape.row_tiles;
     a.status = status;
+    a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
     return a;
 }
 
@@ -185,6 +187,14 @@ int64_t sum_bytes(const Shape &s, int sms) { return 2ll * sms * s.nt * 8; }
 }  // namespace
 
 extern "C" {
+
+spec_status spec_cache_set_wait_limit(int clocks)
+{
+    if (clocks < 0)
+        return SPEC_ERR_INVALID_ARG;
+    g_wait_limit.store(clocks, std::memory_order_relaxed);
+    return SPEC_OK;
+}
 
 spec_status spec_cache_attend_workspace(const spec_cache *cache, int n, int heads, int64_t *bytes)
 {

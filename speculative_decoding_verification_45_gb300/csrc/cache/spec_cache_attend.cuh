@@ -51,6 +51,7 @@ struct AttendArgs {
     float *part;           // [2 * CTAs][NT][D] outputs of parts, then [2 * CTAs][NT] (total, base)
     float2 *part_sum;
     int4 *joins;           // [CTAs]: (first CTA or -1, sequence, head, row tile)
+    int wait_limit;        // clocks
     uint32_t *status;
 };
 
@@ -84,45 +85,62 @@ __device__ __forceinline__ bool mbar_try(uint64_t *bar, uint32_t parity)
                  : "memory");
     return ok;
 }
-// Waits for a phase, about a second at most.  When that runs out `dead` is set
-// and every later wait returns at once: control flow stays the same for all
-// threads, so the CTA runs to its end (with results that the status marks bad).
-constexpr long long kPatience = 1ll << 31;  // clocks
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *dead)  // whether it came
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)  // does not wait
 {
-    if (mbar_try(bar, parity))
+    uint32_t ok;
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity)
+                 : "memory");
+    return ok;
+}
+// Waits for a phase, `limit` clocks at most; whether it came.  When that runs
+// out `dead` is set, and every wait of the CTA that is not over at once gives up.
+// A role whose wait did not come uses nothing that the wait guards as an address
+// or a count and goes to the end of the kernel; the threads of a warpgroup, which
+// share barriers, agree on that by a vote.  (The softmax finishes its segment, on
+// numbers that may not have come; they decide no address there.)
+struct Guard {
+    int dead, limit;
+};
+// NOW: a limit below the time that mbar_try itself waits (microseconds) counts as well.
+template <bool NOW = false> __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volatile Guard *guard)
+{
+    if (NOW ? mbar_test(bar, parity) : mbar_try(bar, parity))
         return true;
-    const long long since = clock64();
-    while (!mbar_try(bar, parity)) {
-        if (*dead)
+    const uint32_t since = (uint32_t)clock();
+    do {
+        if (guard->dead | ((uint32_t)clock() - since > (uint32_t)guard->limit)) {
+            guard->dead = 1;
             return false;
-        if (clock64() - since > kPatience)
-            *dead = 1;
-    }
+        }
+    } while (!mbar_try(bar, parity));
     return true;
 }
 
-// After a wait ran out: copies and products in flight end before the CTA's memory is given back.
-template <int ST>
-__device__ __forceinline__ void drain(uint64_t *full, uint32_t issued, volatile int *dead, uint32_t *status)
+// After a wait ran out: what is in flight lands before the CTA's memory is given back (2^24 clocks at most).
+__device__ __forceinline__ void land(uint64_t *bar, uint32_t parity)
 {
-    if (!*dead)
-        return;
-    for (uint32_t i = 0; i < ST && i < issued; ++i) {
-        const uint32_t parity = ((issued - 1 - i) / ST) & 1;  // of the stage's last copy
-        for (uint32_t k = 0; k < 4096 && !mbar_try(&full[i], parity); ++k)
-            ;
-    }
-    report(status, SPEC_STATUS_INTERNAL);
+    const long long since = clock64();
+    while (!mbar_try(bar, parity) && clock64() - since < (1 << 24))
+        ;
+}
+// The last copies into each of ST stages, `issued` in all.
+template <int ST> __device__ __forceinline__ void land_stages(uint64_t *full, uint32_t issued)
+{
+    for (uint32_t i = 0; i < ST && i < issued; ++i)
+        land(&full[i], ((issued - 1 - i) / ST) & 1);
 }
 __device__ __forceinline__ void tc_commit(uint64_t *bar);
-__device__ __forceinline__ void drain_products(uint64_t *bar, volatile int *dead)
+__device__ __forceinline__ bool elected();
+// The products of this warp.
+__device__ __forceinline__ void land_products(uint64_t *bar)
 {
-    if (!*dead || (threadIdx.x & 31))
-        return;
-    tc_commit(bar);
-    for (uint32_t k = 0; k < 4096 && !mbar_try(bar, 0); ++k)
-        ;
+    if (elected()) {
+        tc_commit(bar);
+        land(bar, 0);
+    }
+    __syncwarp();
 }
 
 __device__ __forceinline__ bool elected()  // one lane of a warp whose lanes are all here
@@ -807,7 +825,8 @@ template <int D, int NT> struct AttendShared {
     uint64_t s_full[S::NW], s_free[S::NW], p_ready[S::kRing], p_free[S::NW], o_full[2], o_free[2], seg_ready[4], q_ready[2];
     uint64_t sum_ready[2], sum_free[2], drained[2];
     uint32_t tmem;
-    int dead;
+    uint32_t issued[2], asked;  // copies of keys and of values, segments' queries
+    Guard guard;
 };
 
 constexpr uint32_t kNoScale = 253u << 23;  // 2^126, where a tile leaves nothing to a row; others have 2^125 at most
@@ -921,10 +940,12 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
     extern __shared__ uint8_t raw[];
     Shared &sh = *(Shared *)(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
     const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    volatile int *dead = &sh.dead;
+    volatile Guard *guard = &sh.guard;
 
     if (tid == 0) {
-        sh.dead = 0;
+        sh.guard.dead = 0;
+        sh.guard.limit = a.wait_limit;
+        sh.issued[0] = sh.issued[1] = sh.asked = 0;
         for (int i = 0; i < KS; ++i) {
             mbar_init(&sh.k_full[i], 1);
             mbar_init(&sh.k_empty[i], 1);
@@ -990,7 +1011,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 #pragma unroll 1
         for (uint32_t seg = 0;; ++seg) {
             const uint32_t i = seg & 1;
-            mbar_wait(&sh.sum_free[i], ((seg >> 1) & 1) ^ 1, dead);  // the segment before the last is complete
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.sum_free[i], ((seg >> 1) & 1) ^ 1, guard)))
+                break;  // else the segment before the last is complete
             // descriptions run two segments ahead, so that the producer need not stop between segments
             while (!end && described <= (seg ? seg + 2 : 0)) {
                 const auto row_of = [&](const RowAt &at, int c) {
@@ -999,7 +1021,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     return q <= walk.u.i1 ? ((long long)walk.b * a.n + q) * a.heads + walk.h * a.group + g : -1ll;
                 };
                 const Unit &u = walk.u;
-                end = walk.at >= walk.end || __any_sync(0xffffffffu, *dead);
+                end = walk.at >= walk.end;
                 Segment &g = sh.seg[described & 3];
                 if (!end) {
                     const RowAt at(a, walk.rt * NT);
@@ -1036,7 +1058,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     walk.next(a);
             }
             const Segment &g = sh.seg[seg & 3];
-            const bool some = g.tiles > 0 && !__any_sync(0xffffffffu, *dead);
+            const bool some = g.tiles > 0;
             if (some) {
                 const bool tree = a.f.parent && (long long)(g.tile(0) + 1) * kTile > g.first;
                 describe_columns<NT, 32>(a, g, g.b, g.h, g.rt, tree, sh.col[i], lane);
@@ -1051,12 +1073,10 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 if (some)
                     load_queries<D, NT>(a, g.b, g.h, g.rt, sh.q[i][0], sh.col[i], &sh.q_ready[i]);
             }
-            if (!some) {
-                if (*dead && seg > 0)  // the last queries in flight land
-                    for (uint32_t k = 0; k < 4096 && !mbar_try(&sh.q_ready[i ^ 1], ((seg - 1) >> 1) & 1); ++k)
-                        ;
+            if (lane == 0)
+                sh.asked = seg + 1;
+            if (!some)
                 break;
-            }
         }
     } else if (wid >= kProducer) {
         // ---------------- producer ----------------
@@ -1064,10 +1084,12 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         if (lane < 2)
             asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &vmap : &kmap));
         int ks = 0, vs = 0;
-        uint32_t k_phase = 1, v_phase = 1, issued = 0;
+        uint32_t k_phase = 1, v_phase = 1, k_issued = 0, v_issued = 0;
         const bool pos = a.f.slopes && a.c.positions;
-        for (uint32_t seg = 0; !__any_sync(0xffffffffu, *dead); ++seg) {
-            mbar_wait(&sh.seg_ready[seg & 3], (seg >> 2) & 1, dead);
+        bool go = true;
+        for (uint32_t seg = 0; go; ++seg) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.seg_ready[seg & 3], (seg >> 2) & 1, guard)))
+                break;
             const Segment &u = sh.seg[seg & 3];
             const int tiles = u.tiles, h = u.h;
             if (tiles == 0)
@@ -1097,19 +1119,22 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     report(a.status, SPEC_STATUS_BAD_PAGE);
                 const uint32_t came = __ballot_sync(0xffffffffu, ok);
                 const size_t at = (size_t)max(page, 0) * a.c.kv_heads + h;
-                bool go = true;
-                if (keys)
-                    go = __all_sync(0xffffffffu, mbar_wait(&sh.k_empty[ks], k_phase, dead));
-                if (keys && go) {
+                if (keys) {
+                    go = __all_sync(0xffffffffu, mbar_wait(&sh.k_empty[ks], k_phase, guard));
+                    if (!go)
+                        break;
+                    ++k_issued;
                     if (lane == 0)
                         mbar_expect(&sh.k_full[ks], (uint32_t)__popc(came) * (uint32_t)(P * D));
                     __syncwarp();
                     if (ok)
                         tma_load(&kmap, sh.k[ks] + lane * P * D, &sh.k_full[ks], 0, 0, h, page);
                 }
-                if (values)
-                    go = __all_sync(0xffffffffu, mbar_wait(&sh.v_empty[vs], v_phase, dead)) && go;
-                if (values && go) {
+                if (values) {
+                    go = __all_sync(0xffffffffu, mbar_wait(&sh.v_empty[vs], v_phase, guard));
+                    if (!go)
+                        break;
+                    ++v_issued;
                     StageInfo &info = sh.info[vs];
                     if (lane == 0) {
                         info.came = came;
@@ -1126,7 +1151,6 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     if (lane < blocks)
                         copies_arrive(&sh.v_full[vs]);
                 }
-                issued += go;
                 if (++ks == KS) {
                     ks = 0;
                     k_phase ^= 1;
@@ -1137,10 +1161,10 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 }
             }
         }
-        if (keys)
-            drain<KS>(sh.k_full, issued, dead, a.status);
-        if (values)
-            drain<VS>(sh.v_full, issued, dead, a.status);
+        if (keys && lane == 0)
+            sh.issued[0] = k_issued;
+        if (values && lane == 0)
+            sh.issued[1] = v_issued;
     } else if (wid == kScores) {
         // ---------------- S^T = K Q^T ----------------
         const uint32_t desc = instr_desc(NT, a.c.code, false, false);
@@ -1150,17 +1174,20 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                        q_desc = smem_desc(smem_u32(sh.q[0][0]), 16, 8 * D, swizzle);
         int ks = 0, w = 0;
         uint32_t k_phase = 0, s_phase = 1;
+        bool go = true;
 #pragma unroll 1
-        for (uint32_t seg = 0; !__any_sync(0xffffffffu, *dead); ++seg) {
-            mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, dead);
+        for (uint32_t seg = 0; go; ++seg) {
+            if (!__all_sync(0xffffffffu, mbar_wait<true>(&sh.q_ready[seg & 1], (seg >> 1) & 1, guard)))
+                break;
             const int tiles = __shfl_sync(0xffffffffu, sh.seg[seg & 3].tiles, 0);
             if (tiles == 0)
                 break;
             const uint64_t qd = q_desc + (seg & 1) * (2 * NT * D >> 4);
 #pragma unroll 1
             for (int x = 0; x < tiles; ++x) {
-                mbar_wait(&sh.k_full[ks], k_phase, dead);
-                mbar_wait(&sh.s_free[w], s_phase, dead);
+                go = __all_sync(0xffffffffu, mbar_wait(&sh.k_full[ks], k_phase, guard) && mbar_wait(&sh.s_free[w], s_phase, guard));
+                if (!go)
+                    break;
                 tc_after();
                 if (elected()) {
                     const uint64_t kd = k_desc + (uint32_t)ks * (S::kBytes >> 4);
@@ -1179,7 +1206,6 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 k_phase ^= ks == 0;
             }
         }
-        drain_products(&sh.drained[0], dead);
     } else if (wid == kValues) {
         // ---------------- O^T = V^T P^T ----------------
         const uint32_t desc = instr_desc(NT, a.c.code, true, true);
@@ -1187,18 +1213,22 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                        p_desc = smem_desc(smem_u32(sh.p[0][0]), 128, kTile * 16, 0);
         int vs = 0, w = 0;
         uint32_t v_phase = 0, g = 0;
+        bool go = true;
 #pragma unroll 1
-        for (uint32_t seg = 0; !__any_sync(0xffffffffu, *dead); ++seg) {
-            mbar_wait(&sh.seg_ready[seg & 3], (seg >> 2) & 1, dead);
+        for (uint32_t seg = 0; go; ++seg) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&sh.seg_ready[seg & 3], (seg >> 2) & 1, guard)))
+                break;
             const int tiles = __shfl_sync(0xffffffffu, sh.seg[seg & 3].tiles, 0);
             if (tiles == 0)
                 break;
 #pragma unroll 1
             for (int x = 0; x < tiles; ++x) {
                 const uint32_t i = g % NO;
-                mbar_wait(&sh.p_ready[g % kRing], (g / kRing) & 1, dead);
-                mbar_wait(&sh.v_full[vs], v_phase, dead);
-                mbar_wait(&sh.o_free[i], ((g / NO) & 1) ^ 1, dead);
+                go = __all_sync(0xffffffffu, mbar_wait(&sh.p_ready[g % kRing], (g / kRing) & 1, guard) &&
+                                                 mbar_wait(&sh.v_full[vs], v_phase, guard) &&
+                                                 mbar_wait(&sh.o_free[i], ((g / NO) & 1) ^ 1, guard));
+                if (!go)
+                    break;
                 tc_after();
                 if (elected()) {
                     const uint64_t vd = v_desc + (uint32_t)vs * (S::kBytes >> 4),
@@ -1220,7 +1250,6 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 v_phase ^= vs == 0;
             }
         }
-        drain_products(&sh.drained[1], dead);
     } else if (wid >= 4) {
         // ---------------- softmax ----------------
         const int w = (wid >> 2) - 1, t = tid & 127, bar = 1 + w;
@@ -1229,11 +1258,11 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         uint32_t v_phase = 0, g = 0, mine = 0;
 #pragma unroll 1
         for (uint32_t seg = 0;; ++seg) {
-            mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, dead);
+            const bool came_here = mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, guard);
             const Segment &u = sh.seg[seg & 3];
             const Columns<NT> &col = sh.col[seg & 1];
-            const int tiles = u.tiles;
-            if (barrier_or<128>(bar, tiles == 0 || *dead))
+            const int tiles = came_here ? u.tiles : 0;
+            if (barrier_or<128>(bar, tiles == 0))
                 break;
             bool fresh = true;  // no tile of this segment yet
             {
@@ -1249,7 +1278,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 #pragma unroll 1
             for (int x = 0; x < tiles; ++x) {
                 if (turn == w) {
-                    mbar_wait(&sh.v_full[vs], v_phase, dead);
+                    mbar_wait(&sh.v_full[vs], v_phase, guard);
                     const StageInfo &info = sh.info[vs];
                     const int tile = u.tile(x), j = tile * kTile + t;
                     const uint32_t came = info.came;
@@ -1299,7 +1328,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     // the largest scale among the warp's blocks (positive: the bits order as they do)
                     v_most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v_most)));
                     uint32_t *scales = sh.scale[w][mine & 3];
-                    mbar_wait(&sh.s_full[w], mine & 1, dead);
+                    mbar_wait(&sh.s_full[w], mine & 1, guard);
                     tc_after();
 
                     if (t < NT)
@@ -1435,7 +1464,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     if (t < NT)
                         sh.power[g % kRing][t] =
                             scales[t] == kNoScale ? kNothing : 127 - (int)(scales[t] >> 23) - (int)sh.less[w][t];
-                    mbar_wait(&sh.p_free[w], (mine & 1) ^ 1, dead);
+                    mbar_wait(&sh.p_free[w], (mine & 1) ^ 1, guard);
 #pragma unroll 1
                     for (int c0 = 0; c0 < NT; c0 += 16) {
                         alignas(8) float e[16], l[16];
@@ -1488,7 +1517,8 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 }
             }
             // the rows' totals, warp by warp
-            mbar_wait(&sh.sum_free[seg & 1], ((seg >> 1) & 1) ^ 1, dead);
+            if (barrier_or<128>(bar, !mbar_wait(&sh.sum_free[seg & 1], ((seg >> 1) & 1) ^ 1, guard)))
+                break;
             if (t < NT)
                 sh.last_base[seg & 1][w][t] = -sh.less[w][t];
 #pragma unroll 1
@@ -1505,6 +1535,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
             if (lane == 0)
                 mbar_arrive(&sh.sum_ready[seg & 1]);
         }
+        tmem_store_wait();
     } else {
         // ---------------- adding up ----------------
         const int o0 = D == 128 ? 0 : (wid >> 1) * OC, d = D == 128 ? tid : tid & 63, bar = 1 + NW;
@@ -1514,10 +1545,10 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         alignas(8) float o[OC];
 #pragma unroll 1
         for (uint32_t seg = 0;; ++seg) {
-            mbar_wait(&sh.seg_ready[seg & 3], (seg >> 2) & 1, dead);
+            bool lost = !mbar_wait(&sh.seg_ready[seg & 3], (seg >> 2) & 1, guard), stop = false;
             const Segment &u = sh.seg[seg & 3];
-            const int tiles = u.tiles;
-            if (barrier_or<128>(bar, tiles == 0 || *dead))
+            const int tiles = lost ? 0 : u.tiles;
+            if (barrier_or<128>(bar, tiles == 0))
                 break;
 #pragma unroll
             for (int c = 0; c < OC; ++c)
@@ -1526,7 +1557,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 #pragma unroll 1
             for (int x = 0; x < tiles; ++x) {
                 const uint32_t i = g & 1, io = g % NO;
-                mbar_wait(&sh.p_ready[g % kRing], (g / kRing) & 1, dead);  // the tile's powers
+                lost = !mbar_wait(&sh.p_ready[g % kRing], (g / kRing) & 1, guard) || lost;  // the tile's powers
                 bool moved = false;
                 float alpha = 1.0f;
                 if (tid < NT) {
@@ -1540,15 +1571,17 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     }
                     sh.factor[i][tid] = power == kNothing ? 0.0f : power_gap(power, ref);
                 }
-                if (barrier_or<128>(bar, moved)) {
+                if (barrier_or<128>(bar, moved || lost)) {
                     if (tid < NT)
                         sh.inverse[tid] = alpha;
-                    named_barrier<128>(bar);
+                    stop = barrier_or<128>(bar, lost);
+                    if (stop)
+                        break;
 #pragma unroll
                     for (int c = 0; c < OC; ++c)
                         o[c] *= sh.inverse[o0 + c];
                 }
-                mbar_wait(&sh.o_full[io], (g / NO) & 1, dead);
+                lost = !mbar_wait(&sh.o_full[io], (g / NO) & 1, guard);
                 tc_after();
 #pragma unroll
                 for (int c1 = 0; c1 < OC; c1 += kPart) {
@@ -1569,11 +1602,14 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                     mbar_arrive(&sh.o_free[io]);
                 ++g;
             }
+            if (stop)
+                break;
             // whole units are finished here; parts go to the workspace for join_kernel
             const bool whole = u.whole;
             const long long slot = 2ll * blockIdx.x + (u.x0 == 0);
-            mbar_wait(&sh.sum_ready[seg & 1], (seg >> 1) & 1, dead);
-            named_barrier<128>(bar);
+            lost = !mbar_wait(&sh.sum_ready[seg & 1], (seg >> 1) & 1, guard) || lost;
+            if (barrier_or<128>(bar, lost))
+                break;
             bool far = false;
             if (tid < NT) {
                 float total = 0.0f, base = 0.0f, part[NW];
@@ -1641,6 +1677,22 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
     tc_before();
     __syncthreads();
     tc_after();
+    if (guard->dead) {
+        if (wid == kQueries) {
+            for (uint32_t k = 1; k <= 2 && k <= sh.asked; ++k)
+                land(&sh.q_ready[(sh.asked - k) & 1], ((sh.asked - k) >> 1) & 1);
+        } else if (wid >= kProducer) {
+            if (S::NP == 1 || wid == kProducer)
+                land_stages<KS>(sh.k_full, sh.issued[0]);
+            if (S::NP == 1 || wid != kProducer)
+                land_stages<VS>(sh.v_full, sh.issued[1]);
+        } else if (wid == kScores || wid == kValues) {
+            land_products(&sh.drained[wid == kValues]);
+        }
+        if (tid == 0)
+            report(a.status, SPEC_STATUS_INTERNAL);
+        __syncthreads();
+    }
     if (wid == kValues)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::kAlloc));
 }
@@ -1665,7 +1717,8 @@ template <int D, int NT> struct WeighShared {
     alignas(8) uint64_t full[kStages], empty[kStages];
     uint64_t s_full[kWeighGroups], s_free[kWeighGroups], q_ready, drained;
     uint32_t tmem;
-    int dead;
+    uint32_t issued[2], asked;  // tiles up to the last one of each producer, row tiles' queries
+    Guard guard;
 };
 
 __device__ __forceinline__ bool covers(const Unit &u, int tile)
@@ -1682,9 +1735,11 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     extern __shared__ uint8_t raw[];
     Shared &sh = *(Shared *)(raw + ((1024 - (smem_u32(raw) & 1023)) & 1023));
     const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    volatile int *dead = &sh.dead;
+    volatile Guard *guard = &sh.guard;
     if (tid == 0) {
-        sh.dead = 0;
+        sh.guard.dead = 0;
+        sh.guard.limit = a.wait_limit;
+        sh.issued[0] = sh.issued[1] = sh.asked = 0;
         for (int i = 0; i < ST; ++i) {
             mbar_init(&sh.full[i], 1 + kTile / a.c.block);  // the expected bytes, and each block's scales
             mbar_init(&sh.empty[i], 5);  // the products, and the four warps that read the scales
@@ -1717,9 +1772,10 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
     int b = range.b;
     long long at = range.begin, skip = range.skip;
     int st = 0;
-    uint32_t phase = 0, g = 0, seg = 0, issued = 0;
+    uint32_t phase = 0, g = 0, seg = 0;
+    bool go = true;
     // a stretch of tiles of one sequence and head; within it, the row tiles one after the other
-    while (at < range.end) {
+    while (go && at < range.end) {
         const Unit all = unit_for(a, b, 0, a.n - 1);
         if (skip >= (long long)all.count * a.c.kv_heads) {
             skip = 0;
@@ -1729,7 +1785,7 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         }
         const int h = (int)(skip / all.count), x0 = (int)(skip % all.count);
         const int x1 = (int)min((long long)all.count, x0 + (range.end - at));
-        for (int rt = 0; rt < a.row_tiles; ++rt) {
+        for (int rt = 0; go && rt < a.row_tiles; ++rt) {
             const Unit u = row_unit<NT>(a, b, rt);
             const int low = all.tile(x0), high = all.tile(x1 - 1);
             if (u.count == 0 || !(low < u.head_tiles || (high >= u.low && low < u.low + u.count - u.head_tiles)))
@@ -1759,10 +1815,13 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                     const bool ok = (unsigned)page < (unsigned)a.c.num_pages;
                     if (page != -2 && !ok)
                         report(a.status, SPEC_STATUS_BAD_PAGE);
-                    if ((int)(g++ & 1) == wid - kProducer &&  // two producers, tiles in turn
-                        __all_sync(0xffffffffu, mbar_wait(&sh.empty[st], phase ^ 1, dead))) {
+                    if ((int)(g++ & 1) == wid - kProducer) {  // two producers, tiles in turn
+                        go = __all_sync(0xffffffffu, mbar_wait(&sh.empty[st], phase ^ 1, guard));
+                        if (!go)
+                            break;
                         load_keys<D>(a, &kmap, h, page, ok, blocks, sh.info[st], sh.tiles[st], &sh.full[st], lane);
-                        issued = g;
+                        if (lane == 0)
+                            sh.issued[wid - kProducer] = g;
                     }
                     if (++st == ST) {
                         st = 0;
@@ -1772,12 +1831,14 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
             } else if (wid == kProducts) {
                 // ---------------- products ----------------
                 const uint32_t desc = instr_desc(2 * NT, a.c.code, false, false);  // both terms' columns side by side
-                mbar_wait(&sh.q_ready, seg++ & 1, dead);
-                for (int x = x0; x < x1; ++x) {
+                go = __all_sync(0xffffffffu, mbar_wait<true>(&sh.q_ready, seg++ & 1, guard));
+                for (int x = x0; go && x < x1; ++x) {
                     if (!covers(u, all.tile(x)))
                         continue;
-                    mbar_wait(&sh.full[st], phase, dead);
-                    mbar_wait(&sh.s_free[g % NW], ((g / NW) & 1) ^ 1, dead);
+                    go = __all_sync(0xffffffffu, mbar_wait(&sh.full[st], phase, guard) &&
+                                                     mbar_wait(&sh.s_free[g % NW], ((g / NW) & 1) ^ 1, guard));
+                    if (!go)
+                        break;
                     tc_after();
                     if (elected()) {
                         const uint64_t kd = smem_desc(smem_u32(sh.tiles[st]), 16, 8 * D, D == 128 ? 2 : 4),
@@ -1799,7 +1860,9 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                 // ---------------- sums ----------------
                 const int w = wid >> 2, t = tid & 127;
                 const Askers askers{u.first, u.prefix, u.i1, rt * NT, a.group};
-                named_barrier<128 * NW>(3);
+                go = !barrier_or<128 * NW>(3, guard->dead);
+                if (!go)
+                    break;
                 const bool tree = a.f.parent && (long long)(all.tile(x1 - 1) + 1) * kTile > u.first;
                 describe_columns<NT, 128 * NW>(a, u, b, h, rt, tree, sh.col, tid);
                 if (tid < NT) {
@@ -1811,29 +1874,31 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                 if (tid == 0) {
                     mbar_expect(&sh.q_ready, kQueryBytes<D, NT>);
                     load_queries<D, NT>(a, b, h, rt, sh.q[0], sh.col, &sh.q_ready);
+                    sh.asked = seg + 1;
                 }
                 named_barrier<128 * NW>(3);
                 if (tree) {
                     mark_kin<NT, 128 * NW>(sh.col, tid);
                     named_barrier<128 * NW>(3);
                 }
-                mbar_wait(&sh.q_ready, seg++ & 1, dead);
+                mbar_wait(&sh.q_ready, seg++ & 1, guard);
                 for (int x = x0; x < x1; ++x) {
                     const int tile = all.tile(x);
                     if (!covers(u, tile))
                         continue;
                     if ((int)(g % NW) == w) {
-                        mbar_wait(&sh.full[st], phase, dead);
+                        // where a wait runs out, nothing came and nothing is added
+                        bool came_all = mbar_wait(&sh.full[st], phase, guard);
                         const StageInfo &info = sh.info[st];
                         const int j0 = tile * kTile, j = j0 + t, page = info.page[t >> log_p];
-                        const uint32_t came = info.came;
+                        const uint32_t came = came_all ? info.came : 0;
                         const bool edge = came != (1u << blocks) - 1 || !interior(a, u, j0);
                         const bool cached = !edge || (j < u.len && ((came >> (t >> log_p)) & 1));
                         const float ks = cached ? info.k_scale[t >> log_p] : 0.0f;
                         const float pos = FORM && a.f.slopes ? from_origin(a.c.positions ? info.pos[t] : j, sh.col.origin) : 0.0f;
                         const Mask<NT> see = edge && cached ? seen_by<NT>(a, askers, sh.col, j) : 0;
                         float *weight = a.weights + ((size_t)(cached ? page : 0) * a.c.kv_heads + h) * P + (t & (P - 1));
-                        mbar_wait(&sh.s_full[w], (g / NW) & 1, dead);
+                        came_all = mbar_wait(&sh.s_full[w], (g / NW) & 1, guard) && came_all;
                         tc_after();
                         float sum = 0.0f;
 #pragma unroll 1
@@ -1868,13 +1933,13 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
                         }
                         tc_before();
                         __syncwarp();
-                        if (lane == 0) {
+                        if (lane == 0 && came_all) {  // a tile that did not come is not given back
                             mbar_arrive(&sh.s_free[w]);
                             mbar_arrive(&sh.empty[st]);
                         }
                         // one addition a token and row tile, those of several row tiles a barrier apart: no order is left open,
                         // and nothing waits for the weight's old value
-                        if (cached)
+                        if (cached && came_all)
                             atomicAdd(weight, sum);
                     }
                     ++g;
@@ -1888,17 +1953,21 @@ __global__ void __launch_bounds__(kWeighThreads, 1)
         at += x1 - x0;
         skip += x1 - x0;
     }
-    if (wid >= kProducer && *dead) {  // the copies of this producer's last tiles land
-        for (int t = (int)issued - 1; t >= 0 && t + ST >= (int)issued; t -= 2)
-            for (uint32_t k = 0; k < 4096 && !mbar_try(&sh.full[t % ST], (t / ST) & 1); ++k)
-                ;
-        report(a.status, SPEC_STATUS_INTERNAL);
-    }
-    if (wid == kProducts)
-        drain_products(&sh.drained, dead);
     tc_before();
     __syncthreads();
     tc_after();
+    if (guard->dead) {
+        if (wid == 0 && sh.asked > 0)
+            land(&sh.q_ready, (sh.asked - 1) & 1);
+        if (wid >= kProducer)  // the copies of this producer's last tiles
+            for (int t = (int)sh.issued[wid - kProducer] - 1, k = 0; t >= 0 && k < ST; t -= 2, k += 2)
+                land(&sh.full[t % ST], (t / ST) & 1);
+        if (wid == kProducts)
+            land_products(&sh.drained);
+        if (tid == 0)
+            report(a.status, SPEC_STATUS_INTERNAL);
+        __syncthreads();
+    }
     if (wid == kProducts)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Shared::kAlloc));
 }
