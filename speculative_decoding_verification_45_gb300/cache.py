@@ -9,7 +9,9 @@
 
 Every call checks its tensors, enqueues its kernels on the current stream (or
 ``stream``) and returns; include/spec_verify.h states the operations, layouts and
-error behaviour.  All tensors are CUDA tensors on the cache's device.
+error behaviour.  All tensors are CUDA tensors on the cache's device, which is
+the current one.  ``status`` tells of bad lengths, pages and trees, and of a wait
+in a kernel that ran out: without it such a call looks like any other.
 """
 from __future__ import annotations
 
@@ -80,6 +82,14 @@ def _strides(t, name, multiple):
     return st
 
 
+def _on_current(device):
+    """The kernels are launched on the current device, where the cache has to be."""
+    current = torch.cuda.current_device()
+    if device.index != current:
+        raise ValueError(f"cache.k lives on {device}, but the current device is cuda:{current}: call under "
+                         f"torch.cuda.device({device.index})")
+
+
 def _describe(cache, block_table, lengths):
     """The spec_cache of these tensors, checked; their device; the lengths' address."""
     k, v, k_scale, v_scale, positions = cache
@@ -91,6 +101,7 @@ def _describe(cache, block_table, lengths):
     if not k.is_cuda:
         raise ValueError("cache.k must be a CUDA tensor")
     dev, shape = k.device, k.shape
+    _on_current(dev)
     if v.shape != shape or v.device != dev:
         raise ValueError(f"cache.v: expected shape {tuple(shape)} on {dev}, got {tuple(v.shape)} on {v.device}")
     pages, heads, block, dim = shape
@@ -197,12 +208,11 @@ def _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent):
 
 @functools.lru_cache(maxsize=256)
 def _workspace_bytes(batch, kv_heads, block, dim, n, heads, device):
-    """Bytes that spec_cache_attend_workspace asks for; they follow from these sizes and the device."""
+    """Bytes that spec_cache_attend_workspace asks for; they follow from these sizes and the device, which is current."""
     fake = 16  # an address for the check of the description; nothing is read
     c = _native.Cache(fake, fake, fake, fake, None, fake, (16,) * 3, (16,) * 3, 1, batch, 1, 1, kv_heads, block, dim, 0)
     need = ctypes.c_int64()
-    with torch.cuda.device(device):
-        rc = _native.load().spec_cache_attend_workspace(ctypes.byref(c), n, heads, ctypes.byref(need))
+    rc = _native.load().spec_cache_attend_workspace(ctypes.byref(c), n, heads, ctypes.byref(need))
     if rc:
         _fail(rc, "spec_cache_attend_workspace")
     return need.value
