@@ -321,7 +321,8 @@ spec_status spec_device_pointer(const void *ptr, const void **device_ptr);
  * outputs zero (lse -inf, lengths 0), and a token on a page outside
  * [0, num_pages) counts as not cached; SPEC_STATUS_BAD_LENGTH and
  * SPEC_STATUS_BAD_PAGE are OR-ed into *status when status is not NULL.  Scales
- * that a call reads are positive and finite.
+ * that a call reads are positive and finite (attention is made for those that
+ * spec_cache_append chooses, 2^-100 to 2^120; smaller ones may count as 0).
  * Ownership, stream and error rules as for spec_verify, but that a call may
  * enqueue up to three kernels; every array is device memory.  Nothing is
  * allocated. */
@@ -390,7 +391,18 @@ typedef struct spec_cache_form {
  *        16-byte aligned, the last dimension dense
  *   out  [batch, n, heads, dim] bf16, 16-byte aligned; lse [batch, n, heads] float32
  *   workspace  spec_cache_attend_workspace bytes, 16-byte aligned; its contents
- *              do not matter and concurrent calls need one each */
+ *              do not matter and concurrent calls need one each
+ * Precision.  Scores, the softmax's sums and lse are 32-bit; out is rounded to
+ * bf16 once.  The products take 8-bit operands, so what multiplies the codes is
+ * held as two e4m3 numbers:
+ *   a query's elements are exact down to 2^-10 of the largest of their row, and
+ *     off by at most 2^-17 of that one below;
+ *   a token's softmax weight is off by at most 2^-8 of itself, as one in bf16
+ *     would be, or by 2^-17 of the largest weight times the largest value scale
+ *     of the block of 128 tokens (counted from the sequence's first) that it lies
+ *     in, divided by its own value scale, where that is more.
+ * The second part matters only in dimensions that the tokens of most weight leave
+ * near 0; there, weights of less than 2^-18 of the largest one count as 0. */
 spec_status spec_cache_attend(const spec_cache *cache, const int32_t *lengths, const void *q,
                               const int64_t q_stride[3], int n, int heads, const spec_cache_form *form, void *out,
                               float *lse, void *workspace, int64_t workspace_bytes, uint32_t *status, void *stream);
@@ -411,7 +423,8 @@ spec_status spec_cache_set_wait_limit(int clocks);
  * leaves them as they are): a slot must hold 0 when a token is written to it.  In
  * a speculative round, call this after the accept test with the accepted tokens
  * only (their number as num_new, lengths to match, the same q and lse); then the
- * slots of rejected tokens stay at 0 and what those looked at does not count.  workspace: as for spec_cache_attend.  Pages that several sequences share must not be weighed in one
+ * slots of rejected tokens stay at 0 and what those looked at does not count.
+ * Queries are held as for spec_cache_attend; all else is 32-bit.  workspace: as for spec_cache_attend.  Pages that several sequences share must not be weighed in one
  * call: their sums would race. */
 spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, const void *q,
                              const int64_t q_stride[3], int n, int heads, const spec_cache_form *form,

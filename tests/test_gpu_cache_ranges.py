@@ -153,3 +153,33 @@ def test_an_evicted_block_of_bad_pages_has_a_scale(sv):  # noqa: F811
     assert torch.isfinite(value).all() and torch.isfinite(lse).all()
     sv.cache_evict(cache, out.cuda(), lengths, w, 32, 4, torch.tensor([[1, 2]], dtype=torch.int32, device="cuda"))
     assert not torch.isnan(cache.k.float()).any() and (cache.k_scale > 0).all()
+
+
+@pytest.mark.parametrize("columns", COLUMNS, ids=[16, 32, 48])
+@pytest.mark.parametrize("apart", [0, 8, 12, 16, 24])
+@pytest.mark.parametrize("block", [16, 64])
+def test_dimensions_that_only_small_blocks_fill(sv, columns, apart, block):  # noqa: F811
+    """The stated precision of weights: 2^-8 of each, or 2^-17 of the largest weight times the largest scale of its
+    128 tokens.  Where large-scaled blocks hold zeros, the second part shows."""
+    case = Case([500], dim=64, block=block, seed=59, **columns)
+    case.pool.scale[1] = 1.0
+    large = case.table[0, :: 2].long()
+    case.pool.scale[1, large] = 2.0 ** apart
+    case.pool.codes[1, large, :, :, :32] = 0
+    ref = case.reference()
+    _, _, (out, lse) = case.run(sv)
+    assert ((lse.cpu() - ref["lse"]).abs() <= ref["dx"]).all()
+    step, group = torch.zeros_like(ref["out"]), columns["heads"] // columns["kv_heads"]
+    for (b, i, h), (see, x, _) in ref["xs"].items():
+        j = see.nonzero()[:, 0]
+        page, row, tile = case.table[b][j // block].long(), j % block, j // 128
+        p, scale = torch.exp(x - ref["lse"][b, i, h]), case.pool.scale[1, page, h // group]
+
+        def most(y):
+            return torch.zeros(4, dtype=torch.float64).scatter_reduce(0, tile, y, "amax")[tile]
+
+        step[b, i, h] = 2.0 ** -17 * (most(p) * most(scale)) @ case.pool.codes[1, page, h // group, row].abs()
+    bound = (2.0 ** -8 * ref["out"].abs() + (2.0 ** -8 + 2.0 ** -11 + 2 * ref["dx"][..., None]) * ref["mean"] + step
+             + 2.0 ** -30 * 2.0 ** apart)
+    far = (out.cpu().double() - ref["out"]).abs() - bound
+    assert (far <= 0).all(), float(far.max())
