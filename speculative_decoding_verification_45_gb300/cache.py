@@ -143,6 +143,16 @@ def _new(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _dense(t, stream):
+    """The tensor, or a dense copy that the call's stream makes and uses."""
+    if t.is_contiguous():
+        return t
+    if stream is None:
+        return t.contiguous()
+    with torch.cuda.stream(stream):
+        return t.contiguous()
+
+
 def _output(t, name, dtype, shape, device, stream):
     """An output that the caller gave, or a new one; and its address."""
     if t is not None:
@@ -265,7 +275,8 @@ def cache_weigh(q, cache, block_table, lengths, lse, weights, num_new=None, scal
                 window=0, prefix=None, parent=None, status=None, stream=None):
     """Add the attention weight that each cached token received (spec_cache_weigh).
 
-    ``lse`` is what cache_attend returned for the same q and form; ``weights``
+    ``lse`` is what cache_attend returned for the same q and form, or that of
+    another attention with any strides (copied if it is not dense); ``weights``
     [num_pages, kv_heads, block] float32 grows by the sum over queries and query
     heads of exp(score - lse).  Returns ``weights``.  In a speculative round this
     comes after the accept test, with the accepted tokens only (``num_new`` their
@@ -275,6 +286,7 @@ def cache_weigh(q, cache, block_table, lengths, lse, weights, num_new=None, scal
     """
     c, dev, len_ptr = _describe(cache, block_table, lengths)
     f, n, heads, stride = _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent)
+    lse = _dense(lse, stream)
     lse_ptr = _check(lse, "lse", torch.float32, (c.batch, n, heads), dev)
     w_ptr = _check(weights, "weights", torch.float32, (c.num_pages, c.kv_heads, c.block), dev)
     work, size = _workspace(c, n, heads, dev, stream)
