@@ -183,3 +183,19 @@ def test_dimensions_that_only_small_blocks_fill(sv, columns, apart, block):  # n
              + 2.0 ** -30 * 2.0 ** apart)
     far = (out.cpu().double() - ref["out"]).abs() - bound
     assert (far <= 0).all(), float(far.max())
+
+
+def test_a_nan_value_reaches_the_rows_that_see_it_even_without_weight(sv):  # noqa: F811
+    """Some rows see it with an exponential of 0, some do not see it; the latter are as without it."""
+    kw = dict(lengths=[300], new=4, heads=8, kv_heads=2, block=16, window=150)
+    clean, case = Case(seed=60, **kw), Case(seed=60, **kw)
+    for x in (clean, case):
+        opposed(x, 400.0, first=5)
+    at = 300 - 4 - 150 + 2  # the windows of queries 0 and 1 reach it
+    case.pool.codes[1, case.table[0, at // 16], :, at % 16, 7] = math.nan
+    ref = clean.reference()
+    _, _, (out, lse) = case.run(sv)
+    assert torch.isnan(out[0, :2]).any(-1).all() and torch.isfinite(out[0, 2:]).all()
+    assert ((lse.cpu() - ref["lse"]).abs() <= ref["dx"]).all()
+    _, _, (want, _) = clean.run(sv)
+    assert torch.equal(out[0, 2:], want[0, 2:])
