@@ -756,16 +756,17 @@ template <int NT> struct Walk {
 //
 // The exponents' base: exp2(x - base) in 32 bits has room for 2^127, so a
 // warpgroup keeps a row's base (0, unless the row's first scores lie far below)
-// until a score passes it by 2^64: no running maximum has to be agreed upon
-// before the exponentials.  What the 8-bit weights need is the maximum's exponent
+// until a score passes it by 2^64, or the exponential times the value scale
+// comes to 2^119: no running maximum has to be agreed upon before the
+// exponentials.  What the 8-bit weights need is the maximum's exponent
 // only: 16-bit halves of the exponentials are compared two at a time (9 shuffles
 // for 16 columns) and the four warps meet in shared memory.
 //
 // What bounds it: up to 48 rows a key head, memory (2 D bytes a token; 64
-// sequences of 4,000 to 8,000 tokens, 20 rows: 152 us, 5.4 TB/s; one token per
-// sequence, 4 rows: 143 us, 5.7 TB/s, of 6.8 that a copy reaches), and between
+// sequences of 4,000 to 8,000 tokens, 20 rows: 155 us, 5.3 TB/s; one token per
+// sequence, 4 rows: 144 us, 5.7 TB/s, of 6.7 that a copy reaches), and between
 // units the filling and draining of this chain, about 5,000 cycles each (256
-// sequences of 1,000 to 2,000 tokens: 193 us for 828 MB).  With a cap or a bias,
+// sequences of 1,000 to 2,000 tokens: 190 us for 828 MB).  With a cap or a bias,
 // or more rows, the softmax's instructions: about 900 issue slots of an SM
 // quarter for a tile of 32 columns, issued at 0.5 to 0.6 a cycle.  The program
 // has to stay short: columns are taken 16 at a time by the same instructions
@@ -1705,7 +1706,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 // += sum over the rows of exp2(x - lse).  A thread owns a token of its tile and
 // adds its columns up, so a sum needs no other thread and no atomic.  Three
 // warpgroups take tiles in turn.  Keys only: half of what attention reads.
-constexpr int kWeighGroups = 3;  // 55 us for 32 sequences of 8192 tokens; two took 60, four 56
+constexpr int kWeighGroups = 3;  // 32 sequences of 8192 tokens took 55 us when it was chosen (51 now); two 60, four 56
 constexpr int kWeighThreads = 128 * kWeighGroups + 96;
 
 template <int D, int NT> struct WeighShared {
