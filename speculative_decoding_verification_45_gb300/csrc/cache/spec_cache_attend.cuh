@@ -415,6 +415,7 @@ template <int NT> struct Columns {
     float pos[NT];     // position, from origin on
     int origin;        // position of the first column's query: differences keep their bits however far out they lie
     int query[NT];     // its query, -1: none
+    uint32_t nan_rows[2];  // columns, one bit each, that see a NaN value which others of its tile do not
     uint32_t kin[NT][kMaxNodes / 32];
     int up[kMaxNodes];
 };
@@ -548,8 +549,10 @@ __device__ __forceinline__ void describe_columns(const AttendArgs &a, const Unit
 {
     const RowAt at(a, rt * NT);
     const int origin = a.f.slopes && at.i0 <= u.i1 ? position_of(a, b, h, u.first + at.i0) : 0;
-    if (t == 0)
+    if (t == 0) {
         col.origin = origin;
+        col.nan_rows[0] = col.nan_rows[1] = 0;
+    }
     for (int c = t; c < NT; c += THREADS) {
         int i, g;
         at.of(a, c, i, g);
@@ -832,7 +835,6 @@ template <int D, int NT> struct AttendShared {
 
 constexpr uint32_t kNoScale = 253u << 23;  // 2^126, where a tile leaves nothing to a row; others have 2^125 at most
 constexpr int kNothing = INT_MIN;           // the power of such a tile's sums, and of none yet: it says nothing of the row's level
-constexpr uint32_t kUnseen = 0x80000000u;  // -0: the exponential of a token that the row does not see
 
 __device__ __forceinline__ int ordered(float x)
 {
@@ -840,13 +842,8 @@ __device__ __forceinline__ int ordered(float x)
     return i ^ ((i >> 31) & 0x7fffffff);
 }
 
-struct MaxHalves {  // signed: kUnseen is the least
-    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const
-    {
-        uint32_t r;
-        asm("max.s16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    }
+struct MaxHalves {
+    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return max_halves(a, b); }
 };
 struct MaxInt {
     __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
@@ -1261,7 +1258,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
         for (uint32_t seg = 0;; ++seg) {
             const bool came_here = mbar_wait(&sh.q_ready[seg & 1], (seg >> 1) & 1, guard);
             const Segment &u = sh.seg[seg & 3];
-            const Columns<NT> &col = sh.col[seg & 1];
+            Columns<NT> &col = sh.col[seg & 1];
             const int tiles = came_here ? u.tiles : 0;
             if (barrier_or<128>(bar, tiles == 0))
                 break;
@@ -1296,17 +1293,16 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                         const Askers askers{u.first, u.prefix, u.i1, u.rt * NT, a.group};
                         see = cached ? seen_by<NT>(a, askers, col, j) : 0;
                         const bool all = see == all_columns<NT>(askers);
-                        v_most = see ? v_scale : 0.0f;
+                        v_scale = v_most = see ? v_scale : 0.0f;
                         uint4 *row = (uint4 *)(sh.v[vs] + t * D);
                         if (!cached) {  // nothing was loaded here
                             k_scale = 0.0f;
-                            v_scale = 1.0f;
 #pragma unroll 1
                             for (int k = 0; k < D / 16; ++k)
                                 row[(k + t) & (D / 16 - 1)] = make_uint4(0, 0, 0, 0);
                         } else if (!all) {
                             // a NaN that some row does not see must not reach the product: 0 stands in its place, and
-                            // the weights of the rows that do see it become NaN
+                            // the rows that do see it are noted
                             const uint32_t add = a.c.code == SPEC_E4M3 ? 0x01010101u : 0x04040404u;
                             uint32_t bad = 0;
 #pragma unroll 4
@@ -1321,7 +1317,9 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                                     const uint32_t v = ((uint32_t *)row)[k], nan = ((v & 0x7f7f7f7fu) + add) & 0x80808080u;
                                     ((uint32_t *)row)[k] = v & ~((nan >> 7) * 0xffu);
                                 }
-                                v_scale = __int_as_float(0x7fffffff);
+                                atomicOr(&col.nan_rows[0], (uint32_t)see);
+                                if (NT > 32)
+                                    atomicOr(&col.nan_rows[1], (uint32_t)((uint64_t)see >> 32));
                             }
                         }
                         __syncwarp();
@@ -1345,7 +1343,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             const uint32_t bits = (uint32_t)(see >> c0);
 #pragma unroll
                             for (int c = 0; c < 16; ++c)
-                                e[c] = (bits >> c) & 1 ? e[c] : __uint_as_float(kUnseen);
+                                e[c] = (bits >> c) & 1 ? e[c] : 0.0f;
                         }
                     };
                     while (true) {
@@ -1420,7 +1418,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             for (int c = 0; c < 8; ++c)
                                 half[c] = __byte_perm(__float_as_uint(e[2 * c]), __float_as_uint(e[2 * c + 1]), 0x7632);
                             int which;
-                            const uint32_t two = warp_combine<8>(half, lane, which, MaxHalves()) & 0x7fff7fffu;
+                            const uint32_t two = warp_combine<8>(half, lane, which, MaxHalves());
                             const uint32_t most = lane & 1 ? two & 0xffff0000u : two << 16;  // a float, cut to 16 bits
                             // 2^k with 224 <= 2^k * largest weight <= 448 (448 = 1.75 * 2^8)
                             const uint32_t largest = __float_as_uint(__uint_as_float(most) * v_most), top = (largest + (0x1fu << 16)) >> 23;
@@ -1486,11 +1484,6 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                             const float2 p0 = mul2(mul2(((float2 *)e)[2 * c4], v2), make_float2(y.x, y.y)),
                                          p1 = mul2(mul2(((float2 *)e)[2 * c4 + 1], v2), make_float2(y.z, y.w));
                             float p[4] = {p0.x, p0.y, p1.x, p1.y};
-                            if (edge) {  // a scale that is NaN does not reach the rows that do not see it
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    p[k] = __float_as_uint(e[4 * c4 + k]) == kUnseen ? 0.0f : p[k];
-                            }
                             uint32_t first[2], rest[2];
                             split8(p[0], p[1], first[0], rest[0]);
                             split8(p[2], p[3], first[1], rest[1]);
@@ -1640,6 +1633,13 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 const int first = far ? level / 2 : 0;
                 sh.factor[0][tid] = power2(first);
                 sh.inverse[tid] = live && ref != kNothing ? power2(level - first) / significand : 0.0f;
+                if (sh.col[seg & 1].nan_rows[tid >> 5] >> (tid & 31) & 1) {
+                    sh.inverse[tid] = __int_as_float(0x7fffffff);
+                    if (!whole && !live) {  // a part of no weight has to be joined all the same
+                        total = 0x1p-126f;
+                        base = -0x1p30f;
+                    }
+                }
                 if (whole) {
                     if (row >= 0)
                         a.lse[row] = live ? (base + log2f(total)) * 0.6931471805599453f : -INFINITY;
