@@ -394,15 +394,17 @@ typedef struct spec_cache_form {
  *              do not matter and concurrent calls need one each
  * Precision.  Scores, the softmax's sums and lse are 32-bit; out is rounded to
  * bf16 once.  The products take 8-bit operands, so what multiplies the codes is
- * held as two e4m3 numbers:
- *   a query's elements are exact down to 2^-10 of the largest of their row, and
- *     off by at most 2^-17 of that one below;
- *   a token's softmax weight is off by at most 2^-8 of itself, as one in bf16
- *     would be, or by 2^-17 of the largest weight times the largest value scale
- *     of the block of 128 tokens (counted from the sequence's first) that it lies
- *     in, divided by its own value scale, where that is more.
+ * held as two or three of them:
+ *   a query's elements are exact down to 2^-14 of the largest of their row, and
+ *     off by at most 2^-21 of that one below;
+ *   a token's softmax weight is off by at most r of itself or, where that is more,
+ *     by s of the largest weight times the largest value scale of the 128 tokens
+ *     (counted from the sequence's first) that it lies among, divided by its own
+ *     value scale: r = 2^-10 and s = 2^-21 with up to 32 rows (queries times query
+ *     heads) a key head, as in a round of drafts; r = 2^-8, as in bf16, and s =
+ *     2^-17 with more, as in a prompt.
  * The second part matters only in dimensions that the tokens of most weight leave
- * near 0; there, weights of less than 2^-18 of the largest one count as 0. */
+ * near 0; there, weights of less than s / 2 of the largest one count as 0. */
 spec_status spec_cache_attend(const spec_cache *cache, const int32_t *lengths, const void *q,
                               const int64_t q_stride[3], int n, int heads, const spec_cache_form *form, void *out,
                               float *lse, void *workspace, int64_t workspace_bytes, uint32_t *status, void *stream);
@@ -424,7 +426,8 @@ spec_status spec_cache_set_wait_limit(int clocks);
  * a speculative round, call this after the accept test with the accepted tokens
  * only (their number as num_new, lengths to match, the same q and lse); then the
  * slots of rejected tokens stay at 0 and what those looked at does not count.
- * Queries are held as for spec_cache_attend; all else is 32-bit.  workspace: as for spec_cache_attend.  Pages that several sequences share must not be weighed in one
+ * A query's elements are exact down to 2^-10 of the largest of their row and off
+ * by at most 2^-17 of it below; all else is 32-bit.  workspace: as for spec_cache_attend.  Pages that several sequences share must not be weighed in one
  * call: their sums would race. */
 spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, const void *q,
                              const int64_t q_stride[3], int n, int heads, const spec_cache_form *form,

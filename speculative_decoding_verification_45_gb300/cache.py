@@ -254,10 +254,11 @@ def cache_attend(q, cache, block_table, lengths, num_new=None, scale=None, softc
 
     Rows that see nothing, and rows i >= num_new[b], are zeros with lse -inf.
 
-    Precision: scores, sums and lse in 32 bits; softmax weights to 2^-8 of
-    themselves, as in bf16, but no finer than 2^-17 of the largest weight (times
-    value scale) among their 128 tokens; query elements to 2^-17 of the largest
-    of their row or better.  spec_verify.h has it in full.
+    Precision: scores, sums and lse in 32 bits; query elements to 2^-21 of the
+    largest of their row or better; softmax weights to 2^-10 of themselves, but
+    no finer than 2^-21 of the largest weight (times value scale) among their 128
+    tokens.  With n * heads / kv_heads above 32, weights to 2^-8 of themselves, as
+    in bf16, and no finer than 2^-17 of that.  spec_verify.h has it in full.
     """
     c, dev, len_ptr = _describe(cache, block_table, lengths)
     f, n, heads, stride = _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent)

@@ -5,14 +5,22 @@
 // The matrix products take the codes as they lie in memory: kind::f8f6f4
 // multiplies 8-bit floats, so keys and values go from HBM through TMA into
 // shared memory and from there into tcgen05.mma, with no conversion between.
-// What multiplies them is split so that 8 bits lose nothing:
-//   q    a bf16 value (8-bit significand), scaled by a power of two per row, is
-//        exactly the sum of two e4m3 values (4 bits each; the remainder after
-//        rounding to 4 bits needs no more than 4), down to 2^-10 of the row's
-//        largest element;
+// What multiplies them is split so that 8 bits lose next to nothing (products of
+// e4m3 and e5m2 values may be mixed):
+//   q    a bf16 value (8-bit significand), scaled by a power of two per row so
+//        that the row's largest lies in [128, 256), as an e4m3 value and, of what
+//        its 4 bits leave (8 units of the last bit at most, either sign: 3 bits),
+//        an e5m2 value: exact down to 2^-14 of the row's largest element, off by
+//        2^-21 of it at most below;
 //   p    exp(x - ..) scaled per tile and row so that the largest lies in
-//        [224, 448], as the sum of two e4m3 values: 2^-8 relative, the rounding
-//        of a bf16 weight, on a grid of 2^-17 of the largest.
+//        [224, 448], rounded to 16 bits (2^-11), as two e4m3 values (2^-9 more, on
+//        a grid of 2^-17 of the largest) and, with up to 32 rows a key head, an
+//        e5m2 value of what they leave (2^-12 and 2^-21 in their place).  The
+//        third term costs nothing at 16 columns (81 us for 64 sequences and a
+//        window of 1,024) and 3% at 32 (195 us against 190 for 256 sequences of
+//        1,000 to 2,000 tokens); at 48, where the softmax's instructions are the
+//        time, it would cost 7% (209 against 195 us for four sequences of up to
+//        100,001 tokens, 345 against 332 for 1,000 queries).
 // Each product is issued once per term into the same accumulator.
 //
 // Tokens are the M side (128 per tile), query rows the N side: a decode step
@@ -281,7 +289,8 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
     return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)((lbo >> 4) & 0x3fff) << 16 | (uint64_t)((sbo >> 4) & 0x3fff) << 32 |
            1ull << 46 | swizzle << 61;
 }
-// Instruction descriptor: float accumulator, M = 128; a_code 0 e4m3, 1 e5m2; B is e4m3.
+// Instruction descriptor: float accumulator, M = 128; a_code 0 e4m3, 1 e5m2; B is e4m3, or e5m2 with kWideB.
+constexpr uint32_t kWideB = 1u << 10;
 __device__ __forceinline__ uint32_t instr_desc(int nt, int a_code, bool a_mn, bool b_mn)
 {
     return 1u << 4 | (uint32_t)a_code << 7 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 | (uint32_t)(nt >> 3) << 17 |
@@ -421,21 +430,30 @@ template <int NT> struct Columns {
 };
 static_assert(sizeof(Columns<16>) % 16 == 0 && sizeof(Columns<48>) % 16 == 0, "copies arrive at 16 bytes");
 
-// Two values as pairs of e4m3: what 4 bits hold of them, and of the rest.
-__device__ __forceinline__ void split8(float x0, float x1, uint32_t &first, uint32_t &rest)
+// Pairs of 16-bit floats to 8 bits: what 4 bits hold of them, which is taken off; what 3 bits hold of the rest.
+__device__ __forceinline__ uint32_t take4(uint32_t &h)
 {
-    uint32_t h, back;
-    uint16_t b1, b2;
+    uint16_t b;
+    uint32_t back;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b) : "r"(h));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(b));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(h) : "r"(h), "r"(back));
+    return b;
+}
+__device__ __forceinline__ uint32_t take3(uint32_t h)
+{
+    uint16_t b;
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(b) : "r"(h));
+    return b;
+}
+__device__ __forceinline__ uint32_t to_halves(float x0, float x1)
+{
+    uint32_t h;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(x1), "f"(x0));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b1) : "r"(h));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(b1));
-    asm("sub.f16x2 %0, %1, %2;" : "=r"(back) : "r"(h), "r"(back));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(b2) : "r"(back));
-    first = b1;
-    rest = b2;
+    return h;
 }
 
-// Queries as two e4m3 terms, row tile by row tile, laid out as the products read
+// Queries as an e4m3 and an e5m2 term (for the weights two e4m3 terms), row tile by row tile, laid out as the products read
 // them from shared memory (128- or 64-byte swizzled), and the factor of each
 // row's accumulators; rows of `out` without a query are written here too.  A kernel of its own, D / 8 lanes a row: one warp of the
 // attention kernel took 18,000 cycles for the 32 rows of a segment, as long as
@@ -501,7 +519,11 @@ template <int D> __global__ void __launch_bounds__(256) split_kernel(const __gri
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            split8(__uint_as_float(x[e] << 16) * inv, __uint_as_float(x[e] & 0xffff0000u) * inv, hi[e], lo[e]);
+        {
+            uint32_t h = to_halves(__uint_as_float(x[e] << 16) * inv, __uint_as_float(x[e] & 0xffff0000u) * inv);
+            hi[e] = take4(h);
+            lo[e] = a.out ? take3(h) : take4(h);
+        }
         if (m[k] < 0)
             continue;
         uint8_t *to = a.split + (size_t)tile[k] * (2 * nt * D) + c[k] * D +
@@ -769,7 +791,7 @@ template <int NT> struct Walk {
 // sequences of 4,000 to 8,000 tokens, 20 rows: 155 us, 5.3 TB/s; one token per
 // sequence, 4 rows: 144 us, 5.7 TB/s, of 6.7 that a copy reaches), and between
 // units the filling and draining of this chain, about 5,000 cycles each (256
-// sequences of 1,000 to 2,000 tokens: 190 us for 828 MB).  With a cap or a bias,
+// sequences of 1,000 to 2,000 tokens: 195 us for 828 MB).  With a cap or a bias,
 // or more rows, the softmax's instructions: about 900 issue slots of an SM
 // quarter for a tile of 32 columns, issued at 0.5 to 0.6 a cycle.  The program
 // has to stay short: columns are taken 16 at a time by the same instructions
@@ -782,6 +804,7 @@ template <int D, int NT> struct AttendShape {
     static constexpr int NO = NT == 48 ? 1 : 2;                 // O^T at a time (one: room to keep the exponentials)
     static constexpr int kBytes = kTile * D;                    // one side of a tile
     static constexpr int KS = 3, VS = D == 64 || NT == 16 ? 8 : NT >= 48 ? 5 : 6;  // tiles of keys and values in shared memory
+    static constexpr int kTerms = NT <= 32 ? 3 : 2;             // of a weight (see the top)
     static constexpr int kColumns = (3 * NW + NO) * NT;         // S^T, totals and exponentials of each warpgroup, O^T
     static constexpr int kAlloc = kColumns <= 256 ? 256 : 512;
     static_assert(kColumns <= 512, "tensor memory");
@@ -811,7 +834,7 @@ template <int D, int NT> struct AttendShared {
     alignas(1024) uint8_t k[S::KS][S::kBytes];
     alignas(1024) uint8_t v[S::VS][S::kBytes];
     alignas(1024) uint8_t q[2][2][NT * D];
-    alignas(1024) uint8_t p[S::NW][2][kTile * NT];
+    alignas(1024) uint8_t p[S::NW][S::kTerms][kTile * NT];
     alignas(16) Columns<NT> col[2];
     Segment seg[4];
     alignas(16) StageInfo info[S::VS];
@@ -1192,7 +1215,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 #pragma unroll
                     for (int d = 0; d < D / 32; ++d) {
                         tc_mma(tmem + w * NT, kd + (d * 32 >> 4), qd + (d * 32 >> 4), desc, d > 0);
-                        tc_mma(tmem + w * NT, kd + (d * 32 >> 4), qd + ((NT * D + d * 32) >> 4), desc, true);
+                        tc_mma(tmem + w * NT, kd + (d * 32 >> 4), qd + ((NT * D + d * 32) >> 4), desc | kWideB, true);
                     }
                     tc_commit(&sh.s_full[w]);
                     tc_commit(&sh.k_empty[ks]);
@@ -1230,12 +1253,14 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 tc_after();
                 if (elected()) {
                     const uint64_t vd = v_desc + (uint32_t)vs * (S::kBytes >> 4),
-                                   pd = p_desc + (uint32_t)w * (2 * kTile * NT >> 4);
+                                   pd = p_desc + (uint32_t)w * (S::kTerms * kTile * NT >> 4);
                     const uint32_t d = tmem + kO + i * NT;
 #pragma unroll
                     for (int k = 0; k < kTile / 32; ++k) {
                         tc_mma(d, vd + (k * 32 * D >> 4), pd + (k * 512 >> 4), desc, k > 0);
                         tc_mma(d, vd + (k * 32 * D >> 4), pd + ((kTile * NT + k * 512) >> 4), desc, true);
+                        if (S::kTerms == 3)
+                            tc_mma(d, vd + (k * 32 * D >> 4), pd + ((2 * kTile * NT + k * 512) >> 4), desc | kWideB, true);
                     }
                     tc_commit(&sh.o_full[i]);
                     tc_commit(&sh.p_free[w]);
@@ -1476,23 +1501,23 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                         for (int c = 0; c < 8; ++c)
                             ((float2 *)l)[c] = add2(((float2 *)l)[c], ((float2 *)e)[c]);
                         tmem_store16(l_at + c0, l);
-                        uint32_t hi[4], lo[4];
+                        uint32_t hi[4], lo[4], rest[4];
 #pragma unroll
                         for (int c4 = 0; c4 < 4; ++c4) {
                             const float4 y = *(const float4 *)(scales + c0 + c4 * 4);
                             // e * v first: y * v may pass the floats where e is 0
                             const float2 p0 = mul2(mul2(((float2 *)e)[2 * c4], v2), make_float2(y.x, y.y)),
                                          p1 = mul2(mul2(((float2 *)e)[2 * c4 + 1], v2), make_float2(y.z, y.w));
-                            float p[4] = {p0.x, p0.y, p1.x, p1.y};
-                            uint32_t first[2], rest[2];
-                            split8(p[0], p[1], first[0], rest[0]);
-                            split8(p[2], p[3], first[1], rest[1]);
-                            hi[c4] = first[0] | first[1] << 16;
-                            lo[c4] = rest[0] | rest[1] << 16;
+                            uint32_t h0 = to_halves(p0.x, p0.y), h1 = to_halves(p1.x, p1.y);
+                            hi[c4] = take4(h0) | take4(h1) << 16;
+                            lo[c4] = take4(h0) | take4(h1) << 16;
+                            rest[c4] = take3(h0) | take3(h1) << 16;
                         }
                         uint8_t *dst = sh.p[w][0] + (c0 >> 4) * (kTile * 16) + t * 16;
                         *(uint4 *)dst = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *(uint4 *)(dst + kTile * NT) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        if (S::kTerms == 3)
+                            *(uint4 *)(dst + 2 * kTile * NT) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
                     }
                     tmem_store_wait();
                     proxy_fence();
@@ -1704,7 +1729,11 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
 // ===========================================================================
 // The same S^T tiles, read once more against the known lse: weight of a token
 // += sum over the rows of exp2(x - lse).  A thread owns a token of its tile and
-// adds its columns up, so a sum needs no other thread and no atomic.  Three
+// adds its columns up, so a sum needs no other thread and no atomic.  One product
+// makes both terms of the queries, side by side; so both are e4m3 values, exact
+// down to 2^-10 of the row's largest element and off by 2^-17 of it at most below
+// (an e5m2 term needs a product of its own: 54 us against 52 for 32 sequences of
+// 8192 tokens).  Three
 // warpgroups take tiles in turn.  Keys only: half of what attention reads.
 constexpr int kWeighGroups = 3;  // 32 sequences of 8192 tokens took 55 us when it was chosen (51 now); two 60, four 56
 constexpr int kWeighThreads = 128 * kWeighGroups + 96;

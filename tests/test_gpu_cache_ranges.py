@@ -199,3 +199,53 @@ def test_a_nan_value_reaches_the_rows_that_see_it_even_without_weight(sv):  # no
     assert ((lse.cpu() - ref["lse"]).abs() <= ref["dx"]).all()
     _, _, (want, _) = clean.run(sv)
     assert torch.equal(out[0, 2:], want[0, 2:])
+
+
+@pytest.mark.parametrize("columns,r,s", [(COLUMNS[0], 2.0 ** -10, 2.0 ** -21), (COLUMNS[1], 2.0 ** -10, 2.0 ** -21),
+                                         (COLUMNS[2], 2.0 ** -8, 2.0 ** -17)], ids=[16, 32, 48])
+@pytest.mark.parametrize("apart", [6, 14, 18, 20])
+def test_weights_to_the_stated_precision(sv, columns, r, s, apart):  # noqa: F811
+    """Of a weight r, or s of the largest weight times scale of its 128 tokens; a dimension that the heavy blocks
+    leave at 0 shows the second part."""
+    case = Case([500], dim=64, block=32, seed=62, **columns)
+    case.pool.scale[1] = 1.0
+    large = case.table[0, :: 2].long()
+    case.pool.scale[1, large] = 2.0 ** apart
+    case.pool.codes[1, large, :, :, :32] = 0
+    case.pool.codes[0] = 0  # equal scores and values of one sign: the weights' errors add up
+    case.pool.codes[1] = case.pool.codes[1].abs()
+    ref = case.reference()
+    _, _, (out, _) = case.run(sv)
+    step, group = torch.zeros_like(ref["out"]), columns["heads"] // columns["kv_heads"]
+    for (b, i, h), (see, x, _) in ref["xs"].items():
+        j = see.nonzero()[:, 0]
+        page, row, tile = case.table[b][j // 32].long(), j % 32, j // 128
+        p, scale = torch.exp(x - ref["lse"][b, i, h]), case.pool.scale[1, page, h // group]
+        most = torch.zeros(2, 4, dtype=torch.float64).scatter_reduce(1, tile.expand(2, -1), torch.stack([p, scale]), "amax")
+        step[b, i, h] = s * most.prod(0)[tile] @ case.pool.codes[1, page, h // group, row].abs()
+    bound = 2.0 ** -8 * ref["out"].abs() + (r + 2 * ref["dx"][..., None]) * ref["mean"] + step + 2.0 ** -30
+    far = ((out.cpu().double() - ref["out"]).abs() - bound)[..., :32]
+    assert (far <= 0).all(), float(far.max())
+
+
+@pytest.mark.parametrize("small", [0, 4, 6, 9, 12])
+@pytest.mark.parametrize("columns", COLUMNS, ids=[16, 32, 48])
+def test_queries_to_the_stated_precision(sv, columns, small):  # noqa: F811
+    """Exact down to 2^-14 of the row's largest element, 2^-21 of it below: that one meets keys of 0 here.  Beside it
+    32-bit sums of 64 products."""
+    case = Case([300], dim=64, block=16, seed=63, **columns)
+    case.q = (case.q.float() * 2.0 ** -small).to(torch.bfloat16)
+    case.q[..., 5] = 200.0
+    case.pool.codes[0, ..., 5] = 0
+    case.form["scale"] = 2.0 ** small / 8
+    ref = case.reference()
+    _, _, (_, lse) = case.run(sv)
+    group = columns["heads"] // columns["kv_heads"]
+    for (b, i, h), (see, x, _) in ref["xs"].items():
+        k, _ = case.pool.tokens(0, case.table[b], h // group, 300)
+        q, k = case.q[b, i, h].double(), k[see].abs()
+        below = (q.abs() < 2.0 ** -14 * 200).double() * 2.0 ** -21 * 200
+        err = case.form["scale"] * (k @ below + 2.0 ** -18 * k @ q.abs()) + 2.0 ** -22 * x.abs()
+        p = torch.exp(x - ref["lse"][b, i, h])
+        off = float((p * err).sum()) + 2.0 ** -20 * (1 + abs(float(ref["lse"][b, i, h])))
+        assert abs(float(lse[b, i, h]) - float(ref["lse"][b, i, h])) <= off
