@@ -17,10 +17,10 @@
 //        a grid of 2^-17 of the largest) and, with up to 32 rows a key head, an
 //        e5m2 value of what they leave (2^-12 and 2^-21 in their place).  The
 //        third term costs nothing at 16 columns (81 us for 64 sequences and a
-//        window of 1,024) and 3% at 32 (195 us against 190 for 256 sequences of
+//        window of 1,024) and 3% at 32 (196 us against 190 for 256 sequences of
 //        1,000 to 2,000 tokens); at 48, where the softmax's instructions are the
-//        time, it would cost 7% (209 against 195 us for four sequences of up to
-//        100,001 tokens, 345 against 332 for 1,000 queries).
+//        time, it would cost 4 to 8% (209 against 192 us for four sequences of up
+//        to 100,001 tokens, 345 against 334 for 1,000 queries).
 // Each product is issued once per term into the same accumulator.
 //
 // Tokens are the M side (128 per tile), query rows the N side: a decode step
@@ -788,10 +788,10 @@ template <int NT> struct Walk {
 // for 16 columns) and the four warps meet in shared memory.
 //
 // What bounds it: up to 48 rows a key head, memory (2 D bytes a token; 64
-// sequences of 4,000 to 8,000 tokens, 20 rows: 155 us, 5.3 TB/s; one token per
-// sequence, 4 rows: 144 us, 5.7 TB/s, of 6.7 that a copy reaches), and between
+// sequences of 4,000 to 8,000 tokens, 20 rows: 158 us, 5.2 TB/s; one token per
+// sequence, 4 rows: 146 us, 5.6 TB/s, of 6.7 that a copy reaches), and between
 // units the filling and draining of this chain, about 5,000 cycles each (256
-// sequences of 1,000 to 2,000 tokens: 195 us for 828 MB).  With a cap or a bias,
+// sequences of 1,000 to 2,000 tokens: 196 us for 828 MB).  With a cap or a bias,
 // or more rows, the softmax's instructions: about 900 issue slots of an SM
 // quarter for a tile of 32 columns, issued at 0.5 to 0.6 a cycle.  The program
 // has to stay short: columns are taken 16 at a time by the same instructions
