@@ -371,7 +371,9 @@ spec_status spec_cache_append(const spec_cache *cache, const int32_t *lengths, c
  *   or j < prefix[b] (a prefix that every query sees, also outside the window).
  * Its score is x = scale * q.k, then softcap * tanh(x / softcap) where softcap
  * > 0, then - slopes[head] * |position(a_i) - position(j)| where slopes is given.
- * A row that sees nothing gets zeros and lse = -inf.  A parent outside [0, k)
+ * A row that sees nothing gets zeros and lse = -inf.  Scores past 2^29 in magnitude
+ * count as infinite: a row that sees a positive one becomes NaN, one that sees none
+ * but negative ones is as if it saw nothing.  A parent outside [0, k)
  * counts as no parent and sets SPEC_STATUS_BAD_TREE.  What a query does not see
  * changes nothing in its row, NaN included; a NaN key that it sees makes its row
  * NaN, a NaN value that dimension of its row or all of it. */

@@ -1652,7 +1652,7 @@ __global__ void __launch_bounds__((AttendShape<D, NT>::kThreads), 1)
                 sh.out_row[tid] = row;
                 // sums count 2^ref, totals 2^base
                 int up = 0;
-                const float significand = isfinite(total) ? frexpf(total, &up) : total;
+                const float significand = isfinite(total) ? frexpf(total, &up) : __int_as_float(0x7fffffff);
                 const int level = (int)max(min((long long)ref - (long long)base - up, 250ll), -250ll);
                 far = live && abs(level) > 100;  // a power that no float may hold goes in two
                 const int first = far ? level / 2 : 0;

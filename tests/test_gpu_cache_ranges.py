@@ -249,3 +249,18 @@ def test_queries_to_the_stated_precision(sv, columns, small):  # noqa: F811
         p = torch.exp(x - ref["lse"][b, i, h])
         off = float((p * err).sum()) + 2.0 ** -20 * (1 + abs(float(ref["lse"][b, i, h])))
         assert abs(float(lse[b, i, h]) - float(ref["lse"][b, i, h])) <= off
+
+
+@pytest.mark.parametrize("length", [90, 3000])
+def test_scores_without_bounds_are_not_silent(sv, length):  # noqa: F811
+    """Scores of 10^12: NaN where one is positive, as if nothing were seen where all are negative, never zeros with a
+    finite lse."""
+    case = Case([length], 3, heads=8, kv_heads=2, seed=64)
+    case.form["scale"] = 1e12
+    _, _, (out, lse) = case.run(sv)
+    assert torch.isnan(out).all() and torch.isposinf(lse).all()
+    case.form["scale"] = 0.125
+    opposed(case, 33.0)
+    case.form["scale"] = 1e12
+    _, _, (out, lse) = case.run(sv)
+    assert (out == 0).all() and torch.isneginf(lse).all()
