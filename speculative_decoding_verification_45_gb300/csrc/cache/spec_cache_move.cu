@@ -244,6 +244,12 @@ __device__ __forceinline__ void load_keys(const EvictArgs &a, int b, int h, int 
     for (int i = 0; i < kAhead; ++i)
         page[i] = j + i * step < end ? page_of(a.c, b, (j + i * step) >> log_p) : -1;
     float w[kAhead];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        bad = bad || (page[i] < 0 && j + i * step < end);
+    if (bad)
+        report(a.status, SPEC_STATUS_BAD_PAGE);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
         w[i] = page[i] < 0 ? __int_as_float(0x7fffffff)

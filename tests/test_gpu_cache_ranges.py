@@ -10,7 +10,7 @@ import pytest
 import torch
 
 from tests import cache_reference as cr
-from tests.test_gpu_cache import Case, sv  # noqa: F401
+from tests.test_gpu_cache import Case, sv, table_for  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -264,3 +264,22 @@ def test_scores_without_bounds_are_not_silent(sv, length):  # noqa: F811
     case.form["scale"] = 1e12
     _, _, (out, lse) = case.run(sv)
     assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("lengths,blocks,block", [([60, 40], 4, 16), ([40000], 625, 64), ([70000], 1100, 64)])
+def test_evict_reports_a_bad_page_whose_tokens_it_drops(sv, lengths, blocks, block):  # noqa: F811
+    pages, B = len(lengths) * (blocks + 2), len(lengths)
+    x = torch.zeros(pages, 1, block, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    cache = sv.KVCache(x, x.clone(), torch.ones(pages, 1, device="cuda"), torch.ones(pages, 1, device="cuda"))
+    table = table_for(B, blocks + 2, pages, 65)
+    w = torch.rand(pages, 1, block, generator=torch.Generator().manual_seed(65)).cuda() + 1
+    for bad, want in ((None, 0), (-5, sv.STATUS_BAD_PAGE), (pages, sv.STATUS_BAD_PAGE)):
+        t = table.clone()
+        if bad is not None:
+            t[0, 1] = bad
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        kept, index = sv.cache_evict(cache, t[:, :blocks].cuda(), torch.tensor(lengths).int().cuda(), w.clone(), 20, 4,
+                                     t[:, blocks:].cuda(), status=status)
+        assert status.item() == want and kept.tolist() == [20] * B
+        if bad is not None:  # its tokens weigh less than any number
+            assert not ((index[0, 0] >= block) & (index[0, 0] < 2 * block)).any()
