@@ -353,7 +353,8 @@ typedef struct spec_cache {
  * A power of two costs a floating-point code no precision, and moving a code to
  * a larger power of two is exact down to the subnormal codes.  Infinities and
  * NaN are stored as NaN and do not enter s.  lengths is not changed (the caller
- * adds num_new, or, after a verification round, the accepted part of it).
+ * adds num_new, or, after a verification round, the accepted part of it).  A
+ * block that a call writes belongs to one sequence; full blocks may be shared.
  *   num_new    [batch] int32 in [0, n], or NULL: n for every sequence
  *   positions  [batch, n] int32 or NULL (lengths[b] + i), written to
  *              cache.positions where that is present */
