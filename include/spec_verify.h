@@ -128,7 +128,7 @@ typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 /* spec_cache_*: a length or a number of new tokens out of range; a page id out of range. */
 #define SPEC_STATUS_BAD_LENGTH 64u
 #define SPEC_STATUS_BAD_PAGE 128u
-/* spec_cache_*: a bounded wait inside a kernel ran out; the call's outputs are not valid. */
+/* spec_cache_*, spec_rows_product: a bounded wait inside a kernel ran out; the call's outputs are not valid. */
 #define SPEC_STATUS_INTERNAL 256u
 
 /* One verification round for B independent sequences (see the top of this
@@ -413,8 +413,8 @@ spec_status spec_cache_attend(const spec_cache *cache, const int32_t *lengths, c
                               float *lse, void *workspace, int64_t workspace_bytes, uint32_t *status, void *stream);
 spec_status spec_cache_attend_workspace(const spec_cache *cache, int n, int heads, int64_t *bytes);
 
-/* How many clocks of an SM a wait inside spec_cache_attend's and spec_cache_weigh's
- * kernels may take (2^31 - 1, about a second, if this is never called).  A kernel
+/* How many clocks of an SM a wait inside spec_cache_attend's, spec_cache_weigh's and
+ * spec_rows_product's kernels may take (2^31 - 1, about a second, if this is never called).  A kernel
  * whose wait ran out ends all the same and sets SPEC_STATUS_INTERNAL: give those
  * calls a status to learn of it.  The limit holds for the calls that this process
  * makes from now on; a captured call keeps the one it was captured with. */
@@ -452,6 +452,77 @@ spec_status spec_cache_weigh(const spec_cache *cache, const int32_t *lengths, co
 spec_status spec_cache_evict(const spec_cache *cache, const int32_t *lengths, float *weights, int keep, int recent,
                              const int32_t *out_table, int64_t out_stride, int32_t *out_lengths, int32_t *out_index,
                              uint32_t *status, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit rows: what a target's projections read, and their product.
+ *
+ * A matrix of `rows` x `dim` in 8 bits: codes (e4m3 or e5m2), and for every 128
+ * neighbouring elements of a row (the last block of a row may be shorter) one
+ * scale that is a power of two, held as its biased exponent: value = code *
+ * 2^(byte - 127), a byte of 255 standing for NaN (the e8m0 form).  Activations have
+ * a scale for each row, scale [rows, ceil(dim / 128)]; weights one for each 128
+ * rows, scale [ceil(rows / 128), ceil(dim / 128)].  A power of two costs a
+ * floating-point code no precision but at the smallest codes, and is what the tensor
+ * cores apply by themselves.
+ *   codes   element (r, d) at r * stride + d; 16-byte aligned, stride a multiple of 16
+ *   scale   byte (r, b) at r * scale_stride + b
+ *   dim     a multiple of 16 in [16, SPEC_MAX_ROW]
+ * Scales are chosen as for the cache: 2^e the smallest power of two with |x| <= 2^e
+ * * (448 or 57344) for every finite x of the block, e = -100 at least.  Infinities
+ * and NaN become the code NaN and do not enter the scale.  Rows behind `rows` are not
+ * touched.  Ownership, stream and error rules as for spec_verify; each call enqueues
+ * one kernel, every array is device memory, nothing is allocated, and no result
+ * depends on the order of threads. */
+#define SPEC_MAX_ROW 131072
+#define SPEC_MAX_NORM_ROW 32768
+#define SPEC_MAX_CODED_ROWS (1 << 30)
+
+typedef struct spec_coded {
+    void *codes;
+    uint8_t *scale;
+    int64_t stride, scale_stride;
+    int32_t rows, dim;
+    int32_t code; /* spec_code */
+} spec_coded;
+
+typedef enum { SPEC_SILU = 0, SPEC_GELU_TANH = 1 } spec_act;
+
+/* Rows as they are: x [rows, dim] float32 or bf16, row r at r * x_stride elements
+ * (16-byte aligned, strides multiples of 16 bytes, here and below).
+ * block_rows: 1 (activations) or 128 (a weight; at most 2^23 - 128 rows). */
+spec_status spec_rows_quantise(const void *x, int64_t x_stride, spec_dtype dtype, const spec_coded *out, int block_rows,
+                               void *stream);
+
+/* h = x + residual; sum = h rounded to the residual's type; the coded rows are
+ * y = h / sqrt(mean over the row of h^2 + eps) * weight, of the 32-bit h.
+ *   residual, sum  [rows, dim] of residual_dtype, or both NULL (h = x); sum may be
+ *                  residual itself, or x where types and strides are the same
+ *   weight         [dim] of weight_dtype, 16-byte aligned, or NULL (1)
+ *   eps            positive (2^-126 at least) and finite
+ * Squares are added in 32 bits: a row with elements past 2^63 may become zeros, one
+ * with an infinity or a NaN becomes zeros and NaN.  dim is at most SPEC_MAX_NORM_ROW. */
+spec_status spec_rows_norm(const void *x, int64_t x_stride, spec_dtype dtype, const void *residual,
+                           int64_t residual_stride, spec_dtype residual_dtype, const void *weight,
+                           spec_dtype weight_dtype, float eps, void *sum, int64_t sum_stride, const spec_coded *out,
+                           void *stream);
+
+/* The coded rows are act(gate) * up, act(g) = g / (1 + exp(-g)) or, for
+ * SPEC_GELU_TANH, g / 2 * (1 + tanh(sqrt(2 / pi) * (g + 0.044715 g^3))); gate and
+ * up [rows, dim] of one type, each with its stride (halves of one product's output
+ * need no copy). */
+spec_status spec_rows_gate(const void *gate, int64_t gate_stride, const void *up, int64_t up_stride, spec_dtype dtype,
+                           spec_act act, const spec_coded *out, void *stream);
+
+/* out[t, n] = sum over d of rows[t, d] * weight[n, d]: a projection, or the logits
+ * that spec_verify reads.  rows has scales for each row, weight for each 128; codes
+ * of either form may meet.  Products and sums are 32-bit, out (float32 or bf16, row t
+ * at t * out_stride elements, aligned to its element) is rounded once.  The sums' order
+ * follows from the sizes alone: the same bits every time.  A NaN (code or scale)
+ * makes NaN the outputs that it enters.
+ * Waits in the kernel are bounded (spec_cache_set_wait_limit): if one runs out,
+ * SPEC_STATUS_INTERNAL is OR-ed into *status (may be NULL). */
+spec_status spec_rows_product(const spec_coded *rows, const spec_coded *weight, void *out, int64_t out_stride,
+                              spec_dtype dtype, uint32_t *status, void *stream);
 
 /* Static description of a status code. */
 const char *spec_status_string(spec_status s);

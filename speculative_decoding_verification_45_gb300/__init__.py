@@ -38,7 +38,7 @@ STATUS_BAD_LOGITS = 8
 STATUS_BAD_TREE = 32
 STATUS_BAD_LENGTH = 64  # cache_*: a length or a number of new tokens out of range
 STATUS_BAD_PAGE = 128   # cache_*: a page id out of range
-STATUS_INTERNAL = 256   # cache_*: a bounded wait inside a kernel ran out; the outputs are not valid
+STATUS_INTERNAL = 256   # cache_*, rows_product: a bounded wait inside a kernel ran out; the outputs are not valid
 
 MAX_GAMMA = 16
 MAX_TREE_NODES = 256
@@ -430,16 +430,19 @@ def to_device(batch, device="cuda"):
     )
 
 
-# The cache's operators need torch; the rest of this module imports it inside its
-# calls, so that the host-only parts load without it.
+# The operators of the cache and of 8-bit rows need torch; the rest of this module imports
+# it inside its calls, so that the host-only parts load without it.
 _CACHE_NAMES = ("KVCache", "cache_append", "cache_attend", "cache_weigh", "cache_evict")
+_ROWS_NAMES = ("Coded", "rows_quantise", "weight_quantise", "rows_norm", "rows_gate", "rows_product")
 
 
 def __getattr__(name):
-    if name in _CACHE_NAMES:
-        from . import cache
+    for module, names in (("cache", _CACHE_NAMES), ("rows", _ROWS_NAMES)):
+        if name in names:
+            import importlib
 
-        for n in _CACHE_NAMES:
-            globals()[n] = getattr(cache, n)
-        return globals()[name]
+            m = importlib.import_module(f"{__name__}.{module}")
+            for n in names:
+                globals()[n] = getattr(m, n)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

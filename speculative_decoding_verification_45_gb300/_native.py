@@ -13,13 +13,16 @@ ROOT = os.path.dirname(PKG)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 CACHE = os.path.join(CSRC, "cache")
-# The host unit, one unit per (dtype, proposal form) of kernels, and the cache's four: compiled in parallel.
+ROWS = os.path.join(CSRC, "rows")
+# The host unit, one unit per (dtype, proposal form) of kernels, the cache's four and the rows' two: compiled in parallel.
 SOURCES = ([os.path.join(CSRC, f) for f in ("spec_verify.cu", "kernels_bf16.cu", "kernels_bf16_point.cu",
                                              "kernels_f32.cu", "kernels_f32_point.cu")]
            + [os.path.join(CACHE, f) for f in ("spec_cache_move.cu", "spec_cache_attend.cu",
-                                               "spec_cache_attend_d64.cu", "spec_cache_attend_d128.cu")])
+                                               "spec_cache_attend_d64.cu", "spec_cache_attend_d128.cu")]
+           + [os.path.join(ROWS, f) for f in ("spec_rows_code.cu", "spec_rows_product.cu")])
 HEADERS = [os.path.join(INCLUDE, "spec_verify.h"), os.path.join(CSRC, "spec_verify_kernels.cuh"),
-           os.path.join(CACHE, "spec_cache.cuh"), os.path.join(CACHE, "spec_cache_attend.cuh")]
+           os.path.join(CSRC, "spec_ptx.cuh"), os.path.join(CACHE, "spec_cache.cuh"),
+           os.path.join(CACHE, "spec_cache_attend.cuh"), os.path.join(ROWS, "spec_rows.cuh")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libspec_verify.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -51,6 +54,14 @@ class CacheForm(ctypes.Structure):
                 ("num_new", ctypes.c_void_p)]
 
 
+class Coded(ctypes.Structure):
+    """spec_coded of include/spec_verify.h."""
+
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("scale_stride", ctypes.c_int64), ("rows", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("code", ctypes.c_int32)]
+
+
 def nvcc_path() -> str:
     for cand in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
@@ -73,7 +84,7 @@ def _run(cmd):
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/*.cu and csrc/cache/*.cu for sm_103a (one nvcc per unit, in parallel) and link
+    """Compile the units of csrc for sm_103a (one nvcc per unit, in parallel) and link
     _build/libspec_verify.so."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     if not force and not _stale():
@@ -139,6 +150,15 @@ def load() -> ctypes.CDLL:
         lib.spec_cache_weigh.restype = i32
         lib.spec_cache_evict.argtypes = [vp, vp, vp, i32, i32, vp, ctypes.c_int64, vp, vp, vp, vp]
         lib.spec_cache_evict.restype = i32
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        lib.spec_rows_quantise.argtypes = [vp, i64, i32, vp, i32, vp]
+        lib.spec_rows_quantise.restype = i32
+        lib.spec_rows_norm.argtypes = [vp, i64, i32, vp, i64, i32, vp, i32, f32, vp, i64, vp, vp]
+        lib.spec_rows_norm.restype = i32
+        lib.spec_rows_gate.argtypes = [vp, i64, vp, i64, i32, i32, vp, vp]
+        lib.spec_rows_gate.restype = i32
+        lib.spec_rows_product.argtypes = [vp, vp, vp, i64, i32, vp, vp]
+        lib.spec_rows_product.restype = i32
         lib.spec_status_string.argtypes = [i32]
         lib.spec_status_string.restype = ctypes.c_char_p
         _lib = lib

@@ -11,6 +11,29 @@ using namespace specc;
 
 namespace {
 
+std::atomic<int> g_wait_limit{INT_MAX};  // clocks
+
+}  // namespace
+
+int specc::wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+
+EncodeTiled specc::encoder()
+{
+    static const EncodeTiled f = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return (EncodeTiled)p;
+    }();
+    return f;
+}
+
+namespace {
+
 spec_status check_call(const spec_cache *cache, const int32_t *lengths, const void *q, const int64_t q_stride[3],
                        int n, int heads, const spec_cache_form *form, const uint32_t *status)
 {
@@ -37,7 +60,6 @@ spec_status check_call(const spec_cache *cache, const int32_t *lengths, const vo
 
 constexpr int kMaxDevices = 64;
 std::atomic<int> g_sms[kMaxDevices];  // SM count, once the kernels' attributes are set
-std::atomic<int> g_wait_limit{INT_MAX};  // clocks
 
 spec_status device_sms(int *sms)
 {
@@ -68,25 +90,6 @@ spec_status device_sms(int *sms)
     }
     *sms = v;
     return SPEC_OK;
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder()
-{
-    static const EncodeTiled f = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            p = nullptr;
-        }
-        return (EncodeTiled)p;
-    }();
-    return f;
 }
 
 // [dim, token, head, page] over the codes; a box is one block of one head.  A
@@ -135,7 +138,7 @@ AttendArgs make_args(const spec_cache *cache, const int32_t *lengths, const void
     a.per_group = a.group == 1 ? 0 : (uint32_t)(((1ull << 32) + a.group - 1) / a.group);
     a.row_tiles = shape.row_tiles;
     a.status = status;
-    a.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
+    a.wait_limit = wait_limit();
     return a;
 }
 

@@ -1,0 +1,436 @@
+// spec_rows_code.cu -- rows and weights to 8 bits: as they are (spec_rows_quantise),
+// after the residual's addition and the root-mean-square norm (spec_rows_norm),
+// and as the product of an activated gate and its partner (spec_rows_gate).
+// include/spec_verify.h states the operations.
+//
+// Each is one pass over memory, which bounds it: an element is read once, kept in
+// registers while its block's (or row's) largest is found, and written as a code.
+// A thread takes eight neighbouring elements, so sixteen lanes hold a block of 128
+// and agree on its scale by four shuffles.  All arithmetic is 32-bit; the only
+// rounding to fewer bits is that to the code, and of the sum that spec_rows_norm
+// writes back (which its norm does not read again: it takes the 32-bit sum).
+
+#include "spec_rows.cuh"
+
+using namespace specc;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kLanes = kScaleBlock / 8;  // of a block
+
+struct Eight {
+    float v[8];
+};
+
+__device__ __forceinline__ void unpack(uint32_t two, float &a, float &b)
+{
+    a = __uint_as_float(two << 16);
+    b = __uint_as_float(two & 0xffff0000u);
+}
+
+template <typename T> struct Raw;  // eight elements as they lie in memory
+template <> struct Raw<__nv_bfloat16> {
+    uint4 q;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { q = *(const uint4 *)p; }
+    __device__ __forceinline__ void clear() { q = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ Eight values() const
+    {
+        Eight e;
+        unpack(q.x, e.v[0], e.v[1]);
+        unpack(q.y, e.v[2], e.v[3]);
+        unpack(q.z, e.v[4], e.v[5]);
+        unpack(q.w, e.v[6], e.v[7]);
+        return e;
+    }
+};
+template <> struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = *(const float4 *)p;
+        b = *(const float4 *)(p + 4);
+    }
+    __device__ __forceinline__ void clear() { a = b = make_float4(0, 0, 0, 0); }
+    __device__ __forceinline__ Eight values() const { return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}; }
+};
+
+__device__ __forceinline__ uint32_t pack(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *(const uint32_t *)&h;
+}
+__device__ __forceinline__ void store(__nv_bfloat16 *p, const Eight &e)
+{
+    *(uint4 *)p = make_uint4(pack(e.v[0], e.v[1]), pack(e.v[2], e.v[3]), pack(e.v[4], e.v[5]), pack(e.v[6], e.v[7]));
+}
+__device__ __forceinline__ void store(float *p, const Eight &e)
+{
+    *(float4 *)p = make_float4(e.v[0], e.v[1], e.v[2], e.v[3]);
+    *(float4 *)(p + 4) = make_float4(e.v[4], e.v[5], e.v[6], e.v[7]);
+}
+
+// The largest finite magnitude.  Magnitudes as integers are in the same order, and
+// those that are not finite are the ones from 0x7f800000 up.
+__device__ __forceinline__ uint32_t largest(const Eight &e)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t u = __float_as_uint(e.v[i]) & 0x7fffffffu;
+        m = max(m, u < 0x7f800000u ? u : 0u);
+    }
+    return m;
+}
+// Over the sixteen lanes of a block.
+__device__ __forceinline__ uint32_t of_block(uint32_t m)
+{
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1)
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+// The scale's exponent byte, from the largest magnitude's bits.
+__device__ __forceinline__ uint32_t exponent_byte(uint32_t most, int code)
+{
+    return __float_as_uint(scale_for(__uint_as_float(most), code)) >> 23;
+}
+
+// Codes of eight elements; the byte is in [27, 247], so the reciprocal is a normal power of two.
+__device__ __forceinline__ uint2 encode(const Eight &e, uint32_t byte, int code)
+{
+    const float inv = __uint_as_float((254u - byte) << 23);
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[i] = encode2(e.v[2 * i] * inv, e.v[2 * i + 1] * inv, code);
+    return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
+
+struct Out {
+    uint8_t *codes, *scale;
+    int64_t stride, scale_stride;
+    int rows, dim, code;
+};
+
+// ---------------------------------------------------------------------------
+// One scale for each row and 128 elements
+// ---------------------------------------------------------------------------
+struct Plain {
+    static constexpr int kInputs = 1;
+    static __device__ __forceinline__ Eight of(const Eight &a, const Eight &) { return a; }
+};
+// a / (1 + exp(-z)) * b.  exp by the fast base-2 form: off by 2^-22 and |z| * 2^-24, with no effect where z is large
+// (positive: the sum is 1; negative: the result is next to 0 beside its block).
+template <bool GELU> struct Gated {
+    static constexpr int kInputs = 2;
+    static __device__ __forceinline__ Eight of(const Eight &a, const Eight &b)
+    {
+        Eight r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float g = a.v[i];
+            // 0.5 (1 + tanh(y)) = 1 / (1 + exp(-2 y)), y = sqrt(2 / pi) (g + 0.044715 g^3)
+            const float z = GELU ? g * fmaf(0.0713548162726f * g, g, 1.59576912161f) : g;
+            r.v[i] = __fdividef(g, 1.0f + __expf(-z)) * b.v[i];
+        }
+        return r;
+    }
+};
+
+struct Inputs {
+    const void *a, *b;
+    int64_t a_stride, b_stride;
+};
+
+// Chunks of eight in order, kUnroll a thread: slots of a row are filled up to whole blocks, so that the sixteen lanes
+// of a block are neighbours.  per_slots: ceil(2^32 / slots), exact for what is divided by it (below slots + 512).
+constexpr int kUnroll = 2;
+
+template <typename T, typename F> __global__ void __launch_bounds__(kThreads) code_kernel(const Inputs in, const Out o,
+                                                                                         const int slots, const uint32_t per_slots)
+{
+    const int64_t first = (int64_t)blockIdx.x * (kThreads * kUnroll);
+    const int64_t row0 = first / slots;
+    const uint32_t slot0 = (uint32_t)(first - row0 * slots) + threadIdx.x;
+    Raw<T> a[kUnroll], b[kUnroll];
+    int64_t row[kUnroll];
+    int col[kUnroll];
+    bool in_row[kUnroll], in_all[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        const uint32_t s = slot0 + u * kThreads, down = __umulhi(s, per_slots);
+        row[u] = row0 + down;
+        col[u] = (int)(s - down * (uint32_t)slots) * 8;
+        in_all[u] = row[u] < o.rows;
+        in_row[u] = in_all[u] && col[u] < o.dim;
+        a[u].clear();
+        b[u].clear();
+        if (in_row[u]) {
+            a[u].load((const T *)in.a + row[u] * in.a_stride + col[u]);
+            if (F::kInputs == 2)
+                b[u].load((const T *)in.b + row[u] * in.b_stride + col[u]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+        const Eight e = F::of(a[u].values(), b[u].values());
+        const uint32_t byte = exponent_byte(of_block(largest(e)), o.code);
+        if (in_row[u])
+            *(uint2 *)(o.codes + row[u] * o.stride + col[u]) = encode(e, byte, o.code);
+        if (in_all[u] && (threadIdx.x & (kLanes - 1)) == 0)
+            o.scale[row[u] * o.scale_stride + col[u] / kScaleBlock] = (uint8_t)byte;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// One scale for each 128 x 128: a CTA a block
+// ---------------------------------------------------------------------------
+template <typename T> __global__ void __launch_bounds__(kThreads) block_kernel(const T *x, int64_t x_stride, const Out o)
+{
+    constexpr int kEach = kScaleBlock * kLanes / kThreads;
+    __shared__ uint32_t most[kThreads / 32];
+    const int col = blockIdx.x * kScaleBlock + (threadIdx.x & (kLanes - 1)) * 8;
+    const int64_t row0 = (int64_t)blockIdx.y * kScaleBlock + threadIdx.x / kLanes;
+    Raw<T> raw[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int64_t row = row0 + i * (kThreads / kLanes);
+        raw[i].clear();
+        if (row < o.rows && col < o.dim)
+            raw[i].load(x + row * x_stride + col);
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+        m = max(m, largest(raw[i].values()));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0)
+        most[threadIdx.x / 32] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i)
+        m = max(m, most[i]);
+    const uint32_t byte = exponent_byte(m, o.code);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int64_t row = row0 + i * (kThreads / kLanes);
+        if (row < o.rows && col < o.dim)
+            *(uint2 *)(o.codes + row * o.stride + col) = encode(raw[i].values(), byte, o.code);
+    }
+    if (threadIdx.x == 0)
+        o.scale[(int64_t)blockIdx.y * o.scale_stride + blockIdx.x] = (uint8_t)byte;
+}
+
+// ---------------------------------------------------------------------------
+// Residual, norm, codes: a CTA a row, which stays in registers
+// ---------------------------------------------------------------------------
+struct NormArgs {
+    const void *x, *residual, *weight;
+    void *sum;
+    int64_t x_stride, residual_stride, sum_stride;
+    float eps;
+    int weight_bf16;
+};
+
+struct None {};  // no residual
+
+template <typename T, typename R, int EACH> __global__ void __launch_bounds__(1024 / (EACH > 2 ? 2 : 1))
+norm_kernel(const NormArgs a, const Out o)
+{
+    constexpr bool kResidual = !std::is_same<R, None>::value;
+    using S = typename std::conditional<kResidual, R, float>::type;
+    __shared__ float part[32];
+    const int64_t row = blockIdx.x;
+    Raw<T> x[EACH];
+    Raw<S> r[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int col = (i * blockDim.x + threadIdx.x) * 8;
+        x[i].clear();
+        r[i].clear();
+        if (col < o.dim) {
+            x[i].load((const T *)a.x + row * a.x_stride + col);
+            if (kResidual)
+                r[i].load((const S *)a.residual + row * a.residual_stride + col);
+        }
+    }
+    Eight h[EACH];
+    float squares = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int col = (i * blockDim.x + threadIdx.x) * 8;
+        h[i] = x[i].values();
+        if (kResidual) {
+            const Eight more = r[i].values();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                h[i].v[j] += more.v[j];
+            if (col < o.dim)
+                store((S *)a.sum + row * a.sum_stride + col, h[i]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            squares = fmaf(h[i].v[j], h[i].v[j], squares);
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1)
+        squares += __shfl_xor_sync(0xffffffffu, squares, k);
+    if (blockDim.x > 32) {
+        if ((threadIdx.x & 31) == 0)
+            part[threadIdx.x / 32] = squares;
+        __syncthreads();
+        squares = (threadIdx.x & 31) < blockDim.x / 32 ? part[threadIdx.x & 31] : 0.0f;
+#pragma unroll
+        for (int k = 16; k; k >>= 1)
+            squares += __shfl_xor_sync(0xffffffffu, squares, k);
+    }
+    const float factor = __frsqrt_rn(__fdiv_rn(squares, (float)o.dim) + a.eps);
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int slot = i * blockDim.x + threadIdx.x, col = slot * 8;
+        Eight w{1, 1, 1, 1, 1, 1, 1, 1};
+        if (a.weight && col < o.dim) {
+            if (a.weight_bf16) {
+                Raw<__nv_bfloat16> raw;
+                raw.load((const __nv_bfloat16 *)a.weight + col);
+                w = raw.values();
+            } else {
+                Raw<float> raw;
+                raw.load((const float *)a.weight + col);
+                w = raw.values();
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            h[i].v[j] = h[i].v[j] * factor * w.v[j];
+        const uint32_t byte = exponent_byte(of_block(largest(h[i])), o.code);
+        if (col < o.dim) {
+            *(uint2 *)(o.codes + row * o.stride + col) = encode(h[i], byte, o.code);
+            if ((threadIdx.x & (kLanes - 1)) == 0)
+                o.scale[row * o.scale_stride + slot / kLanes] = (uint8_t)byte;
+        }
+    }
+}
+
+Out make_out(const spec_coded *c)
+{
+    return {(uint8_t *)c->codes, c->scale, c->stride, c->scale_stride, c->rows, c->dim, c->code};
+}
+
+template <typename T, typename F> spec_status launch_code(const Inputs &in, const spec_coded *out, cudaStream_t stream)
+{
+    const int slots = scale_blocks(out->dim) * kLanes;
+    const int64_t all = (int64_t)out->rows * slots, each = kThreads * kUnroll, ctas = (all + each - 1) / each;
+    if (ctas > INT_MAX)
+        return SPEC_ERR_UNSUPPORTED;
+    const uint32_t per = (uint32_t)(((1ull << 32) + slots - 1) / slots);
+    code_kernel<T, F><<<(unsigned)ctas, kThreads, 0, stream>>>(in, make_out(out), slots, per);
+    return launched();
+}
+
+template <typename T, typename R> spec_status launch_norm(const NormArgs &a, const spec_coded *out, cudaStream_t stream)
+{
+    const int slots = scale_blocks(out->dim) * kLanes;
+    const Out o = make_out(out);
+    const unsigned rows = (unsigned)out->rows;
+    const auto threads = [&](int each) { return (unsigned)(((slots + each - 1) / each + 31) / 32 * 32); };
+    if (slots <= 128)
+        norm_kernel<T, R, 1><<<rows, threads(1), 0, stream>>>(a, o);
+    else if (slots <= 256)
+        norm_kernel<T, R, 2><<<rows, threads(2), 0, stream>>>(a, o);
+    else if (slots <= 2048)
+        norm_kernel<T, R, 4><<<rows, threads(4), 0, stream>>>(a, o);
+    else
+        norm_kernel<T, R, 8><<<rows, threads(8), 0, stream>>>(a, o);
+    return launched();
+}
+
+template <typename T> spec_status norm_of(const NormArgs &a, int residual, const spec_coded *out, cudaStream_t stream)
+{
+    if (!a.residual)
+        return launch_norm<T, None>(a, out, stream);
+    return residual == SPEC_BF16 ? launch_norm<T, __nv_bfloat16>(a, out, stream) : launch_norm<T, float>(a, out, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+spec_status spec_rows_quantise(const void *x, int64_t x_stride, spec_dtype dtype, const spec_coded *out, int block_rows,
+                               void *stream)
+{
+    NvtxScope nvtx("spec_rows_quantise");
+    const spec_status st = check_coded(out);
+    if (st != SPEC_OK)
+        return st;
+    if (bad_dtype(dtype) || (block_rows != 1 && block_rows != kScaleBlock))
+        return SPEC_ERR_UNSUPPORTED;
+    if (out->rows == 0)
+        return SPEC_OK;
+    if (bad_rows(x, x_stride, dtype))
+        return SPEC_ERR_INVALID_ARG;
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (block_rows == 1) {
+        const Inputs in{x, nullptr, x_stride, 0};
+        return dtype == SPEC_BF16 ? launch_code<__nv_bfloat16, Plain>(in, out, s) : launch_code<float, Plain>(in, out, s);
+    }
+    const int64_t down = ((int64_t)out->rows + kScaleBlock - 1) / kScaleBlock;
+    if (down > 65535)
+        return SPEC_ERR_UNSUPPORTED;
+    const dim3 grid(scale_blocks(out->dim), (unsigned)down);
+    if (dtype == SPEC_BF16)
+        block_kernel<<<grid, kThreads, 0, s>>>((const __nv_bfloat16 *)x, x_stride, make_out(out));
+    else
+        block_kernel<<<grid, kThreads, 0, s>>>((const float *)x, x_stride, make_out(out));
+    return launched();
+}
+
+spec_status spec_rows_norm(const void *x, int64_t x_stride, spec_dtype dtype, const void *residual,
+                           int64_t residual_stride, spec_dtype residual_dtype, const void *weight,
+                           spec_dtype weight_dtype, float eps, void *sum, int64_t sum_stride, const spec_coded *out,
+                           void *stream)
+{
+    NvtxScope nvtx("spec_rows_norm");
+    const spec_status st = check_coded(out);
+    if (st != SPEC_OK)
+        return st;
+    if (bad_dtype(dtype) || (residual && bad_dtype(residual_dtype)) || (weight && bad_dtype(weight_dtype)) ||
+        out->dim > SPEC_MAX_NORM_ROW)
+        return SPEC_ERR_UNSUPPORTED;
+    if (!(eps >= 0x1p-126f) || !(eps - eps == 0.0f))
+        return SPEC_ERR_INVALID_ARG;
+    if (out->rows == 0)
+        return SPEC_OK;
+    if (bad_rows(x, x_stride, dtype) || ((uintptr_t)weight & 15u) || !residual != !sum ||
+        (residual && (bad_rows(residual, residual_stride, residual_dtype) || bad_rows(sum, sum_stride, residual_dtype) ||
+                      sum_stride < out->dim)))
+        return SPEC_ERR_INVALID_ARG;
+    const NormArgs a{x, residual, weight, sum, x_stride, residual_stride, sum_stride, eps, weight_dtype == SPEC_BF16};
+    return dtype == SPEC_BF16 ? norm_of<__nv_bfloat16>(a, residual_dtype, out, (cudaStream_t)stream)
+                              : norm_of<float>(a, residual_dtype, out, (cudaStream_t)stream);
+}
+
+spec_status spec_rows_gate(const void *gate, int64_t gate_stride, const void *up, int64_t up_stride, spec_dtype dtype,
+                           spec_act act, const spec_coded *out, void *stream)
+{
+    NvtxScope nvtx("spec_rows_gate");
+    const spec_status st = check_coded(out);
+    if (st != SPEC_OK)
+        return st;
+    if (bad_dtype(dtype) || (act != SPEC_SILU && act != SPEC_GELU_TANH))
+        return SPEC_ERR_UNSUPPORTED;
+    if (out->rows == 0)
+        return SPEC_OK;
+    if (bad_rows(gate, gate_stride, dtype) || bad_rows(up, up_stride, dtype))
+        return SPEC_ERR_INVALID_ARG;
+    const Inputs in{gate, up, gate_stride, up_stride};
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (dtype == SPEC_BF16)
+        return act == SPEC_SILU ? launch_code<__nv_bfloat16, Gated<false>>(in, out, s)
+                                : launch_code<__nv_bfloat16, Gated<true>>(in, out, s);
+    return act == SPEC_SILU ? launch_code<float, Gated<false>>(in, out, s) : launch_code<float, Gated<true>>(in, out, s);
+}
+
+}  // extern "C"
