@@ -20,10 +20,11 @@ from typing import NamedTuple
 import torch
 
 from . import _native
-from .cache import _CODES, _fail, _new, _status, _stream
+from .cache import _CODES, _fail, _status
 
 SCALE = torch.float8_e8m0fnu
 BLOCK = 128
+_Struct, _byref, _current = _native.Coded, ctypes.byref, torch._C._cuda_getDevice
 _ACTS = {"silu": 0, "gelu_tanh": 1}
 _FLOATS = {torch.float32: 0, torch.bfloat16: 1}
 
@@ -40,18 +41,35 @@ class Coded(NamedTuple):
     scale: torch.Tensor
 
 
-def _rows(t, name):
-    """Rows, width and row stride of a tensor whose leading dimensions lie at one stride."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    shape = t.shape
-    if not shape:
-        raise ValueError(f"{name} must have a row dimension")
-    dim = shape[-1]
-    if t.is_contiguous():
-        return (t.numel() // dim if dim else 0), dim, dim
-    stride = t.stride()
-    if stride[-1] != 1 and dim > 1:
+def _stream(stream, index):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+# torch.empty costs 5 us a call beside launches here, and this form of it (the one that torch's compiled code calls) less
+# than 1: for one token it is half of a call's time.
+_empty = torch._C._dynamo.guards._empty_strided_cuda
+
+
+def _new(shape, dtype, stream):
+    """A new tensor on the current device, whose block belongs to the stream that will write it."""
+    shape = tuple(shape)
+    if len(shape) == 2:
+        stride = (shape[1], 1)
+    else:
+        stride, step = (), 1
+        for x in reversed(shape):
+            stride = (step, *stride)
+            step *= x
+    if stream is None:
+        return _empty(shape, stride, dtype)
+    with torch.cuda.stream(stream):
+        return _empty(shape, stride, dtype)
+
+
+def _step(t, name):
+    """Row stride of a tensor whose leading dimensions lie at one stride."""
+    shape, stride = t.shape, t.stride()
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be dense")
     rows, step = 1, None
     for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
@@ -62,61 +80,70 @@ def _rows(t, name):
         elif s != step * rows:
             raise ValueError(f"{name}: rows must lie at one stride, got strides {tuple(stride)} of {tuple(shape)}")
         rows *= n
-    return rows, dim, dim if step is None else step
+    return shape[-1] if step is None else step
 
 
-def _input(t, name, shape, device, dtypes=_FLOATS):
-    """Address, row stride and type code of rows that a kernel reads."""
-    code = dtypes.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    _, dim, step = _rows(t, name)
-    if t.device != device:
-        raise ValueError(f"{name} must live on {device}, found {t.device}")
-    at = t.data_ptr()
-    if at & 15 or step * t.element_size() & 15:
+def _index(t, name):
+    """The current device's index, where the first tensor of a call lives."""
+    index = t.get_device()
+    if index < 0 or index != _current():
+        _elsewhere(t, name, _current() if index >= 0 else index)
+    return index
+
+
+def _matrix(t, name, index, types):
+    """(address, rows, width, row stride, type code) of a tensor of rows on device `index`."""
+    kind = types.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name}: expected {' or '.join(str(d) for d in types)}, got {t.dtype}")
+    if t.get_device() != index:
+        _elsewhere(t, name, index)
+    at, shape = t.data_ptr(), t.shape
+    if not shape or not shape[-1]:
+        raise ValueError(f"{name}: expected rows of some width, got shape {tuple(shape)}")
+    dim = shape[-1]
+    step = dim if t.is_contiguous() else _step(t, name)
+    if (at | step * t.itemsize) & 15:
         raise ValueError(f"{name}: rows must begin at multiples of 16 bytes, got a stride of {step} elements at {at:#x}")
-    return at, step, code
+    return at, t.numel() // dim, dim, step, kind
 
 
-def _device(t, name):
+def _elsewhere(t, name, index):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    device, current = t.device, torch.cuda.current_device()
-    if device.index != current:
-        raise ValueError(f"{name} lives on {device}, but the current device is cuda:{current}: call under "
-                         f"torch.cuda.device({device.index})")
-    return device
+    raise ValueError(f"{name} lives on {t.device}, but the current device is cuda:{index}: call under "
+                     f"torch.cuda.device({t.get_device()})")
 
 
-def _made(t, name, dtype, shape, device, stream):
-    """An output that the caller gave (dense), or a new one."""
-    if t is None:
-        return _new(shape, dtype, device, stream)
+def _made(t, name, dtype, shape, index):
+    """The address of an output that the caller gave, dense."""
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != torch.Size(shape) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a dense {tuple(shape)} tensor on {device}, got {tuple(t.shape)} on {t.device}")
-    return t
+    if t.get_device() != index:
+        _elsewhere(t, name, index)
+    if t.shape != torch.Size(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a dense {tuple(shape)} tensor, got {tuple(t.shape)} with strides {t.stride()}")
+    return t.data_ptr()
 
 
-def _coded_out(out, shape, device, code, stream, weight=False):
-    """The Coded that a call writes, and its spec_coded."""
-    dim = shape[-1]
-    if dim < 16 or dim % 16:
-        raise ValueError(f"the last dimension must be a multiple of 16, got {dim}")
+def _coded_out(out, like, shape, rows, dim, code, stream, weight=False):
+    """The Coded of `shape` that a call writes, beside `like`, and its spec_coded."""
     form = _CODES.get(code)
     if form is None:
         raise TypeError(f"code must be torch.float8_e4m3fn or torch.float8_e5m2, got {code}")
-    blocks = -(-dim // BLOCK)
-    above = (-(-shape[0] // BLOCK),) if weight else shape[:-1]
-    codes, scale = (None, None) if out is None else out
-    codes = _made(codes, "out.codes", code, shape, device, stream)
-    scale = _made(scale, "out.scale", SCALE, (*above, blocks), device, stream)
-    c = _native.Coded(codes.data_ptr(), scale.data_ptr(), dim, blocks, codes.numel() // dim, dim, form)
-    return Coded(codes, scale), c
+    if dim & 15:
+        raise ValueError(f"the last dimension must be a multiple of 16, got {dim}")
+    blocks = (dim + 127) // 128
+    above = ((rows + 127) // 128, blocks) if weight else (*shape[:-1], blocks)
+    if out is None:
+        out = Coded(_new(shape, code, stream), _new(above, SCALE, stream))
+        at, scale_at = out[0].data_ptr(), out[1].data_ptr()
+    else:
+        index = like.get_device()
+        at, scale_at = _made(out[0], "out.codes", code, shape, index), _made(out[1], "out.scale", SCALE, above, index)
+        if at & 15:
+            raise ValueError(f"out.codes: must begin at a multiple of 16 bytes, got {at:#x}")
+    return out, _byref(_Struct(at, scale_at, dim, blocks, rows, dim, form))
 
 
 def rows_quantise(x, code=torch.float8_e4m3fn, out=None, stream=None):
@@ -126,10 +153,10 @@ def rows_quantise(x, code=torch.float8_e4m3fn, out=None, stream=None):
     bytes.  Returns Coded(codes [..., dim], scale [..., ceil(dim / 128)]); ``out``:
     such a Coded to write into.
     """
-    device = _device(x, "x")
-    at, step, dtype = _input(x, "x", x.shape, device)
-    out, c = _coded_out(out, x.shape, device, code, stream)
-    rc = _native.load().spec_rows_quantise(at, step, dtype, ctypes.byref(c), 1, _stream(stream, device))
+    index = _index(x, "x")
+    at, rows, dim, step, dtype = _matrix(x, "x", index, _FLOATS)
+    out, c = _coded_out(out, x, x.shape, rows, dim, code, stream)
+    rc = _native.load().spec_rows_quantise(at, step, dtype, c, 1, _stream(stream, index))
     if rc:
         _fail(rc, "spec_rows_quantise")
     return out
@@ -143,10 +170,10 @@ def weight_quantise(weight, code=torch.float8_e4m3fn, out=None, stream=None):
     """
     if weight.dim() != 2:
         raise ValueError("weight must be an [outputs, width] tensor")
-    device = _device(weight, "weight")
-    at, step, dtype = _input(weight, "weight", weight.shape, device)
-    out, c = _coded_out(out, weight.shape, device, code, stream, weight=True)
-    rc = _native.load().spec_rows_quantise(at, step, dtype, ctypes.byref(c), BLOCK, _stream(stream, device))
+    index = _index(weight, "weight")
+    at, rows, dim, step, dtype = _matrix(weight, "weight", index, _FLOATS)
+    out, c = _coded_out(out, weight, weight.shape, rows, dim, code, stream, True)
+    rc = _native.load().spec_rows_quantise(at, step, dtype, c, BLOCK, _stream(stream, index))
     if rc:
         _fail(rc, "spec_rows_quantise")
     return out
@@ -162,32 +189,38 @@ def rows_norm(x, weight=None, residual=None, eps=1e-6, code=torch.float8_e4m3fn,
     weight       [dim] bfloat16 or float32, or None (1)
     out, out_sum to write into; out_sum may be ``residual`` itself
     """
-    device = _device(x, "x")
+    index = _index(x, "x")
+    at, rows, dim, step, dtype = _matrix(x, "x", index, _FLOATS)
     shape = x.shape
-    at, step, dtype = _input(x, "x", shape, device)
     if not eps >= 2.0 ** -126 or eps == math.inf:
         raise ValueError(f"eps must be positive and finite, got {eps}")
-    out, c = _coded_out(out, shape, device, code, stream)
     w_at, w_type = None, 0
     if weight is not None:
-        if weight.shape != shape[-1:] or not weight.is_contiguous():
-            raise ValueError(f"weight: expected a dense ({shape[-1]},) tensor, got {tuple(weight.shape)}")
-        w_at, _, w_type = _input(weight, "weight", weight.shape, device)
+        w_at, one, w_dim, _, w_type = _matrix(weight, "weight", index, _FLOATS)
+        if one != 1 or w_dim != dim or weight.dim() != 1:
+            raise ValueError(f"weight: expected shape ({dim},), got {tuple(weight.shape)}")
     r_at = s_at = None
     r_step = s_step = r_type = 0
     if residual is not None:
-        r_at, r_step, r_type = _input(residual, "residual", shape, device)
+        if residual.shape != shape:
+            raise ValueError(f"residual: expected shape {tuple(shape)}, got {tuple(residual.shape)}")
+        r_at, _, _, r_step, r_type = _matrix(residual, "residual", index, _FLOATS)
         if out_sum is None:
-            out_sum = _new(shape, residual.dtype, device, stream)
-        elif out_sum.dtype != residual.dtype:
-            raise TypeError(f"out_sum: expected {residual.dtype}, got {out_sum.dtype}")
-        s_at, s_step, _ = _input(out_sum, "out_sum", shape, device)
-        if s_step < shape[-1]:
-            raise ValueError("out_sum: rows must not overlap")
+            out_sum = _new(shape, residual.dtype, stream)
+            s_at, s_step = out_sum.data_ptr(), dim
+        else:
+            if out_sum.dtype != residual.dtype:
+                raise TypeError(f"out_sum: expected {residual.dtype}, got {out_sum.dtype}")
+            if out_sum.shape != shape:
+                raise ValueError(f"out_sum: expected shape {tuple(shape)}, got {tuple(out_sum.shape)}")
+            s_at, _, _, s_step, _ = _matrix(out_sum, "out_sum", index, _FLOATS)
+            if s_step < dim:
+                raise ValueError("out_sum: rows must not overlap")
     elif out_sum is not None:
         raise ValueError("out_sum needs a residual")
-    rc = _native.load().spec_rows_norm(at, step, dtype, r_at, r_step, r_type, w_at, w_type, eps, s_at, s_step,
-                                       ctypes.byref(c), _stream(stream, device))
+    out, c = _coded_out(out, x, shape, rows, dim, code, stream)
+    rc = _native.load().spec_rows_norm(at, step, dtype, r_at, r_step, r_type, w_at, w_type, eps, s_at, s_step, c,
+                                       _stream(stream, index))
     if rc:
         _fail(rc, "spec_rows_norm")
     return out, out_sum
@@ -200,41 +233,46 @@ def rows_gate(gate, up, act="silu", code=torch.float8_e4m3fn, out=None, stream=N
     stride, so halves of one product's output need no copy.  ``act``: "silu" or
     "gelu_tanh".
     """
-    device = _device(gate, "gate")
+    index = _index(gate, "gate")
     kind = _ACTS.get(act)
     if kind is None:
         raise ValueError(f"act must be 'silu' or 'gelu_tanh', got {act!r}")
-    g_at, g_step, dtype = _input(gate, "gate", gate.shape, device)
-    u_at, u_step, u_type = _input(up, "up", gate.shape, device)
+    g_at, rows, dim, g_step, dtype = _matrix(gate, "gate", index, _FLOATS)
+    shape = gate.shape
+    if up.shape != shape:
+        raise ValueError(f"up: expected shape {tuple(shape)}, got {tuple(up.shape)}")
+    u_at, _, _, u_step, u_type = _matrix(up, "up", index, _FLOATS)
     if u_type != dtype:
         raise TypeError(f"up: expected {gate.dtype}, got {up.dtype}")
-    out, c = _coded_out(out, gate.shape, device, code, stream)
-    rc = _native.load().spec_rows_gate(g_at, g_step, u_at, u_step, dtype, kind, ctypes.byref(c), _stream(stream, device))
+    out, c = _coded_out(out, gate, shape, rows, dim, code, stream)
+    rc = _native.load().spec_rows_gate(g_at, g_step, u_at, u_step, dtype, kind, c, _stream(stream, index))
     if rc:
         _fail(rc, "spec_rows_gate")
     return out
 
 
-def _coded_in(coded, name, device, weight):
-    """The spec_coded of codes and scales that a product reads."""
+def _coded_in(coded, name, index, weight):
+    """The spec_coded of codes and scales that a product reads; its rows and width."""
     codes, scale = coded
-    at, step, form = _input(codes, f"{name}.codes", codes.shape, device, _CODES)
-    rows, dim, _ = _rows(codes, f"{name}.codes")
+    at, rows, dim, step, form = _matrix(codes, f"{name}.codes", index, _CODES)
+    if dim % 16:
+        raise ValueError(f"{name}.codes: the last dimension must be a multiple of 16, got {dim}")
     if weight and codes.dim() != 2:
         raise ValueError(f"{name}.codes must be an [outputs, width] tensor")
-    if dim < 16 or dim % 16:
-        raise ValueError(f"{name}.codes: the last dimension must be a multiple of 16, got {dim}")
-    blocks = -(-dim // BLOCK)
-    above = (-(-rows // BLOCK),) if weight else codes.shape[:-1]
-    if scale.dtype != SCALE:
+    blocks = (dim + 127) // 128
+    if scale.dtype is not SCALE:
         raise TypeError(f"{name}.scale: expected {SCALE}, got {scale.dtype}")
-    if scale.shape != torch.Size((*above, blocks)) or scale.device != device:
-        raise ValueError(f"{name}.scale: expected shape {(*above, blocks)} on {device}, got {tuple(scale.shape)} on "
-                         f"{scale.device}")
-    _, _, scale_step = _rows(scale, f"{name}.scale")
-    if rows > 1 and step < dim or scale.numel() > blocks and scale_step < blocks:
-        raise ValueError(f"{name}: rows must not overlap")
-    return _native.Coded(at, scale.data_ptr(), max(step, dim), max(scale_step, blocks), rows, dim, form)
+    if scale.get_device() != index:
+        _elsewhere(scale, f"{name}.scale", index)
+    above = ((rows + 127) // 128, blocks) if weight else (*codes.shape[:-1], blocks)
+    if scale.shape != above:
+        raise ValueError(f"{name}.scale: expected shape {above}, got {tuple(scale.shape)}")
+    scale_step = blocks if scale.is_contiguous() else _step(scale, f"{name}.scale")
+    if step < dim or scale_step < blocks:
+        if rows > 1 and (step < dim or scale.numel() > blocks):
+            raise ValueError(f"{name}: rows must not overlap")
+        step, scale_step = max(step, dim), max(scale_step, blocks)
+    return _byref(_Struct(at, scale.data_ptr(), step, scale_step, rows, dim, form)), rows, dim
 
 
 def rows_product(rows, weight, dtype=torch.bfloat16, out=None, status=None, stream=None):
@@ -245,28 +283,33 @@ def rows_product(rows, weight, dtype=torch.bfloat16, out=None, status=None, stre
     dtype   of the result [..., outputs]: torch.bfloat16 or torch.float32; sums are 32-bit
     out     to write into, rows at any one stride (then ``dtype`` is its type)
     """
-    device = _device(rows[0], "rows.codes")
-    r = _coded_in(rows, "rows", device, False)
-    w = _coded_in(weight, "weight", device, True)
-    if r.dim != w.dim:
-        raise ValueError(f"rows are {r.dim} wide, weight {w.dim}")
-    shape = (*rows[0].shape[:-1], w.rows)
+    index = _index(rows[0], "rows.codes")
+    r, count, dim = _coded_in(rows, "rows", index, False)
+    w, outs, width = _coded_in(weight, "weight", index, True)
+    if dim != width:
+        raise ValueError(f"rows are {dim} wide, weight {width}")
+    shape = (*rows[0].shape[:-1], outs)
     if out is None:
-        if dtype not in _FLOATS:
+        kind = _FLOATS.get(dtype)
+        if kind is None:
             raise TypeError(f"dtype must be torch.bfloat16 or torch.float32, got {dtype}")
-        out = _new(shape, dtype, device, stream)
-        step = w.rows
+        out = _new(shape, dtype, stream)
+        step = outs
     else:
-        if out.dtype not in _FLOATS:
+        kind = _FLOATS.get(out.dtype)
+        if kind is None:
             raise TypeError(f"out: expected torch.bfloat16 or torch.float32, got {out.dtype}")
-        if out.shape != torch.Size(shape) or out.device != device:
-            raise ValueError(f"out: expected shape {shape} on {device}, got {tuple(out.shape)} on {out.device}")
-        _, _, step = _rows(out, "out")
-        if r.rows > 1 and step < w.rows:
+        if out.get_device() != index:
+            _elsewhere(out, "out", index)
+        if out.shape != shape:
+            raise ValueError(f"out: expected shape {shape}, got {tuple(out.shape)}")
+        step = outs if out.is_contiguous() else _step(out, "out")
+        if count > 1 and step < outs:
             raise ValueError("out: rows must not overlap")
-        step = max(step, w.rows)
-    rc = _native.load().spec_rows_product(ctypes.byref(r), ctypes.byref(w), out.data_ptr(), step, _FLOATS[out.dtype],
-                                          _status(status, device), _stream(stream, device))
+        step = max(step, outs)
+    if status is not None:
+        status = _status(status, torch.device("cuda", index))
+    rc = _native.load().spec_rows_product(r, w, out.data_ptr(), step, kind, status, _stream(stream, index))
     if rc:
         _fail(rc, "spec_rows_product")
     return out
