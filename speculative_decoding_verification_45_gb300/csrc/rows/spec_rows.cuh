@@ -35,6 +35,37 @@ inline bool bad_rows(const void *p, int64_t stride, int dtype)
 }
 inline bool bad_dtype(int dtype) { return dtype != SPEC_F32 && dtype != SPEC_BF16; }
 
+// Kernels here may begin while the one before them in the stream ends, and let the next one do so: each sets up what it
+// can and then waits for everything before it (all threads, ahead of any access to global memory).
+__device__ __forceinline__ void after_previous()
+{
+    asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::: "memory");
+}
+
+template <typename... Params, typename... Given>
+inline spec_status launch(void (*kernel)(Params...), dim3 grid, int threads, uint32_t smem, int cluster, cudaStream_t stream,
+                          const Given &...given)
+{
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, Params(given)...) != cudaSuccess) {
+        cudaGetLastError();
+        return SPEC_ERR_CUDA;
+    }
+    return SPEC_OK;
+}
+
 }  // namespace specc
 
 #endif

@@ -154,6 +154,7 @@ template <typename T, typename F> __global__ void __launch_bounds__(kThreads) co
     const int64_t first = (int64_t)blockIdx.x * (kThreads * kUnroll);
     const int64_t row0 = first / slots;
     const uint32_t slot0 = (uint32_t)(first - row0 * slots) + threadIdx.x;
+    after_previous();
     Raw<T> a[kUnroll], b[kUnroll];
     int64_t row[kUnroll];
     int col[kUnroll];
@@ -193,6 +194,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) block_kernel(c
     __shared__ uint32_t most[kThreads / 32];
     const int col = blockIdx.x * kScaleBlock + (threadIdx.x & (kLanes - 1)) * 8;
     const int64_t row0 = (int64_t)blockIdx.y * kScaleBlock + threadIdx.x / kLanes;
+    after_previous();
     Raw<T> raw[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
@@ -243,6 +245,7 @@ norm_kernel(const NormArgs a, const Out o)
     using S = typename std::conditional<kResidual, R, float>::type;
     __shared__ float part[32];
     const int64_t row = blockIdx.x;
+    after_previous();
     Raw<T> x[EACH];
     Raw<S> r[EACH];
 #pragma unroll
@@ -326,25 +329,22 @@ template <typename T, typename F> spec_status launch_code(const Inputs &in, cons
     if (ctas > INT_MAX)
         return SPEC_ERR_UNSUPPORTED;
     const uint32_t per = (uint32_t)(((1ull << 32) + slots - 1) / slots);
-    code_kernel<T, F><<<(unsigned)ctas, kThreads, 0, stream>>>(in, make_out(out), slots, per);
-    return launched();
+    return launch(code_kernel<T, F>, dim3((unsigned)ctas), kThreads, 0, 1, stream, in, make_out(out), slots, per);
 }
 
 template <typename T, typename R> spec_status launch_norm(const NormArgs &a, const spec_coded *out, cudaStream_t stream)
 {
     const int slots = scale_blocks(out->dim) * kLanes;
     const Out o = make_out(out);
-    const unsigned rows = (unsigned)out->rows;
-    const auto threads = [&](int each) { return (unsigned)(((slots + each - 1) / each + 31) / 32 * 32); };
+    const dim3 rows((unsigned)out->rows);
+    const auto threads = [&](int each) { return ((slots + each - 1) / each + 31) / 32 * 32; };
     if (slots <= 128)
-        norm_kernel<T, R, 1><<<rows, threads(1), 0, stream>>>(a, o);
-    else if (slots <= 256)
-        norm_kernel<T, R, 2><<<rows, threads(2), 0, stream>>>(a, o);
-    else if (slots <= 2048)
-        norm_kernel<T, R, 4><<<rows, threads(4), 0, stream>>>(a, o);
-    else
-        norm_kernel<T, R, 8><<<rows, threads(8), 0, stream>>>(a, o);
-    return launched();
+        return launch(norm_kernel<T, R, 1>, rows, threads(1), 0, 1, stream, a, o);
+    if (slots <= 256)
+        return launch(norm_kernel<T, R, 2>, rows, threads(2), 0, 1, stream, a, o);
+    if (slots <= 2048)
+        return launch(norm_kernel<T, R, 4>, rows, threads(4), 0, 1, stream, a, o);
+    return launch(norm_kernel<T, R, 8>, rows, threads(8), 0, 1, stream, a, o);
 }
 
 template <typename T> spec_status norm_of(const NormArgs &a, int residual, const spec_coded *out, cudaStream_t stream)
@@ -380,11 +380,8 @@ spec_status spec_rows_quantise(const void *x, int64_t x_stride, spec_dtype dtype
     if (down > 65535)
         return SPEC_ERR_UNSUPPORTED;
     const dim3 grid(scale_blocks(out->dim), (unsigned)down);
-    if (dtype == SPEC_BF16)
-        block_kernel<<<grid, kThreads, 0, s>>>((const __nv_bfloat16 *)x, x_stride, make_out(out));
-    else
-        block_kernel<<<grid, kThreads, 0, s>>>((const float *)x, x_stride, make_out(out));
-    return launched();
+    return dtype == SPEC_BF16 ? launch(block_kernel<__nv_bfloat16>, grid, kThreads, 0, 1, s, (const __nv_bfloat16 *)x, x_stride, make_out(out))
+                              : launch(block_kernel<float>, grid, kThreads, 0, 1, s, (const float *)x, x_stride, make_out(out));
 }
 
 spec_status spec_rows_norm(const void *x, int64_t x_stride, spec_dtype dtype, const void *residual,

@@ -10,25 +10,26 @@
 // blocks.  (With scales of any value each block's sums would have to be read from
 // tensor memory, scaled and added: 128 x 240 values for every 64 instructions.)
 //
-// The weight's rows are the M side (128 to a CTA), the activations' rows the N side
-// (16 to 240): a round has few rows, which would fill a fraction of an M tile.  A
-// tile of 128 weight rows has one scale a block: all lanes of its column hold the
-// same word.  Four exponent bytes (four blocks, 512 elements of k) make one 32-bit
-// column entry; the instruction descriptor says which byte is meant.
+// Two CTAs on neighbouring SMs work as a pair (cta_group::2): 256 of the weight's rows are the M side, 128 to each, and
+// 32 to 240 of the activations' rows the N side, half of them brought by each.  (A round has few rows, which would fill
+// a fraction of an M tile.)  A tile of 128 weight rows has one scale a block: all lanes of its columns hold the same
+// word.  Four exponent bytes (four blocks, 512 elements of k) make one 32-bit column entry; the instruction descriptor
+// says which byte is meant.
 //
-// Warps of a CTA: four that read accumulators and write the output, four that bring
-// scales into tensor memory (each its 32 lanes), one for the copies, one that issues
-// the products.
+// Warps of a CTA: four that read accumulators and write the output, four that bring scales into tensor memory (each its
+// 32 lanes), one for the copies and, in the first CTA of a pair, one that issues the products.
 //
-// Two arrangements (the rule is at `plan`):
-//   pair    two CTAs share tiles of 256 weight rows; each brings half of the other
-//           operand (cta_group::2).  Persistent, accumulators in two halves of tensor
-//           memory, so that writing one tile overlaps the products of the next.
-//   split   a tile for each cluster; its CTAs take equal parts of k and add their
-//           sums through distributed shared memory, in the order of their ranks.
+// Pairs are persistent, with accumulators in two places, so that writing one tile overlaps the products of the next.
+// Where tiles are too few for the SMs, two or three pairs share one, a part of k each, and add their sums through
+// distributed shared memory in the order of the parts (`plan` has the rule and what it rests on).
+//
+// Bound by the weight's bytes for few rows (1 x 4,096 to 128,256: 78.7 us, the copy rate; 1 x 4,096 to 4,096: 8.7 us, of
+// which 5 are the kernel's start and end), by the products for many (16,376 x 4,096 to 6,144: 200 to 213 us, 3.9 to 4.1
+// PFLOP/s).  Without the scales' path that product took 190 us, without copies 177 (4.6 PFLOP/s).
 
 #include <algorithm>
 #include <atomic>
+#include <new>
 
 #include "../spec_ptx.cuh"
 #include "spec_rows.cuh"
@@ -38,14 +39,18 @@ using namespace specc;
 namespace {
 
 constexpr int kRowsM = 128;   // weight rows of a CTA
-// Two accumulators of up to 240 rows and the scales fill 504 of the 512 columns of tensor memory.
 constexpr int kMaxStages = 12;
 constexpr int kThreads = 320;
 constexpr int kScaleWarp = 4, kCopyWarp = 8, kIssueWarp = 9;
 constexpr int kScaleColumns = 12;  // of one buffer: 4 for the weight's rows, 8 for up to 256 others
 constexpr uint32_t kABytes = kRowsM * kScaleBlock;
-constexpr int kChunk = 32;  // activations' rows that are written together
-constexpr uint32_t kChunkBytes = kChunk * kRowsM * 2;
+constexpr uint32_t kChunkBytes = 32 * 32 * 2;  // outputs in bf16 that a warp writes together
+constexpr int kOutRing = 4;                    // of them on their way
+constexpr uint32_t kOutBytes = 4 * kOutRing * kChunkBytes;
+constexpr int kDepth = 2;             // blocks of k to a stage
+constexpr uint32_t kColumns = 512;    // of tensor memory: all of them
+constexpr int kMostRows = 240;        // of a tile: two accumulators and the scales take 504 columns
+constexpr int kMaxSplits = 3;         // pairs that share a tile's k, in a cluster of twice as many CTAs
 
 struct Args {
     const uint8_t *row_scale, *weight_scale;
@@ -57,7 +62,6 @@ struct Args {
     int row_tiles, out_tiles, group;
     int stages;
     uint32_t stage_bytes, b_bytes;
-    uint32_t columns;        // of tensor memory
     uint32_t idesc;          // without the scales' bytes
     int splits, wide_out;    // wide_out: fp32
     int tma_out;             // bf16 rows at multiples of 16 bytes
@@ -90,17 +94,18 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The address of another CTA's shared memory, at the same place as `p` in this one's.
-__device__ __forceinline__ uint32_t in_cta(const void *p, uint32_t rank)
+// The address of another CTA's shared memory, at the same place as `at` in this one's.
+__device__ __forceinline__ uint32_t in_cluster(uint32_t at, uint32_t rank)
 {
     uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float load_cluster(uint32_t a)
+__device__ __forceinline__ uint32_t in_cta(const void *p, uint32_t rank) { return in_cluster(smem_u32(p), rank); }
+__device__ __forceinline__ float4 load_cluster(uint32_t a)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
     return v;
 }
 // For what went through tensor memory, which tcgen05.fence orders.  (A release at cluster scope, which nothing here needs,
@@ -110,65 +115,42 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar)
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-template <int CG> struct Pair;
-template <> struct Pair<1> {
-    static __device__ __forceinline__ void alloc(uint32_t *to, uint32_t columns)
-    {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(to)), "r"(columns) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    static __device__ __forceinline__ void dealloc(uint32_t at, uint32_t columns)
-    {
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
-    }
-    static __device__ __forceinline__ void commit(uint64_t *bar) { tc_commit(bar); }
-    static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add)
-    {
-        asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
-                     "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-                     "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
-                     : "memory");
-    }
-    static __device__ __forceinline__ void load(const CUtensorMap *map, uint32_t dst, uint32_t bar, int k, int row)
-    {
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
-                         dst),
-                     "l"(map), "r"(bar), "r"(k), "r"(row)
-                     : "memory");
-    }
-};
-template <> struct Pair<2> {
-    static __device__ __forceinline__ void alloc(uint32_t *to, uint32_t columns)
-    {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(to)), "r"(columns) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-    }
-    static __device__ __forceinline__ void dealloc(uint32_t at, uint32_t columns)
-    {
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
-    }
-    static __device__ __forceinline__ void commit(uint64_t *bar)  // in both CTAs
-    {
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                         smem_u32(bar)),
-                     "h"((uint16_t)3)
-                     : "memory");
-    }
-    static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add)
-    {
-        asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
-                     "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
-                     "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
-                     : "memory");
-    }
-    static __device__ __forceinline__ void load(const CUtensorMap *map, uint32_t dst, uint32_t bar, int k, int row)
-    {
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, "
-                     "%4}], [%2];" ::"r"(dst),
-                     "l"(map), "r"(bar), "r"(k), "r"(row)
-                     : "memory");
-    }
-};
+__device__ __forceinline__ void prefetch(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// What two CTAs do together: `mask` has a bit for the rank of each.
+__device__ __forceinline__ void tmem_alloc(uint32_t *to, uint32_t columns)
+{
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(to)), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_dealloc(uint32_t at, uint32_t columns)
+{
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+}
+__device__ __forceinline__ void commit(uint64_t *bar, uint32_t mask)  // in the CTAs of a pair
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"((uint16_t)mask)
+                 : "memory");
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add)
+{
+    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %6, 0;\n"
+                 "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load(const CUtensorMap *map, uint32_t dst, uint32_t bar, int k, int row)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, "
+                 "%4}], [%2];" ::"r"(dst),
+                 "l"(map), "r"(bar), "r"(k), "r"(row)
+                 : "memory");
+}
 
 // mbar_wait for a whole warp: all of its lanes go on, or none does.
 template <bool NOW = false> __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile Guard *guard)
@@ -271,23 +253,37 @@ __device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, 
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ void put(const Args &a, int64_t row, int col, float v)
+// Four neighbouring outputs of a row, together where the row lets them.
+__device__ __forceinline__ void put4(const Args &a, int64_t row, int n, const float4 &v)
 {
-    if (a.wide_out)
-        ((float *)a.out)[row * a.out_stride + col] = v;
-    else
-        ((__nv_bfloat16 *)a.out)[row * a.out_stride + col] = __float2bfloat16_rn(v);
+    const float e[4] = {v.x, v.y, v.z, v.w};
+    if (a.wide_out) {
+        float *const to = (float *)a.out + row * a.out_stride + n;
+        if (n + 4 <= a.outs && ((uintptr_t)to & 15) == 0) {
+            *(float4 *)to = v;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < a.outs)
+                to[i] = e[i];
+    } else {
+        __nv_bfloat16 *const to = (__nv_bfloat16 *)a.out + row * a.out_stride + n;
+        if (n + 4 <= a.outs && ((uintptr_t)to & 7) == 0) {
+            *(uint2 *)to = make_uint2(pack(v.x, v.y), pack(v.z, v.w));
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < a.outs)
+                to[i] = __float2bfloat16_rn(e[i]);
+    }
 }
 
-// Blocks of k to a stage.
-template <int CG> struct Depth {
-    static constexpr int value = CG;
-};
-
 // ---------------------------------------------------------------------------
-// The kernel.  CG: CTAs that issue products together.
+// The kernel
 // ---------------------------------------------------------------------------
-template <int CG> __global__ void __launch_bounds__(kThreads, CG == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap rmap,
                const __grid_constant__ CUtensorMap omap)
 {
@@ -298,10 +294,8 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     uint8_t *const stage0 = (uint8_t *)(((uintptr_t)dynamic + 1023) & ~(uintptr_t)1023);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    const bool lead = CG == 1 || rank == 0;
-    const bool linked = CG == 2 || a.splits > 1;
-    constexpr int kDepth = Depth<CG>::value;
-    constexpr int kBuffers = CG;  // accumulators: a CTA of a split has one tile
+    const uint32_t side = rank & 1, leader = rank - side, mask = 3u << leader;  // of its pair
+    const bool lead = side == 0;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
@@ -309,42 +303,46 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&scale_full[i], 4 * CG);
+            mbar_init(&scale_full[i], 8);
             mbar_init(&scale_empty[i], 1);
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 4 * CG);
+            mbar_init(&acc_empty[i], 8);
         }
         mbar_init(&landed, 1);
         guard.dead = 0;
         guard.limit = a.wait_limit;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kCopyWarp)
-        Pair<CG>::alloc(&tmem_at, a.columns);
+    if (warp == kCopyWarp) {
+        if (elected()) {
+            prefetch(&wmap);
+            prefetch(&rmap);
+        }
+        __syncwarp();
+        tmem_alloc(&tmem_at, kColumns);
+    }
     tc_before();
-    if (linked)
-        cluster_sync();
-    else
-        __syncthreads();
+    cluster_sync();
     tc_after();
-    const uint32_t tmem = tmem_at, scales = tmem + a.columns - 2 * kScaleColumns;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // before any wait that is counted in clocks begins
+    const uint32_t tmem = tmem_at, scales = tmem + kColumns - 2 * kScaleColumns;
 
     // blocks of k of this CTA
-    const int part = CG == 1 ? (int)rank : 0;
+    const int part = (int)rank / 2;
     const int k0 = (int)((int64_t)a.blocks * part / a.splits), k1 = (int)((int64_t)a.blocks * (part + 1) / a.splits);
     const int units = a.row_tiles * a.out_tiles, step = (int)cluster_count();
-    const int own_rows = CG * kRowsM;  // weight rows of a tile
+    constexpr int kTileM = 2 * kRowsM;  // weight rows of a tile
 
     // A stage holds kDepth blocks of k.  The two loops below ask for the next barrier before they issue what the last one
     // allowed: a wait that begins when it is needed takes some 190 clocks even if there is nothing to wait for.
     if (warp == kCopyWarp) {
         Ring ring;
         uint32_t issued = 0;
-        const uint32_t bar0 = CG == 1 ? smem_u32(full) : in_cta(full, 0), base = smem_u32(stage0);
+        const uint32_t bar0 = in_cta(full, leader), base = smem_u32(stage0);
         bool free = true;
         for (int u = (int)cluster_index(); u < units; u += step) {
             const Tile t = tile_of(a, u);
-            const int n0 = t.out * own_rows + (CG == 2 ? (int)rank * kRowsM : 0), r0 = t.row * a.tile + (CG == 2 ? (int)rank * (a.tile / 2) : 0);
+            const int n0 = t.out * kTileM + (int)side * kRowsM, r0 = t.row * a.tile + (int)side * (a.tile / 2);
             for (int b = k0; b < k1; b += kDepth, ++issued) {
                 if (!__all_sync(0xffffffffu, free) && !wait(&empty[ring.at], ring.parity ^ 1, &guard))
                     goto out;
@@ -355,12 +353,12 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
                     const uint32_t at = base + s * a.stage_bytes, bar = bar0 + s * 8;
                     const int blocks = min(kDepth, k1 - b);
                     if (lead)
-                        mbar_expect(&full[s], CG * blocks * (kABytes + a.b_bytes));
+                        mbar_expect(&full[s], 2 * blocks * (kABytes + a.b_bytes));
 #pragma unroll
                     for (int i = 0; i < kDepth; ++i)
                         if (i < blocks) {
-                            Pair<CG>::load(&wmap, at + i * kABytes, bar, (b + i) * kScaleBlock, n0);
-                            Pair<CG>::load(&rmap, at + kDepth * kABytes + i * a.b_bytes, bar, (b + i) * kScaleBlock, r0);
+                            tma_load(&wmap, at + i * kABytes, bar, (b + i) * kScaleBlock, n0);
+                            tma_load(&rmap, at + kDepth * kABytes + i * a.b_bytes, bar, (b + i) * kScaleBlock, r0);
                         }
                 }
                 __syncwarp();
@@ -377,8 +375,8 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         const uint32_t base = smem_u32(stage0);
         bool here = false, scaled = false;
         for (int u = (int)cluster_index(); u < units; u += step, ++done) {
-            const uint32_t buf = done % kBuffers, acc = tmem + buf * a.tile;
-            if (!wait(&acc_empty[buf], (done / kBuffers & 1) ^ 1, &guard))
+            const uint32_t buf = (done & 1), acc = tmem + buf * a.tile;
+            if (!wait(&acc_empty[buf], (done >> 1 & 1) ^ 1, &guard))
                 goto out;
             for (int b = k0; b < k1; b += kDepth) {
                 const int blocks = min(kDepth, k1 - b);
@@ -410,13 +408,13 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
                             const uint32_t sa = scales + g * kScaleColumns;
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                Pair<CG>::mma(acc, da + 2 * j, db + 2 * j, id, sa, sa + 4, k > k0 || j > 0);
+                                mma(acc, da + 2 * j, db + 2 * j, id, sa, sa + 4, k > k0 || j > 0);
                             if (i == blocks - 1)
-                                Pair<CG>::commit(&empty[s]);
+                                commit(&empty[s], mask);
                             if (last)
-                                Pair<CG>::commit(&scale_empty[g]);
+                                commit(&scale_empty[g], mask);
                             if (k == k1 - 1)
-                                Pair<CG>::commit(&acc_full[buf]);
+                                commit(&acc_full[buf], mask);
                         }
                         __syncwarp();
                         groups += last;
@@ -434,7 +432,7 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         uint32_t groups = 0;
         for (int u = (int)cluster_index(); u < units; u += step) {
             const Tile t = tile_of(a, u);
-            const int wb = t.out * CG + (CG == 2 ? (int)rank : 0), r0 = t.row * a.tile;
+            const int wb = t.out * 2 + (int)side, r0 = t.row * a.tile;
             const bool has = (int64_t)wb * kRowsM < a.outs, has0 = mine < a.tile && r0 + mine < a.rows,
                        has1 = mine + 128 < a.tile && r0 + mine + 128 < a.rows;
             const uint8_t *const wp = a.weight_scale + wb * a.weight_scale_stride,
@@ -447,9 +445,9 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
             };
             fetch(k0 >> 4);
             w = s0 = s1 = one4;
-            for (int q = k0 >> 2, first = q; q <= (k1 - 1) >> 2; ++q, ++groups) {
+            for (int q = k0 >> 2; q <= (k1 - 1) >> 2; ++q, ++groups) {
                 const uint32_t g = groups & 1;
-                if (q == first || (q & 3) == 0) {
+                if (q == k0 >> 2 || (q & 3) == 0) {
                     w = next_w;
                     s0 = next0;
                     s1 = next1;
@@ -477,105 +475,144 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
                 tmem_store_wait();
                 tc_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if (CG == 1)
-                        mbar_arrive(&scale_full[g]);
-                    else
-                        arrive_cluster(in_cta(&scale_full[g], 0));
-                }
+                if (lane == 0)
+                    arrive_cluster(in_cta(&scale_full[g], leader));
             }
         }
         for (uint32_t i = groups > 2 ? groups - 2 : 0; i < groups; ++i)
             if (!wait(&scale_empty[i & 1], i >> 1 & 1, &guard))
                 goto out;
     } else if (warp < kScaleWarp) {
-        const uint32_t lanes = (uint32_t)warp << 21, chunk0 = smem_u32(stage0) + a.stages * a.stage_bytes;
+        const uint32_t lanes = (uint32_t)warp << 21, chunk0 = smem_u32(stage0) + a.stages * a.stage_bytes + warp * (kOutRing * kChunkBytes);
         uint32_t done = 0, chunks = 0;
         for (int u = (int)cluster_index(); u < units; u += step, ++done) {
             const Tile t = tile_of(a, u);
-            const uint32_t buf = done % kBuffers, acc = tmem + buf * a.tile + lanes;
-            const int m = warp * 32 + lane, n = t.out * own_rows + (CG == 2 ? (int)rank * kRowsM : 0) + m, r0 = t.row * a.tile;
+            const uint32_t buf = (done & 1), acc = tmem + buf * a.tile + lanes;
+            const int m = warp * 32 + lane, n = t.out * kTileM + (int)side * kRowsM + m, r0 = t.row * a.tile;
             const int used = min(a.tile, a.rows - r0);
-            if (barrier_or<128>(2, !wait<true>(&acc_full[buf], done / kBuffers & 1, &guard)))
+            if (barrier_or<128>(2, !wait<true>(&acc_full[buf], done >> 1 & 1, &guard)))
                 goto out;
             tc_after();
             if (a.tma_out) {
-                for (int c = 0; c < used; c += kChunk, ++chunks) {
-                    float v[32];
+                // 32 outputs and up to 32 rows at a time, transposed on their way through shared memory; the next ones are
+                // on their way from tensor memory meanwhile, and up to kOutRing of them to global memory
+                const auto load = [&](int c, float *v) {
                     tmem_load_pairs(acc + c, v);
                     tmem_load_pairs(acc + (16u << 16) + c, v + 16);
-                    const uint32_t at = chunk0 + (chunks & 1) * kChunkBytes;
-                    if (threadIdx.x == 0)
-                        store_wait_read<1>();  // of this thread's two copies in flight the older one has left its buffer
-                    named_barrier<128>(2);
-                    tmem_wait<32>(v);
+                };
+                const auto write = [&](int c, const float *v) {
+                    const uint32_t at = chunk0 + (chunks++ % kOutRing) * kChunkBytes;
+                    if (lane == 0)
+                        store_wait_read<kOutRing - 1>();
+                    __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         // matrix j of the four: weight rows 8 j to 8 j + 7 of the warp's, activations' rows 8 i to 8 i + 7
-                        const int row = 8 * i + (lane & 7), piece = (warp & 1) * 4 + lane / 8;
-                        store_transposed(at + warp / 2 * (kChunkBytes / 2) + row * 128 + ((piece ^ (row & 7)) << 4),
-                                         pack(v[4 * i], v[4 * i + 1]), pack(v[4 * i + 2], v[4 * i + 3]),
-                                         pack(v[16 + 4 * i], v[17 + 4 * i]), pack(v[18 + 4 * i], v[19 + 4 * i]));
+                        const int row = 8 * i + (lane & 7);
+                        store_transposed(at + row * 64 + ((lane / 8 ^ (row >> 1 & 3)) << 4), pack(v[4 * i], v[4 * i + 1]),
+                                         pack(v[4 * i + 2], v[4 * i + 3]), pack(v[16 + 4 * i], v[17 + 4 * i]),
+                                         pack(v[18 + 4 * i], v[19 + 4 * i]));
                     }
                     proxy_fence();
-                    named_barrier<128>(2);
-                    if (threadIdx.x == 0) {
-                        // boxes of 64 outputs and 16 rows, those that begin inside the tile and the output
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            const int from = n - m + 64 * (h / 2), row = c + 16 * (h & 1);
-                            if (from < a.outs && row < used)
-                                tma_store(&omap, at + h * (kChunkBytes / 4), from, r0 + row);
+                    __syncwarp();
+                    if (lane == 0) {
+                        // boxes of 32 outputs and 16 rows, those that begin inside the tile and the output
+                        if (n < a.outs) {
+                            tma_store(&omap, at, n, r0 + c);
+                            if (c + 16 < used)
+                                tma_store(&omap, at + kChunkBytes / 2, n, r0 + c + 16);
                         }
                         store_commit();
                     }
+                };
+                float v[32], w[32];
+                load(0, v);
+                for (int c = 0; c < used; c += 64) {
+                    tmem_wait<32>(v);
+                    if (c + 32 < used)
+                        load(c + 32, w);
+                    write(c, v);
+                    if (c + 32 >= used)
+                        break;
+                    tmem_wait<32>(w);
+                    if (c + 64 < used)
+                        load(c + 64, v);
+                    write(c + 32, w);
                 }
             } else {
-                for (int c = 0; c < used; c += 16) {
-                    float v[16];
+                for (int c = 0; c < used; c += 32) {
+                    float v[32];
                     TmemLoad<16>::go(acc + c, v);
-                    tmem_wait<16>(v);
-                    if (CG == 1 && a.splits > 1) {
+                    TmemLoad<16>::go(acc + c + 16, v + 16);
+                    tmem_wait<32>(v);
+                    if (a.splits > 1) {
                         // the copies into the stages have all been used by now
                         float *const sums = (float *)stage0 + m;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
+                        for (int i = 0; i < 32; ++i)
                             sums[(c + i) * kRowsM] = v[i];
                     } else if (n < a.outs) {
+                        const int64_t first = (r0 + c) * a.out_stride + n;
+                        if (a.wide_out) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c + i < used)
-                                put(a, r0 + c + i, n, v[i]);
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i < used)
+                                    ((float *)a.out)[first + i * a.out_stride] = v[i];
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (c + i < used)
+                                    ((__nv_bfloat16 *)a.out)[first + i * a.out_stride] = __float2bfloat16_rn(v[i]);
+                        }
                     }
                 }
             }
             tc_before();
             __syncwarp();
-            if (lane == 0 && CG == 2)
-                arrive_cluster(in_cta(&acc_empty[buf], 0));
+            if (lane == 0)
+                arrive_cluster(in_cta(&acc_empty[buf], leader));
         }
     }
 out:
-    if (threadIdx.x == 0)
+    // The next kernel's CTAs need this one's shared memory; begun any earlier they wait beside it (212 to 225 us against 200
+    // for 16,376 x 4,096 to 6,144).
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp < kScaleWarp && lane == 0)
         store_wait_read<0>();  // the buffers are the CTA's for as long as copies read them
     __syncwarp();
-    if (CG == 1 && a.splits > 1) {
+    if (a.splits > 1) {
         cluster_sync();
-        // each CTA adds its share of the tile's rows, rank by rank
+        // each CTA adds its share of the tile's rows, part by part
         const Tile t = tile_of(a, (int)cluster_index());
-        const int m = threadIdx.x % kRowsM, n = t.out * kRowsM + m, r0 = t.row * a.tile, used = min(a.tile, a.rows - r0);
-        const int c1 = used * ((int)rank + 1) / a.splits;
-        if (n < a.outs && threadIdx.x < 2 * kRowsM) {
-            for (int c = used * (int)rank / a.splits + (int)threadIdx.x / kRowsM; c < c1; c += 2) {
-                float v[8];
+        const int m = lane * 4, n = t.out * kTileM + (int)side * kRowsM + m, r0 = t.row * a.tile, used = min(a.tile, a.rows - r0),
+                  c1 = used * (part + 1) / a.splits;
+        if (n < a.outs && warp < 8) {
+            const uint32_t at = smem_u32((float *)stage0 + m);
+            uint32_t from[kMaxSplits];
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    v[r] = r < a.splits ? load_cluster(in_cta((float *)stage0 + c * kRowsM + m, r)) : 0.0f;
-                float sum = v[0];
+            for (int r = 0; r < kMaxSplits; ++r)
+                from[r] = in_cluster(at, r < a.splits ? 2 * r + side : rank);
+            constexpr int kMore = 4;  // rows whose loads are in flight together
+            for (int c = used * part / a.splits + warp; c < c1; c += 8 * kMore) {
+                float4 v[kMore][kMaxSplits];
 #pragma unroll
-                for (int r = 1; r < 8; ++r)
-                    sum += v[r];  // what is not there is 0
-                put(a, r0 + c, n, sum);
+                for (int i = 0; i < kMore; ++i)
+#pragma unroll
+                    for (int r = 0; r < kMaxSplits; ++r)
+                        v[i][r] = r < a.splits && c + 8 * i < c1 ? load_cluster(from[r] + (c + 8 * i) * (kRowsM * 4)) : make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < kMore; ++i) {
+                    float4 sum = v[i][0];
+#pragma unroll
+                    for (int r = 1; r < kMaxSplits; ++r) {  // what is not there is 0
+                        sum.x += v[i][r].x;
+                        sum.y += v[i][r].y;
+                        sum.z += v[i][r].z;
+                        sum.w += v[i][r].w;
+                    }
+                    if (c + 8 * i < c1)
+                        put4(a, r0 + c + 8 * i, n, sum);
+                }
             }
         }
     }
@@ -585,7 +622,7 @@ out:
         // one CTA of a pair filled never completes its phase), so a time is waited out that a copy takes many times over.
         if (warp == kIssueWarp && lead) {
             if (elected()) {
-                Pair<CG>::commit(&landed);
+                commit(&landed, mask);
                 land(&landed, 0);
             }
         } else if (warp == kCopyWarp && lane == 0) {
@@ -598,61 +635,58 @@ out:
         __syncwarp();
     }
     tc_before();
-    if (linked)
-        cluster_sync();
-    else
-        __syncthreads();
+    cluster_sync();
     tc_after();
     if (warp == kCopyWarp)
-        Pair<CG>::dealloc(tmem, a.columns);
+        tmem_dealloc(tmem, kColumns);
 }
 
 // ---------------------------------------------------------------------------
 // Host
 // ---------------------------------------------------------------------------
+struct Device {
+    int sms = 0;
+    int clusters[kMaxSplits + 1] = {};  // clusters of 2 n CTAs that run at once
+};
+
 struct Plan {
-    bool pair;
     int tile, splits;
 };
 
-Plan plan(int rows, int outs, int blocks, int sms)
+// The tile and the parts of k of least estimated time.  In units of 0.1 ns: a block of k takes 185 ns + 0.6 a row of the
+// tile (issue, then copies and products; 32 blocks of 16,376 rows to 6,144: 6.5 us with 32 rows, 9.7 with 240), in as many
+// rounds as there are tiles to a pair of SMs; adding up n parts takes n times 0.5 us + 4 ns a row.  Parts that do not all
+// run at once cost a round more than they save (8,192 x 8,192 in three parts: 22 us, in two 15.6, in one 18.8).
+Plan plan(const Device &d, int rows, int outs, int blocks)
 {
-    const int out_tiles = (outs + kRowsM - 1) / kRowsM;
+    const int64_t out_tiles = (outs + 2 * kRowsM - 1) / (2 * kRowsM);
     Plan p{};
-    if (rows > 64 && out_tiles >= 2 && (int64_t)rows * out_tiles > 128 * 76) {
-        p.pair = true;
-        p.splits = 1;
-        const int pairs = (out_tiles + 1) / 2, units = sms / 2;
-        int64_t best = INT64_MAX;
-        for (int tile = 32; tile <= 240; tile += 16) {
-            // a block takes as long as its instructions' issue, then as its products and copies: measured at 64 to 240 rows
-            const int64_t tiles = (int64_t)pairs * ((rows + tile - 1) / tile),
-                          cost = (tiles + units - 1) / units * std::max(tile + 160, 270);
-            if (cost <= best) {
+    int64_t best = INT64_MAX;
+    for (int tile = 32; tile <= kMostRows; tile += 16) {
+        const int64_t units = out_tiles * ((rows + tile - 1) / tile), rounds = (units + d.sms / 2 - 1) / (d.sms / 2);
+        for (int n = 1; n <= kMaxSplits; ++n) {
+            if (n > 1 && (units > d.clusters[n] || n > blocks))
+                break;
+            const int64_t each = (blocks + n - 1) / n * (1850 + 6 * tile), cost = n == 1 ? rounds * each : each + n * (5000 + 40 * tile);
+            if (cost < best) {
                 best = cost;
-                p.tile = tile;
+                p = {tile, n};
             }
         }
-        return p;
+        if (tile >= rows)
+            break;
     }
-    const int row_tiles = (rows + 127) / 128;
-    p.tile = ((rows + row_tiles - 1) / row_tiles + 15) / 16 * 16;
-    p.splits = 1;
-    while (p.splits < 8 && (int64_t)out_tiles * row_tiles * p.splits * 2 <= 2 * sms && blocks >= 4 * p.splits)
-        p.splits *= 2;
     return p;
 }
 
 constexpr int kMaxDevices = 64;
-std::atomic<int> g_sms[kMaxDevices];
+std::atomic<const Device *> g_devices[kMaxDevices];  // made once each, and kept
 
-constexpr uint32_t kMostShared = 227 * 1024;
-// Bytes for the stages.  A CTA of a pair holds all of tensor memory, so nothing else that waits for some may be on its
-// SM, where two clusters could each hold what the other waits for: it takes all of shared memory.  Two CTAs of splits
-// share an SM, 256 columns each; a third one must not fit.
-constexpr uint32_t kPairShared = kMostShared - 4096, kSplitShared = 110 * 1024;
+// Dynamic shared memory: nearly all of it.  A CTA holds all of tensor memory, so nothing else that waits for some may be
+// on its SM, where two clusters could each hold what the other waits for.
+constexpr uint32_t kShared = 223 * 1024;
 
-spec_status device_sms(int *sms)
+spec_status this_device(const Device **out)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -661,37 +695,63 @@ spec_status device_sms(int *sms)
     }
     if (dev < 0 || dev >= kMaxDevices)
         return SPEC_ERR_UNSUPPORTED;
-    int v = g_sms[dev].load(std::memory_order_acquire);
-    if (!v) {
-        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaFuncSetAttribute(product_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplitShared) != cudaSuccess ||
-            cudaFuncSetAttribute(product_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairShared) != cudaSuccess) {
+    const Device *found = g_devices[dev].load(std::memory_order_acquire);
+    if (!found) {
+        Device d;
+        if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaFuncSetAttribute(product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared) != cudaSuccess) {
             cudaGetLastError();
             return SPEC_ERR_CUDA;
         }
-        g_sms[dev].store(v, std::memory_order_release);
+        for (int n = 1; n <= kMaxSplits; ++n) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2 * n;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2 * n * d.sms);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = kShared;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&d.clusters[n], product_kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                return SPEC_ERR_CUDA;
+            }
+        }
+        if (d.sms < 2 || d.clusters[1] < 1)
+            return SPEC_ERR_UNSUPPORTED;
+        Device *const made = new (std::nothrow) Device(d);
+        if (!made)
+            return SPEC_ERR_CUDA;
+        found = nullptr;
+        if (!g_devices[dev].compare_exchange_strong(found, made, std::memory_order_acq_rel))
+            delete made;  // another thread was first
+        else
+            found = made;
     }
-    *sms = v;
+    *out = found;
     return SPEC_OK;
 }
 
-// [element, row], rows `stride` bytes apart; a box is 128 bytes of `box_rows` rows.
-spec_status make_map(CUtensorMapDataType type, int element, void *at, int64_t dim, int64_t rows, int64_t stride, int box_rows,
+// [element, row], rows `stride` bytes apart; a box is box_bytes (64 or 128, swizzled as wide) of box_rows rows.
+spec_status make_map(CUtensorMapDataType type, int element, int box_bytes, void *at, int64_t dim, int64_t rows, int64_t stride, int box_rows,
                      CUtensorMap *map)
 {
     const EncodeTiled encode = encoder();
     if (!encode)
         return SPEC_ERR_CUDA;
     const cuuint64_t size[2] = {(cuuint64_t)dim, (cuuint64_t)rows}, step[1] = {(cuuint64_t)stride};
-    const cuuint32_t box[2] = {128u / (cuuint32_t)element, (cuuint32_t)box_rows}, one[2] = {1, 1};
-    return encode(map, type, 2, at, size, step, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const cuuint32_t box[2] = {(cuuint32_t)(box_bytes / element), (cuuint32_t)box_rows}, one[2] = {1, 1};
+    return encode(map, type, 2, at, size, step, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? SPEC_OK
                : SPEC_ERR_INVALID_ARG;
 }
 spec_status make_map(const spec_coded *c, int box_rows, CUtensorMap *map)
 {
-    return make_map(CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, c->codes, c->dim, c->rows, c->stride, box_rows, map);
+    return make_map(CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128, c->codes, c->dim, c->rows, c->stride, box_rows, map);
 }
 
 }  // namespace
@@ -714,8 +774,8 @@ extern "C" spec_status spec_rows_product(const spec_coded *rows, const spec_code
     const int64_t size = dtype == SPEC_BF16 ? 2 : 4;
     if (!out || ((uintptr_t)out & (size - 1)) || out_stride < weight->rows || out_stride >= (1ll << 38) || bad4(status, false))
         return SPEC_ERR_INVALID_ARG;
-    int sms = 0;
-    st = device_sms(&sms);
+    const Device *device = nullptr;
+    st = this_device(&device);
     if (st != SPEC_OK)
         return st;
     Args a{};
@@ -728,52 +788,34 @@ extern "C" spec_status spec_rows_product(const spec_coded *rows, const spec_code
     a.rows = rows->rows;
     a.outs = weight->rows;
     a.blocks = scale_blocks(rows->dim);
-    const Plan p = plan(a.rows, a.outs, a.blocks, sms);
-    const int cg = p.pair ? 2 : 1;
+    const Plan p = plan(*device, a.rows, a.outs, a.blocks);
     a.tile = p.tile;
     a.splits = p.splits;
     a.row_tiles = (a.rows + p.tile - 1) / p.tile;
-    a.out_tiles = (a.outs + cg * kRowsM - 1) / (cg * kRowsM);
-    if ((int64_t)a.row_tiles * a.out_tiles * p.splits > INT_MAX)
+    a.out_tiles = (a.outs + 2 * kRowsM - 1) / (2 * kRowsM);
+    if ((int64_t)a.row_tiles * a.out_tiles > INT_MAX / (2 * kMaxSplits))
         return SPEC_ERR_UNSUPPORTED;
     // Eight weight tiles side by side share the rows that pass through L2; as many as stay there (32 MB of them) where the
     // rows themselves do not, so that those pass once (16,376 x 4,096 to 6,144: 224 us with 8, 197 with all 24; 1,280 x
     // 4,096 to 128,256: 395 us with 8, 440 with 64).
     a.group = 8;
     if ((int64_t)a.rows * a.blocks > (16 << 20) / kScaleBlock)
-        a.group = std::max(8, (int)std::min<int64_t>(a.out_tiles, (32 << 20) / ((int64_t)cg * kRowsM * kScaleBlock * a.blocks)));
-    a.b_bytes = (uint32_t)(p.tile / cg) * kScaleBlock;
-    a.stage_bytes = (p.pair ? Depth<2>::value : Depth<1>::value) * (kABytes + a.b_bytes);  // a multiple of 1,024: tiles are multiples of 16, of 32 for a pair
-    const uint32_t shared = p.pair ? kPairShared : kSplitShared;
+        a.group = std::max(8, (int)std::min<int64_t>(a.out_tiles, (32 << 20) / ((int64_t)2 * kRowsM * kScaleBlock * a.blocks)));
+    a.b_bytes = (uint32_t)(p.tile / 2) * kScaleBlock;  // a multiple of 1,024
+    a.stage_bytes = kDepth * (kABytes + a.b_bytes);
     a.tma_out = dtype == SPEC_BF16 && p.splits == 1 && ((uintptr_t)out & 15u) == 0 && (out_stride * 2 & 15) == 0;
-    a.stages = (int)std::min<uint32_t>(kMaxStages, (shared - 1024 - (a.tma_out ? 2 * kChunkBytes : 0)) / a.stage_bytes);
-    a.columns = p.pair ? 512 : 256;
+    a.stages = (int)std::min<uint32_t>(kMaxStages, (kShared - 1024 - (a.tma_out ? kOutBytes : 0)) / a.stage_bytes);
     // as in the unscaled kinds, and: bytes of the scales at bits 4 and 29 (set for each block), scales of powers of two (bit 23)
     a.idesc = (uint32_t)(weight->code == SPEC_E5M2) << 7 | (uint32_t)(rows->code == SPEC_E5M2) << 10 | (uint32_t)(p.tile >> 3) << 17 |
-              1u << 23 | (uint32_t)(cg * kRowsM >> 7) << 27;
+              1u << 23 | (uint32_t)(2 * kRowsM >> 7) << 27;
     a.wide_out = dtype == SPEC_F32;
     a.wait_limit = wait_limit();
     a.status = status;
     CUtensorMap wmap, rmap, omap{};
-    if ((st = make_map(weight, kRowsM, &wmap)) != SPEC_OK || (st = make_map(rows, p.tile / cg, &rmap)) != SPEC_OK ||
-        (a.tma_out && (st = make_map(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, a.outs, a.rows, out_stride * 2, 16, &omap)) != SPEC_OK))
+    if ((st = make_map(weight, kRowsM, &wmap)) != SPEC_OK || (st = make_map(rows, p.tile / 2, &rmap)) != SPEC_OK ||
+        (a.tma_out && (st = make_map(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 64, out, a.outs, a.rows, out_stride * 2, 16, &omap)) != SPEC_OK))
         return st;
     const int units = a.row_tiles * a.out_tiles;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.pair ? 2 : p.splits;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.pair ? 2 * std::min(units, sms / 2) : units * p.splits);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = shared;
-    cfg.stream = (cudaStream_t)stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    void *args[] = {&a, &wmap, &rmap, &omap};
-    if (cudaLaunchKernelExC(&cfg, p.pair ? (const void *)product_kernel<2> : (const void *)product_kernel<1>, args) != cudaSuccess) {
-        cudaGetLastError();
-        return SPEC_ERR_CUDA;
-    }
-    return SPEC_OK;
+    const dim3 grid((unsigned)(2 * p.splits * (p.splits == 1 ? std::min(units, device->sms / 2) : units)));
+    return launch(product_kernel, grid, kThreads, kShared, 2 * p.splits, (cudaStream_t)stream, a, wmap, rmap, omap);
 }
