@@ -10,6 +10,9 @@
 // rounding to fewer bits is that to the code, and of the sum that spec_rows_norm
 // writes back (which its norm does not read again: it takes the 32-bit sum).
 
+#include <type_traits>
+
+#include "../spec_ptx.cuh"
 #include "spec_rows.cuh"
 
 using namespace specc;
@@ -19,14 +22,23 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kLanes = kScaleBlock / 8;  // of a block
 
-struct Eight {
-    float v[8];
+struct Eight {  // values, two by two for the instructions that take two
+    float2 v[4];
 };
 
-__device__ __forceinline__ void unpack(uint32_t two, float &a, float &b)
+__device__ __forceinline__ float2 unpack(uint32_t two) { return {__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u)}; }
+
+// The largest magnitude's bits: magnitudes as integers are in the same order.  From 0x7f800000 up it stands for an infinity
+// (or, in `most_of` 16-bit values, a NaN; the other form passes over those).
+constexpr uint32_t kInfinity = 0x7f800000u;
+
+__device__ __forceinline__ uint32_t most(const Eight &e)
 {
-    a = __uint_as_float(two << 16);
-    b = __uint_as_float(two & 0xffff0000u);
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m = fmaxf(fmaxf(m, fabsf(e.v[i].x)), fabsf(e.v[i].y));
+    return __float_as_uint(m);
 }
 
 template <typename T> struct Raw;  // eight elements as they lie in memory
@@ -34,14 +46,12 @@ template <> struct Raw<__nv_bfloat16> {
     uint4 q;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { q = *(const uint4 *)p; }
     __device__ __forceinline__ void clear() { q = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ Eight values() const
+    __device__ __forceinline__ Eight values() const { return {{unpack(q.x), unpack(q.y), unpack(q.z), unpack(q.w)}}; }
+    __device__ __forceinline__ uint32_t most_of() const
     {
-        Eight e;
-        unpack(q.x, e.v[0], e.v[1]);
-        unpack(q.y, e.v[2], e.v[3]);
-        unpack(q.z, e.v[4], e.v[5]);
-        unpack(q.w, e.v[6], e.v[7]);
-        return e;
+        constexpr uint32_t kMagnitude = 0x7fff7fffu;
+        const uint32_t m = max_halves(max_halves(q.x & kMagnitude, q.y & kMagnitude), max_halves(q.z & kMagnitude, q.w & kMagnitude));
+        return max(m << 16, m & 0xffff0000u);
     }
 };
 template <> struct Raw<float> {
@@ -52,33 +62,33 @@ template <> struct Raw<float> {
         b = *(const float4 *)(p + 4);
     }
     __device__ __forceinline__ void clear() { a = b = make_float4(0, 0, 0, 0); }
-    __device__ __forceinline__ Eight values() const { return {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}; }
+    __device__ __forceinline__ Eight values() const { return {{{a.x, a.y}, {a.z, a.w}, {b.x, b.y}, {b.z, b.w}}}; }
+    __device__ __forceinline__ uint32_t most_of() const { return most(values()); }
 };
 
-__device__ __forceinline__ uint32_t pack(float a, float b)
+__device__ __forceinline__ uint32_t pack(float2 a)
 {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a.x, a.y);
     return *(const uint32_t *)&h;
 }
 __device__ __forceinline__ void store(__nv_bfloat16 *p, const Eight &e)
 {
-    *(uint4 *)p = make_uint4(pack(e.v[0], e.v[1]), pack(e.v[2], e.v[3]), pack(e.v[4], e.v[5]), pack(e.v[6], e.v[7]));
+    *(uint4 *)p = make_uint4(pack(e.v[0]), pack(e.v[1]), pack(e.v[2]), pack(e.v[3]));
 }
 __device__ __forceinline__ void store(float *p, const Eight &e)
 {
-    *(float4 *)p = make_float4(e.v[0], e.v[1], e.v[2], e.v[3]);
-    *(float4 *)(p + 4) = make_float4(e.v[4], e.v[5], e.v[6], e.v[7]);
+    *(float4 *)p = make_float4(e.v[0].x, e.v[0].y, e.v[1].x, e.v[1].y);
+    *(float4 *)(p + 4) = make_float4(e.v[2].x, e.v[2].y, e.v[3].x, e.v[3].y);
 }
 
-// The largest finite magnitude.  Magnitudes as integers are in the same order, and
-// those that are not finite are the ones from 0x7f800000 up.
-__device__ __forceinline__ uint32_t largest(const Eight &e)
+// The largest finite magnitude's bits, for the rare block that holds something else.
+__device__ __forceinline__ uint32_t most_finite(const Eight &e)
 {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t u = __float_as_uint(e.v[i]) & 0x7fffffffu;
-        m = max(m, u < 0x7f800000u ? u : 0u);
+        const uint32_t u = __float_as_uint(i & 1 ? e.v[i / 2].y : e.v[i / 2].x) & 0x7fffffffu;
+        m = max(m, u < kInfinity ? u : 0u);
     }
     return m;
 }
@@ -97,15 +107,40 @@ __device__ __forceinline__ uint32_t exponent_byte(uint32_t most, int code)
     return __float_as_uint(scale_for(__uint_as_float(most), code)) >> 23;
 }
 
-// Codes of eight elements; the byte is in [27, 247], so the reciprocal is a normal power of two.
-__device__ __forceinline__ uint2 encode(const Eight &e, uint32_t byte, int code)
+// Codes of eight elements; the byte is in [27, 247], so the reciprocal is a normal power of two.  finite: no infinity is
+// among them (it would become the largest code; a NaN is the code NaN either way).
+__device__ __forceinline__ uint2 encode(const Eight &e, uint32_t byte, int code, bool finite)
 {
     const float inv = __uint_as_float((254u - byte) << 23);
     uint32_t h[4];
+    float2 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        h[i] = encode2(e.v[2 * i] * inv, e.v[2 * i + 1] * inv, code);
+        x[i] = mul2(e.v[i], {inv, inv});
+    if (!finite) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            h[i] = encode2(x[i].x, x[i].y, code);
+    } else if (code == SPEC_E4M3) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            h[i] = encode2_finite(x[i].x, x[i].y, SPEC_E4M3);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            h[i] = encode2_finite(x[i].x, x[i].y, SPEC_E5M2);
+    }
     return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
+
+// The scale's byte for the sixteen lanes of a block, from each lane's largest magnitude; whether all in the warp is finite.
+__device__ __forceinline__ uint32_t block_byte(uint32_t m, const Eight &e, int code, bool *finite)
+{
+    m = of_block(m);
+    *finite = !__any_sync(0xffffffffu, m >= kInfinity);
+    if (!*finite)
+        m = of_block(most_finite(e));
+    return exponent_byte(m, code);
 }
 
 struct Out {
@@ -119,7 +154,6 @@ struct Out {
 // ---------------------------------------------------------------------------
 struct Plain {
     static constexpr int kInputs = 1;
-    static __device__ __forceinline__ Eight of(const Eight &a, const Eight &) { return a; }
 };
 // a / (1 + exp(-z)) * b.  exp by the fast base-2 form: off by 2^-22 and |z| * 2^-24, with no effect where z is large
 // (positive: the sum is 1; negative: the result is next to 0 beside its block).
@@ -127,13 +161,22 @@ template <bool GELU> struct Gated {
     static constexpr int kInputs = 2;
     static __device__ __forceinline__ Eight of(const Eight &a, const Eight &b)
     {
+        // 0.5 (1 + tanh(y)) = 1 / (1 + exp(-2 y)), y = sqrt(2 / pi) (g + 0.044715 g^3); exp(x) = 2^(x log2 e)
+        constexpr float kLog2e = 1.44269504088896f, kOne = -1.59576912160573f * kLog2e, kThree = -0.0713548162726003f * kLog2e;
         Eight r;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float g = a.v[i];
-            // 0.5 (1 + tanh(y)) = 1 / (1 + exp(-2 y)), y = sqrt(2 / pi) (g + 0.044715 g^3)
-            const float z = GELU ? g * fmaf(0.0713548162726f * g, g, 1.59576912161f) : g;
-            r.v[i] = __fdividef(g, 1.0f + __expf(-z)) * b.v[i];
+        for (int i = 0; i < 4; ++i) {
+            const float2 g = a.v[i];
+            float2 z;
+            if (GELU)
+                z = mul2(g, fma2(mul2(g, {kThree, kThree}), g, {kOne, kOne}));
+            else
+                z = mul2(g, {-kLog2e, -kLog2e});
+            const float2 d = add2({exp2_fast(z.x), exp2_fast(z.y)}, {1.0f, 1.0f});
+            float2 s;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(d.x));
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(d.y));
+            r.v[i] = mul2(mul2(g, s), b.v[i]);
         }
         return r;
     }
@@ -144,16 +187,17 @@ struct Inputs {
     int64_t a_stride, b_stride;
 };
 
-// Chunks of eight in order, kUnroll a thread: slots of a row are filled up to whole blocks, so that the sixteen lanes
+// Chunks of eight in order: slots of a row are filled up to whole blocks, so that the sixteen lanes
 // of a block are neighbours.  per_slots: ceil(2^32 / slots), exact for what is divided by it (below slots + 512).
 constexpr int kUnroll = 2;
 
 template <typename T, typename F> __global__ void __launch_bounds__(kThreads) code_kernel(const Inputs in, const Out o,
                                                                                          const int slots, const uint32_t per_slots)
 {
-    const int64_t first = (int64_t)blockIdx.x * (kThreads * kUnroll);
-    const int64_t row0 = first / slots;
-    const uint32_t slot0 = (uint32_t)(first - row0 * slots) + threadIdx.x;
+    // in units of a block's lanes the first chunk's place fits 32 bits
+    const uint32_t blocks = (uint32_t)slots / kLanes, first = blockIdx.x * (kThreads * kUnroll / kLanes), above = first / blocks;
+    const int64_t row0 = above;
+    const uint32_t slot0 = (first - above * blocks) * kLanes + threadIdx.x;
     after_previous();
     Raw<T> a[kUnroll], b[kUnroll];
     int64_t row[kUnroll];
@@ -176,29 +220,40 @@ template <typename T, typename F> __global__ void __launch_bounds__(kThreads) co
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-        const Eight e = F::of(a[u].values(), b[u].values());
-        const uint32_t byte = exponent_byte(of_block(largest(e)), o.code);
+        Eight e;
+        uint32_t m;
+        if constexpr (F::kInputs == 2) {
+            e = F::of(a[u].values(), b[u].values());
+            m = most(e);
+        } else {
+            e = a[u].values();
+            m = a[u].most_of();
+        }
+        bool finite;
+        const uint32_t byte = block_byte(m, e, o.code, &finite);
         if (in_row[u])
-            *(uint2 *)(o.codes + row[u] * o.stride + col[u]) = encode(e, byte, o.code);
+            *(uint2 *)(o.codes + row[u] * o.stride + col[u]) = encode(e, byte, o.code, finite);
         if (in_all[u] && (threadIdx.x & (kLanes - 1)) == 0)
             o.scale[row[u] * o.scale_stride + col[u] / kScaleBlock] = (uint8_t)byte;
     }
 }
 
 // ---------------------------------------------------------------------------
-// One scale for each 128 x 128: a CTA a block
+// One scale for each 128 x 128: a CTA a block, which stays in registers as it was read
 // ---------------------------------------------------------------------------
-template <typename T> __global__ void __launch_bounds__(kThreads) block_kernel(const T *x, int64_t x_stride, const Out o)
+constexpr int kBlockThreads = 512;
+
+template <typename T> __global__ void __launch_bounds__(kBlockThreads, 3) block_kernel(const T *x, int64_t x_stride, const Out o)
 {
-    constexpr int kEach = kScaleBlock * kLanes / kThreads;
-    __shared__ uint32_t most[kThreads / 32];
+    constexpr int kEach = kScaleBlock * kLanes / kBlockThreads;
+    __shared__ uint32_t found[kBlockThreads / 32];
     const int col = blockIdx.x * kScaleBlock + (threadIdx.x & (kLanes - 1)) * 8;
     const int64_t row0 = (int64_t)blockIdx.y * kScaleBlock + threadIdx.x / kLanes;
     after_previous();
     Raw<T> raw[kEach];
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        const int64_t row = row0 + i * (kThreads / kLanes);
+        const int64_t row = row0 + i * (kBlockThreads / kLanes);
         raw[i].clear();
         if (row < o.rows && col < o.dim)
             raw[i].load(x + row * x_stride + col);
@@ -206,27 +261,34 @@ template <typename T> __global__ void __launch_bounds__(kThreads) block_kernel(c
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
-        m = max(m, largest(raw[i].values()));
+        m = max(m, raw[i].most_of());
+    const bool finite = !__syncthreads_or(m >= kInfinity);
+    if (!finite) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            m = max(m, most_finite(raw[i].values()));
+    }
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0)
-        most[threadIdx.x / 32] = m;
+        found[threadIdx.x / 32] = m;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i)
-        m = max(m, most[i]);
+    for (int i = 0; i < kBlockThreads / 32; ++i)
+        m = max(m, found[i]);
     const uint32_t byte = exponent_byte(m, o.code);
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        const int64_t row = row0 + i * (kThreads / kLanes);
+        const int64_t row = row0 + i * (kBlockThreads / kLanes);
         if (row < o.rows && col < o.dim)
-            *(uint2 *)(o.codes + row * o.stride + col) = encode(raw[i].values(), byte, o.code);
+            *(uint2 *)(o.codes + row * o.stride + col) = encode(raw[i].values(), byte, o.code, finite);
     }
     if (threadIdx.x == 0)
         o.scale[(int64_t)blockIdx.y * o.scale_stride + blockIdx.x] = (uint8_t)byte;
 }
 
 // ---------------------------------------------------------------------------
-// Residual, norm, codes: a CTA a row, which stays in registers
+// Residual, norm, codes: a CTA a row, or a warp for up to 1,024 elements, which stays in registers
 // ---------------------------------------------------------------------------
 struct NormArgs {
     const void *x, *residual, *weight;
@@ -238,19 +300,24 @@ struct NormArgs {
 
 struct None {};  // no residual
 
-template <typename T, typename R, int EACH> __global__ void __launch_bounds__(1024 / (EACH > 2 ? 2 : 1))
+// EACH: chunks of eight to a thread.  WARP: eight rows to a CTA, so that short ones do not each cost a CTA's start
+// (16,376 of 512 elements: 17.4 us with a CTA each, 9.9 so).
+template <typename T, typename R, int EACH, bool WARP = false> __global__ void __launch_bounds__(WARP ? kThreads : 512)
 norm_kernel(const NormArgs a, const Out o)
 {
     constexpr bool kResidual = !std::is_same<R, None>::value;
     using S = typename std::conditional<kResidual, R, float>::type;
     __shared__ float part[32];
-    const int64_t row = blockIdx.x;
+    const int threads = WARP ? 32 : blockDim.x, mine = WARP ? threadIdx.x & 31 : threadIdx.x;  // of the row
+    const int64_t row = WARP ? (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32 : blockIdx.x;
     after_previous();
+    if (WARP && row >= o.rows)
+        return;
     Raw<T> x[EACH];
     Raw<S> r[EACH];
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
-        const int col = (i * blockDim.x + threadIdx.x) * 8;
+        const int col = (i * threads + mine) * 8;
         x[i].clear();
         r[i].clear();
         if (col < o.dim) {
@@ -260,27 +327,28 @@ norm_kernel(const NormArgs a, const Out o)
         }
     }
     Eight h[EACH];
-    float squares = 0.0f;
+    float2 two = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
-        const int col = (i * blockDim.x + threadIdx.x) * 8;
+        const int col = (i * threads + mine) * 8;
         h[i] = x[i].values();
         if (kResidual) {
             const Eight more = r[i].values();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                h[i].v[j] += more.v[j];
+            for (int j = 0; j < 4; ++j)
+                h[i].v[j] = add2(h[i].v[j], more.v[j]);
             if (col < o.dim)
                 store((S *)a.sum + row * a.sum_stride + col, h[i]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            squares = fmaf(h[i].v[j], h[i].v[j], squares);
+        for (int j = 0; j < 4; ++j)
+            two = fma2(h[i].v[j], h[i].v[j], two);
     }
+    float squares = two.x + two.y;
 #pragma unroll
     for (int k = 16; k; k >>= 1)
         squares += __shfl_xor_sync(0xffffffffu, squares, k);
-    if (blockDim.x > 32) {
+    if (!WARP) {
         if ((threadIdx.x & 31) == 0)
             part[threadIdx.x / 32] = squares;
         __syncthreads();
@@ -292,8 +360,8 @@ norm_kernel(const NormArgs a, const Out o)
     const float factor = __frsqrt_rn(__fdiv_rn(squares, (float)o.dim) + a.eps);
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
-        const int slot = i * blockDim.x + threadIdx.x, col = slot * 8;
-        Eight w{1, 1, 1, 1, 1, 1, 1, 1};
+        const int slot = i * threads + mine, col = slot * 8;
+        Eight w{{{1, 1}, {1, 1}, {1, 1}, {1, 1}}};
         if (a.weight && col < o.dim) {
             if (a.weight_bf16) {
                 Raw<__nv_bfloat16> raw;
@@ -306,12 +374,13 @@ norm_kernel(const NormArgs a, const Out o)
             }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            h[i].v[j] = h[i].v[j] * factor * w.v[j];
-        const uint32_t byte = exponent_byte(of_block(largest(h[i])), o.code);
+        for (int j = 0; j < 4; ++j)
+            h[i].v[j] = mul2(mul2(h[i].v[j], {factor, factor}), w.v[j]);
+        bool finite;
+        const uint32_t byte = block_byte(most(h[i]), h[i], o.code, &finite);
         if (col < o.dim) {
-            *(uint2 *)(o.codes + row * o.stride + col) = encode(h[i], byte, o.code);
-            if ((threadIdx.x & (kLanes - 1)) == 0)
+            *(uint2 *)(o.codes + row * o.stride + col) = encode(h[i], byte, o.code, finite);
+            if ((mine & (kLanes - 1)) == 0)
                 o.scale[row * o.scale_stride + slot / kLanes] = (uint8_t)byte;
         }
     }
@@ -326,7 +395,7 @@ template <typename T, typename F> spec_status launch_code(const Inputs &in, cons
 {
     const int slots = scale_blocks(out->dim) * kLanes;
     const int64_t all = (int64_t)out->rows * slots, each = kThreads * kUnroll, ctas = (all + each - 1) / each;
-    if (ctas > INT_MAX)
+    if (all / kLanes > INT_MAX)
         return SPEC_ERR_UNSUPPORTED;
     const uint32_t per = (uint32_t)(((1ull << 32) + slots - 1) / slots);
     return launch(code_kernel<T, F>, dim3((unsigned)ctas), kThreads, 0, 1, stream, in, make_out(out), slots, per);
@@ -337,10 +406,15 @@ template <typename T, typename R> spec_status launch_norm(const NormArgs &a, con
     const int slots = scale_blocks(out->dim) * kLanes;
     const Out o = make_out(out);
     const dim3 rows((unsigned)out->rows);
-    const auto threads = [&](int each) { return ((slots + each - 1) / each + 31) / 32 * 32; };
+    const dim3 few((unsigned)((out->rows + kThreads / 32 - 1) / (kThreads / 32)));
+    if (slots <= 32)
+        return launch(norm_kernel<T, R, 1, true>, few, kThreads, 0, 1, stream, a, o);
+    if (slots <= 64)
+        return launch(norm_kernel<T, R, 2, true>, few, kThreads, 0, 1, stream, a, o);
     if (slots <= 128)
-        return launch(norm_kernel<T, R, 1>, rows, threads(1), 0, 1, stream, a, o);
-    if (slots <= 256)
+        return launch(norm_kernel<T, R, 4, true>, few, kThreads, 0, 1, stream, a, o);
+    const auto threads = [&](int each) { return ((slots + each - 1) / each + 31) / 32 * 32; };
+    if (slots <= 512)
         return launch(norm_kernel<T, R, 2>, rows, threads(2), 0, 1, stream, a, o);
     if (slots <= 2048)
         return launch(norm_kernel<T, R, 4>, rows, threads(4), 0, 1, stream, a, o);
@@ -380,8 +454,8 @@ spec_status spec_rows_quantise(const void *x, int64_t x_stride, spec_dtype dtype
     if (down > 65535)
         return SPEC_ERR_UNSUPPORTED;
     const dim3 grid(scale_blocks(out->dim), (unsigned)down);
-    return dtype == SPEC_BF16 ? launch(block_kernel<__nv_bfloat16>, grid, kThreads, 0, 1, s, (const __nv_bfloat16 *)x, x_stride, make_out(out))
-                              : launch(block_kernel<float>, grid, kThreads, 0, 1, s, (const float *)x, x_stride, make_out(out));
+    return dtype == SPEC_BF16 ? launch(block_kernel<__nv_bfloat16>, grid, kBlockThreads, 0, 1, s, (const __nv_bfloat16 *)x, x_stride, make_out(out))
+                              : launch(block_kernel<float>, grid, kBlockThreads, 0, 1, s, (const float *)x, x_stride, make_out(out));
 }
 
 spec_status spec_rows_norm(const void *x, int64_t x_stride, spec_dtype dtype, const void *residual,
