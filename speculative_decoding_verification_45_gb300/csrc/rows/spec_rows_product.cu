@@ -62,7 +62,7 @@ struct Args {
     int row_tiles, out_tiles, group;
     int stages;
     uint32_t stage_bytes, b_bytes;
-    uint32_t idesc;          // without the scales' bytes
+    uint32_t idesc;          // without the scales' bytes and the rows
     int splits, wide_out;    // wide_out: fp32
     int tma_out;             // bf16 rows at multiples of 16 bytes
     int wait_limit;
@@ -253,6 +253,9 @@ __device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, 
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 
+// Activations' rows that the products of a tile take: all of it, or as many as the last one has, in units of 16.
+__device__ __forceinline__ int rows_of(const Args &a, const Tile &t) { return max(min(a.tile, (a.rows - t.row * a.tile + 15) & ~15), 32); }
+
 // Four neighbouring outputs of a row, together where the row lets them.
 __device__ __forceinline__ void put4(const Args &a, int64_t row, int n, const float4 &v)
 {
@@ -342,7 +345,7 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         bool free = true;
         for (int u = (int)cluster_index(); u < units; u += step) {
             const Tile t = tile_of(a, u);
-            const int n0 = t.out * kTileM + (int)side * kRowsM, r0 = t.row * a.tile + (int)side * (a.tile / 2);
+            const int n0 = t.out * kTileM + (int)side * kRowsM, r0 = t.row * a.tile + (int)side * (rows_of(a, t) / 2);
             for (int b = k0; b < k1; b += kDepth, ++issued) {
                 if (!__all_sync(0xffffffffu, free) && !wait(&empty[ring.at], ring.parity ^ 1, &guard))
                     goto out;
@@ -375,7 +378,7 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         const uint32_t base = smem_u32(stage0);
         bool here = false, scaled = false;
         for (int u = (int)cluster_index(); u < units; u += step, ++done) {
-            const uint32_t buf = (done & 1), acc = tmem + buf * a.tile;
+            const uint32_t buf = (done & 1), acc = tmem + buf * a.tile, n_bits = (uint32_t)rows_of(a, tile_of(a, u)) >> 3 << 17;
             if (!wait(&acc_empty[buf], (done >> 1 & 1) ^ 1, &guard))
                 goto out;
             for (int b = k0; b < k1; b += kDepth) {
@@ -404,7 +407,7 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
                             // K-major, 128-byte rows in groups of eight; 32 elements further on are 32 bytes
                             const uint64_t da = smem_desc(at + i * kABytes, 16, 1024, 2),
                                            db = smem_desc(at + kDepth * kABytes + i * a.b_bytes, 16, 1024, 2);
-                            const uint32_t id = a.idesc | (uint32_t)(k & 3) << 4 | (uint32_t)(k & 3) << 29;
+                            const uint32_t id = a.idesc | n_bits | (uint32_t)(k & 3) << 4 | (uint32_t)(k & 3) << 29;
                             const uint32_t sa = scales + g * kScaleColumns;
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
@@ -805,8 +808,9 @@ extern "C" spec_status spec_rows_product(const spec_coded *rows, const spec_code
     a.stage_bytes = kDepth * (kABytes + a.b_bytes);
     a.tma_out = dtype == SPEC_BF16 && p.splits == 1 && ((uintptr_t)out & 15u) == 0 && (out_stride * 2 & 15) == 0;
     a.stages = (int)std::min<uint32_t>(kMaxStages, (kShared - 1024 - (a.tma_out ? kOutBytes : 0)) / a.stage_bytes);
-    // as in the unscaled kinds, and: bytes of the scales at bits 4 and 29 (set for each block), scales of powers of two (bit 23)
-    a.idesc = (uint32_t)(weight->code == SPEC_E5M2) << 7 | (uint32_t)(rows->code == SPEC_E5M2) << 10 | (uint32_t)(p.tile >> 3) << 17 |
+    // as in the unscaled kinds, and: bytes of the scales at bits 4 and 29 (set for each block, as the rows at bit 17 are for each tile), scales of powers of
+    // two (bit 23)
+    a.idesc = (uint32_t)(weight->code == SPEC_E5M2) << 7 | (uint32_t)(rows->code == SPEC_E5M2) << 10 |
               1u << 23 | (uint32_t)(2 * kRowsM >> 7) << 27;
     a.wide_out = dtype == SPEC_F32;
     a.wait_limit = wait_limit();

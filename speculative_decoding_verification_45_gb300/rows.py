@@ -109,7 +109,7 @@ def _matrix(t, name, index, types):
 
 
 def _elsewhere(t, name, index):
-    if not t.is_cuda:
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     raise ValueError(f"{name} lives on {t.device}, but the current device is cuda:{index}: call under "
                      f"torch.cuda.device({t.get_device()})")

@@ -80,3 +80,121 @@ def test_gate(sv, rows, dim, dtype, code, act):
     # the exponential is off by 2^-21 and its argument, in units of log 2 and through up to four roundings, by 2^-22 of
     # it; the sum, the division (2 units) and the product by 2^-22
     ref.check_coded(coded, y, code, 2.0 ** -20 + z.abs() * 2.0 ** -22)
+
+
+def test_what_is_not_finite(sv):
+    """Infinities and NaN become NaN and enter no scale, whether alone in a block or with others."""
+    x = rand(260, 400, 20, F32)
+    x[3, 5], x[3, 200], x[77, 390] = float("inf"), float("nan"), -float("inf")
+    x[100, 128:256] = float("nan")
+    x[200, :128] = float("inf")
+    for dtype in (F32, BF16):
+        for call, block in ((sv.rows_quantise, 1), (sv.weight_quantise, 128)):
+            y = x.to(dtype)
+            got = call(y.cuda())
+            codes, scale = ref.quantise(y.double(), E4, block)
+            assert torch.equal(ref.scale_values(got.scale), scale)
+            assert torch.equal(got.codes.cpu().double().nan_to_num(nan=1e9), codes.nan_to_num(nan=1e9))
+    one = torch.ones_like(x)
+    for coded in (sv.rows_gate(x.cuda(), one.cuda()), sv.rows_gate(one.cuda(), x.cuda())):
+        assert torch.equal(coded.codes.float().isnan().cpu(), ~x.isfinite())
+    # a row with an infinity or a NaN: zeros and NaN, or NaN alone; other rows are as ever
+    coded, _ = sv.rows_norm(x.cuda())
+    rows = x.isfinite().all(1)
+    y, _ = ref.norm(x[rows], None, None, 1e-6)
+    some = [t.cpu().view(torch.uint8)[rows].view(t.dtype) for t in coded]
+    ref.check_coded(sv.Coded(*some), y, E4, NORM_SLACK)
+    bad = coded.codes.float().cpu()[~rows]
+    assert (bad.isnan() | (bad == 0)).all() and bad.isnan().any(1).all()
+
+
+def test_zeros_and_the_smallest(sv):
+    x = torch.zeros(4, 256)
+    x[1, 3], x[2, 130], x[3] = 1e-40, 2.0 ** -120, 2.0 ** -110
+    for coded in (sv.rows_quantise(x.cuda()), sv.rows_norm(torch.zeros(4, 256).cuda())[0]):
+        assert not coded.codes.float().isnan().any()
+    got = sv.rows_quantise(x.cuda())
+    codes, scale = ref.quantise(x.double(), E4)
+    assert torch.equal(ref.scale_values(got.scale), scale) and torch.equal(got.codes.cpu().double(), codes)
+
+
+def test_borders_of_scales_and_codes(sv):
+    """448 and 57344 times powers of two, the next number up, and the middles between codes."""
+    for code, top in ((E4, 448.0), (E5, 57344.0)):
+        x = torch.zeros(64, 128)
+        for i in range(32):
+            x[2 * i, 0] = top * 2.0 ** (i - 16)
+            x[2 * i + 1, 0] = torch.nextafter(x[2 * i, 0], torch.tensor(1e9))
+        steps = torch.arange(127) * 2.0 ** -10
+        x[:, 1:] = x[:, :1] * steps
+        got = sv.rows_quantise(x.cuda(), code=code)
+        codes, scale = ref.quantise(x.double(), code)
+        assert torch.equal(ref.scale_values(got.scale), scale) and torch.equal(got.codes.cpu().double(), codes)
+
+
+def test_slices_and_leading_dimensions(sv):
+    """Halves of one tensor, every other row, rows broadcast to many: as their dense copies."""
+    both = rand(12, 2 * 288, 21).cuda()
+    g, u = both[:, :288], both[:, 288:]
+    a, b = sv.rows_gate(g, u), sv.rows_gate(g.contiguous(), u.contiguous())
+    assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+    x = both[::2, :288]
+    assert torch.equal(sv.rows_quantise(x).codes.view(torch.uint8), sv.rows_quantise(x.contiguous()).codes.view(torch.uint8))
+    three = both.view(3, 4, 576)[..., :288]
+    c = sv.rows_quantise(three)
+    assert c.codes.shape == (3, 4, 288) and c.scale.shape == (3, 4, 3)
+    assert torch.equal(c.codes.view(torch.uint8).view(12, 288), sv.rows_quantise(g).codes.view(torch.uint8))
+    r = both[:1, :288].expand(12, 288)
+    one, s1 = sv.rows_norm(g, residual=r)
+    two, s2 = sv.rows_norm(g, residual=r.contiguous())
+    assert torch.equal(s1, s2) and torch.equal(one.codes.view(torch.uint8), two.codes.view(torch.uint8))
+    row = sv.rows_quantise(both[0, :288])
+    assert row.codes.shape == (288,) and row.scale.shape == (3,) and torch.equal(row.codes.view(torch.uint8), c.codes.view(torch.uint8)[0, 0])
+
+
+def test_the_sum_in_place(sv):
+    x, r = rand(33, 2048, 22).cuda(), rand(33, 2048, 23, F32).cuda()
+    want, total = sv.rows_norm(x, residual=r)
+    kept = r.clone()
+    got, back = sv.rows_norm(x, residual=kept, out_sum=kept)
+    assert back is kept and torch.equal(kept, total) and torch.equal(got.codes.view(torch.uint8), want.codes.view(torch.uint8))
+
+
+def guarded(shape, dtype):
+    n = 1
+    for s in shape:
+        n *= s
+    whole = torch.full((n + 2048,), 77, dtype=torch.uint8, device="cuda")
+    return whole[1024:1024 + n].view(dtype).view(shape), whole
+
+
+@pytest.mark.parametrize("rows,dim", [(1, 16), (7, 144), (130, 1040)])
+def test_nothing_else_is_written(sv, rows, dim):
+    x = rand(rows, dim, 24).cuda()
+    for call, above in ((lambda o: sv.rows_quantise(x, out=o), rows), (lambda o: sv.weight_quantise(x, out=o), ref.blocks(rows)),
+                        (lambda o: sv.rows_norm(x, out=o), rows), (lambda o: sv.rows_gate(x, x, out=o), rows)):
+        (c, whole_c), (s, whole_s) = guarded((rows, dim), E4), guarded((above, ref.blocks(dim)), torch.float8_e8m0fnu)
+        call(sv.Coded(c, s))
+        for whole in (whole_c, whole_s):
+            assert (whole[:1024] == 77).all() and (whole[-1024:] == 77).all()
+    assert sv.rows_quantise(x[:0]).codes.shape == (0, dim) and sv.rows_norm(x[:0], residual=x[:0])[1].shape == (0, dim)
+
+
+def test_elements_past_32_bits(sv):
+    """More than 2^32 elements: the last rows are where they belong."""
+    x = torch.zeros(131100, 32768, dtype=BF16, device="cuda")
+    last = rand(40, 32768, 25)
+    x[-40:] = last.cuda()
+    codes, scale = ref.quantise(last.double(), E4)
+    got = sv.rows_quantise(x)
+    assert torch.equal(got.codes[-40:].cpu().double(), codes) and torch.equal(ref.scale_values(got.scale[-40:]), scale)
+    got = sv.rows_gate(x, x)
+    assert torch.equal(got.codes[-40:].view(torch.uint8), sv.rows_gate(last.cuda(), last.cuda()).codes.view(torch.uint8))
+    got, total = sv.rows_norm(x, residual=x)
+    want, _ = sv.rows_norm(last.cuda(), residual=last.cuda())
+    assert torch.equal(got.codes[-40:].view(torch.uint8), want.codes.view(torch.uint8)) and torch.equal(total[-40:].cpu(), last * 2)
+    del total
+    got = sv.weight_quantise(x)
+    tail = 131100 - 131100 // 128 * 128
+    codes, scale = ref.quantise(last[-tail:].double(), E4, 128)
+    assert torch.equal(got.codes[-tail:].cpu().double(), codes) and torch.equal(ref.scale_values(got.scale[-1:]), scale)
