@@ -11,6 +11,11 @@ to ``keep`` tokens (cache_evict).  Rejected drafts leave the cache by length
 alone: the next append writes over them.  Weights are added after the accept
 test, from the accepted tokens' queries only: what a rejected draft looked at
 must not count, and its own slot must hold no weight when another token takes it.
+
+With ``--eight-bit`` the target is a whole layer whose projections run in 8 bits:
+norm, q, k and v in one product (rows_norm, rows_product), the attention's output
+(rows_quantise), residual and norm, a gated feed-forward layer (rows_gate), and the
+logits.
 """
 from __future__ import annotations
 
@@ -26,7 +31,7 @@ class Decoder:
     """Weights, cache and state of a batch; ``step`` runs one round."""
 
     def __init__(self, batch=4, vocab=512, heads=8, kv_heads=2, dim=64, block=16, limit=192, keep=96, recent=32, gamma=4,
-                 room=1024, seed=0, device="cuda"):
+                 room=1024, seed=0, device="cuda", eight_bit=False):
         g = torch.Generator(device=device).manual_seed(seed)
 
         def rand(*shape, scale=1.0):
@@ -54,21 +59,54 @@ class Decoder:
         self.text_len = torch.full((batch,), 2, dtype=torch.int32, device=device)
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self.evictions = 0
+        self.eight_bit = eight_bit
+        if eight_bit:
+            self.inner = 4 * width
+
+            def weight(outs, ins):
+                return sv.weight_quantise(rand(outs, ins, scale=1 / math.sqrt(ins)))
+
+            # q, k and v side by side, and gate and up: one product each
+            self.qkv = sv.weight_quantise(torch.cat([self.wq, self.wkv], 1).t().contiguous())
+            self.wo, self.gate_up, self.down = weight(width, width), weight(2 * self.inner, width), weight(width, self.inner)
+            self.head = sv.weight_quantise(self.embed)
+            self.norms = [torch.ones(width, device=device) for _ in range(3)]
+
+    def _project(self, x):
+        """q [batch, n, heads, dim] and k, v [batch, n, 2, kv heads, dim] of the embedded tokens."""
+        if self.eight_bit:
+            rows, _ = sv.rows_norm(x, self.norms[0])
+            both = sv.rows_product(rows, self.qkv, status=self.status)
+            width = self.heads * self.dim
+            return both[..., :width].unflatten(-1, (self.heads, self.dim)), both[..., width:].unflatten(-1, (2, self.kv_heads, self.dim))
+        return ((x @ self.wq).unflatten(-1, (self.heads, self.dim)),
+                (x @ self.wkv).unflatten(-1, (2, self.kv_heads, self.dim)))
+
+    def _logits(self, x, out):
+        """Logits [batch, n, vocab] from the embedded tokens and what attention gave them."""
+        if not self.eight_bit:
+            return (x + out) @ self.embed.t()
+        delta = sv.rows_product(sv.rows_quantise(out), self.wo, status=self.status)
+        rows, x = sv.rows_norm(delta, self.norms[1], residual=x)
+        both = sv.rows_product(rows, self.gate_up, status=self.status)
+        rows = sv.rows_gate(both[..., :self.inner], both[..., self.inner:])
+        delta = sv.rows_product(rows, self.down, status=self.status)
+        rows, _ = sv.rows_norm(delta, self.norms[2], residual=x)
+        return sv.rows_product(rows, self.head, status=self.status)
 
     def forward(self, tokens, num_new, positions):
         """Logits [batch, n, vocab] of the newest tokens; their keys and values enter the cache.  What `weigh` needs of
         them is kept until the next forward."""
         batch, n = tokens.shape
         x = self.embed[tokens.long()]
-        q = (x @ self.wq).view(batch, n, self.heads, self.dim)
-        kv = (x @ self.wkv).view(batch, n, 2, self.kv_heads, self.dim)
+        q, kv = self._project(x)
         sv.cache_append(self.cache, self.table, self.lengths, kv[:, :, 0], kv[:, :, 1], num_new=num_new,
                         positions=positions, status=self.status)
         lengths = self.lengths + num_new
         out, lse = sv.cache_attend(q, self.cache, self.table, lengths, num_new=num_new, slopes=self.slopes,
                                    status=self.status)
         self.asked = q, lse
-        return (x + out.view(batch, n, -1)) @ self.embed.t()
+        return self._logits(x, out.view(batch, n, -1))
 
     def weigh(self, num_new):
         """Weights from the first num_new queries of the last forward; `lengths` counts their tokens already."""
@@ -108,8 +146,9 @@ def main(argv=None):
     p = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     p.add_argument("--rounds", type=int, default=200)
     p.add_argument("--batch", type=int, default=4)
+    p.add_argument("--eight-bit", action="store_true", help="a whole layer whose projections run in 8 bits")
     a = p.parse_args(argv)
-    d = Decoder(batch=a.batch)
+    d = Decoder(batch=a.batch, eight_bit=a.eight_bit)
     total = torch.zeros(a.batch, dtype=torch.int64, device="cuda")
     for _ in range(a.rounds):
         total += d.step()[1]
