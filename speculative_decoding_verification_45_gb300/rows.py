@@ -251,26 +251,29 @@ def rows_gate(gate, up, act="silu", code=torch.float8_e4m3fn, out=None, stream=N
     return out
 
 
-def _coded_in(coded, name, index, weight):
+_ROWS, _WEIGHT = ("rows.codes", "rows.scale"), ("weight.codes", "weight.scale")
+
+
+def _coded_in(coded, names, index, weight):
     """The spec_coded of codes and scales that a product reads; its rows and width."""
     codes, scale = coded
-    at, rows, dim, step, form = _matrix(codes, f"{name}.codes", index, _CODES)
-    if dim % 16:
-        raise ValueError(f"{name}.codes: the last dimension must be a multiple of 16, got {dim}")
+    at, rows, dim, step, form = _matrix(codes, names[0], index, _CODES)
+    if dim & 15:
+        raise ValueError(f"{names[0]}: the last dimension must be a multiple of 16, got {dim}")
     if weight and codes.dim() != 2:
-        raise ValueError(f"{name}.codes must be an [outputs, width] tensor")
+        raise ValueError(f"{names[0]} must be an [outputs, width] tensor")
     blocks = (dim + 127) // 128
     if scale.dtype is not SCALE:
-        raise TypeError(f"{name}.scale: expected {SCALE}, got {scale.dtype}")
+        raise TypeError(f"{names[1]}: expected {SCALE}, got {scale.dtype}")
     if scale.get_device() != index:
-        _elsewhere(scale, f"{name}.scale", index)
+        _elsewhere(scale, names[1], index)
     above = ((rows + 127) // 128, blocks) if weight else (*codes.shape[:-1], blocks)
     if scale.shape != above:
-        raise ValueError(f"{name}.scale: expected shape {above}, got {tuple(scale.shape)}")
-    scale_step = blocks if scale.is_contiguous() else _step(scale, f"{name}.scale")
+        raise ValueError(f"{names[1]}: expected shape {above}, got {tuple(scale.shape)}")
+    scale_step = blocks if scale.is_contiguous() else _step(scale, names[1])
     if step < dim or scale_step < blocks:
         if rows > 1 and (step < dim or scale.numel() > blocks):
-            raise ValueError(f"{name}: rows must not overlap")
+            raise ValueError(f"{names[0]}: rows must not overlap")
         step, scale_step = max(step, dim), max(scale_step, blocks)
     return _byref(_Struct(at, scale.data_ptr(), step, scale_step, rows, dim, form)), rows, dim
 
@@ -284,8 +287,8 @@ def rows_product(rows, weight, dtype=torch.bfloat16, out=None, status=None, stre
     out     to write into, rows at any one stride (then ``dtype`` is its type)
     """
     index = _index(rows[0], "rows.codes")
-    r, count, dim = _coded_in(rows, "rows", index, False)
-    w, outs, width = _coded_in(weight, "weight", index, True)
+    r, count, dim = _coded_in(rows, _ROWS, index, False)
+    w, outs, width = _coded_in(weight, _WEIGHT, index, True)
     if dim != width:
         raise ValueError(f"rows are {dim} wide, weight {width}")
     shape = (*rows[0].shape[:-1], outs)
