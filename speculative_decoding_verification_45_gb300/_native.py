@@ -2,9 +2,11 @@
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 import threading
 from concurrent.futures import ThreadPoolExecutor
 
@@ -23,8 +25,11 @@ SOURCES = ([os.path.join(CSRC, f) for f in ("spec_verify.cu", "kernels_bf16.cu",
 HEADERS = [os.path.join(INCLUDE, "spec_verify.h"), os.path.join(CSRC, "spec_verify_kernels.cuh"),
            os.path.join(CSRC, "spec_ptx.cuh"), os.path.join(CACHE, "spec_cache.cuh"),
            os.path.join(CACHE, "spec_cache_attend.cuh"), os.path.join(ROWS, "spec_rows.cuh")]
+# The binding's common calls of 8-bit rows, in C: an extension module of this interpreter.
+PY_SOURCE = os.path.join(ROWS, "spec_rows_py.c")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libspec_verify.so")
+PY_PATH = os.path.join(BUILD_DIR, "spec_rows_py" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 _lock = threading.Lock()
@@ -70,22 +75,22 @@ def nvcc_path() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(PY_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(f) > t for f in SOURCES + HEADERS)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(PY_PATH))
+    return any(os.path.getmtime(f) > t for f in SOURCES + HEADERS + [PY_SOURCE])
 
 
 def _run(cmd):
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({res.returncode}):\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     return res.stdout + res.stderr
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the units of csrc for sm_103a (one nvcc per unit, in parallel) and link
-    _build/libspec_verify.so."""
+    """Compile the units of csrc for sm_103a (one nvcc per unit, in parallel), link
+    _build/libspec_verify.so, and compile the binding's extension module beside it."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     if not force and not _stale():
         return LIB_PATH
@@ -93,7 +98,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     objs = [os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + f".{tag}.o") for src in SOURCES]
     cmds = [[nvcc, "-O3", "-std=c++17", *ARCH_FLAGS, "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE,
              *(["-Xptxas=-v"] if verbose else []), "-c", "-o", obj, src] for src, obj in zip(SOURCES, objs)]
-    tmp = LIB_PATH + f".{tag}"
+    tmp, py_tmp = LIB_PATH + f".{tag}", PY_PATH + f".{tag}"
+    cmds.append([shutil.which("gcc") or "cc", "-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+                 "-o", py_tmp, PY_SOURCE])
     try:
         with ThreadPoolExecutor(max_workers=len(cmds)) as pool:
             logs = list(pool.map(_run, cmds))
@@ -105,7 +112,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print("".join(logs))
     os.replace(tmp, LIB_PATH)
+    os.replace(py_tmp, PY_PATH)
     return LIB_PATH
+
+
+def load_extension():
+    """The binding's extension module; raises if it has not been built."""
+    if not os.path.exists(PY_PATH):
+        raise RuntimeError(f"{PY_PATH} is missing: run __graft_entry__.build() (or "
+                           "speculative_decoding_verification_45_gb300._native.build()) first")
+    spec = importlib.util.spec_from_file_location("spec_rows_py", PY_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
 def load() -> ctypes.CDLL:

@@ -45,6 +45,22 @@ def _stream(stream, index):
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
+class _Unloaded:
+    """Stands for the calls in C (csrc/rows/spec_rows_py.c) until the first of them: they do the usual case, and return None
+    for anything else, which the checks below then tell of."""
+
+    def __getattr__(self, name):
+        global _quick
+        lib, module = _native.load(), _native.load_extension()
+        address = [ctypes.cast(getattr(lib, f"spec_rows_{x}"), ctypes.c_void_p).value for x in ("quantise", "norm", "gate", "product")]
+        module.setup((torch.float32, torch.bfloat16, torch.float8_e4m3fn, torch.float8_e5m2, SCALE, torch.int32), Coded, _empty,
+                     torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, tuple(address))
+        _quick = module
+        return getattr(module, name)
+
+
+_quick = _Unloaded()
+
 # torch.empty costs 5 us a call beside launches here, and this form of it (the one that torch's compiled code calls) less
 # than 1: for one token it is half of a call's time.
 _empty = torch._C._dynamo.guards._empty_strided_cuda
@@ -153,6 +169,10 @@ def rows_quantise(x, code=torch.float8_e4m3fn, out=None, stream=None):
     bytes.  Returns Coded(codes [..., dim], scale [..., ceil(dim / 128)]); ``out``:
     such a Coded to write into.
     """
+    if out is None and stream is None:
+        made = _quick.quantise(x, code, 1)
+        if made is not None:
+            return made
     index = _index(x, "x")
     at, rows, dim, step, dtype = _matrix(x, "x", index, _FLOATS)
     out, c = _coded_out(out, x, x.shape, rows, dim, code, stream)
@@ -168,6 +188,10 @@ def weight_quantise(weight, code=torch.float8_e4m3fn, out=None, stream=None):
     Returns Coded(codes [outputs, width], scale [ceil(outputs / 128), ceil(width /
     128)]), which rows_product takes; done once, when weights are loaded.
     """
+    if out is None and stream is None:
+        made = _quick.quantise(weight, code, BLOCK)
+        if made is not None:
+            return made
     if weight.dim() != 2:
         raise ValueError("weight must be an [outputs, width] tensor")
     index = _index(weight, "weight")
@@ -189,6 +213,10 @@ def rows_norm(x, weight=None, residual=None, eps=1e-6, code=torch.float8_e4m3fn,
     weight       [dim] bfloat16 or float32, or None (1)
     out, out_sum to write into; out_sum may be ``residual`` itself
     """
+    if out is None and out_sum is None and stream is None:
+        made = _quick.norm(x, weight, residual, eps, code)
+        if made is not None:
+            return made
     index = _index(x, "x")
     at, rows, dim, step, dtype = _matrix(x, "x", index, _FLOATS)
     shape = x.shape
@@ -233,8 +261,12 @@ def rows_gate(gate, up, act="silu", code=torch.float8_e4m3fn, out=None, stream=N
     stride, so halves of one product's output need no copy.  ``act``: "silu" or
     "gelu_tanh".
     """
-    index = _index(gate, "gate")
     kind = _ACTS.get(act)
+    if out is None and stream is None and kind is not None:
+        made = _quick.gate(gate, up, kind, code)
+        if made is not None:
+            return made
+    index = _index(gate, "gate")
     if kind is None:
         raise ValueError(f"act must be 'silu' or 'gelu_tanh', got {act!r}")
     g_at, rows, dim, g_step, dtype = _matrix(gate, "gate", index, _FLOATS)
@@ -286,6 +318,10 @@ def rows_product(rows, weight, dtype=torch.bfloat16, out=None, status=None, stre
     dtype   of the result [..., outputs]: torch.bfloat16 or torch.float32; sums are 32-bit
     out     to write into, rows at any one stride (then ``dtype`` is its type)
     """
+    if out is None and stream is None:
+        made = _quick.product(rows, weight, dtype, status)
+        if made is not None:
+            return made
     index = _index(rows[0], "rows.codes")
     r, count, dim = _coded_in(rows, _ROWS, index, False)
     w, outs, width = _coded_in(weight, _WEIGHT, index, True)
