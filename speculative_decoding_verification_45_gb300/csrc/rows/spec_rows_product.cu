@@ -64,7 +64,7 @@ struct Args {
     uint32_t stage_bytes, b_bytes;
     uint32_t idesc;          // without the scales' bytes and the rows
     int splits, wide_out;    // wide_out: fp32
-    int tma_out;             // bf16 rows at multiples of 16 bytes
+    int boxes;               // outputs are written in boxes of 32 and 16 rows: 2 bf16, 4 fp32, 0 not
     int wait_limit;
     uint32_t *status;
 };
@@ -183,34 +183,49 @@ template <> __device__ __forceinline__ void tmem_store<8>(uint32_t a, const uint
                  : "memory");
 }
 
-// Exponent bytes of blocks 16 q to 16 q + 15 of a row, in one load where row and bytes allow; 1 behind the last block (no
-// instruction names those).
-__device__ __forceinline__ uint4 scale_words(const uint8_t *row, int q, int blocks, int aligned)
-{
-    uint32_t w[4];
-    const uint8_t *const p = row + 16 * q;
-    if (aligned == 16 && 16 * q + 16 <= blocks)
-        return __ldg((const uint4 *)p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int left = blocks - 16 * q - 4 * i;
-        w[i] = 0x7f7f7f7fu;
-        if (aligned >= 4 && left >= 4) {
-            w[i] = __ldg((const uint32_t *)(p + 4 * i));
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < left)
-                    w[i] = (w[i] & ~(0xffu << 8 * j)) | (uint32_t)__ldg(p + 4 * i + j) << 8 * j;
-        }
+// A matrix of exponent bytes, from its first to behind its last.
+struct Bytes {
+    const uint8_t *begin, *end;
+    bool aligned;  // rows at multiples of 16 bytes
+    __device__ __forceinline__ Bytes(const uint8_t *p, int64_t stride, int64_t rows, int blocks)
+        : begin(p), end(p + (rows - 1) * stride + blocks), aligned((((uint64_t)(uintptr_t)p | (uint64_t)stride) & 15) == 0)
+    {
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ int alignment_of(const uint8_t *p, int64_t stride)
-{
-    const uint64_t u = (uint64_t)(uintptr_t)p | (uint64_t)stride;
-    return (u & 15) == 0 ? 16 : (u & 3) == 0 ? 4 : 1;
-}
+    __device__ __forceinline__ uint32_t word(const uint8_t *p) const  // at a multiple of 4
+    {
+        if (p >= begin && p + 4 <= end)
+            return __ldg((const uint32_t *)p);
+        uint32_t w = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (p + i >= begin && p + i < end)
+                w |= (uint32_t)__ldg(p + i) << 8 * i;
+        return w;
+    }
+    // Blocks 16 q to 16 q + 15 of a row; behind the last block anything, which no instruction names.  Rows that begin
+    // anywhere are read by aligned words, which may take in bytes of the row before or behind (333 x 2,832 to 5,000:
+    // 12.9 us byte by byte, 12.3 so).
+    __device__ __forceinline__ uint4 blocks16(const uint8_t *row, int q, int blocks) const
+    {
+        const uint8_t *const p = row + 16 * q;
+        const int left = blocks - 16 * q;
+        if (aligned && left >= 16)
+            return __ldg((const uint4 *)p);
+        const int off = (int)((uintptr_t)p & 3);
+        if (off == 0 && left >= 16) {
+            const uint32_t *const q4 = (const uint32_t *)p;
+            return make_uint4(__ldg(q4), __ldg(q4 + 1), __ldg(q4 + 2), __ldg(q4 + 3));
+        }
+        uint32_t w[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+            w[i] = 4 * i < left + off ? word(p - off + 4 * i) : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = __funnelshift_r(w[i], w[i + 1], 8 * off);
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
 __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 // Unit u of the grid: `group` weight tiles beside each other share the activations' rows that pass through L2.
@@ -255,6 +270,94 @@ template <int N> __device__ __forceinline__ void store_wait_read() { asm volatil
 
 // Activations' rows that the products of a tile take: all of it, or as many as the last one has, in units of 16.
 __device__ __forceinline__ int rows_of(const Args &a, const Tile &t) { return max(min(a.tile, (a.rows - t.row * a.tile + 15) & ~15), 32); }
+
+__device__ __forceinline__ void store_shared(uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); }
+__device__ __forceinline__ uint32_t load_shared(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+// Outputs of one type on their way to rows at any address: `rows` of them are staged together, `pitch` bytes apart (16 more
+// than their values, so that eight rows lie in different banks).
+template <typename T> struct Staged {
+    static constexpr int rows = sizeof(T) == 2 ? 96 : 32;
+    static constexpr uint32_t pitch = sizeof(T) * kRowsM + 16;
+    static_assert(rows * pitch <= kOutBytes, "rows are staged in place of the boxes");
+};
+// Up to four rows of `width` outputs (128 at most) from shared memory to addresses that only their type aligns: a lane takes
+// four values that lie together at a multiple of four, and eight lanes to a row the values before and behind those.
+template <typename T> __device__ __forceinline__ void write_rows(T *to, int64_t stride, int count, int width, uint32_t from, int lane)
+{
+    constexpr int kWords = sizeof(T) == 2 ? 3 : 4;
+    constexpr uint32_t kPitch = Staged<T>::pitch;
+    const auto before = [](const T *p) { return (int)(-((uintptr_t)p / sizeof(T)) & 3); };
+    uint32_t w[4][kWords];
+    int first[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        first[j] = before(to + j * stride) + 4 * lane;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            w[j][i] = load_shared(from + j * kPitch + (first[j] * (uint32_t)sizeof(T) & ~3u) + 4 * i);
+    }
+    const int j = lane / 8, k = lane & 7;
+    T *const mine = to + j * stride;
+    const int off = min(before(mine), width), at = k < 4 ? k : off + ((width - off) & ~3) + (k & 3);
+    const uint32_t end = load_shared(from + j * kPitch + (at * (uint32_t)sizeof(T) & ~3u));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i < count && first[i] + 4 <= width) {
+            T *const p = to + i * stride + first[i];
+            if constexpr (sizeof(T) == 4)
+                *(uint4 *)p = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+            else if (first[i] & 1)
+                *(uint2 *)p = make_uint2(__funnelshift_r(w[i][0], w[i][1], 16), __funnelshift_r(w[i][1], w[i][2], 16));
+            else
+                *(uint2 *)p = make_uint2(w[i][0], w[i][1]);
+        }
+    }
+    if (j < count && at < (k < 4 ? off : width)) {
+        if constexpr (sizeof(T) == 4)
+            *(uint32_t *)(mine + at) = end;
+        else
+            *(uint16_t *)(mine + at) = (uint16_t)(at & 1 ? end >> 16 : end);
+    }
+}
+
+// 128 outputs of `used` rows by four warps, through shared memory at `at`: staged by all, then written a quarter each.
+// acc: the warp's lanes of the accumulator.
+template <typename T> __device__ __forceinline__ void write_tile(T *to, int64_t stride, int used, int width, uint32_t at, uint32_t acc, int warp, int lane)
+{
+    constexpr uint32_t kPitch = Staged<T>::pitch;
+    for (int p = 0; p < used; p += Staged<T>::rows) {
+        const int rows = min(Staged<T>::rows, used - p);
+        for (int c = 0; c < rows; c += 32) {
+            float v[32];
+            if constexpr (sizeof(T) == 2) {
+                tmem_load_pairs(acc + p + c, v);
+                tmem_load_pairs(acc + (16u << 16) + p + c, v + 16);
+                tmem_wait<32>(v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    store_transposed(at + (c + 8 * i + (lane & 7)) * kPitch + warp * 64 + lane / 8 * 16, pack(v[4 * i], v[4 * i + 1]),
+                                     pack(v[4 * i + 2], v[4 * i + 3]), pack(v[16 + 4 * i], v[17 + 4 * i]),
+                                     pack(v[18 + 4 * i], v[19 + 4 * i]));
+            } else {
+                TmemLoad<16>::go(acc + p + c, v);
+                TmemLoad<16>::go(acc + p + c + 16, v + 16);
+                tmem_wait<32>(v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    store_shared(at + (c + i) * kPitch + (warp * 32 + lane) * 4, v[i]);
+            }
+        }
+        named_barrier<128>(2);
+        for (int r = 4 * warp; r < rows && width > 0; r += 16)
+            write_rows<T>(to + (p + r) * stride, stride, rows - r, width, at + r * kPitch, lane);
+        named_barrier<128>(2);
+    }
+}
 
 // Four neighbouring outputs of a row, together where the row lets them.
 __device__ __forceinline__ void put4(const Args &a, int64_t row, int n, const float4 &v)
@@ -430,7 +533,8 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         // the four warps, which all store all rows (each for its 32 lanes, which the tensor cores read side by side).
         const int mine = threadIdx.x - kScaleWarp * 32;
         const uint32_t lanes = (uint32_t)(warp - kScaleWarp) << 21;  // 32 lanes of tensor memory each, at bit 16
-        const int row_aligned = alignment_of(a.row_scale, a.row_scale_stride), weight_aligned = alignment_of(a.weight_scale, a.weight_scale_stride);
+        const Bytes row_bytes(a.row_scale, a.row_scale_stride, a.rows, a.blocks),
+            weight_bytes(a.weight_scale, a.weight_scale_stride, (a.outs + kRowsM - 1) / kRowsM, a.blocks);
         const uint4 one4 = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
         uint32_t groups = 0;
         for (int u = (int)cluster_index(); u < units; u += step) {
@@ -442,9 +546,9 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
                                 *const p0 = a.row_scale + (r0 + mine) * a.row_scale_stride, *const p1 = p0 + 128 * a.row_scale_stride;
             uint4 w, s0, s1, next_w, next0, next1;
             const auto fetch = [&](int q) {
-                next_w = has ? scale_words(wp, q, a.blocks, weight_aligned) : one4;
-                next0 = has0 ? scale_words(p0, q, a.blocks, row_aligned) : one4;
-                next1 = has1 ? scale_words(p1, q, a.blocks, row_aligned) : one4;
+                next_w = has ? weight_bytes.blocks16(wp, q, a.blocks) : one4;
+                next0 = has0 ? row_bytes.blocks16(p0, q, a.blocks) : one4;
+                next1 = has1 ? row_bytes.blocks16(p1, q, a.blocks) : one4;
             };
             fetch(k0 >> 4);
             w = s0 = s1 = one4;
@@ -496,7 +600,7 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
             if (barrier_or<128>(2, !wait<true>(&acc_full[buf], done >> 1 & 1, &guard)))
                 goto out;
             tc_after();
-            if (a.tma_out) {
+            if (a.boxes == 2) {
                 // 32 outputs and up to 32 rows at a time, transposed on their way through shared memory; the next ones are
                 // on their way from tensor memory meanwhile, and up to kOutRing of them to global memory
                 const auto load = [&](int c, float *v) {
@@ -542,33 +646,51 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
                         load(c + 64, v);
                     write(c + 32, w);
                 }
-            } else {
+            } else if (a.boxes == 4) {
+                for (int c = 0; c < used; c += 32, ++chunks) {
+                    float v[32];
+                    TmemLoad<16>::go(acc + c, v);
+                    TmemLoad<16>::go(acc + c + 16, v + 16);
+                    const uint32_t at = chunk0 + (chunks & 1) * (2 * kChunkBytes);
+                    if (lane == 0)
+                        store_wait_read<1>();
+                    __syncwarp();
+                    tmem_wait<32>(v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        store_shared(at + i * 128 + lane * 4, v[i]);
+                    proxy_fence();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (n < a.outs) {
+                            tma_store(&omap, at, n, r0 + c);
+                            if (c + 16 < used)
+                                tma_store(&omap, at + kChunkBytes, n, r0 + c + 16);
+                        }
+                        store_commit();
+                    }
+                }
+            } else if (a.splits > 1) {
+                // the copies into the stages have all been used by now
                 for (int c = 0; c < used; c += 32) {
                     float v[32];
                     TmemLoad<16>::go(acc + c, v);
                     TmemLoad<16>::go(acc + c + 16, v + 16);
                     tmem_wait<32>(v);
-                    if (a.splits > 1) {
-                        // the copies into the stages have all been used by now
-                        float *const sums = (float *)stage0 + m;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            sums[(c + i) * kRowsM] = v[i];
-                    } else if (n < a.outs) {
-                        const int64_t first = (r0 + c) * a.out_stride + n;
-                        if (a.wide_out) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c + i < used)
-                                    ((float *)a.out)[first + i * a.out_stride] = v[i];
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (c + i < used)
-                                    ((__nv_bfloat16 *)a.out)[first + i * a.out_stride] = __float2bfloat16_rn(v[i]);
-                        }
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        ((float *)stage0)[(c + i) * kRowsM + m] = v[i];
                 }
+            } else {
+                // Rows at any address (bf16, 16,384 x 64 to 12,207: 307 us with single values from the registers, 244 so; 131
+                // in boxes)
+                const uint32_t at = smem_u32(stage0) + a.stages * a.stage_bytes;
+                const int64_t begin = r0 * a.out_stride + (n - m);
+                const int width = min(kRowsM, a.outs - (n - m));
+                if (a.wide_out)
+                    write_tile((float *)a.out + begin, a.out_stride, used, width, at, acc, warp, lane);
+                else
+                    write_tile((__nv_bfloat16 *)a.out + begin, a.out_stride, used, width, at, acc, warp, lane);
             }
             tc_before();
             __syncwarp();
@@ -737,24 +859,23 @@ spec_status this_device(const Device **out)
     return SPEC_OK;
 }
 
-// [element, row], rows `stride` bytes apart; a box is box_bytes (64 or 128, swizzled as wide) of box_rows rows.
-spec_status make_map(CUtensorMapDataType type, int element, int box_bytes, void *at, int64_t dim, int64_t rows, int64_t stride, int box_rows,
-                     CUtensorMap *map)
+// [element, row], rows `stride` bytes apart; a box is box_bytes of box_rows rows.
+spec_status make_map(CUtensorMapDataType type, int element, int box_bytes, CUtensorMapSwizzle swizzle, void *at, int64_t dim, int64_t rows,
+                     int64_t stride, int box_rows, CUtensorMap *map)
 {
     const EncodeTiled encode = encoder();
     if (!encode)
         return SPEC_ERR_CUDA;
     const cuuint64_t size[2] = {(cuuint64_t)dim, (cuuint64_t)rows}, step[1] = {(cuuint64_t)stride};
     const cuuint32_t box[2] = {(cuuint32_t)(box_bytes / element), (cuuint32_t)box_rows}, one[2] = {1, 1};
-    return encode(map, type, 2, at, size, step, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+    return encode(map, type, 2, at, size, step, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? SPEC_OK
                : SPEC_ERR_INVALID_ARG;
 }
 spec_status make_map(const spec_coded *c, int box_rows, CUtensorMap *map)
 {
-    return make_map(CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128, c->codes, c->dim, c->rows, c->stride, box_rows, map);
+    return make_map(CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, 128, CU_TENSOR_MAP_SWIZZLE_128B, c->codes, c->dim, c->rows, c->stride, box_rows, map);
 }
 
 }  // namespace
@@ -806,8 +927,8 @@ extern "C" spec_status spec_rows_product(const spec_coded *rows, const spec_code
         a.group = std::max(8, (int)std::min<int64_t>(a.out_tiles, (32 << 20) / ((int64_t)2 * kRowsM * kScaleBlock * a.blocks)));
     a.b_bytes = (uint32_t)(p.tile / 2) * kScaleBlock;  // a multiple of 1,024
     a.stage_bytes = kDepth * (kABytes + a.b_bytes);
-    a.tma_out = dtype == SPEC_BF16 && p.splits == 1 && ((uintptr_t)out & 15u) == 0 && (out_stride * 2 & 15) == 0;
-    a.stages = (int)std::min<uint32_t>(kMaxStages, (kShared - 1024 - (a.tma_out ? kOutBytes : 0)) / a.stage_bytes);
+    a.boxes = p.splits == 1 && ((uintptr_t)out & 15u) == 0 && (out_stride * size & 15) == 0 ? (int)size : 0;
+    a.stages = (int)std::min<uint32_t>(kMaxStages, (kShared - 1024 - (p.splits == 1 ? kOutBytes : 0)) / a.stage_bytes);
     // as in the unscaled kinds, and: bytes of the scales at bits 4 and 29 (set for each block, as the rows at bit 17 are for each tile), scales of powers of
     // two (bit 23)
     a.idesc = (uint32_t)(weight->code == SPEC_E5M2) << 7 | (uint32_t)(rows->code == SPEC_E5M2) << 10 |
@@ -817,7 +938,11 @@ extern "C" spec_status spec_rows_product(const spec_coded *rows, const spec_code
     a.status = status;
     CUtensorMap wmap, rmap, omap{};
     if ((st = make_map(weight, kRowsM, &wmap)) != SPEC_OK || (st = make_map(rows, p.tile / 2, &rmap)) != SPEC_OK ||
-        (a.tma_out && (st = make_map(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 64, out, a.outs, a.rows, out_stride * 2, 16, &omap)) != SPEC_OK))
+        (a.boxes &&
+         (st = dtype == SPEC_BF16
+                   ? make_map(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 64, CU_TENSOR_MAP_SWIZZLE_64B, out, a.outs, a.rows, out_stride * 2, 16, &omap)
+                   : make_map(CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, 128, CU_TENSOR_MAP_SWIZZLE_NONE, out, a.outs, a.rows, out_stride * 4, 16,
+                              &omap)) != SPEC_OK))
         return st;
     const int units = a.row_tiles * a.out_tiles;
     const dim3 grid((unsigned)(2 * p.splits * (p.splits == 1 ? std::min(units, device->sms / 2) : units)));
