@@ -23,7 +23,7 @@ SOURCES = ([os.path.join(CSRC, f) for f in ("spec_verify.cu", "kernels_bf16.cu",
                                                "spec_cache_attend_d64.cu", "spec_cache_attend_d128.cu")]
            + [os.path.join(ROWS, f) for f in ("spec_rows_code.cu", "spec_rows_product.cu")])
 HEADERS = [os.path.join(INCLUDE, "spec_verify.h"), os.path.join(CSRC, "spec_verify_kernels.cuh"),
-           os.path.join(CSRC, "spec_ptx.cuh"), os.path.join(CACHE, "spec_cache.cuh"),
+           os.path.join(CACHE, "spec_ptx.cuh"), os.path.join(CACHE, "spec_cache.cuh"),
            os.path.join(CACHE, "spec_cache_attend.cuh"), os.path.join(ROWS, "spec_rows.cuh")]
 # The binding's common calls of 8-bit rows, in C: an extension module of this interpreter.
 PY_SOURCE = os.path.join(ROWS, "spec_rows_py.c")

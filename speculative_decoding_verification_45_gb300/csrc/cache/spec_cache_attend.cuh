@@ -38,7 +38,7 @@
 #include <type_traits>
 
 #include "spec_cache.cuh"
-#include "../spec_ptx.cuh"
+#include "spec_ptx.cuh"
 
 namespace specc {
 

@@ -12,7 +12,7 @@
 
 #include <type_traits>
 
-#include "../spec_ptx.cuh"
+#include "../cache/spec_ptx.cuh"
 #include "spec_rows.cuh"
 
 using namespace specc;

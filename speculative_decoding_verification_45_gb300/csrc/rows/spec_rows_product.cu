@@ -31,7 +31,7 @@
 #include <atomic>
 #include <new>
 
-#include "../spec_ptx.cuh"
+#include "../cache/spec_ptx.cuh"
 #include "spec_rows.cuh"
 
 using namespace specc;
