@@ -216,3 +216,40 @@ def test_a_wait_that_runs_out_is_reported(sv, limit, rows, outs, dim):
             assert status.item() == sv.STATUS_INTERNAL
         if clocks == 2 ** 31 - 1:
             assert status.item() == 0
+
+
+def test_captured_behind_other_work(sv):
+    """In a graph, calls behind a memset, a copy, a torch kernel, another stream's work and one another."""
+    g = torch.Generator().manual_seed(8)
+    w = sv.weight_quantise(torch.randn(640, 512, generator=g).to(torch.bfloat16).cuda())
+    src, held, extra = torch.randn(50, 512, generator=g).cuda(), torch.empty(50, 512, device="cuda"), torch.empty(50, 512, device="cuda")
+    side = torch.cuda.Stream()
+
+    def work():
+        held.zero_()
+        zero = sv.rows_quantise(held)
+        held.copy_(src)
+        first = sv.rows_quantise(held)
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            extra.copy_(src).mul_(2)
+            other = sv.rows_product(sv.rows_quantise(extra), w)
+        mine = sv.rows_product(first, w)
+        main.wait_stream(side)
+        joined, total = sv.rows_norm(mine, residual=other)
+        held.fill_(3)
+        return zero.codes.clone(), mine, other, joined.codes, joined.scale, total, sv.rows_product(sv.rows_quantise(held), w)
+
+    want = work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = work()
+    for t in got:
+        bits(t).fill_(7)
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(bits(a), bits(b))
