@@ -20,7 +20,7 @@
 // 32 lanes), one for the copies and, in the first CTA of a pair, one that issues the products.
 //
 // Pairs are persistent, with accumulators in two places, so that writing one tile overlaps the products of the next.
-// Where tiles are too few for the SMs, two or three pairs share one, a part of k each, and add their sums through
+// Where tiles are too few for the SMs, up to eight pairs share one, a part of k each, and add their sums through
 // distributed shared memory in the order of the parts (`plan` has the rule and what it rests on).
 //
 // Bound by the weight's bytes for few rows (1 x 4,096 to 128,256: 78.7 us, the copy rate; 1 x 4,096 to 4,096: 8.7 us, of
@@ -50,7 +50,7 @@ constexpr uint32_t kOutBytes = 4 * kOutRing * kChunkBytes;
 constexpr int kDepth = 2;             // blocks of k to a stage
 constexpr uint32_t kColumns = 512;    // of tensor memory: all of them
 constexpr int kMostRows = 240;        // of a tile: two accumulators and the scales take 504 columns
-constexpr int kMaxSplits = 3;         // pairs that share a tile's k, in a cluster of twice as many CTAs
+constexpr int kMaxSplits = 8;         // pairs that share a tile's k, in a cluster of twice as many CTAs
 
 struct Args {
     const uint8_t *row_scale, *weight_scale;
@@ -709,35 +709,39 @@ out:
         cluster_sync();
         // each CTA adds its share of the tile's rows, part by part
         const Tile t = tile_of(a, (int)cluster_index());
-        const int m = lane * 4, n = t.out * kTileM + (int)side * kRowsM + m, r0 = t.row * a.tile, used = min(a.tile, a.rows - r0),
+        const int m = lane * 4, n = t.out * kTileM + (int)side * kRowsM + m, row0 = t.row * a.tile, used = min(a.tile, a.rows - row0),
                   c1 = used * (part + 1) / a.splits;
         if (n < a.outs && warp < 8) {
             const uint32_t at = smem_u32((float *)stage0 + m);
-            uint32_t from[kMaxSplits];
-#pragma unroll
-            for (int r = 0; r < kMaxSplits; ++r)
-                from[r] = in_cluster(at, r < a.splits ? 2 * r + side : rank);
-            constexpr int kMore = 4;  // rows whose loads are in flight together
+            constexpr int kMore = 4, kAtOnce = 4;  // rows and parts whose loads are in flight together
             for (int c = used * part / a.splits + warp; c < c1; c += 8 * kMore) {
-                float4 v[kMore][kMaxSplits];
+                float4 sum[kMore];
 #pragma unroll
                 for (int i = 0; i < kMore; ++i)
+                    sum[i] = make_float4(0, 0, 0, 0);
+                for (int r0 = 0; r0 < a.splits; r0 += kAtOnce) {
+                    float4 v[kMore][kAtOnce];
 #pragma unroll
-                    for (int r = 0; r < kMaxSplits; ++r)
-                        v[i][r] = r < a.splits && c + 8 * i < c1 ? load_cluster(from[r] + (c + 8 * i) * (kRowsM * 4)) : make_float4(0, 0, 0, 0);
+                    for (int r = 0; r < kAtOnce; ++r) {
+                        const uint32_t from = in_cluster(at, r0 + r < a.splits ? 2 * (r0 + r) + side : rank);
 #pragma unroll
-                for (int i = 0; i < kMore; ++i) {
-                    float4 sum = v[i][0];
-#pragma unroll
-                    for (int r = 1; r < kMaxSplits; ++r) {  // what is not there is 0
-                        sum.x += v[i][r].x;
-                        sum.y += v[i][r].y;
-                        sum.z += v[i][r].z;
-                        sum.w += v[i][r].w;
+                        for (int i = 0; i < kMore; ++i)
+                            v[i][r] = r0 + r < a.splits && c + 8 * i < c1 ? load_cluster(from + (c + 8 * i) * (kRowsM * 4)) : make_float4(0, 0, 0, 0);
                     }
-                    if (c + 8 * i < c1)
-                        put4(a, r0 + c + 8 * i, n, sum);
+#pragma unroll
+                    for (int i = 0; i < kMore; ++i)
+#pragma unroll
+                        for (int r = 0; r < kAtOnce; ++r) {  // what is not there is 0
+                            sum[i].x += v[i][r].x;
+                            sum[i].y += v[i][r].y;
+                            sum[i].z += v[i][r].z;
+                            sum[i].w += v[i][r].w;
+                        }
                 }
+#pragma unroll
+                for (int i = 0; i < kMore; ++i)
+                    if (c + 8 * i < c1)
+                        put4(a, row0 + c + 8 * i, n, sum[i]);
             }
         }
     }
@@ -780,8 +784,12 @@ struct Plan {
 
 // The tile and the parts of k of least estimated time.  In units of 0.1 ns: a block of k takes 185 ns + 0.6 a row of the
 // tile (issue, then copies and products; 32 blocks of 16,376 rows to 6,144: 6.5 us with 32 rows, 9.7 with 240), in as many
-// rounds as there are tiles to a pair of SMs; adding up n parts takes n times 0.5 us + 4 ns a row.  Parts that do not all
-// run at once cost a round more than they save (8,192 x 8,192 in three parts: 22 us, in two 15.6, in one 18.8).
+// rounds as there are tiles to a pair of SMs; adding up n parts takes 0.3 us and n times 80 ns + 2.8 a row (one row of
+// 14,336 to one output: 27.6 us whole, 16.6, 10.9 and 8.4 in 2, 4 and 8 parts; 112 rows of 4,096 to 1,024: 7.4 in 4 parts,
+// 7.9 in 6), and each pair at work 25 ns more, as they start together and meet (256 rows of 2,048 to 2,048 in 32 pairs
+// whole: 7.4 us, in 64 of two parts: 8.0).  Parts that do not all run at once cost a round more than they save (8,192 x
+// 8,192 in three parts: 22 us, in two 15.6, in one 18.8).  Over 108 sizes the choice is within 4 % of the best of them in
+// most and within 10 % in all.
 Plan plan(const Device &d, int rows, int outs, int blocks)
 {
     const int64_t out_tiles = (outs + 2 * kRowsM - 1) / (2 * kRowsM);
@@ -792,7 +800,8 @@ Plan plan(const Device &d, int rows, int outs, int blocks)
         for (int n = 1; n <= kMaxSplits; ++n) {
             if (n > 1 && (units > d.clusters[n] || n > blocks))
                 break;
-            const int64_t each = (blocks + n - 1) / n * (1850 + 6 * tile), cost = n == 1 ? rounds * each : each + n * (5000 + 40 * tile);
+            const int64_t each = (blocks + n - 1) / n * (1850 + 6 * tile);
+            const int64_t cost = n == 1 ? rounds * each : each + 3000 + n * (800 + 28 * tile + 250 * units);
             if (cost < best) {
                 best = cost;
                 p = {tile, n};
@@ -824,7 +833,8 @@ spec_status this_device(const Device **out)
     if (!found) {
         Device d;
         if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            cudaFuncSetAttribute(product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared) != cudaSuccess) {
+            cudaFuncSetAttribute(product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared) != cudaSuccess ||
+            cudaFuncSetAttribute(product_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
             cudaGetLastError();
             return SPEC_ERR_CUDA;
         }

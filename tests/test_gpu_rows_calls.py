@@ -218,6 +218,11 @@ def test_a_wait_that_runs_out_is_reported(sv, limit, rows, outs, dim):
             assert status.item() == 0
 
 
+@pytest.mark.parametrize("rows,outs,dim", [(1, 300, 14336), (33, 1025, 16400), (200, 250, 12672)])
+def test_a_wait_of_many_parts_that_runs_out(sv, limit, rows, outs, dim):
+    test_a_wait_that_runs_out_is_reported(sv, limit, rows, outs, dim)
+
+
 def test_captured_behind_other_work(sv):
     """In a graph, calls behind a memset, a copy, a torch kernel, another stream's work and one another."""
     g = torch.Generator().manual_seed(8)

@@ -150,3 +150,16 @@ def test_outputs_past_32_bits(sv):
     got = sv.rows_product(sv.Coded(codes, scale), dev(w, sv))
     assert not got[:-300].any()
     check(sv, tail, w, got[-300:], torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows,outs,dim", [
+    (1, 1, 100000), (16, 9, 6656), (1, 300, 14336), (200, 250, 12672), (70, 250, 5008), (37, 777, 2048), (9, 2048, 16384), (33, 1025, 16400),
+    (240, 250, 131072), (240, 3840, 16384)])
+def test_many_parts_of_k(sv, rows, outs, dim):
+    """Four to eight parts, narrow and wide tiles, parts that get no equal share; each time the same bits."""
+    gen = torch.Generator().manual_seed(12)
+    a, w = ref.random_coded(rows, dim, E4, gen, sv), ref.random_coded(outs, dim, E4, gen, sv, 128)
+    for dtype in (torch.float32, torch.bfloat16):
+        got = sv.rows_product(dev(a, sv), dev(w, sv), dtype=dtype)
+        check(sv, a, w, got, dtype)
+        assert all(torch.equal(sv.rows_product(dev(a, sv), dev(w, sv), dtype=dtype), got) for _ in range(3))
