@@ -23,7 +23,7 @@
 // Where tiles are too few for the SMs, up to eight pairs share one, a part of k each, and add their sums through
 // distributed shared memory in the order of the parts (`plan` has the rule and what it rests on).
 //
-// Bound by the weight's bytes for few rows (1 x 4,096 to 128,256: 78.7 us, the copy rate; 1 x 4,096 to 4,096: 8.7 us, of
+// Bound by the weight's bytes for few rows (1 x 4,096 to 128,256: 78.7 us, the copy rate; 1 x 4,096 to 4,096: 8.2 us, of
 // which 5 are the kernel's start and end), by the products for many (16,376 x 4,096 to 6,144: 200 to 213 us, 3.9 to 4.1
 // PFLOP/s).  Without the scales' path that product took 190 us, without copies 177 (4.6 PFLOP/s).
 
@@ -48,13 +48,14 @@ constexpr uint32_t kChunkBytes = 32 * 32 * 2;  // outputs in bf16 that a warp wr
 constexpr int kOutRing = 4;                    // of them on their way
 constexpr uint32_t kOutBytes = 4 * kOutRing * kChunkBytes;
 constexpr int kDepth = 2;             // blocks of k to a stage
+constexpr int kAhead = 4;             // of a CTA's first that it asks L2 for while the kernel before ends
 constexpr uint32_t kColumns = 512;    // of tensor memory: all of them
 constexpr int kMostRows = 240;        // of a tile: two accumulators and the scales take 504 columns
 constexpr int kMaxSplits = 8;         // pairs that share a tile's k, in a cluster of twice as many CTAs
 
 struct Args {
-    const uint8_t *row_scale, *weight_scale;
-    int64_t row_scale_stride, weight_scale_stride;
+    const uint8_t *row_scale, *weight, *weight_scale;
+    int64_t row_scale_stride, weight_stride, weight_scale_stride;
     void *out;
     int64_t out_stride;
     int rows, outs, blocks;  // activations' rows, weight rows, blocks of k
@@ -115,6 +116,7 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar)
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_line(const uint8_t *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
 __device__ __forceinline__ void prefetch(const CUtensorMap *map)
 {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -403,6 +405,12 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     const uint32_t side = rank & 1, leader = rank - side, mask = 3u << leader;  // of its pair
     const bool lead = side == 0;
 
+    // blocks of k of this CTA
+    const int part = (int)rank / 2;
+    const int k0 = (int)((int64_t)a.blocks * part / a.splits), k1 = (int)((int64_t)a.blocks * (part + 1) / a.splits);
+    const int units = a.row_tiles * a.out_tiles, step = (int)cluster_count();
+    constexpr int kTileM = 2 * kRowsM;  // weight rows of a tile
+
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
             mbar_init(&full[i], 1);
@@ -430,14 +438,19 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     tc_before();
     cluster_sync();
     tc_after();
+    // L2 may begin to read the weight while the kernel before still runs: a hint, which brings nothing nearer than where
+    // that kernel's writes arrive too, so it needs no promise that the weight stays.  A layer of seven calls (4,096, one row):
+    // 64.9 to 61.8 us; 1 x 4,096 to 4,096 behind itself: 8.7 to 8.3.  (As copies of tiles, or with more blocks than 4, what is
+    // in L2 already costs more: 16 x 1,024 to 1,024 5.4 to 6.5 and 5.8 us.)  The warps that read accumulators have the time.
+    if (warp < kScaleWarp) {
+        const int n = tile_of(a, (int)cluster_index()).out * kTileM + (int)side * kRowsM + threadIdx.x;
+        const uint8_t *const p = a.weight + n * a.weight_stride;
+        if (n < a.outs)
+            for (int b = k0; b < min(k1, k0 + kAhead); ++b)
+                prefetch_line(p + b * kScaleBlock);
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");  // before any wait that is counted in clocks begins
     const uint32_t tmem = tmem_at, scales = tmem + kColumns - 2 * kScaleColumns;
-
-    // blocks of k of this CTA
-    const int part = (int)rank / 2;
-    const int k0 = (int)((int64_t)a.blocks * part / a.splits), k1 = (int)((int64_t)a.blocks * (part + 1) / a.splits);
-    const int units = a.row_tiles * a.out_tiles, step = (int)cluster_count();
-    constexpr int kTileM = 2 * kRowsM;  // weight rows of a tile
 
     // A stage holds kDepth blocks of k.  The two loops below ask for the next barrier before they issue what the last one
     // allowed: a wait that begins when it is needed takes some 190 clocks even if there is nothing to wait for.
@@ -915,6 +928,8 @@ extern "C" spec_status spec_rows_product(const spec_coded *rows, const spec_code
     Args a{};
     a.row_scale = rows->scale;
     a.row_scale_stride = rows->scale_stride;
+    a.weight = (const uint8_t *)weight->codes;
+    a.weight_stride = weight->stride;
     a.weight_scale = weight->scale;
     a.weight_scale_stride = weight->scale_stride;
     a.out = out;

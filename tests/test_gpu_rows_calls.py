@@ -181,6 +181,24 @@ def test_a_chain_sees_what_the_call_before_it_wrote(sv):
         assert torch.equal(chain(buffers()), slow)
 
 
+@pytest.mark.parametrize("rows,outs,dim", [(1, 4096, 4096), (160, 2560, 2560), (5, 32000, 1024)])
+def test_a_weight_written_by_the_call_before(sv, rows, outs, dim):
+    """A product asks for its weight while the kernel ahead still writes it, and reads what that one wrote."""
+    g = torch.Generator().manual_seed(9)
+    sources = [torch.randn(outs, dim, generator=g).to(torch.bfloat16).cuda() for _ in range(3)]
+    x = torch.randn(rows, dim, generator=g).to(torch.bfloat16).cuda()
+    coded = sv.rows_quantise(x)
+    want = [sv.rows_product(coded, sv.weight_quantise(s)) for s in sources]
+    w = sv.weight_quantise(sources[0])
+    torch.cuda.synchronize()
+    got = []
+    for i in range(30):
+        sv.weight_quantise(sources[i % 3], out=w)
+        got.append(sv.rows_product(coded, w))
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 3])
+
+
 @pytest.fixture
 def limit(sv):
     from speculative_decoding_verification_45_gb300 import _native
