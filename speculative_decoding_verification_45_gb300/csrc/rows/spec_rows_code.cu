@@ -301,8 +301,9 @@ struct NormArgs {
 struct None {};  // no residual
 
 // EACH: chunks of eight to a thread.  WARP: eight rows to a CTA, so that short ones do not each cost a CTA's start
-// (16,376 of 512 elements: 17.4 us with a CTA each, 9.9 so).
-template <typename T, typename R, int EACH, bool WARP = false> __global__ void __launch_bounds__(WARP ? kThreads : 512)
+// (16,376 of 512 elements: 17.4 us with a CTA each, 9.9 so).  EARLY: the weight is read beside the row, not when the row's
+// sum is known, for which more of the row's registers are in use at once (`launch_norm` has the rule).
+template <typename T, typename R, int EACH, bool WARP, bool EARLY> __global__ void __launch_bounds__(WARP ? kThreads : 512)
 norm_kernel(const NormArgs a, const Out o)
 {
     constexpr bool kResidual = !std::is_same<R, None>::value;
@@ -326,6 +327,26 @@ norm_kernel(const NormArgs a, const Out o)
                 r[i].load((const S *)a.residual + row * a.residual_stride + col);
         }
     }
+    const auto weight_at = [&](int col) {
+        Eight w{{{1, 1}, {1, 1}, {1, 1}, {1, 1}}};
+        if (a.weight && col < o.dim) {
+            if (a.weight_bf16) {
+                Raw<__nv_bfloat16> raw;
+                raw.load((const __nv_bfloat16 *)a.weight + col);
+                w = raw.values();
+            } else {
+                Raw<float> raw;
+                raw.load((const float *)a.weight + col);
+                w = raw.values();
+            }
+        }
+        return w;
+    };
+    Eight early[EARLY ? EACH : 1];
+    if (EARLY)
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            early[EARLY ? i : 0] = weight_at((i * threads + mine) * 8);
     Eight h[EACH];
     float2 two = {0.0f, 0.0f};
 #pragma unroll
@@ -361,18 +382,7 @@ norm_kernel(const NormArgs a, const Out o)
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int slot = i * threads + mine, col = slot * 8;
-        Eight w{{{1, 1}, {1, 1}, {1, 1}, {1, 1}}};
-        if (a.weight && col < o.dim) {
-            if (a.weight_bf16) {
-                Raw<__nv_bfloat16> raw;
-                raw.load((const __nv_bfloat16 *)a.weight + col);
-                w = raw.values();
-            } else {
-                Raw<float> raw;
-                raw.load((const float *)a.weight + col);
-                w = raw.values();
-            }
-        }
+        const Eight w = EARLY ? early[EARLY ? i : 0] : weight_at(col);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             h[i].v[j] = mul2(mul2(h[i].v[j], {factor, factor}), w.v[j]);
@@ -401,24 +411,35 @@ template <typename T, typename F> spec_status launch_code(const Inputs &in, cons
     return launch(code_kernel<T, F>, dim3((unsigned)ctas), kThreads, 0, 1, stream, in, make_out(out), slots, per);
 }
 
+template <typename T, typename R, int EACH, bool WARP>
+spec_status launch_norm(bool early, unsigned ctas, int threads, cudaStream_t stream, const NormArgs &a, const Out &o)
+{
+    if (early)
+        return launch(norm_kernel<T, R, EACH, WARP, EACH <= 4>, dim3(ctas), threads, 0, 1, stream, a, o);
+    return launch(norm_kernel<T, R, EACH, WARP, false>, dim3(ctas), threads, 0, 1, stream, a, o);
+}
+
 template <typename T, typename R> spec_status launch_norm(const NormArgs &a, const spec_coded *out, cudaStream_t stream)
 {
     const int slots = scale_blocks(out->dim) * kLanes;
     const Out o = make_out(out);
-    const dim3 rows((unsigned)out->rows);
-    const dim3 few((unsigned)((out->rows + kThreads / 32 - 1) / (kThreads / 32)));
+    // The weight is read early where all rows are at work at once, 16,384 elements to each of 152 SMs, and only latency
+    // counts (1 x 4,096: 3.1 to 2.2 us; 1 x 8,192: 4.8 to 3.0; 304 x 8,192: 4.8 to 4.3).  With more, its registers cost rows
+    // in flight (608 x 8,192: 6.7 us late, 7.9 early; 16,376: 135 and 175).
+    const bool early = (int64_t)out->rows * out->dim <= 152 * 16384;
+    const unsigned rows = (unsigned)out->rows, few = (rows + kThreads / 32 - 1) / (kThreads / 32);
     if (slots <= 32)
-        return launch(norm_kernel<T, R, 1, true>, few, kThreads, 0, 1, stream, a, o);
+        return launch_norm<T, R, 1, true>(early, few, kThreads, stream, a, o);
     if (slots <= 64)
-        return launch(norm_kernel<T, R, 2, true>, few, kThreads, 0, 1, stream, a, o);
+        return launch_norm<T, R, 2, true>(early, few, kThreads, stream, a, o);
     if (slots <= 128)
-        return launch(norm_kernel<T, R, 4, true>, few, kThreads, 0, 1, stream, a, o);
+        return launch_norm<T, R, 4, true>(early, few, kThreads, stream, a, o);
     const auto threads = [&](int each) { return ((slots + each - 1) / each + 31) / 32 * 32; };
     if (slots <= 512)
-        return launch(norm_kernel<T, R, 2>, rows, threads(2), 0, 1, stream, a, o);
+        return launch_norm<T, R, 2, false>(early, rows, threads(2), stream, a, o);
     if (slots <= 2048)
-        return launch(norm_kernel<T, R, 4>, rows, threads(4), 0, 1, stream, a, o);
-    return launch(norm_kernel<T, R, 8>, rows, threads(8), 0, 1, stream, a, o);
+        return launch_norm<T, R, 4, false>(early, rows, threads(4), stream, a, o);
+    return launch_norm<T, R, 8, false>(early, rows, threads(8), stream, a, o);
 }
 
 template <typename T> spec_status norm_of(const NormArgs &a, int residual, const spec_coded *out, cudaStream_t stream)
