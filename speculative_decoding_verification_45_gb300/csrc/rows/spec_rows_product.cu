@@ -20,11 +20,12 @@
 // 32 lanes), one for the copies and, in the first CTA of a pair, one that issues the products.
 //
 // Pairs are persistent, with accumulators in two places, so that writing one tile overlaps the products of the next.
-// Where tiles are too few for the SMs, up to eight pairs share one, a part of k each, and add their sums through
-// distributed shared memory in the order of the parts (`plan` has the rule and what it rests on).
+// Where tiles are too few for the SMs, up to eight pairs share one, a part of k each.  Each CTA then adds up a share of the
+// tile's rows, in the order of the parts, from what the others send into its shared memory (by bulk copies: 160 x 4,096 to
+// 1,024 takes 7.1 us, 7.5 if it loads from theirs, 9.6 if they store to its).  `plan` has the rule and what it rests on.
 //
-// Bound by the weight's bytes for few rows (1 x 4,096 to 128,256: 78.7 us, the copy rate; 1 x 4,096 to 4,096: 8.2 us, of
-// which 5 are the kernel's start and end), by the products for many (16,376 x 4,096 to 6,144: 200 to 213 us, 3.9 to 4.1
+// Bound by the weight's bytes for few rows (1 x 4,096 to 128,256: 78.7 us, the copy rate; 1 x 4,096 to 4,096: 7.2 us, of
+// which nearly 5 are the kernel's start and end), by the products for many (16,376 x 4,096 to 6,144: 200 to 213 us, 3.9 to 4.1
 // PFLOP/s).  Without the scales' path that product took 190 us, without copies 177 (4.6 PFLOP/s).
 
 #include <algorithm>
@@ -65,6 +66,7 @@ struct Args {
     uint32_t stage_bytes, b_bytes;
     uint32_t idesc;          // without the scales' bytes and the rows
     int splits, wide_out;    // wide_out: fp32
+    int apart;               // other parts' sums arrive behind the stages, not in their place
     int boxes;               // outputs are written in boxes of 32 and 16 rows: 2 bf16, 4 fp32, 0 not
     int wait_limit;
     uint32_t *status;
@@ -102,10 +104,17 @@ __device__ __forceinline__ uint32_t in_cluster(uint32_t at, uint32_t rank)
     return r;
 }
 __device__ __forceinline__ uint32_t in_cta(const void *p, uint32_t rank) { return in_cluster(smem_u32(p), rank); }
-__device__ __forceinline__ float4 load_cluster(uint32_t a)
+// From this CTA's shared memory to another's, whose barrier learns of the bytes.
+__device__ __forceinline__ void copy_to(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "r"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ float4 load_shared4(uint32_t at)
 {
     float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
     return v;
 }
 // For what went through tensor memory, which tcgen05.fence orders.  (A release at cluster scope, which nothing here needs,
@@ -395,7 +404,7 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
                const __grid_constant__ CUtensorMap omap)
 {
     extern __shared__ uint8_t dynamic[];
-    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], scale_full[2], scale_empty[2], acc_full[2], acc_empty[2], landed;
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], scale_full[2], scale_empty[2], acc_full[2], acc_empty[2], ready, got, landed;
     __shared__ uint32_t tmem_at, scale_row[2][256];
     __shared__ Guard guard;
     uint8_t *const stage0 = (uint8_t *)(((uintptr_t)dynamic + 1023) & ~(uintptr_t)1023);
@@ -421,6 +430,8 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], 8);
         }
+        mbar_init(&ready, max(a.splits - 1, 1));
+        mbar_init(&got, 1);
         mbar_init(&landed, 1);
         guard.dead = 0;
         guard.limit = a.wait_limit;
@@ -440,17 +451,28 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     // that kernel's writes arrive too, so it needs no promise that the weight stays.  A layer of seven calls (4,096, one row):
     // 64.9 to 61.8 us; 1 x 4,096 to 4,096 behind itself: 8.7 to 8.3.  (As copies of tiles, or with more blocks than 4, what is
     // in L2 already costs more: 16 x 1,024 to 1,024 5.4 to 6.5 and 5.8 us.)  The warps that read accumulators have the time.
+    // The first tile of this CTA, or the one that it has a part of.  Found here, where there is time: divisions take hundreds of
+    // clocks.
+    const int u0 = (int)cluster_index();
+    const Tile tile0 = tile_of(a, u0);
+    const int my_out = tile0.out * kTileM + (int)side * kRowsM, my_row = tile0.row * a.tile;
     if (warp < kScaleWarp) {
-        const int n = tile_of(a, (int)cluster_index()).out * kTileM + (int)side * kRowsM + threadIdx.x;
+        const int n = my_out + threadIdx.x;
         const uint8_t *const p = a.weight + n * a.weight_stride;
         if (n < a.outs)
             for (int b = k0; b < min(k1, k0 + kAhead); ++b)
                 prefetch_line(p + b * kScaleBlock);
     }
+    // Where a tile's k is shared, each CTA adds up a share of the tile's rows; the other parts' sums of those arrive at `others`.
+    const int my_used = min(a.tile, a.rows - my_row), share = (my_used + a.splits - 1) / a.splits, my_first = part * share,
+              my_count = max(min(share, my_used - my_first), 0);
+    const uint32_t others = smem_u32(stage0) + (a.apart ? a.stages * a.stage_bytes : my_used * (kRowsM * 4));
     asm volatile("griddepcontrol.wait;" ::: "memory");  // before any wait that is counted in clocks begins
     cluster_wait();
     tc_after();
     const uint32_t tmem = tmem_at, scales = tmem + kColumns - 2 * kScaleColumns;
+    if (a.splits > 1 && threadIdx.x == 0)
+        mbar_expect(&got, (a.splits - 1) * my_count * (kRowsM * 4));
 
     // A stage holds kDepth blocks of k.  The two loops below ask for the next barrier before they issue what the last one
     // allowed: a wait that begins when it is needed takes some 190 clocks even if there is nothing to wait for.
@@ -459,8 +481,8 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         uint32_t issued = 0;
         const uint32_t bar0 = in_cta(full, leader), base = smem_u32(stage0);
         bool free = true;
-        for (int u = (int)cluster_index(); u < units; u += step) {
-            const Tile t = tile_of(a, u);
+        for (int u = u0; u < units; u += step) {
+            const Tile t = u == u0 ? tile0 : tile_of(a, u);
             const int n0 = t.out * kTileM + (int)side * kRowsM, r0 = t.row * a.tile + (int)side * (rows_of(a, t) / 2);
             for (int b = k0; b < k1; b += kDepth, ++issued) {
                 if (!__all_sync(0xffffffffu, free) && !wait(&empty[ring.at], ring.parity ^ 1, &guard))
@@ -493,8 +515,8 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
         uint32_t groups = 0, done = 0;
         const uint32_t base = smem_u32(stage0);
         bool here = false, scaled = false;
-        for (int u = (int)cluster_index(); u < units; u += step, ++done) {
-            const uint32_t buf = (done & 1), acc = tmem + buf * a.tile, n_bits = (uint32_t)rows_of(a, tile_of(a, u)) >> 3 << 17;
+        for (int u = u0; u < units; u += step, ++done) {
+            const uint32_t buf = (done & 1), acc = tmem + buf * a.tile, n_bits = (uint32_t)rows_of(a, u == u0 ? tile0 : tile_of(a, u)) >> 3 << 17;
             if (!wait(&acc_empty[buf], (done >> 1 & 1) ^ 1, &guard))
                 goto out;
             for (int b = k0; b < k1; b += kDepth) {
@@ -550,8 +572,8 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
             weight_bytes(a.weight_scale, a.weight_scale_stride, (a.outs + kRowsM - 1) / kRowsM, a.blocks);
         const uint4 one4 = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
         uint32_t groups = 0;
-        for (int u = (int)cluster_index(); u < units; u += step) {
-            const Tile t = tile_of(a, u);
+        for (int u = u0; u < units; u += step) {
+            const Tile t = u == u0 ? tile0 : tile_of(a, u);
             const int wb = t.out * 2 + (int)side, r0 = t.row * a.tile;
             const bool has = (int64_t)wb * kRowsM < a.outs, has0 = mine < a.tile && r0 + mine < a.rows,
                        has1 = mine + 128 < a.tile && r0 + mine + 128 < a.rows;
@@ -605,8 +627,13 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     } else if (warp < kScaleWarp) {
         const uint32_t lanes = (uint32_t)warp << 21, chunk0 = smem_u32(stage0) + a.stages * a.stage_bytes + warp * (kOutRing * kChunkBytes);
         uint32_t done = 0, chunks = 0;
-        for (int u = (int)cluster_index(); u < units; u += step, ++done) {
-            const Tile t = tile_of(a, u);
+        // what a lane sends to the part of its number, if there is one
+        const bool sends = lane < a.splits && lane != part;
+        const uint32_t other = 2 * lane + side, bytes = max(min(share, my_used - lane * share), 0) * (kRowsM * 4),
+                       to = in_cluster(others + (part - (part > lane)) * share * (kRowsM * 4), sends ? other : rank),
+                       bar = in_cta(&got, sends ? other : rank);
+        for (int u = u0; u < units; u += step, ++done) {
+            const Tile t = u == u0 ? tile0 : tile_of(a, u);
             const uint32_t buf = (done & 1), acc = tmem + buf * a.tile + lanes;
             const int m = warp * 32 + lane, n = t.out * kTileM + (int)side * kRowsM + m, r0 = t.row * a.tile;
             const int used = min(a.tile, a.rows - r0);
@@ -684,7 +711,10 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
                     }
                 }
             } else if (a.splits > 1) {
-                // the copies into the stages have all been used by now
+                // the copies into the stages have all been used by now, in whose place the sums go
+                if (!a.apart && warp == 0 && sends)
+                    arrive_cluster(in_cta(&ready, other));
+                const uint32_t at = smem_u32(stage0) + m * 4;
                 for (int c = 0; c < used; c += 32) {
                     float v[32];
                     TmemLoad<16>::go(acc + c, v);
@@ -692,8 +722,13 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
                     tmem_wait<32>(v);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        ((float *)stage0)[(c + i) * kRowsM + m] = v[i];
+                        if (c + i < used)
+                            store_shared(at + (c + i) * (kRowsM * 4), v[i]);
                 }
+                proxy_fence();
+                named_barrier<128>(2);
+                if (warp == 0 && (a.apart || wait(&ready, 0, &guard)) && sends && bytes)
+                    copy_to(to, smem_u32(stage0) + lane * share * (kRowsM * 4), bytes, bar);
             } else {
                 // Rows at any address (bf16, 16,384 x 64 to 12,207: 307 us with single values from the registers, 244 so; 131
                 // in boxes)
@@ -719,43 +754,33 @@ out:
         store_wait_read<0>();  // the buffers are the CTA's for as long as copies read them
     __syncwarp();
     if (a.splits > 1) {
-        cluster_arrive();
-        cluster_wait();
-        // each CTA adds its share of the tile's rows, part by part
-        const Tile t = tile_of(a, (int)cluster_index());
-        const int m = lane * 4, n = t.out * kTileM + (int)side * kRowsM + m, row0 = t.row * a.tile, used = min(a.tile, a.rows - row0),
-                  c1 = used * (part + 1) / a.splits;
-        if (n < a.outs && warp < 8) {
-            const uint32_t at = smem_u32((float *)stage0 + m);
-            constexpr int kMore = 4, kAtOnce = 4;  // rows and parts whose loads are in flight together
-            for (int c = used * part / a.splits + warp; c < c1; c += 8 * kMore) {
+        __syncthreads();
+        if (wait(&got, 0, &guard) && my_out + lane * 4 < a.outs) {
+            const uint32_t at = lane * 16, own = smem_u32(stage0) + my_first * (kRowsM * 4) + at;
+            constexpr int kWarps = kThreads / 32, kMore = 4;  // rows whose loads are in flight together
+            for (int r = warp; r < my_count; r += kWarps * kMore) {
                 float4 sum[kMore];
 #pragma unroll
                 for (int i = 0; i < kMore; ++i)
                     sum[i] = make_float4(0, 0, 0, 0);
-                for (int r0 = 0; r0 < a.splits; r0 += kAtOnce) {
-                    float4 v[kMore][kAtOnce];
-#pragma unroll
-                    for (int r = 0; r < kAtOnce; ++r) {
-                        const uint32_t from = in_cluster(at, r0 + r < a.splits ? 2 * (r0 + r) + side : rank);
-#pragma unroll
-                        for (int i = 0; i < kMore; ++i)
-                            v[i][r] = r0 + r < a.splits && c + 8 * i < c1 ? load_cluster(from + (c + 8 * i) * (kRowsM * 4)) : make_float4(0, 0, 0, 0);
-                    }
+                for (int k = 0; k < a.splits; ++k) {  // in the order of the parts
+                    const uint32_t from = (k == part ? own : others + at + (k - (k > part)) * share * (kRowsM * 4)) + r * (kRowsM * 4);
+                    float4 v[kMore];
 #pragma unroll
                     for (int i = 0; i < kMore; ++i)
+                        v[i] = r + i * kWarps < my_count ? load_shared4(from + i * (kWarps * kRowsM * 4)) : make_float4(0, 0, 0, 0);
 #pragma unroll
-                        for (int r = 0; r < kAtOnce; ++r) {  // what is not there is 0
-                            sum[i].x += v[i][r].x;
-                            sum[i].y += v[i][r].y;
-                            sum[i].z += v[i][r].z;
-                            sum[i].w += v[i][r].w;
-                        }
+                    for (int i = 0; i < kMore; ++i) {
+                        sum[i].x += v[i].x;
+                        sum[i].y += v[i].y;
+                        sum[i].z += v[i].z;
+                        sum[i].w += v[i].w;
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < kMore; ++i)
-                    if (c + 8 * i < c1)
-                        put4(a, row0 + c + 8 * i, n, sum[i]);
+                    if (r + i * kWarps < my_count)
+                        put4(a, my_row + my_first + r + i * kWarps, my_out + lane * 4, sum[i]);
             }
         }
     }
@@ -778,9 +803,8 @@ out:
         __syncwarp();
     }
     tc_before();
-    // All that was sent to another CTA's barriers has been waited for there, and what was read there is here, unless a wait
-    // ran out: so this need not wait for the outputs on their way (1 x 4,096 to
-    // 4,096: 8.3 us if it does, 7.6 so).
+    // All that was sent to another CTA and its barriers has been waited for there, unless a wait ran out: so this need not wait
+    // for the outputs on their way (1 x 4,096 to 4,096: 8.3 us if it does, 7.6 so).
     if (guard.dead)
         cluster_arrive();
     else
@@ -798,6 +822,23 @@ struct Device {
     int sms = 0;
     int clusters[kMaxSplits + 1] = {};  // clusters of 2 n CTAs that run at once
 };
+
+// Dynamic shared memory: nearly all of it.  A CTA holds all of tensor memory, so nothing else that waits for some may be
+// on its SM, where two clusters could each hold what the other waits for.
+constexpr uint32_t kShared = 223 * 1024;
+
+constexpr uint32_t stage_bytes(int tile) { return kDepth * (kABytes + (uint32_t)(tile / 2) * kScaleBlock); }
+// What arrives from the other parts.
+constexpr uint32_t others_bytes(int tile, int parts) { return (uint32_t)((parts - 1) * ((tile + parts - 1) / parts)) * kRowsM * 4; }
+// They have their own place while that costs no stage that is missed; in the place of stages they must wait until that CTA
+// has used them (1 x 4,096 to 4,096: 7.6 us apart, 7.9 not; 160 x 8,192 to 8,192: 17.7 us apart, 17.3 not).
+constexpr bool others_apart(int tile, int parts) { return parts > 1 && tile <= 64; }
+// Stages, beside the outputs on their way or what arrives from the other parts.
+constexpr int stages_of(int tile, int parts)
+{
+    const uint32_t beside = parts == 1 ? kOutBytes : others_apart(tile, parts) ? others_bytes(tile, parts) : 0;
+    return (int)std::min<uint32_t>(kMaxStages, (kShared - 1024 - beside) / stage_bytes(tile));
+}
 
 struct Plan {
     int tile, splits;
@@ -819,7 +860,7 @@ Plan plan(const Device &d, int rows, int outs, int blocks)
     for (int tile = 32; tile <= kMostRows; tile += 16) {
         const int64_t units = out_tiles * ((rows + tile - 1) / tile), rounds = (units + d.sms / 2 - 1) / (d.sms / 2);
         for (int n = 1; n <= kMaxSplits; ++n) {
-            if (n > 1 && (units > d.clusters[n] || n > blocks))
+            if (n > 1 && (units > d.clusters[n] || n > blocks || (uint32_t)tile * kRowsM * 4 + others_bytes(tile, n) > kShared - 1024))
                 break;
             const int64_t each = (blocks + n - 1) / n * (1850 + 6 * tile);
             const int64_t cost = n == 1 ? rounds * each : each + 3000 + n * (800 + 28 * tile + 250 * units);
@@ -836,10 +877,6 @@ Plan plan(const Device &d, int rows, int outs, int blocks)
 
 constexpr int kMaxDevices = 64;
 std::atomic<const Device *> g_devices[kMaxDevices];  // made once each, and kept
-
-// Dynamic shared memory: nearly all of it.  A CTA holds all of tensor memory, so nothing else that waits for some may be
-// on its SM, where two clusters could each hold what the other waits for.
-constexpr uint32_t kShared = 223 * 1024;
 
 spec_status this_device(const Device **out)
 {
@@ -959,9 +996,10 @@ extern "C" spec_status spec_rows_product(const spec_coded *rows, const spec_code
     if ((int64_t)a.rows * a.blocks > (16 << 20) / kScaleBlock)
         a.group = std::max(8, (int)std::min<int64_t>(a.out_tiles, (32 << 20) / ((int64_t)2 * kRowsM * kScaleBlock * a.blocks)));
     a.b_bytes = (uint32_t)(p.tile / 2) * kScaleBlock;  // a multiple of 1,024
-    a.stage_bytes = kDepth * (kABytes + a.b_bytes);
+    a.stage_bytes = stage_bytes(p.tile);
     a.boxes = p.splits == 1 && ((uintptr_t)out & 15u) == 0 && (out_stride * size & 15) == 0 ? (int)size : 0;
-    a.stages = (int)std::min<uint32_t>(kMaxStages, (kShared - 1024 - (p.splits == 1 ? kOutBytes : 0)) / a.stage_bytes);
+    a.stages = stages_of(p.tile, p.splits);
+    a.apart = others_apart(p.tile, p.splits);
     // as in the unscaled kinds, and: bytes of the scales at bits 4 and 29 (set for each block, as the rows at bit 17 are for each tile), scales of powers of
     // two (bit 23)
     a.idesc = (uint32_t)(weight->code == SPEC_E5M2) << 7 | (uint32_t)(rows->code == SPEC_E5M2) << 10 |
