@@ -846,12 +846,11 @@ struct Plan {
 
 // The tile and the parts of k of least estimated time.  In units of 0.1 ns: a block of k takes 185 ns + 0.6 a row of the
 // tile (issue, then copies and products; 32 blocks of 16,376 rows to 6,144: 6.5 us with 32 rows, 9.7 with 240), in as many
-// rounds as there are tiles to a pair of SMs; adding up n parts takes 0.3 us and n times 80 ns + 2.8 a row (one row of
-// 14,336 to one output: 27.6 us whole, 16.6, 10.9 and 8.4 in 2, 4 and 8 parts; 112 rows of 4,096 to 1,024: 7.4 in 4 parts,
-// 7.9 in 6), and each pair at work 25 ns more, as they start together and meet (256 rows of 2,048 to 2,048 in 32 pairs
-// whole: 7.4 us, in 64 of two parts: 8.0).  Parts that do not all run at once cost a round more than they save (8,192 x
-// 8,192 in three parts: 22 us, in two 15.6, in one 18.8).  Over 108 sizes the choice is within 4 % of the best of them in
-// most and within 10 % in all.
+// rounds as there are tiles to a pair of SMs; adding up n parts takes 0.1 us and n times 40 ns + 3 a row (one row of 14,336
+// to one output: 27.7 us whole, 15.7, 9.6 and 7.1 in 2, 4 and 8 parts), and each pair at work 15 ns more, as they start together
+// and meet.  Parts that do not all run at once cost a round more than they save (256 rows of 2,048 to 2,048, 64 rows to a
+// tile: 7.0 us whole, 7.1 in two parts, 12.8 in three).  Over 108 sizes the choice is within 4 % of the best of them in 102
+// and within 10 % in all but one (512 x 512, one row: 4.6 us, 4.1 in four parts).
 Plan plan(const Device &d, int rows, int outs, int blocks)
 {
     const int64_t out_tiles = (outs + 2 * kRowsM - 1) / (2 * kRowsM);
@@ -863,7 +862,7 @@ Plan plan(const Device &d, int rows, int outs, int blocks)
             if (n > 1 && (units > d.clusters[n] || n > blocks || (uint32_t)tile * kRowsM * 4 + others_bytes(tile, n) > kShared - 1024))
                 break;
             const int64_t each = (blocks + n - 1) / n * (1850 + 6 * tile);
-            const int64_t cost = n == 1 ? rounds * each : each + 3000 + n * (800 + 28 * tile + 250 * units);
+            const int64_t cost = n == 1 ? rounds * each : each + 1000 + n * (400 + 30 * tile + 150 * units);
             if (cost < best) {
                 best = cost;
                 p = {tile, n};
