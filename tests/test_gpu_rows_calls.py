@@ -149,6 +149,35 @@ def test_two_products_at_once(sv):
             assert all(torch.equal(x, want) for x in several)
 
 
+def test_clusters_of_every_size_at_once(sv):
+    """Two to sixteen CTAs to a cluster on five streams, behind and beside one another, as captured graphs too."""
+    g = torch.Generator().manual_seed(10)
+    cases = []
+    for rows, outs, dim in ((1, 300, 14336), (33, 1025, 16400), (1, 4096, 4096), (160, 5000, 2048), (240, 1000, 8192)):
+        a, w = ref.random_coded(rows, dim, E4, g, sv), ref.random_coded(outs, dim, E4, g, sv, 128)
+        a, w = (sv.Coded(c.codes.cuda(), c.scale.cuda()) for c in (a, w))
+        cases.append((a, w, sv.rows_product(a, w), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    graphs = []
+    for a, w, _, s in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            kept = [sv.rows_product(a, w) for _ in range(4)]
+        graphs.append((graph, kept))
+    for i in range(20):
+        got = [[sv.rows_product(a, w, stream=s) for _ in range(3)] for a, w, _, s in cases[i % 2:]]
+        for (graph, kept), (_, _, _, s) in zip(graphs, cases):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        for (_, _, want, _), several in zip(cases[i % 2:], got):
+            assert all(torch.equal(x, want) for x in several)
+        for (_, kept), (_, _, want, _) in zip(graphs, cases):
+            assert all(torch.equal(x, want) for x in kept)
+            for x in kept:
+                x.fill_(7)
+
+
 def test_a_chain_sees_what_the_call_before_it_wrote(sv):
     """Kernels may begin before the one ahead of them has ended: each still reads its results, and writes behind its reads."""
     g = torch.Generator().manual_seed(6)
