@@ -214,26 +214,35 @@ struct Bytes {
     }
     // Blocks 16 q to 16 q + 15 of a row; behind the last block anything, which no instruction names.  Rows that begin
     // anywhere are read by aligned words, which may take in bytes of the row before or behind (333 x 2,832 to 5,000:
-    // 12.9 us byte by byte, 12.3 so).
-    __device__ __forceinline__ uint4 blocks16(const uint8_t *row, int q, int blocks) const
+    // 12.9 us byte by byte, 12.3 so).  They are shifted into place when they are needed: until then loads are on their way.
+    struct Sixteen {
+        uint32_t w[5], shift;
+        __device__ __forceinline__ uint4 get() const
+        {
+            uint32_t v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = __funnelshift_r(w[i], w[i + 1], shift);
+            return make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    };
+    __device__ __forceinline__ void blocks16(const uint8_t *row, int q, int blocks, Sixteen &s) const
     {
         const uint8_t *const p = row + 16 * q;
-        const int left = blocks - 16 * q;
-        if (aligned && left >= 16)
-            return __ldg((const uint4 *)p);
-        const int off = (int)((uintptr_t)p & 3);
-        if (off == 0 && left >= 16) {
-            const uint32_t *const q4 = (const uint32_t *)p;
-            return make_uint4(__ldg(q4), __ldg(q4 + 1), __ldg(q4 + 2), __ldg(q4 + 3));
+        const int left = blocks - 16 * q, off = (int)((uintptr_t)p & 3);
+        s.shift = 8 * off;
+        if (aligned && left >= 16) {
+            const uint4 v = __ldg((const uint4 *)p);
+            s.w[0] = v.x;
+            s.w[1] = v.y;
+            s.w[2] = v.z;
+            s.w[3] = v.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 5; ++i)
+                if (4 * i < left + off)
+                    s.w[i] = word(p - off + 4 * i);
         }
-        uint32_t w[5];
-#pragma unroll
-        for (int i = 0; i < 5; ++i)
-            w[i] = 4 * i < left + off ? word(p - off + 4 * i) : 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = __funnelshift_r(w[i], w[i + 1], 8 * off);
-        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
@@ -451,10 +460,10 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     // that kernel's writes arrive too, so it needs no promise that the weight stays.  A layer of seven calls (4,096, one row):
     // 64.9 to 61.8 us; 1 x 4,096 to 4,096 behind itself: 8.7 to 8.3.  (As copies of tiles, or with more blocks than 4, what is
     // in L2 already costs more: 16 x 1,024 to 1,024 5.4 to 6.5 and 5.8 us.)  The warps that read accumulators have the time.
-    // The first tile of this CTA, or the one that it has a part of.  Found here, where there is time: divisions take hundreds of
-    // clocks.
+    // The first tile of this CTA, or the one that it has a part of, and the next one.  Found here, where there is time: divisions
+    // take hundreds of clocks.
     const int u0 = (int)cluster_index();
-    const Tile tile0 = tile_of(a, u0);
+    const Tile tile0 = tile_of(a, u0), tile1 = tile_of(a, min(u0 + step, units - 1));
     const int my_out = tile0.out * kTileM + (int)side * kRowsM, my_row = tile0.row * a.tile;
     if (warp < kScaleWarp) {
         const int n = my_out + threadIdx.x;
@@ -564,37 +573,45 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
             }
         }
     } else if (warp >= kScaleWarp && warp < kScaleWarp + 4) {
-        // A thread fetches the bytes of one or two rows, sixteen blocks ahead; a word of each goes through shared memory to
-        // the four warps, which all store all rows (each for its 32 lanes, which the tensor cores read side by side).
+        // A thread fetches the bytes of one or two rows, sixteen blocks or a tile ahead, once the word that is needed now has
+        // been handed over (16,376 x 4,096 to 6,144: 199 us with a tile's first bytes fetched when it begins, 196 so; a fetch
+        // ahead of that word makes narrow weights faster, 3 x 128 to 128,256 11.4 us against 12.1, and the first tile of all
+        // slower, 160 x 1,024 to 28,672 11.3 against 10.9).  A word of each row goes through shared memory to the four warps,
+        // which all store all rows (each for its 32 lanes, which the tensor cores read side by side).
         const int mine = threadIdx.x - kScaleWarp * 32;
         const uint32_t lanes = (uint32_t)(warp - kScaleWarp) << 21;  // 32 lanes of tensor memory each, at bit 16
         const Bytes row_bytes(a.row_scale, a.row_scale_stride, a.rows, a.blocks),
             weight_bytes(a.weight_scale, a.weight_scale_stride, (a.outs + kRowsM - 1) / kRowsM, a.blocks);
-        const uint4 one4 = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+        // what is fetched next: of a tile that may be one ahead
+        const uint8_t *wp, *p0, *p1;
+        uint4 w, s0, s1;
+        Bytes::Sixteen next_w{}, next0{}, next1{};
+        const int last_wb = (a.outs - 1) / kRowsM;
+        const auto turn = [&](const Tile &t) {
+            // what has no row of its own reads the last one's bytes: they scale zeros that nothing is made of
+            const int wb = min(t.out * 2 + (int)side, last_wb), r = t.row * a.tile + mine;
+            wp = a.weight_scale + wb * a.weight_scale_stride;
+            p0 = a.row_scale + min(r, a.rows - 1) * a.row_scale_stride;
+            p1 = a.row_scale + min(r + 128, a.rows - 1) * a.row_scale_stride;
+        };
+        const auto fetch = [&](int q) {
+            weight_bytes.blocks16(wp, q, a.blocks, next_w);
+            row_bytes.blocks16(p0, q, a.blocks, next0);
+            if (a.tile > 128)
+                row_bytes.blocks16(p1, q, a.blocks, next1);
+        };
+        turn(tile0);
+        fetch(k0 >> 4);
+        Tile ahead = tile1;
         uint32_t groups = 0;
+        w = s0 = s1 = make_uint4(0, 0, 0, 0);
         for (int u = u0; u < units; u += step) {
-            const Tile t = u == u0 ? tile0 : tile_of(a, u);
-            const int wb = t.out * 2 + (int)side, r0 = t.row * a.tile;
-            const bool has = (int64_t)wb * kRowsM < a.outs, has0 = mine < a.tile && r0 + mine < a.rows,
-                       has1 = mine + 128 < a.tile && r0 + mine + 128 < a.rows;
-            const uint8_t *const wp = a.weight_scale + wb * a.weight_scale_stride,
-                                *const p0 = a.row_scale + (r0 + mine) * a.row_scale_stride, *const p1 = p0 + 128 * a.row_scale_stride;
-            uint4 w, s0, s1, next_w, next0, next1;
-            const auto fetch = [&](int q) {
-                next_w = has ? weight_bytes.blocks16(wp, q, a.blocks) : one4;
-                next0 = has0 ? row_bytes.blocks16(p0, q, a.blocks) : one4;
-                next1 = has1 ? row_bytes.blocks16(p1, q, a.blocks) : one4;
-            };
-            fetch(k0 >> 4);
-            w = s0 = s1 = one4;
             for (int q = k0 >> 2; q <= (k1 - 1) >> 2; ++q, ++groups) {
                 const uint32_t g = groups & 1;
                 if (q == k0 >> 2 || (q & 3) == 0) {
-                    w = next_w;
-                    s0 = next0;
-                    s1 = next1;
-                    if (16 * ((q >> 2) + 1) < k1)
-                        fetch((q >> 2) + 1);
+                    w = next_w.get();
+                    s0 = next0.get();
+                    s1 = next1.get();
                 }
                 scale_row[g][mine] = word_of(s0, q & 3);
                 if (a.tile > 128)
@@ -619,7 +636,16 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
                 __syncwarp();
                 if (lane == 0)
                     arrive_cluster(in_cta(&scale_full[g], leader));
+                if (q == k0 >> 2 || (q & 3) == 0) {
+                    if (16 * ((q >> 2) + 1) < k1) {
+                        fetch((q >> 2) + 1);
+                    } else if (u + step < units) {
+                        turn(ahead);
+                        fetch(k0 >> 4);
+                    }
+                }
             }
+            ahead = tile_of(a, min(u + 2 * step, units - 1));
         }
         for (uint32_t i = groups > 2 ? groups - 2 : 0; i < groups; ++i)
             if (!wait(&scale_empty[i & 1], i >> 1 & 1, &guard))
