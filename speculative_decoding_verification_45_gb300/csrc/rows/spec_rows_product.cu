@@ -25,7 +25,7 @@
 // 1,024 takes 7.1 us, 7.5 if it loads from theirs, 9.6 if they store to its).  `plan` has the rule and what it rests on.
 //
 // Bound by the weight's bytes for few rows (1 x 4,096 to 128,256: 78.7 us, the copy rate; 1 x 4,096 to 4,096: 7.2 us, of
-// which nearly 5 are the kernel's start and end), by the products for many (16,376 x 4,096 to 6,144: 200 to 213 us, 3.9 to 4.1
+// which nearly 5 are the kernel's start and end), by the products for many (16,376 x 4,096 to 6,144: 196 to 213 us, 3.9 to 4.2
 // PFLOP/s).  Without the scales' path that product took 190 us, without copies 177 (4.6 PFLOP/s).
 
 #include <algorithm>
