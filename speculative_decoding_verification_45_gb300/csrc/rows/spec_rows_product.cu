@@ -124,6 +124,10 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar)
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ void tell(int *flag, uint32_t rank)  // sets it in a CTA of the cluster
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(flag, rank)), "r"(1) : "memory");
+}
 __device__ __forceinline__ void prefetch_line(const uint8_t *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory"); }
 __device__ __forceinline__ void prefetch(const CUtensorMap *map)
 {
@@ -810,28 +814,22 @@ out:
             }
         }
     }
-    __syncthreads();
-    if (guard.dead) {
-        // What is in flight lands before the memory is given back.  No barrier tells of all copies (a stage that only
-        // one CTA of a pair filled never completes its phase), so a time is waited out that a copy takes many times over.
-        if (warp == kIssueWarp && lead) {
-            if (elected()) {
-                commit(&landed, mask);
-                land(&landed, 0);
-            }
-        } else if (warp == kCopyWarp && lane == 0) {
-            const long long since = clock64();
-            while (clock64() - since < (1 << 22))
-                ;
+    const bool dead = __syncthreads_or(guard.dead);
+    if (dead) {
+        if (warp == kIssueWarp && lead && elected()) {  // the products in flight
+            commit(&landed, mask);
+            land(&landed, 0);
         }
         if (threadIdx.x == 0)
             report(a.status, SPEC_STATUS_INTERNAL);
+        if (threadIdx.x < 2 * a.splits)
+            tell(&guard.dead, threadIdx.x);
         __syncwarp();
     }
     tc_before();
     // All that was sent to another CTA and its barriers has been waited for there, unless a wait ran out: so this need not wait
     // for the outputs on their way (1 x 4,096 to 4,096: 8.3 us if it does, 7.6 so).
-    if (guard.dead)
+    if (dead)
         cluster_arrive();
     else
         cluster_arrive_relaxed();
@@ -839,6 +837,14 @@ out:
     tc_after();
     if (warp == kCopyWarp)
         tmem_dealloc(tmem, kColumns);
+    // If a wait ran out in any CTA of the cluster, what is in flight between them and into them lands before the memory of one
+    // is given back.  No barrier tells of it (a stage that only one CTA of a pair filled never completes its phase), so each
+    // waits out a time that a copy takes many times over.
+    if (threadIdx.x == 0 && ((volatile Guard &)guard).dead) {
+        const long long since = clock64();
+        while (clock64() - since < (1 << 22))
+            ;
+    }
 }
 
 // ---------------------------------------------------------------------------
