@@ -24,6 +24,7 @@ from .cache import _CODES, _fail, _status
 
 SCALE = torch.float8_e8m0fnu
 BLOCK = 128
+MAX_WIDTH, MAX_ROWS = 1 << 17, 1 << 30  # SPEC_MAX_ROW, SPEC_MAX_CODED_ROWS
 _Struct, _byref, _current = _native.Coded, ctypes.byref, torch._C._cuda_getDevice
 _ACTS = {"silu": 0, "gelu_tanh": 1}
 _FLOATS = {torch.float32: 0, torch.bfloat16: 1}
@@ -118,10 +119,13 @@ def _matrix(t, name, index, types):
     if not shape or not shape[-1]:
         raise ValueError(f"{name}: expected rows of some width, got shape {tuple(shape)}")
     dim = shape[-1]
+    rows = t.numel() // dim
+    if dim > MAX_WIDTH or rows > MAX_ROWS:  # the library's sizes have 32 bits, into which ctypes would cut these
+        raise ValueError(f"{name}: at most {MAX_ROWS} rows of {MAX_WIDTH} elements, got {rows} of {dim}")
     step = dim if t.is_contiguous() else _step(t, name)
     if (at | step * t.itemsize) & 15:
         raise ValueError(f"{name}: rows must begin at multiples of 16 bytes, got a stride of {step} elements at {at:#x}")
-    return at, t.numel() // dim, dim, step, kind
+    return at, rows, dim, step, kind
 
 
 def _elsewhere(t, name, index):
