@@ -499,8 +499,9 @@ spec_status spec_rows_quantise(const void *x, int64_t x_stride, spec_dtype dtype
  *                  residual itself, or x where types and strides are the same
  *   weight         [dim] of weight_dtype, 16-byte aligned, or NULL (1)
  *   eps            positive (2^-126 at least) and finite
- * Squares are added in 32 bits: a row with elements past 2^63 may become zeros, one
- * with an infinity or a NaN becomes zeros and NaN.  dim is at most SPEC_MAX_NORM_ROW. */
+ * h, squares and their sum are 32-bit; where the squares pass that they are taken of
+ * 2^-72 of the row, so every finite row is normalised.  A row with an infinity (an h
+ * past 32 bits is one) or a NaN becomes zeros and NaN.  dim is at most SPEC_MAX_NORM_ROW. */
 spec_status spec_rows_norm(const void *x, int64_t x_stride, spec_dtype dtype, const void *residual,
                            int64_t residual_stride, spec_dtype residual_dtype, const void *weight,
                            spec_dtype weight_dtype, float eps, void *sum, int64_t sum_stride, const spec_coded *out,

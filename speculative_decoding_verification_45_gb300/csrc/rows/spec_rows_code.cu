@@ -365,20 +365,41 @@ norm_kernel(const NormArgs a, const Out o)
         for (int j = 0; j < 4; ++j)
             two = fma2(h[i].v[j], h[i].v[j], two);
     }
-    float squares = two.x + two.y;
-#pragma unroll
-    for (int k = 16; k; k >>= 1)
-        squares += __shfl_xor_sync(0xffffffffu, squares, k);
-    if (!WARP) {
-        if ((threadIdx.x & 31) == 0)
-            part[threadIdx.x / 32] = squares;
-        __syncthreads();
-        squares = (threadIdx.x & 31) < blockDim.x / 32 ? part[threadIdx.x & 31] : 0.0f;
+    // of the row, from each thread's share
+    const auto sum_of = [&](float2 share) {
+        float sum = share.x + share.y;
 #pragma unroll
         for (int k = 16; k; k >>= 1)
-            squares += __shfl_xor_sync(0xffffffffu, squares, k);
+            sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        if (!WARP) {
+            if ((threadIdx.x & 31) == 0)
+                part[threadIdx.x / 32] = sum;
+            __syncthreads();
+            sum = (threadIdx.x & 31) < blockDim.x / 32 ? part[threadIdx.x & 31] : 0.0f;
+#pragma unroll
+            for (int k = 16; k; k >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        }
+        return sum;
+    };
+    const float squares = sum_of(two);
+    float factor = __frsqrt_rn(__fdiv_rn(squares, (float)o.dim) + a.eps);
+    if (__float_as_uint(squares) >= kInfinity) {
+        // The squares pass 32 bits, at elements of 2^64 / sqrt(dim) already, where the row may yet be finite: those of 2^-72 of
+        // it stay below 2^(112 + 15).  The factor is 2^-128 at least, where 32 bits hold 21 digits of it.
+        constexpr float kDown = 0x1p-72f;
+        two = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 v = mul2(h[i].v[j], {kDown, kDown});
+                two = fma2(v, v, two);
+            }
+        if (!WARP)
+            __syncthreads();
+        factor = __frsqrt_rn(__fdiv_rn(sum_of(two), (float)o.dim) + a.eps * kDown * kDown) * kDown;
     }
-    const float factor = __frsqrt_rn(__fdiv_rn(squares, (float)o.dim) + a.eps);
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int slot = i * threads + mine, col = slot * 8;
