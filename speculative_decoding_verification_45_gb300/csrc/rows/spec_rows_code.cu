@@ -41,7 +41,9 @@ __device__ __forceinline__ uint32_t most(const Eight &e)
     return __float_as_uint(m);
 }
 
-template <typename T> struct Raw;  // eight elements as they lie in memory
+// Eight elements as they lie in memory.  lowest(): the bits of the one furthest below 0, which are larger than a positive
+// number's as an integer's (a NaN's, with its sign set, are larger still).
+template <typename T> struct Raw;
 template <> struct Raw<__nv_bfloat16> {
     uint4 q;
     __device__ __forceinline__ void load(const __nv_bfloat16 *p) { q = *(const uint4 *)p; }
@@ -51,6 +53,11 @@ template <> struct Raw<__nv_bfloat16> {
     {
         constexpr uint32_t kMagnitude = 0x7fff7fffu;
         const uint32_t m = max_halves(max_halves(q.x & kMagnitude, q.y & kMagnitude), max_halves(q.z & kMagnitude, q.w & kMagnitude));
+        return max(m << 16, m & 0xffff0000u);
+    }
+    __device__ __forceinline__ uint32_t lowest() const
+    {
+        const uint32_t m = max_halves(max_halves(q.x, q.y), max_halves(q.z, q.w));
         return max(m << 16, m & 0xffff0000u);
     }
 };
@@ -64,6 +71,13 @@ template <> struct Raw<float> {
     __device__ __forceinline__ void clear() { a = b = make_float4(0, 0, 0, 0); }
     __device__ __forceinline__ Eight values() const { return {{{a.x, a.y}, {a.z, a.w}, {b.x, b.y}, {b.z, b.w}}}; }
     __device__ __forceinline__ uint32_t most_of() const { return most(values()); }
+    __device__ __forceinline__ uint32_t lowest() const
+    {
+        const auto of = [](const float4 &f) {
+            return max(max(__float_as_uint(f.x), __float_as_uint(f.y)), max(__float_as_uint(f.z), __float_as_uint(f.w)));
+        };
+        return max(of(a), of(b));
+    }
 };
 
 __device__ __forceinline__ uint32_t pack(float2 a)
@@ -155,28 +169,54 @@ struct Out {
 struct Plain {
     static constexpr int kInputs = 1;
 };
-// a / (1 + exp(-z)) * b.  exp by the fast base-2 form: off by 2^-22 and |z| * 2^-24, with no effect where z is large
-// (positive: the sum is 1; negative: the result is next to 0 beside its block).
+// a / (1 + exp(-z)) * b.  exp by the fast base-2 form, off by 2^-22; its argument goes through up to four roundings and is off
+// by 2^-22 of itself, which is the result's error where z is negative (where it is positive the sum is next to 1).
 template <bool GELU> struct Gated {
     static constexpr int kInputs = 2;
-    static __device__ __forceinline__ Eight of(const Eight &a, const Eight &b)
+    // Above this exp(-z) is below 2^125 and the sum's reciprocal a normal number.  Further down the result would be 0, which with
+    // a large b it is not: such gates are looked for in the inputs' bits, and eight with one among them go a way of their own.
+    // (4,094 x 16,384 in bf16: 54 us, 52.6 without that way, 60 if z is what is looked at, which holds more registers.)
+    static constexpr float kLow = GELU ? -9.875f : -86.0f;
+    static __device__ __forceinline__ float2 exponent(float2 g)  // -z in units of log 2
     {
         // 0.5 (1 + tanh(y)) = 1 / (1 + exp(-2 y)), y = sqrt(2 / pi) (g + 0.044715 g^3); exp(x) = 2^(x log2 e)
         constexpr float kLog2e = 1.44269504088896f, kOne = -1.59576912160573f * kLog2e, kThree = -0.0713548162726003f * kLog2e;
+        if (GELU)
+            return mul2(g, fma2(mul2(g, {kThree, kThree}), g, {kOne, kOne}));
+        return mul2(g, {-kLog2e, -kLog2e});
+    }
+    static __device__ __forceinline__ float2 product(float2 g, float2 z, float2 b)
+    {
+        const float2 d = add2({exp2_fast(z.x), exp2_fast(z.y)}, {1.0f, 1.0f});
+        float2 s;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(d.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(d.y));
+        return mul2(mul2(g, s), b);
+    }
+    // Past 2^125 the exponential is the sum, and its four roots divide by turns.
+    static __device__ __forceinline__ float far_below(float g, float z, float b)
+    {
+        const float root = exp2_fast(-0.25f * z);
+        return b * root * root * root * (g * root);
+    }
+    template <typename Raw> static __device__ __forceinline__ Eight of(const Raw &a, const Raw &b)
+    {
+        const Eight g = a.values(), u = b.values();
         Eight r;
+        if (a.lowest() < __float_as_uint(kLow)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 g = a.v[i];
-            float2 z;
-            if (GELU)
-                z = mul2(g, fma2(mul2(g, {kThree, kThree}), g, {kOne, kOne}));
-            else
-                z = mul2(g, {-kLog2e, -kLog2e});
-            const float2 d = add2({exp2_fast(z.x), exp2_fast(z.y)}, {1.0f, 1.0f});
-            float2 s;
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(d.x));
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(d.y));
-            r.v[i] = mul2(mul2(g, s), b.v[i]);
+            for (int i = 0; i < 4; ++i)
+                r.v[i] = product(g.v[i], exponent(g.v[i]), u.v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 z = exponent(g.v[i]);
+                r.v[i] = product(g.v[i], z, u.v[i]);
+                if (z.x > 125.0f)
+                    r.v[i].x = far_below(g.v[i].x, z.x, u.v[i].x);
+                if (z.y > 125.0f)
+                    r.v[i].y = far_below(g.v[i].y, z.y, u.v[i].y);
+            }
         }
         return r;
     }
@@ -223,7 +263,7 @@ template <typename T, typename F> __global__ void __launch_bounds__(kThreads) co
         Eight e;
         uint32_t m;
         if constexpr (F::kInputs == 2) {
-            e = F::of(a[u].values(), b[u].values());
+            e = F::of(a[u], b[u]);
             m = most(e);
         } else {
             e = a[u].values();

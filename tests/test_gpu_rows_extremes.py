@@ -67,3 +67,45 @@ def test_a_sum_that_is_no_longer_finite(sv):
     last = sv.Coded(coded.codes.cpu()[2:], coded.scale.cpu().view(torch.uint8)[2:].view(coded.scale.dtype))
     ref.check_coded(last, y, E4, NORM_SLACK)
     assert torch.equal(total.cpu(), x + r)
+
+
+def gated(g, u, act):
+    """y = g / (1 + exp(-z)) * u and z, in float64 (which holds 1 + exp(-z) for all z here)."""
+    g, u = g.double(), u.double()
+    z = g if act == "silu" else 2 * math.sqrt(2 / math.pi) * (g + 0.044715 * g ** 3)
+    return g * torch.sigmoid(z) * u, z
+
+
+@pytest.mark.parametrize("act,low,high", [("silu", -170.0, -70.0), ("silu", -95.0, -80.0), ("silu", -90.0, 5.0),
+                                          ("gelu_tanh", -14.0, -9.0), ("gelu_tanh", -11.0, 3.0)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("code", [E4, E5])
+def test_strongly_negative_gates(sv, act, low, high, dtype, code):
+    """1 + exp(-z) passes 32 bits, or its reciprocal does; with a large partner the product is a number like any other."""
+    gen = torch.Generator().manual_seed(11)
+    g = (low + (high - low) * torch.rand(41, 400, generator=gen)).to(dtype)
+    u = (torch.randn(41, 400, generator=gen) * torch.exp2(torch.arange(41) * 3.0)[:, None]).to(dtype)  # up to 2^122
+    coded = sv.rows_gate(g.cuda(), u.cuda(), act=act, code=code)
+    y, z = gated(g, u, act)
+    # as for other gates: the exponential's argument is off by 2^-22 of itself through up to four roundings; four
+    # exponentials of a quarter of it are off by 2^-22 each, and five products by 2^-24 each
+    ref.check_coded(coded, y, code, 2.0 ** -19 + z.abs() * 2.0 ** -22)
+
+
+def test_gates_at_the_ends(sv):
+    """Gates past every exponential: 0, the gate's own size, or NaN where the definition has none."""
+    big = torch.finfo(F32).max
+    g = torch.tensor([-big, -1e30, -1e4, -1000.0, -400.0, 0.0, 400.0, 1e30, big, -math.inf, math.inf, math.nan])
+    for act in ("silu", "gelu_tanh"):
+        for partner in (1.0, 2.0 ** -20, big):
+            gate = g[:, None].expand(12, 128).contiguous()
+            coded = sv.rows_gate(gate.cuda(), torch.full((12, 128), partner).cuda(), act=act)
+            got = coded.codes.double().cpu() * ref.scale_values(coded.scale)
+            assert (got[:6] == 0).all()
+            assert got[9].isnan().all() and got[11].isnan().all() and got[10].isnan().all()
+            for i in (6, 7, 8):
+                want = g[i].double().item() * partner
+                if want > big:
+                    assert got[i].isnan().all()
+                else:
+                    assert ((got[i] - want).abs() <= 2.0 ** -4 * want).all()
