@@ -62,9 +62,16 @@ class _Unloaded:
 
 _quick = _Unloaded()
 
+def _empty_strided(shape, stride, dtype):
+    return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
+
+
 # torch.empty costs 5 us a call beside launches here, and this form of it (the one that torch's compiled code calls) less
-# than 1: for one token it is half of a call's time.
-_empty = torch._C._dynamo.guards._empty_strided_cuda
+# than 1: for one token it is half of a call's time.  It is no public function: a torch without it gives the other.
+try:
+    _empty = torch._C._dynamo.guards._empty_strided_cuda
+except AttributeError:
+    _empty = _empty_strided
 
 
 def _new(shape, dtype, stream):
