@@ -121,6 +121,7 @@ def _prepare(target, draft, tokens, num_draft, uniforms, temperature, out_tokens
     dev = _device_of(target, draft, tokens, num_draft, uniforms, temperature, out_tokens, out_num)
     B, g1, V = target.shape
     gmax = g1 - 1
+    _native.fit("target_logits", B, gmax, V)
     code = _dtype_code(target)
     _check_input(target, "target_logits", target.dtype, (B, gmax + 1, V), dev)
     if draft is not None:  # None: point-mass proposals (q_i is 1 at the drafted id)
@@ -290,6 +291,7 @@ def tree_verify(target_logits, parent, tokens, num_nodes, uniforms, temperature,
     dev = _device_of(target_logits, parent, tokens, num_nodes, uniforms, temperature, out_tokens, out_num_accepted,
                      out_path)
     B, N, V = target_logits.shape
+    _native.fit("target_logits", B, N, V)
     code = _dtype_code(target_logits)
     _check_input(target_logits, "target_logits", target_logits.dtype, (B, N, V), dev)
     _check_input(parent, "parent", torch.int32, (B, N), dev)
@@ -346,6 +348,7 @@ def sample(logits, uniforms, temperature, out_tokens=None, status=None, stream=N
         raise ValueError("logits must be a [B, V] tensor")
     dev = _device_of(logits, uniforms, temperature, out_tokens)
     B, V = logits.shape
+    _native.fit("logits", B, V)
     code = _dtype_code(logits)
     _check_input(logits, "logits", logits.dtype, (B, V), dev)
     _check_input(uniforms, "uniforms", torch.float32, (B,), dev)
@@ -374,6 +377,7 @@ def ngram_propose(context, context_len, min_n: int, max_n: int, gamma_max: int, 
         raise ValueError("context must be an int32 [B, S] tensor")
     dev = _device_of(context, context_len, out_tokens, out_num)
     B = context.shape[0]
+    _native.fit("ngram_propose", B, min_n, max_n, gamma_max)
     if context.stride(1) != 1:
         raise ValueError("context rows must be contiguous")
     if context.device.type == "cpu" and not context.is_pinned():
@@ -400,6 +404,7 @@ def ngram_propose(context, context_len, min_n: int, max_n: int, gamma_max: int, 
 def launch_shape(B: int, gamma_max: int, V: int, dtype: str = "bf16"):
     """(cluster size, CTAs, threads per CTA, kernel) the library picks for these
     sizes on the current device; kernel is KERNEL_REGISTER or KERNEL_EARLY."""
+    _native.fit("launch_shape", B, gamma_max, V)
     lib = _native.load()
     c, n, t, k = ctypes.c_int(), ctypes.c_int(), ctypes.c_int(), ctypes.c_int()
     rc = lib.spec_verify_launch_shape(B, gamma_max, V, SPEC_BF16 if dtype == "bf16" else SPEC_F32,

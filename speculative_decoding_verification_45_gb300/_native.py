@@ -67,6 +67,13 @@ class Coded(ctypes.Structure):
                 ("code", ctypes.c_int32)]
 
 
+def fit(name: str, *sizes: int) -> None:
+    """Sizes are handed to the library in 32 bits, into which ctypes cuts larger ones without a word."""
+    for n in sizes:
+        if not -(1 << 31) <= n < 1 << 31:
+            raise ValueError(f"{name}: sizes must be below 2^31, got {n}")
+
+
 def nvcc_path() -> str:
     for cand in (os.environ.get("NVCC"), shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):

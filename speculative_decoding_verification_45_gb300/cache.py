@@ -110,6 +110,7 @@ def _describe(cache, block_table, lengths):
     if block_table.dim() != 2:
         raise ValueError("block_table must be a [batch, blocks] tensor")
     batch, blocks = block_table.shape
+    _native.fit("cache", pages, heads, batch, blocks)
     step, dense = block_table.stride()
     if block_table.dtype != torch.int32 or block_table.device != dev or (blocks > 1 and dense != 1):
         raise ValueError(f"block_table must be int32 on {dev} with dense rows")
@@ -184,6 +185,7 @@ def cache_append(cache, block_table, lengths, k, v, num_new=None, positions=None
     if k.device != dev or v.device != dev:
         raise ValueError(f"k and v must live on {dev}")
     n = k.shape[1]
+    _native.fit("k", n)
     new = None if num_new is None else _check(num_new, "num_new", torch.int32, (c.batch,), dev)
     pos = None if positions is None else _check(positions, "positions", torch.int32, (c.batch, n), dev)
     rc = _native.load().spec_cache_append(
@@ -201,6 +203,7 @@ def _form(c, dev, q, num_new, scale, softcap, slopes, window, prefix, parent):
     if q.device != dev:
         raise ValueError(f"q must live on {dev}, found {q.device}")
     n, heads = q.shape[1], q.shape[2]
+    _native.fit("q", n, heads)
     if parent is not None and n > MAX_TREE_NODES:
         raise ValueError(f"a candidate tree has at most {MAX_TREE_NODES} nodes, got {n}")
     if window < 0 or not 0 <= softcap < math.inf:
@@ -313,6 +316,7 @@ def cache_evict(cache, block_table, lengths, weights, keep: int, recent: int, ou
     c, dev, len_ptr = _describe(cache, block_table, lengths)
     if keep < 1 or not 0 <= recent <= keep:
         raise ValueError(f"keep must be at least 1 and recent in [0, keep], got {keep} and {recent}")
+    _native.fit("keep", keep)
     blocks = -(-keep // c.block)
     if out_table.dim() != 2 or out_table.shape[0] != c.batch or out_table.shape[1] < blocks:
         raise ValueError(f"out_table: expected shape ({c.batch}, at least {blocks}), got {tuple(out_table.shape)}")
