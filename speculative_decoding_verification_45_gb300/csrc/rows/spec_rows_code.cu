@@ -487,8 +487,8 @@ template <typename T, typename R> spec_status launch_norm(const NormArgs &a, con
     const int slots = scale_blocks(out->dim) * kLanes;
     const Out o = make_out(out);
     // The weight is read early where all rows are at work at once, 16,384 elements to each of 152 SMs, and only latency
-    // counts (1 x 4,096: 3.1 to 2.2 us; 1 x 8,192: 4.8 to 3.0; 304 x 8,192: 4.8 to 4.3).  With more, its registers cost rows
-    // in flight (608 x 8,192: 6.7 us late, 7.9 early; 16,376: 135 and 175).
+    // counts (1 x 4,096: 3.2 to 2.3 us; 1 x 8,192: 4.9 to 3.0; 304 x 8,192: 6.0 to 5.0).  With more, its registers cost rows
+    // in flight (608 x 8,192: 8.1 us late, 9.3 early; 16,376: 136 and 178).
     const bool early = (int64_t)out->rows * out->dim <= 152 * 16384;
     const unsigned rows = (unsigned)out->rows, few = (rows + kThreads / 32 - 1) / (kThreads / 32);
     if (slots <= 32)

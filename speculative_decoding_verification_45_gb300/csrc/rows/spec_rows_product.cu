@@ -21,12 +21,14 @@
 //
 // Pairs are persistent, with accumulators in two places, so that writing one tile overlaps the products of the next.
 // Where tiles are too few for the SMs, up to eight pairs share one, a part of k each.  Each CTA then adds up a share of the
-// tile's rows, in the order of the parts, from what the others send into its shared memory (by bulk copies: 160 x 4,096 to
-// 1,024 takes 7.1 us, 7.5 if it loads from theirs, 9.6 if they store to its).  `plan` has the rule and what it rests on.
+// tile's rows, in the order of the parts, from what the others send into its shared memory (by bulk copies, which are faster
+// than loads from theirs, 160 x 4,096 to 1,024 by 0.4 us, and than stores to its, by 2.5).  `plan` has the rule and what it
+// rests on.
 //
-// Bound by the weight's bytes for few rows (1 x 4,096 to 128,256: 78.7 us, the copy rate; 1 x 4,096 to 4,096: 7.2 us, of
-// which nearly 5 are the kernel's start and end), by the products for many (16,376 x 4,096 to 6,144: 196 to 213 us, 3.9 to 4.2
-// PFLOP/s).  Without the scales' path that product took 190 us, without copies 177 (4.6 PFLOP/s).
+// Bound by the weight's bytes for few rows (1 x 4,096 to 128,256: 79.7 us, 98 % of the copy rate; 1 x 4,096 to 4,096: 6.9 us,
+// of which more than 4 are this kernel's start and end), by the products for many (16,376 x 4,096 to 6,144: 196 to 213 us in
+// short runs, 3.9 to 4.2 PFLOP/s, which a power limit lowers to 3.1 in long ones).  Without the scales' path that product took
+// 190 us, without copies 177.  Few rows' times are of weights in memory; from L2 one row of 4,096 takes as long.
 
 #include <algorithm>
 #include <atomic>
@@ -118,7 +120,7 @@ __device__ __forceinline__ float4 load_shared4(uint32_t at)
     return v;
 }
 // For what went through tensor memory, which tcgen05.fence orders.  (A release at cluster scope, which nothing here needs,
-// waits for the thread's loads in flight and more: 1,600 clocks each time, 311 us against 290 for 16,376 x 4,096 to 6,144.)
+// waits for the thread's loads in flight and more: 1,600 clocks each time.)
 __device__ __forceinline__ void arrive_cluster(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -483,9 +485,9 @@ product_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorM
     tc_before();
     cluster_arrive();
     // L2 may begin to read the weight while the kernel before still runs: a hint, which brings nothing nearer than where
-    // that kernel's writes arrive too, so it needs no promise that the weight stays.  A layer of seven calls (4,096, one row):
-    // 64.9 to 61.8 us; 1 x 4,096 to 4,096 behind itself: 8.7 to 8.3.  (As copies of tiles, or with more blocks than 4, what is
-    // in L2 already costs more: 16 x 1,024 to 1,024 5.4 to 6.5 and 5.8 us.)  The warps that read accumulators have the time.
+    // that kernel's writes arrive too, so it needs no promise that the weight stays.  A layer (width 4,096, one row):
+    // 62.7 to 59.0 us; 1 x 4,096 to 4,096 behind itself: 7.9 to 6.9.  (As copies of tiles, or with more blocks than 4, what is
+    // in L2 already costs more: 16 x 1,024 to 1,024 1.1 and 0.4 us.)  The warps that read accumulators have the time.
     // The first tile of this CTA, or the one that it has a part of, and the next one.  Found here, where there is time: divisions
     // take hundreds of clocks.
     const int u0 = (int)cluster_index();
@@ -850,7 +852,7 @@ out:
     }
     tc_before();
     // All that was sent to another CTA and its barriers has been waited for there, unless a wait ran out: so this need not wait
-    // for the outputs on their way (1 x 4,096 to 4,096: 8.3 us if it does, 7.6 so).
+    // for the outputs on their way (1 x 4,096 to 4,096: 7.3 us if it does, 6.9 so).
     if (dead)
         cluster_arrive();
     else
@@ -885,7 +887,7 @@ constexpr uint32_t stage_bytes(int tile) { return kDepth * (kABytes + (uint32_t)
 // What arrives from the other parts.
 constexpr uint32_t others_bytes(int tile, int parts) { return (uint32_t)((parts - 1) * ((tile + parts - 1) / parts)) * kRowsM * 4; }
 // They have their own place while that costs no stage that is missed; in the place of stages they must wait until that CTA
-// has used them (1 x 4,096 to 4,096: 7.6 us apart, 7.9 not; 160 x 8,192 to 8,192: 17.7 us apart, 17.3 not).
+// has used them (14 x 14,336 to 1: 7.05 us apart, 7.2 not; 160 x 8,192 to 8,192: 17.3 us apart, 16.4 not).
 constexpr bool others_apart(int tile, int parts) { return parts > 1 && tile <= 64; }
 // Stages, beside the outputs on their way or what arrives from the other parts.
 constexpr int stages_of(int tile, int parts)
@@ -904,7 +906,8 @@ struct Plan {
 // to one output: 27.7 us whole, 15.7, 9.6 and 7.1 in 2, 4 and 8 parts), and each pair at work 15 ns more, as they start together
 // and meet.  Parts that do not all run at once cost a round more than they save (256 rows of 2,048 to 2,048, 64 rows to a
 // tile: 7.0 us whole, 7.1 in two parts, 12.8 in three).  Over 108 sizes the choice is within 4 % of the best of them in 102
-// and within 10 % in all but one (512 x 512, one row: 4.6 us, 4.1 in four parts).
+// and within 10 % in all but one (640 to 4,096, 128 rows: 5.6 us, 5.0 in tiles of 64 rows).  It does not look at where outputs
+// lie, nor at what writing them takes.
 Plan plan(const Device &d, int rows, int outs, int blocks)
 {
     const int64_t out_tiles = (outs + 2 * kRowsM - 1) / (2 * kRowsM);

@@ -9,7 +9,8 @@ each 128 x 128 block (weights).  Every call checks its tensors, enqueues one ker
 on the current stream (or ``stream``) and returns; include/spec_verify.h states the
 operations, layouts and error behaviour.  All tensors are CUDA tensors on the
 current device; a tensor of rows may have any leading dimensions that lie at one
-stride.
+stride, up to 2^30 rows of up to 131,072 elements.  Results have no history:
+tensors that require a gradient are read like others, and none flows back to them.
 """
 from __future__ import annotations
 
@@ -328,6 +329,9 @@ def rows_product(rows, weight, dtype=torch.bfloat16, out=None, status=None, stre
     weight  Coded [outputs, width], a scale for each 128 x 128 (weight_quantise)
     dtype   of the result [..., outputs]: torch.bfloat16 or torch.float32; sums are 32-bit
     out     to write into, rows at any one stride (then ``dtype`` is its type)
+    status  int32 CUDA tensor whose first element receives STATUS_INTERNAL where a wait in
+            the kernel ran out: without it such a call, whose result is not valid, looks
+            like any other
     """
     if out is None and stream is None:
         made = _quick.product(rows, weight, dtype, status)
